@@ -1,0 +1,382 @@
+"""The operators this package offers beside the 4-bit linears, as cases to
+measure: layer norm (affine, or modulated per sample as an adaptive layer norm
+is) with its gradients, and the FP8 linear (E4M3 codes, one power-of-two scale
+per block of 128) with its gradients and with the layer norm in front of it.
+
+Formulas, with q8(v) the E4M3 rounding of a block of 128 values v: 2^e is the
+smallest power of two (e >= -126) with max|v| 2^-e <= 448, and q8(v) = 2^e
+rne_e4m3(v 2^-e).
+
+  norm         xhat = (x - mean) rstd, rstd = 1 / sqrt(var + eps),
+               y = xhat g + b, g = weight or 1 + weight; row m takes the
+               weight and bias of group m // rows_per_group
+  norm_grad    d = dy g: dx = rstd (d - mean_c(d) - xhat mean_c(d xhat)),
+               dweight = sum over the group's rows of dy xhat, dbias of dy
+  linear       y = q8_k(x) W^T + b, blocks along the input channels, W held
+               as E4M3 codes with a scale per 128 x 128 block
+  norm_linear  linear(bf16(norm(x)))
+  linear_grad  dx = q8_n(dy) W (blocks along the output channels),
+               dw = q8_m(dy)^T q8_m(x) (blocks along the tokens), db = sum dy
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-6
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def listed():
+    return [
+        # layer norm of one conditioning vector: nothing but latency
+        {"name": "norm 1x3072", "op": "norm", "rows": 1, "channels": 3072, "groups": 1, "dtype": "bf16",
+         "params": "bf16", "one_plus": False},
+        # the adaptive layer norm in front of a double-stream block's linears, two samples of 4608 tokens
+        {"name": "norm 9216x3072 modulated", "op": "norm", "rows": 9216, "channels": 3072, "groups": 2,
+         "dtype": "bf16", "params": "bf16", "one_plus": True},
+        # a width that no vector load divides, in half precision with float parameters
+        {"name": "norm 5003x1283 fp16", "op": "norm", "rows": 5003, "channels": 1283, "groups": 1, "dtype": "fp16",
+         "params": "fp32", "one_plus": False},
+        # training the modulated norm: gradients of the stream and of each sample's scale and shift
+        {"name": "norm_grad 9216x3072 modulated", "op": "norm_grad", "rows": 9216, "channels": 3072, "groups": 2,
+         "dtype": "bf16", "params": "bf16", "one_plus": True},
+        # an affine norm over many narrow odd rows (per-head norms are like this), in 32 bits
+        {"name": "norm_grad 16387x517 fp32", "op": "norm_grad", "rows": 16387, "channels": 517, "groups": 1,
+         "dtype": "fp32", "params": "fp32", "one_plus": False},
+        # one token through an MLP-up layer: the weight stream of a single step
+        {"name": "linear 1x3072->12288", "op": "linear", "tokens": 1, "inputs": 3072, "outputs": 12288},
+        # a few rows through the MLP-down layer
+        {"name": "linear 64x12288->3072", "op": "linear", "tokens": 64, "inputs": 12288, "outputs": 3072},
+        # sizes that end inside every tile and block
+        {"name": "linear 1003x2064->1552", "op": "linear", "tokens": 1003, "inputs": 2064, "outputs": 1552},
+        # the MLP-up projection of a 1024 x 1024 image with its text tokens
+        {"name": "linear 4608x3072->12288", "op": "linear", "tokens": 4608, "inputs": 3072, "outputs": 12288},
+        # the same tokens through the modulated norm and the QKV projection in one call
+        {"name": "norm_linear 4608x3072->9216", "op": "norm_linear", "tokens": 4608, "inputs": 3072, "outputs": 9216,
+         "groups": 2},
+        # training the MLP-up projection
+        {"name": "linear_grad 4608x3072->12288", "op": "linear_grad", "tokens": 4608, "inputs": 3072,
+         "outputs": 12288, "grads": "bf16"},
+        # a ragged microbatch with gradients kept in 32 bits
+        {"name": "linear_grad 777x1552->2064", "op": "linear_grad", "tokens": 777, "inputs": 1552, "outputs": 2064,
+         "grads": "fp32"},
+    ]
+
+
+def _spread(rng, lo, hi, step=1):
+    """A size of [lo, hi], spread over its logarithm, a multiple of step."""
+    v = math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))
+    return max(lo, min(hi, int(v) // step * step))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm_grad", "linear", "linear", "norm_linear", "linear_grad"])
+    if op in ("norm", "norm_grad"):
+        dtype = rng.choice(["bf16", "bf16", "fp16", "fp32"])
+        channels = _spread(rng, 33, 12289)
+        rows = _spread(rng, 1, min(16384, 9216 * 3072 // channels // (2 if dtype == "fp32" else 1)))
+        return {"op": op, "rows": rows, "channels": channels, "groups": rng.randint(1, min(rows, 4)), "dtype": dtype,
+                "params": rng.choice([dtype, "fp32"]), "one_plus": rng.random() < 0.5}
+    inputs = _spread(rng, 64, 12288, 16)
+    outputs = _spread(rng, 64, min(12288, (9216 if op == "norm_linear" else 12288) * 3072 // inputs), 16)
+    tokens = _spread(rng, 1, 4608)
+    case = {"op": op, "tokens": tokens, "inputs": inputs, "outputs": outputs}
+    if op == "norm_linear":
+        case["groups"] = rng.randint(1, min(tokens, 4))
+    if op == "linear_grad":
+        case["grads"] = rng.choice(["bf16", "fp32"])
+    return case
+
+
+def _rows_per_group(rows, groups):
+    return -(-rows // groups)
+
+
+def _power(e):
+    """2^e of whole numbers e in [-126, 127], exactly."""
+    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _block_exponent(amax):
+    """The e of the formula for float32 maxima."""
+    m, e = torch.frexp(amax)   # amax = m 2^e, 1/2 <= m < 1, and 448 = 0.875 2^9
+    return (e - 9 + (m > 0.875)).clamp(min=-126)
+
+
+def _pad(v, n, dim):
+    short = -v.shape[dim] % n
+    if not short:
+        return v
+    shape = list(v.shape)
+    shape[dim] = short
+    return torch.cat([v, v.new_zeros(shape)], dim)
+
+
+def _stream_of_activations(gen, rows, channels, dtype):
+    """Activations of a diffusion transformer: unit normal, one channel in a
+    hundred fifty times larger, with an offset of its own per channel."""
+    x = torch.randn(rows, channels, device="cuda", generator=gen)
+    big = torch.rand(channels, device="cuda", generator=gen) < 0.01
+    x = (x + 0.25 * torch.randn(channels, device="cuda", generator=gen)) * torch.where(big, 50.0, 1.0)
+    return x.to(dtype)
+
+
+def _affine(gen, case, channels, dtype):
+    """(weight, bias) of each group: the scale and the shift that a modulation
+    layer's output holds side by side, or a norm's own parameters."""
+    g = case["groups"]
+    if case.get("one_plus", True):
+        modulation = (0.3 * torch.randn(g, 6 * channels, device="cuda", generator=gen)).to(dtype)
+        return modulation[:, channels:2 * channels], modulation[:, :channels]
+    weight = 1 + 0.2 * torch.randn(g, channels, device="cuda", generator=gen)
+    return weight.to(dtype), (0.2 * torch.randn(g, channels, device="cuda", generator=gen)).to(dtype)
+
+
+def _weights(gen, inputs, outputs):
+    """An FP8 layer as a program keeps it: codes and scale bytes (2^(s - 127)
+    per 128 x 128 block, rows of scales padded to whole words), the same
+    transposed for the gradient of the input, and the bias."""
+    w = torch.randn(outputs, inputs, device="cuda", generator=gen) / math.sqrt(inputs)
+    bias = (0.1 * torch.randn(outputs, device="cuda", generator=gen)).to(torch.bfloat16)
+    p = _pad(_pad(w, 128, 0), 128, 1)
+    blocks = p.view(p.shape[0] // 128, 128, p.shape[1] // 128, 128)
+    e = _block_exponent(blocks.abs().amax((1, 3)))
+    codes = (blocks * _power(-e)[:, None, :, None]).view_as(p).to(torch.float8_e4m3fn)
+    codes = codes.view(torch.uint8)[:outputs, :inputs].contiguous()
+    s = (e + 127).to(torch.uint8)
+    return {"q": codes, "s": _pad(s, 4, 1).contiguous(), "qt": codes.t().contiguous(),
+            "st": _pad(s.t(), 4, 1).contiguous(), "bias": bias}
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    state = {"case": dict(case)}
+    if case["op"] in ("norm", "norm_grad"):
+        rows, channels, dtype = case["rows"], case["channels"], TYPES[case["dtype"]]
+        state["x"] = _stream_of_activations(gen, rows, channels, dtype)
+        state["weight"], state["bias"] = _affine(gen, case, channels, TYPES[case["params"]])
+        if case["op"] == "norm_grad":
+            state["dy"] = torch.randn(rows, channels, device="cuda", generator=gen).to(dtype)
+            # what the forward pass left for the backward pass
+            x = state["x"].double()
+            mean = x.mean(1)
+            state["mean"] = mean.float()
+            state["rstd"] = ((x - mean[:, None]).square().mean(1) + EPS).rsqrt().float()
+        return state
+    tokens, inputs, outputs = case["tokens"], case["inputs"], case["outputs"]
+    state["x"] = _stream_of_activations(gen, tokens, inputs, torch.bfloat16)
+    state["layer"] = _weights(gen, inputs, outputs)
+    if case["op"] == "norm_linear":
+        state["weight"], state["bias"] = _affine(gen, case, inputs, torch.bfloat16)
+    if case["op"] == "linear_grad":
+        # gradients of a loss that averages over the tokens: small, and uneven between channels
+        dy = torch.randn(tokens, outputs, device="cuda", generator=gen)
+        spread = torch.exp(torch.randn(outputs, device="cuda", generator=gen))
+        state["dy"] = (dy * spread / tokens).to(torch.bfloat16)
+    return state
+
+
+# ---------------------------------------------------------------------------
+# the plain forms
+# ---------------------------------------------------------------------------
+def _plain_q8(v):
+    """q8 of blocks of 128 along the last axis of a float32 matrix."""
+    p = _pad(v, 128, 1)
+    blocks = p.view(p.shape[0], -1, 128)
+    e = _block_exponent(blocks.abs().amax(2, keepdim=True))
+    q = (blocks * _power(-e)).to(torch.float8_e4m3fn).float() * _power(e)
+    return q.view_as(p)[:, :v.shape[1]]
+
+
+def _plain_weight(layer):
+    codes = layer["q"]
+    n, k = codes.shape
+    scale = _power(layer["s"].int() - 127)
+    scale = scale.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    return codes.view(torch.float8_e4m3fn).float() * scale
+
+
+def _plain_gain(weight, bias, rows, one_plus):
+    """The gain and the shift of each row, in 32 bits."""
+    of_row = torch.arange(rows, device=weight.device) // _rows_per_group(rows, weight.shape[0])
+    gain = weight.float() + 1 if one_plus else weight.float()
+    return gain[of_row], bias.float()[of_row]
+
+
+def _plain_norm(x, weight, bias, one_plus):
+    gain, shift = _plain_gain(weight, bias, x.shape[0], one_plus)
+    v = x.float()
+    mean = v.mean(1)
+    centred = v - mean[:, None]
+    rstd = (centred.square().mean(1) + EPS).rsqrt()
+    return (centred * rstd[:, None] * gain + shift).to(x.dtype), mean, rstd
+
+
+def _plain_norm_grad(state):
+    case, weight, x, dy = state["case"], state["weight"], state["x"].float(), state["dy"].float()
+    rows, channels = x.shape
+    groups, run = weight.shape[0], _rows_per_group(x.shape[0], weight.shape[0])
+    gain, _ = _plain_gain(weight, weight, rows, case["one_plus"])
+    xhat = (x - state["mean"][:, None]) * state["rstd"][:, None]
+    d = dy * gain
+    dx = state["rstd"][:, None] * (d - d.mean(1, keepdim=True) - xhat * (d * xhat).mean(1, keepdim=True))
+    dweight = _pad_rows(dy * xhat, groups * run).view(groups, run, channels).sum(1)
+    dbias = _pad_rows(dy, groups * run).view(groups, run, channels).sum(1)
+    return dx.to(state["x"].dtype), dweight.to(weight.dtype), dbias.to(weight.dtype)
+
+
+def _pad_rows(v, rows):
+    return torch.cat([v, v.new_zeros(rows - v.shape[0], v.shape[1])]) if rows > v.shape[0] else v
+
+
+def _plain_linear(x, layer):
+    return (_plain_q8(x.float()) @ _plain_weight(layer).t() + layer["bias"].float()).to(torch.bfloat16)
+
+
+def _plain_linear_grad(state):
+    x, dy, grads = state["x"].float(), state["dy"].float(), TYPES[state["case"]["grads"]]
+    dx = _plain_q8(dy) @ _plain_weight(state["layer"])
+    dw = _plain_q8(dy.t().contiguous()) @ _plain_q8(x.t().contiguous()).t()
+    return dx.to(torch.bfloat16), dw.to(grads), dy.sum(0).to(grads)
+
+
+def run(state):
+    case, op = state["case"], state["case"]["op"]
+    if own:
+        import bit_svdquant_diffusion_amd as S
+
+        if op == "norm":
+            return S.layer_norm_forward(state["x"], state["weight"], state["bias"], eps=EPS, one_plus=case["one_plus"],
+                                        rows_per_group=_rows_per_group(case["rows"], case["groups"]))
+        if op == "norm_grad":
+            return S.layer_norm_backward(state["dy"], state["x"], state["mean"], state["rstd"], state["weight"],
+                                         one_plus=case["one_plus"],
+                                         rows_per_group=_rows_per_group(case["rows"], case["groups"]))
+        K, N = case["inputs"], case["outputs"]
+        if op == "linear":
+            return S.fp8_forward(K, N, state["layer"], state["x"])
+        if op == "norm_linear":
+            return S.fp8_norm_forward(K, N, state["layer"], state["x"], state["weight"], state["bias"], eps=EPS,
+                                      one_plus=True, rows_per_group=_rows_per_group(case["tokens"], case["groups"]))
+        return S.fp8_backward(K, N, state["layer"], state["x"], state["dy"], grad_dtype=TYPES[case["grads"]])
+    if op == "norm":
+        return _plain_norm(state["x"], state["weight"], state["bias"], case["one_plus"])
+    if op == "norm_grad":
+        return _plain_norm_grad(state)
+    if op == "linear":
+        return _plain_linear(state["x"], state["layer"])
+    if op == "norm_linear":
+        return _plain_linear(_plain_norm(state["x"], state["weight"], state["bias"], True)[0], state["layer"])
+    return _plain_linear_grad(state)
+
+
+def work(case):
+    if case["op"] in ("norm", "norm_grad"):
+        rows, channels, g = case["rows"], case["channels"], case["groups"]
+        e = 4 if case["dtype"] == "fp32" else 2
+        p = 4 if case["params"] == "fp32" else 2
+        if case["op"] == "norm":
+            return {"bytes": 2 * rows * channels * e + 2 * g * channels * p + 8 * rows, "flops": 8 * rows * channels}
+        return {"bytes": 3 * rows * channels * e + 3 * g * channels * p + 8 * rows, "flops": 14 * rows * channels}
+    m, k, n = case["tokens"], case["inputs"], case["outputs"]
+    weights = n * k + -(-n // 128) * -(-k // 128)
+    if case["op"] == "linear_grad":
+        p = 4 if case["grads"] == "fp32" else 2
+        return {"bytes": 4 * m * k + 2 * m * n + weights + p * n * k + p * n, "flops": 4 * m * n * k}
+    extra = 4 * case["groups"] * k if case["op"] == "norm_linear" else 0
+    return {"bytes": 2 * m * k + weights + 2 * n + 2 * m * n + extra, "flops": 2 * m * n * k}
+
+
+# ---------------------------------------------------------------------------
+# the definitions in 64 bits
+# ---------------------------------------------------------------------------
+def _round_e4m3(v):
+    """Nearest E4M3 value, ties to even, of float64 values up to 448: the grid
+    has a spacing of 2^(floor(log2|v|) - 3), and of 2^-9 below 2^-6."""
+    exponent = torch.frexp(v)[1].to(torch.float64) - 1
+    spacing = torch.exp2(exponent.clamp(min=-6.0) - 3)
+    return torch.round(v / spacing) * spacing
+
+
+def _exact_q8(v, axis):
+    """q8 with the blocks along `axis`, the scale found by trying: the
+    exponent of max / 448 and its two neighbours."""
+    if axis == 0:
+        return _exact_q8(v.t(), 1).t()
+    out = torch.empty_like(v)
+    for at in range(0, v.shape[1], 128):
+        block = v[:, at:at + 128]
+        top = block.abs().max(1, keepdim=True).values
+        guess = torch.floor(torch.log2(torch.where(top > 0, top, torch.ones_like(top)) / 448))
+        e = guess + 2
+        for less in (1, 0, -1):
+            e = torch.where(top <= 448 * torch.exp2(guess + less), guess + less, e)
+        scale = torch.exp2(e.clamp(min=-126.0))
+        out[:, at:at + 128] = _round_e4m3(block / scale) * scale
+    return out
+
+
+def _exact_weight(layer):
+    """The weight from its bytes: sign, four exponent bits, three mantissa bits."""
+    b = layer["q"].to(torch.int64)
+    exponent, mantissa = (b >> 3) & 15, (b & 7).double()
+    value = torch.where(exponent == 0, mantissa * 2.0 ** -9,
+                        (8 + mantissa) * torch.exp2(exponent.double() - 10))
+    value = torch.where(b >= 128, -value, value)
+    n, k = b.shape
+    rows = torch.arange(n, device=b.device) // 128
+    cols = torch.arange(k, device=b.device) // 128
+    return value * torch.exp2(layer["s"].double() - 127)[rows][:, cols]
+
+
+def _exact_norm(x, weight, bias, one_plus, groups):
+    y = torch.empty(x.shape, dtype=torch.float64, device=x.device)
+    mean = torch.empty(x.shape[0], dtype=torch.float64, device=x.device)
+    rstd = torch.empty_like(mean)
+    run_of = _rows_per_group(x.shape[0], groups)
+    for g in range(groups):
+        rows = slice(g * run_of, min((g + 1) * run_of, x.shape[0]))
+        v = x[rows].double()
+        if not v.shape[0]:
+            continue
+        mean[rows] = v.sum(1) / v.shape[1]
+        off = v - mean[rows, None]
+        rstd[rows] = 1 / torch.sqrt((off * off).sum(1) / v.shape[1] + EPS)
+        y[rows] = off * rstd[rows, None] * (weight[g].double() + (1.0 if one_plus else 0.0)) + bias[g].double()
+    return y, mean, rstd
+
+
+def exact(case, seed):
+    state = prepare(case, seed)
+    op, x = case["op"], state["x"]
+    if op == "norm":
+        return _exact_norm(x, state["weight"], state["bias"], case["one_plus"], case["groups"])
+    if op == "norm_grad":
+        run_of = _rows_per_group(case["rows"], case["groups"])
+        dx = torch.empty(x.shape, dtype=torch.float64, device=x.device)
+        dweight = torch.zeros(state["weight"].shape, dtype=torch.float64, device=x.device)
+        dbias = torch.zeros_like(dweight)
+        for g in range(case["groups"]):
+            rows = slice(g * run_of, min((g + 1) * run_of, x.shape[0]))
+            v, dy = x[rows].double(), state["dy"][rows].double()
+            if not v.shape[0]:
+                continue
+            rstd = state["rstd"][rows].double()[:, None]
+            xhat = (v - state["mean"][rows].double()[:, None]) * rstd
+            d = dy * (state["weight"][g].double() + (1.0 if case["one_plus"] else 0.0))
+            n = v.shape[1]
+            dx[rows] = rstd / n * (n * d - d.sum(1, keepdim=True) - xhat * (d * xhat).sum(1, keepdim=True))
+            dweight[g] = (dy * xhat).sum(0)
+            dbias[g] = dy.sum(0)
+        return dx, dweight, dbias
+    w = _exact_weight(state["layer"])
+    if op == "linear_grad":
+        dy = state["dy"].double()
+        return (torch.matmul(_exact_q8(dy, 1), w), torch.matmul(_exact_q8(dy, 0).t().contiguous(), _exact_q8(x.double(), 0)),
+                dy.sum(0))
+    v = x.double()
+    if op == "norm_linear":
+        v = _exact_norm(x, state["weight"], state["bias"], True, case["groups"])[0].to(torch.bfloat16).double()
+    return torch.matmul(_exact_q8(v, 1), w.t().contiguous()) + state["layer"]["bias"].double()
