@@ -58,10 +58,9 @@ def listed():
          "groups": 2},
         # training the MLP-up projection
         {"name": "linear_grad 4608x3072->12288", "op": "linear_grad", "tokens": 4608, "inputs": 3072,
-         "outputs": 12288, "grads": "bf16"},
-        # a ragged microbatch with gradients kept in 32 bits
-        {"name": "linear_grad 777x1552->2064", "op": "linear_grad", "tokens": 777, "inputs": 1552, "outputs": 2064,
-         "grads": "fp32"},
+         "outputs": 12288},
+        # a ragged microbatch
+        {"name": "linear_grad 777x1552->2064", "op": "linear_grad", "tokens": 777, "inputs": 1552, "outputs": 2064},
     ]
 
 
@@ -85,8 +84,6 @@ def draw(rng):
     case = {"op": op, "tokens": tokens, "inputs": inputs, "outputs": outputs}
     if op == "norm_linear":
         case["groups"] = rng.randint(1, min(tokens, 4))
-    if op == "linear_grad":
-        case["grads"] = rng.choice(["bf16", "fp32"])
     return case
 
 
@@ -236,10 +233,10 @@ def _plain_linear(x, layer):
 
 
 def _plain_linear_grad(state):
-    x, dy, grads = state["x"].float(), state["dy"].float(), TYPES[state["case"]["grads"]]
+    x, dy = state["x"].float(), state["dy"].float()
     dx = _plain_q8(dy) @ _plain_weight(state["layer"])
     dw = _plain_q8(dy.t().contiguous()) @ _plain_q8(x.t().contiguous()).t()
-    return dx.to(torch.bfloat16), dw.to(grads), dy.sum(0).to(grads)
+    return dx.to(torch.bfloat16), dw.to(torch.bfloat16), dy.sum(0).to(torch.bfloat16)
 
 
 def run(state):
@@ -260,7 +257,7 @@ def run(state):
         if op == "norm_linear":
             return S.fp8_norm_forward(K, N, state["layer"], state["x"], state["weight"], state["bias"], eps=EPS,
                                       one_plus=True, rows_per_group=_rows_per_group(case["tokens"], case["groups"]))
-        return S.fp8_backward(K, N, state["layer"], state["x"], state["dy"], grad_dtype=TYPES[case["grads"]])
+        return S.fp8_backward(K, N, state["layer"], state["x"], state["dy"])
     if op == "norm":
         return _plain_norm(state["x"], state["weight"], state["bias"], case["one_plus"])
     if op == "norm_grad":
@@ -283,8 +280,7 @@ def work(case):
     m, k, n = case["tokens"], case["inputs"], case["outputs"]
     weights = n * k + -(-n // 128) * -(-k // 128)
     if case["op"] == "linear_grad":
-        p = 4 if case["grads"] == "fp32" else 2
-        return {"bytes": 4 * m * k + 2 * m * n + weights + p * n * k + p * n, "flops": 4 * m * n * k}
+        return {"bytes": 4 * m * k + 2 * m * n + weights + 2 * n * k + 2 * n, "flops": 4 * m * n * k}
     extra = 4 * case["groups"] * k if case["op"] == "norm_linear" else 0
     return {"bytes": 2 * m * k + weights + 2 * n + 2 * m * n + extra, "flops": 2 * m * n * k}
 
