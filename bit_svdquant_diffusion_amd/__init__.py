@@ -22,6 +22,9 @@ __all__ = [
     "awq_packed_bytes", "awq_pack", "awq_unpack", "awq_to_device", "awq_forward",
     "pack_weights_gpu", "calibrate_alpha", "to_host", "mlp_workspace_bytes", "mlp_fused", "mlp_forward",
     "MLP_AUTO", "MLP_UNFUSED", "stage1_outputs",
+    "layer_norm_forward", "layer_norm_backward",
+    "fp8_packed_bytes", "fp8_pack", "fp8_forward", "fp8_norm_forward", "fp8_backward", "fp8_quantize",
+    "fp8_workspace_bytes", "fp8_norm_workspace_bytes", "fp8_backward_workspace_bytes", "Fp8Linear",
 ]
 
 FMT_INT4 = 0
@@ -40,6 +43,10 @@ EXPORTED_SYMBOLS = [
     "svdq_awq_packed_bytes", "svdq_awq_pack", "svdq_awq_unpack", "svdq_awq_forward",
     "svdq_pack_gpu_workspace_bytes", "svdq_pack_weights_gpu", "svdq_calibrate_workspace_bytes",
     "svdq_calibrate_alpha", "svdq_mlp_workspace_bytes", "svdq_mlp_fused", "svdq_mlp_forward",
+    "svdq_layer_norm_forward", "svdq_layer_norm_backward_workspace_bytes", "svdq_layer_norm_backward",
+    "svdq_fp8_packed_bytes", "svdq_fp8_pack", "svdq_fp8_workspace_bytes", "svdq_fp8_forward",
+    "svdq_fp8_norm_workspace_bytes", "svdq_fp8_norm_forward", "svdq_fp8_backward_workspace_bytes",
+    "svdq_fp8_backward", "svdq_fp8_quantize",
 ]
 
 # svdq_mlp_forward modes
@@ -85,6 +92,27 @@ class AwqSizes(ctypes.Structure):
 
 class AwqPacked(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in AWQ_FIELDS]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("channels", "dtype", "param_dtype", "one_plus", "groups")] + \
+               [("eps", ctypes.c_float), ("rows_per_group", ctypes.c_int64)]
+
+
+class Fp8Desc(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32)]
+
+
+FP8_FIELDS = ("q", "s", "qt", "st", "bias")
+
+
+class Fp8Sizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in FP8_FIELDS]
+
+
+class Fp8Packed(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in FP8_FIELDS]
+
 
 _lib = None
 
@@ -134,6 +162,20 @@ def lib() -> ctypes.CDLL:
         "svdq_gemm": [D, P(Packed), vp, sz, i64, vp, vp],
         "svdq_unpack_workspace": [D, i64, vp, sz, vp, vp, vp],
         "svdq_debug_int4_group_sums": [D, P(Packed), vp, sz, i64, i64, i64, i64, i64, vp, vp],
+        "svdq_layer_norm_forward": [P(NormDesc), vp, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp, vp],
+        "svdq_layer_norm_backward_workspace_bytes": [P(NormDesc), i64, P(sz)],
+        "svdq_layer_norm_backward": [P(NormDesc), vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp,
+                                     ctypes.c_int32, vp, sz, vp],
+        "svdq_fp8_packed_bytes": [P(Fp8Desc), P(Fp8Sizes)],
+        "svdq_fp8_pack": [P(Fp8Desc), vp, ctypes.c_int32, P(Fp8Packed), vp],
+        "svdq_fp8_workspace_bytes": [P(Fp8Desc), i64, P(sz)],
+        "svdq_fp8_forward": [P(Fp8Desc), P(Fp8Packed), vp, i64, vp, vp, sz, vp],
+        "svdq_fp8_norm_workspace_bytes": [P(Fp8Desc), i64, P(sz)],
+        "svdq_fp8_norm_forward": [P(NormDesc), vp, i64, vp, i64, P(Fp8Desc), P(Fp8Packed), vp, i64, vp, vp, vp, vp, sz,
+                                  vp],
+        "svdq_fp8_backward_workspace_bytes": [P(Fp8Desc), i64, P(sz)],
+        "svdq_fp8_backward": [P(Fp8Desc), P(Fp8Packed), vp, vp, i64, vp, vp, vp, vp, sz, vp],
+        "svdq_fp8_quantize": [vp, i64, ctypes.c_int32, vp, vp, vp],
         "svdq_mlp_workspace_bytes": [D, D, i64, P(sz), P(sz)],
         "svdq_mlp_fused": [D, D, i64, P(ctypes.c_int32)],
         "svdq_mlp_forward": [D, P(Packed), D, P(Packed), vp, i64, vp, vp, sz, ctypes.c_int32, vp],
@@ -593,3 +635,334 @@ class SVDQLinear:
         if self._ws is None or self._ws.numel() < need or self._ws.device != x.device:
             self._ws = torch.empty(need, dtype=torch.uint8, device=x.device)
         return linear_forward(self.layer, self.dev, x, y=y, workspace=self._ws, stream=stream)
+
+
+# ----------------------------------------------------------------------------
+# Layer norm and the FP8 linear, forward and backward
+# ----------------------------------------------------------------------------
+_DT_CODES = None
+
+
+def _dt(dtype) -> int:
+    """svdq_dtype of a torch dtype."""
+    global _DT_CODES
+    if _DT_CODES is None:
+        import torch
+        _DT_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if dtype not in _DT_CODES:
+        raise ValueError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
+    return _DT_CODES[dtype]
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(device, *tensors):
+    """Every given tensor lives on `device`, a GPU."""
+    _need(device.type == "cuda", "the tensors must be on a GPU")
+    for t in tensors:
+        _need(t is None or t.device == device, f"tensors on {device} and {t.device if t is not None else None}")
+
+
+def _allocating(device, stream):
+    """Where outputs and workspaces of a call on `stream` are allocated: under
+    that stream, so that the allocator does not hand their memory to other work
+    while the call runs."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _call(name: str, device, stream, *args):
+    """The library's function on the tensors' device and the given stream (by
+    default the device's current one)."""
+    import torch
+    f = getattr(lib(), name)
+    s = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    _check(st, name)
+
+
+def _rows(t, what: str):
+    """(pointer, row stride) of a matrix whose rows are contiguous."""
+    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{what}: a matrix with contiguous rows")
+    return t.data_ptr(), max(t.stride(0), t.shape[1])
+
+
+def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype):
+    """(NormDesc, weight pointer, stride, bias pointer, stride) of [C] or [groups][C] parameters."""
+    some = weight if weight is not None else bias
+    groups, pdt, ptrs = 1, dtype, []
+    if some is not None:
+        pdt = some.dtype
+        groups = 1 if some.dim() == 1 else some.shape[0]
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            ptrs += [None, C]
+            continue
+        _need(t.dtype == pdt and t.shape[-1] == C and (groups if t.dim() == 2 else 1) == groups and t.dim() in (1, 2)
+              and (t.dim() == 1 or t.shape[0] == groups), f"{what}: [channels] or [groups][channels], both of one type")
+        _need(C <= 1 or t.stride(-1) == 1, f"{what}: contiguous channels")
+        ptrs += [t.data_ptr(), max(t.stride(0), C) if t.dim() == 2 else C]
+    if rows_per_group is None:
+        rows_per_group = max(1, -(-M // groups))
+    return NormDesc(C, _dt(dtype), _dt(pdt), 1 if one_plus else 0, groups, float(eps), int(rows_per_group)), *ptrs
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: bool = False, rows_per_group=None,
+                       y=None, stream=None):
+    """svdq_layer_norm_forward: (y, mean, rstd) of the rows of x [M][C]
+    (bfloat16, float16 or float32; rows contiguous, any row stride).
+
+    weight and bias: [C], or [groups][C] for rows in groups of rows_per_group
+    (default: the rows split evenly); the gain is weight, or 1 + weight with
+    one_plus. mean and rstd are float32 [M], for layer_norm_backward."""
+    import torch
+    _on_device(x.device, weight, bias, y)
+    xp, ldx = _rows(x, "x")
+    M, C = x.shape
+    d, wp, ldw, bp, ldb = _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
+    with _allocating(x.device, stream):
+        if y is None:
+            y = torch.empty((M, C), dtype=x.dtype, device=x.device)
+        stats = torch.empty((2, M), dtype=torch.float32, device=x.device)
+    _need(y.dtype == x.dtype and y.shape == x.shape, "y: the shape and type of x")
+    yp, ldy = _rows(y, "y")
+    sp = stats.data_ptr()
+    _call("svdq_layer_norm_forward", x.device, stream, ctypes.byref(d), xp, ldx, wp, ldw, bp, ldb, M, yp, ldy, sp,
+          sp + 4 * M)
+    return y, stats[0], stats[1]
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, rows_per_group=None, groups=None,
+                        grad_dtype=None, param_grads: bool = True, dx=None, stream=None):
+    """svdq_layer_norm_backward: (dx, dweight, dbias) for dy [M][C], from the
+    forward's x, mean, rstd, weight and grouping. dweight and dbias are
+    [groups][C] ([C] for a [C] or absent weight) of grad_dtype (default: the
+    weight's type, float32 without one); None without param_grads."""
+    import torch
+    _on_device(x.device, dy, mean, rstd, weight, dx)
+    M, C = x.shape
+    _need(dy.shape == x.shape and dy.dtype == x.dtype, "dy: the shape and type of x")
+    for t in (mean, rstd):
+        _need(t.dtype == torch.float32 and t.shape == (M,) and t.is_contiguous(), "mean, rstd: float32 [rows]")
+    d, wp, ldw, _, _ = _norm_params(C, weight, None, one_plus, 0.0, rows_per_group, M, x.dtype)
+    flat = weight is None and groups is None or weight is not None and weight.dim() == 1
+    if weight is None and groups is not None:
+        d.groups = int(groups)
+        d.rows_per_group = int(rows_per_group) if rows_per_group is not None else max(1, -(-M // int(groups)))
+    gdt = grad_dtype if grad_dtype is not None else (weight.dtype if weight is not None else torch.float32)
+    need = ctypes.c_size_t()
+    _check(lib().svdq_layer_norm_backward_workspace_bytes(ctypes.byref(d), M, ctypes.byref(need)),
+           "svdq_layer_norm_backward_workspace_bytes")
+    dw = db = ws = None
+    with _allocating(x.device, stream):
+        if dx is None:
+            dx = torch.empty((M, C), dtype=x.dtype, device=x.device)
+        if param_grads:
+            grads = torch.empty((2, d.groups, C), dtype=gdt, device=x.device)
+            dw, db = grads[0], grads[1]
+            if need.value:
+                ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    _need(dx.dtype == x.dtype and dx.shape == x.shape, "dx: the shape and type of x")
+    (dyp, lddy), (xp, ldx), (dxp, lddx) = _rows(dy, "dy"), _rows(x, "x"), _rows(dx, "dx")
+    _call("svdq_layer_norm_backward", x.device, stream, ctypes.byref(d), dyp, lddy, xp, ldx, wp, ldw, mean.data_ptr(),
+          rstd.data_ptr(), M, dxp, lddx, _ptr(dw), _ptr(db), _dt(gdt), _ptr(ws), need.value if ws is not None else 0)
+    if flat and param_grads:
+        dw, db = dw[0], db[0]
+    return dx, dw, db
+
+
+def _fp8_bytes(name: str, K: int, N: int, M: int) -> int:
+    out = ctypes.c_size_t()
+    _check(getattr(lib(), name)(ctypes.byref(Fp8Desc(int(K), int(N))), int(M), ctypes.byref(out)), name)
+    return out.value
+
+
+def fp8_workspace_bytes(K: int, N: int, M: int) -> int:
+    return _fp8_bytes("svdq_fp8_workspace_bytes", K, N, M)
+
+
+def fp8_norm_workspace_bytes(K: int, N: int, M: int) -> int:
+    return _fp8_bytes("svdq_fp8_norm_workspace_bytes", K, N, M)
+
+
+def fp8_backward_workspace_bytes(K: int, N: int, M: int) -> int:
+    return _fp8_bytes("svdq_fp8_backward_workspace_bytes", K, N, M)
+
+
+def fp8_packed_bytes(K: int, N: int) -> dict:
+    s = Fp8Sizes()
+    _check(lib().svdq_fp8_packed_bytes(ctypes.byref(Fp8Desc(int(K), int(N))), ctypes.byref(s)), "svdq_fp8_packed_bytes")
+    return {n: getattr(s, n) for n in FP8_FIELDS}
+
+
+def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, stream=None) -> dict:
+    """svdq_fp8_pack of a weight [N][K] (bfloat16, float16 or float32, on the
+    GPU): {"q", "s", "qt", "st", "bias"}, device tensors (qt and st, which the
+    gradient of x reads, are None without `transposed`). `out`: a dict of an
+    earlier call to overwrite, as after an update of w."""
+    import torch
+    _need(w.dim() == 2 and w.is_contiguous(), "w: a contiguous matrix [N][K]")
+    N, K = w.shape
+    sizes = fp8_packed_bytes(K, N)
+    if out is None:
+        with _allocating(w.device, stream):
+            def new(rows, name):
+                return torch.empty((rows, sizes[name] // rows), dtype=torch.uint8, device=w.device)
+            out = {"q": new(N, "q"), "s": new(-(-N // 128), "s"), "qt": new(K, "qt") if transposed else None,
+                   "st": new(-(-K // 128), "st") if transposed else None, "bias": None}
+    if bias is not None:
+        out["bias"] = bias.to(torch.bfloat16).contiguous()
+    _on_device(w.device, *out.values())
+    p = _fp8_struct(K, N, out)
+    _call("svdq_fp8_pack", w.device, stream, ctypes.byref(Fp8Desc(K, N)), w.data_ptr(), _dt(w.dtype), ctypes.byref(p))
+    return out
+
+
+def _fp8_struct(K: int, N: int, dev: dict) -> Fp8Packed:
+    """The buffers of a layer, each of at least its size."""
+    rk, rn = -(-K // 128), -(-N // 128)
+    least = {"q": N * K, "s": rn * (-(-rk // 4) * 4), "qt": N * K, "st": rk * (-(-rn // 4) * 4), "bias": N}
+    ptrs = []
+    for n in FP8_FIELDS:
+        t = dev.get(n)
+        if t is None:
+            ptrs.append(None)
+            continue
+        _need(t.is_contiguous() and t.numel() >= least[n] and t.element_size() == (2 if n == "bias" else 1),
+              f"fp8 layer: {n} must be contiguous with {least[n]} elements")
+        ptrs.append(t.data_ptr())
+    return Fp8Packed(*ptrs)
+
+
+def _bf16_rows(t, cols: int, what: str):
+    import torch
+    _need(t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[1] == cols and t.is_contiguous(),
+          f"{what}: a contiguous bfloat16 matrix of {cols} columns")
+
+
+def fp8_forward(K: int, N: int, dev: dict, x, y=None, workspace=None, stream=None):
+    """y[M][N] bf16 = FP8 layer(x[M][K] bf16) via svdq_fp8_forward."""
+    import torch
+    _on_device(x.device, y, workspace, *dev.values())
+    _bf16_rows(x, K, "x")
+    M = x.shape[0]
+    need = fp8_workspace_bytes(K, N, M)
+    with _allocating(x.device, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _bf16_rows(y, N, "y")
+    _need(y.shape[0] == M, "y: as many rows as x")
+    p = _fp8_struct(K, N, dev)
+    _call("svdq_fp8_forward", x.device, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(p), x.data_ptr(), M,
+          y.data_ptr(), _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return y
+
+
+def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: float = 1e-6, one_plus: bool = False,
+                     rows_per_group=None, y=None, workspace=None, stats: bool = False, stream=None):
+    """y[M][N] = FP8 layer(layer norm(x)) via svdq_fp8_norm_forward, the norm's
+    parameters as in layer_norm_forward (`bias` is the norm's; the layer's own
+    is in dev). With stats: (y, mean, rstd)."""
+    import torch
+    _on_device(x.device, weight, bias, y, workspace, *dev.values())
+    _bf16_rows(x, K, "x")
+    M = x.shape[0]
+    d, wp, ldw, bp, ldb = _norm_params(K, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
+    need = fp8_norm_workspace_bytes(K, N, M)
+    mean = rstd = None
+    with _allocating(x.device, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if stats:
+            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device)
+    _bf16_rows(y, N, "y")
+    _need(y.shape[0] == M, "y: as many rows as x")
+    p = _fp8_struct(K, N, dev)
+    _call("svdq_fp8_norm_forward", x.device, stream, ctypes.byref(d), wp, ldw, bp, ldb, ctypes.byref(Fp8Desc(K, N)),
+          ctypes.byref(p), x.data_ptr(), M, y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(workspace),
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return (y, mean, rstd) if stats else y
+
+
+def fp8_backward(K: int, N: int, dev: dict, x, dy, need=(True, True, True), workspace=None, stream=None):
+    """svdq_fp8_backward: (dx [M][K], dw [N][K], db [N]), bf16, of fp8_forward
+    for dy [M][N] bf16; None where `need` says no. Without dx, dev may lack qt
+    and st; without dw, x may be None."""
+    import torch
+    _on_device(dy.device, x, workspace, *dev.values())
+    _bf16_rows(dy, N, "dy")
+    M = dy.shape[0]
+    if x is not None:
+        _bf16_rows(x, K, "x")
+        _need(x.shape[0] == M, "x: as many rows as dy")
+    size = fp8_backward_workspace_bytes(K, N, M)
+    dx = dw = db = None
+    with _allocating(dy.device, stream):
+        if need[0]:
+            dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+        if need[1]:
+            dw = torch.empty((N, K), dtype=torch.bfloat16, device=dy.device)
+        if need[2]:
+            db = torch.empty(N, dtype=torch.bfloat16, device=dy.device)
+        if workspace is None and size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    p = _fp8_struct(K, N, dev)
+    _call("svdq_fp8_backward", dy.device, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(p), _ptr(x), dy.data_ptr(), M,
+          _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace),
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return dx, dw, db
+
+
+def fp8_quantize(x, stream=None):
+    """svdq_fp8_quantize: (codes uint8 [M][K padded to 128], scale bytes uint8
+    [blocks / 4][M][4]) of x bf16 [M][K]."""
+    import torch
+    _on_device(x.device)
+    _bf16_rows(x, x.shape[1], "x")
+    M, K = x.shape
+    nb = -(-K // 128)
+    with _allocating(x.device, stream):
+        q = torch.empty((M, nb * 128), dtype=torch.uint8, device=x.device)
+        s = torch.zeros((-(-nb // 4), M, 4), dtype=torch.uint8, device=x.device)
+    _call("svdq_fp8_quantize", x.device, stream, x.data_ptr(), M, K, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+class Fp8Linear:
+    """An FP8 linear in device memory: call it on bf16 input; `backward` gives
+    its gradients; `update` quantizes a new weight into the same buffers."""
+
+    def __init__(self, w, bias=None, trainable: bool = True):
+        self.N, self.K = w.shape
+        self.dev = fp8_pack(w, bias, transposed=trainable)
+
+    def __call__(self, x, y=None, stream=None):
+        return fp8_forward(self.K, self.N, self.dev, x, y=y, stream=stream)
+
+    def after_norm(self, x, weight=None, bias=None, eps: float = 1e-6, one_plus: bool = False, rows_per_group=None,
+                   stats: bool = False, stream=None):
+        """The layer on layer_norm_forward(x, weight, bias, ...), in one call."""
+        return fp8_norm_forward(self.K, self.N, self.dev, x, weight, bias, eps, one_plus, rows_per_group, stats=stats,
+                                stream=stream)
+
+    def backward(self, x, dy, need=(True, True, True), stream=None):
+        return fp8_backward(self.K, self.N, self.dev, x, dy, need, stream=stream)
+
+    def update(self, w, bias=None, stream=None):
+        fp8_pack(w, bias, out=self.dev, stream=stream)

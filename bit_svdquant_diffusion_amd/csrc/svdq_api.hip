@@ -28,9 +28,11 @@ std::atomic<int> g_dev_cus[kMaxDevices];     // compute units of each ready devi
 std::atomic<void*> g_dev_scratch[kMaxDevices];   // device address of `scratch` on each ready device
 std::mutex g_dev_mu;
 
+}  // namespace
+
 // One-time set-up per device, with that device current: the gfx950 check,
 // the kernels' LDS attributes and the address of this device's `scratch`.
-svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr) {
+svdq_status check_device(int* cus, void** scratch_ptr) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return SVDQ_ERR_DEVICE;
   int s = g_dev_state[dev].load(std::memory_order_acquire);
@@ -43,6 +45,7 @@ svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr) {
       bool ok = hipGetDeviceProperties(&p, dev) == hipSuccess &&
                 std::strncmp(p.gcnArchName, "gfx950", 6) == 0 && prepare_gemm_mxfp4() == hipSuccess &&
                 prepare_gemm_int4() == hipSuccess && prepare_stage1() == hipSuccess && prepare_awq() == hipSuccess &&
+                prepare_fp8() == hipSuccess &&
                 hipGetSymbolAddress(&sp, HIP_SYMBOL(scratch)) == hipSuccess && sp != nullptr;
       s = ok ? 1 : 2;
       if (ok) {
@@ -57,6 +60,8 @@ svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr) {
   if (scratch_ptr) *scratch_ptr = g_dev_scratch[dev].load(std::memory_order_relaxed);
   return SVDQ_OK;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -194,11 +199,15 @@ bool sync_debug() {
   return v;
 }
 
+}  // namespace
+
 svdq_status after_launch(hipError_t e, hipStream_t s) {
   if (e != hipSuccess) return SVDQ_ERR_DEVICE;
   if (sync_debug() && hipStreamSynchronize(s) != hipSuccess) return SVDQ_ERR_DEVICE;
   return SVDQ_OK;
 }
+
+namespace {
 
 // Logical views of a stage-1 workspace, the layouts of svdq_unpack_workspace:
 // codes int8 [M][K] (INT4 values, or E2M1 code bits), scales fp32 [M][K/64]

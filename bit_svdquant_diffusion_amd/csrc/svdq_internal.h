@@ -98,6 +98,88 @@ struct AwqArgs {
 hipError_t launch_awq(const AwqArgs& a, int num_cus, hipStream_t st);
 hipError_t prepare_awq();
 
+// Layer norm and its gradients (svdq_norm.hip); strides in elements
+struct NormArgs {
+  int dtype, pdtype, one_plus, C, G;
+  float eps;
+  int64_t M, rpg;
+  const void* x;
+  int64_t ldx;
+  const void* w;   // [G][ldw] or null (gain 1)
+  int64_t ldw;
+  const void* b;   // [G][ldb] or null (0)
+  int64_t ldb;
+  void* y;
+  int64_t ldy;
+  float* mean;     // [M], may be null in the forward
+  float* rstd;
+  // q != nullptr (bf16 rows): instead of y, its E4M3 codes [M][Kp] and block
+  // scales (fp8_scale_index over qs_rows rows)
+  uint8_t* q;
+  uint8_t* qs;
+  int Kp;
+  int64_t qs_rows;
+};
+struct NormGradPlan;
+struct NormGradArgs {
+  NormArgs f;        // x, weight, mean and rstd
+  const void* dy;
+  int64_t lddy;
+  void* dx;
+  int64_t lddx;
+  void* dw;          // [G][C] of gdtype, may be null
+  void* db;
+  int gdtype;
+  float* part;       // [G][runs][2][C], null when a group is one run
+};
+hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st);
+hipError_t launch_norm_grad(const NormGradArgs& g, const NormGradPlan& p, hipStream_t st);
+
+// E4M3 quantizers (svdq_fp8_quant.hip)
+hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, hipStream_t st);
+// one or two matrices bf16 [M][C] quantized along M (codes [C][round128(M)]);
+// the first also along C (row codes) and summed over M where asked
+struct Fp8QuantT {
+  const uint16_t* x;
+  int C;
+  uint8_t* qt;       // [C][round128(M)], or null
+  uint8_t* st;
+  uint8_t* q;        // [M][round128(C)], or null
+  uint8_t* s;
+  float* sums;       // [round128(M)/128][C], or null
+};
+hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M, hipStream_t st);
+hipError_t launch_fp8_bias_grad(const float* sums, int64_t blocks, int N, uint16_t* db, hipStream_t st);
+hipError_t launch_fp8_zero(void* p, size_t bytes, int num_cus, hipStream_t st);   // bytes % 4 == 0
+hipError_t launch_fp8_pack(const void* w, int dtype, int K, int N, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st,
+                           hipStream_t stream);
+
+// out[a_rows][b_rows] = A B^T (+ bias per column): E4M3 codes with the
+// contracted channels contiguous and an E8M0 scale per row and 128 of them
+// (A; B as well with b_row_scales), or per 128 x 128 block of B
+struct Fp8Gemm {
+  const uint8_t* a;
+  const uint8_t* as;
+  int64_t a_rows, lda;
+  const uint8_t* b;
+  const uint8_t* bs;
+  int b_rows;
+  int64_t ldb;
+  int b_row_scales;
+  int64_t K;           // contracted channels
+  const uint16_t* bias;
+  uint16_t* out;       // bf16 [a_rows][b_rows]
+  const uint16_t* x;   // few tokens: A as bf16 rows [a_rows][K], quantized by the product itself (a null)
+};
+bool fp8_gemm_small_fits(const Fp8Gemm& g);
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st);
+hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st);
+hipError_t prepare_fp8();
+
+// shared by the files with C entry points (svdq_api.hip)
+svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr);
+svdq_status after_launch(hipError_t e, hipStream_t s);
+
 // measured ceilings of the part (not part of the layer): an MFMA-only loop
 // (kind 0 scaled FP4, 1 i8, 2 bf16; *flops = its flop count) and a device copy
 hipError_t launch_mfma_peak(int kind, int constant, int iters, int grid, float* sink, hipStream_t st, double* flops);

@@ -170,5 +170,81 @@ inline size_t l1_index(int K, int r32, int k, int col) {
   return (((((size_t)s * 4 + w) * (r32 / 16) + cb) * 2 + t) * 64 + (16 * j + c)) * 8 + e;
 }
 
+// ---------------------------------------------------------------------------
+// FP8 (E4M3) operands: codes row-major, contracted channels contiguous, and
+// one E8M0 byte per row and 128 channels; four blocks' bytes of a row are a
+// word: [ceil(blocks / 4)][rows][4].
+// ---------------------------------------------------------------------------
+constexpr int kFp8Block = 128;
+SVDQ_HD inline int64_t round128(int64_t v) { return (v + 127) / 128 * 128; }
+SVDQ_HD inline size_t fp8_scale_index(int64_t rows, int64_t row, int64_t block) {
+  return ((size_t)(block / 4) * rows + row) * 4 + block % 4;
+}
+inline size_t fp8_scale_bytes(int64_t rows, int64_t channels) {
+  return (size_t)((round128(channels) / kFp8Block + 3) / 4) * rows * 4;
+}
+// bytes of a row of an FP8 weight's 128 x 128 block scales
+SVDQ_HD SVDQ_HD inline int fp8_block_row(int channels) { return ((channels + 127) / 128 + 3) / 4 * 4; }
+
+inline svdq_status check_fp8_desc(const svdq_fp8_desc* d) {
+  if (!d) return SVDQ_ERR_NULL;
+  if (d->K <= 0 || d->N <= 0 || d->K % 16 != 0 || d->N % 16 != 0 || d->K > 65536 || d->N > 65536)
+    return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
+// Workspace of the FP8 forward: the activations' codes [M][round128(K)] and
+// their scales.
+struct Fp8Ws {
+  size_t q, s, total;
+};
+inline Fp8Ws fp8_ws(const svdq_fp8_desc* d, int64_t M) {
+  Fp8Ws w;
+  w.q = 0;
+  w.s = align256((size_t)M * round128(d->K));
+  w.total = w.s + align256(fp8_scale_bytes(M, d->K));
+  return w;
+}
+// Workspace of the backward: dY's codes along the output channels [M][round128(N)],
+// dY^T [N][round128(M)] and X^T [K][round128(M)] along the tokens, their
+// scales, and dY's sums per 128 tokens fp32 [round128(M)/128][N].
+struct Fp8GradWs {
+  size_t q, s, yt, yts, xt, xts, db, total;
+};
+inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
+  Fp8GradWs w;
+  const int64_t mp = round128(M);
+  w.q = 0;
+  w.s = align256((size_t)M * round128(d->N));
+  w.yt = w.s + align256(fp8_scale_bytes(M, d->N));
+  w.yts = w.yt + align256((size_t)d->N * mp);
+  w.xt = w.yts + align256(fp8_scale_bytes(d->N, M));
+  w.xts = w.xt + align256((size_t)d->K * mp);
+  w.db = w.xts + align256(fp8_scale_bytes(d->K, M));
+  w.total = w.db + align256((size_t)(mp / 128) * d->N * 4);
+  return w;
+}
+
+// Layer-norm backward: every group's rows in `runs` runs of rows_per_run, one
+// workgroup each, about 512 in all (two per CU).
+struct NormGradPlan {
+  int runs;
+  int64_t rows_per_run;
+};
+inline NormGradPlan norm_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group) {
+  const int64_t rows = rows_per_group < M ? rows_per_group : M;
+  const int64_t live = M > 0 ? (M + rows_per_group - 1) / rows_per_group : 1;   // groups that have rows
+  int64_t runs = 512 / live;
+  if (runs > (rows + 7) / 8) runs = (rows + 7) / 8;   // at least eight rows each
+  if (runs < 1 || groups > 512) runs = 1;
+  NormGradPlan p;
+  p.rows_per_run = rows > 0 ? (rows + runs - 1) / runs : 1;
+  p.runs = rows > 0 ? (int)((rows + p.rows_per_run - 1) / p.rows_per_run) : 1;
+  return p;
+}
+inline size_t norm_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C) {
+  const NormGradPlan p = norm_grad_plan(M, groups, rows_per_group);
+  return p.runs > 1 ? (size_t)groups * p.runs * 2 * C * 4 : 0;
+}
 
 }  // namespace svdq

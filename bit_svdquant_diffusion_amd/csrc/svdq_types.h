@@ -1,0 +1,197 @@
+// Device-side element types of the layer norm: vectors of 16 bytes of bf16,
+// fp16 or fp32 read from and written to addresses aligned to one element
+// (gfx950 global loads and stores take any alignment), and wave-wide sums.
+#pragma once
+#include <string.h>
+
+#include "svdq_device.h"
+
+namespace svdq {
+
+struct Bf16 {
+  uint16_t bits;
+};
+typedef _Float16 Half;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<Half>(Half v) { return (float)v; }
+template <>
+__device__ __forceinline__ float to_f32<Bf16>(Bf16 v) { return __uint_as_float((uint32_t)v.bits << 16); }
+
+// one rounding, to nearest even (NaN stays NaN)
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ Half from_f32<Half>(float v) { return (Half)v; }
+template <>
+__device__ __forceinline__ Bf16 from_f32<Bf16>(float v) { return Bf16{__builtin_bit_cast(uint16_t, (__bf16)v)}; }
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);   // elements of a 16-byte vector
+
+// 16 bytes of a row, kept packed in four registers; at(i) unpacks an element
+template <typename T>
+struct Vec {
+  u32x4 w;
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[i]);
+    } else if constexpr (__is_same(T, Bf16)) {
+      return i & 1 ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
+    } else {
+      return (float)__builtin_bit_cast(Half, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+    }
+  }
+  // the roundings of v
+  __device__ __forceinline__ void set(const float (&v)[kVec<T>]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(v[i]);
+      else if constexpr (__is_same(T, Bf16))
+        w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+      else
+        w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (Half)v[2 * i]) |
+               ((uint32_t)__builtin_bit_cast(uint16_t, (Half)v[2 * i + 1]) << 16);
+    }
+  }
+};
+
+// elements [c, c + kVec) of a row of C elements: one 16-byte load, or, where
+// the row ends inside the vector, its elements one by one with zeros after
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* row, int c, int C) {
+  Vec<T> o;
+  o.w = u32x4{0, 0, 0, 0};
+  if (c + kVec<T> <= C) {
+    memcpy(&o.w, row + c, 16);
+  } else if (c < C) {
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i)
+      if (c + i < C) {
+        if constexpr (sizeof(T) == 4)
+          o.w[i] = __float_as_uint(row[c + i]);
+        else
+          o.w[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + i]) << (16 * (i & 1));
+      }
+  }
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* row, int c, int C, const Vec<T>& o) {
+  if (c + kVec<T> <= C) {
+    memcpy(row + c, &o.w, 16);
+  } else if (c < C) {
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i)
+      if (c + i < C) {
+        if constexpr (sizeof(T) == 4)
+          row[c + i] = __uint_as_float(o.w[i]);
+        else
+          row[c + i] = __builtin_bit_cast(T, (uint16_t)(o.w[i >> 1] >> (16 * (i & 1))));
+      }
+  }
+}
+
+// n consecutive parameters from element c on as floats, in any of the three
+// types (a uniform branch); zeros past C
+template <int n, typename P>
+__device__ __forceinline__ void load_params_as(const P* p, int c, int C, float* o) {
+  if (c + n <= C) {
+    P v[n];
+    memcpy(v, p + c, sizeof(v));
+#pragma unroll
+    for (int i = 0; i < n; ++i) o[i] = to_f32<P>(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) o[i] = c + i < C ? to_f32<P>(p[c + i]) : 0.f;
+  }
+}
+template <int n>
+__device__ __forceinline__ void load_params(const void* p, int dtype, int64_t at, int c, int C, float* o) {
+  if (dtype == SVDQ_DT_F32)
+    load_params_as<n>(static_cast<const float*>(p) + at, c, C, o);
+  else if (dtype == SVDQ_DT_BF16)
+    load_params_as<n>(static_cast<const Bf16*>(p) + at, c, C, o);
+  else
+    load_params_as<n>(static_cast<const Half*>(p) + at, c, C, o);
+}
+__device__ __forceinline__ void store_param(void* p, int dtype, int64_t at, float v) {
+  if (dtype == SVDQ_DT_F32)
+    static_cast<float*>(p)[at] = v;
+  else if (dtype == SVDQ_DT_BF16)
+    static_cast<Bf16*>(p)[at] = from_f32<Bf16>(v);
+  else
+    static_cast<Half*>(p)[at] = from_f32<Half>(v);
+}
+
+// Butterflies over 16 lanes with DPP moves (quad permutes for distances 1 and
+// 2, then the mirrored half row and row, whose lanes hold the other halves'
+// sums), then over the rows with the gfx950 lane swaps: every lane ends with
+// the result, in one fixed order.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_mov(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+__device__ __forceinline__ float add_dpp16(float v) {
+  v += __uint_as_float(dpp_mov<kDppXor1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<kDppXor2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<kDppHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<kDppMirror>(__float_as_uint(v)));
+  return v;
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// the largest of 8 lanes' (a half row's) or 16 lanes' (a row's) values
+__device__ __forceinline__ uint32_t max_dpp8(uint32_t v) {
+  v = umax(v, dpp_mov<kDppXor1>(v));
+  v = umax(v, dpp_mov<kDppXor2>(v));
+  return umax(v, dpp_mov<kDppHalfMirror>(v));
+}
+__device__ __forceinline__ uint32_t max_dpp16(uint32_t v) {
+  v = max_dpp8(v);
+  return umax(v, dpp_mov<kDppMirror>(v));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp16(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// ---------------------------------------------------------------------------
+// E4M3 blocks of 128 with a power-of-two scale
+// ---------------------------------------------------------------------------
+// The exponent of a block whose largest magnitude has the float bits `amax`
+// (sign cleared): the least e >= -126 with amax 2^-e <= 448 = 1.75 2^8. An
+// infinity or a NaN (the largest bits of all) gives 120; its element then
+// becomes the NaN code, and so do the sums it enters.
+__device__ __forceinline__ int e4m3_exponent(uint32_t amax) {
+  const int e = (int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < -126 ? -126 : (e > 120 ? 120 : e);
+}
+// E4M3 codes of four values times 2^-e: v_cvt_scalef32_pk_fp8_f32 divides by
+// the (normal) scale exactly and rounds once, to nearest even; |v| 2^-e <= 448
+// never overflows; infinities and NaN become the NaN code.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float scale) {
+  typedef __attribute__((ext_vector_type(2))) short s16x2;
+  s16x2 r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// the larger magnitude bits of a packed bf16 pair and m (as float bits)
+__device__ __forceinline__ uint32_t amax_bf16x2(uint32_t m, uint32_t w) {
+  m = umax(m, (w << 16) & 0x7fffffffu);
+  return umax(m, w & 0x7fff0000u);
+}
+
+}  // namespace svdq

@@ -498,6 +498,178 @@ SVDQ_API svdq_status svdq_awq_forward(const svdq_awq_desc* desc, const svdq_awq_
                                       int64_t M, uint16_t* y, void* hip_stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Layer norm, forward and backward: the norm in front of a transformer
+ * block's linears, with parameters of its own or modulated per sample (the
+ * adaptive norm whose scale and shift are slices of the output of the W4A16
+ * modulation layer above).
+ *
+ *   mean = sum_c x / C, rstd = 1 / sqrt(sum_c (x - mean)^2 / C + eps),
+ *   xhat = (x - mean) rstd,  y = xhat g + b,
+ *
+ * g = weight, or 1 + weight (one_plus), or 1 where weight is NULL; b = bias, or
+ * 0 where bias is NULL. Row m belongs to group m / rows_per_group: its weight
+ * and bias start at weight + group * ldw and bias + group * ldb. Statistics and
+ * sums are in fp32 from one read of the row (mean first, then the squares of
+ * the differences); y is rounded once, from fp32.
+ *
+ * dtype is the type of x, y, dy and dx, param_dtype that of weight and bias.
+ * Strides (ldx, ...) are in elements between rows, at least `channels`; a row's
+ * elements are contiguous. Pointers need the alignment of one element.
+ * Limits: 1 <= channels <= 16384, 1 <= groups <= 2^24, rows_per_group >= 1,
+ * 0 <= M <= 2^24, M <= groups * rows_per_group, eps >= 0. M == 0 launches no
+ * forward kernel; the backward then writes zero parameter gradients.
+ * A row that holds an infinity or a NaN gives NaN in that row alone (and in
+ * its group's parameter gradients).
+ * ---------------------------------------------------------------------------
+ */
+typedef enum { SVDQ_DT_BF16 = 0, SVDQ_DT_F16 = 1, SVDQ_DT_F32 = 2 } svdq_dtype;
+
+typedef struct {
+  int32_t channels, dtype, param_dtype, one_plus, groups;
+  float eps;
+  int64_t rows_per_group;
+} svdq_norm_desc;
+
+/*
+ * y = layer norm of the M rows of x, on hip_stream; mean and rstd fp32 [M]
+ * (each may be NULL) are what the backward reads. y may be x itself (with the
+ * same stride), not a part of it. One kernel, no workspace.
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE (a size outside the limits, a stride
+ * below `channels`, a pointer not aligned to its element), SVDQ_ERR_FORMAT
+ * (unknown type), SVDQ_ERR_DEVICE.
+ */
+SVDQ_API svdq_status svdq_layer_norm_forward(const svdq_norm_desc* desc, const void* x, int64_t ldx,
+                                             const void* weight, int64_t ldw, const void* bias, int64_t ldb, int64_t M,
+                                             void* y, int64_t ldy, float* mean, float* rstd, void* hip_stream);
+
+/*
+ * The gradients for dy of the forward with the same desc, x and weight (eps
+ * and bias do not enter), from its mean and rstd:
+ *   d = dy g,  dx = rstd (d - sum_c d / C - xhat sum_c(d xhat) / C)
+ *   dweight = sum over the group's rows of dy xhat, dbias = sum of dy,
+ * [groups][channels] contiguous of type grad_dtype; either may be NULL. A group
+ * without rows gets zeros. Sums in fp32 in an order fixed by M, groups and
+ * rows_per_group alone. dx may be dy or x (with the same stride).
+ * workspace: >= svdq_layer_norm_backward_workspace_bytes device bytes, 16-byte
+ * aligned, used when dweight or dbias is asked for; may be NULL where that is 0.
+ * Errors: as the forward, SVDQ_ERR_WORKSPACE.
+ */
+SVDQ_API svdq_status svdq_layer_norm_backward_workspace_bytes(const svdq_norm_desc* desc, int64_t M, size_t* out);
+SVDQ_API svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const void* dy, int64_t lddy, const void* x,
+                                              int64_t ldx, const void* weight, int64_t ldw, const float* mean,
+                                              const float* rstd, int64_t M, void* dx, int64_t lddx, void* dweight,
+                                              void* dbias, int32_t grad_dtype, void* workspace, size_t workspace_bytes,
+                                              void* hip_stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * FP8 linear, for the layers that 4 bits hurt, and its gradients:
+ *
+ *   y = q8(x) W^T + b,   W held as E4M3 codes.
+ *
+ * q8 takes blocks of 128 values v: with e the least whole number >= -126 for
+ * which max|v| 2^-e <= 448, the code of v is v 2^-e rounded to the nearest
+ * E4M3 value (ties to even), and stands for code 2^e; the scale byte is
+ * e + 127 (E8M0). An infinity or a NaN has the NaN code, which makes every sum
+ * it enters NaN. A power of two keeps the quotient exact, and CDNA4's
+ * block-scaled MFMA applies the scales itself. W has one scale per 128 x 128
+ * block; x is quantized in the call, per row and 128 channels. Sums are the
+ * matrix unit's fp32 sums. Last blocks may be short.
+ * Shapes: K % 16 == 0, N % 16 == 0, K, N <= 65536; 0 <= M <= 2^24 (forward),
+ * 2^20 (backward). Device pointers 16-byte aligned.
+ * Device layout, plain rows:
+ *   q    u8 [N][K]  E4M3 codes (OCP: no infinities, 0x7F and 0xFF are NaN)
+ *   s    u8 [ceil(N/128)][round4(ceil(K/128))]  scale bytes of the 128 x 128
+ *        blocks, rows padded to whole 4-byte words
+ *   qt   u8 [K][N], st u8 [ceil(K/128)][round4(ceil(N/128))]: the same
+ *        transposed, read by the gradient of x only; NULL for inference
+ *   bias bf16 [N], or NULL
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  int32_t K, N;
+} svdq_fp8_desc;
+
+typedef struct {
+  size_t q, s, qt, st, bias;
+} svdq_fp8_sizes;
+
+typedef struct {
+  uint8_t* q;
+  uint8_t* s;
+  uint8_t* qt;
+  uint8_t* st;
+  uint16_t* bias;
+} svdq_fp8_packed;
+
+/* Byte sizes of the buffers of an FP8 layer. Host only.
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE. */
+SVDQ_API svdq_status svdq_fp8_packed_bytes(const svdq_fp8_desc* desc, svdq_fp8_sizes* out);
+
+/*
+ * Quantizes a weight on the GPU: w [N][K] (device, of type dtype) to
+ * dev_out->q and s and, unless both are NULL, qt and st, in one read of w; on
+ * hip_stream, without synchronizing (a training step calls it after each
+ * update). The padding bytes of s and st are written as well. dev_out->bias is
+ * not touched. Errors: SVDQ_ERR_NULL (also one of qt and st alone),
+ * SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_DEVICE.
+ */
+SVDQ_API svdq_status svdq_fp8_pack(const svdq_fp8_desc* desc, const void* w, int32_t dtype,
+                                   const svdq_fp8_packed* dev_out, void* hip_stream);
+
+/*
+ * y bf16 [M][N] = layer(x bf16 [M][K]) on hip_stream. Up to 16 tokens one
+ * kernel streams the weight and quantizes the tokens itself (no workspace is
+ * used); above, one kernel quantizes x into the workspace and one multiplies.
+ * workspace: >= svdq_fp8_workspace_bytes(desc, M) device bytes (may be NULL
+ * where that is 0), contents ignored on entry.
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_WORKSPACE, SVDQ_ERR_DEVICE.
+ */
+SVDQ_API svdq_status svdq_fp8_workspace_bytes(const svdq_fp8_desc* desc, int64_t M, size_t* out);
+SVDQ_API svdq_status svdq_fp8_forward(const svdq_fp8_desc* desc, const svdq_fp8_packed* dev, const uint16_t* x, int64_t M,
+                                      uint16_t* y, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * y = layer(bf16(layer norm(x))): svdq_layer_norm_forward followed by
+ * svdq_fp8_forward, the same bits, but the norm's kernel emits the codes and
+ * scales and its output never goes to memory. norm->channels == desc->K,
+ * norm->dtype is bf16. mean and rstd fp32 [M] may be NULL. workspace: >=
+ * svdq_fp8_norm_workspace_bytes(desc, M) device bytes.
+ * Errors: as the two calls.
+ */
+SVDQ_API svdq_status svdq_fp8_norm_workspace_bytes(const svdq_fp8_desc* desc, int64_t M, size_t* out);
+SVDQ_API svdq_status svdq_fp8_norm_forward(const svdq_norm_desc* norm, const void* weight, int64_t ldw, const void* bias,
+                                           int64_t ldb, const svdq_fp8_desc* desc, const svdq_fp8_packed* dev,
+                                           const uint16_t* x, int64_t M, uint16_t* y, float* mean, float* rstd,
+                                           void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Gradients of svdq_fp8_forward for dy bf16 [M][N]; each output may be NULL:
+ *   dx bf16 [M][K] = q8(dy) W, blocks along the output channels (reads qt, st)
+ *   dw [N][K]      = q8(dy)^T q8(x), blocks along the tokens (reads x)
+ *   db [N]         = the sum of dy over the tokens, in fp32 (no quantizing)
+ * dw and db bf16, overwritten (M == 0: zeros). The order of every sum is fixed
+ * by the shapes.
+ * workspace: >= svdq_fp8_backward_workspace_bytes(desc, M) device bytes.
+ * Errors: SVDQ_ERR_NULL (x may be NULL without dw, qt and st without dx),
+ * SVDQ_ERR_SHAPE, SVDQ_ERR_WORKSPACE, SVDQ_ERR_DEVICE.
+ */
+SVDQ_API svdq_status svdq_fp8_backward_workspace_bytes(const svdq_fp8_desc* desc, int64_t M, size_t* out);
+SVDQ_API svdq_status svdq_fp8_backward(const svdq_fp8_desc* desc, const svdq_fp8_packed* dev, const uint16_t* x,
+                                       const uint16_t* dy, int64_t M, uint16_t* dx, uint16_t* dw, uint16_t* db,
+                                       void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Test hook: q8 of x bf16 [M][K] as svdq_fp8_forward quantizes it: codes u8
+ * [M][round128(K)] (zeros past K) and scale bytes u8
+ * [ceil(ceil(K/128) / 4)][M][4], block b of row m at [b / 4][m][b % 4].
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_DEVICE.
+ */
+SVDQ_API svdq_status svdq_fp8_quantize(const uint16_t* x, int64_t M, int32_t K, uint8_t* codes, uint8_t* scales,
+                                       void* hip_stream);
+
+/*
  * Measured ceilings of the GPU (not part of the layer; the benchmark reports
  * the kernels against them beside the published peaks).
  * svdq_measure_mfma_peak enqueues one MFMA-only loop on every compute unit:
