@@ -220,7 +220,7 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
     return after_launch(launch_fp8_gemm_small(g, cus, s), s);
   }
   uint8_t* b = (uint8_t*)ws;
-  SVDQ_TRY(after_launch(launch_fp8_quant_rows(x, M, d->K, b + L.q, b + L.s, s), s));
+  SVDQ_TRY(after_launch(launch_fp8_quant_rows(x, M, d->K, b + L.q, b + L.s, false, s), s));
   g.a = b + L.q;
   g.as = b + L.s;
   return after_launch(launch_fp8_gemm(g, cus, s), s);
@@ -359,7 +359,7 @@ svdq_status svdq_fp8_quantize(const uint16_t* x, int64_t M, int32_t K, uint8_t* 
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return SVDQ_ERR_SHAPE;
   SVDQ_TRY(check_device());
   hipStream_t s = (hipStream_t)stream;
-  return after_launch(launch_fp8_quant_rows(x, M, K, codes, scales, s), s);
+  return after_launch(launch_fp8_quant_rows(x, M, K, codes, scales, true, s), s);
 }
 
 }  // extern "C"

@@ -48,111 +48,178 @@ struct Tile {
                 "every wave issues whole pairs of transfers of both operands");
 };
 
-// BROW: B has a scale per row (else per 128 x 128 block).
+// BROW: B has a scale per row (else per 128 x 128 block: one word per wave
+// and four stages, as a wave's channels lie in one block).
 template <int BM, int BN, int WGM, int WGN, bool BROW>
-__global__ __launch_bounds__(64 * WGM * WGN) void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1)))
+void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   typedef Tile<BM, BN, WGM, WGN> TL;
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int TM = TL::TM, TN = TL::TN;
+  constexpr int TM = TL::TM, TN = TL::TN, SB = BROW ? TN : 1;
+  static_assert(128 % TL::WN == 0, "a wave's channels lie in one block of 128");
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   const TileMap tm = map_tile((int)blockIdx.x, tiles_m, tiles_n, group_m);
-  const int64_t m0 = (int64_t)tm.tm * TL::BM;
-  const int n0 = tm.tn * TL::BN;
-  const int rows_a = (int)min((int64_t)TL::BM, g.a_rows - m0), rows_b = min(TL::BN, g.b_rows - n0);
-  const int KB = (int)((g.K + 127) / 128);
+  const int Ra = (int)g.a_rows, Rb = g.b_rows, K = (int)g.K, KB = (K + 127) / 128;
+  const int m0 = __builtin_amdgcn_readfirstlane(tm.tm) * TL::BM, n0 = __builtin_amdgcn_readfirstlane(tm.tn) * TL::BN;
+  const int lda = (int)g.lda, ldb = (int)g.ldb;
 
   // transfers: the tile's rows of each operand as a buffer resource (rows past
   // it read as zeros), a lane's chunk of the two kinds of row octets
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(g.a + m0 * g.lda), 0, (int)(rows_a * g.lda), kRsrcWord3);
-  const __amdgpu_buffer_rsrc_t rb =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(g.b + (int64_t)n0 * g.ldb), 0, (int)(rows_b * g.ldb), kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(g.a + (size_t)m0 * lda), 0, min(TL::BM, Ra - m0) * lda, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(g.b + (size_t)n0 * ldb), 0, min(TL::BN, Rb - n0) * ldb, kRsrcWord3);
   const int ck[2] = {(lane & 7) ^ (lane >> 4), (lane & 7) ^ (4 + (lane >> 4))};   // chunk for even and odd octets
   uint32_t va[2], vb[2];
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
-    va[o] = (uint32_t)((lane >> 3) * g.lda + 16 * ck[o]);
-    vb[o] = (uint32_t)((lane >> 3) * g.ldb + 16 * ck[o]);
+    va[o] = (uint32_t)((wave * TL::kOpsA * 8 + (lane >> 3)) * lda + 16 * ck[o]);
+    vb[o] = (uint32_t)((wave * TL::kOpsB * 8 + (lane >> 3)) * ldb + 16 * ck[o]);
   }
-  // the transfers of stage S
-#define SVDQ_ISSUE(S)                                                                                     \
-  {                                                                                                       \
-    uint8_t* slot_w = smem + ((S) & 1) * TL::kSlot;                                                       \
-    const int k0 = (S) * 128;                                                                             \
-    uint32_t xa[2] = {va[0], va[1]}, xb[2] = {vb[0], vb[1]};                                              \
-    if ((S) == KB - 1) { /* chunks past the contracted channels are zeros */                              \
-      _Pragma("unroll") for (int o = 0; o < 2; ++o) if (k0 + 16 * ck[o] >= g.K) xa[o] = xb[o] = kOutside; \
-    }                                                                                                     \
-    _Pragma("unroll") for (int i = 0; i < TL::kOpsA; ++i) {                                               \
-      const int oct = wave * TL::kOpsA + i;                                                               \
-      lds_transfer(ra, slot_w + oct * 1024, xa[i & 1], (int)(oct * 8 * g.lda) + k0);                      \
-    }                                                                                                     \
-    _Pragma("unroll") for (int i = 0; i < TL::kOpsB; ++i) {                                               \
-      const int oct = wave * TL::kOpsB + i;                                                               \
-      lds_transfer(rb, slot_w + TL::kSlotA + oct * 1024, xb[i & 1], (int)(oct * 8 * g.ldb) + k0);         \
-    }                                                                                                     \
+  // the transfers of stage S into slot S % 2; chunks past the contracted
+  // channels (and every chunk of a stage past the last) are zeros
+#define SVDQ_ISSUE(S)                                                                                       \
+  {                                                                                                         \
+    uint8_t* slot_w = smem + ((S) & 1) * TL::kSlot;                                                         \
+    const int k0 = (S) * 128;                                                                               \
+    uint32_t ta[2], tb[2];                                                                                  \
+    _Pragma("unroll") for (int o = 0; o < 2; ++o) {                                                         \
+      const bool out = 16 * ck[o] >= K - k0;                                                                \
+      ta[o] = out ? kOutside : va[o];                                                                       \
+      tb[o] = out ? kOutside : vb[o];                                                                       \
+    }                                                                                                       \
+    _Pragma("unroll") for (int i = 0; i < TL::kOpsA; ++i)                                                   \
+        lds_transfer(ra, slot_w + (wave * TL::kOpsA + i) * 1024, ta[i & 1], i * 8 * lda + k0);              \
+    _Pragma("unroll") for (int i = 0; i < TL::kOpsB; ++i)                                                   \
+        lds_transfer(rb, slot_w + TL::kSlotA + (wave * TL::kOpsB + i) * 1024, tb[i & 1], i * 8 * ldb + k0); \
   }
-  // scale words (four blocks' bytes) of this wave's rows
-  const uint32_t* pa = reinterpret_cast<const uint32_t*>(g.as);
-  const uint32_t* pb = reinterpret_cast<const uint32_t*>(g.bs);
-  int64_t sa_at[TM], sb_at[TN];
-#pragma unroll
-  for (int t = 0; t < TM; ++t) sa_at[t] = min(m0 + wm * TL::WM + 32 * t + lr, g.a_rows - 1);
-#pragma unroll
-  for (int t = 0; t < TN; ++t) {
-    const int n = min(n0 + wn * TL::WN + 32 * t + (BROW ? lr : 0), g.b_rows - 1);
-    sb_at[t] = BROW ? n : (n / 128) * ((KB + 3) / 4);
+  // scale words (four blocks' bytes) of this wave's rows, read one stage
+  // ahead: of A (and of B with a scale per row) the words of a lane's rows in
+  // the wave's 32-row blocks stand together
+  typedef uint32_t words_a __attribute__((ext_vector_type(TM)));
+  typedef uint32_t words_b __attribute__((ext_vector_type(TN)));
+  const int wrow = m0 + wm * TL::WM, wcol = n0 + wn * TL::WN;
+  const uint32_t* pa = reinterpret_cast<const uint32_t*>(g.as) + wrow / 128 * 128 + lr * 4 + wrow % 128 / 32;
+  const uint32_t* pb = reinterpret_cast<const uint32_t*>(g.bs) +
+                       (BROW ? wcol / 128 * 128 + lr * 4 + wcol % 128 / 32 : min(wcol, Rb - 1) / 128 * ((KB + 3) / 4));
+  const int ga = (Ra + 127) / 128 * 128, gb = BROW ? (Rb + 127) / 128 * 128 : 1;   // words between groups of four blocks
+  // (rows past the last 128 of the operand, whose outputs are not stored, read its first words)
+  if (wrow >= ga) pa = reinterpret_cast<const uint32_t*>(g.as) + lr * 4;
+  if (BROW && wcol >= gb) pb = reinterpret_cast<const uint32_t*>(g.bs) + lr * 4;
+  words_a na, ca;
+  words_b nb, cb;
+#define SVDQ_SCALES(S)                                                                                      \
+  {                                                                                                         \
+    const int grp = min((S), KB - 1) / 4;                                                                   \
+    na = *reinterpret_cast<const words_a*>(pa + (size_t)grp * ga);                                          \
+    if constexpr (BROW)                                                                                     \
+      nb = *reinterpret_cast<const words_b*>(pb + (size_t)grp * gb);                                        \
+    else                                                                                                    \
+      nb[0] = pb[grp];                                                                                      \
   }
-  // LDS offsets of this lane's fragment chunks: rows wm WM + lr (+ 32 t),
+  // LDS addresses of this lane's fragment chunks: rows wm WM + lr (+ 32 t),
   // chunk 4 step + 2 h + e at place chunk ^ (row / 2 % 8)
-  const uint32_t rd_a = (wm * TL::WM + lr) * 128, rd_b = TL::kSlotA + (wn * TL::WN + lr) * 128;
   const int sw = (lr >> 1) & 7;
+  uint32_t at_a[2][2], at_b[2][2];
+#pragma unroll
+  for (int st = 0; st < 2; ++st)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t c = (uint32_t)((4 * st + 2 * h + e) ^ sw) * 16;
+      at_a[st][e] = (wm * TL::WM + lr) * 128 + c;
+      at_b[st][e] = TL::kSlotA + (wn * TL::WN + lr) * 128 + c;
+    }
+#define SVDQ_READ(S, ST, FA, FB)                                                                            \
+  {                                                                                                         \
+    const uint8_t* slot = smem + ((S) & 1) * TL::kSlot;                                                     \
+    _Pragma("unroll") for (int t = 0; t < TN; ++t) {                                                        \
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + at_b[ST][0] + t * 4096);                      \
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + at_b[ST][1] + t * 4096);                      \
+      FB[t] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                                \
+    }                                                                                                       \
+    _Pragma("unroll") for (int t = 0; t < TM; ++t) {                                                        \
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + at_a[ST][0] + t * 4096);                      \
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + at_a[ST][1] + t * 4096);                      \
+      FA[t] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                                \
+    }                                                                                                       \
+  }
+#define SVDQ_MFMA(FA, FB)                                                                                   \
+  _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j)             \
+      acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(FB[j], FA[i], acc[j][i], 0, 0, 0,          \
+                                                                  (int)cb[BROW ? j : 0], 0, (int)ca[i]);
 
   f32x16 acc[TN][TM];
 #pragma unroll
   for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int i = 0; i < TM; ++i) acc[j][i] = f32x16{};
+  // Per stage: the first step's fragments are read while the previous stage's
+  // second half multiplies, the second step's while the first half does, and
+  // the next stage's transfers are issued among the first of these. The
+  // scheduling groups spread the reads and transfers evenly between the MFMAs
+  // (left to itself the compiler reuses the fragments' registers and reads
+  // only when the multiplications are through).
+#define SVDQ_SPREAD(PER)                                                                                    \
+  _Pragma("unroll") for (int q = 0; q < TM * TN; ++q) {                                                     \
+    __builtin_amdgcn_sched_group_barrier(0x100, PER, 0); /* LDS reads */                                    \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   /* MFMA */                                         \
+  }
+// the reads two to an MFMA (twice the average), the transfers after them
+#define SVDQ_SPREAD_ISSUE                                                                                   \
+  _Pragma("unroll") for (int q = 0; q < TM * TN / 2; ++q) {                                                 \
+    __builtin_amdgcn_sched_group_barrier(0x100, 4 * (TM + TN) / (TM * TN), 0);                              \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                      \
+  }                                                                                                         \
+  _Pragma("unroll") for (int q = 0; q < TM * TN / 2; ++q) {                                                 \
+    __builtin_amdgcn_sched_group_barrier(0x020, 2 * (TL::kOpsA + TL::kOpsB) / (TM * TN), 0);                \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                      \
+  }
+#define SVDQ_RING_WAIT                                                                                      \
+  __builtin_amdgcn_sched_barrier(0);                                                                        \
+  __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt 0, lgkmcnt 0: this stage's transfers, earlier reads */       \
+  __builtin_amdgcn_s_barrier();                                                                             \
+  __builtin_amdgcn_sched_barrier(0);
+#define SVDQ_SECOND_HALF(S)                                                                                 \
+  _Pragma("unroll") for (int t = 0; t < TM; ++t) ca[t] = wa[t] >> (8 * ((S) & 3));                          \
+  _Pragma("unroll") for (int t = 0; t < SB; ++t) cb[t] = wb[t] >> (8 * ((S) & 3));                          \
+  SVDQ_READ(S, 1, ya, yb)                                                                                   \
+  SVDQ_MFMA(xa, xb)                                                                                         \
+  SVDQ_SPREAD(2 * (TM + TN) / (TM * TN))
+  i32x8 xa[TM], xb[TN], ya[TM], yb[TN];
   SVDQ_ISSUE(0)
-  for (int s4 = 0; s4 < KB; s4 += 4) {
-    uint32_t sa[TM], sb[TN];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) sa[t] = pa[(int64_t)(s4 / 4) * g.a_rows + sa_at[t]];
-#pragma unroll
-    for (int t = 0; t < TN; ++t) sb[t] = BROW ? pb[(int64_t)(s4 / 4) * g.b_rows + sb_at[t]] : pb[s4 / 4 + sb_at[t]];
-#define SVDQ_STAGE(U)                                                                                     \
-  if (s4 + (U) < KB) {                                                                                    \
-    __builtin_amdgcn_sched_barrier(0);                                                                    \
-    __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt 0, lgkmcnt 0: this stage's transfers, earlier reads */   \
-    __builtin_amdgcn_s_barrier();                                                                         \
-    __builtin_amdgcn_sched_barrier(0);                                                                    \
-    if (s4 + (U) + 1 < KB) SVDQ_ISSUE(s4 + (U) + 1)                                                       \
-    const uint8_t* slot = smem + ((U) & 1) * TL::kSlot;                                                   \
-    _Pragma("unroll") for (int st = 0; st < 2; ++st) {                                                    \
-      i32x8 fa[TM], fb[TN];                                                                               \
-      const int c0 = ((4 * st + 2 * h) ^ sw) * 16, c1 = ((4 * st + 2 * h + 1) ^ sw) * 16;                 \
-      _Pragma("unroll") for (int t = 0; t < TM; ++t) {                                                    \
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + rd_a + t * 4096 + c0);                    \
-        const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + rd_a + t * 4096 + c1);                    \
-        fa[t] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                            \
-      }                                                                                                   \
-      _Pragma("unroll") for (int t = 0; t < TN; ++t) {                                                    \
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + rd_b + t * 4096 + c0);                    \
-        const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + rd_b + t * 4096 + c1);                    \
-        fb[t] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                            \
-      }                                                                                                   \
-      _Pragma("unroll") for (int j = 0; j < TN; ++j) _Pragma("unroll") for (int i = 0; i < TM; ++i)       \
-          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[j][i], 0, 0, (U),  \
-                                                                      (int)sb[j], (U), (int)sa[i]);       \
-    }                                                                                                     \
+  SVDQ_SCALES(0)
+  {
+    SVDQ_RING_WAIT
+    const words_a wa = na;
+    const words_b wb = nb;
+    SVDQ_ISSUE(1)
+    SVDQ_SCALES(1)
+    SVDQ_READ(0, 0, xa, xb)
+    SVDQ_SECOND_HALF(0)
   }
-    SVDQ_STAGE(0)
-    SVDQ_STAGE(1)
-    SVDQ_STAGE(2)
-    SVDQ_STAGE(3)
-#undef SVDQ_STAGE
+  for (int s = 1; s < KB; ++s) {
+    SVDQ_RING_WAIT
+    const words_a wa = na;
+    const words_b wb = nb;
+    SVDQ_SCALES(s + 1)
+    __builtin_amdgcn_sched_barrier(0);
+    SVDQ_READ(s, 0, xa, xb)
+    SVDQ_ISSUE(s + 1)
+    SVDQ_MFMA(ya, yb)
+    SVDQ_SPREAD_ISSUE
+    __builtin_amdgcn_sched_barrier(0);
+    SVDQ_SECOND_HALF(s)
   }
+  SVDQ_MFMA(ya, yb)
+#undef SVDQ_MFMA
+#undef SVDQ_READ
+#undef SVDQ_SCALES
+#undef SVDQ_SECOND_HALF
+#undef SVDQ_RING_WAIT
+#undef SVDQ_SPREAD
+#undef SVDQ_SPREAD_ISSUE
+#undef SVDQ_ISSUE
+  __builtin_amdgcn_s_waitcnt(0x0070);   // the transfers issued past the end land before the LDS is given up
   // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3).
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
@@ -225,7 +292,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void fp8_small_kernel(Fp8Gemm g) 
   for (int t = 0; t < TT; ++t) {
     const int64_t m = min((int64_t)(16 * t + r), g.a_rows - 1);
     arow[t] = QUANT ? reinterpret_cast<const uint8_t*>(g.x + m * g.K) : g.a + m * g.lda;
-    asc[t] = QUANT ? nullptr : g.as + m * 4;
+    asc[t] = QUANT ? nullptr : g.as + fp8_scale_index(g.a_rows, m, 0);
   }
   i32x4 wq[kRing][NT][2];
   u32x4 xv[kRing][TT][QUANT ? 4 : 2];
@@ -253,7 +320,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void fp8_small_kernel(Fp8Gemm g) 
     for (int t = 0; t < NT; ++t) ws[u][t] = wsc[t][kb];
     if constexpr (!QUANT) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t) xs[u][t] = asc[t][(int64_t)(kb / 4) * g.a_rows * 4 + kb % 4];
+      for (int t = 0; t < TT; ++t) xs[u][t] = asc[t][(size_t)(kb / 4) * round128(g.a_rows) * 4 + kb % 4];
     }
   };
   f32x4 acc[NT][TT];
@@ -334,7 +401,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void fp8_small_kernel(Fp8Gemm g) 
   }
 }
 
-typedef Tile<256, 256, 2, 4> TileL;
+typedef Tile<256, 256, 2, 2> TileL;
 typedef Tile<128, 128, 2, 2> TileM;
 
 template <class TL, bool BROW>

@@ -17,10 +17,10 @@ namespace {
 
 // Blocks along the rows: eight lanes a block, 16 channels (32 bytes) a lane;
 // a wave takes kUnits chunks of 1024 channels of consecutive (row, chunk)s,
-// all loads first. Channels in [K, Kp) get zero codes (K % 16 == 0: whole lanes).
+// all loads first. `plain` scales: [blocks / 4][M][4]. Channels in [K, Kp) get zero codes (K % 16 == 0: whole lanes).
 constexpr int kUnits = 2;
 __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, uint32_t units, uint32_t chunks, int64_t M, int K,
-                                                             int Kp, uint8_t* q, uint8_t* s) {
+                                                             int Kp, int plain, uint8_t* q, uint8_t* s) {
   const int lane = threadIdx.x & 63;
   const uint32_t u0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kUnits;
   u32x4 v[kUnits][2];
@@ -52,7 +52,9 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, 
     }
     if (u0 + u < units && at[u] < Kp) {
       *reinterpret_cast<u32x4*>(q + (size_t)row[u] * Kp + at[u]) = o;
-      if ((lane & 7) == 0) s[fp8_scale_index(M, row[u], at[u] / 128)] = (uint8_t)(e + 127);
+      const int kb = at[u] / 128;
+      if ((lane & 7) == 0)
+        s[plain ? ((size_t)(kb / 4) * M + row[u]) * 4 + kb % 4 : fp8_scale_index(M, row[u], kb)] = (uint8_t)(e + 127);
     }
   }
 }
@@ -240,11 +242,11 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const T* w, int K, int N,
 
 }  // namespace
 
-hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, hipStream_t st) {
+hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, bool plain, hipStream_t st) {
   const int Kp = (int)round128(K), chunks = (Kp + 1023) / 1024;
   const int64_t units = M * chunks;
   const int64_t grid = (units + 4 * kUnits - 1) / (4 * kUnits);
-  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, q, s);
+  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, q, s);
   return hipGetLastError();
 }
 

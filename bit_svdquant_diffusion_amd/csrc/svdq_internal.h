@@ -136,7 +136,8 @@ hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st);
 hipError_t launch_norm_grad(const NormGradArgs& g, const NormGradPlan& p, hipStream_t st);
 
 // E4M3 quantizers (svdq_fp8_quant.hip)
-hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, hipStream_t st);
+// (plain: the scale bytes as svdq_fp8_quantize documents them, not the product's order)
+hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, bool plain, hipStream_t st);
 // one or two matrices bf16 [M][C] quantized along M (codes [C][round128(M)]);
 // the first also along C (row codes) and summed over M where asked
 struct Fp8QuantT {

@@ -173,15 +173,18 @@ inline size_t l1_index(int K, int r32, int k, int col) {
 // ---------------------------------------------------------------------------
 // FP8 (E4M3) operands: codes row-major, contracted channels contiguous, and
 // one E8M0 byte per row and 128 channels; four blocks' bytes of a row are a
-// word: [ceil(blocks / 4)][rows][4].
+// word, and the words of rows r, r + 32, r + 64 and r + 96 of 128 rows (a lane
+// of the product's four 32-row blocks) stand together:
+// [ceil(blocks / 4)][round128(rows) / 128][32][4][4 bytes].
 // ---------------------------------------------------------------------------
 constexpr int kFp8Block = 128;
 SVDQ_HD inline int64_t round128(int64_t v) { return (v + 127) / 128 * 128; }
 SVDQ_HD inline size_t fp8_scale_index(int64_t rows, int64_t row, int64_t block) {
-  return ((size_t)(block / 4) * rows + row) * 4 + block % 4;
+  const int64_t at = row / 128 * 128 + row % 32 * 4 + row % 128 / 32;
+  return ((size_t)(block / 4) * round128(rows) + at) * 4 + block % 4;
 }
 inline size_t fp8_scale_bytes(int64_t rows, int64_t channels) {
-  return (size_t)((round128(channels) / kFp8Block + 3) / 4) * rows * 4;
+  return (size_t)((round128(channels) / kFp8Block + 3) / 4) * round128(rows) * 4;
 }
 // bytes of a row of an FP8 weight's 128 x 128 block scales
 SVDQ_HD SVDQ_HD inline int fp8_block_row(int channels) { return ((channels + 127) / 128 + 3) / 4 * 4; }

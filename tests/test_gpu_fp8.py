@@ -182,13 +182,8 @@ def test_norm_forward_is_the_composition(M, K, N, groups):
     assert torch.equal(mean, m2) and torch.equal(rstd, r2)
     if M > 16:
         assert torch.equal(y, S.fp8_forward(K, N, dev, h))
-    q, s = S.fp8_quantize(h)
-    nb = -(-K // 128)
+    q, _ = S.fp8_quantize(h)
     assert torch.equal(ws[:q.numel()].view(q.shape), q)
-    at = -(-q.numel() // 256) * 256
-    got = ws[at:at + s.numel()].view(s.shape)
-    for b in range(nb):
-        assert torch.equal(got[b // 4, :, b % 4], s[b // 4, :, b % 4])
     a, w = R.q8(h.double())[0], _weight(dev, K, N)
     bias = dev["bias"].double()
     _close(y, a @ w.t().contiguous() + bias, R.product_bound(a, w, bias), (M, K, N))
