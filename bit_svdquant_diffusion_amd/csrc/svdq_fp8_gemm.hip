@@ -76,23 +76,23 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
     va[o] = (uint32_t)((wave * TL::kOpsA * 8 + (lane >> 3)) * lda + 16 * ck[o]);
     vb[o] = (uint32_t)((wave * TL::kOpsB * 8 + (lane >> 3)) * ldb + 16 * ck[o]);
   }
-  // the transfers of stage S into slot S % 2; chunks past the contracted
+  // transfer i (of kOps) of stage S into slot S % 2; chunks past the contracted
   // channels (and every chunk of a stage past the last) are zeros
-#define SVDQ_ISSUE(S)                                                                                       \
-  {                                                                                                         \
-    uint8_t* slot_w = smem + ((S) & 1) * TL::kSlot;                                                         \
-    const int k0 = (S) * 128;                                                                               \
-    uint32_t ta[2], tb[2];                                                                                  \
-    _Pragma("unroll") for (int o = 0; o < 2; ++o) {                                                         \
-      const bool out = 16 * ck[o] >= K - k0;                                                                \
-      ta[o] = out ? kOutside : va[o];                                                                       \
-      tb[o] = out ? kOutside : vb[o];                                                                       \
-    }                                                                                                       \
-    _Pragma("unroll") for (int i = 0; i < TL::kOpsA; ++i)                                                   \
-        lds_transfer(ra, slot_w + (wave * TL::kOpsA + i) * 1024, ta[i & 1], i * 8 * lda + k0);              \
-    _Pragma("unroll") for (int i = 0; i < TL::kOpsB; ++i)                                                   \
-        lds_transfer(rb, slot_w + TL::kSlotA + (wave * TL::kOpsB + i) * 1024, tb[i & 1], i * 8 * ldb + k0); \
+#define SVDQ_ISSUE_BEGIN(S)                                                                                 \
+  uint8_t* slot_w = smem + ((S) & 1) * TL::kSlot + wave * TL::kOpsA * 1024;                                 \
+  const int k0 = (S) * 128;                                                                                 \
+  uint32_t ta[2], tb[2];                                                                                    \
+  _Pragma("unroll") for (int o = 0; o < 2; ++o) {                                                           \
+    const bool out = 16 * ck[o] >= K - k0;                                                                  \
+    ta[o] = out ? kOutside : va[o];                                                                         \
+    tb[o] = out ? kOutside : vb[o];                                                                         \
   }
+#define SVDQ_ISSUE(i)                                                                                       \
+  if ((i) < TL::kOpsA)                                                                                      \
+    lds_transfer(ra, slot_w + (i) * 1024, ta[(i) & 1], (i) * 8 * lda + k0);                                 \
+  else                                                                                                      \
+    lds_transfer(rb, slot_w + TL::kSlotA + (wave * (TL::kOpsB - TL::kOpsA) + (i) - TL::kOpsA) * 1024,       \
+                 tb[((i) - TL::kOpsA) & 1], ((i) - TL::kOpsA) * 8 * ldb + k0);
   // scale words (four blocks' bytes) of this wave's rows, read one stage
   // ahead: of A (and of B with a scale per row) the words of a lane's rows in
   // the wave's 32-row blocks stand together
@@ -129,19 +129,14 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
       at_a[st][e] = (wm * TL::WM + lr) * 128 + c;
       at_b[st][e] = TL::kSlotA + (wn * TL::WN + lr) * 128 + c;
     }
-#define SVDQ_READ(S, ST, FA, FB)                                                                            \
+// fragment t of the step (B's TN, then A's TM)
+#define SVDQ_READ(S, ST, FA, FB, t)                                                                         \
   {                                                                                                         \
-    const uint8_t* slot = smem + ((S) & 1) * TL::kSlot;                                                     \
-    _Pragma("unroll") for (int t = 0; t < TN; ++t) {                                                        \
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + at_b[ST][0] + t * 4096);                      \
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + at_b[ST][1] + t * 4096);                      \
-      FB[t] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                                \
-    }                                                                                                       \
-    _Pragma("unroll") for (int t = 0; t < TM; ++t) {                                                        \
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + at_a[ST][0] + t * 4096);                      \
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + at_a[ST][1] + t * 4096);                      \
-      FA[t] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                                \
-    }                                                                                                       \
+    const uint8_t* slot = smem + ((S) & 1) * TL::kSlot + ((t) < TN ? (t) : (t) - TN) * 4096;                \
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + ((t) < TN ? at_b[ST][0] : at_a[ST][0]));        \
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + ((t) < TN ? at_b[ST][1] : at_a[ST][1]));        \
+    ((t) < TN ? FB[(t) < TN ? (t) : 0] : FA[(t) < TN ? 0 : (t) - TN]) =                                     \
+        i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                                      \
   }
 #define SVDQ_MFMA(FA, FB)                                                                                   \
   _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j)             \
@@ -154,47 +149,52 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) acc[j][i] = f32x16{};
   // Per stage: the first step's fragments are read while the previous stage's
-  // second half multiplies, the second step's while the first half does, and
-  // the next stage's transfers are issued among the first of these. The
-  // scheduling groups spread the reads and transfers evenly between the MFMAs
-  // (left to itself the compiler reuses the fragments' registers and reads
-  // only when the multiplications are through).
-#define SVDQ_SPREAD(PER)                                                                                    \
-  _Pragma("unroll") for (int q = 0; q < TM * TN; ++q) {                                                     \
-    __builtin_amdgcn_sched_group_barrier(0x100, PER, 0); /* LDS reads */                                    \
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   /* MFMA */                                         \
-  }
-// the reads two to an MFMA (twice the average), the transfers after them
-#define SVDQ_SPREAD_ISSUE                                                                                   \
-  _Pragma("unroll") for (int q = 0; q < TM * TN / 2; ++q) {                                                 \
-    __builtin_amdgcn_sched_group_barrier(0x100, 4 * (TM + TN) / (TM * TN), 0);                              \
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                      \
-  }                                                                                                         \
-  _Pragma("unroll") for (int q = 0; q < TM * TN / 2; ++q) {                                                 \
-    __builtin_amdgcn_sched_group_barrier(0x020, 2 * (TL::kOpsA + TL::kOpsB) / (TM * TN), 0);                \
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                      \
-  }
+  // second half multiplies, the second step's while the first half does; the
+  // next stage's transfers are issued from the start of the stage on, as they
+  // take about half of its time (64 bytes a clock) and then the memory's
+  // latency. Reads and transfers stand in this order in the source (the
+  // compiler does not move LDS reads over transfers into LDS); the scheduling
+  // groups place them between the MFMAs: a fragment and a transfer to an MFMA
+  // first, then the other transfers. (Left to itself the compiler reuses the
+  // fragments' registers and reads only when the multiplications are through.)
+  constexpr int kFrags = TM + TN, kMfma = TM * TN, kOps = TL::kOpsA + TL::kOpsB;
+  constexpr int kFirst = kMfma / 2, kPerF = kFrags / kFirst, kPerT = kOps / kMfma;
+  static_assert(kFirst * kPerF == kFrags && kMfma * kPerT == kOps, "whole fragments and transfers per MFMA");
 #define SVDQ_RING_WAIT                                                                                      \
   __builtin_amdgcn_sched_barrier(0);                                                                        \
   __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt 0, lgkmcnt 0: this stage's transfers, earlier reads */       \
   __builtin_amdgcn_s_barrier();                                                                             \
   __builtin_amdgcn_sched_barrier(0);
+#define SVDQ_FIRST_HALF(S)                                                                                  \
+  SVDQ_ISSUE_BEGIN((S) + 1)                                                                                 \
+  _Pragma("unroll") for (int q = 0; q < kMfma; ++q) {                                                       \
+    if (q < kFirst) {                                                                                       \
+      _Pragma("unroll") for (int f = 0; f < kPerF; ++f) SVDQ_READ(S, 0, xa, xb, q * kPerF + f)              \
+    }                                                                                                       \
+    _Pragma("unroll") for (int f = 0; f < kPerT; ++f) { SVDQ_ISSUE(q * kPerT + f) }                         \
+  }
 #define SVDQ_SECOND_HALF(S)                                                                                 \
   _Pragma("unroll") for (int t = 0; t < TM; ++t) ca[t] = wa[t] >> (8 * ((S) & 3));                          \
   _Pragma("unroll") for (int t = 0; t < SB; ++t) cb[t] = wb[t] >> (8 * ((S) & 3));                          \
-  SVDQ_READ(S, 1, ya, yb)                                                                                   \
+  _Pragma("unroll") for (int f = 0; f < kFrags; ++f) SVDQ_READ(S, 1, ya, yb, f)                             \
   SVDQ_MFMA(xa, xb)                                                                                         \
-  SVDQ_SPREAD(2 * (TM + TN) / (TM * TN))
+  _Pragma("unroll") for (int q = 0; q < kMfma; ++q) {                                                       \
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kFrags / kMfma, 0); /* LDS reads */                     \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  /* MFMA */                          \
+  }
   i32x8 xa[TM], xb[TN], ya[TM], yb[TN];
-  SVDQ_ISSUE(0)
+  {
+    SVDQ_ISSUE_BEGIN(0)
+#pragma unroll
+    for (int q = 0; q < kOps; ++q) { SVDQ_ISSUE(q) }
+  }
   SVDQ_SCALES(0)
   {
     SVDQ_RING_WAIT
     const words_a wa = na;
     const words_b wb = nb;
-    SVDQ_ISSUE(1)
     SVDQ_SCALES(1)
-    SVDQ_READ(0, 0, xa, xb)
+    SVDQ_FIRST_HALF(0)
     SVDQ_SECOND_HALF(0)
   }
   for (int s = 1; s < KB; ++s) {
@@ -203,10 +203,14 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
     const words_b wb = nb;
     SVDQ_SCALES(s + 1)
     __builtin_amdgcn_sched_barrier(0);
-    SVDQ_READ(s, 0, xa, xb)
-    SVDQ_ISSUE(s + 1)
+    SVDQ_FIRST_HALF(s)
     SVDQ_MFMA(ya, yb)
-    SVDQ_SPREAD_ISSUE
+#pragma unroll
+    for (int q = 0; q < kMfma; ++q) {
+      if (q < kFirst) __builtin_amdgcn_sched_group_barrier(0x100, 2 * kPerF, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, kPerT, 0);   // transfers
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
     SVDQ_SECOND_HALF(s)
   }
@@ -214,11 +218,11 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
 #undef SVDQ_MFMA
 #undef SVDQ_READ
 #undef SVDQ_SCALES
+#undef SVDQ_FIRST_HALF
 #undef SVDQ_SECOND_HALF
 #undef SVDQ_RING_WAIT
-#undef SVDQ_SPREAD
-#undef SVDQ_SPREAD_ISSUE
 #undef SVDQ_ISSUE
+#undef SVDQ_ISSUE_BEGIN
   __builtin_amdgcn_s_waitcnt(0x0070);   // the transfers issued past the end land before the LDS is given up
   // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3).
 #pragma unroll
