@@ -33,6 +33,9 @@ __device__ __forceinline__ lds_void* lds_ptr(uint8_t* p) { return (lds_void*)p; 
 __device__ __forceinline__ void lds_transfer(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_ptr(dst), 16, voff, soff, 0, 0);
 }
+__device__ __forceinline__ void store_16(__amdgpu_buffer_rsrc_t r, u32x4 v, int off) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+}
 constexpr int kRsrcWord3 = 0x00020000;   // buffer resources: raw bytes
 constexpr uint32_t kOutside = 0x7ffffff0u;   // a lane offset past the end of every resource: loads zero
 
@@ -42,83 +45,120 @@ template <int BM_, int BN_, int WGM_, int WGN_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NW = WGM * WGN;
   static constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
-  static constexpr int kSlotA = BM * 128, kSlot = (BM + BN) * 128;
-  static constexpr int kOpsA = BM / 8 / NW, kOpsB = BN / 8 / NW;   // transfers per wave and stage
+  // LDS: a ring of five units, a unit one operand's 128 channels of a stage
+  static constexpr int kUnit = (BM > BN ? BM : BN) * 128, kUnits = 5, kLds = kUnits * kUnit;
+  static constexpr int kOpsA = BM / 8 / NW, kOpsB = BN / 8 / NW, kOps = kOpsA + kOpsB;   // transfers per wave and stage
+  static constexpr int kFrags = TM + TN, kMfma = TM * TN;   // fragments and MFMAs per wave and half stage
+  static constexpr int kStores = 2 * TM * TN;               // 16-byte stores per wave and tile
   static_assert(kOpsA % 2 == 0 && kOpsB % 2 == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0,
                 "every wave issues whole pairs of transfers of both operands");
+  static_assert(kOpsA + kStores < 64 && kFrags <= kMfma, "vmcnt range; a fragment or less to an MFMA");
+  // transfers issued up to MFMA q of a first half
+  static constexpr int ops_until(int q) { return q * kOps / kMfma; }
 };
 
-// BROW: B has a scale per row (else per 128 x 128 block: one word per wave
-// and four stages, as a wave's channels lie in one block).
+// Scheduling groups of a first half: to MFMA q a fragment's two LDS reads
+// while there are any, and the transfers that are due; of a second half: the
+// reads spread evenly.
+template <class TL, int Q>
+__device__ __forceinline__ void spread_first() {
+  if constexpr (Q < TL::kFrags) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  constexpr int kDue = TL::ops_until(Q + 1) - TL::ops_until(Q);
+  if constexpr (kDue > 0) __builtin_amdgcn_sched_group_barrier(0x020, kDue, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  if constexpr (Q + 1 < TL::kMfma) spread_first<TL, Q + 1>();
+}
+template <class TL, int Q>
+__device__ __forceinline__ void spread_second() {
+  constexpr int kDue = (Q + 1) * 2 * TL::kFrags / TL::kMfma - Q * 2 * TL::kFrags / TL::kMfma;
+  if constexpr (kDue > 0) __builtin_amdgcn_sched_group_barrier(0x100, kDue, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  if constexpr (Q + 1 < TL::kMfma) spread_second<TL, Q + 1>();
+}
+
+// wait until at most N vector-memory operations are outstanding and all LDS
+// reads have returned, then the workgroup's barrier; nothing moves across
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// BROW: B has a scale per row (else per 128 x 128 block).
+//
+// Persistent workgroups of four waves (one a SIMD, so a wave has 512
+// registers: 256 accumulators and two sets of fragments) walk their tiles; the
+// stages of all their tiles are one sequence. LDS is a ring of five units
+// A0 B0 A1 B1 A2 ...: while stage s is read, B of stage s + 1 and then A of
+// stage s + 2 are fetched into the units that stage s - 1 was read from, so A
+// has two stages' time to arrive and B, fetched first, one. Near a tile's end
+// these are the next tile's, which arrive while the tile is stored.
+//
+// Per stage: the first step's fragments are read while the previous stage's
+// second half multiplies, the second step's while the first half does. Reads
+// and transfers stand in their order in the source (the compiler does not
+// move LDS reads over transfers into LDS) and the scheduling groups place
+// them between the MFMAs. (Left to itself the compiler reuses the fragments'
+// registers and reads only when the multiplications are through.)
 template <int BM, int BN, int WGM, int WGN, bool BROW>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1)))
 void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   typedef Tile<BM, BN, WGM, WGN> TL;
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int TM = TL::TM, TN = TL::TN, SB = BROW ? TN : 1;
-  static_assert(128 % TL::WN == 0, "a wave's channels lie in one block of 128");
+  constexpr int TM = TL::TM, TN = TL::TN;
+  constexpr bool kOneBlock = !BROW && 128 % TL::WN == 0;   // a wave's channels lie in one block of 128
+  constexpr int SB = kOneBlock ? 1 : TN;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
-  const TileMap tm = map_tile((int)blockIdx.x, tiles_m, tiles_n, group_m);
-  const int Ra = (int)g.a_rows, Rb = g.b_rows, K = (int)g.K, KB = (K + 127) / 128;
-  const int m0 = __builtin_amdgcn_readfirstlane(tm.tm) * TL::BM, n0 = __builtin_amdgcn_readfirstlane(tm.tn) * TL::BN;
+  const int wm = wave / WGN, wn = wave % WGN;
+  // KR blocks of 128 channels; at least three stages (the rest multiply zeros), so
+  // that fetching two stages ahead never passes the next tile
+  const int Ra = (int)g.a_rows, Rb = g.b_rows, K = (int)g.K, KR = (K + 127) / 128, KB = max(KR, 3);
   const int lda = (int)g.lda, ldb = (int)g.ldb;
+  const int ntiles = tiles_m * tiles_n, grid = (int)gridDim.x;
 
-  // transfers: the tile's rows of each operand as a buffer resource (rows past
-  // it read as zeros), a lane's chunk of the two kinds of row octets
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(g.a + (size_t)m0 * lda), 0, min(TL::BM, Ra - m0) * lda, kRsrcWord3);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(g.b + (size_t)n0 * ldb), 0, min(TL::BN, Rb - n0) * ldb, kRsrcWord3);
-  const int ck[2] = {(lane & 7) ^ (lane >> 4), (lane & 7) ^ (4 + (lane >> 4))};   // chunk for even and odd octets
+  // Transfers: a tile's rows of an operand as a buffer resource (rows past it
+  // read as zeros); a lane's chunk of the even and the odd row octets.
+  const int ck[2] = {(lane & 7) ^ (lane >> 4), (lane & 7) ^ (4 + (lane >> 4))};
   uint32_t va[2], vb[2];
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
     va[o] = (uint32_t)((wave * TL::kOpsA * 8 + (lane >> 3)) * lda + 16 * ck[o]);
     vb[o] = (uint32_t)((wave * TL::kOpsB * 8 + (lane >> 3)) * ldb + 16 * ck[o]);
   }
-  // transfer i (of kOps) of stage S into slot S % 2; chunks past the contracted
-  // channels (and every chunk of a stage past the last) are zeros
-#define SVDQ_ISSUE_BEGIN(S)                                                                                 \
-  uint8_t* slot_w = smem + ((S) & 1) * TL::kSlot + wave * TL::kOpsA * 1024;                                 \
-  const int k0 = (S) * 128;                                                                                 \
+#define SVDQ_RSRC_A(m0) \
+  __builtin_amdgcn_make_buffer_rsrc((void*)(g.a + (size_t)(m0) * lda), 0, min(BM, Ra - (m0)) * lda, kRsrcWord3)
+#define SVDQ_RSRC_B(n0) \
+  __builtin_amdgcn_make_buffer_rsrc((void*)(g.b + (size_t)(n0) * ldb), 0, min(BN, Rb - (n0)) * ldb, kRsrcWord3)
+  // the fetched stages: operand, channel offset, LDS unit
+  __amdgpu_buffer_rsrc_t fa_res, fb_res;
+  int fa_k = 0, fb_k = 0;
+  uint32_t fa_unit = 0, fb_unit = TL::kUnit;
+  // chunks past the contracted channels are zeros
+#define SVDQ_FETCH_BEGIN                                                                                    \
   uint32_t ta[2], tb[2];                                                                                    \
   _Pragma("unroll") for (int o = 0; o < 2; ++o) {                                                           \
-    const bool out = 16 * ck[o] >= K - k0;                                                                  \
-    ta[o] = out ? kOutside : va[o];                                                                         \
-    tb[o] = out ? kOutside : vb[o];                                                                         \
+    ta[o] = 16 * ck[o] >= K - fa_k ? kOutside : va[o];                                                      \
+    tb[o] = 16 * ck[o] >= K - fb_k ? kOutside : vb[o];                                                      \
   }
-#define SVDQ_ISSUE(i)                                                                                       \
-  if ((i) < TL::kOpsA)                                                                                      \
-    lds_transfer(ra, slot_w + (i) * 1024, ta[(i) & 1], (i) * 8 * lda + k0);                                 \
-  else                                                                                                      \
-    lds_transfer(rb, slot_w + TL::kSlotA + (wave * (TL::kOpsB - TL::kOpsA) + (i) - TL::kOpsA) * 1024,       \
-                 tb[((i) - TL::kOpsA) & 1], ((i) - TL::kOpsA) * 8 * ldb + k0);
-  // scale words (four blocks' bytes) of this wave's rows, read one stage
-  // ahead: of A (and of B with a scale per row) the words of a lane's rows in
-  // the wave's 32-row blocks stand together
-  typedef uint32_t words_a __attribute__((ext_vector_type(TM)));
-  typedef uint32_t words_b __attribute__((ext_vector_type(TN)));
-  const int wrow = m0 + wm * TL::WM, wcol = n0 + wn * TL::WN;
-  const uint32_t* pa = reinterpret_cast<const uint32_t*>(g.as) + wrow / 128 * 128 + lr * 4 + wrow % 128 / 32;
-  const uint32_t* pb = reinterpret_cast<const uint32_t*>(g.bs) +
-                       (BROW ? wcol / 128 * 128 + lr * 4 + wcol % 128 / 32 : min(wcol, Rb - 1) / 128 * ((KB + 3) / 4));
-  const int ga = (Ra + 127) / 128 * 128, gb = BROW ? (Rb + 127) / 128 * 128 : 1;   // words between groups of four blocks
-  // (rows past the last 128 of the operand, whose outputs are not stored, read its first words)
-  if (wrow >= ga) pa = reinterpret_cast<const uint32_t*>(g.as) + lr * 4;
-  if (BROW && wcol >= gb) pb = reinterpret_cast<const uint32_t*>(g.bs) + lr * 4;
-  words_a na, ca;
-  words_b nb, cb;
-#define SVDQ_SCALES(S)                                                                                      \
+#define SVDQ_FETCH_A(i) \
+  lds_transfer(fa_res, smem + fa_unit + (wave * TL::kOpsA + (i)) * 1024, ta[(i) & 1], (i) * 8 * lda + fa_k);
+#define SVDQ_FETCH_B(i) \
+  lds_transfer(fb_res, smem + fb_unit + (wave * TL::kOpsB + (i)) * 1024, tb[(i) & 1], (i) * 8 * ldb + fb_k);
+  // the next stage of an operand; past the tile's last the next tile's first
+#define SVDQ_FETCHED(X, NEXT)                                                                               \
   {                                                                                                         \
-    const int grp = min((S), KB - 1) / 4;                                                                   \
-    na = *reinterpret_cast<const words_a*>(pa + (size_t)grp * ga);                                          \
-    if constexpr (BROW)                                                                                     \
-      nb = *reinterpret_cast<const words_b*>(pb + (size_t)grp * gb);                                        \
-    else                                                                                                    \
-      nb[0] = pb[grp];                                                                                      \
+    f##X##_unit = f##X##_unit >= 3 * TL::kUnit ? f##X##_unit - 3 * TL::kUnit : f##X##_unit + 2 * TL::kUnit;  \
+    f##X##_k += 128;                                                                                        \
+    if (f##X##_k >= KB * 128) {                                                                             \
+      f##X##_k = 0;                                                                                         \
+      f##X##_res = NEXT;                                                                                    \
+    }                                                                                                       \
   }
-  // LDS addresses of this lane's fragment chunks: rows wm WM + lr (+ 32 t),
-  // chunk 4 step + 2 h + e at place chunk ^ (row / 2 % 8)
+  // LDS offsets in a unit of this lane's fragment chunks: rows wm WM + lr
+  // (+ 32 t), chunk 4 step + 2 h + e at place chunk ^ (row / 2 % 8)
   const int sw = (lr >> 1) & 7;
   uint32_t at_a[2][2], at_b[2][2];
 #pragma unroll
@@ -127,120 +167,168 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
     for (int e = 0; e < 2; ++e) {
       const uint32_t c = (uint32_t)((4 * st + 2 * h + e) ^ sw) * 16;
       at_a[st][e] = (wm * TL::WM + lr) * 128 + c;
-      at_b[st][e] = TL::kSlotA + (wn * TL::WN + lr) * 128 + c;
+      at_b[st][e] = (wn * TL::WN + lr) * 128 + c;
     }
-// fragment t of the step (B's TN, then A's TM)
-#define SVDQ_READ(S, ST, FA, FB, t)                                                                         \
+  // fragment t of step ST (B's TN, then A's TM)
+#define SVDQ_READ(ST, FA, FB, t)                                                                            \
   {                                                                                                         \
-    const uint8_t* slot = smem + ((S) & 1) * TL::kSlot + ((t) < TN ? (t) : (t) - TN) * 4096;                \
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(slot + ((t) < TN ? at_b[ST][0] : at_a[ST][0]));        \
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(slot + ((t) < TN ? at_b[ST][1] : at_a[ST][1]));        \
+    const uint8_t* unit = smem + ((t) < TN ? rb_unit + (t) * 4096 : ra_unit + ((t) - TN) * 4096);           \
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(unit + ((t) < TN ? at_b[ST][0] : at_a[ST][0]));        \
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(unit + ((t) < TN ? at_b[ST][1] : at_a[ST][1]));        \
     ((t) < TN ? FB[(t) < TN ? (t) : 0] : FA[(t) < TN ? 0 : (t) - TN]) =                                     \
         i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};                                      \
   }
 #define SVDQ_MFMA(FA, FB)                                                                                   \
   _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j)             \
       acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(FB[j], FA[i], acc[j][i], 0, 0, 0,          \
-                                                                  (int)cb[BROW ? j : 0], 0, (int)ca[i]);
-
-  f32x16 acc[TN][TM];
-#pragma unroll
-  for (int j = 0; j < TN; ++j)
-#pragma unroll
-    for (int i = 0; i < TM; ++i) acc[j][i] = f32x16{};
-  // Per stage: the first step's fragments are read while the previous stage's
-  // second half multiplies, the second step's while the first half does; the
-  // next stage's transfers are issued from the start of the stage on, as they
-  // take about half of its time (64 bytes a clock) and then the memory's
-  // latency. Reads and transfers stand in this order in the source (the
-  // compiler does not move LDS reads over transfers into LDS); the scheduling
-  // groups place them between the MFMAs: a fragment and a transfer to an MFMA
-  // first, then the other transfers. (Left to itself the compiler reuses the
-  // fragments' registers and reads only when the multiplications are through.)
-  constexpr int kFrags = TM + TN, kMfma = TM * TN, kOps = TL::kOpsA + TL::kOpsB;
-  constexpr int kFirst = kMfma / 2, kPerF = kFrags / kFirst, kPerT = kOps / kMfma;
-  static_assert(kFirst * kPerF == kFrags && kMfma * kPerT == kOps, "whole fragments and transfers per MFMA");
-#define SVDQ_RING_WAIT                                                                                      \
-  __builtin_amdgcn_sched_barrier(0);                                                                        \
-  __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt 0, lgkmcnt 0: this stage's transfers, earlier reads */       \
-  __builtin_amdgcn_s_barrier();                                                                             \
-  __builtin_amdgcn_sched_barrier(0);
-#define SVDQ_FIRST_HALF(S)                                                                                  \
-  SVDQ_ISSUE_BEGIN((S) + 1)                                                                                 \
-  _Pragma("unroll") for (int q = 0; q < kMfma; ++q) {                                                       \
-    if (q < kFirst) {                                                                                       \
-      _Pragma("unroll") for (int f = 0; f < kPerF; ++f) SVDQ_READ(S, 0, xa, xb, q * kPerF + f)              \
+                                                                  (int)cb[kOneBlock ? 0 : j], 0, (int)ca[i]);
+  // Scale words (four blocks' bytes) of this wave's rows, read a stage ahead.
+  // The words of a lane's rows in four 32-row blocks stand together, so a wave
+  // whose rows lie in one run of 128 reads them with one load.
+  constexpr bool kVecA = 128 % TL::WM == 0, kVecB = BROW && 128 % TL::WN == 0;
+  uint32_t na[TM], nb[SB], wa[TM], wb[SB], ca[TM], cb[SB];
+  const uint32_t *pa[kVecA ? 1 : TM], *pb[kVecB ? 1 : SB];
+  const size_t ga = (size_t)round128(Ra), gb = BROW ? (size_t)round128(Rb) : 1;   // words between groups of four blocks
+  // (rows past the operand, whose outputs are not stored, read its first words)
+#define SVDQ_SCALE_ROWS(m0, n0)                                                                             \
+  _Pragma("unroll") for (int t = 0; t < (kVecA ? 1 : TM); ++t) {                                            \
+    const int blk = (m0) + wm * TL::WM + 32 * t;                                                            \
+    pa[t] = reinterpret_cast<const uint32_t*>(g.as) + lr * 4 + (blk < Ra ? blk / 128 * 128 + blk % 128 / 32 : 0); \
+  }                                                                                                         \
+  _Pragma("unroll") for (int t = 0; t < (kVecB ? 1 : SB); ++t) {                                            \
+    const int blk = (n0) + wn * TL::WN + 32 * t;                                                            \
+    pb[t] = reinterpret_cast<const uint32_t*>(g.bs) +                                                       \
+            (BROW ? lr * 4 + (blk < Rb ? blk / 128 * 128 + blk % 128 / 32 : 0) : min(blk, Rb - 1) / 128 * ((KR + 3) / 4)); \
+  }
+#define SVDQ_SCALES(S)                                                                                      \
+  {                                                                                                         \
+    const int grp = min((S), KR - 1) / 4;                                                                   \
+    if constexpr (kVecA)                                                                                    \
+      memcpy(na, __builtin_assume_aligned(pa[0] + grp * ga, TM * 4), sizeof(na));                           \
+    else                                                                                                    \
+      _Pragma("unroll") for (int t = 0; t < TM; ++t) na[t] = pa[kVecA ? 0 : t][grp * ga];                   \
+    if constexpr (kVecB)                                                                                    \
+      memcpy(nb, __builtin_assume_aligned(pb[0] + grp * gb, SB * 4), sizeof(nb));                           \
+    else                                                                                                    \
+      _Pragma("unroll") for (int t = 0; t < SB; ++t) nb[t] = pb[kVecB ? 0 : t][grp * gb];                   \
+  }
+#define SVDQ_TAKE_SCALES                                                                                    \
+  _Pragma("unroll") for (int t = 0; t < TM; ++t) wa[t] = na[t];                                             \
+  _Pragma("unroll") for (int t = 0; t < SB; ++t) wb[t] = nb[t];
+  // a stage's first half reads its first step and fetches; the multiplication
+  // that belongs to it is the previous stage's second half
+#define SVDQ_FIRST_HALF                                                                                     \
+  {                                                                                                         \
+    SVDQ_FETCH_BEGIN                                                                                        \
+    _Pragma("unroll") for (int q = 0; q < TL::kMfma; ++q) {                                                 \
+      if (q < TL::kFrags) SVDQ_READ(0, xa, xb, q)                                                           \
+      _Pragma("unroll") for (int f = TL::ops_until(q); f < TL::ops_until(q + 1); ++f) {                     \
+        if (f < TL::kOpsB) {                                                                                \
+          SVDQ_FETCH_B(f)                                                                                   \
+        } else {                                                                                            \
+          SVDQ_FETCH_A(f - TL::kOpsB)                                                                       \
+        }                                                                                                   \
+      }                                                                                                     \
     }                                                                                                       \
-    _Pragma("unroll") for (int f = 0; f < kPerT; ++f) { SVDQ_ISSUE(q * kPerT + f) }                         \
   }
 #define SVDQ_SECOND_HALF(S)                                                                                 \
-  _Pragma("unroll") for (int t = 0; t < TM; ++t) ca[t] = wa[t] >> (8 * ((S) & 3));                          \
-  _Pragma("unroll") for (int t = 0; t < SB; ++t) cb[t] = wb[t] >> (8 * ((S) & 3));                          \
-  _Pragma("unroll") for (int f = 0; f < kFrags; ++f) SVDQ_READ(S, 1, ya, yb, f)                             \
-  SVDQ_MFMA(xa, xb)                                                                                         \
-  _Pragma("unroll") for (int q = 0; q < kMfma; ++q) {                                                       \
-    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kFrags / kMfma, 0); /* LDS reads */                     \
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  /* MFMA */                          \
+  {                                                                                                         \
+    _Pragma("unroll") for (int t = 0; t < TM; ++t) ca[t] = wa[t] >> (8 * (min((S), KR - 1) & 3));            \
+    _Pragma("unroll") for (int t = 0; t < SB; ++t) cb[t] = wb[t] >> (8 * (min((S), KR - 1) & 3));            \
+    _Pragma("unroll") for (int f = 0; f < TL::kFrags; ++f) SVDQ_READ(1, ya, yb, f)                          \
+    SVDQ_MFMA(xa, xb)                                                                                       \
+    spread_second<TL, 0>();                                                                                 \
+    SVDQ_FETCHED(b, nb_res)                                                                                 \
+    SVDQ_FETCHED(a, na_res)                                                                                 \
+    ra_unit = ra_unit >= 3 * TL::kUnit ? ra_unit - 3 * TL::kUnit : ra_unit + 2 * TL::kUnit;                 \
+    rb_unit = rb_unit >= 3 * TL::kUnit ? rb_unit - 3 * TL::kUnit : rb_unit + 2 * TL::kUnit;                 \
   }
+
+  f32x16 acc[TN][TM];
   i32x8 xa[TM], xb[TN], ya[TM], yb[TN];
-  {
-    SVDQ_ISSUE_BEGIN(0)
+  uint32_t ra_unit = 0, rb_unit = TL::kUnit;   // the units of the stage being read
+  int t_cur = (int)blockIdx.x;
+  TileMap tm = map_tile(t_cur, tiles_m, tiles_n, group_m);
+  int m0 = __builtin_amdgcn_readfirstlane(tm.tm) * BM, n0 = __builtin_amdgcn_readfirstlane(tm.tn) * BN;
+  fa_res = SVDQ_RSRC_A(m0);
+  fb_res = SVDQ_RSRC_B(n0);
+  bool first = true;
+  while (true) {
+    // the next tile (none: resources of no bytes, whose transfers are zeros)
+    const int t_next = t_cur + grid;
+    const bool more = t_next < ntiles;
+    const TileMap tn = map_tile(more ? t_next : t_cur, tiles_m, tiles_n, group_m);
+    const int m_next = __builtin_amdgcn_readfirstlane(tn.tm) * BM, n_next = __builtin_amdgcn_readfirstlane(tn.tn) * BN;
+    __amdgpu_buffer_rsrc_t na_res = SVDQ_RSRC_A(m_next), nb_res = SVDQ_RSRC_B(n_next);
+    if (!more) na_res = nb_res = __builtin_amdgcn_make_buffer_rsrc(nullptr, 0, 0, kRsrcWord3);
 #pragma unroll
-    for (int q = 0; q < kOps; ++q) { SVDQ_ISSUE(q) }
-  }
-  SVDQ_SCALES(0)
-  {
-    SVDQ_RING_WAIT
-    const words_a wa = na;
-    const words_b wb = nb;
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int i = 0; i < TM; ++i) acc[j][i] = f32x16{};
+    if (first) {
+      // A0, B0, A1
+      SVDQ_SCALE_ROWS(m0, n0)
+      SVDQ_SCALES(0)
+      __builtin_amdgcn_sched_barrier(0);
+      SVDQ_FETCH_BEGIN
+#pragma unroll
+      for (int i = 0; i < TL::kOpsA; ++i) { SVDQ_FETCH_A(i) }
+#pragma unroll
+      for (int i = 0; i < TL::kOpsB; ++i) { SVDQ_FETCH_B(i) }
+      SVDQ_FETCHED(a, na_res)
+      SVDQ_FETCHED(b, nb_res)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) ta[o] = 16 * ck[o] >= K - fa_k ? kOutside : va[o];
+#pragma unroll
+      for (int i = 0; i < TL::kOpsA; ++i) { SVDQ_FETCH_A(i) }
+      SVDQ_FETCHED(a, na_res)
+      first = false;
+      ring_barrier<TL::kOpsA>();   // all but A1
+    } else {
+      ring_barrier<TL::kOpsA + TL::kStores>();   // A1 and the last tile's stores may be outstanding
+    }
+    SVDQ_TAKE_SCALES
     SVDQ_SCALES(1)
-    SVDQ_FIRST_HALF(0)
+    __builtin_amdgcn_sched_barrier(0);
+    SVDQ_FIRST_HALF
     SVDQ_SECOND_HALF(0)
-  }
-  for (int s = 1; s < KB; ++s) {
-    SVDQ_RING_WAIT
-    const words_a wa = na;
-    const words_b wb = nb;
-    SVDQ_SCALES(s + 1)
+    for (int s = 1; s < KB; ++s) {
+      ring_barrier<TL::kOpsA>();   // all but A of the stage after
+      SVDQ_TAKE_SCALES
+      SVDQ_SCALES(s + 1)
+      __builtin_amdgcn_sched_barrier(0);
+      SVDQ_FIRST_HALF
+      SVDQ_MFMA(ya, yb)
+      spread_first<TL, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      SVDQ_SECOND_HALF(s)
+    }
     __builtin_amdgcn_sched_barrier(0);
-    SVDQ_FIRST_HALF(s)
+    SVDQ_SCALE_ROWS(m_next, n_next)   // (without a next tile this tile's again)
+    SVDQ_SCALES(0)
     SVDQ_MFMA(ya, yb)
+
+    // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3).
+    // Every store is issued by every wave, as the ring's waits count them: the
+    // resource drops rows past the operand, and channels past it are sent past
+    // its end.
+    const int nrec = min(BM, Ra - m0) * Rb * 2;
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(g.out + (size_t)m0 * Rb, 0, nrec, kRsrcWord3);
 #pragma unroll
-    for (int q = 0; q < kMfma; ++q) {
-      if (q < kFirst) __builtin_amdgcn_sched_group_barrier(0x100, 2 * kPerF, 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, kPerT, 0);   // transfers
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    SVDQ_SECOND_HALF(s)
-  }
-  SVDQ_MFMA(ya, yb)
-#undef SVDQ_MFMA
-#undef SVDQ_READ
-#undef SVDQ_SCALES
-#undef SVDQ_FIRST_HALF
-#undef SVDQ_SECOND_HALF
-#undef SVDQ_RING_WAIT
-#undef SVDQ_ISSUE
-#undef SVDQ_ISSUE_BEGIN
-  __builtin_amdgcn_s_waitcnt(0x0070);   // the transfers issued past the end land before the LDS is given up
-  // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3).
+    for (int j = 0; j < TN; ++j) {
+      const int col = n0 + wn * TL::WN + 32 * j;
+      float bv[16];
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int nb = n0 + wn * TL::WN + 32 * j;
-    float bv[16];
+      for (int q = 0; q < 4; ++q) {
+        u32x2 w = u32x2{0, 0};
+        if (g.bias) w = *reinterpret_cast<const u32x2*>(g.bias + min(col + 8 * q + 4 * h, Rb - 4));
+        bv[4 * q] = bf16lo(w.x);
+        bv[4 * q + 1] = bf16hi(w.x);
+        bv[4 * q + 2] = bf16lo(w.y);
+        bv[4 * q + 3] = bf16hi(w.y);
+      }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      u32x2 w = u32x2{0, 0};
-      if (g.bias && nb + 8 * q + 4 * h < g.b_rows) w = *reinterpret_cast<const u32x2*>(g.bias + nb + 8 * q + 4 * h);
-      bv[4 * q] = bf16lo(w.x);
-      bv[4 * q + 1] = bf16hi(w.x);
-      bv[4 * q + 2] = bf16lo(w.y);
-      bv[4 * q + 3] = bf16hi(w.y);
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t m = m0 + wm * TL::WM + 32 * i + lr;
+      for (int i = 0; i < TM; ++i) {
         uint32_t o[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p) o[p] = cvt_bf16x2(acc[j][i][2 * p] + bv[2 * p], acc[j][i][2 * p + 1] + bv[2 * p + 1]);
@@ -254,13 +342,30 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
             o[4 * p + w] = r[0];
             o[4 * p + 2 + w] = r[1];
           }
-        uint16_t* y = g.out + m * g.b_rows + nb + 8 * h;
-        if (m < g.a_rows) {
-          if (nb < g.b_rows) *reinterpret_cast<u32x4*>(y) = u32x4{o[0], o[1], o[2], o[3]};
-          if (nb + 16 < g.b_rows) *reinterpret_cast<u32x4*>(y + 16) = u32x4{o[4], o[5], o[6], o[7]};
-        }
+        const int off = ((wm * TL::WM + 32 * i + lr) * Rb + col + 8 * h) * 2;
+        store_16(out, u32x4{o[0], o[1], o[2], o[3]}, col < Rb ? off : nrec);
+        store_16(out, u32x4{o[4], o[5], o[6], o[7]}, col + 16 < Rb ? off + 32 : nrec);
+      }
     }
+    if (!more) break;
+    t_cur = t_next;
+    m0 = m_next;
+    n0 = n_next;
   }
+  __builtin_amdgcn_s_waitcnt(0);   // the transfers past the end land before the LDS is given up
+#undef SVDQ_RSRC_A
+#undef SVDQ_RSRC_B
+#undef SVDQ_FETCH_BEGIN
+#undef SVDQ_FETCH_A
+#undef SVDQ_FETCH_B
+#undef SVDQ_FETCHED
+#undef SVDQ_READ
+#undef SVDQ_MFMA
+#undef SVDQ_SCALE_ROWS
+#undef SVDQ_SCALES
+#undef SVDQ_TAKE_SCALES
+#undef SVDQ_FIRST_HALF
+#undef SVDQ_SECOND_HALF
 }
 
 // Few tokens: the weight stream. A workgroup of eight waves owns 16 NT output
@@ -406,23 +511,30 @@ __global__ __launch_bounds__(64 * kSmallWaves) void fp8_small_kernel(Fp8Gemm g) 
 }
 
 typedef Tile<256, 256, 2, 2> TileL;
+typedef Tile<256, 192, 2, 2> TileW;
 typedef Tile<128, 128, 2, 2> TileM;
+// The 32 workgroups of an XCD take 4 tile-rows x 8 tile-columns (8 x 4 took
+// 2% longer at 8192^3, 16 x 2 8%).
+constexpr int kGroupM = 4;
 
 template <class TL, bool BROW>
-hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
+hipError_t launch_tile(const Fp8Gemm& g, int num_cus, hipStream_t st) {
   const int tm = (int)((g.a_rows + TL::BM - 1) / TL::BM), tn = (g.b_rows + TL::BN - 1) / TL::BN;
-  hipLaunchKernelGGL((fp8_gemm_kernel<TL::BM, TL::BN, TL::WGM, TL::WGN, BROW>), dim3((unsigned)(tm * tn)), dim3(64 * TL::NW), 2 * TL::kSlot, st, g, tm, tn, 8);
+  const int resident = num_cus * (int)(160 * 1024 / TL::kLds);   // workgroups that the LDS holds
+  hipLaunchKernelGGL((fp8_gemm_kernel<TL::BM, TL::BN, TL::WGM, TL::WGN, BROW>), dim3((unsigned)std::min(tm * tn, resident)),
+                     dim3(64 * TL::NW), TL::kLds, st, g, tm, tn, kGroupM);
   return hipGetLastError();
 }
 template <class TL, bool BROW>
 hipError_t prepare_tile() {
-  return hipFuncSetAttribute((const void*)fp8_gemm_kernel<TL::BM, TL::BN, TL::WGM, TL::WGN, BROW>, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * TL::kSlot);
+  return hipFuncSetAttribute((const void*)fp8_gemm_kernel<TL::BM, TL::BN, TL::WGM, TL::WGN, BROW>,
+                             hipFuncAttributeMaxDynamicSharedMemorySize, TL::kLds);
 }
 
 }  // namespace
 
 hipError_t prepare_fp8() {
-  for (hipError_t e : {prepare_tile<TileL, false>(), prepare_tile<TileL, true>(), prepare_tile<TileM, false>(),
+  for (hipError_t e : {prepare_tile<TileW, false>(), prepare_tile<TileW, true>(), prepare_tile<TileL, false>(), prepare_tile<TileL, true>(), prepare_tile<TileM, false>(),
                        prepare_tile<TileM, true>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
@@ -447,10 +559,23 @@ hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st) 
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st) {
   if (fp8_gemm_small_fits(g)) return launch_fp8_gemm_small(g, num_cus, st);
-  const int64_t large = ((g.a_rows + 255) / 256) * ((g.b_rows + 255) / 256);
-  if (large >= num_cus)
-    return g.b_row_scales ? launch_tile<TileL, true>(g, st) : launch_tile<TileL, false>(g, st);
-  return g.b_row_scales ? launch_tile<TileM, true>(g, st) : launch_tile<TileM, false>(g, st);
+  // The tile of least cost, a cost being the rounds of tiles over the CUs times
+  // a round's time relative to TileL's, as measured on the products of K from
+  // 2048 to 12288: TileW 0.85 (it fills the CUs where TileL's rounds do not:
+  // 12288 x 3072 outputs over 4608 tokens 180 us against 198), TileM 0.62 with
+  // two tiles a CU and 0.5 with one (512 x 3072 outputs over 12288 channels
+  // 59 us against TileL's 110; 4608 x 3072 208 against 162).
+  auto tiles = [&](int bm, int bn) { return ((g.a_rows + bm - 1) / bm) * ((g.b_rows + bn - 1) / bn); };
+  auto rounds = [&](int64_t n, int64_t at_once) { return (float)((n + at_once - 1) / at_once); };
+  const int64_t nm = tiles(TileM::BM, TileM::BN);
+  const float cost_l = rounds(tiles(TileL::BM, TileL::BN), num_cus);
+  const float cost_w = 0.85f * rounds(tiles(TileW::BM, TileW::BN), num_cus);
+  const float cost_m = nm <= num_cus ? 0.5f : 0.62f * rounds(nm, 2 * num_cus);
+  if (cost_m <= cost_l && cost_m <= cost_w)
+    return g.b_row_scales ? launch_tile<TileM, true>(g, num_cus, st) : launch_tile<TileM, false>(g, num_cus, st);
+  if (cost_w < cost_l)
+    return g.b_row_scales ? launch_tile<TileW, true>(g, num_cus, st) : launch_tile<TileW, false>(g, num_cus, st);
+  return g.b_row_scales ? launch_tile<TileL, true>(g, num_cus, st) : launch_tile<TileL, false>(g, num_cus, st);
 }
 
 }  // namespace svdq
