@@ -640,15 +640,26 @@ class SVDQLinear:
 # ----------------------------------------------------------------------------
 # Layer norm and the FP8 linear, forward and backward
 # ----------------------------------------------------------------------------
-_DT_CODES = None
+_t = None         # torch, imported on first use
+_DT_CODES = {}    # svdq_dtype of the torch dtypes
+_raw_stream = None   # the current stream's handle on a GPU
+
+
+def _torch():
+    global _t, _raw_stream
+    if _t is None:
+        import torch
+        _DT_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        # (without a Stream object where this torch has the call)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda at: torch.cuda.current_stream(at).cuda_stream)
+        _t = torch
+    return _t
 
 
 def _dt(dtype) -> int:
     """svdq_dtype of a torch dtype."""
-    global _DT_CODES
-    if _DT_CODES is None:
-        import torch
-        _DT_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    _torch()
     if dtype not in _DT_CODES:
         raise ValueError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
     return _DT_CODES[dtype]
@@ -659,64 +670,82 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
-def _on_device(device, *tensors):
-    """Every given tensor lives on `device`, a GPU."""
-    _need(device.type == "cuda", "the tensors must be on a GPU")
+def _on_device(x, *tensors) -> int:
+    """The index of the GPU that x and every other given tensor live on."""
+    at = x.get_device()
+    if at < 0:
+        raise ValueError("the tensors must be on a GPU")
     for t in tensors:
-        _need(t is None or t.device == device, f"tensors on {device} and {t.device if t is not None else None}")
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"tensors on {x.device} and {t.device}")
+    return at
 
 
-def _allocating(device, stream):
-    """Where outputs and workspaces of a call on `stream` are allocated: under
-    that stream, so that the allocator does not hand their memory to other work
-    while the call runs."""
-    import contextlib
-    import torch
+def _empty(shape, dtype, like, stream):
+    """A tensor for a call on `stream`, allocated under it, so that the
+    allocator does not hand its memory to other work while the call runs."""
+    torch = _torch()
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _call(name: str, device, stream, *args):
-    """The library's function on the tensors' device and the given stream (by
-    default the device's current one)."""
-    import torch
+def _call(name: str, at: int, stream, *args):
+    """The library's function on GPU `at` and the given stream (by default the
+    GPU's current one)."""
+    torch = _torch()
     f = getattr(lib(), name)
-    s = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
-    if torch.cuda.current_device() == device.index:
+    s = _raw_stream(at) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == at:
         st = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(at):
             st = f(*args, s)
-    _check(st, name)
+    if st != 0:
+        raise SvdqError(st, name)
 
 
 def _rows(t, what: str):
     """(pointer, row stride) of a matrix whose rows are contiguous."""
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{what}: a matrix with contiguous rows")
-    return t.data_ptr(), max(t.stride(0), t.shape[1])
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: a matrix with contiguous rows")
+    ld, step = t.stride()
+    cols = shape[1]
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}: a matrix with contiguous rows")
+    return t.data_ptr(), ld if ld > cols else cols
+
+
+def _param(t, C, groups, dtype, what):
+    """(pointer, group stride) of a [C] or [groups][C] parameter."""
+    shape = t.shape
+    if t.dtype != dtype or shape[-1] != C or len(shape) > 2 or (len(shape) == 2 and shape[0] or 1) != groups \
+            or (C > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: [channels] or [groups][channels], contiguous channels, both of one type")
+    return t.data_ptr(), max(t.stride(0), C) if len(shape) == 2 else C
 
 
 def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype):
     """(NormDesc, weight pointer, stride, bias pointer, stride) of [C] or [groups][C] parameters."""
     some = weight if weight is not None else bias
-    groups, pdt, ptrs = 1, dtype, []
+    wp = bp = None
+    ldw = ldb = C
+    groups, pdt = 1, dtype
     if some is not None:
         pdt = some.dtype
-        groups = 1 if some.dim() == 1 else some.shape[0]
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            ptrs += [None, C]
-            continue
-        _need(t.dtype == pdt and t.shape[-1] == C and (groups if t.dim() == 2 else 1) == groups and t.dim() in (1, 2)
-              and (t.dim() == 1 or t.shape[0] == groups), f"{what}: [channels] or [groups][channels], both of one type")
-        _need(C <= 1 or t.stride(-1) == 1, f"{what}: contiguous channels")
-        ptrs += [t.data_ptr(), max(t.stride(0), C) if t.dim() == 2 else C]
+        if some.dim() == 2:
+            groups = some.shape[0]
+        if weight is not None:
+            wp, ldw = _param(weight, C, groups, pdt, "weight")
+        if bias is not None:
+            bp, ldb = _param(bias, C, groups, pdt, "bias")
     if rows_per_group is None:
         rows_per_group = max(1, -(-M // groups))
-    return NormDesc(C, _dt(dtype), _dt(pdt), 1 if one_plus else 0, groups, float(eps), int(rows_per_group)), *ptrs
+    return NormDesc(C, _dt(dtype), _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group), wp, ldw, bp, ldb
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: bool = False, rows_per_group=None,
@@ -727,21 +756,19 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: b
     weight and bias: [C], or [groups][C] for rows in groups of rows_per_group
     (default: the rows split evenly); the gain is weight, or 1 + weight with
     one_plus. mean and rstd are float32 [M], for layer_norm_backward."""
-    import torch
-    _on_device(x.device, weight, bias, y)
+    at = _on_device(x, weight, bias, y)
     xp, ldx = _rows(x, "x")
     M, C = x.shape
     d, wp, ldw, bp, ldb = _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
-    with _allocating(x.device, stream):
-        if y is None:
-            y = torch.empty((M, C), dtype=x.dtype, device=x.device)
-        stats = torch.empty((2, M), dtype=torch.float32, device=x.device)
-    _need(y.dtype == x.dtype and y.shape == x.shape, "y: the shape and type of x")
+    if y is None:
+        y = _empty((M, C), x.dtype, x, stream)
+    elif y.dtype != x.dtype or y.shape != x.shape:
+        raise ValueError("y: the shape and type of x")
+    mean, rstd = _empty((2, M), _t.float32, x, stream).unbind()
     yp, ldy = _rows(y, "y")
-    sp = stats.data_ptr()
-    _call("svdq_layer_norm_forward", x.device, stream, ctypes.byref(d), xp, ldx, wp, ldw, bp, ldb, M, yp, ldy, sp,
-          sp + 4 * M)
-    return y, stats[0], stats[1]
+    _call("svdq_layer_norm_forward", at, stream, ctypes.byref(d), xp, ldx, wp, ldw, bp, ldb, M, yp, ldy, mean.data_ptr(),
+          rstd.data_ptr())
+    return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, rows_per_group=None, groups=None,
@@ -750,42 +777,43 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, 
     forward's x, mean, rstd, weight and grouping. dweight and dbias are
     [groups][C] ([C] for a [C] or absent weight) of grad_dtype (default: the
     weight's type, float32 without one); None without param_grads."""
-    import torch
-    _on_device(x.device, dy, mean, rstd, weight, dx)
+    at = _on_device(x, dy, mean, rstd, weight, dx)
     M, C = x.shape
     _need(dy.shape == x.shape and dy.dtype == x.dtype, "dy: the shape and type of x")
+    f32 = _torch().float32
     for t in (mean, rstd):
-        _need(t.dtype == torch.float32 and t.shape == (M,) and t.is_contiguous(), "mean, rstd: float32 [rows]")
+        _need(t.dtype == f32 and t.shape == (M,) and t.is_contiguous(), "mean, rstd: float32 [rows]")
     d, wp, ldw, _, _ = _norm_params(C, weight, None, one_plus, 0.0, rows_per_group, M, x.dtype)
-    flat = weight is None and groups is None or weight is not None and weight.dim() == 1
+    flat = groups is None if weight is None else weight.dim() == 1
     if weight is None and groups is not None:
-        d.groups = int(groups)
-        d.rows_per_group = int(rows_per_group) if rows_per_group is not None else max(1, -(-M // int(groups)))
-    gdt = grad_dtype if grad_dtype is not None else (weight.dtype if weight is not None else torch.float32)
-    need = ctypes.c_size_t()
-    _check(lib().svdq_layer_norm_backward_workspace_bytes(ctypes.byref(d), M, ctypes.byref(need)),
-           "svdq_layer_norm_backward_workspace_bytes")
-    dw = db = ws = None
-    with _allocating(x.device, stream):
-        if dx is None:
-            dx = torch.empty((M, C), dtype=x.dtype, device=x.device)
-        if param_grads:
-            grads = torch.empty((2, d.groups, C), dtype=gdt, device=x.device)
-            dw, db = grads[0], grads[1]
-            if need.value:
-                ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-    _need(dx.dtype == x.dtype and dx.shape == x.shape, "dx: the shape and type of x")
+        d.groups = groups
+        d.rows_per_group = rows_per_group if rows_per_group is not None else max(1, -(-M // groups))
+    gdt = grad_dtype if grad_dtype is not None else (weight.dtype if weight is not None else f32)
+    if dx is None:
+        dx = _empty((M, C), x.dtype, x, stream)
+    elif dx.dtype != x.dtype or dx.shape != x.shape:
+        raise ValueError("dx: the shape and type of x")
+    dw = db = wsp = ws = None
+    size = 0
+    if param_grads:
+        need = ctypes.c_size_t()
+        _check(lib().svdq_layer_norm_backward_workspace_bytes(ctypes.byref(d), M, ctypes.byref(need)),
+               "svdq_layer_norm_backward_workspace_bytes")
+        size = need.value
+        dw, db = _empty((2, C) if flat else (2, d.groups, C), gdt, x, stream).unbind()
+        if size:
+            ws = _empty((size,), _t.uint8, x, stream)
+            wsp = ws.data_ptr()
     (dyp, lddy), (xp, ldx), (dxp, lddx) = _rows(dy, "dy"), _rows(x, "x"), _rows(dx, "dx")
-    _call("svdq_layer_norm_backward", x.device, stream, ctypes.byref(d), dyp, lddy, xp, ldx, wp, ldw, mean.data_ptr(),
-          rstd.data_ptr(), M, dxp, lddx, _ptr(dw), _ptr(db), _dt(gdt), _ptr(ws), need.value if ws is not None else 0)
-    if flat and param_grads:
-        dw, db = dw[0], db[0]
+    _call("svdq_layer_norm_backward", at, stream, ctypes.byref(d), dyp, lddy, xp, ldx, wp, ldw, mean.data_ptr(),
+          rstd.data_ptr(), M, dxp, lddx, None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
+          _dt(gdt), wsp, size)
     return dx, dw, db
 
 
 def _fp8_bytes(name: str, K: int, N: int, M: int) -> int:
     out = ctypes.c_size_t()
-    _check(getattr(lib(), name)(ctypes.byref(Fp8Desc(int(K), int(N))), int(M), ctypes.byref(out)), name)
+    _check(getattr(lib(), name)(ctypes.byref(Fp8Desc(K, N)), M, ctypes.byref(out)), name)
     return out.value
 
 
@@ -812,63 +840,68 @@ def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, str
     GPU): {"q", "s", "qt", "st", "bias"}, device tensors (qt and st, which the
     gradient of x reads, are None without `transposed`). `out`: a dict of an
     earlier call to overwrite, as after an update of w."""
-    import torch
+    torch = _torch()
     _need(w.dim() == 2 and w.is_contiguous(), "w: a contiguous matrix [N][K]")
     N, K = w.shape
     sizes = fp8_packed_bytes(K, N)
     if out is None:
-        with _allocating(w.device, stream):
-            def new(rows, name):
-                return torch.empty((rows, sizes[name] // rows), dtype=torch.uint8, device=w.device)
-            out = {"q": new(N, "q"), "s": new(-(-N // 128), "s"), "qt": new(K, "qt") if transposed else None,
-                   "st": new(-(-K // 128), "st") if transposed else None, "bias": None}
+        def new(rows, name):
+            return _empty((rows, sizes[name] // rows), torch.uint8, w, stream)
+        out = {"q": new(N, "q"), "s": new(-(-N // 128), "s"), "qt": new(K, "qt") if transposed else None,
+               "st": new(-(-K // 128), "st") if transposed else None, "bias": None}
     if bias is not None:
         out["bias"] = bias.to(torch.bfloat16).contiguous()
-    _on_device(w.device, *out.values())
+    at = _on_device(w, *out.values())
     p = _fp8_struct(K, N, out)
-    _call("svdq_fp8_pack", w.device, stream, ctypes.byref(Fp8Desc(K, N)), w.data_ptr(), _dt(w.dtype), ctypes.byref(p))
+    _call("svdq_fp8_pack", at, stream, ctypes.byref(Fp8Desc(K, N)), w.data_ptr(), _dt(w.dtype), ctypes.byref(p))
     return out
 
 
 def _fp8_struct(K: int, N: int, dev: dict) -> Fp8Packed:
     """The buffers of a layer, each of at least its size."""
-    rk, rn = -(-K // 128), -(-N // 128)
-    least = {"q": N * K, "s": rn * (-(-rk // 4) * 4), "qt": N * K, "st": rk * (-(-rn // 4) * 4), "bias": N}
+    rk, rn = (K + 127) // 128, (N + 127) // 128
     ptrs = []
-    for n in FP8_FIELDS:
+    for n, least in (("q", N * K), ("s", rn * ((rk + 3) // 4 * 4)), ("qt", N * K), ("st", rk * ((rn + 3) // 4 * 4)),
+                     ("bias", N)):
         t = dev.get(n)
         if t is None:
             ptrs.append(None)
             continue
-        _need(t.is_contiguous() and t.numel() >= least[n] and t.element_size() == (2 if n == "bias" else 1),
-              f"fp8 layer: {n} must be contiguous with {least[n]} elements")
+        if not t.is_contiguous() or t.numel() < least or t.element_size() != (2 if n == "bias" else 1):
+            raise ValueError(f"fp8 layer: {n} must be contiguous with {least} elements")
         ptrs.append(t.data_ptr())
     return Fp8Packed(*ptrs)
 
 
 def _bf16_rows(t, cols: int, what: str):
-    import torch
-    _need(t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[1] == cols and t.is_contiguous(),
-          f"{what}: a contiguous bfloat16 matrix of {cols} columns")
+    shape = t.shape
+    if t.dtype != _torch().bfloat16 or len(shape) != 2 or shape[1] != cols or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous bfloat16 matrix of {cols} columns")
+
+
+def _scratch(workspace, size: int, like, stream):
+    """(tensor to keep, pointer, bytes) of the caller's workspace or a new one."""
+    if workspace is None:
+        if not size:
+            return None, None, 0
+        workspace = _empty((size,), _t.uint8, like, stream)
+        return workspace, workspace.data_ptr(), size
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def fp8_forward(K: int, N: int, dev: dict, x, y=None, workspace=None, stream=None):
     """y[M][N] bf16 = FP8 layer(x[M][K] bf16) via svdq_fp8_forward."""
-    import torch
-    _on_device(x.device, y, workspace, *dev.values())
+    at = _on_device(x, y, workspace, *dev.values())
     _bf16_rows(x, K, "x")
     M = x.shape[0]
-    need = fp8_workspace_bytes(K, N, M)
-    with _allocating(x.device, stream):
-        if y is None:
-            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _bf16_rows(y, N, "y")
-    _need(y.shape[0] == M, "y: as many rows as x")
-    p = _fp8_struct(K, N, dev)
-    _call("svdq_fp8_forward", x.device, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(p), x.data_ptr(), M,
-          y.data_ptr(), _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    if y is None:
+        y = _empty((M, N), _t.bfloat16, x, stream)
+    else:
+        _bf16_rows(y, N, "y")
+        _need(y.shape[0] == M, "y: as many rows as x")
+    ws, wsp, size = _scratch(workspace, fp8_workspace_bytes(K, N, M), x, stream)
+    _call("svdq_fp8_forward", at, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(_fp8_struct(K, N, dev)), x.data_ptr(),
+          M, y.data_ptr(), wsp, size)
     return y
 
 
@@ -877,26 +910,21 @@ def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: 
     """y[M][N] = FP8 layer(layer norm(x)) via svdq_fp8_norm_forward, the norm's
     parameters as in layer_norm_forward (`bias` is the norm's; the layer's own
     is in dev). With stats: (y, mean, rstd)."""
-    import torch
-    _on_device(x.device, weight, bias, y, workspace, *dev.values())
+    at = _on_device(x, weight, bias, y, workspace, *dev.values())
     _bf16_rows(x, K, "x")
     M = x.shape[0]
     d, wp, ldw, bp, ldb = _norm_params(K, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
-    need = fp8_norm_workspace_bytes(K, N, M)
+    if y is None:
+        y = _empty((M, N), _t.bfloat16, x, stream)
+    else:
+        _bf16_rows(y, N, "y")
+        _need(y.shape[0] == M, "y: as many rows as x")
+    ws, wsp, size = _scratch(workspace, fp8_norm_workspace_bytes(K, N, M), x, stream)
     mean = rstd = None
-    with _allocating(x.device, stream):
-        if y is None:
-            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        if stats:
-            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device)
-    _bf16_rows(y, N, "y")
-    _need(y.shape[0] == M, "y: as many rows as x")
-    p = _fp8_struct(K, N, dev)
-    _call("svdq_fp8_norm_forward", x.device, stream, ctypes.byref(d), wp, ldw, bp, ldb, ctypes.byref(Fp8Desc(K, N)),
-          ctypes.byref(p), x.data_ptr(), M, y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(workspace),
-          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    if stats:
+        mean, rstd = _empty((2, M), _t.float32, x, stream).unbind()
+    _call("svdq_fp8_norm_forward", at, stream, ctypes.byref(d), wp, ldw, bp, ldb, ctypes.byref(Fp8Desc(K, N)),
+          ctypes.byref(_fp8_struct(K, N, dev)), x.data_ptr(), M, y.data_ptr(), _ptr(mean), _ptr(rstd), wsp, size)
     return (y, mean, rstd) if stats else y
 
 
@@ -904,43 +932,32 @@ def fp8_backward(K: int, N: int, dev: dict, x, dy, need=(True, True, True), work
     """svdq_fp8_backward: (dx [M][K], dw [N][K], db [N]), bf16, of fp8_forward
     for dy [M][N] bf16; None where `need` says no. Without dx, dev may lack qt
     and st; without dw, x may be None."""
-    import torch
-    _on_device(dy.device, x, workspace, *dev.values())
+    at = _on_device(dy, x, workspace, *dev.values())
     _bf16_rows(dy, N, "dy")
     M = dy.shape[0]
     if x is not None:
         _bf16_rows(x, K, "x")
         _need(x.shape[0] == M, "x: as many rows as dy")
-    size = fp8_backward_workspace_bytes(K, N, M)
-    dx = dw = db = None
-    with _allocating(dy.device, stream):
-        if need[0]:
-            dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
-        if need[1]:
-            dw = torch.empty((N, K), dtype=torch.bfloat16, device=dy.device)
-        if need[2]:
-            db = torch.empty(N, dtype=torch.bfloat16, device=dy.device)
-        if workspace is None and size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
-    p = _fp8_struct(K, N, dev)
-    _call("svdq_fp8_backward", dy.device, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(p), _ptr(x), dy.data_ptr(), M,
-          _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace),
-          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    bf16 = _t.bfloat16
+    dx = _empty((M, K), bf16, dy, stream) if need[0] else None
+    dw = _empty((N, K), bf16, dy, stream) if need[1] else None
+    db = _empty((N,), bf16, dy, stream) if need[2] else None
+    ws, wsp, size = _scratch(workspace, fp8_backward_workspace_bytes(K, N, M), dy, stream)
+    _call("svdq_fp8_backward", at, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(_fp8_struct(K, N, dev)), _ptr(x),
+          dy.data_ptr(), M, _ptr(dx), _ptr(dw), _ptr(db), wsp, size)
     return dx, dw, db
 
 
 def fp8_quantize(x, stream=None):
     """svdq_fp8_quantize: (codes uint8 [M][K padded to 128], scale bytes uint8
     [blocks / 4][M][4]) of x bf16 [M][K]."""
-    import torch
-    _on_device(x.device)
-    _bf16_rows(x, x.shape[1], "x")
+    at = _on_device(x)
+    _bf16_rows(x, x.shape[-1], "x")
     M, K = x.shape
     nb = -(-K // 128)
-    with _allocating(x.device, stream):
-        q = torch.empty((M, nb * 128), dtype=torch.uint8, device=x.device)
-        s = torch.zeros((-(-nb // 4), M, 4), dtype=torch.uint8, device=x.device)
-    _call("svdq_fp8_quantize", x.device, stream, x.data_ptr(), M, K, q.data_ptr(), s.data_ptr())
+    q = _empty((M, nb * 128), _t.uint8, x, stream)
+    s = _empty((-(-nb // 4), M, 4), _t.uint8, x, stream)
+    _call("svdq_fp8_quantize", at, stream, x.data_ptr(), M, K, q.data_ptr(), s.data_ptr())
     return q, s
 
 
