@@ -13,7 +13,6 @@ namespace {
 
 constexpr int64_t kMaxRows = 1 << 24;
 constexpr int64_t kMaxGradRows = 1 << 20;   // keeps a tile of a transposed operand below 2^31 bytes
-constexpr int64_t kFp8InlineRows = 16;      // up to here the product quantizes its tokens itself
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 int elem_bytes(int dtype) { return dtype == SVDQ_DT_F32 ? 4 : 2; }
@@ -193,7 +192,7 @@ svdq_status svdq_fp8_pack(const svdq_fp8_desc* d, const void* w, int32_t dtype, 
 svdq_status svdq_fp8_workspace_bytes(const svdq_fp8_desc* d, int64_t M, size_t* out) {
   SVDQ_TRY(check_fp8_m(d, M, kMaxRows));
   if (!out) return SVDQ_ERR_NULL;
-  *out = M <= kFp8InlineRows ? 0 : fp8_ws(d, M).total;
+  *out = fp8_inline(M, d->K) ? 0 : fp8_ws(d, M).total;
   return SVDQ_OK;
 }
 
@@ -204,7 +203,7 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
   if (M == 0) return SVDQ_OK;
   if (!x || !y) return SVDQ_ERR_NULL;
   if (!aligned(x, 16) || !aligned(y, 16)) return SVDQ_ERR_SHAPE;
-  const bool in_line = M <= kFp8InlineRows;
+  const bool in_line = fp8_inline(M, d->K);
   const Fp8Ws L = fp8_ws(d, M);
   if (!in_line) {
     if (!ws) return SVDQ_ERR_NULL;
@@ -223,6 +222,7 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
   SVDQ_TRY(after_launch(launch_fp8_quant_rows(x, M, d->K, b + L.q, b + L.s, false, s), s));
   g.a = b + L.q;
   g.as = b + L.s;
+  g.part = (float*)(b + L.part);
   return after_launch(launch_fp8_gemm(g, cus, s), s);
 }
 
@@ -264,7 +264,9 @@ svdq_status svdq_fp8_norm_forward(const svdq_norm_desc* n, const void* weight, i
   Fp8Gemm g = forward_gemm(d, dev, M, y);
   g.a = b + L.q;
   g.as = b + L.s;
-  return after_launch(launch_fp8_gemm(g, cus, s), s);
+  g.part = (float*)(b + L.part);
+  // (the same kernel as svdq_fp8_forward, so the same sums)
+  return after_launch(fp8_inline(M, d->K) ? launch_fp8_gemm_small(g, cus, s) : launch_fp8_gemm(g, cus, s), s);
 }
 
 svdq_status svdq_fp8_backward_workspace_bytes(const svdq_fp8_desc* d, int64_t M, size_t* out) {
@@ -330,6 +332,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     g.ldb = d->N;
     g.K = d->N;
     g.out = dx;
+    g.part = (float*)(b + L.part);
     SVDQ_TRY(after_launch(launch_fp8_gemm(g, cus, s), s));
   }
   if (dw) {
@@ -346,6 +349,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     g.b_row_scales = 1;
     g.K = round128(M);
     g.out = dw;
+    g.part = (float*)(b + L.part);
     SVDQ_TRY(after_launch(launch_fp8_gemm(g, cus, s), s));
   }
   return SVDQ_OK;

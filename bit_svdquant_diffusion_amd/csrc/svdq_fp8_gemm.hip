@@ -368,146 +368,269 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
 #undef SVDQ_SECOND_HALF
 }
 
-// Few tokens: the weight stream. A workgroup of eight waves owns 16 NT output
-// channels; the waves split the contracted blocks in eight fixed runs (so a
-// token's sum does not depend on the launch) and add their sums in order
-// through LDS. Weights go from memory to the MFMA's operand registers
-// directly: lane (r, c) of v_mfma_f32_16x16x128 holds row r, channels
-// 16 c + (0..15) and 64 + 16 c + (0..15) of the block, so each of its two
-// 16-byte loads covers 64 contiguous bytes of a row. (The order of the
-// channels within a block is free as both operands share it.) With one token
-// tile (TT = 1) and QUANT the wave quantizes its tokens' channels itself in
-// that layout: the four lanes of a token hold a block.
-constexpr int kSmallWaves = 8;
-template <int TT, int NT, bool QUANT>
-__global__ __launch_bounds__(64 * kSmallWaves) void fp8_small_kernel(Fp8Gemm g) {
-  constexpr int kRing = NT * (QUANT ? 2 : TT) >= 4 ? 2 : 4;   // blocks in flight per wave
-  __shared__ float red[kSmallWaves][NT * TT * 4][64];
+// A few tokens: the weight stream, in one launch. A workgroup of W waves owns
+// 16 output channels; the waves take the contracted blocks in turn and add
+// their sums in order through LDS. Weights go from memory to the
+// MFMA's operand registers directly, kRing blocks of a wave in flight:
+// lane (r, c) of v_mfma_f32_16x16x128 holds row r, channels 16 c + (0..15) and
+// 64 + 16 c + (0..15) of the block, so each of its two 16-byte loads covers 64
+// contiguous bytes of a row. (The order of the channels within a block is free
+// as both operands share it.) While its first weights arrive the workgroup
+// quantizes all the tokens, into LDS: they are few enough, and come from the
+// cache. (With every wave quantizing its own runs' channels the codes took
+// as many registers as the weights and their exchange stood between the
+// loads: 15.7 us against 9.0 for one token, 3072 -> 12288, whose weights alone
+// take 7.6 us at the rate of a copy.)
+// CODES: the tokens are codes already (a norm's) and only copied.
+constexpr int kSmallPad = 16;   // bytes between rows of codes in LDS
+template <int W, int kRing, bool CODES>
+__global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
+  extern __shared__ __align__(16) uint8_t smem[];   // codes [a_rows][round128(K) + kSmallPad], scale bytes [a_rows][KB]
+  __shared__ float red[W][4][64];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int KB = (int)((g.K + 127) / 128), b0 = KB * wave / kSmallWaves, b1 = KB * (wave + 1) / kSmallWaves;
-  const int n0 = blockIdx.x * 16 * NT;
-  const uint8_t* wrow[NT];
-  const uint8_t* wsc[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int n = min(n0 + 16 * t + r, g.b_rows - 1);
-    wrow[t] = g.b + (int64_t)n * g.ldb;
-    wsc[t] = g.bs + (int64_t)(min(n0 + 16 * t, g.b_rows - 1) / 128) * ((KB + 3) / 4 * 4);
-  }
-  const uint8_t* arow[TT];
-  const uint8_t* asc[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t m = min((int64_t)(16 * t + r), g.a_rows - 1);
-    arow[t] = QUANT ? reinterpret_cast<const uint8_t*>(g.x + m * g.K) : g.a + m * g.lda;
-    asc[t] = QUANT ? nullptr : g.as + fp8_scale_index(g.a_rows, m, 0);
-  }
-  i32x4 wq[kRing][NT][2];
-  u32x4 xv[kRing][TT][QUANT ? 4 : 2];
-  uint32_t ws[kRing][NT], xs[kRing][TT];
-  auto load = [&](int u, int kb) {
-    kb = min(kb, b1 - 1);   // past the run's end: its last block again, not used
+  const int K = (int)g.K, M = (int)g.a_rows, KB = (K + 127) / 128;
+  const int nb = (KB - wave + W - 1) / W;   // this wave's blocks: wave, wave + W, ...
+  const int n0 = blockIdx.x * 16;   // b_rows % 16 == 0
+  const uint8_t* wrow = g.b + (int64_t)(n0 + r) * g.ldb;
+  const uint8_t* wsc = g.bs + (int64_t)(n0 / 128) * ((KB + 3) / 4 * 4);
+  const int ldx = KB * 128 + kSmallPad;
+  const uint8_t* arow = smem + min(r, M - 1) * ldx;
+  uint8_t* scales = smem + M * ldx;
+  const uint8_t* asc = scales + min(r, M - 1) * KB;
+  i32x4 wq[kRing][2];
+  uint32_t ws[kRing];
+  auto load = [&](int u, int i) {
+    if (i >= nb) return;
+    const int kb = wave + W * i;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int k = kb * 128 + 64 * e + 16 * c;
-      const bool in = k < g.K;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) wq[u][t][e] = in ? *reinterpret_cast<const i32x4*>(wrow[t] + k) : i32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        if constexpr (QUANT) {
-          const u32x4* p = reinterpret_cast<const u32x4*>(arow[t] + 2 * k);
-          xv[u][t][2 * e] = in ? p[0] : u32x4{0, 0, 0, 0};
-          xv[u][t][2 * e + 1] = in ? p[1] : u32x4{0, 0, 0, 0};
-        } else {
-          xv[u][t][e] = *reinterpret_cast<const u32x4*>(arow[t] + k);   // padded to whole blocks
-        }
-      }
+      wq[u][e] = k < K ? *reinterpret_cast<const i32x4*>(wrow + k) : i32x4{0, 0, 0, 0};
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) ws[u][t] = wsc[t][kb];
-    if constexpr (!QUANT) {
-#pragma unroll
-      for (int t = 0; t < TT; ++t) xs[u][t] = asc[t][(size_t)(kb / 4) * round128(g.a_rows) * 4 + kb % 4];
-    }
+    ws[u] = wsc[kb];
   };
-  f32x4 acc[NT][TT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int u = 0; u < kRing; ++u) load(u, u);
+  // eight lanes a block, 16 channels a lane
+  const int per_row = KB * 8, items = M * per_row;
+  for (int i = tid; i < items; i += 64 * W) {
+    const int m = i / per_row, k = (i - m * per_row) * 16;
+    if constexpr (CODES) {
+      *reinterpret_cast<u32x4*>(smem + m * ldx + k) = *reinterpret_cast<const u32x4*>(g.a + (size_t)m * g.lda + k);
+      if ((tid & 7) == 0) scales[m * KB + k / 128] = g.as[fp8_scale_index(M, m, k / 128)];
+      continue;
+    }
+    u32x4 v0 = u32x4{0, 0, 0, 0}, v1 = v0;
+    if (k < K) {
+      const u32x4* p = reinterpret_cast<const u32x4*>(g.x + (size_t)m * K + k);
+      v0 = p[0];
+      v1 = p[1];
+    }
+    uint32_t amax = 0;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (b0 < b1) {
+    for (int q = 0; q < 4; ++q) amax = amax_bf16x2(amax_bf16x2(amax, v0[q]), v1[q]);
+    const int e = e4m3_exponent(max_dpp8(amax));
+    const float sc = exp2_int(e);
+    *reinterpret_cast<u32x4*>(smem + m * ldx + k) =
+        u32x4{e4m3x4(bf16lo(v0[0]), bf16hi(v0[0]), bf16lo(v0[1]), bf16hi(v0[1]), sc),
+              e4m3x4(bf16lo(v0[2]), bf16hi(v0[2]), bf16lo(v0[3]), bf16hi(v0[3]), sc),
+              e4m3x4(bf16lo(v1[0]), bf16hi(v1[0]), bf16lo(v1[1]), bf16hi(v1[1]), sc),
+              e4m3x4(bf16lo(v1[2]), bf16hi(v1[2]), bf16lo(v1[3]), bf16hi(v1[3]), sc)};
+    if ((tid & 7) == 0) scales[m * KB + k / 128] = (uint8_t)(e + 127);
+  }
+  __syncthreads();
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < nb; i += kRing) {
 #pragma unroll
-    for (int u = 0; u < kRing; ++u) load(u, b0 + u);
-    for (int kb = b0; kb < b1; kb += kRing) {
-#pragma unroll
-      for (int u = 0; u < kRing; ++u) {
-        if (kb + u < b1) {
-          i32x8 fx[TT];
-          int sx[TT];
-#pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            if constexpr (QUANT) {
-              uint32_t amax = 0;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) amax = amax_bf16x2(amax, xv[u][t][i >> 2][i & 3]);
-              // the token's other lanes: c ^ 1 (16 lanes on) and c ^ 2 (32)
-              auto s1 = __builtin_amdgcn_permlane16_swap(amax, amax, false, false);
-              amax = umax(s1[0], s1[1]);
-              auto s2 = __builtin_amdgcn_permlane32_swap(amax, amax, false, false);
-              amax = umax(s2[0], s2[1]);
-              const int e = e4m3_exponent(amax);
-              const float sc = exp2_int(e);
-              sx[t] = e + 127;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t w0 = xv[u][t][i >> 1][2 * (i & 1)], w1 = xv[u][t][i >> 1][2 * (i & 1) + 1];
-                fx[t][i] = (int)e4m3x4(bf16lo(w0), bf16hi(w0), bf16lo(w1), bf16hi(w1), sc);
-              }
-            } else {
-              const u32x4 x0 = xv[u][t][0], x1 = xv[u][t][1];
-              fx[t] = i32x8{(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-              sx[t] = (int)xs[u][t];
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const i32x4 w0 = wq[u][n][0], w1 = wq[u][n][1];
-            const i32x8 fw = i32x8{w0[0], w0[1], w0[2], w0[3], w1[0], w1[1], w1[2], w1[3]};
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-              acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fx[t], acc[n][t], 0, 0, 0, (int)ws[u][n], 0, sx[t]);
-          }
-          if (kb + u + kRing < b1) load(u, kb + u + kRing);
-        }
+    for (int u = 0; u < kRing; ++u) {
+      if (i + u < nb) {
+        const int kb = wave + W * (i + u);
+        const uint8_t* p = arow + kb * 128 + 16 * c;
+        const i32x4 x0 = *reinterpret_cast<const i32x4*>(p), x1 = *reinterpret_cast<const i32x4*>(p + 64);
+        const i32x4 w0 = wq[u][0], w1 = wq[u][1];
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            i32x8{w0[0], w0[1], w0[2], w0[3], w1[0], w1[1], w1[2], w1[3]},
+            i32x8{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]}, acc, 0, 0, 0, (int)ws[u], 0, (int)asc[kb]);
+        load(u, i + u + kRing);
       }
     }
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][(n * TT + t) * 4 + e][lane] = acc[n][t][e];
+  for (int e = 0; e < 4; ++e) red[wave][e][lane] = acc[e];
   __syncthreads();
-  // a thread adds the waves' sums of pairs of consecutive channels: value e of
-  // lane (r, c) is token 16 t + r, channel n0 + 16 n + 4 c + e
-  for (int i = tid; i < NT * TT * 2 * 64; i += 64 * kSmallWaves) {
-    const int l = i & 63, pe = (i >> 6) & 1, nt = i >> 7, n = nt / TT, t = nt % TT;
+  // a thread adds the waves' sums of two consecutive channels: value e of
+  // lane (r, c) is token r, channel n0 + 4 c + e
+  if (tid < 128) {
+    const int pe = tid >> 6;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSmallWaves; ++w) {
-      s0 += red[w][nt * 4 + 2 * pe][l];
-      s1 += red[w][nt * 4 + 2 * pe + 1][l];
+    for (int w = 0; w < W; ++w) {
+      s0 += red[w][2 * pe][lane];
+      s1 += red[w][2 * pe + 1][lane];
     }
-    const int64_t m = 16 * t + (l & 15);
-    const int col = n0 + 16 * n + 4 * (l >> 4) + 2 * pe;
-    if (m < g.a_rows && col < g.b_rows) {
+    if (r < M) {
+      const int col = n0 + 4 * c + 2 * pe;
       const uint32_t b = g.bias ? *reinterpret_cast<const uint32_t*>(g.bias + col) : 0u;
-      *reinterpret_cast<uint32_t*>(g.out + m * g.b_rows + col) = cvt_bf16x2(s0 + bf16lo(b), s1 + bf16hi(b));
+      *reinterpret_cast<uint32_t*>(g.out + (size_t)r * g.b_rows + col) = cvt_bf16x2(s0 + bf16lo(b), s1 + bf16hi(b));
     }
   }
+}
+
+// Few tiles (fp8_deep): 64 x 64 outputs a workgroup, and where those do not
+// fill the CUs a tile's contracted blocks in several runs (`chunk` blocks, a
+// multiple of four), whose fp32 sums fp8_join_kernel adds in order. There is
+// little work a CU, so a stage's time is the wait for its transfers: LDS is a
+// ring of D whole stages with all but one in flight. Per stage: the wait for
+// the next one, the barrier, the transfers into the slot of the stage whose
+// fragments have been read, the next stage's fragment reads, and this one's
+// multiplications behind them. Four waves hold 32 x 32 each. Scale words (four
+// stages' bytes) are read four stages ahead.
+//
+// With D = 5 two workgroups fit a CU, with 3 three. Measured: a stage takes
+// 0.28 us without its transfers (the LDS reads), 0.3 to 0.45 with them (the
+// misses of the L2s). Tiles of 64 x 128 and 128 x 128 took as long or longer
+// wherever they are fewer than the CUs (12288 channels, 64 tokens, 3072
+// outputs: 20.5 us, 20.7 and 22; 2064, 1003 and 1552: 16.2, 15.8 and 18.1).
+constexpr int kDeepStage = 2 * 64 * 128, kDeepOps = 4;   // bytes of a stage; transfers per wave and stage
+template <int D, bool BROW>
+__global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int chunk) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  static_assert(D - 2 <= 4, "scale words are four stages ahead of their use, the transfers no more");
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int Ra = (int)g.a_rows, Rb = g.b_rows, K = (int)g.K, KR = (K + 127) / 128;
+  const int lda = (int)g.lda, ldb = (int)g.ldb;
+  // an XCD (workgroups 8 apart) takes consecutive tiles of one run of
+  // channels, those of the same weights next to each other
+  const int all = (int)gridDim.x, xcd = (int)blockIdx.x & 7;
+  const int t = xcd * (all >> 3) + min(xcd, all & 7) + ((int)blockIdx.x >> 3);
+  const int m0 = t % tiles_m * 64, tn_ = t / tiles_m, n0 = tn_ % tiles_n * 64, run = tn_ / tiles_n;
+  const int s0 = run * chunk, s1 = min(KR, s0 + chunk);
+
+  // Transfers: the first two waves' are A's row octets, the others' B's; rows
+  // past the operand read as zeros.
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(g.a + (size_t)m0 * lda), 0, min(64, Ra - m0) * lda, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(g.b + (size_t)n0 * ldb), 0, min(64, Rb - n0) * ldb, kRsrcWord3);
+  const int ck0 = (lane & 7) ^ (lane >> 4);   // the lane's chunk of the even octets; of the odd ones ^ 4
+  auto fetch = [&](int s, int slot) {
+    const int k = s * 128;
+    uint8_t* dst = smem + slot * kDeepStage + wave * kDeepOps * 1024;
+    const __amdgpu_buffer_rsrc_t res = wave < 2 ? ra : rb;
+    const int ld = wave < 2 ? lda : ldb;
+#pragma unroll
+    for (int i = 0; i < kDeepOps; ++i) {
+      const int ck = (i & 1) ? ck0 ^ 4 : ck0;
+      lds_transfer(res, dst + i * 1024, s < s1 && 16 * ck < K - k ? (uint32_t)((lane >> 3) * ld + 16 * ck) : kOutside,
+                   ((wave & 1) * kDeepOps + i) * 8 * ld + k);
+    }
+  };
+  // LDS offsets in a stage of this lane's fragment chunks: rows (+ 32 t),
+  // chunk 4 step + 2 h + e at place chunk ^ (row / 2 % 8)
+  const int sw = (lr >> 1) & 7;
+  uint32_t at[2][2];
+#pragma unroll
+  for (int st = 0; st < 2; ++st)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) at[st][e] = (uint32_t)(lr * 128 + ((4 * st + 2 * h + e) ^ sw) * 16);
+  const uint32_t base_a = wm * 4096, base_b = 8192 + wn * 4096;
+  // scale words of this lane's rows (rows past the operand read its first words)
+  const int row0 = m0 + wm * 32, col0 = n0 + wn * 32;
+  const size_t ga = (size_t)round128(Ra), gb = BROW ? (size_t)round128(Rb) : 1;
+  const uint32_t* pa = reinterpret_cast<const uint32_t*>(g.as) + lr * 4 + (row0 < Ra ? row0 / 128 * 128 + row0 % 128 / 32 : 0);
+  const uint32_t* pb = reinterpret_cast<const uint32_t*>(g.bs) +
+                       (BROW ? lr * 4 + (col0 < Rb ? col0 / 128 * 128 + col0 % 128 / 32 : 0) : n0 / 128 * ((KR + 3) / 4));
+  uint32_t na, nb;
+  auto scales = [&](int grp) {
+    grp = min(grp, (KR - 1) / 4);
+    na = pa[grp * ga];
+    nb = pb[grp * gb];
+  };
+  f32x16 acc = f32x16{};
+  i32x8 fa[2][2], fb[2][2];   // a stage's fragments: set, step
+  auto read = [&](int set, int slot) {
+    const uint8_t* stage = smem + slot * kDeepStage;
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const i32x4 b0 = *reinterpret_cast<const i32x4*>(stage + base_b + at[st][0]);
+      const i32x4 b1 = *reinterpret_cast<const i32x4*>(stage + base_b + at[st][1]);
+      const i32x4 a0 = *reinterpret_cast<const i32x4*>(stage + base_a + at[st][0]);
+      const i32x4 a1 = *reinterpret_cast<const i32x4*>(stage + base_a + at[st][1]);
+      fb[set][st] = i32x8{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
+      fa[set][st] = i32x8{a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+    }
+  };
+  scales(s0 / 4);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u) fetch(s0 + u, u);
+  ring_barrier<(D - 2) * kDeepOps>();   // the first stage
+  fetch(s0 + D - 1, D - 1);
+  __builtin_amdgcn_sched_barrier(0);
+  read(0, 0);
+  int slot = 0;
+  for (int s = s0; s < s1; s += 4) {
+    const uint32_t wa = na, wb = nb;
+    scales(s / 4 + 1);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (s + u < s1) {
+        // the next stage has arrived, and every wave has read this one
+        ring_barrier<(D - 2) * kDeepOps>();
+        fetch(s + u + D, slot);
+        __builtin_amdgcn_sched_barrier(0);
+        slot = slot + 1 == D ? 0 : slot + 1;
+        read((u + 1) & 1, slot);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+          acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[u & 1][st], fa[u & 1][st], acc, 0, 0, 0,
+                                                                (int)(wb >> (8 * u)), 0, (int)(wa >> (8 * u)));
+      }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // the transfers past the end land before the LDS is given up
+
+  // a lane holds token row0 + lr and channels col0 + 8 q + 4 h + (0..3)
+  const int row = row0 + lr, col = col0 + 4 * h;
+  if (row >= Ra) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (col + 8 * q >= Rb) continue;
+    f32x4 v = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    if (g.part) {
+      *reinterpret_cast<f32x4*>(g.part + ((size_t)run * Ra + row) * Rb + col + 8 * q) = v;
+    } else {
+      if (g.bias) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(g.bias + col + 8 * q);
+        v += f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
+      }
+      *reinterpret_cast<u32x2*>(g.out + (size_t)row * Rb + col + 8 * q) = u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+    }
+  }
+}
+
+// the runs' sums, in order, and the bias: four channels a thread
+__global__ __launch_bounds__(256) void fp8_join_kernel(const float* part, int runs, int64_t quads, int N, const uint16_t* bias,
+                                                       uint16_t* out) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= quads) return;
+  const f32x4* p = reinterpret_cast<const f32x4*>(part) + at;
+  f32x4 v = p[0];
+  int r = 1;
+  for (; r + 4 <= runs; r += 4) {
+    const f32x4 a = p[(r)*quads], b = p[(r + 1) * quads], c = p[(r + 2) * quads], d = p[(r + 3) * quads];
+    v = (((v + a) + b) + c) + d;
+  }
+  for (; r < runs; ++r) v += p[r * quads];
+  if (bias) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(bias + at % (N / 4) * 4);
+    v += f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
+  }
+  *reinterpret_cast<u32x2*>(out + 4 * at) = u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
 }
 
 typedef Tile<256, 256, 2, 2> TileL;
@@ -537,28 +660,53 @@ hipError_t prepare_fp8() {
   for (hipError_t e : {prepare_tile<TileW, false>(), prepare_tile<TileW, true>(), prepare_tile<TileL, false>(), prepare_tile<TileL, true>(), prepare_tile<TileM, false>(),
                        prepare_tile<TileM, true>()})
     if (e != hipSuccess) return e;
+  for (const void* f : {(const void*)fp8_deep_kernel<5, false>, (const void*)fp8_deep_kernel<5, true>,
+                        (const void*)fp8_small_kernel<16, 2, false>, (const void*)fp8_small_kernel<16, 2, true>}) {
+    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, 5 * kDeepStage);
+    if (e != hipSuccess) return e;
+  }
   return hipSuccess;
 }
 
-bool fp8_gemm_small_fits(const Fp8Gemm& g) { return g.a_rows <= 64 && !g.b_row_scales; }
-
 hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st) {
-  (void)num_cus;
-  const dim3 b(64 * kSmallWaves);
-  if (g.x) {
-    hipLaunchKernelGGL((fp8_small_kernel<1, 1, true>), dim3((g.b_rows + 15) / 16), b, 0, st, g);
-  } else if (g.a_rows <= 16) {
-    hipLaunchKernelGGL((fp8_small_kernel<1, 1, false>), dim3((g.b_rows + 15) / 16), b, 0, st, g);
-  } else if (g.a_rows <= 32) {
-    hipLaunchKernelGGL((fp8_small_kernel<2, 1, false>), dim3((g.b_rows + 15) / 16), b, 0, st, g);
+  const int KB = (int)((g.K + 127) / 128), grid = g.b_rows / 16;
+  const size_t lds = (size_t)g.a_rows * (KB * 128 + kSmallPad + KB);
+  // Where a wave of eight has more than four blocks and no CU has two
+  // workgroups, sixteen share them (one token, 12288 -> 3072: 10.6 us against
+  // 13.3; with 24 blocks, 3072 -> 3072, eight take 4.5 us and sixteen 5.0).
+  const dim3 n((unsigned)grid);
+  if (grid <= num_cus && KB > 32) {
+    if (g.x) hipLaunchKernelGGL((fp8_small_kernel<16, 2, false>), n, dim3(1024), lds, st, g);
+    else hipLaunchKernelGGL((fp8_small_kernel<16, 2, true>), n, dim3(1024), lds, st, g);
   } else {
-    hipLaunchKernelGGL((fp8_small_kernel<4, 1, false>), dim3((g.b_rows + 15) / 16), b, 0, st, g);
+    if (g.x) hipLaunchKernelGGL((fp8_small_kernel<8, 3, false>), n, dim3(512), lds, st, g);
+    else hipLaunchKernelGGL((fp8_small_kernel<8, 3, true>), n, dim3(512), lds, st, g);
   }
   return hipGetLastError();
 }
 
+namespace {
+template <bool BROW>
+hipError_t launch_deep(Fp8Gemm g, const Fp8Deep& p, hipStream_t st) {
+  if (p.runs == 1) g.part = nullptr;
+  const int tm = (int)((g.a_rows + 63) / 64), tn = (g.b_rows + 63) / 64;
+  const unsigned grid = (unsigned)(tm * tn * p.runs);
+  if (grid <= kFp8Cus)
+    hipLaunchKernelGGL((fp8_deep_kernel<5, BROW>), dim3(grid), dim3(256), 5 * kDeepStage, st, g, tm, tn, p.chunk);
+  else
+    hipLaunchKernelGGL((fp8_deep_kernel<3, BROW>), dim3(grid), dim3(256), 3 * kDeepStage, st, g, tm, tn, p.chunk);
+  if (p.runs > 1) {
+    const int64_t quads = g.a_rows * g.b_rows / 4;
+    hipLaunchKernelGGL(fp8_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, g.part, p.runs, quads, g.b_rows,
+                       g.bias, g.out);
+  }
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st) {
-  if (fp8_gemm_small_fits(g)) return launch_fp8_gemm_small(g, num_cus, st);
+  const Fp8Deep p = fp8_deep(g.a_rows, g.b_rows, g.K);
+  if (p.runs > 0) return g.b_row_scales ? launch_deep<true>(g, p, st) : launch_deep<false>(g, p, st);
   // The tile of least cost, a cost being the rounds of tiles over the CUs times
   // a round's time relative to TileL's, as measured on the products of K from
   // 2048 to 12288: TileW 0.85 (it fills the CUs where TileL's rounds do not:

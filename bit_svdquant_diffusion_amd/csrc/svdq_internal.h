@@ -170,9 +170,9 @@ struct Fp8Gemm {
   int64_t K;           // contracted channels
   const uint16_t* bias;
   uint16_t* out;       // bf16 [a_rows][b_rows]
-  const uint16_t* x;   // few tokens: A as bf16 rows [a_rows][K], quantized by the product itself (a null)
+  float* part;         // fp32 [fp8_deep's runs][a_rows][b_rows], where there are more than one
+  const uint16_t* x;   // launch_fp8_gemm_small: A as bf16 rows [a_rows][K], or null
 };
-bool fp8_gemm_small_fits(const Fp8Gemm& g);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st);
 hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st);
 hipError_t prepare_fp8();

@@ -196,23 +196,57 @@ inline svdq_status check_fp8_desc(const svdq_fp8_desc* d) {
   return SVDQ_OK;
 }
 
-// Workspace of the FP8 forward: the activations' codes [M][round128(K)] and
-// their scales.
+// Up to here the FP8 product quantizes its tokens itself: 16 rows fill the
+// MFMA's tile, and their codes fit in 64 KB of LDS beside the waves' sums.
+inline bool fp8_inline(int64_t M, int64_t K) { return M <= 16 && M * round128(K) <= 49152; }
+
+// The FP8 product with few tiles: runs of `chunk` blocks of 128 contracted
+// channels per 64 x 64 tile, or runs = 0 where the large tiles are faster.
+// Measured on 256 CUs (workspaces' sizes are asked for without a device, so
+// the plan is this card's): up to 448 tiles it is (400 tiles of 2064 channels
+// 16.2 us against 16.5, 384 of 3072 16.4 against 19.1, 512 of 1024 12.6
+// against 12.2, 768 of 3072 25.8 against 23.4); runs fill the CUs where each
+// is then at least twelve blocks shorter than the whole, which pays for the
+// launch that joins them (96 tiles of 24 blocks: 12.3 us with one run or two).
+constexpr int kFp8Cus = 256;
+struct Fp8Deep {
+  int runs, chunk;
+};
+inline Fp8Deep fp8_deep(int64_t rows, int64_t cols, int64_t K) {
+  const int64_t tiles = ((rows + 63) / 64) * ((cols + 63) / 64), KB = (K + 127) / 128;
+  if (tiles == 0 || KB == 0 || tiles > 448) return Fp8Deep{0, 0};
+  const int64_t want = kFp8Cus / tiles;
+  if (want > 1) {
+    const int64_t chunk = ((KB + want - 1) / want + 3) / 4 * 4;
+    if (KB - chunk >= 12) return Fp8Deep{(int)((KB + chunk - 1) / chunk), (int)chunk};
+  }
+  return Fp8Deep{1, (int)((KB + 3) / 4 * 4)};
+}
+// bytes of its runs' sums
+inline size_t fp8_deep_bytes(int64_t rows, int64_t cols, int64_t K) {
+  const Fp8Deep p = fp8_deep(rows, cols, K);
+  return p.runs > 1 ? align256((size_t)p.runs * rows * cols * 4) : 0;
+}
+
+// Workspace of the FP8 forward: the activations' codes [M][round128(K)],
+// their scales and the sums of runs.
 struct Fp8Ws {
-  size_t q, s, total;
+  size_t q, s, part, total;
 };
 inline Fp8Ws fp8_ws(const svdq_fp8_desc* d, int64_t M) {
   Fp8Ws w;
   w.q = 0;
   w.s = align256((size_t)M * round128(d->K));
-  w.total = w.s + align256(fp8_scale_bytes(M, d->K));
+  w.part = w.s + align256(fp8_scale_bytes(M, d->K));
+  w.total = w.part + fp8_deep_bytes(M, d->N, d->K);
   return w;
 }
 // Workspace of the backward: dY's codes along the output channels [M][round128(N)],
 // dY^T [N][round128(M)] and X^T [K][round128(M)] along the tokens, their
-// scales, and dY's sums per 128 tokens fp32 [round128(M)/128][N].
+// scales, dY's sums per 128 tokens fp32 [round128(M)/128][N], and the sums of
+// runs of one product after the other.
 struct Fp8GradWs {
-  size_t q, s, yt, yts, xt, xts, db, total;
+  size_t q, s, yt, yts, xt, xts, db, part, total;
 };
 inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   Fp8GradWs w;
@@ -224,7 +258,9 @@ inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   w.xt = w.yts + align256(fp8_scale_bytes(d->N, M));
   w.xts = w.xt + align256((size_t)d->K * mp);
   w.db = w.xts + align256(fp8_scale_bytes(d->K, M));
-  w.total = w.db + align256((size_t)(mp / 128) * d->N * 4);
+  w.part = w.db + align256((size_t)(mp / 128) * d->N * 4);
+  const size_t px = fp8_deep_bytes(M, d->K, d->N), pw = fp8_deep_bytes(d->N, d->K, mp);
+  w.total = w.part + (px > pw ? px : pw);
   return w;
 }
 

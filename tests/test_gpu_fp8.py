@@ -327,3 +327,62 @@ def test_modulated_norm_between_the_w4a16_and_w4a4_layers():
     assert bool(((h.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-4).all())
     y = lin(h)
     C.check_y(C.bf16_tensor_to_f32(y), O.forward(ref, h.float().cpu().numpy()), "norm then w4a4")
+
+
+# few outputs over many channels (their runs are joined), the last run short,
+# and persistent workgroups with several of the largest tiles
+@pytest.mark.parametrize("M,K,N", [(17, 4112, 80), (33, 12288, 64), (64, 2064, 1040), (130, 8208, 272), (20, 65536, 16),
+                                   (300, 1936, 144), (4090, 272, 4080), (8200, 144, 8208)])
+def test_forward_runs_and_tiles(M, K, N):
+    g = torch.Generator(device="cuda").manual_seed(M + K + N)
+    x = _bf16(g, M, K)
+    _, dev = _layer(g, K, N, transposed=False)
+    need = S.fp8_workspace_bytes(K, N, M)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    y = S.fp8_forward(K, N, dev, x, workspace=ws[:need])
+    assert bool((ws[need:] == 0xFF).all())
+    a, w = R.q8(x.double())[0], _weight(dev, K, N)
+    bias = dev["bias"].double()
+    _close(y, a @ w.t().contiguous() + bias, R.product_bound(a, w, bias), (M, K, N))
+    assert torch.equal(y, S.fp8_forward(K, N, dev, x))
+
+
+@pytest.mark.parametrize("M,K,N", [(4112, 80, 48), (40, 48, 4112), (300, 4080, 4096)])
+def test_backward_runs_and_tiles(M, K, N):
+    g = torch.Generator(device="cuda").manual_seed(M + K + N)
+    x, dy = _bf16(g, M, K), _bf16(g, M, N, scale=1e-3)
+    _, dev = _layer(g, K, N)
+    need = S.fp8_backward_workspace_bytes(K, N, M)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    dx, dw, _ = S.fp8_backward(K, N, dev, x, dy, workspace=ws[:need])
+    assert bool((ws[need:] == 0xFF).all())
+    w = _weight(dev, K, N)
+    a = R.q8(dy.double())[0]
+    _close(dx, a @ w, R.product_bound(a, w.t().contiguous()), ("dx", M, K, N))
+    ty, tx = R.q8(dy.double(), 0)[0].t().contiguous(), R.q8(x.double(), 0)[0].t().contiguous()
+    _close(dw, ty @ tx.t().contiguous(), R.product_bound(ty, tx), ("dw", M, K, N))
+
+
+@pytest.mark.parametrize("M", [1, 2, 16])
+def test_norm_forward_of_a_few_tokens_is_the_composition(M):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    K, N = 528, 272
+    x = _bf16(g, M, K)
+    _, dev = _layer(g, K, N, transposed=False)
+    w = torch.randn(K, device="cuda", generator=g).to(torch.bfloat16)
+    h = S.layer_norm_forward(x, w)[0]
+    assert torch.equal(S.fp8_norm_forward(K, N, dev, x, w), S.fp8_forward(K, N, dev, h))
+
+
+def test_inline_limit():
+    """Both sides of the size up to which one kernel quantizes its own tokens."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N = 48
+    for M, K in [(16, 3072), (16, 3088), (1, 49152), (1, 49168), (3, 16384), (3, 16400)]:
+        x = _bf16(g, M, K)
+        _, dev = _layer(g, K, N, transposed=False)
+        assert (S.fp8_workspace_bytes(K, N, M) == 0) == (M * (-(-K // 128) * 128) <= 49152)
+        y = S.fp8_forward(K, N, dev, x)
+        a, w = R.q8(x.double())[0], _weight(dev, K, N)
+        bias = dev["bias"].double()
+        _close(y, a @ w.t().contiguous() + bias, R.product_bound(a, w, bias), (M, K, N))
