@@ -45,7 +45,7 @@ svdq_status check_device(int* cus, void** scratch_ptr) {
       bool ok = hipGetDeviceProperties(&p, dev) == hipSuccess &&
                 std::strncmp(p.gcnArchName, "gfx950", 6) == 0 && prepare_gemm_mxfp4() == hipSuccess &&
                 prepare_gemm_int4() == hipSuccess && prepare_stage1() == hipSuccess && prepare_awq() == hipSuccess &&
-                prepare_fp8() == hipSuccess &&
+                prepare_fp8() == hipSuccess && prepare_norm() == hipSuccess &&
                 hipGetSymbolAddress(&sp, HIP_SYMBOL(scratch)) == hipSuccess && sp != nullptr;
       s = ok ? 1 : 2;
       if (ok) {

@@ -1,6 +1,7 @@
 // C-ABI entry points of the layer norm and the FP8 linear: argument checks,
 // workspace carving and launches on the caller's stream. No allocation, no
 // synchronization, nothing printed.
+#include <algorithm>
 #include <cstring>
 
 #include "svdq.h"
@@ -50,7 +51,7 @@ NormArgs norm_args(const svdq_norm_desc* d, const void* x, int64_t ldx, const vo
   a.G = d->groups;
   a.eps = d->eps;
   a.M = M;
-  a.rpg = d->rows_per_group;
+  a.rpg = std::min<int64_t>(d->rows_per_group, std::max<int64_t>(M, 1));   // (past M the same groups)
   a.x = x;
   a.ldx = ldx;
   a.w = w;

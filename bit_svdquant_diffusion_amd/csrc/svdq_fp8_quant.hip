@@ -191,7 +191,7 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const T* w, int K, int N,
     for (int i = 0; i < 16; i += kVec<T>) {
       Vec<T> in;
       in.w = u32x4{0, 0, 0, 0};
-      if (n < N && k < K) in = load_vec<T>(w + (size_t)n * K, k + i, K);
+      if (n < N && k < K) in = load_vec<T>(w + (size_t)n * K, k + i, kVec<T>);
 #pragma unroll
       for (int t = 0; t < kVec<T>; ++t) {
         v[p][i + t] = in.at(t);

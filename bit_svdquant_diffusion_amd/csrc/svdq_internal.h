@@ -133,6 +133,7 @@ struct NormGradArgs {
   float* part;       // [G][runs][2][C], null when a group is one run
 };
 hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st);
+hipError_t prepare_norm();
 hipError_t launch_norm_grad(const NormGradArgs& g, const NormGradPlan& p, hipStream_t st);
 
 // E4M3 quantizers (svdq_fp8_quant.hip)

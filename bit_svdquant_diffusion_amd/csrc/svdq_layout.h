@@ -264,21 +264,22 @@ inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   return w;
 }
 
-// Layer-norm backward: every group's rows in `runs` runs of rows_per_run, one
-// workgroup each, about 512 in all (two per CU).
+// Layer-norm backward: every group's rows in `runs` runs, one workgroup each,
+// about kNormRuns in all.
+constexpr int kNormRuns = 256;
 struct NormGradPlan {
   int runs;
-  int64_t rows_per_run;
+  int64_t rows_per_run;   // at most
 };
 inline NormGradPlan norm_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group) {
   const int64_t rows = rows_per_group < M ? rows_per_group : M;
   const int64_t live = M > 0 ? (M + rows_per_group - 1) / rows_per_group : 1;   // groups that have rows
-  int64_t runs = 512 / live;
-  if (runs > (rows + 7) / 8) runs = (rows + 7) / 8;   // at least eight rows each
-  if (runs < 1 || groups > 512) runs = 1;
+  int64_t runs = kNormRuns / live;
+  if (runs > (rows + 3) / 4) runs = (rows + 3) / 4;   // at least four rows each
+  if (runs < 1 || groups > kNormRuns) runs = 1;
   NormGradPlan p;
+  p.runs = (int)runs;
   p.rows_per_run = rows > 0 ? (rows + runs - 1) / runs : 1;
-  p.runs = rows > 0 ? (int)((rows + p.rows_per_run - 1) / p.rows_per_run) : 1;
   return p;
 }
 inline size_t norm_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C) {

@@ -63,64 +63,84 @@ struct Vec {
   }
 };
 
-// elements [c, c + kVec) of a row of C elements: one 16-byte load, or, where
-// the row ends inside the vector, its elements one by one with zeros after
+// The n elements of a row of C that the lane with vector c / n handles. Where
+// the row ends inside the vector it is moved back to end with the row, so that
+// one wide access serves (its first elements are then another lane's, too:
+// `own` is zero for them and all ones for the lane's own, and what both lanes
+// write is the same). A row shorter than a vector is taken element by element
+// (len < n). A lane past the row reads the row's end and owns nothing.
+template <int n>
+struct Window {
+  int at, len;
+  uint32_t own[n];
+};
+template <int n>
+__device__ __forceinline__ Window<n> window(int c, int C) {
+  Window<n> w;
+  w.at = C < n ? 0 : min(c, C - n);
+  w.len = min(C, n);
+#pragma unroll
+  for (int i = 0; i < n; ++i) w.own[i] = w.at + i >= c && w.at + i < C ? ~0u : 0u;
+  return w;
+}
+__device__ __forceinline__ float own_or_0(float v, uint32_t own) { return __uint_as_float(__float_as_uint(v) & own); }
+
 template <typename T>
-__device__ __forceinline__ Vec<T> load_vec(const T* row, int c, int C) {
+__device__ __forceinline__ Vec<T> load_vec(const T* row, int at, int len) {
   Vec<T> o;
-  o.w = u32x4{0, 0, 0, 0};
-  if (c + kVec<T> <= C) {
-    memcpy(&o.w, row + c, 16);
-  } else if (c < C) {
+  if (len == kVec<T>) {   // uniform
+    memcpy(&o.w, row + at, 16);
+  } else {
+    o.w = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kVec<T>; ++i)
-      if (c + i < C) {
+      if (i < len) {
         if constexpr (sizeof(T) == 4)
-          o.w[i] = __float_as_uint(row[c + i]);
+          o.w[i] = __float_as_uint(row[i]);
         else
-          o.w[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + i]) << (16 * (i & 1));
+          o.w[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[i]) << (16 * (i & 1));
       }
   }
   return o;
 }
 template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int c, int C, const Vec<T>& o) {
-  if (c + kVec<T> <= C) {
-    memcpy(row + c, &o.w, 16);
-  } else if (c < C) {
+__device__ __forceinline__ void store_vec(T* row, int at, int len, const Vec<T>& o) {
+  if (len == kVec<T>) {
+    memcpy(row + at, &o.w, 16);
+  } else {
 #pragma unroll
     for (int i = 0; i < kVec<T>; ++i)
-      if (c + i < C) {
+      if (i < len) {
         if constexpr (sizeof(T) == 4)
-          row[c + i] = __uint_as_float(o.w[i]);
+          row[i] = __uint_as_float(o.w[i]);
         else
-          row[c + i] = __builtin_bit_cast(T, (uint16_t)(o.w[i >> 1] >> (16 * (i & 1))));
+          row[i] = __builtin_bit_cast(T, (uint16_t)(o.w[i >> 1] >> (16 * (i & 1))));
       }
   }
 }
 
-// n consecutive parameters from element c on as floats, in any of the three
-// types (a uniform branch); zeros past C
+// a window's parameters as floats, in any of the three types (a uniform
+// branch); zeros past the row
 template <int n, typename P>
-__device__ __forceinline__ void load_params_as(const P* p, int c, int C, float* o) {
-  if (c + n <= C) {
+__device__ __forceinline__ void load_params_as(const P* p, int at, int len, float* o) {
+  if (len == n) {
     P v[n];
-    memcpy(v, p + c, sizeof(v));
+    memcpy(v, p + at, sizeof(v));
 #pragma unroll
     for (int i = 0; i < n; ++i) o[i] = to_f32<P>(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < n; ++i) o[i] = c + i < C ? to_f32<P>(p[c + i]) : 0.f;
+    for (int i = 0; i < n; ++i) o[i] = i < len ? to_f32<P>(p[i]) : 0.f;
   }
 }
 template <int n>
-__device__ __forceinline__ void load_params(const void* p, int dtype, int64_t at, int c, int C, float* o) {
+__device__ __forceinline__ void load_params(const void* p, int dtype, int64_t row, int at, int len, float* o) {
   if (dtype == SVDQ_DT_F32)
-    load_params_as<n>(static_cast<const float*>(p) + at, c, C, o);
+    load_params_as<n>(static_cast<const float*>(p) + row, at, len, o);
   else if (dtype == SVDQ_DT_BF16)
-    load_params_as<n>(static_cast<const Bf16*>(p) + at, c, C, o);
+    load_params_as<n>(static_cast<const Bf16*>(p) + row, at, len, o);
   else
-    load_params_as<n>(static_cast<const Half*>(p) + at, c, C, o);
+    load_params_as<n>(static_cast<const Half*>(p) + row, at, len, o);
 }
 __device__ __forceinline__ void store_param(void* p, int dtype, int64_t at, float v) {
   if (dtype == SVDQ_DT_F32)
@@ -129,6 +149,29 @@ __device__ __forceinline__ void store_param(void* p, int dtype, int64_t at, floa
     static_cast<Bf16*>(p)[at] = from_f32<Bf16>(v);
   else
     static_cast<Half*>(p)[at] = from_f32<Half>(v);
+}
+
+template <int n, typename P>
+__device__ __forceinline__ void store_params_as(P* p, int len, const float* v) {
+  P o[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) o[i] = from_f32<P>(v[i]);
+  if (len == n) {
+    memcpy(p, o, sizeof(o));
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      if (i < len) p[i] = o[i];
+  }
+}
+template <int n>
+__device__ __forceinline__ void store_params(void* p, int dtype, int64_t at, int len, const float* v) {
+  if (dtype == SVDQ_DT_F32)
+    store_params_as<n>(static_cast<float*>(p) + at, len, v);
+  else if (dtype == SVDQ_DT_BF16)
+    store_params_as<n>(static_cast<Bf16*>(p) + at, len, v);
+  else
+    store_params_as<n>(static_cast<Half*>(p) + at, len, v);
 }
 
 // Butterflies over 16 lanes with DPP moves (quad permutes for distances 1 and
@@ -158,12 +201,33 @@ __device__ __forceinline__ uint32_t max_dpp16(uint32_t v) {
   v = max_dpp8(v);
   return umax(v, dpp_mov<kDppMirror>(v));
 }
-__device__ __forceinline__ float wave_sum(float v) {
+// sums over 16, 32 or 64 lanes
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
   v = add_dpp16(v);
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  if constexpr (LANES >= 32) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if constexpr (LANES == 64) {
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
+}
+
+// sums over the lanes at the same place of a wave's SHARES parts
+template <int SHARES>
+__device__ __forceinline__ float shares_sum(float v) {
+  if constexpr (SHARES == 4) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if constexpr (SHARES >= 2) {
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
 }
 
 // ---------------------------------------------------------------------------

@@ -1,7 +1,7 @@
 """svdq_layer_norm_forward and _backward against float64 (MI355X only).
 
 Tolerances. u = 2^-24 is half a step of an fp32 operation. A sum over a row
-takes at most D = 48 additions in a chain (32 in a lane, 6 over the wave, 8
+takes at most D = 48 additions in a chain (16 in a lane, 6 over the wave, 16
 waves, 2 for the scaling), so a mean of values v is off by D u mean|v|. The
 bounds below add each operation's half step to first order; the last rounding
 adds half a step of the output type."""
@@ -65,7 +65,7 @@ def _check_backward(dy, x, mean, rstd, w, one_plus, rpg, groups, dx, dw, db, wha
     for i in range(groups):
         rows = g == i
         n = int(rows.sum())
-        # a run of rows is one chain, then the runs (at most 512, sixteen chains of them)
+        # a lane's rows (a run's, shared by its teams), the teams (16, and 2 in a wave), the runs (8, then 32)
         runs = max(1, min(512 // max(1, -(-x.shape[0] // rpg)), -(-min(rpg, x.shape[0]) // 8)))
         chain = -(-n // runs) + 2 + 32 + 16 + 6
         for got, terms, name in ((dw, dyd * xhat, "dweight"), (db, dyd, "dbias")):
@@ -225,3 +225,20 @@ def test_norm_on_another_stream_and_in_a_graph():
         y, mean, rstd = S.layer_norm_forward(x, w, b, rows_per_group=300)
         e = S.layer_norm_backward(dy, x, mean, rstd, w, rows_per_group=300)
         assert torch.equal(y, yg) and all(torch.equal(a, c) for a, c in zip(e, gg)), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,C,rpg", [(513, 250, 100), (300, 129, 7), (1000, 64, 333), (77, 16, 1), (50, 3, 20), (9, 2, 1 << 40),
+                                     (2051, 65, 1000), (20, 5000, 9), (12, 12288, 12), (5, 15001, 3), (260, 6000, 130),
+                                     (40, 9000, 40), (64, 1537, 64)])
+def test_norm_teams(M, C, rpg, dtype):
+    """Rows that share a wave (also of different groups), rows shorter than a
+    vector, rows of a wave and of many."""
+    groups = (M - 1) // rpg + 1
+    x, w, b, dy = _inputs(M, C, TYPES[dtype], torch.float32, groups, M + C, True)
+    y, mean, rstd = S.layer_norm_forward(x, w, b, one_plus=True, rows_per_group=rpg)
+    _check_forward(x, w, b, 1e-6, True, rpg, y, mean, rstd, (M, C, rpg))
+    dx, dw, db = S.layer_norm_backward(dy, x, mean, rstd, w, one_plus=True, rows_per_group=rpg)
+    _check_backward(dy, x, mean, rstd, w, True, rpg, groups, dx, dw, db, (M, C, rpg))
+    again = S.layer_norm_backward(dy, x, mean, rstd, w, one_plus=True, rows_per_group=rpg)
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
