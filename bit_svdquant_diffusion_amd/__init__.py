@@ -9,6 +9,7 @@ raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -709,43 +710,71 @@ def _call(name: str, at: int, stream, *args):
 
 
 def _rows(t, what: str):
-    """(pointer, row stride) of a matrix whose rows are contiguous."""
+    """(pointer, row stride) of a matrix whose rows are contiguous and apart."""
     shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{what}: a matrix with contiguous rows")
-    ld, step = t.stride()
-    cols = shape[1]
-    if step != 1 and cols > 1:
-        raise ValueError(f"{what}: a matrix with contiguous rows")
-    return t.data_ptr(), ld if ld > cols else cols
+    if len(shape) == 2:
+        cols = shape[1]
+        if t.is_contiguous():
+            return t.data_ptr(), cols
+        ld, step = t.stride()
+        if (step == 1 or cols <= 1) and (ld >= cols or shape[0] <= 1):
+            return t.data_ptr(), max(ld, cols)
+    raise ValueError(f"{what}: a matrix with contiguous rows")
 
 
 def _param(t, C, groups, dtype, what):
     """(pointer, group stride) of a [C] or [groups][C] parameter."""
     shape = t.shape
-    if t.dtype != dtype or shape[-1] != C or len(shape) > 2 or (len(shape) == 2 and shape[0] or 1) != groups \
-            or (C > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{what}: [channels] or [groups][channels], contiguous channels, both of one type")
-    return t.data_ptr(), max(t.stride(0), C) if len(shape) == 2 else C
+    if t.dtype == dtype and shape[-1] == C:
+        if len(shape) == 1:
+            if groups == 1 and (C == 1 or t.stride(0) == 1):
+                return t.data_ptr(), C
+        elif len(shape) == 2 and shape[0] == groups:
+            ld, step = t.stride()
+            if (step == 1 or C == 1) and (ld >= C or groups == 1):
+                return t.data_ptr(), max(ld, C)
+    raise ValueError(f"{what}: [channels] or [groups][channels], contiguous channels, both of one type")
 
 
-def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype):
-    """(NormDesc, weight pointer, stride, bias pointer, stride) of [C] or [groups][C] parameters."""
+@functools.lru_cache(maxsize=1024)
+def _norm_desc(C, dt, pdt, one_plus, groups, eps, rows_per_group):
+    """A reference to the descriptor (the library only reads it) and itself."""
+    d = NormDesc(C, dt, pdt, one_plus, groups, eps, rows_per_group)
+    return ctypes.byref(d), d
+
+
+def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, groups=None):
+    """(NormDesc reference, groups, weight pointer, stride, bias pointer,
+    stride) of [C] or [groups][C] parameters."""
     some = weight if weight is not None else bias
     wp = bp = None
     ldw = ldb = C
-    groups, pdt = 1, dtype
+    pdt = dtype
     if some is not None:
         pdt = some.dtype
-        if some.dim() == 2:
-            groups = some.shape[0]
+        groups = some.shape[0] if some.dim() == 2 else 1
         if weight is not None:
             wp, ldw = _param(weight, C, groups, pdt, "weight")
         if bias is not None:
             bp, ldb = _param(bias, C, groups, pdt, "bias")
+    elif groups is None:
+        groups = 1
     if rows_per_group is None:
-        rows_per_group = max(1, -(-M // groups))
-    return NormDesc(C, _dt(dtype), _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group), wp, ldw, bp, ldb
+        rows_per_group = max(1, -(-M // max(1, groups)))
+    return _norm_desc(C, _dt(dtype), _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group)[0], groups, wp, ldw, bp, ldb
+
+
+def _rows_like(x, shape, stream):
+    """An uninitialised matrix of x's type."""
+    if stream is None and x.is_contiguous():
+        return _t.empty_like(x)
+    return _empty(shape, x.dtype, x, stream)
+
+
+def _stats(M, x, stream):
+    """Uninitialised mean and rstd of M rows."""
+    mean = _empty((M,), _t.float32, x, stream)
+    return mean, _t.empty_like(mean) if stream is None else _empty((M,), _t.float32, x, stream)
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: bool = False, rows_per_group=None,
@@ -759,14 +788,14 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: b
     at = _on_device(x, weight, bias, y)
     xp, ldx = _rows(x, "x")
     M, C = x.shape
-    d, wp, ldw, bp, ldb = _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
+    d, _, wp, ldw, bp, ldb = _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
     if y is None:
-        y = _empty((M, C), x.dtype, x, stream)
+        y = _rows_like(x, (M, C), stream)
     elif y.dtype != x.dtype or y.shape != x.shape:
         raise ValueError("y: the shape and type of x")
-    mean, rstd = _empty((2, M), _t.float32, x, stream).unbind()
+    mean, rstd = _stats(M, x, stream)
     yp, ldy = _rows(y, "y")
-    _call("svdq_layer_norm_forward", at, stream, ctypes.byref(d), xp, ldx, wp, ldw, bp, ldb, M, yp, ldy, mean.data_ptr(),
+    _call("svdq_layer_norm_forward", at, stream, d, xp, ldx, wp, ldw, bp, ldb, M, yp, ldy, mean.data_ptr(),
           rstd.data_ptr())
     return y, mean, rstd
 
@@ -783,34 +812,32 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, 
     f32 = _torch().float32
     for t in (mean, rstd):
         _need(t.dtype == f32 and t.shape == (M,) and t.is_contiguous(), "mean, rstd: float32 [rows]")
-    d, wp, ldw, _, _ = _norm_params(C, weight, None, one_plus, 0.0, rows_per_group, M, x.dtype)
     flat = groups is None if weight is None else weight.dim() == 1
-    if weight is None and groups is not None:
-        d.groups = groups
-        d.rows_per_group = rows_per_group if rows_per_group is not None else max(1, -(-M // groups))
+    d, G, wp, ldw, _, _ = _norm_params(C, weight, None, one_plus, 0.0, rows_per_group, M, x.dtype, groups)
     gdt = grad_dtype if grad_dtype is not None else (weight.dtype if weight is not None else f32)
     if dx is None:
-        dx = _empty((M, C), x.dtype, x, stream)
+        dx = _rows_like(x, (M, C), stream)
     elif dx.dtype != x.dtype or dx.shape != x.shape:
         raise ValueError("dx: the shape and type of x")
     dw = db = wsp = ws = None
     size = 0
     if param_grads:
         need = ctypes.c_size_t()
-        _check(lib().svdq_layer_norm_backward_workspace_bytes(ctypes.byref(d), M, ctypes.byref(need)),
+        _check(lib().svdq_layer_norm_backward_workspace_bytes(d, M, ctypes.byref(need)),
                "svdq_layer_norm_backward_workspace_bytes")
         size = need.value
-        dw, db = _empty((2, C) if flat else (2, d.groups, C), gdt, x, stream).unbind()
+        dw, db = _empty((2, C) if flat else (2, G, C), gdt, x, stream).unbind()
         if size:
             ws = _empty((size,), _t.uint8, x, stream)
             wsp = ws.data_ptr()
     (dyp, lddy), (xp, ldx), (dxp, lddx) = _rows(dy, "dy"), _rows(x, "x"), _rows(dx, "dx")
-    _call("svdq_layer_norm_backward", at, stream, ctypes.byref(d), dyp, lddy, xp, ldx, wp, ldw, mean.data_ptr(),
+    _call("svdq_layer_norm_backward", at, stream, d, dyp, lddy, xp, ldx, wp, ldw, mean.data_ptr(),
           rstd.data_ptr(), M, dxp, lddx, None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
           _dt(gdt), wsp, size)
     return dx, dw, db
 
 
+@functools.lru_cache(maxsize=4096)
 def _fp8_bytes(name: str, K: int, N: int, M: int) -> int:
     out = ctypes.c_size_t()
     _check(getattr(lib(), name)(ctypes.byref(Fp8Desc(K, N)), M, ctypes.byref(out)), name)
@@ -913,7 +940,7 @@ def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: 
     at = _on_device(x, weight, bias, y, workspace, *dev.values())
     _bf16_rows(x, K, "x")
     M = x.shape[0]
-    d, wp, ldw, bp, ldb = _norm_params(K, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
+    d, _, wp, ldw, bp, ldb = _norm_params(K, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
     if y is None:
         y = _empty((M, N), _t.bfloat16, x, stream)
     else:
@@ -922,8 +949,8 @@ def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: 
     ws, wsp, size = _scratch(workspace, fp8_norm_workspace_bytes(K, N, M), x, stream)
     mean = rstd = None
     if stats:
-        mean, rstd = _empty((2, M), _t.float32, x, stream).unbind()
-    _call("svdq_fp8_norm_forward", at, stream, ctypes.byref(d), wp, ldw, bp, ldb, ctypes.byref(Fp8Desc(K, N)),
+        mean, rstd = _stats(M, x, stream)
+    _call("svdq_fp8_norm_forward", at, stream, d, wp, ldw, bp, ldb, ctypes.byref(Fp8Desc(K, N)),
           ctypes.byref(_fp8_struct(K, N, dev)), x.data_ptr(), M, y.data_ptr(), _ptr(mean), _ptr(rstd), wsp, size)
     return (y, mean, rstd) if stats else y
 

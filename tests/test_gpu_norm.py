@@ -242,3 +242,27 @@ def test_norm_teams(M, C, rpg, dtype):
     _check_backward(dy, x, mean, rstd, w, True, rpg, groups, dx, dw, db, (M, C, rpg))
     again = S.layer_norm_backward(dy, x, mean, rstd, w, one_plus=True, rows_per_group=rpg)
     assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
+
+
+def test_norm_refuses_overlapping_rows():
+    """Expanded tensors (rows or groups a stride of 0 apart) and rows closer
+    than their length are errors, not other memory."""
+    x, w, b, dy = _inputs(6, 40, torch.bfloat16, torch.bfloat16, 2, 1)
+    y, mean, rstd = S.layer_norm_forward(x, w, b)
+    one = x[:1].expand(6, 40)
+    with pytest.raises(ValueError):
+        S.layer_norm_forward(one)
+    with pytest.raises(ValueError):
+        S.layer_norm_forward(x, y=one)
+    with pytest.raises(ValueError):
+        S.layer_norm_forward(x, w[:1].expand(2, 40))
+    with pytest.raises(ValueError):
+        S.layer_norm_forward(x, w, b[:1].expand(2, 40))
+    with pytest.raises(ValueError):
+        S.layer_norm_forward(x.reshape(-1).as_strided((6, 40), (39, 1)))
+    with pytest.raises(ValueError):
+        S.layer_norm_forward(x.t())
+    with pytest.raises(ValueError):
+        S.layer_norm_backward(one, x, mean, rstd, w)
+    with pytest.raises(ValueError):
+        S.layer_norm_backward(dy, x, mean[:1].expand(6), rstd, w)
