@@ -644,26 +644,31 @@ class SVDQLinear:
 _t = None         # torch, imported on first use
 _DT_CODES = {}    # svdq_dtype of the torch dtypes
 _raw_stream = None   # the current stream's handle on a GPU
+_current_device = None
 
 
 def _torch():
-    global _t, _raw_stream
+    global _t, _raw_stream, _current_device
     if _t is None:
         import torch
         _DT_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
         # (without a Stream object where this torch has the call)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda at: torch.cuda.current_stream(at).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _t = torch
     return _t
 
 
 def _dt(dtype) -> int:
     """svdq_dtype of a torch dtype."""
-    _torch()
-    if dtype not in _DT_CODES:
-        raise ValueError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
-    return _DT_CODES[dtype]
+    code = _DT_CODES.get(dtype)
+    if code is None:
+        _torch()
+        if dtype not in _DT_CODES:
+            raise ValueError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
+        code = _DT_CODES[dtype]
+    return code
 
 
 def _need(ok, what: str):
@@ -687,7 +692,7 @@ def _empty(shape, dtype, like, stream):
     allocator does not hand its memory to other work while the call runs."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
@@ -697,13 +702,12 @@ def _empty(shape, dtype, like, stream):
 def _call(name: str, at: int, stream, *args):
     """The library's function on GPU `at` and the given stream (by default the
     GPU's current one)."""
-    torch = _torch()
     f = getattr(lib(), name)
     s = _raw_stream(at) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == at:
+    if _current_device() == at:
         st = f(*args, s)
     else:
-        with torch.cuda.device(at):
+        with _t.cuda.device(at):
             st = f(*args, s)
     if st != 0:
         raise SvdqError(st, name)
@@ -725,11 +729,13 @@ def _rows(t, what: str):
 def _param(t, C, groups, dtype, what):
     """(pointer, group stride) of a [C] or [groups][C] parameter."""
     shape = t.shape
-    if t.dtype == dtype and shape[-1] == C:
+    if t.dtype is dtype:
         if len(shape) == 1:
-            if groups == 1 and (C == 1 or t.stride(0) == 1):
+            if groups == 1 and shape[0] == C and t.is_contiguous():
                 return t.data_ptr(), C
-        elif len(shape) == 2 and shape[0] == groups:
+        elif len(shape) == 2 and shape[0] == groups and shape[1] == C:
+            if t.is_contiguous():
+                return t.data_ptr(), C
             ld, step = t.stride()
             if (step == 1 or C == 1) and (ld >= C or groups == 1):
                 return t.data_ptr(), max(ld, C)
@@ -752,7 +758,8 @@ def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, group
     pdt = dtype
     if some is not None:
         pdt = some.dtype
-        groups = some.shape[0] if some.dim() == 2 else 1
+        shape = some.shape
+        groups = shape[0] if len(shape) == 2 else 1
         if weight is not None:
             wp, ldw = _param(weight, C, groups, pdt, "weight")
         if bias is not None:
@@ -761,7 +768,9 @@ def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, group
         groups = 1
     if rows_per_group is None:
         rows_per_group = max(1, -(-M // max(1, groups)))
-    return _norm_desc(C, _dt(dtype), _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group)[0], groups, wp, ldw, bp, ldb
+    dt = _dt(dtype)
+    return (_norm_desc(C, dt, dt if pdt is dtype else _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group)[0], groups,
+            wp, ldw, bp, ldb)
 
 
 def _rows_like(x, shape, stream):
@@ -773,8 +782,10 @@ def _rows_like(x, shape, stream):
 
 def _stats(M, x, stream):
     """Uninitialised mean and rstd of M rows."""
-    mean = _empty((M,), _t.float32, x, stream)
-    return mean, _t.empty_like(mean) if stream is None else _empty((M,), _t.float32, x, stream)
+    if stream is None:
+        mean = x.new_empty((M,), dtype=_t.float32)
+        return mean, _t.empty_like(mean)
+    return _empty((M,), _t.float32, x, stream), _empty((M,), _t.float32, x, stream)
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: bool = False, rows_per_group=None,
