@@ -76,6 +76,26 @@ __device__ __forceinline__ void spread_second() {
   if constexpr (Q + 1 < TL::kMfma) spread_second<TL, Q + 1>();
 }
 
+// The bf16 pairs of a lane's 16 channels 8 q + 4 h + (0..3) of row lr of a
+// 32 x 32 block, o[2 q], o[2 q + 1], exchanged so that o[0..3] are channels
+// 8 h + 16 (lr / 16) + (0..7) of row lr % 16 and o[4..7] of row lr % 16 + 16
+__device__ __forceinline__ void spread_rows(uint32_t (&o)[8]) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {   // to channels 16 p + 8 h + (0..7) of row lr
+      const auto r = __builtin_amdgcn_permlane32_swap(o[4 * p + w], o[4 * p + 2 + w], false, false);
+      o[4 * p + w] = r[0];
+      o[4 * p + 2 + w] = r[1];
+    }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const auto r = __builtin_amdgcn_permlane16_swap(o[w], o[4 + w], false, false);
+    o[w] = r[0];
+    o[4 + w] = r[1];
+  }
+}
+
 // wait until at most N vector-memory operations are outstanding and all LDS
 // reads have returned, then the workgroup's barrier; nothing moves across
 template <int N>
@@ -248,6 +268,13 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   i32x8 xa[TM], xb[TN], ya[TM], yb[TN];
   uint32_t ra_unit = 0, rb_unit = TL::kUnit;   // the units of the stage being read
   int t_cur = (int)blockIdx.x;
+  // Where some workgroups have one tile fewer they start about a third of a
+  // tile later (a stage takes 1.6 us): then not all tiles' outputs go to
+  // memory at the same time, whose 33 MB take longer than a stage (3.4 rounds
+  // at 4608 x 12288 outputs over 3072 channels 170 us against 175, without
+  // any stores 148).
+  if (ntiles > grid && ntiles % grid != 0 && t_cur >= ntiles % grid)
+    for (int i = 0; i < KB / 2; ++i) __builtin_amdgcn_s_sleep(32);   // 2048 cycles
   TileMap tm = map_tile(t_cur, tiles_m, tiles_n, group_m);
   int m0 = __builtin_amdgcn_readfirstlane(tm.tm) * BM, n0 = __builtin_amdgcn_readfirstlane(tm.tn) * BN;
   fa_res = SVDQ_RSRC_A(m0);
@@ -308,10 +335,15 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
     SVDQ_SCALES(0)
     SVDQ_MFMA(ya, yb)
 
-    // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3).
+    // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3);
+    // spread_rows leaves it channels at_c .. at_c + 7 of tokens lr % 16 and
+    // lr % 16 + 16, so that a store fills 64 contiguous bytes of sixteen rows
+    // (32 bytes of 32 rows take the L2 twice the requests: 13 us more of 172
+    // at 4608 x 12288 outputs, whose tiles are stored all at once).
     // Every store is issued by every wave, as the ring's waits count them: the
     // resource drops rows past the operand, and channels past it are sent past
     // its end.
+    const int at_c = 8 * h + (lr & 16);
     const int nrec = min(BM, Ra - m0) * Rb * 2;
     const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(g.out + (size_t)m0 * Rb, 0, nrec, kRsrcWord3);
 #pragma unroll
@@ -332,19 +364,10 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
         uint32_t o[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p) o[p] = cvt_bf16x2(acc[j][i][2 * p] + bv[2 * p], acc[j][i][2 * p + 1] + bv[2 * p + 1]);
-        // (o[4p], o[4p+1]) is q = 2p, (o[4p+2], o[4p+3]) is q = 2p + 1: after
-        // the swap lane half h holds channels 8 h + (0..7) and 16 + 8 h + (0..7)
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const auto r = __builtin_amdgcn_permlane32_swap(o[4 * p + w], o[4 * p + 2 + w], false, false);
-            o[4 * p + w] = r[0];
-            o[4 * p + 2 + w] = r[1];
-          }
-        const int off = ((wm * TL::WM + 32 * i + lr) * Rb + col + 8 * h) * 2;
-        store_16(out, u32x4{o[0], o[1], o[2], o[3]}, col < Rb ? off : nrec);
-        store_16(out, u32x4{o[4], o[5], o[6], o[7]}, col + 16 < Rb ? off + 32 : nrec);
+        spread_rows(o);
+        const int off = ((wm * TL::WM + 32 * i + (lr & 15)) * Rb + col + at_c) * 2;
+        store_16(out, u32x4{o[0], o[1], o[2], o[3]}, col + at_c < Rb ? off : nrec);
+        store_16(out, u32x4{o[4], o[5], o[6], o[7]}, col + at_c < Rb ? off + 32 * Rb : nrec);
       }
     }
     if (!more) break;
@@ -595,22 +618,43 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
   __builtin_amdgcn_s_waitcnt(0);   // the transfers past the end land before the LDS is given up
 
   // a lane holds token row0 + lr and channels col0 + 8 q + 4 h + (0..3)
-  const int row = row0 + lr, col = col0 + 4 * h;
-  if (row >= Ra) return;
+  if (g.part) {
+    // fp32: of each pair of q, 64 contiguous bytes of sixteen rows a store
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      f32x4 v[2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[8 * p + e]), __float_as_uint(acc[8 * p + 4 + e]), false, false);
+        v[0][e] = __uint_as_float(r[0]);
+        v[1][e] = __uint_as_float(r[1]);
+      }
+      const int c = col0 + 16 * p + 4 * h + (lr & 16) / 2;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = row0 + (lr & 15) + 16 * u;
+        if (row < Ra && c < Rb) *reinterpret_cast<f32x4*>(g.part + ((size_t)run * Ra + row) * Rb + c) = v[u];
+      }
+    }
+    return;
+  }
+  uint32_t o[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (col + 8 * q >= Rb) continue;
     f32x4 v = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-    if (g.part) {
-      *reinterpret_cast<f32x4*>(g.part + ((size_t)run * Ra + row) * Rb + col + 8 * q) = v;
-    } else {
-      if (g.bias) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(g.bias + col + 8 * q);
-        v += f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
-      }
-      *reinterpret_cast<u32x2*>(g.out + (size_t)row * Rb + col + 8 * q) = u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+    if (g.bias) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(g.bias + min(col0 + 8 * q + 4 * h, Rb - 4));
+      v += f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
     }
+    o[2 * q] = cvt_bf16x2(v[0], v[1]);
+    o[2 * q + 1] = cvt_bf16x2(v[2], v[3]);
   }
+  spread_rows(o);
+  const int row = row0 + (lr & 15), c = col0 + 8 * h + (lr & 16);
+  if (c >= Rb) return;
+  uint16_t* p = g.out + (size_t)row * Rb + c;
+  if (row < Ra) *reinterpret_cast<u32x4*>(p) = u32x4{o[0], o[1], o[2], o[3]};
+  if (row + 16 < Ra) *reinterpret_cast<u32x4*>(p + (size_t)16 * Rb) = u32x4{o[4], o[5], o[6], o[7]};
 }
 
 // the runs' sums, in order, and the bias: four channels a thread
