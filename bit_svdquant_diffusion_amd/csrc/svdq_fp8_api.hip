@@ -220,10 +220,11 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
     return after_launch(launch_fp8_gemm_small(g, cus, s), s);
   }
   uint8_t* b = (uint8_t*)ws;
-  SVDQ_TRY(after_launch(launch_fp8_quant_rows(x, M, d->K, b + L.q, b + L.s, false, s), s));
+  SVDQ_TRY(after_launch(launch_fp8_quant_rows(x, M, d->K, b + L.q, b + L.s, false, (uint32_t*)(b + L.tickets), s), s));
   g.a = b + L.q;
   g.as = b + L.s;
   g.part = (float*)(b + L.part);
+  g.tickets = (uint32_t*)(b + L.tickets);
   return after_launch(launch_fp8_gemm(g, cus, s), s);
 }
 
@@ -261,11 +262,13 @@ svdq_status svdq_fp8_norm_forward(const svdq_norm_desc* n, const void* weight, i
   a.qs = b + L.s;
   a.Kp = (int)round128(d->K);
   a.qs_rows = M;
+  a.tickets = (uint32_t*)(b + L.tickets);
   SVDQ_TRY(after_launch(launch_norm(a, cus, s), s));
   Fp8Gemm g = forward_gemm(d, dev, M, y);
   g.a = b + L.q;
   g.as = b + L.s;
   g.part = (float*)(b + L.part);
+  g.tickets = (uint32_t*)(b + L.tickets);
   // (the same kernel as svdq_fp8_forward, so the same sums)
   return after_launch(fp8_inline(M, d->K) ? launch_fp8_gemm_small(g, cus, s) : launch_fp8_gemm(g, cus, s), s);
 }
@@ -318,7 +321,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     qx.qt = b + L.xt;
     qx.st = b + L.xts;
   }
-  SVDQ_TRY(after_launch(launch_fp8_quant_t(qy, qx, M, s), s));
+  SVDQ_TRY(after_launch(launch_fp8_quant_t(qy, qx, M, (uint32_t*)(b + L.tickets), s), s));
   if (db) SVDQ_TRY(after_launch(launch_fp8_bias_grad(qy.sums, round128(M) / 128, d->N, db, s), s));
   if (dx) {
     Fp8Gemm g;
@@ -334,6 +337,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     g.K = d->N;
     g.out = dx;
     g.part = (float*)(b + L.part);
+    g.tickets = (uint32_t*)(b + L.tickets);
     SVDQ_TRY(after_launch(launch_fp8_gemm(g, cus, s), s));
   }
   if (dw) {
@@ -351,6 +355,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     g.K = round128(M);
     g.out = dw;
     g.part = (float*)(b + L.part);
+    g.tickets = (uint32_t*)(b + L.tickets) + kFp8Tickets;
     SVDQ_TRY(after_launch(launch_fp8_gemm(g, cus, s), s));
   }
   return SVDQ_OK;
@@ -364,7 +369,7 @@ svdq_status svdq_fp8_quantize(const uint16_t* x, int64_t M, int32_t K, uint8_t* 
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return SVDQ_ERR_SHAPE;
   SVDQ_TRY(check_device());
   hipStream_t s = (hipStream_t)stream;
-  return after_launch(launch_fp8_quant_rows(x, M, K, codes, scales, true, s), s);
+  return after_launch(launch_fp8_quant_rows(x, M, K, codes, scales, true, nullptr, s), s);
 }
 
 }  // extern "C"

@@ -502,7 +502,8 @@ __global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
 
 // Few tiles (fp8_deep): 64 x 64 outputs a workgroup, and where those do not
 // fill the CUs a tile's contracted blocks in several runs (`chunk` blocks, a
-// multiple of four), whose fp32 sums fp8_join_kernel adds in order. There is
+// multiple of four), whose fp32 sums the workgroup that comes last to the
+// tile's ticket adds in order. There is
 // little work a CU, so a stage's time is the wait for its transfers: LDS is a
 // ring of D whole stages with all but one in flight. Per stage: the wait for
 // the next one, the barrier, the transfers into the slot of the stage whose
@@ -517,8 +518,9 @@ __global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
 // outputs: 20.5 us, 20.7 and 22; 2064, 1003 and 1552: 16.2, 15.8 and 18.1).
 constexpr int kDeepStage = 2 * 64 * 128, kDeepOps = 4;   // bytes of a stage; transfers per wave and stage
 template <int D, bool BROW>
-__global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int chunk) {
+__global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int chunk, int runs) {
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int ticket_last;
   static_assert(D - 2 <= 4, "scale words are four stages ahead of their use, the transfers no more");
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -617,27 +619,39 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
   }
   __builtin_amdgcn_s_waitcnt(0);   // the transfers past the end land before the LDS is given up
 
-  // a lane holds token row0 + lr and channels col0 + 8 q + 4 h + (0..3)
-  if (g.part) {
-    // fp32: of each pair of q, 64 contiguous bytes of sixteen rows a store
+  if (runs > 1) {
+    // The sums go through the device's coherence point and not the XCD's L2
+    // (relaxed atomics of agent scope, of 8 bytes), so that no cache has to be
+    // written back or invalidated: with plain stores and an agent-scope
+    // release and acquire the call took 26.6 us for 64 tokens, 12288 -> 3072,
+    // with a second kernel that adds the runs 19.8, this way 19.9 and a launch
+    // (2.8 us of host time) less.
+    const int tile = t % (tiles_m * tiles_n);
+    auto part = [&](int r, int q) {
+      return reinterpret_cast<uint64_t*>(g.part) + ((size_t)((tile * runs + r) * 4 + wave) * 8 + q) * 64 + lane;
+    };
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      f32x4 v[2];
+    for (int q = 0; q < 8; ++q)
+      __hip_atomic_store(part(run, q), (uint64_t)__float_as_uint(acc[2 * q + 1]) << 32 | __float_as_uint(acc[2 * q]),
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0);   // every wave's sums have landed ...
+    __syncthreads();                  // ... before the ticket is taken
+    if (tid == 0)
+      ticket_last = __hip_atomic_fetch_add(g.tickets + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)runs;
+    __syncthreads();
+    if (!ticket_last) return;
+    acc = f32x16{};
+#pragma unroll 4
+    for (int r = 0; r < runs; ++r) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[8 * p + e]), __float_as_uint(acc[8 * p + 4 + e]), false, false);
-        v[0][e] = __uint_as_float(r[0]);
-        v[1][e] = __uint_as_float(r[1]);
-      }
-      const int c = col0 + 16 * p + 4 * h + (lr & 16) / 2;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int row = row0 + (lr & 15) + 16 * u;
-        if (row < Ra && c < Rb) *reinterpret_cast<f32x4*>(g.part + ((size_t)run * Ra + row) * Rb + c) = v[u];
+      for (int q = 0; q < 8; ++q) {
+        const uint64_t v = __hip_atomic_load(part(r, q), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        acc[2 * q] += __uint_as_float((uint32_t)v);
+        acc[2 * q + 1] += __uint_as_float((uint32_t)(v >> 32));
       }
     }
-    return;
   }
+  // a lane holds token row0 + lr and channels col0 + 8 q + 4 h + (0..3)
   uint32_t o[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -655,26 +669,6 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
   uint16_t* p = g.out + (size_t)row * Rb + c;
   if (row < Ra) *reinterpret_cast<u32x4*>(p) = u32x4{o[0], o[1], o[2], o[3]};
   if (row + 16 < Ra) *reinterpret_cast<u32x4*>(p + (size_t)16 * Rb) = u32x4{o[4], o[5], o[6], o[7]};
-}
-
-// the runs' sums, in order, and the bias: four channels a thread
-__global__ __launch_bounds__(256) void fp8_join_kernel(const float* part, int runs, int64_t quads, int N, const uint16_t* bias,
-                                                       uint16_t* out) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= quads) return;
-  const f32x4* p = reinterpret_cast<const f32x4*>(part) + at;
-  f32x4 v = p[0];
-  int r = 1;
-  for (; r + 4 <= runs; r += 4) {
-    const f32x4 a = p[(r)*quads], b = p[(r + 1) * quads], c = p[(r + 2) * quads], d = p[(r + 3) * quads];
-    v = (((v + a) + b) + c) + d;
-  }
-  for (; r < runs; ++r) v += p[r * quads];
-  if (bias) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(bias + at % (N / 4) * 4);
-    v += f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
-  }
-  *reinterpret_cast<u32x2*>(out + 4 * at) = u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
 }
 
 typedef Tile<256, 256, 2, 2> TileL;
@@ -731,19 +725,13 @@ hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st) 
 
 namespace {
 template <bool BROW>
-hipError_t launch_deep(Fp8Gemm g, const Fp8Deep& p, hipStream_t st) {
-  if (p.runs == 1) g.part = nullptr;
+hipError_t launch_deep(const Fp8Gemm& g, const Fp8Deep& p, hipStream_t st) {
   const int tm = (int)((g.a_rows + 63) / 64), tn = (g.b_rows + 63) / 64;
   const unsigned grid = (unsigned)(tm * tn * p.runs);
   if (grid <= kFp8Cus)
-    hipLaunchKernelGGL((fp8_deep_kernel<5, BROW>), dim3(grid), dim3(256), 5 * kDeepStage, st, g, tm, tn, p.chunk);
+    hipLaunchKernelGGL((fp8_deep_kernel<5, BROW>), dim3(grid), dim3(256), 5 * kDeepStage, st, g, tm, tn, p.chunk, p.runs);
   else
-    hipLaunchKernelGGL((fp8_deep_kernel<3, BROW>), dim3(grid), dim3(256), 3 * kDeepStage, st, g, tm, tn, p.chunk);
-  if (p.runs > 1) {
-    const int64_t quads = g.a_rows * g.b_rows / 4;
-    hipLaunchKernelGGL(fp8_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, g.part, p.runs, quads, g.b_rows,
-                       g.bias, g.out);
-  }
+    hipLaunchKernelGGL((fp8_deep_kernel<3, BROW>), dim3(grid), dim3(256), 3 * kDeepStage, st, g, tm, tn, p.chunk, p.runs);
   return hipGetLastError();
 }
 }  // namespace

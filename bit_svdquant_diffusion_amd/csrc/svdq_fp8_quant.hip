@@ -23,7 +23,8 @@ namespace {
 // all loads first. `plain` scales: [blocks / 4][M][4]. Channels in [K, Kp) get zero codes (K % 16 == 0: whole lanes).
 constexpr int kUnits = 2;
 __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, uint32_t units, uint32_t chunks, int64_t M, int K,
-                                                             int Kp, int plain, uint8_t* q, uint8_t* s) {
+                                                             int Kp, int plain, uint8_t* q, uint8_t* s, uint32_t* tickets) {
+  if (tickets && blockIdx.x == 0 && threadIdx.x < kFp8Tickets) tickets[threadIdx.x] = 0;
   const int lane = threadIdx.x & 63;
   const uint32_t u0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kUnits;
   u32x4 v[kUnits][2];
@@ -75,7 +76,8 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, 
 // from the caches); 777 of 1552 and 2064 9.8 us, of which 4.5 go when the two
 // kinds of codes are not stored and 3.2 are the launch and the loads.
 constexpr int kTLd = 33;   // words of a transposed row in LDS (32 and one against bank conflicts)
-__global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a) {
+__global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a, uint32_t* tickets) {
+  if (blockIdx.x == 0 && threadIdx.x < 2 * kFp8Tickets) tickets[threadIdx.x] = 0;
   __shared__ uint32_t lds[2 * 32 * 128];   // maxima and sums [32][128] each, then codes [128][kTLd]
   __shared__ uint32_t red[2][4][128];
   __shared__ float col_scale[128];
@@ -263,19 +265,20 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const T* w, int K, int N,
 
 }  // namespace
 
-hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, bool plain, hipStream_t st) {
+hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, bool plain, uint32_t* tickets,
+                                 hipStream_t st) {
   const int Kp = (int)round128(K), chunks = (Kp + 1023) / 1024;
   const int64_t units = M * chunks;
   const int64_t grid = (units + 4 * kUnits - 1) / (4 * kUnits);
-  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, q, s);
+  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, q, s, tickets);
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M, hipStream_t st) {
+hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M, uint32_t* tickets, hipStream_t st) {
   const int64_t rows = (M + 127) / 128;
   const int64_t na = a.x ? rows * ((a.C + 127) / 128) : 0, nb = b.x ? rows * ((b.C + 127) / 128) : 0;
   if (na + nb == 0) return hipSuccess;
-  hipLaunchKernelGGL(fp8_quant_t_kernel, dim3((unsigned)(na + nb)), dim3(512), 0, st, a, b, M, na);
+  hipLaunchKernelGGL(fp8_quant_t_kernel, dim3((unsigned)(na + nb)), dim3(512), 0, st, a, b, M, na, tickets);
   return hipGetLastError();
 }
 

@@ -119,6 +119,7 @@ struct NormArgs {
   uint8_t* qs;
   int Kp;
   int64_t qs_rows;
+  uint32_t* tickets;   // kFp8Tickets words to zero for the product, may be null
 };
 struct NormGradPlan;
 struct NormGradArgs {
@@ -131,6 +132,7 @@ struct NormGradArgs {
   void* db;
   int gdtype;
   float* part;       // [G][runs][2][C], null when a group is one run
+  int once;          // set by launch_norm_grad: x and dy are read past the caches
 };
 hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st);
 hipError_t prepare_norm();
@@ -138,7 +140,9 @@ hipError_t launch_norm_grad(const NormGradArgs& g, const NormGradPlan& p, hipStr
 
 // E4M3 quantizers (svdq_fp8_quant.hip)
 // (plain: the scale bytes as svdq_fp8_quantize documents them, not the product's order)
-hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, bool plain, hipStream_t st);
+// `tickets`, where given: kFp8Tickets words that the kernel zeroes for the product behind it
+hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q, uint8_t* s, bool plain, uint32_t* tickets,
+                                 hipStream_t st);
 // one or two matrices bf16 [M][C] quantized along M (codes [C][round128(M)]);
 // the first also along C (row codes) and summed over M where asked
 struct Fp8QuantT {
@@ -150,7 +154,7 @@ struct Fp8QuantT {
   uint8_t* s;
   float* sums;       // [round128(M)/128][C], or null
 };
-hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M, hipStream_t st);
+hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M, uint32_t* tickets, hipStream_t st);   // 2 kFp8Tickets
 hipError_t launch_fp8_bias_grad(const float* sums, int64_t blocks, int N, uint16_t* db, hipStream_t st);
 hipError_t launch_fp8_zero(void* p, size_t bytes, int num_cus, hipStream_t st);   // bytes % 4 == 0
 hipError_t launch_fp8_pack(const void* w, int dtype, int K, int N, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st,
@@ -171,7 +175,8 @@ struct Fp8Gemm {
   int64_t K;           // contracted channels
   const uint16_t* bias;
   uint16_t* out;       // bf16 [a_rows][b_rows]
-  float* part;         // fp32 [fp8_deep's runs][a_rows][b_rows], where there are more than one
+  float* part;         // where fp8_deep has several runs: their sums, and a zeroed ticket per tile
+  uint32_t* tickets;
   const uint16_t* x;   // launch_fp8_gemm_small: A as bf16 rows [a_rows][K], or null
 };
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st);

@@ -206,47 +206,49 @@ inline bool fp8_inline(int64_t M, int64_t K) { return M <= 16 && M * round128(K)
 // the plan is this card's): up to 448 tiles it is (400 tiles of 2064 channels
 // 16.2 us against 16.5, 384 of 3072 16.4 against 19.1, 512 of 1024 12.6
 // against 12.2, 768 of 3072 25.8 against 23.4); runs fill the CUs where each
-// is then at least twelve blocks shorter than the whole, which pays for the
-// launch that joins them (96 tiles of 24 blocks: 12.3 us with one run or two).
-constexpr int kFp8Cus = 256;
+// is then at least twelve blocks shorter than the whole, which pays for
+// joining them (96 tiles of 24 blocks: 12.3 us with one run or two), up to
+// sixteen, which their last workgroup adds.
+constexpr int kFp8Cus = 256, kFp8Tickets = kFp8Cus / 2;
 struct Fp8Deep {
   int runs, chunk;
 };
 inline Fp8Deep fp8_deep(int64_t rows, int64_t cols, int64_t K) {
   const int64_t tiles = ((rows + 63) / 64) * ((cols + 63) / 64), KB = (K + 127) / 128;
   if (tiles == 0 || KB == 0 || tiles > 448) return Fp8Deep{0, 0};
-  const int64_t want = kFp8Cus / tiles;
+  const int64_t want = kFp8Cus / tiles < 16 ? kFp8Cus / tiles : 16;
   if (want > 1) {
     const int64_t chunk = ((KB + want - 1) / want + 3) / 4 * 4;
     if (KB - chunk >= 12) return Fp8Deep{(int)((KB + chunk - 1) / chunk), (int)chunk};
   }
   return Fp8Deep{1, (int)((KB + 3) / 4 * 4)};
 }
-// bytes of its runs' sums
+// bytes of its runs' sums, whole tiles
 inline size_t fp8_deep_bytes(int64_t rows, int64_t cols, int64_t K) {
   const Fp8Deep p = fp8_deep(rows, cols, K);
-  return p.runs > 1 ? align256((size_t)p.runs * rows * cols * 4) : 0;
+  return p.runs > 1 ? (size_t)p.runs * ((rows + 63) / 64) * ((cols + 63) / 64) * 64 * 64 * 4 : 0;
 }
 
 // Workspace of the FP8 forward: the activations' codes [M][round128(K)],
-// their scales and the sums of runs.
+// their scales, the tickets of tiles and the sums of their runs.
 struct Fp8Ws {
-  size_t q, s, part, total;
+  size_t q, s, tickets, part, total;
 };
 inline Fp8Ws fp8_ws(const svdq_fp8_desc* d, int64_t M) {
   Fp8Ws w;
   w.q = 0;
   w.s = align256((size_t)M * round128(d->K));
-  w.part = w.s + align256(fp8_scale_bytes(M, d->K));
+  w.tickets = w.s + align256(fp8_scale_bytes(M, d->K));
+  w.part = w.tickets + kFp8Tickets * 4;
   w.total = w.part + fp8_deep_bytes(M, d->N, d->K);
   return w;
 }
 // Workspace of the backward: dY's codes along the output channels [M][round128(N)],
 // dY^T [N][round128(M)] and X^T [K][round128(M)] along the tokens, their
-// scales, dY's sums per 128 tokens fp32 [round128(M)/128][N], and the sums of
-// runs of one product after the other.
+// scales, dY's sums per 128 tokens fp32 [round128(M)/128][N], the tickets of
+// both products and the sums of runs of one after the other.
 struct Fp8GradWs {
-  size_t q, s, yt, yts, xt, xts, db, part, total;
+  size_t q, s, yt, yts, xt, xts, db, tickets, part, total;
 };
 inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   Fp8GradWs w;
@@ -258,7 +260,8 @@ inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   w.xt = w.yts + align256(fp8_scale_bytes(d->N, M));
   w.xts = w.xt + align256((size_t)d->K * mp);
   w.db = w.xts + align256(fp8_scale_bytes(d->K, M));
-  w.part = w.db + align256((size_t)(mp / 128) * d->N * 4);
+  w.tickets = w.db + align256((size_t)(mp / 128) * d->N * 4);
+  w.part = w.tickets + 2 * kFp8Tickets * 4;
   const size_t px = fp8_deep_bytes(M, d->K, d->N), pw = fp8_deep_bytes(d->N, d->K, mp);
   w.total = w.part + (px > pw ? px : pw);
   return w;

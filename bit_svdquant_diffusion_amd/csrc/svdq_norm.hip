@@ -94,6 +94,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(NormArgs a, in
   const int m_begin = team * per + min(team, extra), m_end = min(m_begin + per + (team < extra ? 1 : 0), last_row + 1);
   const int steps = per + (extra > 0 ? 1 : 0);   // of every team (a barrier is the workgroup's)
   const float fc = (float)C;
+  if constexpr (QUANT) {
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < kFp8Tickets; i += blockDim.x) a.tickets[i] = 0;
+  }
   const Place<NV, VEC> pl(tid, TH, C);
   Vec<T> next[NV];
   auto fetch = [&](int m) {
@@ -209,10 +213,19 @@ __global__ __launch_bounds__(64 * MAXW) void norm_bwd_kernel(NormGradArgs g, int
   float nmean = 0.f, nrstd = 0.f;
   auto fetch = [&](int m) {
     m = min(m, m_end - 1);   // past the end: the last row again, not used
+    const T *x = static_cast<const T*>(a.x) + m * a.ldx, *dy = static_cast<const T*>(g.dy) + m * g.lddy;
+    if (g.once) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      nx[j] = load_vec<T>(static_cast<const T*>(a.x) + m * a.ldx, pl.at(j), pl.len(j));
-      ndy[j] = load_vec<T>(static_cast<const T*>(g.dy) + m * g.lddy, pl.at(j), pl.len(j));
+      for (int j = 0; j < NV; ++j) {
+        nx[j] = load_vec<T, true>(x, pl.at(j), pl.len(j));
+        ndy[j] = load_vec<T, true>(dy, pl.at(j), pl.len(j));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        nx[j] = load_vec<T>(x, pl.at(j), pl.len(j));
+        ndy[j] = load_vec<T>(dy, pl.at(j), pl.len(j));
+      }
     }
     nmean = a.mean[m];
     nrstd = a.rstd[m];
@@ -436,7 +449,13 @@ hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st) {
   return launch_fwd<Half, false>(a, num_cus, st);
 }
 
-hipError_t launch_norm_grad(const NormGradArgs& g, const NormGradPlan& p, hipStream_t st) {
+hipError_t launch_norm_grad(const NormGradArgs& args, const NormGradPlan& p, hipStream_t st) {
+  // What the caches (256 MB) cannot keep until it is used again is read past
+  // them: from 128 MB of x, dy and dx on (9216 x 3072 bf16, 170 MB: 38.2 us
+  // against 42.7, 3000 x 9000 bf16, 162 MB: 45.0 against 51.7; 16387 x 517
+  // fp32, 102 MB: 25.2 against 23.0, inputs rotating through three sets).
+  NormGradArgs g = args;
+  g.once = (double)g.f.M * g.f.C * 3 * (g.f.dtype == SVDQ_DT_F32 ? 4 : 2) > 128e6;
   const hipError_t e = g.f.dtype == SVDQ_DT_F32    ? launch_bwd<float>(g, p, st)
                        : g.f.dtype == SVDQ_DT_BF16 ? launch_bwd<Bf16>(g, p, st)
                                                    : launch_bwd<Half>(g, p, st);

@@ -85,11 +85,18 @@ __device__ __forceinline__ Window<n> window(int c, int C) {
 }
 __device__ __forceinline__ float own_or_0(float v, uint32_t own) { return __uint_as_float(__float_as_uint(v) & own); }
 
-template <typename T>
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;   // at any element's address
+
+// ONCE: past the caches (non-temporal)
+template <typename T, bool ONCE = false>
 __device__ __forceinline__ Vec<T> load_vec(const T* row, int at, int len) {
   Vec<T> o;
   if (len == kVec<T>) {   // uniform
-    memcpy(&o.w, row + at, 16);
+    const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + at);
+    if constexpr (ONCE)
+      o.w = __builtin_nontemporal_load(p);
+    else
+      o.w = *p;
   } else {
     o.w = u32x4{0, 0, 0, 0};
 #pragma unroll

@@ -622,8 +622,7 @@ SVDQ_API svdq_status svdq_fp8_pack(const svdq_fp8_desc* desc, const void* w, int
  * y bf16 [M][N] = layer(x bf16 [M][K]) on hip_stream. A few tokens
  * (M <= 16 and M * K, K rounded up to 128, <= 49152) take one kernel, which
  * streams the weight and quantizes the tokens itself (no workspace is used);
- * more take one that quantizes x into the workspace, one that multiplies, and
- * where the outputs are few a third that joins the sums of runs of channels.
+ * more take one that quantizes x into the workspace and one that multiplies.
  * workspace: >= svdq_fp8_workspace_bytes(desc, M) device bytes (may be NULL
  * where that is 0), contents ignored on entry.
  * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_WORKSPACE, SVDQ_ERR_DEVICE.
