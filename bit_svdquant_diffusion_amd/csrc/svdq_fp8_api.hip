@@ -322,10 +322,11 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     qx.st = b + L.xts;
   }
   SVDQ_TRY(after_launch(launch_fp8_quant_t(qy, qx, M, (uint32_t*)(b + L.tickets), s), s));
-  if (db) SVDQ_TRY(after_launch(launch_fp8_bias_grad(qy.sums, round128(M) / 128, d->N, db, s), s));
+  Fp8Gemm gx, gw;
+  std::memset(&gx, 0, sizeof(gx));
+  std::memset(&gw, 0, sizeof(gw));
   if (dx) {
-    Fp8Gemm g;
-    std::memset(&g, 0, sizeof(g));
+    Fp8Gemm& g = gx;
     g.a = qy.q;
     g.as = qy.s;
     g.a_rows = M;
@@ -338,11 +339,9 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     g.out = dx;
     g.part = (float*)(b + L.part);
     g.tickets = (uint32_t*)(b + L.tickets);
-    SVDQ_TRY(after_launch(launch_fp8_gemm(g, cus, s), s));
   }
   if (dw) {
-    Fp8Gemm g;
-    std::memset(&g, 0, sizeof(g));
+    Fp8Gemm& g = gw;
     g.a = qy.qt;
     g.as = qy.st;
     g.a_rows = d->N;
@@ -356,8 +355,13 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     g.out = dw;
     g.part = (float*)(b + L.part);
     g.tickets = (uint32_t*)(b + L.tickets) + kFp8Tickets;
-    SVDQ_TRY(after_launch(launch_fp8_gemm(g, cus, s), s));
   }
+  // the bias gradient: in the first product's launch that takes it, else its own
+  const Fp8BiasGrad bias = {qy.sums, (int)(round128(M) / 128), d->N, db};
+  const bool in_dx = db && dx && fp8_gemm_takes_bias(gx), in_dw = db && dw && !in_dx && fp8_gemm_takes_bias(gw);
+  if (db && !in_dx && !in_dw) SVDQ_TRY(after_launch(launch_fp8_bias_grad(bias, s), s));
+  if (dx) SVDQ_TRY(after_launch(launch_fp8_gemm(gx, cus, s, in_dx ? &bias : nullptr), s));
+  if (dw) SVDQ_TRY(after_launch(launch_fp8_gemm(gw, cus, s, in_dw ? &bias : nullptr), s));
   return SVDQ_OK;
 }
 

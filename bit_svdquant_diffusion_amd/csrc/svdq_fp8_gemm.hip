@@ -518,8 +518,13 @@ __global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
 // outputs: 20.5 us, 20.7 and 22; 2064, 1003 and 1552: 16.2, 15.8 and 18.1).
 constexpr int kDeepStage = 2 * 64 * 128, kDeepOps = 4;   // bytes of a stage; transfers per wave and stage
 template <int D, bool BROW>
-__global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int chunk, int runs) {
+__global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int chunk, int runs, Fp8BiasGrad bias) {
   extern __shared__ __align__(16) uint8_t smem[];
+  const int all = tiles_m * tiles_n * runs;
+  if ((int)blockIdx.x >= all) {
+    bias_grad_32<256>(bias.sums, bias.blocks, bias.N, ((int)blockIdx.x - all) * 32, bias.db, reinterpret_cast<float*>(smem));
+    return;
+  }
   __shared__ int ticket_last;
   static_assert(D - 2 <= 4, "scale words are four stages ahead of their use, the transfers no more");
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
@@ -529,7 +534,7 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
   const int lda = (int)g.lda, ldb = (int)g.ldb;
   // an XCD (workgroups 8 apart) takes consecutive tiles of one run of
   // channels, those of the same weights next to each other
-  const int all = (int)gridDim.x, xcd = (int)blockIdx.x & 7;
+  const int xcd = (int)blockIdx.x & 7;
   const int t = xcd * (all >> 3) + min(xcd, all & 7) + ((int)blockIdx.x >> 3);
   const int m0 = t % tiles_m * 64, tn_ = t / tiles_m, n0 = tn_ % tiles_n * 64, run = tn_ / tiles_n;
   const int s0 = run * chunk, s1 = min(KR, s0 + chunk);
@@ -725,20 +730,24 @@ hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st) 
 
 namespace {
 template <bool BROW>
-hipError_t launch_deep(const Fp8Gemm& g, const Fp8Deep& p, hipStream_t st) {
-  const int tm = (int)((g.a_rows + 63) / 64), tn = (g.b_rows + 63) / 64;
-  const unsigned grid = (unsigned)(tm * tn * p.runs);
-  if (grid <= kFp8Cus)
-    hipLaunchKernelGGL((fp8_deep_kernel<5, BROW>), dim3(grid), dim3(256), 5 * kDeepStage, st, g, tm, tn, p.chunk, p.runs);
+hipError_t launch_deep(const Fp8Gemm& g, const Fp8Deep& p, const Fp8BiasGrad* bias, hipStream_t st) {
+  const int tm = (int)((g.a_rows + 63) / 64), tn = (g.b_rows + 63) / 64, all = tm * tn * p.runs;
+  const Fp8BiasGrad b = bias ? *bias : Fp8BiasGrad{nullptr, 0, 0, nullptr};
+  const dim3 grid((unsigned)(all + (b.N + 31) / 32));
+  if (all <= kFp8Cus)
+    hipLaunchKernelGGL((fp8_deep_kernel<5, BROW>), grid, dim3(256), 5 * kDeepStage, st, g, tm, tn, p.chunk, p.runs, b);
   else
-    hipLaunchKernelGGL((fp8_deep_kernel<3, BROW>), dim3(grid), dim3(256), 3 * kDeepStage, st, g, tm, tn, p.chunk, p.runs);
+    hipLaunchKernelGGL((fp8_deep_kernel<3, BROW>), grid, dim3(256), 3 * kDeepStage, st, g, tm, tn, p.chunk, p.runs, b);
   return hipGetLastError();
 }
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st) {
+// (a launch of its own takes 3 us of a small backward's 30)
+bool fp8_gemm_takes_bias(const Fp8Gemm& g) { return fp8_deep(g.a_rows, g.b_rows, g.K).runs > 0; }
+
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st, const Fp8BiasGrad* bias) {
   const Fp8Deep p = fp8_deep(g.a_rows, g.b_rows, g.K);
-  if (p.runs > 0) return g.b_row_scales ? launch_deep<true>(g, p, st) : launch_deep<false>(g, p, st);
+  if (p.runs > 0) return g.b_row_scales ? launch_deep<true>(g, p, bias, st) : launch_deep<false>(g, p, bias, st);
   // The tile of least cost, a cost being the rounds of tiles over the CUs times
   // a round's time relative to TileL's, as measured on the products of K from
   // 2048 to 12288: TileW 0.85 (it fills the CUs where TileL's rounds do not:

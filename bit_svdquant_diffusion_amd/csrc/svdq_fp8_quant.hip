@@ -4,10 +4,7 @@
 //
 // the scale byte e + 127 (E8M0). A power of two makes the quotient exact, so
 // a code is one correct rounding of v / scale, and the block-scaled MFMA
-// applies the scale by itself. Memory-bound: bf16 in once, codes out once; the
-// inputs are read past the caches (non-temporal), which keeps the codes in
-// them for the product (4608 tokens, 3072 -> 12288 with inputs that rotate
-// through more than the caches hold: 167 us against 175).
+// applies the scale by itself. Memory-bound: bf16 in once, codes out once.
 #include <algorithm>
 
 #include "svdq_internal.h"
@@ -18,48 +15,47 @@ namespace svdq {
 
 namespace {
 
-// Blocks along the rows: eight lanes a block, 16 channels (32 bytes) a lane;
-// a wave takes kUnits chunks of 1024 channels of consecutive (row, chunk)s,
-// all loads first. `plain` scales: [blocks / 4][M][4]. Channels in [K, Kp) get zero codes (K % 16 == 0: whole lanes).
-constexpr int kUnits = 2;
+// Inputs of 16 MB and more are read past the caches (non-temporal), which
+// keeps the codes in them for the product (4608 tokens, 3072 -> 12288, calls
+// that rotate through more than the caches hold: 167 us against 175; 1003
+// tokens of 2064 channels 16.0 us with plain loads, 16.2 without).
+constexpr double kOnceBytes = 16e6;
+__device__ __forceinline__ u32x4 load_input(const uint16_t* p, int once) {
+  const u32x4* v = reinterpret_cast<const u32x4*>(p);
+  return once ? __builtin_nontemporal_load(v) : *v;
+}
+
+// Blocks along the rows: eight lanes a block, 16 channels (32 bytes) a lane; a
+// wave takes 1024 channels of a row (two rows' took 0.5 us longer for 1003
+// rows). `plain` scales: [blocks / 4][M][4]. Channels in [K, Kp) get zero
+// codes (K % 16 == 0: whole lanes).
 __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, uint32_t units, uint32_t chunks, int64_t M, int K,
-                                                             int Kp, int plain, uint8_t* q, uint8_t* s, uint32_t* tickets) {
+                                                             int Kp, int plain, int once, uint8_t* q, uint8_t* s,
+                                                             uint32_t* tickets) {
   if (tickets && blockIdx.x == 0 && threadIdx.x < kFp8Tickets) tickets[threadIdx.x] = 0;
-  const int lane = threadIdx.x & 63;
-  const uint32_t u0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kUnits;
-  u32x4 v[kUnits][2];
-  uint32_t row[kUnits];
-  int at[kUnits];
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    row[u] = (u0 + u) / chunks;
-    at[u] = (int)((u0 + u) - row[u] * chunks) * 1024 + lane * 16;
-    v[u][0] = v[u][1] = u32x4{0, 0, 0, 0};
-    if (u0 + u < units && at[u] < K) {
-      const u32x4* p = reinterpret_cast<const u32x4*>(x + (size_t)row[u] * K + at[u]);
-      v[u][0] = __builtin_nontemporal_load(p);
-      v[u][1] = __builtin_nontemporal_load(p + 1);
-    }
+  const uint32_t unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= units) return;
+  const uint32_t row = unit / chunks;
+  const int lane = threadIdx.x & 63, at = (int)(unit - row * chunks) * 1024 + lane * 16;
+  u32x4 v0 = u32x4{0, 0, 0, 0}, v1 = v0;
+  if (at < K) {
+    const uint16_t* p = x + (size_t)row * K + at;
+    v0 = load_input(p, once);
+    v1 = load_input(p + 8, once);
   }
+  uint32_t amax = 0;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) amax = amax_bf16x2(amax_bf16x2(amax, v[u][0][i]), v[u][1][i]);
-    const int e = e4m3_exponent(max_dpp8(amax));
-    const float sc = exp2_int(e);
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w0 = v[u][i >> 1][2 * (i & 1)], w1 = v[u][i >> 1][2 * (i & 1) + 1];
-      o[i] = e4m3x4(bf16lo(w0), bf16hi(w0), bf16lo(w1), bf16hi(w1), sc);
-    }
-    if (u0 + u < units && at[u] < Kp) {
-      *reinterpret_cast<u32x4*>(q + (size_t)row[u] * Kp + at[u]) = o;
-      const int kb = at[u] / 128;
-      if ((lane & 7) == 0)
-        s[plain ? ((size_t)(kb / 4) * M + row[u]) * 4 + kb % 4 : fp8_scale_index(M, row[u], kb)] = (uint8_t)(e + 127);
-    }
+  for (int i = 0; i < 4; ++i) amax = amax_bf16x2(amax_bf16x2(amax, v0[i]), v1[i]);
+  const int e = e4m3_exponent(max_dpp8(amax));
+  const float sc = exp2_int(e);
+  if (at < Kp) {
+    *reinterpret_cast<u32x4*>(q + (size_t)row * Kp + at) =
+        u32x4{e4m3x4(bf16lo(v0[0]), bf16hi(v0[0]), bf16lo(v0[1]), bf16hi(v0[1]), sc),
+              e4m3x4(bf16lo(v0[2]), bf16hi(v0[2]), bf16lo(v0[3]), bf16hi(v0[3]), sc),
+              e4m3x4(bf16lo(v1[0]), bf16hi(v1[0]), bf16lo(v1[1]), bf16hi(v1[1]), sc),
+              e4m3x4(bf16lo(v1[2]), bf16hi(v1[2]), bf16lo(v1[3]), bf16hi(v1[3]), sc)};
+    const int kb = at / 128;
+    if ((lane & 7) == 0) s[plain ? ((size_t)(kb / 4) * M + row) * 4 + kb % 4 : fp8_scale_index(M, row, kb)] = (uint8_t)(e + 127);
   }
 }
 
@@ -76,7 +72,8 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, 
 // from the caches); 777 of 1552 and 2064 9.8 us, of which 4.5 go when the two
 // kinds of codes are not stored and 3.2 are the launch and the loads.
 constexpr int kTLd = 33;   // words of a transposed row in LDS (32 and one against bank conflicts)
-__global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a, uint32_t* tickets) {
+__global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a, int once,
+                                                          uint32_t* tickets) {
   if (blockIdx.x == 0 && threadIdx.x < 2 * kFp8Tickets) tickets[threadIdx.x] = 0;
   __shared__ uint32_t lds[2 * 32 * 128];   // maxima and sums [32][128] each, then codes [128][kTLd]
   __shared__ uint32_t red[2][4][128];
@@ -93,7 +90,7 @@ __global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8Quant
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     v[p] = u32x4{0, 0, 0, 0};
-    if (m0 + p < M && c < t.C) v[p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(t.x + (m0 + p) * t.C + c));
+    if (m0 + p < M && c < t.C) v[p] = load_input(t.x + (m0 + p) * t.C + c, once);
   }
   // value of token p, channel i of this thread
   auto val = [&](int p, int i) { return (i & 1) ? bf16hi(v[p][i >> 1]) : bf16lo(v[p][i >> 1]); };
@@ -167,28 +164,9 @@ __global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8Quant
   }
 }
 
-// The blocks' sums per channel: 32 threads a channel, each every 32nd block in
-// order, eight loads at a time (there are few workgroups, so this is latency),
-// then the 32 in order.
-__global__ __launch_bounds__(1024) void fp8_bias_grad_kernel(const float* sums, int blocks, int N, uint16_t* db) {
-  __shared__ float red[32][33];
-  const int cl = threadIdx.x & 31, k = threadIdx.x >> 5, n = blockIdx.x * 32 + cl;
-  float s = 0.f;
-  for (int i = k; i < blocks; i += 8 * 32) {
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = n < N && i + 32 * u < blocks ? sums[(size_t)(i + 32 * u) * N + n] : 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s += v[u];
-  }
-  red[k][cl] = s;
-  __syncthreads();
-  if (k == 0 && n < N) {
-    float t = red[0][cl];
-#pragma unroll
-    for (int i = 1; i < 32; ++i) t += red[i][cl];
-    db[n] = from_f32<Bf16>(t).bits;
-  }
+__global__ __launch_bounds__(1024) void fp8_bias_grad_kernel(Fp8BiasGrad a) {
+  __shared__ float red[32 * 33];
+  bias_grad_32<1024>(a.sums, a.blocks, a.N, blockIdx.x * 32, a.db, red);
 }
 
 __global__ __launch_bounds__(256) void fp8_zero_kernel(uint32_t* p, size_t n) {
@@ -269,8 +247,8 @@ hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q
                                  hipStream_t st) {
   const int Kp = (int)round128(K), chunks = (Kp + 1023) / 1024;
   const int64_t units = M * chunks;
-  const int64_t grid = (units + 4 * kUnits - 1) / (4 * kUnits);
-  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, q, s, tickets);
+  const int64_t grid = (units + 3) / 4;
+  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, (double)M * K * 2 >= kOnceBytes, q, s, tickets);
   return hipGetLastError();
 }
 
@@ -278,12 +256,13 @@ hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M,
   const int64_t rows = (M + 127) / 128;
   const int64_t na = a.x ? rows * ((a.C + 127) / 128) : 0, nb = b.x ? rows * ((b.C + 127) / 128) : 0;
   if (na + nb == 0) return hipSuccess;
-  hipLaunchKernelGGL(fp8_quant_t_kernel, dim3((unsigned)(na + nb)), dim3(512), 0, st, a, b, M, na, tickets);
+  hipLaunchKernelGGL(fp8_quant_t_kernel, dim3((unsigned)(na + nb)), dim3(512), 0, st, a, b, M, na,
+                     (double)M * ((a.x ? a.C : 0) + (b.x ? b.C : 0)) * 2 >= kOnceBytes, tickets);
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_bias_grad(const float* sums, int64_t blocks, int N, uint16_t* db, hipStream_t st) {
-  hipLaunchKernelGGL(fp8_bias_grad_kernel, dim3((N + 31) / 32), dim3(1024), 0, st, sums, (int)blocks, N, db);
+hipError_t launch_fp8_bias_grad(const Fp8BiasGrad& a, hipStream_t st) {
+  hipLaunchKernelGGL(fp8_bias_grad_kernel, dim3((a.N + 31) / 32), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

@@ -155,7 +155,13 @@ struct Fp8QuantT {
   float* sums;       // [round128(M)/128][C], or null
 };
 hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M, uint32_t* tickets, hipStream_t st);   // 2 kFp8Tickets
-hipError_t launch_fp8_bias_grad(const float* sums, int64_t blocks, int N, uint16_t* db, hipStream_t st);
+// the bias gradient: the blocks' sums per channel
+struct Fp8BiasGrad {
+  const float* sums;   // [blocks][N]
+  int blocks, N;
+  uint16_t* db;
+};
+hipError_t launch_fp8_bias_grad(const Fp8BiasGrad& a, hipStream_t st);
 hipError_t launch_fp8_zero(void* p, size_t bytes, int num_cus, hipStream_t st);   // bytes % 4 == 0
 hipError_t launch_fp8_pack(const void* w, int dtype, int K, int N, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st,
                            hipStream_t stream);
@@ -179,7 +185,9 @@ struct Fp8Gemm {
   uint32_t* tickets;
   const uint16_t* x;   // launch_fp8_gemm_small: A as bf16 rows [a_rows][K], or null
 };
-hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st);
+// bias: that gradient too, by further workgroups, where fp8_gemm_takes_bias
+bool fp8_gemm_takes_bias(const Fp8Gemm& g);
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st, const Fp8BiasGrad* bias = nullptr);
 hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st);
 hipError_t prepare_fp8();
 

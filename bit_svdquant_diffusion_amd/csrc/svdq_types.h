@@ -265,4 +265,32 @@ __device__ __forceinline__ uint32_t amax_bf16x2(uint32_t m, uint32_t w) {
   return umax(m, w & 0x7fff0000u);
 }
 
+// The bias gradient of 32 channels (n0 on) by a workgroup of THREADS: 32 chains
+// a channel, each every 32nd block in order with eight loads at a time (there
+// are few workgroups, so this is latency), then the 32 in order. `red` holds
+// 32 * 33 floats of LDS.
+template <int THREADS>
+__device__ __forceinline__ void bias_grad_32(const float* sums, int blocks, int N, int n0, uint16_t* db, float* red) {
+  const int cl = threadIdx.x & 31, n = n0 + cl;
+#pragma unroll
+  for (int k = threadIdx.x >> 5; k < 32; k += THREADS / 32) {
+    float s = 0.f;
+    for (int i = k; i < blocks; i += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = n < N && i + 32 * u < blocks ? sums[(size_t)(i + 32 * u) * N + n] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    red[k * 33 + cl] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32 && n < N) {
+    float t = red[cl];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) t += red[i * 33 + cl];
+    db[n] = from_f32<Bf16>(t).bits;
+  }
+}
+
 }  // namespace svdq
