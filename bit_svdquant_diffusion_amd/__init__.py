@@ -693,10 +693,15 @@ def _empty(shape, dtype, like, stream):
     torch = _torch()
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
-    with torch.cuda.stream(stream):
+    with _under(stream, like.device):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _under(stream, device):
+    """The context of a stream, given as torch's object or as its handle."""
+    if isinstance(stream, int):
+        stream = _t.cuda.ExternalStream(stream, device=device)
+    return _t.cuda.stream(stream)
 
 
 def _call(name: str, at: int, stream, *args):
@@ -747,6 +752,16 @@ def _norm_desc(C, dt, pdt, one_plus, groups, eps, rows_per_group):
     """A reference to the descriptor (the library only reads it) and itself."""
     d = NormDesc(C, dt, pdt, one_plus, groups, eps, rows_per_group)
     return ctypes.byref(d), d
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_ws(C, groups, rows_per_group, M) -> int:
+    """Workspace bytes of the gradients (the types do not matter)."""
+    need = ctypes.c_size_t()
+    _check(lib().svdq_layer_norm_backward_workspace_bytes(_norm_desc(C, 0, 0, 0, groups, 0.0, rows_per_group)[0], M,
+                                                          ctypes.byref(need)),
+           "svdq_layer_norm_backward_workspace_bytes")
+    return need.value
 
 
 def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, groups=None):
@@ -825,6 +840,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, 
         _need(t.dtype == f32 and t.shape == (M,) and t.is_contiguous(), "mean, rstd: float32 [rows]")
     flat = groups is None if weight is None else weight.dim() == 1
     d, G, wp, ldw, _, _ = _norm_params(C, weight, None, one_plus, 0.0, rows_per_group, M, x.dtype, groups)
+    rpg = rows_per_group if rows_per_group is not None else max(1, -(-M // max(1, G)))
     gdt = grad_dtype if grad_dtype is not None else (weight.dtype if weight is not None else f32)
     if dx is None:
         dx = _rows_like(x, (M, C), stream)
@@ -833,11 +849,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, 
     dw = db = wsp = ws = None
     size = 0
     if param_grads:
-        need = ctypes.c_size_t()
-        _check(lib().svdq_layer_norm_backward_workspace_bytes(d, M, ctypes.byref(need)),
-               "svdq_layer_norm_backward_workspace_bytes")
-        size = need.value
-        dw, db = _empty((2, C) if flat else (2, G, C), gdt, x, stream).unbind()
+        size = _norm_ws(C, G, rpg, M)
+        dw = _empty((C,) if flat else (G, C), gdt, x, stream)
+        db = _t.empty_like(dw) if stream is None else _empty(dw.shape, gdt, x, stream)
         if size:
             ws = _empty((size,), _t.uint8, x, stream)
             wsp = ws.data_ptr()
@@ -888,7 +902,12 @@ def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, str
         out = {"q": new(N, "q"), "s": new(-(-N // 128), "s"), "qt": new(K, "qt") if transposed else None,
                "st": new(-(-K // 128), "st") if transposed else None, "bias": None}
     if bias is not None:
-        out["bias"] = bias.to(torch.bfloat16).contiguous()
+        _need(bias.shape == (N,), "bias: [N]")
+        if stream is None:
+            out["bias"] = bias.to(torch.bfloat16).contiguous()
+        else:
+            with _under(stream, w.device):   # a conversion belongs to the call's stream
+                out["bias"] = bias.to(torch.bfloat16).contiguous()
     at = _on_device(w, *out.values())
     p = _fp8_struct(K, N, out)
     _call("svdq_fp8_pack", at, stream, ctypes.byref(Fp8Desc(K, N)), w.data_ptr(), _dt(w.dtype), ctypes.byref(p))
@@ -897,6 +916,7 @@ def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, str
 
 def _fp8_struct(K: int, N: int, dev: dict) -> Fp8Packed:
     """The buffers of a layer, each of at least its size."""
+    _torch()
     rk, rn = (K + 127) // 128, (N + 127) // 128
     ptrs = []
     for n, least in (("q", N * K), ("s", rn * ((rk + 3) // 4 * 4)), ("qt", N * K), ("st", rk * ((rn + 3) // 4 * 4)),
@@ -905,8 +925,8 @@ def _fp8_struct(K: int, N: int, dev: dict) -> Fp8Packed:
         if t is None:
             ptrs.append(None)
             continue
-        if not t.is_contiguous() or t.numel() < least or t.element_size() != (2 if n == "bias" else 1):
-            raise ValueError(f"fp8 layer: {n} must be contiguous with {least} elements")
+        if not t.is_contiguous() or t.numel() < least or (t.dtype != _t.bfloat16 if n == "bias" else t.element_size() != 1):
+            raise ValueError(f"fp8 layer: {n} must be contiguous with {least} elements of {'bfloat16' if n == 'bias' else 'a byte'}")
         ptrs.append(t.data_ptr())
     return Fp8Packed(*ptrs)
 
@@ -1020,4 +1040,5 @@ class Fp8Linear:
         return fp8_backward(self.K, self.N, self.dev, x, dy, need, stream=stream)
 
     def update(self, w, bias=None, stream=None):
+        _need(w.shape == (self.N, self.K), "w: the layer's shape")
         fp8_pack(w, bias, out=self.dev, stream=stream)

@@ -386,3 +386,60 @@ def test_inline_limit():
         a, w = R.q8(x.double())[0], _weight(dev, K, N)
         bias = dev["bias"].double()
         _close(y, a @ w.t().contiguous() + bias, R.product_bound(a, w, bias), (M, K, N))
+
+
+def test_layer_refusals():
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = torch.randn(64, 128, device="cuda", generator=g)
+    lin = S.Fp8Linear(w)
+    x = _bf16(g, 4, 128)
+    for bad in (torch.randn(48, 128, device="cuda"), torch.randn(128, 64, device="cuda")):
+        with pytest.raises(ValueError):
+            lin.update(bad)
+    with pytest.raises(ValueError):
+        S.fp8_pack(w, torch.zeros(65, device="cuda"))
+    half = dict(lin.dev, bias=torch.zeros(64, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError):
+        S.fp8_forward(128, 64, half, x)
+    for call in (lambda: lin(x.float()), lambda: lin(x[:, :112]), lambda: lin(x.t()), lambda: lin(x, y=x),
+                 lambda: lin.backward(x, x), lambda: lin.after_norm(x, torch.ones(128, device="cuda").expand(2, 128))):
+        with pytest.raises(ValueError):
+            call()
+    dy = _bf16(g, 4, 64)
+    with pytest.raises(S.SvdqError):   # the input's gradient needs the transposed codes
+        S.Fp8Linear(w, trainable=False).backward(x, dy)
+    with pytest.raises(S.SvdqError):   # 16-byte alignment
+        odd = _bf16(g, 5 * 128 + 1)[1:].view(5, 128)
+        lin(odd)
+
+
+def test_runs_in_graphs_and_on_two_streams():
+    """Runs of channels (their tiles take tickets in the workspace): two graphs
+    that share a workspace, replayed in turn with eager calls between, and two
+    streams at once with workspaces of their own."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    M, K, N = 40, 8208, 272
+    layers = [_layer(g, K, N, transposed=False)[1] for _ in range(2)]
+    xs = [_bf16(g, M, K) for _ in range(2)]
+    want = [S.fp8_forward(K, N, layers[i], xs[i]) for i in range(2)]
+    ws = torch.empty(S.fp8_workspace_bytes(K, N, M), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    ys = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            S.fp8_forward(K, N, layers[i], xs[i], y=ys[i], workspace=ws)
+        graphs.append(graph)
+    for k in range(4):
+        for i in range(2):
+            ys[i].zero_()
+            graphs[i].replay()
+            again = S.fp8_forward(K, N, layers[1 - i], xs[1 - i], workspace=ws)
+            torch.cuda.synchronize()
+            assert torch.equal(ys[i], want[i]) and torch.equal(again, want[1 - i]), (k, i)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(5):
+        got = [S.fp8_forward(K, N, layers[i], xs[i], stream=streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k

@@ -266,3 +266,16 @@ def test_norm_refuses_overlapping_rows():
         S.layer_norm_backward(one, x, mean, rstd, w)
     with pytest.raises(ValueError):
         S.layer_norm_backward(dy, x, mean[:1].expand(6), rstd, w)
+
+
+@pytest.mark.parametrize("C", [5, 40, 100, 250])
+def test_norm_infinities_and_nan_in_rows_that_share_a_wave(C):
+    x, w, b, dy = _inputs(40, C, torch.bfloat16, torch.bfloat16, 1, 8)
+    x[3, C // 2], x[17, 0], x[38, C - 1] = float("inf"), float("nan"), float("-inf")
+    y, mean, rstd = S.layer_norm_forward(x, w, b)
+    dx, dw, db = S.layer_norm_backward(dy, x, mean, rstd, w)
+    bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+    bad[[3, 17, 38]] = True
+    assert bool(y[bad].isnan().all()) and bool(y[~bad].isfinite().all())
+    assert bool(dx[bad].isnan().all()) and bool(dx[~bad].isfinite().all())
+    assert bool(db.isfinite().all())
