@@ -681,10 +681,14 @@ def _on_device(x, *tensors) -> int:
     at = x.get_device()
     if at < 0:
         raise ValueError("the tensors must be on a GPU")
+    _same_device(at, *tensors)
+    return at
+
+
+def _same_device(at: int, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != at:
-            raise ValueError(f"tensors on {x.device} and {t.device}")
-    return at
+            raise ValueError(f"tensors on GPU {at} and on {t.device}")
 
 
 def _empty(shape, dtype, like, stream):
@@ -908,27 +912,46 @@ def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, str
         else:
             with _under(stream, w.device):   # a conversion belongs to the call's stream
                 out["bias"] = bias.to(torch.bfloat16).contiguous()
-    at = _on_device(w, *out.values())
-    p = _fp8_struct(K, N, out)
-    _call("svdq_fp8_pack", at, stream, ctypes.byref(Fp8Desc(K, N)), w.data_ptr(), _dt(w.dtype), ctypes.byref(p))
+    at = _on_device(w)
+    d, p = _fp8_struct(K, N, out, at)
+    _call("svdq_fp8_pack", at, stream, d, w.data_ptr(), _dt(w.dtype), p)
     return out
 
 
-def _fp8_struct(K: int, N: int, dev: dict) -> Fp8Packed:
-    """The buffers of a layer, each of at least its size."""
-    _torch()
-    rk, rn = (K + 127) // 128, (N + 127) // 128
-    ptrs = []
-    for n, least in (("q", N * K), ("s", rn * ((rk + 3) // 4 * 4)), ("qt", N * K), ("st", rk * ((rn + 3) // 4 * 4)),
-                     ("bias", N)):
-        t = dev.get(n)
-        if t is None:
-            ptrs.append(None)
-            continue
-        if not t.is_contiguous() or t.numel() < least or (t.dtype != _t.bfloat16 if n == "bias" else t.element_size() != 1):
-            raise ValueError(f"fp8 layer: {n} must be contiguous with {least} elements of {'bfloat16' if n == 'bias' else 'a byte'}")
-        ptrs.append(t.data_ptr())
-    return Fp8Packed(*ptrs)
+@functools.lru_cache(maxsize=1024)
+def _fp8_desc(K: int, N: int):
+    """(descriptor reference, itself, bytes of q and qt, s, st, bias)"""
+    d, rk, rn = Fp8Desc(K, N), (K + 127) // 128, (N + 127) // 128
+    return ctypes.byref(d), d, N * K, rn * ((rk + 3) // 4 * 4), rk * ((rn + 3) // 4 * 4), 2 * N
+
+
+def _fp8_buffer(t, least: int, name: str):
+    """The address of a layer's buffer of at least `least` bytes."""
+    if t is None:
+        return None
+    if t.nbytes < least or not t.is_contiguous():
+        raise ValueError(f"fp8 layer: {name} must be contiguous with {least} bytes")
+    return t.data_ptr()
+
+
+def _fp8_struct(K: int, N: int, dev: dict, at: int = -1, forward: bool = True, backward: bool = True):
+    """(reference to the descriptor, reference to the buffers) of a layer on
+    GPU `at`: those that the forward or the backward read, or all."""
+    ref, _, nq, ns, nst, nb = _fp8_desc(K, N)
+    p = Fp8Packed()
+    if forward:
+        q, s, bias = dev.get("q"), dev.get("s"), dev.get("bias")
+        p.q, p.s = _fp8_buffer(q, nq, "q"), _fp8_buffer(s, ns, "s")
+        if bias is not None:
+            if bias.dtype != _torch().bfloat16:
+                raise ValueError("fp8 layer: bias must be bfloat16")
+            p.bias = _fp8_buffer(bias, nb, "bias")
+        _same_device(at, q, s, bias)
+    if backward:
+        qt, st = dev.get("qt"), dev.get("st")
+        p.qt, p.st = _fp8_buffer(qt, nq, "qt"), _fp8_buffer(st, nst, "st")
+        _same_device(at, qt, st)
+    return ref, ctypes.byref(p)
 
 
 def _bf16_rows(t, cols: int, what: str):
@@ -944,12 +967,13 @@ def _scratch(workspace, size: int, like, stream):
             return None, None, 0
         workspace = _empty((size,), _t.uint8, like, stream)
         return workspace, workspace.data_ptr(), size
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _need(workspace.is_contiguous(), "workspace: contiguous")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def fp8_forward(K: int, N: int, dev: dict, x, y=None, workspace=None, stream=None):
     """y[M][N] bf16 = FP8 layer(x[M][K] bf16) via svdq_fp8_forward."""
-    at = _on_device(x, y, workspace, *dev.values())
+    at = _on_device(x, y, workspace)
     _bf16_rows(x, K, "x")
     M = x.shape[0]
     if y is None:
@@ -958,8 +982,8 @@ def fp8_forward(K: int, N: int, dev: dict, x, y=None, workspace=None, stream=Non
         _bf16_rows(y, N, "y")
         _need(y.shape[0] == M, "y: as many rows as x")
     ws, wsp, size = _scratch(workspace, fp8_workspace_bytes(K, N, M), x, stream)
-    _call("svdq_fp8_forward", at, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(_fp8_struct(K, N, dev)), x.data_ptr(),
-          M, y.data_ptr(), wsp, size)
+    d, p = _fp8_struct(K, N, dev, at, backward=False)
+    _call("svdq_fp8_forward", at, stream, d, p, x.data_ptr(), M, y.data_ptr(), wsp, size)
     return y
 
 
@@ -968,7 +992,7 @@ def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: 
     """y[M][N] = FP8 layer(layer norm(x)) via svdq_fp8_norm_forward, the norm's
     parameters as in layer_norm_forward (`bias` is the norm's; the layer's own
     is in dev). With stats: (y, mean, rstd)."""
-    at = _on_device(x, weight, bias, y, workspace, *dev.values())
+    at = _on_device(x, weight, bias, y, workspace)
     _bf16_rows(x, K, "x")
     M = x.shape[0]
     d, _, wp, ldw, bp, ldb = _norm_params(K, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
@@ -981,8 +1005,9 @@ def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: 
     mean = rstd = None
     if stats:
         mean, rstd = _stats(M, x, stream)
-    _call("svdq_fp8_norm_forward", at, stream, d, wp, ldw, bp, ldb, ctypes.byref(Fp8Desc(K, N)),
-          ctypes.byref(_fp8_struct(K, N, dev)), x.data_ptr(), M, y.data_ptr(), _ptr(mean), _ptr(rstd), wsp, size)
+    fd, p = _fp8_struct(K, N, dev, at, backward=False)
+    _call("svdq_fp8_norm_forward", at, stream, d, wp, ldw, bp, ldb, fd, p, x.data_ptr(), M, y.data_ptr(), _ptr(mean),
+          _ptr(rstd), wsp, size)
     return (y, mean, rstd) if stats else y
 
 
@@ -990,7 +1015,7 @@ def fp8_backward(K: int, N: int, dev: dict, x, dy, need=(True, True, True), work
     """svdq_fp8_backward: (dx [M][K], dw [N][K], db [N]), bf16, of fp8_forward
     for dy [M][N] bf16; None where `need` says no. Without dx, dev may lack qt
     and st; without dw, x may be None."""
-    at = _on_device(dy, x, workspace, *dev.values())
+    at = _on_device(dy, x, workspace)
     _bf16_rows(dy, N, "dy")
     M = dy.shape[0]
     if x is not None:
@@ -1001,8 +1026,8 @@ def fp8_backward(K: int, N: int, dev: dict, x, dy, need=(True, True, True), work
     dw = _empty((N, K), bf16, dy, stream) if need[1] else None
     db = _empty((N,), bf16, dy, stream) if need[2] else None
     ws, wsp, size = _scratch(workspace, fp8_backward_workspace_bytes(K, N, M), dy, stream)
-    _call("svdq_fp8_backward", at, stream, ctypes.byref(Fp8Desc(K, N)), ctypes.byref(_fp8_struct(K, N, dev)), _ptr(x),
-          dy.data_ptr(), M, _ptr(dx), _ptr(dw), _ptr(db), wsp, size)
+    d, p = _fp8_struct(K, N, dev, at, forward=False)
+    _call("svdq_fp8_backward", at, stream, d, p, _ptr(x), dy.data_ptr(), M, _ptr(dx), _ptr(dw), _ptr(db), wsp, size)
     return dx, dw, db
 
 

@@ -398,6 +398,9 @@ def test_layer_refusals():
             lin.update(bad)
     with pytest.raises(ValueError):
         S.fp8_pack(w, torch.zeros(65, device="cuda"))
+    ws = torch.empty(2, S.fp8_workspace_bytes(128, 64, 40), dtype=torch.uint8, device="cuda").t()
+    with pytest.raises(ValueError):
+        S.fp8_forward(128, 64, lin.dev, _bf16(g, 40, 128), workspace=ws)
     half = dict(lin.dev, bias=torch.zeros(64, dtype=torch.float16, device="cuda"))
     with pytest.raises(ValueError):
         S.fp8_forward(128, 64, half, x)
