@@ -271,8 +271,8 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   // Where some workgroups have one tile fewer they start about a third of a
   // tile later (a stage takes 1.6 us): then not all tiles' outputs go to
   // memory at the same time, whose 33 MB take longer than a stage (3.4 rounds
-  // at 4608 x 12288 outputs over 3072 channels 170 us against 175, without
-  // any stores 148).
+  // at 4608 x 12288 outputs over 3072 channels, the whole call 166 us against
+  // 169; without any stores 148).
   if (ntiles > grid && ntiles % grid != 0 && t_cur >= ntiles % grid)
     for (int i = 0; i < KB / 2; ++i) __builtin_amdgcn_s_sleep(32);   // 2048 cycles
   TileMap tm = map_tile(t_cur, tiles_m, tiles_n, group_m);
@@ -333,13 +333,23 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
     __builtin_amdgcn_sched_barrier(0);
     SVDQ_SCALE_ROWS(m_next, n_next)   // (without a next tile this tile's again)
     SVDQ_SCALES(0)
+    // All bias words before the first store: vector memory completes in order,
+    // so the wait for a later load is a wait for the stores before it (170 us
+    // against 165 at 4608 x 12288 outputs over 3072 channels).
+    u32x2 bias[TN][4];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bias[j][q] = u32x2{0, 0};
+        if (g.bias) bias[j][q] = *reinterpret_cast<const u32x2*>(g.bias + min(n0 + wn * TL::WN + 32 * j + 8 * q + 4 * h, Rb - 4));
+      }
+    __builtin_amdgcn_sched_barrier(0);
     SVDQ_MFMA(ya, yb)
 
     // A lane holds token m0 + 32 i + lr and channels 32 j + 8 q + 4 h + (0..3);
     // spread_rows leaves it channels at_c .. at_c + 7 of tokens lr % 16 and
-    // lr % 16 + 16, so that a store fills 64 contiguous bytes of sixteen rows
-    // (32 bytes of 32 rows take the L2 twice the requests: 13 us more of 172
-    // at 4608 x 12288 outputs, whose tiles are stored all at once).
+    // lr % 16 + 16, so that a store fills 64 contiguous bytes of sixteen rows.
     // Every store is issued by every wave, as the ring's waits count them: the
     // resource drops rows past the operand, and channels past it are sent past
     // its end.
@@ -352,8 +362,7 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
       float bv[16];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        u32x2 w = u32x2{0, 0};
-        if (g.bias) w = *reinterpret_cast<const u32x2*>(g.bias + min(col + 8 * q + 4 * h, Rb - 4));
+        const u32x2 w = bias[j][q];
         bv[4 * q] = bf16lo(w.x);
         bv[4 * q + 1] = bf16hi(w.x);
         bv[4 * q + 2] = bf16lo(w.y);
@@ -435,6 +444,8 @@ __global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
   };
 #pragma unroll
   for (int u = 0; u < kRing; ++u) load(u, u);
+  const int n_out = n0 + 4 * c + 2 * (wave & 1);   // the output channels of a thread of the first two waves
+  const uint32_t bias = g.bias ? *reinterpret_cast<const uint32_t*>(g.bias + n_out) : 0u;
   // eight lanes a block, 16 channels a lane
   const int per_row = KB * 8, items = M * per_row;
   for (int i = tid; i < items; i += 64 * W) {
@@ -492,11 +503,8 @@ __global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
       s0 += red[w][2 * pe][lane];
       s1 += red[w][2 * pe + 1][lane];
     }
-    if (r < M) {
-      const int col = n0 + 4 * c + 2 * pe;
-      const uint32_t b = g.bias ? *reinterpret_cast<const uint32_t*>(g.bias + col) : 0u;
-      *reinterpret_cast<uint32_t*>(g.out + (size_t)r * g.b_rows + col) = cvt_bf16x2(s0 + bf16lo(b), s1 + bf16hi(b));
-    }
+    if (r < M)
+      *reinterpret_cast<uint32_t*>(g.out + (size_t)r * g.b_rows + n_out) = cvt_bf16x2(s0 + bf16lo(bias), s1 + bf16hi(bias));
   }
 }
 
@@ -594,6 +602,12 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
     }
   };
   scales(s0 / 4);
+  u32x2 bw[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    bw[q] = u32x2{0, 0};
+    if (g.bias) bw[q] = *reinterpret_cast<const u32x2*>(g.bias + min(col0 + 8 * q + 4 * h, Rb - 4));
+  }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int u = 0; u < D - 1; ++u) fetch(s0 + u, u);
@@ -660,13 +674,8 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
   uint32_t o[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    f32x4 v = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-    if (g.bias) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(g.bias + min(col0 + 8 * q + 4 * h, Rb - 4));
-      v += f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
-    }
-    o[2 * q] = cvt_bf16x2(v[0], v[1]);
-    o[2 * q + 1] = cvt_bf16x2(v[2], v[3]);
+    o[2 * q] = cvt_bf16x2(acc[4 * q] + bf16lo(bw[q].x), acc[4 * q + 1] + bf16hi(bw[q].x));
+    o[2 * q + 1] = cvt_bf16x2(acc[4 * q + 2] + bf16lo(bw[q].y), acc[4 * q + 3] + bf16hi(bw[q].y));
   }
   spread_rows(o);
   const int row = row0 + (lr & 15), c = col0 + 8 * h + (lr & 16);
