@@ -759,10 +759,10 @@ def _norm_desc(C, dt, pdt, one_plus, groups, eps, rows_per_group):
 
 
 @functools.lru_cache(maxsize=4096)
-def _norm_ws(C, groups, rows_per_group, M) -> int:
-    """Workspace bytes of the gradients (the types do not matter)."""
+def _norm_ws(C, dt, groups, rows_per_group, M) -> int:
+    """Workspace bytes of the gradients (the parameters' type does not matter)."""
     need = ctypes.c_size_t()
-    _check(lib().svdq_layer_norm_backward_workspace_bytes(_norm_desc(C, 0, 0, 0, groups, 0.0, rows_per_group)[0], M,
+    _check(lib().svdq_layer_norm_backward_workspace_bytes(_norm_desc(C, dt, 0, 0, groups, 0.0, rows_per_group)[0], M,
                                                           ctypes.byref(need)),
            "svdq_layer_norm_backward_workspace_bytes")
     return need.value
@@ -771,22 +771,28 @@ def _norm_ws(C, groups, rows_per_group, M) -> int:
 def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, groups=None):
     """(NormDesc reference, groups, weight pointer, stride, bias pointer,
     stride) of [C] or [groups][C] parameters."""
-    some = weight if weight is not None else bias
-    wp = bp = None
+    wp = bp = shape = None
     ldw = ldb = C
     pdt = dtype
+    some = weight if weight is not None else bias
     if some is not None:
-        pdt = some.dtype
-        shape = some.shape
+        shape, pdt = some.shape, some.dtype
         groups = shape[0] if len(shape) == 2 else 1
+        plain = (C,) if len(shape) == 1 else (groups, C)
         if weight is not None:
-            wp, ldw = _param(weight, C, groups, pdt, "weight")
+            if shape == plain and weight.is_contiguous():
+                wp = weight.data_ptr()
+            else:
+                wp, ldw = _param(weight, C, groups, pdt, "weight")
         if bias is not None:
-            bp, ldb = _param(bias, C, groups, pdt, "bias")
+            if bias.shape == plain and bias.dtype is pdt and bias.is_contiguous():
+                bp = bias.data_ptr()
+            else:
+                bp, ldb = _param(bias, C, groups, pdt, "bias")
     elif groups is None:
         groups = 1
     if rows_per_group is None:
-        rows_per_group = max(1, -(-M // max(1, groups)))
+        rows_per_group = M if groups == 1 and M > 0 else max(1, -(-M // max(1, groups)))
     dt = _dt(dtype)
     return (_norm_desc(C, dt, dt if pdt is dtype else _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group)[0], groups,
             wp, ldw, bp, ldb)
@@ -853,7 +859,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, 
     dw = db = wsp = ws = None
     size = 0
     if param_grads:
-        size = _norm_ws(C, G, rpg, M)
+        size = _norm_ws(C, _dt(x.dtype), G, rpg, M)
         dw = _empty((C,) if flat else (G, C), gdt, x, stream)
         db = _t.empty_like(dw) if stream is None else _empty(dw.shape, gdt, x, stream)
         if size:

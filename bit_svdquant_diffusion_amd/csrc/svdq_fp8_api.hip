@@ -124,7 +124,7 @@ svdq_status svdq_layer_norm_forward(const svdq_norm_desc* d, const void* x, int6
 svdq_status svdq_layer_norm_backward_workspace_bytes(const svdq_norm_desc* d, int64_t M, size_t* out) {
   SVDQ_TRY(check_norm(d, M));
   if (!out) return SVDQ_ERR_NULL;
-  *out = norm_grad_ws(M, d->groups, d->rows_per_group, d->channels);
+  *out = norm_grad_ws(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype));
   return SVDQ_OK;
 }
 
@@ -145,7 +145,7 @@ svdq_status svdq_layer_norm_backward(const svdq_norm_desc* d, const void* dy, in
     if (!mean || !rstd) return SVDQ_ERR_NULL;
     if (!aligned(mean, 4) || !aligned(rstd, 4)) return SVDQ_ERR_SHAPE;
   }
-  const size_t need = pg ? norm_grad_ws(M, d->groups, d->rows_per_group, d->channels) : 0;
+  const size_t need = pg ? norm_grad_ws(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype)) : 0;
   if (need > 0) {
     if (!ws) return SVDQ_ERR_NULL;
     if (!aligned(ws, 16)) return SVDQ_ERR_SHAPE;
@@ -166,7 +166,7 @@ svdq_status svdq_layer_norm_backward(const svdq_norm_desc* d, const void* dy, in
   g.gdtype = grad_dtype;
   g.part = need > 0 ? (float*)ws : nullptr;
   hipStream_t s = (hipStream_t)stream;
-  return after_launch(launch_norm_grad(g, norm_grad_plan(M, d->groups, d->rows_per_group), s), s);
+  return after_launch(launch_norm_grad(g, norm_grad_plan(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype)), s), s);
 }
 
 svdq_status svdq_fp8_packed_bytes(const svdq_fp8_desc* d, svdq_fp8_sizes* out) {

@@ -267,26 +267,58 @@ inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   return w;
 }
 
+// Layer norm: the lanes that hold a row of n vectors (of `vec` elements). Rows
+// of up to 16 or 32 vectors share a wave; else W waves of nv vectors a lane,
+// nv vec <= 16, the pair that leaves the fewest lanes idle (the fewest waves
+// among those).
+constexpr int kNormWaves = 16;   // of a workgroup, and of a row: 16 x 64 lanes x 16 elements
+struct NormTeam {
+  int nv, waves, sub;
+};
+inline NormTeam norm_team(int n, int vec, bool may_share) {
+  if (may_share && n <= 32) return NormTeam{1, 1, n <= 16 ? 4 : 2};
+  NormTeam best{0, 0, 1};
+  for (int nv = 16 / vec; nv >= 1; --nv) {
+    const int w = (n + 64 * nv - 1) / (64 * nv);
+    if (w <= kNormWaves && (n + 64 * w - 1) / (64 * w) == nv && (best.nv == 0 || nv * w < best.nv * best.waves))
+      best = NormTeam{nv, w, 1};
+  }
+  return best;
+}
+// Waves of the backward's workgroups: sixteen, or twelve where a lane holds 16
+// elements, whose sums and values take 137 (fp32 156) registers of the 168
+// that twelve waves leave. (Rows of more than twelve waves spill a few.)
+SVDQ_HD constexpr int norm_grad_waves(int elements) { return elements > 12 ? 12 : kNormWaves; }
+// the teams of such a workgroup at most
+inline int norm_grad_teams(const NormTeam& t, int vec) {
+  const int waves = norm_grad_waves(t.nv * vec);
+  return (waves > t.waves ? waves / t.waves : 1) * t.sub;
+}
+
 // Layer-norm backward: every group's rows in `runs` runs, one workgroup each,
-// about kNormRuns in all.
+// about kNormRuns in all; one run, which needs nothing joined, where its teams
+// have at most two rows each (24 rows of 1000 bf16 channels: a launch and a
+// workspace less, 13.3 us a call against 18.2 with the host's part, 7.5
+// against 7.0 on the GPU alone).
 constexpr int kNormRuns = 256;
 struct NormGradPlan {
   int runs;
   int64_t rows_per_run;   // at most
 };
-inline NormGradPlan norm_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group) {
+inline NormGradPlan norm_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
   const int64_t rows = rows_per_group < M ? rows_per_group : M;
   const int64_t live = M > 0 ? (M + rows_per_group - 1) / rows_per_group : 1;   // groups that have rows
+  const int vec = 16 / elem_bytes, teams = norm_grad_teams(norm_team((C + vec - 1) / vec, vec, true), vec);
   int64_t runs = kNormRuns / live;
   if (runs > (rows + 3) / 4) runs = (rows + 3) / 4;   // at least four rows each
-  if (runs < 1 || groups > kNormRuns) runs = 1;
+  if (runs < 1 || groups > kNormRuns || rows <= 2 * teams) runs = 1;
   NormGradPlan p;
   p.runs = (int)runs;
   p.rows_per_run = rows > 0 ? (rows + runs - 1) / runs : 1;
   return p;
 }
-inline size_t norm_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C) {
-  const NormGradPlan p = norm_grad_plan(M, groups, rows_per_group);
+inline size_t norm_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
+  const NormGradPlan p = norm_grad_plan(M, groups, rows_per_group, C, elem_bytes);
   return p.runs > 1 ? (size_t)groups * p.runs * 2 * C * 4 : 0;
 }
 

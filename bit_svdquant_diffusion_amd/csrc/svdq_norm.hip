@@ -23,7 +23,7 @@ namespace svdq {
 
 namespace {
 
-constexpr int kMaxWaves = 16;   // of a workgroup, and of a row: 16 x 64 lanes x 16 elements
+constexpr int kMaxWaves = kNormWaves;
 
 // Sums over a team for n rows at once, the same in each of its lanes: LANES
 // of a wave, or W whole waves (first .. first + W - 1 of the workgroup). The
@@ -339,23 +339,6 @@ __global__ __launch_bounds__(1024) void norm_param_grad_kernel(NormGradArgs g, i
   }
 }
 
-// A row of n vectors (of `vec` elements): rows of up to 16 or 32 vectors share
-// a wave; else W waves of nv vectors a lane, nv vec <= 16, the pair that
-// leaves the fewest lanes idle (the fewest waves among those).
-struct Team {
-  int nv, waves, sub;
-};
-Team norm_team(int n, int vec, bool may_share) {
-  if (may_share && n <= 32) return Team{1, 1, n <= 16 ? 4 : 2};
-  Team best{0, 0, 1};
-  for (int nv = 16 / vec; nv >= 1; --nv) {
-    const int w = (n + 64 * nv - 1) / (64 * nv);
-    if (w <= kMaxWaves && (n + 64 * w - 1) / (64 * w) == nv && (best.nv == 0 || nv * w < best.nv * best.waves))
-      best = Team{nv, w, 1};
-  }
-  return best;
-}
-
 #define SVDQ_NORM_LAUNCH(KERNEL, ...)                                                 \
   if (t.sub == 4)                                                                     \
     hipLaunchKernelGGL((KERNEL(1, 4)), grid, block, lds, st, __VA_ARGS__);            \
@@ -379,7 +362,7 @@ Team norm_team(int n, int vec, bool may_share) {
 template <typename T, bool QUANT>
 hipError_t launch_fwd(const NormArgs& a, int num_cus, hipStream_t st) {
   const int span = QUANT ? a.Kp : a.C;
-  const Team t = norm_team((span + kVec<T> - 1) / kVec<T>, kVec<T>, !QUANT);
+  const NormTeam t = norm_team((span + kVec<T> - 1) / kVec<T>, kVec<T>, !QUANT);
   const int e = t.nv * kVec<T>, fit = e <= 12 ? 24 : kVec<T> == 8 ? 20 : 16;   // waves of a CU that its registers hold
   const int wg_waves = t.waves == 1 ? 4 : t.waves, wg_teams = t.waves == 1 ? 4 * t.sub : 1;
   const int64_t M = a.M, most = (int64_t)num_cus * (fit / wg_waves);
@@ -392,25 +375,21 @@ hipError_t launch_fwd(const NormArgs& a, int num_cus, hipStream_t st) {
 #undef SVDQ_FWD
 }
 
-// Waves of the backward's workgroups: sixteen, or twelve where a lane holds 16
-// elements, whose sums and values take 137 (fp32 167) registers of the 168
-// that twelve waves leave. Rows of more than twelve waves spill a few.
 constexpr int kNormLds = kMaxWaves * 64 * 16 * 2 * 4;   // a workgroup's teams' sums at most
 template <typename T, int NV>
-constexpr int kBwdWaves = NV * kVec<T> > 12 ? 12 : kMaxWaves;
+constexpr int kBwdWaves = norm_grad_waves(NV * kVec<T>);
 
 template <typename T>
 hipError_t launch_bwd(const NormGradArgs& g, const NormGradPlan& p, hipStream_t st) {
   constexpr int kWide = 16 / kVec<T>;
-  const Team t = norm_team((g.f.C + kVec<T> - 1) / kVec<T>, kVec<T>, true);
+  const NormTeam t = norm_team((g.f.C + kVec<T> - 1) / kVec<T>, kVec<T>, true);
   // a workgroup's teams: as many as have rows and fit
-  const int fit = t.nv == kWide ? kBwdWaves<T, kWide> : kMaxWaves;
   const int64_t useful = (p.rows_per_run + t.sub - 1) / t.sub;
-  const int wg_teams = (int)std::min<int64_t>(std::max(1, fit / t.waves), useful) * t.sub;
+  const int wg_teams = (int)std::min<int64_t>(norm_grad_teams(t, kVec<T>) / t.sub, useful) * t.sub;
   const int th = t.waves * 64 / t.sub;
   const dim3 grid((unsigned)((int64_t)g.f.G * p.runs)), block(th * wg_teams);
   const size_t lds = g.dw || g.db ? (size_t)wg_teams / t.sub * 2 * kVec<T> * t.nv * th * 4 : 0;
-  if (t.waves > fit) {
+  if (t.waves > norm_grad_waves(t.nv * kVec<T>)) {
     hipLaunchKernelGGL((norm_bwd_kernel<T, kWide, 1, kMaxWaves>), grid, block, lds, st, g, t.waves, p.runs);
     return hipGetLastError();
   }
