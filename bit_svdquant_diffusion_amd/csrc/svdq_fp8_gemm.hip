@@ -36,6 +36,9 @@ __device__ __forceinline__ void lds_transfer(__amdgpu_buffer_rsrc_t r, uint8_t* 
 __device__ __forceinline__ void store_16(__amdgpu_buffer_rsrc_t r, u32x4 v, int off) {
   __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
 }
+__device__ __forceinline__ void store_16_once(__amdgpu_buffer_rsrc_t r, u32x4 v, int off) {   // non-temporal
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 2);
+}
 constexpr int kRsrcWord3 = 0x00020000;   // buffer resources: raw bytes
 constexpr uint32_t kOutside = 0x7ffffff0u;   // a lane offset past the end of every resource: loads zero
 
@@ -122,6 +125,13 @@ __device__ __forceinline__ void ring_barrier() {
 // move LDS reads over transfers into LDS) and the scheduling groups place
 // them between the MFMAs. (Left to itself the compiler reuses the fragments'
 // registers and reads only when the multiplications are through.)
+//
+// Measured, with the quantizer's launch: 8192^3 428 us (2.57 PFLOP/s; a
+// library's product alone 390 to 425), 4608 tokens 3072 -> 12288 149 us (2.34)
+// with inputs that stay in the caches and 152 with inputs that rotate. The
+// matrix units are busy 52% of that: random codes draw so much power that an
+// MFMA loop alone reaches 3.4 to 3.9 of its 5 PFLOP/s, and a stage's 64 KB
+// come from L2s that miss for a third of it.
 template <int BM, int BN, int WGM, int WGN, bool BROW>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1)))
 void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
@@ -138,6 +148,11 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   const int Ra = (int)g.a_rows, Rb = g.b_rows, K = (int)g.K, KR = (K + 127) / 128, KB = max(KR, 3);
   const int lda = (int)g.lda, ldb = (int)g.ldb;
   const int ntiles = tiles_m * tiles_n, grid = (int)gridDim.x;
+  // Outputs of more than 64 MB are written past the caches, where they would
+  // push out the operands and not stay (4608 x 12288, 113 MB: 152 us against
+  // 162, with a GELU that reads them right after 212 against 210; 4608 x 6144,
+  // 57 MB: 80.0 against 79.5).
+  const bool once = (int64_t)Ra * Rb > (int64_t)32000000;
 
   // Transfers: a tile's rows of an operand as a buffer resource (rows past it
   // read as zeros); a lane's chunk of the even and the odd row octets.
@@ -375,8 +390,15 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
         for (int p = 0; p < 8; ++p) o[p] = cvt_bf16x2(acc[j][i][2 * p] + bv[2 * p], acc[j][i][2 * p + 1] + bv[2 * p + 1]);
         spread_rows(o);
         const int off = ((wm * TL::WM + 32 * i + (lr & 15)) * Rb + col + at_c) * 2;
-        store_16(out, u32x4{o[0], o[1], o[2], o[3]}, col + at_c < Rb ? off : nrec);
-        store_16(out, u32x4{o[4], o[5], o[6], o[7]}, col + at_c < Rb ? off + 32 * Rb : nrec);
+        const u32x4 v0 = u32x4{o[0], o[1], o[2], o[3]}, v1 = u32x4{o[4], o[5], o[6], o[7]};
+        const int off0 = col + at_c < Rb ? off : nrec, off1 = col + at_c < Rb ? off + 32 * Rb : nrec;
+        if (once) {
+          store_16_once(out, v0, off0);
+          store_16_once(out, v1, off1);
+        } else {
+          store_16(out, v0, off0);
+          store_16(out, v1, off1);
+        }
       }
     }
     if (!more) break;
