@@ -549,8 +549,8 @@ SVDQ_API svdq_status svdq_layer_norm_forward(const svdq_norm_desc* desc, const v
  *   d = dy g,  dx = rstd (d - sum_c d / C - xhat sum_c(d xhat) / C)
  *   dweight = sum over the group's rows of dy xhat, dbias = sum of dy,
  * [groups][channels] contiguous of type grad_dtype; either may be NULL. A group
- * without rows gets zeros. Sums in fp32 in an order fixed by M, groups and
- * rows_per_group alone. dx may be dy or x (with the same stride).
+ * without rows gets zeros. Sums in fp32 in an order fixed by the sizes and the
+ * type alone. dx may be dy or x (with the same stride).
  * workspace: >= svdq_layer_norm_backward_workspace_bytes device bytes, 16-byte
  * aligned, used when dweight or dbias is asked for; may be NULL where that is 0.
  * Errors: as the forward, SVDQ_ERR_WORKSPACE.
