@@ -286,8 +286,8 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   // Where some workgroups have one tile fewer they start about a third of a
   // tile later (a stage takes 1.6 us): then not all tiles' outputs go to
   // memory at the same time, whose 33 MB take longer than a stage (3.4 rounds
-  // at 4608 x 12288 outputs over 3072 channels, the whole call 166 us against
-  // 169; without any stores 148).
+  // at 4608 x 12288 outputs over 3072 channels, the whole call 159 us against
+  // 166; 2.5 rounds at 4608 x 9216 127 against 133).
   if (ntiles > grid && ntiles % grid != 0 && t_cur >= ntiles % grid)
     for (int i = 0; i < KB / 2; ++i) __builtin_amdgcn_s_sleep(32);   // 2048 cycles
   TileMap tm = map_tile(t_cur, tiles_m, tiles_n, group_m);
