@@ -307,7 +307,7 @@ struct NormGradPlan {
 };
 inline NormGradPlan norm_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
   const int64_t rows = rows_per_group < M ? rows_per_group : M;
-  const int64_t live = M > 0 ? (M + rows_per_group - 1) / rows_per_group : 1;   // groups that have rows
+  const int64_t live = M > 0 ? (M - 1) / rows_per_group + 1 : 1;   // groups that have rows (rows_per_group up to 2^63 - 1)
   const int vec = 16 / elem_bytes, teams = norm_grad_teams(norm_team((C + vec - 1) / vec, vec, true), vec);
   int64_t runs = kNormRuns / live;
   if (runs > (rows + 3) / 4) runs = (rows + 3) / 4;   // at least four rows each
