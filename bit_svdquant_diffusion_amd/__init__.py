@@ -899,28 +899,35 @@ def fp8_packed_bytes(K: int, N: int) -> dict:
 
 def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, stream=None) -> dict:
     """svdq_fp8_pack of a weight [N][K] (bfloat16, float16 or float32, on the
-    GPU): {"q", "s", "qt", "st", "bias"}, device tensors (qt and st, which the
-    gradient of x reads, are None without `transposed`). `out`: a dict of an
-    earlier call to overwrite, as after an update of w."""
+    GPU): {"q", "s", "qt", "st", "bias"}, device tensors of the layer's own (qt
+    and st, which the gradient of x reads, are None without `transposed`; bias
+    is a bfloat16 copy of `bias`, None without one). `out`: a dict of an earlier
+    call, whose tensors are overwritten, as after an update of w: its bias by
+    `bias`, which stays as it is without one. A call that is refused changes
+    nothing."""
     torch = _torch()
+    at = _on_device(w, bias)
     _need(w.dim() == 2 and w.is_contiguous(), "w: a contiguous matrix [N][K]")
     N, K = w.shape
+    _need(bias is None or bias.shape == (N,), "bias: [N]")
     sizes = fp8_packed_bytes(K, N)
     if out is None:
         def new(rows, name):
             return _empty((rows, sizes[name] // rows), torch.uint8, w, stream)
         out = {"q": new(N, "q"), "s": new(-(-N // 128), "s"), "qt": new(K, "qt") if transposed else None,
                "st": new(-(-K // 128), "st") if transposed else None, "bias": None}
-    if bias is not None:
-        _need(bias.shape == (N,), "bias: [N]")
-        if stream is None:
-            out["bias"] = bias.to(torch.bfloat16).contiguous()
-        else:
-            with _under(stream, w.device):   # a conversion belongs to the call's stream
-                out["bias"] = bias.to(torch.bfloat16).contiguous()
-    at = _on_device(w)
     d, p = _fp8_struct(K, N, out, at)
+    own = out.get("bias")
+    if bias is not None and own is None:
+        own = _empty((N,), torch.bfloat16, w, stream)
     _call("svdq_fp8_pack", at, stream, d, w.data_ptr(), _dt(w.dtype), p)
+    if bias is not None:
+        if stream is None:
+            own.copy_(bias.detach())
+        else:
+            with _under(stream, w.device):   # on the call's stream, as the codes
+                own.copy_(bias.detach())
+        out["bias"] = own
     return out
 
 
@@ -1052,7 +1059,8 @@ def fp8_quantize(x, stream=None):
 
 class Fp8Linear:
     """An FP8 linear in device memory: call it on bf16 input; `backward` gives
-    its gradients; `update` quantizes a new weight into the same buffers."""
+    its gradients; `update` quantizes a new weight (and copies a new bias) into
+    the same buffers, which captured graphs of the layer then read."""
 
     def __init__(self, w, bias=None, trainable: bool = True):
         self.N, self.K = w.shape
