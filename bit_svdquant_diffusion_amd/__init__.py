@@ -985,7 +985,8 @@ def _scratch(workspace, size: int, like, stream):
 
 
 def fp8_forward(K: int, N: int, dev: dict, x, y=None, workspace=None, stream=None):
-    """y[M][N] bf16 = FP8 layer(x[M][K] bf16) via svdq_fp8_forward."""
+    """y[M][N] bf16 = FP8 layer(x[M][K] bf16) via svdq_fp8_forward. y may be x
+    itself or overlap it except with a few tokens (fp8_workspace_bytes is 0)."""
     at = _on_device(x, y, workspace)
     _bf16_rows(x, K, "x")
     M = x.shape[0]

@@ -67,6 +67,10 @@ svdq_status check_fp8_m(const svdq_fp8_desc* d, int64_t M, int64_t most) {
   return M < 0 || M > most ? SVDQ_ERR_SHAPE : SVDQ_OK;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
 svdq_status check_fp8_dev(const svdq_fp8_packed* p) {
   if (!p || !p->q || !p->s) return SVDQ_ERR_NULL;
   return aligned(p->q, 16) && aligned(p->s, 16) && aligned(p->bias, 16) ? SVDQ_OK : SVDQ_ERR_SHAPE;
@@ -206,6 +210,8 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
   if (!aligned(x, 16) || !aligned(y, 16)) return SVDQ_ERR_SHAPE;
   const bool in_line = fp8_inline(M, d->K);
   const Fp8Ws L = fp8_ws(d, M);
+  // one kernel, whose workgroups read all of x while others write y
+  if (in_line && overlap(x, (size_t)M * d->K * 2, y, (size_t)M * d->N * 2)) return SVDQ_ERR_SHAPE;
   if (!in_line) {
     if (!ws) return SVDQ_ERR_NULL;
     if (!aligned(ws, 16)) return SVDQ_ERR_SHAPE;

@@ -625,6 +625,8 @@ SVDQ_API svdq_status svdq_fp8_pack(const svdq_fp8_desc* desc, const void* w, int
  * more take one that quantizes x into the workspace and one that multiplies.
  * workspace: >= svdq_fp8_workspace_bytes(desc, M) device bytes (may be NULL
  * where that is 0), contents ignored on entry.
+ * y may overlap x where a workspace is used; in the one kernel of a few tokens
+ * it must not (SVDQ_ERR_SHAPE).
  * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_WORKSPACE, SVDQ_ERR_DEVICE.
  */
 SVDQ_API svdq_status svdq_fp8_workspace_bytes(const svdq_fp8_desc* desc, int64_t M, size_t* out);
@@ -635,8 +637,8 @@ SVDQ_API svdq_status svdq_fp8_forward(const svdq_fp8_desc* desc, const svdq_fp8_
  * y = layer(bf16(layer norm(x))): svdq_layer_norm_forward followed by
  * svdq_fp8_forward, the same bits, but the norm's kernel emits the codes and
  * scales and its output never goes to memory. norm->channels == desc->K,
- * norm->dtype is bf16. mean and rstd fp32 [M] may be NULL. workspace: >=
- * svdq_fp8_norm_workspace_bytes(desc, M) device bytes.
+ * norm->dtype is bf16. mean and rstd fp32 [M] may be NULL. y may overlap x.
+ * workspace: >= svdq_fp8_norm_workspace_bytes(desc, M) device bytes.
  * Errors: as the two calls.
  */
 SVDQ_API svdq_status svdq_fp8_norm_workspace_bytes(const svdq_fp8_desc* desc, int64_t M, size_t* out);
@@ -651,7 +653,7 @@ SVDQ_API svdq_status svdq_fp8_norm_forward(const svdq_norm_desc* norm, const voi
  *   dw [N][K]      = q8(dy)^T q8(x), blocks along the tokens (reads x)
  *   db [N]         = the sum of dy over the tokens, in fp32 (no quantizing)
  * dw and db bf16, overwritten (M == 0: zeros). The order of every sum is fixed
- * by the shapes.
+ * by the shapes. Outputs may overlap x and dy, not one another.
  * workspace: >= svdq_fp8_backward_workspace_bytes(desc, M) device bytes.
  * Errors: SVDQ_ERR_NULL (x may be NULL without dw, qt and st without dx),
  * SVDQ_ERR_SHAPE, SVDQ_ERR_WORKSPACE, SVDQ_ERR_DEVICE.
