@@ -225,7 +225,7 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
     g.x = x;
     return after_launch(launch_fp8_gemm_small(g, cus, s), s);
   }
-  uint8_t* b = (uint8_t*)ws;
+  uint8_t* b = fp8_ws_start(ws);
   SVDQ_TRY(after_launch(launch_fp8_quant_rows(x, M, d->K, b + L.q, b + L.s, false, (uint32_t*)(b + L.tickets), s), s));
   g.a = b + L.q;
   g.as = b + L.s;
@@ -260,7 +260,7 @@ svdq_status svdq_fp8_norm_forward(const svdq_norm_desc* n, const void* weight, i
   int cus = 0;
   SVDQ_TRY(check_device(&cus));
   hipStream_t s = (hipStream_t)stream;
-  uint8_t* b = (uint8_t*)ws;
+  uint8_t* b = fp8_ws_start(ws);
   NormArgs a = norm_args(n, x, d->K, weight, ldw, bias, ldb, M);
   a.mean = mean;
   a.rstd = rstd;
@@ -308,7 +308,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     if (db) SVDQ_TRY(after_launch(launch_fp8_zero(db, (size_t)d->N * 2, cus, s), s));
     return SVDQ_OK;
   }
-  uint8_t* b = (uint8_t*)ws;
+  uint8_t* b = fp8_ws_start(ws);
   Fp8QuantT qy, qx;
   std::memset(&qy, 0, sizeof(qy));
   std::memset(&qx, 0, sizeof(qx));

@@ -669,7 +669,8 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
     // (2.8 us of host time) less. Each store has reached that point before the
     // ticket is taken (the wait), and no XCD can hold an older copy: a kernel
     // starts with nothing of this memory in its caches, a run's sums fill whole
-    // lines, and only the tile's last workgroup reads them.
+    // lines (the workspace is used from a multiple of 256 bytes on), and only
+    // the tile's last workgroup reads them.
     const int tile = t % (tiles_m * tiles_n);
     auto part = [&](int r, int q) {
       return reinterpret_cast<uint64_t*>(g.part) + ((size_t)((tile * runs + r) * 4 + wave) * 8 + q) * 64 + lane;

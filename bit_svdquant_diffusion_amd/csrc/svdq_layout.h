@@ -229,6 +229,11 @@ inline size_t fp8_deep_bytes(int64_t rows, int64_t cols, int64_t K) {
   return p.runs > 1 ? (size_t)p.runs * ((rows + 63) / 64) * ((cols + 63) / 64) * 64 * 64 * 4 : 0;
 }
 
+// The FP8 workspaces may start on any 16 bytes and are used from their first
+// multiple of 256 on, so that the sums of runs, which workgroups of different
+// XCDs exchange, share no cache line with anything else.
+constexpr size_t kFp8WsSlack = 256 - 16;
+inline uint8_t* fp8_ws_start(void* ws) { return (uint8_t*)(((uintptr_t)ws + 255) & ~(uintptr_t)255); }
 // Workspace of the FP8 forward: the activations' codes [M][round128(K)],
 // their scales, the tickets of tiles and the sums of their runs.
 struct Fp8Ws {
@@ -240,7 +245,7 @@ inline Fp8Ws fp8_ws(const svdq_fp8_desc* d, int64_t M) {
   w.s = align256((size_t)M * round128(d->K));
   w.tickets = w.s + align256(fp8_scale_bytes(M, d->K));
   w.part = w.tickets + kFp8Tickets * 4;
-  w.total = w.part + fp8_deep_bytes(M, d->N, d->K);
+  w.total = w.part + fp8_deep_bytes(M, d->N, d->K) + kFp8WsSlack;
   return w;
 }
 // Workspace of the backward: dY's codes along the output channels [M][round128(N)],
@@ -263,7 +268,7 @@ inline Fp8GradWs fp8_grad_ws(const svdq_fp8_desc* d, int64_t M) {
   w.tickets = w.db + align256((size_t)(mp / 128) * d->N * 4);
   w.part = w.tickets + 2 * kFp8Tickets * 4;
   const size_t px = fp8_deep_bytes(M, d->K, d->N), pw = fp8_deep_bytes(d->N, d->K, mp);
-  w.total = w.part + (px > pw ? px : pw);
+  w.total = w.part + (px > pw ? px : pw) + kFp8WsSlack;
   return w;
 }
 
