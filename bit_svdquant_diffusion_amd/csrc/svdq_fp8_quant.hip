@@ -32,8 +32,9 @@ __device__ __forceinline__ u32x4 load_input(const uint16_t* p, int once) {
 __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, uint32_t units, uint32_t chunks, int64_t M, int K,
                                                              int Kp, int plain, int once, uint8_t* q, uint8_t* s,
                                                              uint32_t* tickets) {
-  if (tickets && blockIdx.x == 0 && threadIdx.x < kFp8Tickets) tickets[threadIdx.x] = 0;
-  const uint32_t unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (tickets && block == 0 && threadIdx.x < kFp8Tickets) tickets[threadIdx.x] = 0;
+  const uint32_t unit = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (unit >= units) return;
   const uint32_t row = unit / chunks;
   const int lane = threadIdx.x & 63, at = (int)(unit - row * chunks) * 1024 + lane * 16;
@@ -247,8 +248,8 @@ hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q
                                  hipStream_t st) {
   const int Kp = (int)round128(K), chunks = (Kp + 1023) / 1024;
   const int64_t units = M * chunks;
-  const int64_t grid = (units + 3) / 4;
-  hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, (double)M * K * 2 >= kOnceBytes, q, s, tickets);
+  const dim3 grid = many_groups((units + 3) / 4);   // (at most 2^30 units)
+  hipLaunchKernelGGL(fp8_quant_rows_kernel, grid, dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, (double)M * K * 2 >= kOnceBytes, q, s, tickets);
   return hipGetLastError();
 }
 

@@ -191,6 +191,14 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st, const 
 hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st);
 hipError_t prepare_fp8();
 
+// A grid of at least n workgroups: a launch's dimension takes fewer than 2^32
+// threads, so from 2^20 workgroups on they lie in rows of so many (the last
+// row goes past n).
+inline dim3 many_groups(int64_t n) {
+  const int64_t row = (int64_t)1 << 20;
+  return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
+}
+
 // shared by the files with C entry points (svdq_api.hip)
 svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr);
 svdq_status after_launch(hipError_t e, hipStream_t s);
