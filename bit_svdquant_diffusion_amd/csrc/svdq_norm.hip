@@ -197,8 +197,10 @@ __global__ __launch_bounds__(64 * MAXW) void norm_bwd_kernel(NormGradArgs g, int
   const int lane = threadIdx.x & 63, wg_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int TH = LANES * W, teams = (int)blockDim.x / TH;
   const int team = SUB == 1 ? wg_wave / W : (int)threadIdx.x / LANES, tid = (int)threadIdx.x - team * TH;
-  const int64_t group = blockIdx.x / (uint32_t)runs;
-  const int run = (int)(blockIdx.x % (uint32_t)runs), C = a.C;
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (block >= (uint32_t)a.G * (uint32_t)runs) return;
+  const int64_t group = block / (uint32_t)runs;
+  const int run = (int)(block % (uint32_t)runs), C = a.C;
   // the group's rows in `runs` parts as even as they can be
   const int64_t g_begin = min(group * a.rpg, a.M), g_rows = min(a.rpg, a.M - g_begin);
   const int per = (int)((uint32_t)g_rows / (uint32_t)runs), extra = (int)((uint32_t)g_rows % (uint32_t)runs);
@@ -307,7 +309,7 @@ __global__ __launch_bounds__(64 * MAXW) void norm_bwd_kernel(NormGradArgs g, int
       for (int i = 0; i < VEC; ++i) v[i] += p[i * NV * TH];
     }
     if (g.part) {
-      store_params<VEC>(g.part, SVDQ_DT_F32, ((int64_t)blockIdx.x * 2 + second) * C + at, len, v);
+      store_params<VEC>(g.part, SVDQ_DT_F32, ((int64_t)block * 2 + second) * C + at, len, v);
     } else {
       void* o = second ? g.db : g.dw;
       if (o) store_params<VEC>(o, g.gdtype, group * C + at, len, v);
@@ -388,7 +390,7 @@ hipError_t launch_bwd(const NormGradArgs& g, const NormGradPlan& p, hipStream_t 
   const int64_t useful = (p.rows_per_run + t.sub - 1) / t.sub;
   const int wg_teams = (int)std::min<int64_t>(norm_grad_teams(t, kVec<T>) / t.sub, useful) * t.sub;
   const int th = t.waves * 64 / t.sub;
-  const dim3 grid((unsigned)((int64_t)g.f.G * p.runs)), block(th * wg_teams);
+  const dim3 grid = many_groups((int64_t)g.f.G * p.runs), block(th * wg_teams);
   const size_t lds = g.dw || g.db ? (size_t)wg_teams / t.sub * 2 * kVec<T> * t.nv * th * 4 : 0;
   if (t.waves > norm_grad_waves(t.nv * kVec<T>)) {
     hipLaunchKernelGGL((norm_bwd_kernel<T, kWide, 1, kMaxWaves>), grid, block, lds, st, g, t.waves, p.runs);
