@@ -176,7 +176,10 @@ __global__ __launch_bounds__(256) void fp8_zero_kernel(uint32_t* p, size_t n) {
 
 // A weight matrix [N][K]: one scale per 128 x 128 block, codes [N][K] and,
 // for the input's gradient, transposed [K][N] with the scales transposed. One
-// workgroup a block; a thread holds four output rows of 16 channels.
+// workgroup a block; a thread holds four output rows of 16 channels. The
+// largest finite value gives the scale: infinities and NaN are the NaN code
+// under any, and the block's other channels keep their values. (A token's
+// block needs no such care, as all of its row's sums are NaN.)
 template <typename T>
 __global__ __launch_bounds__(256) void fp8_pack_kernel(const T* w, int K, int N, uint8_t* q, uint8_t* s, uint8_t* qt,
                                                        uint8_t* st) {
@@ -197,7 +200,8 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const T* w, int K, int N,
 #pragma unroll
       for (int t = 0; t < kVec<T>; ++t) {
         v[p][i + t] = in.at(t);
-        amax = umax(amax, __float_as_uint(v[p][i + t]) & 0x7fffffffu);
+        const uint32_t mag = __float_as_uint(v[p][i + t]) & 0x7fffffffu;
+        amax = umax(amax, mag < 0x7f800000u ? mag : 0u);
       }
     }
   }

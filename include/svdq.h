@@ -574,7 +574,7 @@ SVDQ_API svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const 
  * e + 127 (E8M0). An infinity or a NaN has the NaN code, which makes every sum
  * it enters NaN. A power of two keeps the quotient exact, and CDNA4's
  * block-scaled MFMA applies the scales itself. W has one scale per 128 x 128
- * block; x is quantized in the call, per row and 128 channels. Sums are the
+ * block, from its largest finite value; x is quantized in the call, per row and 128 channels. Sums are the
  * matrix unit's fp32 sums. Last blocks may be short.
  * Shapes: K % 16 == 0, N % 16 == 0, K, N <= 65536; 0 <= M <= 2^24 (forward),
  * 2^20 (backward). Device pointers 16-byte aligned.

@@ -102,3 +102,37 @@ def test_captured_update_of_weight_and_bias(dtype):
         torch.cuda.synchronize()
         kept = y.clone()
         assert torch.equal(kept, S.Fp8Linear(w, b)(x)) and torch.equal(kept, lin(x)), k
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_infinities_and_nan_of_a_weight_stay_in_their_channel(dtype):
+    """A weight that is not finite becomes the NaN code; the other values of
+    its 128 x 128 block keep the codes of a block without it (they would all
+    be zeros under a scale for infinity), so other channels keep their outputs."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    K, N = 272, 400
+    w = (torch.randn(N, K, device="cuda", generator=g) / 16).to(dtype)
+    bad = [(3, 5, float("inf")), (140, 130, float("nan")), (399, 271, float("-inf"))]
+    clean = w.clone()
+    for n, k, v in bad:
+        w[n, k], clean[n, k] = v, 0
+    a, b = S.fp8_pack(w), S.fp8_pack(clean)
+    assert torch.equal(a["s"], b["s"]) and torch.equal(a["st"], b["st"])
+    for n, k, _ in bad:
+        assert int(a["q"][n, k]) & 0x7F == 0x7F and int(a["qt"][k, n]) & 0x7F == 0x7F
+        a["q"][n, k] = a["qt"][k, n] = 0
+    assert torch.equal(a["q"], b["q"]) and torch.equal(a["qt"], b["qt"])
+    for M in (3, 70):
+        x = _bf16(g, M, K)
+        y, want = S.Fp8Linear(w)(x), S.Fp8Linear(clean)(x)
+        rows = torch.zeros(N, dtype=torch.bool, device="cuda")
+        rows[[n for n, _, _ in bad]] = True
+        assert bool(y[:, rows].isnan().all()) and torch.equal(y[:, ~rows], want[:, ~rows]), M
+
+
+def test_a_weight_block_without_a_finite_value():
+    w = torch.full((128, 256), float("nan"), device="cuda")
+    w[:, 128:] = 1
+    dev = S.fp8_pack(w)
+    assert bool((dev["q"][:, :128] & 0x7F == 0x7F).all()) and dev["s"][0, :2].tolist() == [1, 127 - 8]
+    assert bool((dev["q"][:, 128:].view(torch.float8_e4m3fn).float() == 256).all())
