@@ -933,37 +933,40 @@ def fp8_pack(w, bias=None, transposed: bool = True, out: dict | None = None, str
 
 @functools.lru_cache(maxsize=1024)
 def _fp8_desc(K: int, N: int):
-    """(descriptor reference, itself, bytes of q and qt, s, st, bias)"""
+    """(descriptor reference, itself, shapes of q, s, qt, st)"""
     d, rk, rn = Fp8Desc(K, N), (K + 127) // 128, (N + 127) // 128
-    return ctypes.byref(d), d, N * K, rn * ((rk + 3) // 4 * 4), rk * ((rn + 3) // 4 * 4), 2 * N
+    return (ctypes.byref(d), d, (N, K), (rn, (rk + 3) // 4 * 4), (K, N), (rk, (rn + 3) // 4 * 4))
 
 
-def _fp8_buffer(t, least: int, name: str):
-    """The address of a layer's buffer of at least `least` bytes."""
+def _fp8_buffer(t, shape: tuple, name: str, at: int):
+    """The address of a layer's buffer of bytes on GPU `at`: of this shape, or,
+    as plain bytes, of at least as many."""
     if t is None:
         return None
-    if t.nbytes < least or not t.is_contiguous():
-        raise ValueError(f"fp8 layer: {name} must be contiguous with {least} bytes")
+    if (t.shape != shape and (t.dim() != 1 or t.shape[0] < shape[0] * shape[1])) or t.element_size() != 1 or \
+            not t.is_contiguous():
+        raise ValueError(f"fp8 layer: {name} must be contiguous bytes {list(shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"tensors on GPU {at} and on {t.device}")
     return t.data_ptr()
 
 
 def _fp8_struct(K: int, N: int, dev: dict, at: int = -1, forward: bool = True, backward: bool = True):
     """(reference to the descriptor, reference to the buffers) of a layer on
     GPU `at`: those that the forward or the backward read, or all."""
-    ref, _, nq, ns, nst, nb = _fp8_desc(K, N)
+    ref, _, nq, ns, nqt, nst = _fp8_desc(K, N)
     p = Fp8Packed()
     if forward:
-        q, s, bias = dev.get("q"), dev.get("s"), dev.get("bias")
-        p.q, p.s = _fp8_buffer(q, nq, "q"), _fp8_buffer(s, ns, "s")
+        p.q, p.s = _fp8_buffer(dev.get("q"), nq, "q", at), _fp8_buffer(dev.get("s"), ns, "s", at)
+        bias = dev.get("bias")
         if bias is not None:
-            if bias.dtype != _torch().bfloat16:
-                raise ValueError("fp8 layer: bias must be bfloat16")
-            p.bias = _fp8_buffer(bias, nb, "bias")
-        _same_device(at, q, s, bias)
+            if bias.dtype != _torch().bfloat16 or bias.numel() != N or not bias.is_contiguous():
+                raise ValueError(f"fp8 layer: bias must be contiguous bfloat16 [{N}]")
+            if bias.get_device() != at:
+                raise ValueError(f"tensors on GPU {at} and on {bias.device}")
+            p.bias = bias.data_ptr()
     if backward:
-        qt, st = dev.get("qt"), dev.get("st")
-        p.qt, p.st = _fp8_buffer(qt, nq, "qt"), _fp8_buffer(st, nst, "st")
-        _same_device(at, qt, st)
+        p.qt, p.st = _fp8_buffer(dev.get("qt"), nqt, "qt", at), _fp8_buffer(dev.get("st"), nst, "st", at)
     return ref, ctypes.byref(p)
 
 
