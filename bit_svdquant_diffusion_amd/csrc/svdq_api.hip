@@ -26,13 +26,15 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];   // 0 unknown, 1 gfx950 ready, 2 unsupported
 std::atomic<int> g_dev_cus[kMaxDevices];     // compute units of each ready device
 std::atomic<void*> g_dev_scratch[kMaxDevices];   // device address of `scratch` on each ready device
+std::atomic<unsigned> g_dev_kernels[kMaxDevices];   // KernelSets that are ready on each ready device
 std::mutex g_dev_mu;
 
 }  // namespace
 
 // One-time set-up per device, with that device current: the gfx950 check,
-// the kernels' LDS attributes and the address of this device's `scratch`.
-svdq_status check_device(int* cus, void** scratch_ptr) {
+// the kernels' LDS attributes and the address of this device's `scratch`. A
+// kernel set whose set-up fails stops the calls that name it alone.
+svdq_status check_device(int* cus, void** scratch_ptr, unsigned kernels) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return SVDQ_ERR_DEVICE;
   int s = g_dev_state[dev].load(std::memory_order_acquire);
@@ -45,17 +47,20 @@ svdq_status check_device(int* cus, void** scratch_ptr) {
       bool ok = hipGetDeviceProperties(&p, dev) == hipSuccess &&
                 std::strncmp(p.gcnArchName, "gfx950", 6) == 0 && prepare_gemm_mxfp4() == hipSuccess &&
                 prepare_gemm_int4() == hipSuccess && prepare_stage1() == hipSuccess && prepare_awq() == hipSuccess &&
-                prepare_fp8() == hipSuccess && prepare_norm() == hipSuccess &&
                 hipGetSymbolAddress(&sp, HIP_SYMBOL(scratch)) == hipSuccess && sp != nullptr;
       s = ok ? 1 : 2;
       if (ok) {
+        const unsigned sets =
+            (prepare_norm() == hipSuccess ? kKernelsNorm : 0) | (prepare_fp8() == hipSuccess ? kKernelsFp8 : 0);
+        if (sets != (kKernelsNorm | kKernelsFp8)) (void)hipGetLastError();   // not the next launch's error
+        g_dev_kernels[dev].store(sets, std::memory_order_relaxed);
         g_dev_cus[dev].store(p.multiProcessorCount, std::memory_order_relaxed);
         g_dev_scratch[dev].store(sp, std::memory_order_relaxed);
       }
       g_dev_state[dev].store(s, std::memory_order_release);
     }
   }
-  if (s != 1) return SVDQ_ERR_DEVICE;
+  if (s != 1 || (kernels & ~g_dev_kernels[dev].load(std::memory_order_relaxed))) return SVDQ_ERR_DEVICE;
   if (cus) *cus = g_dev_cus[dev].load(std::memory_order_relaxed);
   if (scratch_ptr) *scratch_ptr = g_dev_scratch[dev].load(std::memory_order_relaxed);
   return SVDQ_OK;

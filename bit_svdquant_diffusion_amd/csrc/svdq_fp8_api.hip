@@ -115,7 +115,7 @@ svdq_status svdq_layer_norm_forward(const svdq_norm_desc* d, const void* x, int6
   SVDQ_TRY(check_params(d, bias, ldb));
   if (!aligned(mean, 4) || !aligned(rstd, 4)) return SVDQ_ERR_SHAPE;
   int cus = 0;
-  SVDQ_TRY(check_device(&cus));
+  SVDQ_TRY(check_device(&cus, nullptr, kKernelsNorm));
   NormArgs a = norm_args(d, x, ldx, weight, ldw, bias, ldb, M);
   a.y = y;
   a.ldy = ldy;
@@ -155,7 +155,7 @@ svdq_status svdq_layer_norm_backward(const svdq_norm_desc* d, const void* dy, in
     if (!aligned(ws, 16)) return SVDQ_ERR_SHAPE;
     if (ws_bytes < need) return SVDQ_ERR_WORKSPACE;
   }
-  SVDQ_TRY(check_device());
+  SVDQ_TRY(check_device(nullptr, nullptr, kKernelsNorm));
   NormGradArgs g;
   std::memset(&g, 0, sizeof(g));
   g.f = norm_args(d, x, ldx, weight, ldw, nullptr, 0, M);
@@ -189,7 +189,7 @@ svdq_status svdq_fp8_pack(const svdq_fp8_desc* d, const void* w, int32_t dtype, 
   if (!w || !o || !o->q || !o->s || !o->qt != !o->st) return SVDQ_ERR_NULL;
   if (!aligned(w, 16) || !aligned(o->q, 16) || !aligned(o->s, 16) || !aligned(o->qt, 16) || !aligned(o->st, 16))
     return SVDQ_ERR_SHAPE;
-  SVDQ_TRY(check_device());
+  SVDQ_TRY(check_device(nullptr, nullptr, kKernelsFp8));
   hipStream_t s = (hipStream_t)stream;
   return after_launch(launch_fp8_pack(w, dtype, d->K, d->N, o->q, o->s, o->qt, o->st, s), s);
 }
@@ -218,7 +218,7 @@ svdq_status svdq_fp8_forward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev,
     if (ws_bytes < L.total) return SVDQ_ERR_WORKSPACE;
   }
   int cus = 0;
-  SVDQ_TRY(check_device(&cus));
+  SVDQ_TRY(check_device(&cus, nullptr, kKernelsFp8));
   hipStream_t s = (hipStream_t)stream;
   Fp8Gemm g = forward_gemm(d, dev, M, y);
   if (in_line) {
@@ -258,7 +258,7 @@ svdq_status svdq_fp8_norm_forward(const svdq_norm_desc* n, const void* weight, i
   const Fp8Ws L = fp8_ws(d, M);
   if (ws_bytes < L.total) return SVDQ_ERR_WORKSPACE;
   int cus = 0;
-  SVDQ_TRY(check_device(&cus));
+  SVDQ_TRY(check_device(&cus, nullptr, kKernelsNorm | kKernelsFp8));
   hipStream_t s = (hipStream_t)stream;
   uint8_t* b = fp8_ws_start(ws);
   NormArgs a = norm_args(n, x, d->K, weight, ldw, bias, ldb, M);
@@ -301,7 +301,7 @@ svdq_status svdq_fp8_backward(const svdq_fp8_desc* d, const svdq_fp8_packed* dev
     if (ws_bytes < L.total) return SVDQ_ERR_WORKSPACE;
   }
   int cus = 0;
-  SVDQ_TRY(check_device(&cus));
+  SVDQ_TRY(check_device(&cus, nullptr, kKernelsFp8));
   hipStream_t s = (hipStream_t)stream;
   if (M == 0) {
     if (dw) SVDQ_TRY(after_launch(launch_fp8_zero(dw, (size_t)d->N * d->K * 2, cus, s), s));
@@ -377,7 +377,7 @@ svdq_status svdq_fp8_quantize(const uint16_t* x, int64_t M, int32_t K, uint8_t* 
   if (M == 0) return SVDQ_OK;
   if (!x || !codes || !scales) return SVDQ_ERR_NULL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return SVDQ_ERR_SHAPE;
-  SVDQ_TRY(check_device());
+  SVDQ_TRY(check_device(nullptr, nullptr, kKernelsFp8));
   hipStream_t s = (hipStream_t)stream;
   return after_launch(launch_fp8_quant_rows(x, M, K, codes, scales, true, nullptr, s), s);
 }

@@ -200,7 +200,8 @@ inline dim3 many_groups(int64_t n) {
 }
 
 // shared by the files with C entry points (svdq_api.hip)
-svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr);
+enum KernelSets : unsigned { kKernelsNorm = 1, kKernelsFp8 = 2 };
+svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr, unsigned kernels = 0);
 svdq_status after_launch(hipError_t e, hipStream_t s);
 
 // measured ceilings of the part (not part of the layer): an MFMA-only loop

@@ -30,6 +30,7 @@ std::map<const void*, std::string> g_kernels;
 std::vector<Launch> g_launches;
 std::vector<Config> g_configs;
 std::string g_refused;
+hipError_t g_last = hipSuccess;   // what hipGetLastError gives next
 alignas(256) char g_symbol[256];
 
 bool fits(dim3 g, dim3 b) {
@@ -65,7 +66,6 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
   *stream = c.stream;
   return hipSuccess;
 }
-static hipError_t g_last = hipSuccess;
 hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, size_t lds, hipStream_t) {
   Launch l;
   l.kernel = g_kernels[f];
@@ -93,7 +93,8 @@ hipError_t hipGetDevicePropertiesR0600(hipDeviceProp_tR0600* p, int) {
   return hipSuccess;
 }
 hipError_t hipFuncSetAttribute(const void* f, hipFuncAttribute, int) {
-  return !g_refused.empty() && g_kernels[f].find(g_refused) != std::string::npos ? hipErrorInvalidValue : hipSuccess;
+  if (g_refused.empty() || g_kernels[f].find(g_refused) == std::string::npos) return hipSuccess;
+  return g_last = hipErrorInvalidValue;
 }
 hipError_t hipGetSymbolAddress(void** p, const void*) {
   *p = g_symbol;
