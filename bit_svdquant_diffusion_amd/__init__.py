@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 from dataclasses import dataclass
 
 import numpy as np
@@ -639,7 +640,9 @@ class SVDQLinear:
 
 
 # ----------------------------------------------------------------------------
-# Layer norm and the FP8 linear, forward and backward
+# Layer norm and the FP8 linear, forward and backward. The gradients are calls
+# of their own: no call records an autograd graph, and one whose input requires
+# grad (in grad mode) warns that its outputs do not.
 # ----------------------------------------------------------------------------
 _t = None         # torch, imported on first use
 _DT_CODES = {}    # svdq_dtype of the torch dtypes
@@ -689,6 +692,14 @@ def _same_device(at: int, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != at:
             raise ValueError(f"tensors on GPU {at} and on {t.device}")
+
+
+def _no_graph(name: str):
+    """Tells a caller who differentiates with torch that the outputs of a call
+    with an input that requires grad are outside of its graph."""
+    if _torch().is_grad_enabled():
+        warnings.warn(f"{name} records no autograd graph, and an input requires grad: its outputs do not. Call it in a "
+                      "torch.autograd.Function with the matching backward call, or under torch.no_grad()", stacklevel=3)
 
 
 def _empty(shape, dtype, like, stream):
@@ -822,6 +833,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-6, one_plus: b
     (default: the rows split evenly); the gain is weight, or 1 + weight with
     one_plus. mean and rstd are float32 [M], for layer_norm_backward."""
     at = _on_device(x, weight, bias, y)
+    if x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad):
+        _no_graph("layer_norm_forward")
     xp, ldx = _rows(x, "x")
     M, C = x.shape
     d, _, wp, ldw, bp, ldb = _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
@@ -843,6 +856,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, one_plus: bool = False, 
     [groups][C] ([C] for a [C] or absent weight) of grad_dtype (default: the
     weight's type, float32 without one); None without param_grads."""
     at = _on_device(x, dy, mean, rstd, weight, dx)
+    if dy.requires_grad:
+        _no_graph("layer_norm_backward")
     M, C = x.shape
     _need(dy.shape == x.shape and dy.dtype == x.dtype, "dy: the shape and type of x")
     f32 = _torch().float32
@@ -991,6 +1006,8 @@ def fp8_forward(K: int, N: int, dev: dict, x, y=None, workspace=None, stream=Non
     """y[M][N] bf16 = FP8 layer(x[M][K] bf16) via svdq_fp8_forward. y may be x
     itself or overlap it except with a few tokens (fp8_workspace_bytes is 0)."""
     at = _on_device(x, y, workspace)
+    if x.requires_grad:
+        _no_graph("fp8_forward")
     _bf16_rows(x, K, "x")
     M = x.shape[0]
     if y is None:
@@ -1010,6 +1027,8 @@ def fp8_norm_forward(K: int, N: int, dev: dict, x, weight=None, bias=None, eps: 
     parameters as in layer_norm_forward (`bias` is the norm's; the layer's own
     is in dev). With stats: (y, mean, rstd)."""
     at = _on_device(x, weight, bias, y, workspace)
+    if x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad):
+        _no_graph("fp8_norm_forward")
     _bf16_rows(x, K, "x")
     M = x.shape[0]
     d, _, wp, ldw, bp, ldb = _norm_params(K, weight, bias, one_plus, eps, rows_per_group, M, x.dtype)
@@ -1033,6 +1052,8 @@ def fp8_backward(K: int, N: int, dev: dict, x, dy, need=(True, True, True), work
     for dy [M][N] bf16; None where `need` says no. Without dx, dev may lack qt
     and st; without dw, x may be None."""
     at = _on_device(dy, x, workspace)
+    if dy.requires_grad:
+        _no_graph("fp8_backward")
     _bf16_rows(dy, N, "dy")
     M = dy.shape[0]
     if x is not None:
