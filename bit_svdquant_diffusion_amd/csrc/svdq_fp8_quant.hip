@@ -15,23 +15,12 @@ namespace svdq {
 
 namespace {
 
-// Inputs of 16 MB and more are read past the caches (non-temporal), which
-// keeps the codes in them for the product (4608 tokens, 3072 -> 12288, calls
-// that rotate through more than the caches hold: 167 us against 175; 1003
-// tokens of 2064 channels 16.0 us with plain loads, 16.2 without).
-constexpr double kOnceBytes = 16e6;
-__device__ __forceinline__ u32x4 load_input(const uint16_t* p, int once) {
-  const u32x4* v = reinterpret_cast<const u32x4*>(p);
-  return once ? __builtin_nontemporal_load(v) : *v;
-}
-
 // Blocks along the rows: eight lanes a block, 16 channels (32 bytes) a lane; a
 // wave takes 1024 channels of a row (two rows' took 0.5 us longer for 1003
 // rows). `plain` scales: [blocks / 4][M][4]. Channels in [K, Kp) get zero
 // codes (K % 16 == 0: whole lanes).
 __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, uint32_t units, uint32_t chunks, int64_t M, int K,
-                                                             int Kp, int plain, int once, uint8_t* q, uint8_t* s,
-                                                             uint32_t* tickets) {
+                                                             int Kp, int plain, uint8_t* q, uint8_t* s, uint32_t* tickets) {
   const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
   if (tickets && block == 0 && threadIdx.x < kFp8Tickets) tickets[threadIdx.x] = 0;
   const uint32_t unit = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -41,8 +30,8 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, 
   u32x4 v0 = u32x4{0, 0, 0, 0}, v1 = v0;
   if (at < K) {
     const uint16_t* p = x + (size_t)row * K + at;
-    v0 = load_input(p, once);
-    v1 = load_input(p + 8, once);
+    v0 = *reinterpret_cast<const u32x4*>(p);
+    v1 = *reinterpret_cast<const u32x4*>(p + 8);
   }
   uint32_t amax = 0;
 #pragma unroll
@@ -73,7 +62,7 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, 
 // from the caches); 777 of 1552 and 2064 9.8 us, of which 4.5 go when the two
 // kinds of codes are not stored and 3.2 are the launch and the loads.
 constexpr int kTLd = 33;   // words of a transposed row in LDS (32 and one against bank conflicts)
-__global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a, int once,
+__global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a,
                                                           uint32_t* tickets) {
   if (blockIdx.x == 0 && threadIdx.x < 2 * kFp8Tickets) tickets[threadIdx.x] = 0;
   __shared__ uint32_t lds[2 * 32 * 128];   // maxima and sums [32][128] each, then codes [128][kTLd]
@@ -91,7 +80,7 @@ __global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8Quant
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     v[p] = u32x4{0, 0, 0, 0};
-    if (m0 + p < M && c < t.C) v[p] = load_input(t.x + (m0 + p) * t.C + c, once);
+    if (m0 + p < M && c < t.C) v[p] = *reinterpret_cast<const u32x4*>(t.x + (m0 + p) * t.C + c);
   }
   // value of token p, channel i of this thread
   auto val = [&](int p, int i) { return (i & 1) ? bf16hi(v[p][i >> 1]) : bf16lo(v[p][i >> 1]); };
@@ -253,7 +242,8 @@ hipError_t launch_fp8_quant_rows(const uint16_t* x, int64_t M, int K, uint8_t* q
   const int Kp = (int)round128(K), chunks = (Kp + 1023) / 1024;
   const int64_t units = M * chunks;
   const dim3 grid = many_groups((units + 3) / 4);   // (at most 2^30 units)
-  hipLaunchKernelGGL(fp8_quant_rows_kernel, grid, dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0, (double)M * K * 2 >= kOnceBytes, q, s, tickets);
+  hipLaunchKernelGGL(fp8_quant_rows_kernel, grid, dim3(256), 0, st, x, (uint32_t)units, (uint32_t)chunks, M, K, Kp, plain ? 1 : 0,
+                     q, s, tickets);
   return hipGetLastError();
 }
 
@@ -261,8 +251,7 @@ hipError_t launch_fp8_quant_t(const Fp8QuantT& a, const Fp8QuantT& b, int64_t M,
   const int64_t rows = (M + 127) / 128;
   const int64_t na = a.x ? rows * ((a.C + 127) / 128) : 0, nb = b.x ? rows * ((b.C + 127) / 128) : 0;
   if (na + nb == 0) return hipSuccess;
-  hipLaunchKernelGGL(fp8_quant_t_kernel, dim3((unsigned)(na + nb)), dim3(512), 0, st, a, b, M, na,
-                     (double)M * ((a.x ? a.C : 0) + (b.x ? b.C : 0)) * 2 >= kOnceBytes, tickets);
+  hipLaunchKernelGGL(fp8_quant_t_kernel, dim3((unsigned)(na + nb)), dim3(512), 0, st, a, b, M, na, tickets);
   return hipGetLastError();
 }
 

@@ -13,6 +13,6 @@ TOKENS = {4: 450, 5: 600, 6: 768, 7: 777}       # blocks: tokens of a weight gra
 FORWARD = [(tile, blocks, m, CONTRACTED[blocks], n) for tile, (m, n) in OUTPUTS.items() for blocks in CONTRACTED]
 BACKWARD = [(tile, blocks, TOKENS[blocks], k, n) for tile, (n, k) in GRADIENTS.items() for blocks in TOKENS]
 
-# inputs read past the caches: the quantizers' from 16 MB, the layer norm's gradients' from 128 MB of x, dy and dx
+# large inputs: more than 16 MB to quantize; more than 128 MB of x, dy and dx, which the norm's gradients read past the caches
 QUANTIZED = [(4099, 2064), (9001, 912)]                    # rows, channels
 NORM_GRADIENTS = [(10600, 2051, "bf16"), (8600, 1283, "fp32"), (3700, 6001, "fp16")]

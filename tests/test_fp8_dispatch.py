@@ -46,7 +46,7 @@ def test_gradient_tiles(tile):
 
 
 def test_large_inputs_and_outputs():
-    """(the thresholds themselves, as no launch shows them)"""
+    """(sizes, as no launch shows how memory is read)"""
     assert all(M * K * 2 >= 16e6 for M, K in C.QUANTIZED)
     assert any(M * (K + N) * 2 >= 16e6 for _, _, M, K, N in C.BACKWARD) and any(M * (K + N) * 2 < 16e6 for _, _, M, K, N in C.BACKWARD)
     assert all(M * c * 3 * (4 if t == "fp32" else 2) > 128e6 for M, c, t in C.NORM_GRADIENTS)
