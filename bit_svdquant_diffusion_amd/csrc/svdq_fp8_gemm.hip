@@ -126,10 +126,10 @@ __device__ __forceinline__ void ring_barrier() {
 // them between the MFMAs. (Left to itself the compiler reuses the fragments'
 // registers and reads only when the multiplications are through.)
 //
-// Measured, with the quantizer's launch: 8192^3 428 us (2.57 PFLOP/s; a
-// library's product alone 390 to 425), 4608 tokens 3072 -> 12288 149 us (2.34)
-// with inputs that stay in the caches and 152 with inputs that rotate. The
-// matrix units are busy 52% of that: random codes draw so much power that an
+// Measured, with the quantizer's launch: 8192^3 397 us (2.77 PFLOP/s; a
+// library's product alone 390 to 425) with inputs that stay in the caches and
+// 425 with three sets in turn, 4608 tokens 3072 -> 12288 150 us (2.32) with
+// either. The matrix units are busy 52% of that: random codes draw so much power that an
 // MFMA loop alone reaches 3.4 to 3.9 of its 5 PFLOP/s, and a stage's 64 KB
 // come from L2s that miss for a third of it.
 template <int BM, int BN, int WGM, int WGN, bool BROW>
@@ -149,13 +149,16 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   const int lda = (int)g.lda, ldb = (int)g.ldb;
   const int ntiles = tiles_m * tiles_n, grid = (int)gridDim.x;
   // Outputs of more than 64 MB are written past the caches, where they would
-  // push out the operands and not stay (4608 x 12288, 113 MB: 152 us against
-  // 162, with a GELU that reads them right after 212 against 210; 4608 x 6144,
-  // 57 MB: 80.0 against 79.5).
+  // push out the operands and not stay (4608 x 12288, 113 MB: 150 us against
+  // 159, with a GELU that reads them right after 217 either way; 8192 x 8192,
+  // 134 MB: 428 against 436; 4608 x 6144, 57 MB: 80.5 against 83.4, so the
+  // border could lie lower, were a reader never next).
   const bool once = (int64_t)Ra * Rb > (int64_t)32000000;
 
   // Transfers: a tile's rows of an operand as a buffer resource (rows past it
-  // read as zeros); a lane's chunk of the even and the odd row octets.
+  // read as zeros: gfx950 checks the lane's and the scalar offset together
+  // against the resource's size); a lane's chunk of the even and the odd row
+  // octets.
   const int ck[2] = {(lane & 7) ^ (lane >> 4), (lane & 7) ^ (4 + (lane >> 4))};
   uint32_t va[2], vb[2];
 #pragma unroll
@@ -286,8 +289,8 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
   // Where some workgroups have one tile fewer they start about a third of a
   // tile later (a stage takes 1.6 us): then not all tiles' outputs go to
   // memory at the same time, whose 33 MB take longer than a stage (3.4 rounds
-  // at 4608 x 12288 outputs over 3072 channels, the whole call 159 us against
-  // 166; 2.5 rounds at 4608 x 9216 127 against 133).
+  // at 4608 x 12288 outputs over 3072 channels, the whole call 149 us against
+  // 161; 2.5 rounds at 4608 x 9216 114 against 121).
   if (ntiles > grid && ntiles % grid != 0 && t_cur >= ntiles % grid)
     for (int i = 0; i < KB / 2; ++i) __builtin_amdgcn_s_sleep(32);   // 2048 cycles
   TileMap tm = map_tile(t_cur, tiles_m, tiles_n, group_m);
@@ -349,8 +352,8 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
     SVDQ_SCALE_ROWS(m_next, n_next)   // (without a next tile this tile's again)
     SVDQ_SCALES(0)
     // All bias words before the first store: vector memory completes in order,
-    // so the wait for a later load is a wait for the stores before it (170 us
-    // against 165 at 4608 x 12288 outputs over 3072 channels).
+    // so the wait for a later load is a wait for the stores before it (151 us
+    // against 149 at 4608 x 12288 outputs over 3072 channels).
     u32x2 bias[TN][4];
 #pragma unroll
     for (int j = 0; j < TN; ++j)
@@ -433,8 +436,8 @@ void fp8_gemm_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int group_m) {
 // quantizes all the tokens, into LDS: they are few enough, and come from the
 // cache. (With every wave quantizing its own runs' channels the codes took
 // as many registers as the weights and their exchange stood between the
-// loads: 15.7 us against 9.0 for one token, 3072 -> 12288, whose weights alone
-// take 7.6 us at the rate of a copy.)
+// loads: 1.7 times as long for one token, 3072 -> 12288, which takes 8.2 us
+// now, its weights alone 7.9 at the rate of a copy.)
 // CODES: the tokens are codes already (a norm's) and only copied.
 constexpr int kSmallPad = 16;   // bytes between rows of codes in LDS
 template <int W, int kRing, bool CODES>
@@ -541,11 +544,14 @@ __global__ __launch_bounds__(64 * W) void fp8_small_kernel(Fp8Gemm g) {
 // multiplications behind them. Four waves hold 32 x 32 each. Scale words (four
 // stages' bytes) are read four stages ahead.
 //
-// With D = 5 two workgroups fit a CU, with 3 three. Measured: a stage takes
-// 0.28 us without its transfers (the LDS reads), 0.3 to 0.45 with them (the
-// misses of the L2s). Tiles of 64 x 128 and 128 x 128 took as long or longer
-// wherever they are fewer than the CUs (12288 channels, 64 tokens, 3072
-// outputs: 20.5 us, 20.7 and 22; 2064, 1003 and 1552: 16.2, 15.8 and 18.1).
+// With D = 5 the ring is half of a CU's LDS and the ticket's word goes past it,
+// so a CU has one workgroup (these launches have no more product tiles than
+// CUs; workgroups of the bias gradient behind them wait for a CU that is
+// done), with D = 3 three. Measured: a stage takes 0.28 us without its
+// transfers (the LDS reads), 0.3 to 0.45 with them (the misses of the L2s).
+// Tiles of 64 x 128 and 128 x 128 took as long or longer wherever they are
+// fewer than the CUs (12288 channels, 64 tokens, 3072 outputs: 1% and 7%
+// longer; 2064, 1003 and 1552: 2% less and 12% longer).
 constexpr int kDeepStage = 2 * 64 * 128, kDeepOps = 4;   // bytes of a stage; transfers per wave and stage
 template <int D, bool BROW>
 __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, int tiles_n, int chunk, int runs, Fp8BiasGrad bias) {
@@ -663,10 +669,10 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
   if (runs > 1) {
     // The sums go through the device's coherence point and not the XCD's L2
     // (relaxed atomics of agent scope, of 8 bytes), so that no cache has to be
-    // written back or invalidated: with plain stores and an agent-scope
-    // release and acquire the call took 26.6 us for 64 tokens, 12288 -> 3072,
-    // with a second kernel that adds the runs 19.8, this way 19.9 and a launch
-    // (2.8 us of host time) less. Each store has reached that point before the
+    // written back or invalidated: with an agent-scope release and acquire the
+    // call takes 25.8 us for 64 tokens, 12288 -> 3072, with the acquire alone
+    // 20.7, this way 15.7; a second kernel that adds the runs took as long as
+    // this and a launch (2.8 us of host time) more. Each store has reached that point before the
     // ticket is taken (the wait), and no XCD can hold an older copy: a kernel
     // starts with nothing of this memory in its caches, a run's sums fill whole
     // lines (the workspace is used from a multiple of 256 bytes on), and only
@@ -714,8 +720,8 @@ __global__ __launch_bounds__(256) void fp8_deep_kernel(Fp8Gemm g, int tiles_m, i
 typedef Tile<256, 256, 2, 2> TileL;
 typedef Tile<256, 192, 2, 2> TileW;
 typedef Tile<128, 128, 2, 2> TileM;
-// The 32 workgroups of an XCD take 4 tile-rows x 8 tile-columns (8 x 4 took
-// 2% longer at 8192^3, 16 x 2 8%).
+// The 32 workgroups of an XCD take 4 tile-rows x 8 tile-columns (8 x 4 take
+// 4% longer at 8192^3, 16 x 2 8%).
 constexpr int kGroupM = 4;
 
 template <class TL, bool BROW>
@@ -750,8 +756,10 @@ hipError_t launch_fp8_gemm_small(const Fp8Gemm& g, int num_cus, hipStream_t st) 
   const int KB = (int)((g.K + 127) / 128), grid = g.b_rows / 16;
   const size_t lds = (size_t)g.a_rows * (KB * 128 + kSmallPad + KB);
   // Where a wave of eight has more than four blocks and no CU has two
-  // workgroups, sixteen share them (one token, 12288 -> 3072: 10.6 us against
-  // 13.3; with 24 blocks, 3072 -> 3072, eight take 4.5 us and sixteen 5.0).
+  // workgroups, sixteen share them (one token, 12288 -> 3072: 9.4 us against
+  // 9.9, 8192 -> 4096 7.8 against 8.8; with 24 blocks, 3072 -> 3072, 4.2 us
+  // either way, and with more workgroups, 3072 -> 12288, eight take 7.9 us and
+  // sixteen 8.3).
   const dim3 n((unsigned)grid);
   if (grid <= num_cus && KB > 32) {
     if (g.x) hipLaunchKernelGGL((fp8_small_kernel<16, 2, false>), n, dim3(1024), lds, st, g);
@@ -777,7 +785,8 @@ hipError_t launch_deep(const Fp8Gemm& g, const Fp8Deep& p, const Fp8BiasGrad* bi
 }
 }  // namespace
 
-// (a launch of its own takes 3 us of a small backward's 30)
+// (a launch of its own takes 2 us more: 777 tokens, 1552 -> 2064, 28.1 us
+// against 30.1, 64 tokens, 3072 -> 3072, 24.6 against 26.7)
 bool fp8_gemm_takes_bias(const Fp8Gemm& g) { return fp8_deep(g.a_rows, g.b_rows, g.K).runs > 0; }
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st, const Fp8BiasGrad* bias) {
@@ -786,9 +795,10 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, int num_cus, hipStream_t st, const 
   // The tile of least cost, a cost being the rounds of tiles over the CUs times
   // a round's time relative to TileL's, as measured on the products of K from
   // 2048 to 12288: TileW 0.85 (it fills the CUs where TileL's rounds do not:
-  // 12288 x 3072 outputs over 4608 tokens 180 us against 198), TileM 0.62 with
-  // two tiles a CU and 0.5 with one (512 x 3072 outputs over 12288 channels
-  // 59 us against TileL's 110; 4608 x 3072 208 against 162).
+  // the weight gradient of 12288 x 3072 over 4608 tokens 175 us, TileL 188,
+  // TileM 203), TileM 0.62 with two tiles a CU and 0.5 with one (640 x 3072
+  // outputs over 12288 channels 58 us, TileL 110, TileW 97; 4608 x 3072 over
+  // 12288 207 us, TileL 165, TileW 243).
   auto tiles = [&](int bm, int bn) { return ((g.a_rows + bm - 1) / bm) * ((g.b_rows + bn - 1) / bn); };
   auto rounds = [&](int64_t n, int64_t at_once) { return (float)((n + at_once - 1) / at_once); };
   const int64_t nm = tiles(TileM::BM, TileM::BN);

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const uint16_t* x, 
 //
 // Measured, both matrices with row codes and sums: 4608 tokens of 3072 and
 // 12288 channels 48 us (268 MB in and out, 5.6 TB/s: the inputs come partly
-// from the caches); 777 of 1552 and 2064 9.8 us, of which 4.5 go when the two
+// from the caches); 777 of 1552 and 2064 10.0 us, of which 4.5 go when the two
 // kinds of codes are not stored and 3.2 are the launch and the loads.
 constexpr int kTLd = 33;   // words of a transposed row in LDS (32 and one against bank conflicts)
 __global__ __launch_bounds__(512) void fp8_quant_t_kernel(Fp8QuantT ma, Fp8QuantT mb, int64_t M, int64_t blocks_a,

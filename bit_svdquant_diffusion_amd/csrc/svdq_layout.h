@@ -187,7 +187,7 @@ inline size_t fp8_scale_bytes(int64_t rows, int64_t channels) {
   return (size_t)((round128(channels) / kFp8Block + 3) / 4) * round128(rows) * 4;
 }
 // bytes of a row of an FP8 weight's 128 x 128 block scales
-SVDQ_HD SVDQ_HD inline int fp8_block_row(int channels) { return ((channels + 127) / 128 + 3) / 4 * 4; }
+SVDQ_HD inline int fp8_block_row(int channels) { return ((channels + 127) / 128 + 3) / 4 * 4; }
 
 inline svdq_status check_fp8_desc(const svdq_fp8_desc* d) {
   if (!d) return SVDQ_ERR_NULL;
@@ -204,11 +204,12 @@ inline bool fp8_inline(int64_t M, int64_t K) { return M <= 16 && M * round128(K)
 // channels per 64 x 64 tile, or runs = 0 where the large tiles are faster.
 // Measured on 256 CUs (workspaces' sizes are asked for without a device, so
 // the plan is this card's): up to 448 tiles it is (400 tiles of 2064 channels
-// 16.2 us against 16.5, 384 of 3072 16.4 against 19.1, 512 of 1024 12.6
-// against 12.2, 768 of 3072 25.8 against 23.4); runs fill the CUs where each
+// 15.6 us against 19.3, 384 of 3072 16.4 against 20.5, 512 of 1024 10.5
+// against 11.0, 768 of 3072 22.0 against 20.8); runs fill the CUs where each
 // is then at least twelve blocks shorter than the whole, which pays for
-// joining them (96 tiles of 24 blocks: 12.3 us with one run or two), up to
-// sixteen, which their last workgroup adds.
+// joining them (48 tiles of 96 blocks 16.3 us against 33.0 with one run, 32 of
+// 64 blocks 15.3 against 24.4, 96 of 24 blocks 12.5 with two runs against
+// 13.0), up to sixteen, which their last workgroup adds.
 constexpr int kFp8Cus = 256, kFp8Tickets = kFp8Cus / 2;
 struct Fp8Deep {
   int runs, chunk;
@@ -303,8 +304,8 @@ inline int norm_grad_teams(const NormTeam& t, int vec) {
 // Layer-norm backward: every group's rows in `runs` runs, one workgroup each,
 // about kNormRuns in all; one run, which needs nothing joined, where its teams
 // have at most two rows each (24 rows of 1000 bf16 channels: a launch and a
-// workspace less, 13.3 us a call against 18.2 with the host's part, 7.5
-// against 7.0 on the GPU alone).
+// workspace less, 12.0 us a call against 16.6 with the host's part, 7.5
+// against 6.8 on the GPU alone).
 constexpr int kNormRuns = 256;
 struct NormGradPlan {
   int runs;

@@ -13,7 +13,7 @@
 // half wave, a wave, or up to sixteen waves, with the next row's loads in
 // flight. All sums are in fp32: per lane, then a fixed butterfly over the
 // wave, then the waves in order. 9216 x 3072 bf16 takes 23.1 us forward and
-// 35.0 backward, 4.9 TB/s both, as a large copy does.
+// 34.8 backward, 4.9 TB/s both, as a large copy does.
 #include <algorithm>
 
 #include "svdq_internal.h"
@@ -360,8 +360,8 @@ __global__ __launch_bounds__(1024) void norm_param_grad_kernel(NormGradArgs g, i
   return hipGetLastError();
 
 // The forward's teams are all resident at once, with as even a share of the
-// rows as there can be (9216 x 3072 bf16: 28 us; with up to 32 waves a CU
-// asked for, of which 20 fit, 34 us).
+// rows as there can be (9216 x 3072 bf16 into twelve outputs in turn: 27.1 us;
+// with up to 32 waves a CU asked for, of which 20 fit, 29.6 us).
 template <typename T, bool QUANT>
 hipError_t launch_fwd(const NormArgs& a, int num_cus, hipStream_t st) {
   const int span = QUANT ? a.Kp : a.C;
@@ -433,9 +433,9 @@ hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st) {
 
 hipError_t launch_norm_grad(const NormGradArgs& args, const NormGradPlan& p, hipStream_t st) {
   // What the caches (256 MB) cannot keep until it is used again is read past
-  // them: from 128 MB of x, dy and dx on (9216 x 3072 bf16, 170 MB: 38.2 us
-  // against 42.7, 3000 x 9000 bf16, 162 MB: 45.0 against 51.7; 16387 x 517
-  // fp32, 102 MB: 25.2 against 23.0, inputs rotating through three sets).
+  // them: from 128 MB of x, dy and dx on (9216 x 3072 bf16, 170 MB: 34.4 us
+  // against 38.1, 3000 x 9000 bf16, 162 MB: 41.5 against 43.3; 16387 x 517
+  // fp32, 102 MB: 21.6 either way; inputs rotating through three sets).
   NormGradArgs g = args;
   g.once = (double)g.f.M * g.f.C * 3 * (g.f.dtype == SVDQ_DT_F32 ? 4 : 2) > 128e6;
   const hipError_t e = g.f.dtype == SVDQ_DT_F32    ? launch_bwd<float>(g, p, st)
