@@ -27,6 +27,8 @@ __all__ = [
     "layer_norm_forward", "layer_norm_backward",
     "fp8_packed_bytes", "fp8_pack", "fp8_forward", "fp8_norm_forward", "fp8_backward", "fp8_quantize",
     "fp8_workspace_bytes", "fp8_norm_workspace_bytes", "fp8_backward_workspace_bytes", "Fp8Linear",
+    "residual_norm_forward", "residual_norm_backward", "rope", "rope_frequencies", "attention_forward",
+    "attention_backward", "attention_workspace_bytes", "attention_backward_workspace_bytes",
 ]
 
 FMT_INT4 = 0
@@ -49,6 +51,9 @@ EXPORTED_SYMBOLS = [
     "svdq_fp8_packed_bytes", "svdq_fp8_pack", "svdq_fp8_workspace_bytes", "svdq_fp8_forward",
     "svdq_fp8_norm_workspace_bytes", "svdq_fp8_norm_forward", "svdq_fp8_backward_workspace_bytes",
     "svdq_fp8_backward", "svdq_fp8_quantize",
+    "svdq_residual_norm_forward", "svdq_residual_norm_backward_workspace_bytes", "svdq_residual_norm_backward",
+    "svdq_rope", "svdq_attention_workspace_bytes", "svdq_attention_forward",
+    "svdq_attention_backward_workspace_bytes", "svdq_attention_backward",
 ]
 
 # svdq_mlp_forward modes
@@ -116,6 +121,35 @@ class Fp8Packed(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in FP8_FIELDS]
 
 
+class ResidualDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("channels", "dtype", "param_dtype", "norm", "post_norm", "one_plus", "groups")] + \
+               [("eps", ctypes.c_float), ("alpha", ctypes.c_float), ("rows_per_group", ctypes.c_int64)]
+
+
+class ResidualParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "weight", "bias", "post_weight")] + \
+               [(n, ctypes.c_int64) for n in ("ld_gate", "ld_weight", "ld_bias", "ld_post")]
+
+
+class ResidualGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "weight", "bias", "post_weight")]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("batch", "token", "head")]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "position_type", "head_dim", "q_heads", "k_heads", "axes")] + \
+               [("pairs", ctypes.c_int32 * 4), ("half", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("samples", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "head_dim", "heads", "kv_heads", "causal")] + \
+               [("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("samples", "queries", "keys")]
+
+
 _lib = None
 
 
@@ -178,6 +212,15 @@ def lib() -> ctypes.CDLL:
         "svdq_fp8_backward_workspace_bytes": [P(Fp8Desc), i64, P(sz)],
         "svdq_fp8_backward": [P(Fp8Desc), P(Fp8Packed), vp, vp, i64, vp, vp, vp, vp, sz, vp],
         "svdq_fp8_quantize": [vp, i64, ctypes.c_int32, vp, vp, vp],
+        "svdq_residual_norm_forward": [P(ResidualDesc), vp, i64, vp, i64, P(ResidualParams), i64, vp, i64, vp, i64, vp, vp],
+        "svdq_residual_norm_backward_workspace_bytes": [P(ResidualDesc), i64, P(sz)],
+        "svdq_residual_norm_backward": [P(ResidualDesc), vp, i64, vp, i64, vp, i64, vp, i64, P(ResidualParams), vp, i64, vp,
+                                        i64, vp, i64, P(ResidualGrads), ctypes.c_int32, vp, sz, vp],
+        "svdq_rope": [P(RopeDesc), P(Heads), P(Heads), vp, i64, vp, P(Heads), P(Heads), vp],
+        "svdq_attention_workspace_bytes": [P(AttentionDesc), P(sz)],
+        "svdq_attention_forward": [P(AttentionDesc), P(Heads), P(Heads), P(Heads), vp, i64, P(Heads), vp, vp, sz, vp],
+        "svdq_attention_backward_workspace_bytes": [P(AttentionDesc), P(sz)],
+        "svdq_attention_backward": [P(AttentionDesc)] + [P(Heads)] * 5 + [vp, vp, i64] + [P(Heads)] * 3 + [vp, sz, vp],
         "svdq_mlp_workspace_bytes": [D, D, i64, P(sz), P(sz)],
         "svdq_mlp_fused": [D, D, i64, P(ctypes.c_int32)],
         "svdq_mlp_forward": [D, P(Packed), D, P(Packed), vp, i64, vp, vp, sz, ctypes.c_int32, vp],
@@ -1106,3 +1149,264 @@ class Fp8Linear:
     def update(self, w, bias=None, stream=None):
         _need(w.shape == (self.N, self.K), "w: the layer's shape")
         fp8_pack(w, bias, out=self.dev, stream=stream)
+
+
+# ----------------------------------------------------------------------------
+# Between the linears of a block: the gated residual with its norms, rotary
+# positions and attention, forward and backward (as above, no call records an
+# autograd graph).
+# ----------------------------------------------------------------------------
+NORM_KINDS = {"layer": 0, "rms": 1}
+
+
+def _residual_setup(C, M, dtype, params, kind, post, alpha, eps, one_plus, rows_per_group):
+    """(descriptor, parameters, groups, whether they are vectors, rows_per_group) for (gate, weight, bias,
+    post_weight), each [C] or [groups][C] of one type, or None."""
+    groups, pdtype, flat = 1, dtype, True
+    for p in params:
+        if p is not None:
+            groups, pdtype, flat = p.shape[0] if p.dim() == 2 else 1, p.dtype, p.dim() == 1
+            break
+    _need(kind in NORM_KINDS, "kind: layer or rms")
+    s = ResidualParams()
+    for p, name, ld in zip(params, ("gate", "weight", "bias", "post_weight"), ("ld_gate", "ld_weight", "ld_bias", "ld_post")):
+        if p is not None:
+            at, step = _param(p, C, groups, pdtype, name)
+            _need((p.dim() == 1) == flat, "parameters: all [channels] or all [groups][channels]")
+            setattr(s, name, at)
+            setattr(s, ld, step)
+    if rows_per_group is None:
+        rows_per_group = max(1, -(-M // max(1, groups)))
+    d = ResidualDesc(C, _dt(dtype), _dt(pdtype), NORM_KINDS[kind], 1 if post else 0, 1 if one_plus else 0, groups, eps, alpha,
+                     rows_per_group)
+    return d, s, groups, flat, rows_per_group
+
+
+def _residual_out(t, x, what, stream):
+    if t is None:
+        return _rows_like(x, x.shape, stream)
+    _need(t.dtype == x.dtype and t.shape == x.shape, f"{what}: the shape and type of the rows")
+    return t
+
+
+def residual_norm_forward(x, h, gate=None, weight=None, bias=None, post_weight=None, post_norm: bool = False,
+                          kind: str = "layer", alpha: float = 1.0, eps: float = 1e-6, one_plus: bool = False,
+                          rows_per_group=None, s=None, y=None, stream=None):
+    """svdq_residual_norm_forward: (s, y, stats) with s = alpha x + gate hn of
+    the stream x and a block's output h (both [M][C], bfloat16, float16 or
+    float32; rows contiguous, any row stride) and y = norm(s) g + bias for the
+    next block. hn is h, or norm(h) times its weight with post_norm (a given
+    post_weight means it). kind: "layer" or "rms", of both norms.
+
+    gate, weight, bias, post_weight: all [C], or all [groups][C] for rows in
+    groups of rows_per_group (default: the rows split evenly), of one type; with
+    one_plus the gains are 1 + weight and 1 + post_weight. stats: float32
+    [2 or 4 (rms: 1 or 2)][M], for residual_norm_backward. s and y may each be x
+    or h."""
+    params = (gate, weight, bias, post_weight)
+    at = _on_device(x, h, s, y, *params)
+    if any(t is not None and t.requires_grad for t in (x, h) + params):
+        _no_graph("residual_norm_forward")
+    post = post_norm or post_weight is not None
+    M, C = _matrix(x, "x")
+    _need(h.shape == x.shape and h.dtype == x.dtype, "h: the shape and type of x")
+    d, p, _, _, _ = _residual_setup(C, M, x.dtype, params, kind, post, alpha, eps, one_plus, rows_per_group)
+    s, y = _residual_out(s, x, "s", stream), _residual_out(y, x, "y", stream)
+    stats = _empty(((1 + d.post_norm) * (2 - d.norm), M), _t.float32, x, stream)
+    (xp, ldx), (hp, ldh), (sp, lds), (yp, ldy) = _rows(x, "x"), _rows(h, "h"), _rows(s, "s"), _rows(y, "y")
+    _call("svdq_residual_norm_forward", at, stream, ctypes.byref(d), xp, ldx, hp, ldh, ctypes.byref(p), M, sp, lds, yp, ldy,
+          stats.data_ptr())
+    return s, y, stats
+
+
+def _matrix(t, what):
+    _need(t.dim() == 2, f"{what}: a matrix [rows][channels]")
+    return t.shape
+
+
+def residual_norm_backward(dy, s, h, stats, gate=None, weight=None, post_weight=None, ds=None, post_norm: bool = False,
+                           kind: str = "layer", alpha: float = 1.0, one_plus: bool = False, rows_per_group=None,
+                           grad_dtype=None, param_grads: bool = True, dx=None, dh=None, stream=None):
+    """svdq_residual_norm_backward: (dx, dh, dgate, dweight, dbias,
+    dpost_weight) for dy of y and ds of s (None: nothing comes along the
+    stream), from the forward's s, h, stats and parameters. The parameters'
+    gradients are [C], or [groups][C] for such parameters, of grad_dtype
+    (default: the parameters' type, float32 without any); dpost_weight is None
+    without post_norm, all four without param_grads."""
+    params = (gate, weight, None, post_weight)
+    at = _on_device(dy, s, h, stats, ds, dx, dh, *params)
+    if dy.requires_grad or (ds is not None and ds.requires_grad):
+        _no_graph("residual_norm_backward")
+    post = post_norm or post_weight is not None
+    M, C = _matrix(s, "s")
+    for t, name in ((dy, "dy"), (h, "h"), (ds, "ds")):
+        _need(t is None or (t.shape == s.shape and t.dtype == s.dtype), f"{name}: the shape and type of s")
+    d, p, groups, flat, rpg = _residual_setup(C, M, s.dtype, params, kind, post, alpha, 0.0, one_plus, rows_per_group)
+    f32 = _torch().float32
+    _need(stats.dtype == f32 and stats.is_contiguous() and stats.shape == ((1 + d.post_norm) * (2 - d.norm), M),
+          "stats: of the forward")
+    some = [t for t in params if t is not None]
+    gdt = grad_dtype if grad_dtype is not None else (some[0].dtype if some else f32)
+    dx, dh = _residual_out(dx, s, "dx", stream), _residual_out(dh, s, "dh", stream)
+    grads, out, ws, size = None, [None] * 4, None, 0
+    if param_grads:
+        n = 4 if post else 3
+        both = _empty((n, C) if flat else (n, groups, C), gdt, s, stream)
+        out[:n] = list(both)
+        grads = ctypes.byref(ResidualGrads(*[_ptr(t) for t in out]))
+        size = _residual_ws(C, d.dtype, groups, rpg, M)
+        if size:
+            ws = _empty((size,), _t.uint8, s, stream)
+    (yp, ldy), (sp, lds), (hp, ldh) = _rows(dy, "dy"), _rows(s, "s"), _rows(h, "h")
+    (xp, ldx), (gp, ldg) = _rows(dx, "dx"), _rows(dh, "dh")
+    tp, ldt = _rows(ds, "ds") if ds is not None else (None, 0)
+    _call("svdq_residual_norm_backward", at, stream, ctypes.byref(d), yp, ldy, tp, ldt, sp, lds, hp, ldh, ctypes.byref(p),
+          stats.data_ptr(), M, xp, ldx, gp, ldg, grads, _dt(gdt), _ptr(ws), size)
+    return (dx, dh, *out)
+
+
+@functools.lru_cache(maxsize=4096)
+def _residual_ws(C, dt, groups, rows_per_group, M) -> int:
+    need = ctypes.c_size_t()
+    d = ResidualDesc(C, dt, 0, 0, 0, 0, groups, 0.0, 1.0, rows_per_group)
+    _check(lib().svdq_residual_norm_backward_workspace_bytes(ctypes.byref(d), M, ctypes.byref(need)),
+           "svdq_residual_norm_backward_workspace_bytes")
+    return need.value
+
+
+def _heads(t, what, shape=None, dtype=None) -> Heads:
+    """A tensor [samples][tokens][heads][head_dim] for the library."""
+    _need(t.dim() == 4 and (t.shape[3] <= 1 or t.stride(3) == 1),
+          f"{what}: [samples][tokens][heads][head_dim], contiguous along the head")
+    _need(shape is None or t.shape == shape, f"{what}: shape {None if shape is None else list(shape)}")
+    _need(dtype is None or t.dtype == dtype, f"{what}: of type {dtype}")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def rope_frequencies(pairs, theta: float = 10000.0, shared: bool = False, device="cuda"):
+    """float64 frequencies for `rope`: pair j of an axis with n pairs turns by
+    theta^(-j / n) a position; with `shared` the axes divide one ladder over all
+    pairs."""
+    torch = _torch()
+    n = [int(p) for p in pairs]
+    ladder = [torch.arange(m, dtype=torch.float64) / m for m in ([sum(n)] if shared else [m for m in n if m > 0])]
+    return (float(theta) ** -torch.cat(ladder)).to(device)
+
+
+def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """svdq_rope: (q, k) turned, of q [samples][tokens][heads][head_dim] and k
+    (its own number of heads, or None), bfloat16, float16 or float32, any
+    strides of 16 bytes. positions: int32 or float32 [tokens][axes] or
+    [samples][tokens][axes]; pairs: the pairs of each axis (up to four); freqs:
+    float64 [sum of pairs] (rope_frequencies). interleaved: pairs (2 j, 2 j + 1),
+    else (j, j + sum of pairs). inverse turns back, as the gradient does. q_out
+    and k_out may be q and k."""
+    torch = _torch()
+    at = _on_device(q, k, positions, freqs, q_out, k_out)
+    if q.requires_grad or (k is not None and k.requires_grad):
+        _no_graph("rope")
+    qh = _heads(q, "q")
+    B, L, H, D = q.shape
+    pairs = [int(p) for p in pairs]
+    _need(1 <= len(pairs) <= 4, "pairs: of one to four axes")
+    _need(positions.is_contiguous() and positions.shape in ((L, len(pairs)), (B, L, len(pairs))) and
+          positions.dtype in (torch.int32, torch.float32), "positions: contiguous int32 or float32 [tokens][axes]")
+    _need(freqs.is_contiguous() and freqs.dtype == torch.float64 and freqs.shape == (sum(pairs),),
+          "freqs: contiguous float64, one for each pair")
+    _need(k is None or (k.dim() == 4 and k.shape[:2] == q.shape[:2] and k.shape[3] == D and k.dtype == q.dtype),
+          "k: samples, tokens, head_dim and type of q")
+    d = RopeDesc(_dt(q.dtype), int(positions.dtype == torch.float32), D, H, 0 if k is None else k.shape[2], len(pairs),
+                 (ctypes.c_int32 * 4)(*pairs), int(not interleaved), int(inverse), B, L)
+    kh = ko = None
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q, stream)
+    qo = _heads(q_out, "q_out", q.shape, q.dtype)
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k.shape, k.dtype, k, stream)
+        kh, ko = ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(k_out, "k_out", k.shape, k.dtype))
+    _call("svdq_rope", at, stream, ctypes.byref(d), ctypes.byref(qh), kh, positions.data_ptr(),
+          L * len(pairs) if positions.dim() == 3 else 0, freqs.data_ptr(), ctypes.byref(qo), ko)
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_plan(dt, D, H, Hk, causal, scale, B, Lq, Lk):
+    """(descriptor reference, itself, forward's and backward's workspace bytes)"""
+    d = AttentionDesc(dt, D, H, Hk, causal, scale, B, Lq, Lk)
+    sizes = []
+    for name in ("svdq_attention_workspace_bytes", "svdq_attention_backward_workspace_bytes"):
+        n = ctypes.c_size_t()
+        _check(getattr(lib(), name)(ctypes.byref(d), ctypes.byref(n)), name)
+        sizes.append(n.value)
+    return ctypes.byref(d), d, sizes[0], sizes[1]
+
+
+def attention_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None) -> int:
+    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, 0, 1.0, samples, queries, keys)[2]
+
+
+def attention_backward_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None) -> int:
+    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, 0, 1.0, samples, queries, keys)[3]
+
+
+def _attention_setup(q, k, v, key_mask, causal, scale):
+    _need(q.dim() == 4 and k.dim() == 4, "q, k, v: [samples][tokens][heads][head_dim]")
+    B, Lq, H, D = q.shape
+    Lk, Hk = k.shape[1], k.shape[2]
+    _need(k.shape == (B, Lk, Hk, D) and v.shape == k.shape and k.dtype == q.dtype and v.dtype == q.dtype,
+          "k, v: [samples][keys][kv_heads][head_dim] of the type of q")
+    mask = ld = None
+    if key_mask is not None:
+        torch = _torch()
+        _need(key_mask.shape == (B, Lk) and key_mask.dtype in (torch.bool, torch.uint8) and
+              (Lk <= 1 or key_mask.stride(1) == 1), "key_mask: bool or uint8 [samples][keys], contiguous along the keys")
+        mask, ld = key_mask.data_ptr(), key_mask.stride(0)
+    plan = _attention_plan(_dt(q.dtype), D, H, Hk, int(bool(causal)), float(scale if scale is not None else max(D, 1) ** -0.5), B,
+                           Lq, Lk)
+    return plan, mask, ld or 0
+
+
+def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, out=None, workspace=None, stream=None):
+    """svdq_attention_forward: (o, lse) of q [samples][queries][heads][head_dim]
+    and k, v [samples][keys][kv_heads][head_dim] (bfloat16 or float16, any
+    strides of 16 bytes). key_mask: bool or uint8 [samples][keys], true for the
+    keys that take part; causal: query i sees the keys j <= i + keys - queries;
+    scale: default head_dim^(-1/2). lse: float32 [samples][heads][queries]. A
+    query without keys has o = 0, lse = -inf."""
+    at = _on_device(q, k, v, key_mask, out, workspace)
+    if q.requires_grad or k.requires_grad or v.requires_grad:
+        _no_graph("attention_forward")
+    (d, _, size, _), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
+    B, Lq, H, D = q.shape
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+    lse = _empty((B, H, Lq), _t.float32, q, stream)
+    ws, wsp, size = _scratch(workspace, size, q, stream)
+    b = ctypes.byref
+    _call("svdq_attention_forward", at, stream, d, b(_heads(q, "q")), b(_heads(k, "k")), b(_heads(v, "v")), mask, ldm,
+          b(_heads(out, "out", q.shape, q.dtype)), lse.data_ptr(), wsp, size)
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = False, scale=None, dq=None, dk=None, dv=None,
+                       workspace=None, stream=None):
+    """svdq_attention_backward: (dq, dk, dv) for dout of o, from the forward's
+    inputs and its o and lse."""
+    at = _on_device(q, dout, k, v, o, lse, key_mask, dq, dk, dv, workspace)
+    if dout.requires_grad:
+        _no_graph("attention_backward")
+    (d, _, _, size), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
+    B, Lq, H, D = q.shape
+    _need(lse.dtype == _torch().float32 and lse.shape == (B, H, Lq) and lse.is_contiguous(),
+          "lse: float32 [samples][heads][queries]")
+    dq = _empty(q.shape, q.dtype, q, stream) if dq is None else dq
+    dk = _empty(k.shape, q.dtype, q, stream) if dk is None else dk
+    dv = _empty(k.shape, q.dtype, q, stream) if dv is None else dv
+    ws, wsp, size = _scratch(workspace, size, q, stream)
+    b = ctypes.byref
+    t = [b(_heads(x, n, s, q.dtype)) for x, n, s in ((dout, "dout", q.shape), (q, "q", None), (k, "k", None), (v, "v", None),
+                                                    (o, "o", q.shape), (dq, "dq", q.shape), (dk, "dk", k.shape),
+                                                    (dv, "dv", k.shape))]
+    _call("svdq_attention_backward", at, stream, d, *t[:5], lse.data_ptr(), mask, ldm, *t[5:], wsp, size)
+    return dq, dk, dv

@@ -138,6 +138,85 @@ hipError_t launch_norm(const NormArgs& a, int num_cus, hipStream_t st);
 hipError_t prepare_norm();
 hipError_t launch_norm_grad(const NormGradArgs& g, const NormGradPlan& p, hipStream_t st);
 
+// The gated residual with its norms, and its gradients (svdq_residual.hip)
+struct ResidualArgs {
+  int dtype, pdtype, one_plus, layer, C, G;   // layer: subtract the mean (else rms)
+  int post;                                   // h is normed first
+  float eps, alpha;
+  int64_t M, rpg;
+  const void* x;     // forward; the backward's is s
+  int64_t ldx;
+  const void* h;
+  int64_t ldh;
+  // [G][ld] of pdtype, each may be null (gate and gains 1, bias 0)
+  const void *gate, *w, *b, *pw;
+  int64_t ldgate, ldw, ldb, ldpw;
+  void* s;
+  int64_t lds;
+  void* y;
+  int64_t ldy;
+  float* stats;      // rows of M: mean (layer), rstd, and the same of h (post)
+};
+struct ResidualGradArgs {
+  ResidualArgs f;    // s, h, the parameters and stats
+  const void* dy;
+  int64_t lddy;
+  const void* ds;    // the gradient that comes along the stream, may be null
+  int64_t ldds;
+  void* dx;
+  int64_t lddx;
+  void* dh;
+  int64_t lddh;
+  void* out[4];      // of gate, w, b, pw: [G][C] of gdtype, each may be null
+  int gdtype;
+  float* part;       // [G][runs][4][C], null when a group is one run
+};
+struct ResidualGradPlan;
+hipError_t launch_residual(const ResidualArgs& a, int num_cus, hipStream_t st);
+hipError_t launch_residual_grad(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st);
+
+// Heads of a tensor: element strides between samples, tokens and heads
+struct Heads {
+  void* p;
+  int64_t batch, token, head;
+};
+
+// Rotary positions (svdq_rope.hip)
+struct RopeArgs {
+  int dtype, pos_dtype, B, L, H[2], D, axes, pairs, half, inverse;
+  int first[5];         // first pair of each axis, and the end
+  Heads x[2], y[2];     // q and k
+  const void* pos;      // [B or 1][L][axes]
+  int64_t pos_batch;
+  const double* freqs;  // [pairs]
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
+
+// Attention (svdq_attention.hip, svdq_attention_grad.hip). Row r of a key
+// head's query rows is query r / G, head r % G of its G.
+struct AttnArgs {
+  int dtype, B, Lq, Lk, H, Hk, G, D, causal;
+  float scale, scale_log2;   // and times log2 e
+  Heads q, k, v, o;
+  const uint8_t* mask;       // [B][Lk], may be null
+  int64_t mask_batch;
+  float* lse;                // [B][H][Lq]
+  // the launch: blocks of held rows (or keys) times parts of the passing ones
+  int blocks, splits, split_keys;
+  float* part;               // [splits][B Hk][rows][D] (dk and dv: [keys][2][D]) with several parts
+  float* part_lse;           // [splits][B Hk][rows]
+};
+struct AttnGradArgs {
+  AttnArgs f;
+  Heads dout, dq, dk, dv;
+  float *lse2, *delta;       // [B Hk][row_blocks kAttnPrepRows]
+  float* tops;               // [B Hk][row_blocks + key_blocks], fp16 alone
+  int row_blocks, key_blocks;
+};
+struct AttnGradPlan;
+hipError_t launch_attention(const AttnArgs& a, hipStream_t st);
+hipError_t launch_attention_grad(const AttnGradArgs& g, const AttnGradPlan& plan, hipStream_t st);
+
 // E4M3 quantizers (svdq_fp8_quant.hip)
 // (plain: the scale bytes as svdq_fp8_quantize documents them, not the product's order)
 // `tickets`, where given: kFp8Tickets words that the kernel zeroes for the product behind it

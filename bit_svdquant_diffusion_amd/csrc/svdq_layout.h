@@ -4,6 +4,7 @@
 #pragma once
 #include <stddef.h>
 #include <stdint.h>
+#include <algorithm>
 
 #include "svdq.h"
 
@@ -326,6 +327,104 @@ inline NormGradPlan norm_grad_plan(int64_t M, int64_t groups, int64_t rows_per_g
 inline size_t norm_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
   const NormGradPlan p = norm_grad_plan(M, groups, rows_per_group, C, elem_bytes);
   return p.runs > 1 ? (size_t)groups * p.runs * 2 * C * 4 : 0;
+}
+
+// Gated residual: a row's lanes, `waves` waves of nv vectors (of `vec`
+// elements) a lane, or with sub = 4 a quarter wave (rows of up to 16 vectors).
+struct ResidualTeam {
+  int nv, waves, sub;
+};
+constexpr int kResidualChannels = 8192;   // 16 waves x 64 lanes x 8 elements
+inline ResidualTeam residual_team(int C, int vec, int most_nv) {
+  const int n = (C + vec - 1) / vec;
+  if (n <= 16) return ResidualTeam{1, 1, 4};
+  const int nv = n <= 64 ? 1 : most_nv;
+  return ResidualTeam{nv, (n + 64 * nv - 1) / (64 * nv), 1};
+}
+// Its gradients: workgroups of sixteen waves (as many teams as these hold),
+// every group's rows in `runs` runs of one workgroup each.
+constexpr int kResidualRuns = 256;
+struct ResidualGradPlan {
+  int runs, teams;   // teams of a workgroup
+  int64_t rows_per_run;
+};
+inline ResidualGradPlan residual_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
+  const int64_t rows = rows_per_group < M ? rows_per_group : M;
+  const int64_t live = M > 0 ? (M - 1) / rows_per_group + 1 : 1;   // groups that have rows
+  const ResidualTeam t = residual_team(C, 16 / elem_bytes, elem_bytes == 4 ? 2 : 1);
+  ResidualGradPlan p;
+  p.teams = 16 / t.waves * t.sub;
+  int64_t runs = kResidualRuns / live;
+  if (runs > (rows + 3) / 4) runs = (rows + 3) / 4;   // at least four rows each
+  if (runs < 1 || groups > kResidualRuns || rows <= 2 * p.teams) runs = 1;
+  p.runs = (int)runs;
+  p.rows_per_run = rows > 0 ? (rows + runs - 1) / runs : 1;
+  if (p.teams > p.rows_per_run) p.teams = (int)((p.rows_per_run + t.sub - 1) / t.sub * t.sub);
+  return p;
+}
+inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
+  const ResidualGradPlan p = residual_grad_plan(M, groups, rows_per_group, C, elem_bytes);
+  return p.runs > 1 ? (size_t)groups * p.runs * 4 * C * 4 : 0;
+}
+
+// Attention: how the held rows (keys, for their gradients) lie in blocks of
+// `block` and, where these are fewer than the CUs, the passing tiles in parts
+// of at least four, whose results are joined: about two workgroups a CU.
+// (Workspaces' sizes are asked for without a device, so the plan is this
+// card's.)
+constexpr int kAttnCus = 256, kAttnTile = 64, kAttnBlock = 128, kAttnPrepRows = 256;
+struct AttnSplit {
+  int blocks, splits, each;   // each: passing rows of a part
+};
+inline AttnSplit attn_split(int64_t held, int64_t passing, int64_t heads, int block) {
+  const int64_t blocks = (held + block - 1) / block, tiles = (passing + kAttnTile - 1) / kAttnTile;
+  int64_t splits = 1;
+  if (blocks > 0 && blocks * heads < kAttnCus) splits = std::min(2 * kAttnCus / (blocks * heads), tiles / 4);
+  if (splits < 1) splits = 1;
+  const int64_t each = tiles > 0 ? (tiles + splits - 1) / splits : 1;
+  return AttnSplit{(int)blocks, tiles > 0 ? (int)((tiles + each - 1) / each) : 1, (int)each * kAttnTile};
+}
+struct AttnSizes {
+  int64_t B, Lq, Lk, H, Hk, D;
+};
+struct AttnWs {
+  AttnSplit split;
+  size_t part, part_lse, total;
+};
+inline AttnWs attn_ws(const AttnSizes& s) {
+  AttnWs w;
+  const int64_t heads = s.B * s.Hk, rows = s.Lq * (s.H / s.Hk);
+  w.split = attn_split(rows, s.Lk, heads, kAttnBlock);
+  const size_t n = w.split.splits > 1 ? (size_t)w.split.splits * heads * rows : 0;
+  w.part = 0;
+  w.part_lse = align256(n * s.D * 4);
+  w.total = w.part_lse + align256(n * 4);
+  return w;
+}
+struct AttnGradPlan {
+  AttnSplit dkv, dq;
+};
+struct AttnGradWs {
+  AttnGradPlan plan;
+  int row_blocks, key_blocks;
+  size_t lse2, delta, tops, part, total;
+};
+inline AttnGradWs attn_grad_ws(const AttnSizes& s, bool scaled) {
+  AttnGradWs w;
+  const int64_t heads = s.B * s.Hk, rows = s.Lq * (s.H / s.Hk);
+  w.plan.dkv = attn_split(s.Lk, rows, heads, kAttnBlock);
+  w.plan.dq = attn_split(rows, s.Lk, heads, kAttnBlock);
+  w.row_blocks = (int)((rows + kAttnPrepRows - 1) / kAttnPrepRows);
+  w.key_blocks = scaled ? (int)((s.Lk + kAttnPrepRows - 1) / kAttnPrepRows) : 0;
+  const size_t padded = align256((size_t)heads * w.row_blocks * kAttnPrepRows * 4);
+  w.lse2 = 0;
+  w.delta = padded;
+  w.tops = 2 * padded;
+  w.part = w.tops + (scaled ? align256((size_t)heads * (w.row_blocks + w.key_blocks) * 4) : 0);
+  const size_t a = w.plan.dkv.splits > 1 ? (size_t)w.plan.dkv.splits * heads * s.Lk * 2 * s.D * 4 : 0;
+  const size_t b = w.plan.dq.splits > 1 ? (size_t)w.plan.dq.splits * heads * rows * s.D * 4 : 0;
+  w.total = w.part + align256(a > b ? a : b);
+  return w;
 }
 
 }  // namespace svdq

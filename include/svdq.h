@@ -673,6 +673,184 @@ SVDQ_API svdq_status svdq_fp8_quantize(const uint16_t* x, int64_t M, int32_t K, 
                                        void* hip_stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Gated residual with the norms around it: what joins a block to the stream
+ * and norms the stream for the next one, forward and backward. Of a row x of
+ * the stream and the block's output h, with norm(v) = (v - mean) rstd (layer)
+ * or v rstd (rms), rstd = 1 / sqrt(mean of the squares + eps),
+ *
+ *   hn = h, or norm(h) gp (post_norm);  s = alpha x + gate hn;  y = norm(s) g + b
+ *
+ * s is rounded to the rows' type, and its norm is of the rounded values. Row m
+ * belongs to group m / rows_per_group. gate is 1 where it is NULL, g = weight
+ * (1 where NULL) or 1 + weight (one_plus), b = bias (0 where NULL), gp =
+ * post_weight (1 where NULL) or 1 + post_weight; parameters of one group start
+ * at p + group * ld, in elements. Sums are in fp32 from one read of the rows.
+ * Strides and alignment as in the layer norm. Limits: 1 <= channels <= 8192,
+ * 1 <= groups <= 2^24, rows_per_group >= 1, 0 <= M <= 2^24, M <= groups *
+ * rows_per_group, eps >= 0, alpha finite. A row that holds an infinity or a
+ * NaN gives NaN in that row alone (and in its group's parameter gradients).
+ * ---------------------------------------------------------------------------
+ */
+typedef enum { SVDQ_NORM_LAYER = 0, SVDQ_NORM_RMS = 1 } svdq_norm_kind;
+
+typedef struct {
+  int32_t channels, dtype, param_dtype, norm, post_norm, one_plus, groups;
+  float eps, alpha;
+  int64_t rows_per_group;
+} svdq_residual_desc;
+
+typedef struct {
+  const void *gate, *weight, *bias, *post_weight;
+  int64_t ld_gate, ld_weight, ld_bias, ld_post;
+} svdq_residual_params;
+
+typedef struct {
+  void *gate, *weight, *bias, *post_weight;
+} svdq_residual_grads;
+
+/*
+ * s and y of the M rows of x and h, on hip_stream, one kernel, no workspace.
+ * stats: fp32 [n][M], may be NULL: mean (layer norms alone) and rstd of s, then
+ * the same of h with post_norm; the backward reads them. s and y may each be x
+ * or h (with the same stride), not parts of them, and not one another.
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE (a size outside the limits, a stride
+ * below `channels`, a pointer not aligned to its element, s == y),
+ * SVDQ_ERR_FORMAT (unknown type or norm), SVDQ_ERR_DEVICE.
+ */
+SVDQ_API svdq_status svdq_residual_norm_forward(const svdq_residual_desc* desc, const void* x, int64_t ldx, const void* h,
+                                                int64_t ldh, const svdq_residual_params* params, int64_t M, void* s,
+                                                int64_t lds, void* y, int64_t ldy, float* stats, void* hip_stream);
+
+/*
+ * The gradients for dy of y and ds of s (which comes along the stream; may be
+ * NULL), from the forward's s, h, parameters and stats (eps and bias do not
+ * enter). With d = dy g, shat = norm(s), hhat = norm(h):
+ *   t = ds + rstd (d - mean_c(d) - shat mean_c(d shat)),  dx = alpha t
+ *   dgate = sum t hn,  dweight = sum dy shat,  dbias = sum dy
+ *   dh = t gate; with post_norm, e = t gate: dpost = sum e hhat and
+ *   dh = rstd_h (e gp - mean_c(e gp) - hhat mean_c(e gp hhat))
+ * (rms: without the first mean_c of each). Sums over the group's rows, in fp32,
+ * in an order fixed by the sizes and the type: [groups][channels] contiguous of
+ * type grad_dtype; grads and each of its members may be NULL. A group without
+ * rows gets zeros. dx and dh may each be an input of the M rows (with the same
+ * stride), not one another.
+ * workspace: >= svdq_residual_norm_backward_workspace_bytes device bytes,
+ * 16-byte aligned, used when a parameter's gradient is asked for; may be NULL
+ * where that is 0. Errors: as the forward, SVDQ_ERR_WORKSPACE.
+ */
+SVDQ_API svdq_status svdq_residual_norm_backward_workspace_bytes(const svdq_residual_desc* desc, int64_t M, size_t* out);
+SVDQ_API svdq_status svdq_residual_norm_backward(const svdq_residual_desc* desc, const void* dy, int64_t lddy, const void* ds,
+                                                 int64_t ldds, const void* s, int64_t lds, const void* h, int64_t ldh,
+                                                 const svdq_residual_params* params, const float* stats, int64_t M,
+                                                 void* dx, int64_t lddx, void* dh, int64_t lddh,
+                                                 const svdq_residual_grads* grads, int32_t grad_dtype, void* workspace,
+                                                 size_t workspace_bytes, void* hip_stream);
+
+/*
+ * A tensor of heads: element (sample, token, head, d) lies at p + sample *
+ * batch + token * token_stride + head * head_stride + d, in elements, so that
+ * slices of a joint projection's output are taken as they are. Pointers are
+ * 16-byte aligned and the strides multiples of 16 bytes (those of a dimension
+ * of one are not read).
+ */
+typedef struct {
+  void* p;
+  int64_t batch, token, head;
+} svdq_heads;
+
+/*
+ * ---------------------------------------------------------------------------
+ * Rotary positions of several axes (time, height, width, ...). Pair j of a
+ * head's elements, (2 j, 2 j + 1), or (j, j + P) with `half` (P pairs in all),
+ * belongs to an axis (the first pairs[0] to axis 0, and so on) and turns by
+ * p = position[token][axis] * freqs[j]:
+ *
+ *   (u, v) -> (u cos p - v sin p, u sin p + v cos p)
+ *
+ * and by -p with `inverse`, which is also the gradient. Elements behind the
+ * pairs are copied. The angle is formed in 64 bits: positions may be far.
+ * dtype: bf16, fp16 or fp32. positions: int32 or fp32 [samples][tokens][axes],
+ * `position_batch` elements between samples (0: the same for all). freqs: fp64
+ * [P], device memory, radians per position. q and k turn in one launch; k may
+ * be NULL (k_heads 0). An output may be its input (the same strides); tensors
+ * must not overlap otherwise.
+ * Limits: head_dim a multiple of 8 (of the elements of 16 bytes) up to 256,
+ * 1 <= axes <= 4, pairs >= 0, 1 <= P, 2 P <= head_dim, P a multiple of 8 with
+ * `half`; heads 0 .. 65536; samples, tokens >= 0, samples * tokens <= 2^23.
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_DEVICE.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum { SVDQ_POS_I32 = 0, SVDQ_POS_F32 = 1 } svdq_position_type;
+
+typedef struct {
+  int32_t dtype, position_type, head_dim, q_heads, k_heads, axes, pairs[4], half, inverse;
+  int64_t samples, tokens;
+} svdq_rope_desc;
+
+SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, const svdq_heads* k, const void* positions,
+                               int64_t position_batch, const double* freqs, const svdq_heads* q_out,
+                               const svdq_heads* k_out, void* hip_stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Attention, forward and backward, over the keys that a query sees:
+ *
+ *   s = scale q . k,  o = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j)
+ *
+ * Query i of `queries` sees all keys or, causal, the keys j <= i + keys -
+ * queries; of these the ones whose byte of key_mask (u8 [samples][keys],
+ * `mask_batch` bytes between samples, may be NULL) is not zero. A query that
+ * sees no key has o = 0 and lse = -infinity and passes no gradient. Query head
+ * x reads key head x / (heads / kv_heads).
+ * q, o, dout, dq: [samples][queries][heads][head_dim], k, v, dk, dv:
+ * [samples][keys][kv_heads][head_dim], of type bf16 or fp16; lse fp32
+ * [samples][heads][queries]. Scores, statistics and sums are fp32; the
+ * probabilities (and in the backward the scores' gradients) are rounded to the
+ * type for the matrix products, fp16 with powers of two taken out so that small
+ * ones keep their digits. All orders of summation are fixed by the sizes.
+ * Keys and values that the mask drops, and the q and dout of queries that see
+ * no key, are not used whatever they hold. A value that is not finite makes
+ * every row that sees it NaN, and causal may also reach rows that do not see it
+ * but lie in the same tile.
+ * Limits: head_dim a multiple of 8 up to 128; 1 <= kv_heads, heads a multiple
+ * of kv_heads, samples * kv_heads <= 65535; queries * heads / kv_heads < 2^30
+ * and keys < 2^30; blocks of 128 of those times samples * kv_heads <= 2^23;
+ * scale > 0 and finite; 64 tokens (and the heads of one key head) of a tensor
+ * span less than 2^30 elements. Outputs must not overlap inputs or one another.
+ * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_WORKSPACE,
+ * SVDQ_ERR_DEVICE.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  int32_t dtype, head_dim, heads, kv_heads, causal;
+  float scale;
+  int64_t samples, queries, keys;
+} svdq_attention_desc;
+
+/* With few query rows the keys are cut into parts, whose results pass through
+ * the workspace (>= svdq_attention_workspace_bytes device bytes, 16-byte
+ * aligned, may be NULL where that is 0). */
+SVDQ_API svdq_status svdq_attention_workspace_bytes(const svdq_attention_desc* desc, size_t* out);
+SVDQ_API svdq_status svdq_attention_forward(const svdq_attention_desc* desc, const svdq_heads* q, const svdq_heads* k,
+                                            const svdq_heads* v, const uint8_t* key_mask, int64_t mask_batch,
+                                            const svdq_heads* o, float* lse, void* workspace, size_t workspace_bytes,
+                                            void* hip_stream);
+
+/* dq, dk and dv for dout of o, from the forward's inputs, o and lse:
+ *   p = exp(s - lse),  ds = p (dout . v - dout . o),
+ *   dv = sum p dout,  dq = scale sum ds k,  dk = scale sum ds q
+ * (sums over the heads that share a key head, too). The probabilities are
+ * computed again; none are kept. workspace: as above. */
+SVDQ_API svdq_status svdq_attention_backward_workspace_bytes(const svdq_attention_desc* desc, size_t* out);
+SVDQ_API svdq_status svdq_attention_backward(const svdq_attention_desc* desc, const svdq_heads* dout, const svdq_heads* q,
+                                             const svdq_heads* k, const svdq_heads* v, const svdq_heads* o,
+                                             const float* lse, const uint8_t* key_mask, int64_t mask_batch,
+                                             const svdq_heads* dq, const svdq_heads* dk, const svdq_heads* dv,
+                                             void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
  * Measured ceilings of the GPU (not part of the layer; the benchmark reports
  * the kernels against them beside the published peaks).
  * svdq_measure_mfma_peak enqueues one MFMA-only loop on every compute unit:
