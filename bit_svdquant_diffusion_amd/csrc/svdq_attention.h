@@ -75,22 +75,36 @@ __device__ __forceinline__ float sum_halves(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-typedef __attribute__((address_space(3))) void lds_void;
-// 16 bytes a lane from a resource to 1 KiB of LDS (a function of its own: the
-// host pass does not take the builtin inside a template)
-__device__ __forceinline__ void lds_transfer_16(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, 0, 0, 0);
+// 16 (4) bytes a lane from `r` + voff, zeros past r's end, to 1 KiB (256 bytes)
+// of LDS. In assembly, because the compiler lets every transposing LDS read
+// wait for all transfers that it knows of, those of the next tile among them:
+// here tile_barrier alone waits. (No register is written, and the compiler's
+// own counted waits only become stricter by what it does not count.)
+__device__ __forceinline__ void lds_transfer_16(u32x4 r, const void* dst, uint32_t voff) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\ts_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(r), "v"(voff), "s"((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)dst)
+      : "memory");
 }
-__device__ __forceinline__ void lds_transfer_4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, voff, 0, 0, 0);
+__device__ __forceinline__ void lds_transfer_4(u32x4 r, const void* dst, uint32_t voff) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %2, %1, 0 offen lds\n\ts_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(r), "v"(voff), "s"((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)dst)
+      : "memory");
 }
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
 }
 constexpr uint32_t kPastEnd = 0x7ffffff0u;   // a lane offset past the end of every resource: loads zeros
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_resource(const void* base, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+// a buffer resource of raw bytes
+__device__ __forceinline__ u32x4 rows_resource(const void* base, int bytes) {
+  const uint64_t at = (uint64_t)base;
+  return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)bytes, 0x00020000u};
 }
 
 // all transfers have arrived and all LDS reads returned, then the workgroup's

@@ -26,7 +26,6 @@ namespace svdq {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kProbScale = 1024.f;   // of fp16 probabilities
 
 template <typename T>
@@ -52,9 +51,9 @@ __device__ __forceinline__ float dot_x2(float s, uint32_t a, uint32_t b) {
   }
 }
 
-// Per query row, in the order of the tiles' rows: lse in base 2 (+infinity
-// for a row without keys, whose probabilities are then zero) and delta; zeros
-// and infinities up to whole tiles. Sixteen lanes a row. For fp16 also the
+// Per query row, in the order of the tiles' rows: -lse / scale (-infinity for
+// a row without keys, whose probabilities are then zero) and -delta, which the
+// products' accumulators start with; the same up to whole tiles. Sixteen lanes a row. For fp16 also the
 // largest |do| of each workgroup's rows and, by further workgroups, the
 // largest |v| of runs of keys.
 template <typename T>
@@ -85,8 +84,8 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnGradArgs g) {
       if (lane == 0) {
         const float lse = r < R ? a.lse[((int64_t)b * a.H + head) * a.Lq + i] : -__builtin_inff();
         const bool none = lse == -__builtin_inff();
-        g.lse2[hb * Rp + r] = none ? __builtin_inff() : lse * kLog2e;
-        g.delta[hb * Rp + r] = none ? 0.f : s;
+        g.lse[hb * Rp + r] = none ? -__builtin_inff() : -lse / a.scale;
+        g.delta[hb * Rp + r] = none ? 0.f : -s;
       }
     }
   } else if (kScaled<T>) {
@@ -139,14 +138,20 @@ __device__ __forceinline__ float ds_scale(const AttnGradArgs& g, int hb, int lan
   return exp2_int(min(15 - e, 100));
 }
 
-// dk and dv of 32 NB keys a wave; the query rows pass by.
+// dk and dv of 32 NB keys a wave; the query rows pass by. With heads of 128
+// the accumulators and the K fragments take 160 of the 256 registers that two
+// waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads: 574
+// us against 760 with V in registers, of which 53 spill, 768 with one wave a
+// SIMD and two blocks of keys, 870 with workgroups of four waves).
 template <typename T, int DP, int W, int NB>
-__global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
+__global__ __launch_bounds__(64 * W, 2) void attn_dkv_kernel(AttnGradArgs g) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
   __shared__ __align__(1024) uint8_t smem[2][2][TL::kBytes];
-  __shared__ __align__(1024) float stats[2][2][kAttnRows];   // lse2 and delta of a tile's rows
+  constexpr bool kHoldV = DP == 64;   // in registers, else in LDS
+  __shared__ __align__(1024) uint8_t held[kHoldV ? 16 : W * NB * 32 * TL::kRowBytes];
+  __shared__ __align__(1024) float stats[2][2][kAttnRows];   // -lse / scale and -delta of a tile's rows
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const AttnPlace at = attn_place(a, blockIdx.x, false);
@@ -155,12 +160,12 @@ __global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
   const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
   const T* dop = static_cast<const T*>(g.dout.p) + b * g.dout.batch + (int64_t)hk * G * g.dout.head;
   const int64_t Rp = (int64_t)g.row_blocks * kAttnPrepRows;
-  const float *lse2 = g.lse2 + at.hb * Rp, *delta = g.delta + at.hb * Rp;
-  const float c = ds_scale<T>(g, at.hb, lane), pscale_log2 = kScaled<T> ? 10.f : 0.f, dsc = kScaled<T> ? c / kProbScale : 1.f;
+  const float *lse = g.lse + at.hb * Rp, *delta = g.delta + at.hb * Rp;
+  const float c = ds_scale<T>(g, at.hb, lane), dsc = kScaled<T> ? c / kProbScale : 1.f;
 
   // this lane's keys, as operand B (of both products that give scores)
   const int key0 = at.block * (32 * NB * W) + wave * (32 * NB);
-  u32x4 kf[NB][TL::kSteps], vf[NB][TL::kSteps];
+  u32x4 kf[NB][TL::kSteps], vf[kHoldV ? NB : 1][TL::kSteps];
   bool live[NB];
   int first[NB];   // the first row that sees the key
 #pragma unroll
@@ -175,9 +180,14 @@ __global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
       const int d = 16 * s + 8 * h;
       const bool in = live[n] && d < D;
       kf[n][s] = in ? *reinterpret_cast<const u32x4*>(kr + d) : u32x4{0, 0, 0, 0};
-      vf[n][s] = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
+      const u32x4 v = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
+      if constexpr (kHoldV)
+        vf[n][s] = v;
+      else   // (read by this wave alone)
+        *reinterpret_cast<u32x4*>(held + (wave * NB + n) * 32 * TL::kRowBytes + (typename TL::Lane(lane).straight ^ (s << 5))) = v;
     }
   }
+  const uint8_t* my_v = held + (kHoldV ? 0 : wave * NB * 32 * TL::kRowBytes);
   // the rows of this workgroup: from its first key's first on, in its part of
   // the split. Rows that see no key at all are read as zeros.
   const int wg_key = at.block * (32 * NB * W);
@@ -214,7 +224,7 @@ __global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
       lds_transfer_16(rd, td + n * 1024, in ? (uint32_t)(((i - i0) * g.dout.token + hd * g.dout.head + ch * 8) * 2) : kPastEnd);
     }
     if (wave < 2) {   // (rows up to whole tiles are there)
-      const auto rs = rows_resource((wave == 0 ? lse2 : delta) + row0, kAttnRows * 4);
+      const auto rs = rows_resource((wave == 0 ? lse : delta) + row0, kAttnRows * 4);
       lds_transfer_4(rs, reinterpret_cast<uint8_t*>(stats[stage][wave]), lane * 4);
     }
   };
@@ -234,9 +244,22 @@ __global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) {
       if (row0 + 32 * rb + 31 < w_first) continue;   // none of these rows sees a key of this wave
+      // The scores' accumulators start with -lse / scale, those of do v^T with
+      // -delta, each row's in its registers.
       f32x16 s[NB], dp[NB];
+      u32x4 p[2][NB];
+      auto start = [&](const float* rows, f32x16(&to)[NB]) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) s[n] = dp[n] = f32x16{};
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(rows + 32 * rb + 8 * q + 4 * h);
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[n][4 * q + i] = v[i];
+        }
+      };
+      const bool part = row0 + 32 * rb < w_all;
+      start(tl, s);
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
         const u32x4 qf = TL::straight(tq, pl, rb, st);
@@ -244,54 +267,57 @@ __global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
         for (int n = 0; n < NB; ++n) s[n] = mma<T>(qf, kf[n][st], s[n]);
       }
 #pragma unroll
-      for (int st = 0; st < TL::kSteps; ++st) {
-        const u32x4 df = TL::straight(td, pl, rb, st);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) dp[n] = mma<T>(df, vf[n][st], dp[n]);
-      }
-      f32x4 rl[4], rd[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        rl[q] = *reinterpret_cast<const f32x4*>(tl + 32 * rb + 8 * q + 4 * h);
-        rd[q] = *reinterpret_cast<const f32x4*>(tD + 32 * rb + 8 * q + 4 * h);
-      }
-      u32x4 p[2][NB], ds[2][NB];
-      const bool part = row0 + 32 * rb < w_all;
-#pragma unroll
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          s[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], a.scale_log2, pscale_log2 - rl[i / 4][i % 4]));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float d = dp[n][i] - rd[i / 4][i % 4];
-          dp[n][i] = kScaled<T> ? s[n][i] * dsc * d : s[n][i] * d;
-        }
+          s[n][i] = __builtin_amdgcn_exp2f(kScaled<T> ? __builtin_fmaf(s[n][i], a.scale_log2, 10.f) : s[n][i] * a.scale_log2);
         if (part) {
           const int lim = first[n] - row0 - 32 * rb - 4 * h;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const bool sees = 8 * (i / 4) + i % 4 >= lim;
-            s[n][i] = sees ? s[n][i] : 0.f;
-            dp[n][i] = sees ? dp[n][i] : 0.f;
-          }
+          for (int i = 0; i < 16; ++i) s[n][i] = 8 * (i / 4) + i % 4 >= lim ? s[n][i] : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          p[u][n] = as_operand<T>(s[n], u);
-          ds[u][n] = as_operand<T>(dp[n], u);
-        }
+        for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(s[n], u);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < TL::kBlocks; ++i) {
-          const u32x4 df = TL::turned(td, pl, 2 * rb + u, i), qf = TL::turned(tq, pl, 2 * rb + u, i);
+          const u32x4 df = TL::turned(td, pl, 2 * rb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            dv[i][n] = mma<T>(df, p[u][n], dv[i][n]);
-            dk[i][n] = mma<T>(qf, ds[u][n], dk[i][n]);
-          }
+          for (int n = 0; n < NB; ++n) dv[i][n] = mma<T>(df, p[u][n], dv[i][n]);
+        }
+      start(tD, dp);
+#pragma unroll
+      for (int st = 0; st < TL::kSteps; ++st) {
+        const u32x4 df = TL::straight(td, pl, rb, st);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          if constexpr (kHoldV)
+            dp[n] = mma<T>(df, vf[n][st], dp[n]);
+          else
+            dp[n] = mma<T>(df, TL::straight(my_v, pl, n, st), dp[n]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[n][i] *= kScaled<T> ? s[n][i] * dsc : s[n][i];
+        if (part) {   // (do may hold what times 0 is NaN)
+          const int lim = first[n] - row0 - 32 * rb - 4 * h;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dp[n][i] = 8 * (i / 4) + i % 4 >= lim ? dp[n][i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(dp[n], u);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < TL::kBlocks; ++i) {
+          const u32x4 qf = TL::turned(tq, pl, 2 * rb + u, i);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) dk[i][n] = mma<T>(qf, p[u][n], dk[i][n]);
         }
     }
   }
@@ -337,9 +363,10 @@ __global__ __launch_bounds__(64 * W) void attn_dkv_kernel(AttnGradArgs g) {
   }
 }
 
-// dq of 32 NB query rows a wave; the keys pass by, as in the forward.
+// dq of 32 NB query rows a wave; the keys pass by, as in the forward (4608
+// tokens, 24 heads of 128: 345 us, 1.13 PFLOP/s).
 template <typename T, int DP, int W, int NB>
-__global__ __launch_bounds__(64 * W) void attn_dq_kernel(AttnGradArgs g) {
+__global__ __launch_bounds__(64 * W, 2) void attn_dq_kernel(AttnGradArgs g) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
@@ -360,12 +387,12 @@ __global__ __launch_bounds__(64 * W) void attn_dq_kernel(AttnGradArgs g) {
   const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
   u32x4 qf[NB][TL::kSteps], df[NB][TL::kSteps];
   int last[NB];
-  float lse2[NB], delta[NB];
+  float lse[NB], delta[NB];   // both negative
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const int r = r0 + 32 * n + lr, i = r / G, hd = r - i * G;
     last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
-    lse2[n] = r < R ? g.lse2[at.hb * Rp + r] : __builtin_inff();
+    lse[n] = r < R ? g.lse[at.hb * Rp + r] * a.scale_log2 : -__builtin_inff();   // in base 2
     delta[n] = r < R ? g.delta[at.hb * Rp + r] : 0.f;
 #pragma unroll
     for (int s = 0; s < TL::kSteps; ++s) {
@@ -397,11 +424,19 @@ __global__ __launch_bounds__(64 * W) void attn_dq_kernel(AttnGradArgs g) {
     const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
     const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
     uint8_t *tk = smem[stage][0] + wave * NT * 1024, *tv = smem[stage][1] + wave * NT * 1024;
+    if (keep == ~0ull) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const bool in = keep >> row_of[n] & 1;
-      lds_transfer_16(rk, tk + n * 1024, in ? vk[n] : kPastEnd);
-      lds_transfer_16(rv, tv + n * 1024, in ? vv[n] : kPastEnd);
+      for (int n = 0; n < NT; ++n) {
+        lds_transfer_16(rk, tk + n * 1024, vk[n]);
+        lds_transfer_16(rv, tv + n * 1024, vv[n]);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bool in = keep >> row_of[n] & 1;
+        lds_transfer_16(rk, tk + n * 1024, in ? vk[n] : kPastEnd);
+        lds_transfer_16(rv, tv + n * 1024, in ? vv[n] : kPastEnd);
+      }
     }
   };
   auto mask_byte = [&](int k0) -> int {
@@ -437,7 +472,11 @@ __global__ __launch_bounds__(64 * W) void attn_dq_kernel(AttnGradArgs g) {
     for (int kb = 0; kb < 2; ++kb) {
       f32x16 s[NB], dp[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) s[n] = dp[n] = f32x16{};
+      for (int n = 0; n < NB; ++n) {
+        s[n] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[n][i] = delta[n];
+      }
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
         const u32x4 f = TL::straight(tk, pl, kb, st);
@@ -455,8 +494,8 @@ __global__ __launch_bounds__(64 * W) void attn_dq_kernel(AttnGradArgs g) {
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], a.scale_log2, -lse2[n]));
-          dp[n][i] = kScaled<T> ? p * c * (dp[n][i] - delta[n]) : p * (dp[n][i] - delta[n]);
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], a.scale_log2, lse[n]));
+          dp[n][i] *= kScaled<T> ? p * c : p;
         }
         if (part) {
           const int lim = last[n] - k0 - 32 * kb - 4 * h;
@@ -553,13 +592,13 @@ hipError_t launch_bwd(const AttnGradArgs& args, const AttnGradPlan& plan, hipStr
     g.f.split_keys = s.each;
     const dim3 grid((unsigned)(s.blocks * s.splits * heads));
     if (keys && g.f.D <= 64)
-      hipLaunchKernelGGL((attn_dkv_kernel<T, 64, 4, 1>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((attn_dkv_kernel<T, 64, 8, 1>), grid, dim3(512), 0, st, g);
     else if (keys)
-      hipLaunchKernelGGL((attn_dkv_kernel<T, 128, 4, 1>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((attn_dkv_kernel<T, 128, 8, 1>), grid, dim3(512), 0, st, g);
     else if (g.f.D <= 64)
-      hipLaunchKernelGGL((attn_dq_kernel<T, 64, 4, 1>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((attn_dq_kernel<T, 64, 8, 1>), grid, dim3(512), 0, st, g);
     else
-      hipLaunchKernelGGL((attn_dq_kernel<T, 128, 4, 1>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((attn_dq_kernel<T, 128, 8, 1>), grid, dim3(512), 0, st, g);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (s.splits > 1) {

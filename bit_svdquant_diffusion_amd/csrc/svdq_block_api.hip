@@ -147,7 +147,7 @@ svdq_status check_attention(const svdq_attention_desc* d) {
     return SVDQ_ERR_SHAPE;
   const int64_t heads = d->samples * d->kv_heads, rows = d->queries * group;
   const int64_t blocks = (std::max(rows, d->keys) + kAttnBlock - 1) / kAttnBlock;
-  if (heads > 65535 || rows >= most || blocks * std::max<int64_t>(heads, 1) > ((int64_t)1 << 23)) return SVDQ_ERR_SHAPE;
+  if (heads > 65535 || rows >= most || blocks * std::max<int64_t>(heads, 1) > ((int64_t)1 << 22)) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 // a tensor's place, and the span of 64 of its tokens (with `group` heads)
@@ -413,7 +413,7 @@ svdq_status svdq_attention_backward(const svdq_attention_desc* d, const svdq_hea
   SVDQ_TRY(check_ws(ws, ws_bytes, w.total));
   SVDQ_TRY(check_device());
   uint8_t* at = (uint8_t*)ws;
-  g.lse2 = (float*)(at + w.lse2);
+  g.lse = (float*)(at + w.lse);
   g.delta = (float*)(at + w.delta);
   g.tops = (float*)(at + w.tops);
   g.f.part = (float*)(at + w.part);

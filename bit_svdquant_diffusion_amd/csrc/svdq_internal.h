@@ -209,7 +209,7 @@ struct AttnArgs {
 struct AttnGradArgs {
   AttnArgs f;
   Heads dout, dq, dk, dv;
-  float *lse2, *delta;       // [B Hk][row_blocks kAttnPrepRows]
+  float *lse, *delta;        // -lse / scale and -delta, [B Hk][row_blocks kAttnPrepRows]
   float* tops;               // [B Hk][row_blocks + key_blocks], fp16 alone
   int row_blocks, key_blocks;
 };

@@ -372,7 +372,7 @@ inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group
 // of at least four, whose results are joined: about two workgroups a CU.
 // (Workspaces' sizes are asked for without a device, so the plan is this
 // card's.)
-constexpr int kAttnCus = 256, kAttnTile = 64, kAttnBlock = 128, kAttnPrepRows = 256;
+constexpr int kAttnCus = 256, kAttnTile = 64, kAttnBlock = 256, kAttnPrepRows = 256;
 struct AttnSplit {
   int blocks, splits, each;   // each: passing rows of a part
 };
@@ -407,7 +407,7 @@ struct AttnGradPlan {
 struct AttnGradWs {
   AttnGradPlan plan;
   int row_blocks, key_blocks;
-  size_t lse2, delta, tops, part, total;
+  size_t lse, delta, tops, part, total;
 };
 inline AttnGradWs attn_grad_ws(const AttnSizes& s, bool scaled) {
   AttnGradWs w;
@@ -417,7 +417,7 @@ inline AttnGradWs attn_grad_ws(const AttnSizes& s, bool scaled) {
   w.row_blocks = (int)((rows + kAttnPrepRows - 1) / kAttnPrepRows);
   w.key_blocks = scaled ? (int)((s.Lk + kAttnPrepRows - 1) / kAttnPrepRows) : 0;
   const size_t padded = align256((size_t)heads * w.row_blocks * kAttnPrepRows * 4);
-  w.lse2 = 0;
+  w.lse = 0;
   w.delta = padded;
   w.tops = 2 * padded;
   w.part = w.tops + (scaled ? align256((size_t)heads * (w.row_blocks + w.key_blocks) * 4) : 0);

@@ -200,7 +200,9 @@ def attention(q, k, v, mask, causal, scale, grad=None):
             dout, o1, l1 = grad
             do = torch.where(live[:, None], dout[b, :, h].double(), 0.0)
             p = torch.where(see, torch.exp(s - torch.where(live, l1[b, h].double(), 0.0)[:, None]), 0.0)
-            e_p = p * (half + e_s + torch.where(see, (s.abs() + l1[b, h].double().abs().clamp(max=1e30)[:, None]) * 4 * U, 0.0) + 4 * U)
+            # lse enters as the value that the product's accumulator starts with
+            # (D / 16 further roundings of a sum that holds it)
+            e_p = p * (half + e_s + torch.where(see, (s.abs() + l1[b, h].double().abs().clamp(max=1e30)[:, None]) * (4 + D / 16) * U, 0.0) + 4 * U)
             # A probability below 2^-126 is zero in fp32 (the exponential has no
             # subnormal results), and so is a ds: p is off by 2^-126 at most
             # beside its relative error, ds by that much of dp - delta and
