@@ -51,8 +51,9 @@ svdq_status check_device(int* cus, void** scratch_ptr, unsigned kernels) {
       s = ok ? 1 : 2;
       if (ok) {
         const unsigned sets =
-            (prepare_norm() == hipSuccess ? kKernelsNorm : 0) | (prepare_fp8() == hipSuccess ? kKernelsFp8 : 0);
-        if (sets != (kKernelsNorm | kKernelsFp8)) (void)hipGetLastError();   // not the next launch's error
+            (prepare_norm() == hipSuccess ? kKernelsNorm : 0) | (prepare_fp8() == hipSuccess ? kKernelsFp8 : 0) |
+            (prepare_attention() == hipSuccess && prepare_attention_grad() == hipSuccess ? kKernelsAttention : 0);
+        if (sets != (kKernelsNorm | kKernelsFp8 | kKernelsAttention)) (void)hipGetLastError();   // not the next launch's error
         g_dev_kernels[dev].store(sets, std::memory_order_relaxed);
         g_dev_cus[dev].store(p.multiProcessorCount, std::memory_order_relaxed);
         g_dev_scratch[dev].store(sp, std::memory_order_relaxed);

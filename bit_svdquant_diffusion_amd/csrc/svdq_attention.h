@@ -21,21 +21,29 @@
 
 namespace svdq {
 
-// What a workgroup works on. Workgroup i runs on XCD i % 8; each XCD takes a
-// contiguous run of the heads' blocks, so that the tiles that pass by stay in
-// its L2. `last_first`: a causal launch starts with the blocks that see most.
-struct AttnPlace {
-  int hb, block, split;
-};
-__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int id, bool last_first) {
-  const int per_head = a.blocks * a.splits, n = per_head * a.B * a.Hk;
-  const int xcd = id & 7, per = n >> 3, rem = n & 7;
-  const int t = xcd * per + min(xcd, rem) + (id >> 3);
-  const int hb = t / per_head, in = t - hb * per_head, block = in / a.splits;
-  return AttnPlace{hb, a.causal && last_first ? a.blocks - 1 - block : block, in % a.splits};
-}
+constexpr int kAttnRows = kAttnTile;   // of a tile
 
-constexpr int kAttnRows = 64;   // of a tile
+// A workgroup's pieces, from its arguments.
+template <bool SHARED>
+struct AttnDeal;
+template <>
+struct AttnDeal<false> {
+  struct Shares {};
+  AttnWhole walk;
+  __device__ __forceinline__ AttnDeal(const AttnPlan&, int, const Shares&) {}
+};
+template <>
+struct AttnDeal<true> {
+  typedef AttnShares Shares;
+  AttnWalk walk;
+  __device__ __forceinline__ AttnDeal(const AttnPlan& p, int w, const Shares& s) : walk(p, w, s.at[w]) {}
+};
+__device__ __forceinline__ void note_span(const AttnArgs& a, const AttnPiece& at, int w) {
+  if (threadIdx.x == 0) {
+    if (at.starts) a.spans[2 * at.unit] = w;
+    if (at.ends) a.spans[2 * at.unit + 1] = w;
+  }
+}
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -107,13 +115,28 @@ __device__ __forceinline__ u32x4 rows_resource(const void* base, int bytes) {
   return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)bytes, 0x00020000u};
 }
 
-// all transfers have arrived and all LDS reads returned, then the workgroup's
-// barrier; nothing moves across
+// all but the last N transfers have arrived and all LDS reads returned, then
+// the workgroup's barrier; nothing moves across
+template <int N = 0>
 __device__ __forceinline__ void tile_barrier() {
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));   // vmcnt(N) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// The order of what stands before in its block, for the scheduler: AHEAD LDS
+// reads, then the products with STEP further reads after each while there are
+// any. (Left to itself the compiler may read a fragment right before its
+// product and wait for it: the forward at 4608 tokens 270 us against 244.)
+template <int PRODUCTS, int READS, int STEP, int AHEAD, int I = 0>
+__device__ __forceinline__ void sched_products() {
+  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+  if constexpr (I < PRODUCTS) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (AHEAD + (I + 1) * STEP <= READS) __builtin_amdgcn_sched_group_barrier(0x100, STEP, 0);
+    sched_products<PRODUCTS, READS, STEP, AHEAD, I + 1>();
+  }
 }
 
 template <int DP>

@@ -167,7 +167,7 @@ Heads attn_heads(const svdq_heads* t, const svdq_attention_desc* d, bool of_q) {
   return heads_of(t, d->samples, of_q ? d->queries : d->keys, of_q ? d->heads : d->kv_heads);
 }
 AttnSizes sizes_of(const svdq_attention_desc* d) {
-  return AttnSizes{d->samples, d->queries, d->keys, d->heads, d->kv_heads, d->head_dim};
+  return AttnSizes{d->samples, d->queries, d->keys, d->heads, d->kv_heads, d->head_dim, d->causal != 0, d->dtype == SVDQ_DT_F16};
 }
 AttnArgs attn_args(const svdq_attention_desc* d, const uint8_t* mask, int64_t mask_batch) {
   AttnArgs a;
@@ -362,13 +362,14 @@ svdq_status svdq_attention_forward(const svdq_attention_desc* d, const svdq_head
   if (!aligned(lse, 4)) return SVDQ_ERR_SHAPE;
   const AttnWs w = attn_ws(sizes_of(d));
   SVDQ_TRY(check_ws(ws, ws_bytes, w.total));
-  SVDQ_TRY(check_device());
+  SVDQ_TRY(check_device(nullptr, nullptr, kKernelsAttention));
   a.lse = lse;
-  a.blocks = w.split.blocks;
-  a.splits = w.split.splits;
-  a.split_keys = w.split.each;
+  a.cost = attn_row_cost(sizes_of(d));
+  a.plan = w.plan;
+  a.part_rows = (int)attn_part_rows(a.cost);
   a.part = (float*)((uint8_t*)ws + w.part);
   a.part_lse = (float*)((uint8_t*)ws + w.part_lse);
+  a.spans = (int*)((uint8_t*)ws + w.spans);
   hipStream_t st = (hipStream_t)stream;
   return after_launch(launch_attention(a, st), st);
 }
@@ -376,7 +377,7 @@ svdq_status svdq_attention_forward(const svdq_attention_desc* d, const svdq_head
 svdq_status svdq_attention_backward_workspace_bytes(const svdq_attention_desc* d, size_t* out) {
   SVDQ_TRY(check_attention(d));
   if (!out) return SVDQ_ERR_NULL;
-  *out = d->samples * (d->queries + d->keys) == 0 ? 0 : attn_grad_ws(sizes_of(d), d->dtype == SVDQ_DT_F16).total;
+  *out = d->samples * (d->queries + d->keys) == 0 ? 0 : attn_grad_ws(sizes_of(d)).total;
   return SVDQ_OK;
 }
 
@@ -409,18 +410,20 @@ svdq_status svdq_attention_backward(const svdq_attention_desc* d, const svdq_hea
     g.dk = attn_heads(dk, d, false);
     g.dv = attn_heads(dv, d, false);
   }
-  const AttnGradWs w = attn_grad_ws(sizes_of(d), d->dtype == SVDQ_DT_F16);
+  const AttnGradWs w = attn_grad_ws(sizes_of(d));
   SVDQ_TRY(check_ws(ws, ws_bytes, w.total));
-  SVDQ_TRY(check_device());
+  SVDQ_TRY(check_device(nullptr, nullptr, kKernelsAttention));
   uint8_t* at = (uint8_t*)ws;
   g.lse = (float*)(at + w.lse);
   g.delta = (float*)(at + w.delta);
-  g.tops = (float*)(at + w.tops);
+  g.top_do = (float*)(at + w.top_do);
+  g.top_v = (float*)(at + w.top_v);
   g.f.part = (float*)(at + w.part);
-  g.row_blocks = w.row_blocks;
-  g.key_blocks = w.key_blocks;
+  g.f.spans = (int*)(at + w.spans);
+  g.row_blocks = w.dq.blocks;
+  g.key_runs = w.key_runs;
   hipStream_t st = (hipStream_t)stream;
-  return after_launch(launch_attention_grad(g, w.plan, st), st);
+  return after_launch(launch_attention_grad(g, w, st), st);
 }
 
 }  // extern "C"

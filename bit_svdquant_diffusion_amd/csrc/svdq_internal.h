@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "svdq.h"
+#include "svdq_layout.h"
 
 namespace svdq {
 
@@ -201,21 +202,25 @@ struct AttnArgs {
   const uint8_t* mask;       // [B][Lk], may be null
   int64_t mask_batch;
   float* lse;                // [B][H][Lq]
-  // the launch: blocks of held rows (or keys) times parts of the passing ones
-  int blocks, splits, split_keys;
-  float* part;               // [splits][B Hk][rows][D] (dk and dv: [keys][2][D]) with several parts
-  float* part_lse;           // [splits][B Hk][rows]
+  AttnCost cost;             // the launch: what is held and what passes,
+  AttnPlan plan;             // and how it is dealt
+  int part_rows;
+  float* part;               // parts of shared units: [2 grid][part_rows][D] (dk and dv: [2][D])
+  float* part_lse;           // [2 grid][part_rows]
+  int* spans;                // of shared units: the first and the last workgroup
 };
 struct AttnGradArgs {
   AttnArgs f;
   Heads dout, dq, dk, dv;
-  float *lse, *delta;        // -lse / scale and -delta, [B Hk][row_blocks kAttnPrepRows]
-  float* tops;               // [B Hk][row_blocks + key_blocks], fp16 alone
-  int row_blocks, key_blocks;
+  float *lse, *delta;        // -lse / scale and -delta, [B Hk][whole blocks of rows]
+  int row_blocks;
+  float *top_do, *top_v;     // fp16: the largest magnitudes [B Hk][row_blocks], [B Hk][key_runs]
+  int key_runs;
 };
-struct AttnGradPlan;
+hipError_t prepare_attention();   // one-time per device: kernels' dynamic LDS attribute
+hipError_t prepare_attention_grad();
 hipError_t launch_attention(const AttnArgs& a, hipStream_t st);
-hipError_t launch_attention_grad(const AttnGradArgs& g, const AttnGradPlan& plan, hipStream_t st);
+hipError_t launch_attention_grad(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st);
 
 // E4M3 quantizers (svdq_fp8_quant.hip)
 // (plain: the scale bytes as svdq_fp8_quantize documents them, not the product's order)
@@ -279,7 +284,7 @@ inline dim3 many_groups(int64_t n) {
 }
 
 // shared by the files with C entry points (svdq_api.hip)
-enum KernelSets : unsigned { kKernelsNorm = 1, kKernelsFp8 = 2 };
+enum KernelSets : unsigned { kKernelsNorm = 1, kKernelsFp8 = 2, kKernelsAttention = 4 };
 svdq_status check_device(int* cus = nullptr, void** scratch_ptr = nullptr, unsigned kernels = 0);
 svdq_status after_launch(hipError_t e, hipStream_t s);
 

@@ -25,7 +25,7 @@ constexpr int kStepK = 128;       // K per stage-1 step (two INT4 groups)
 constexpr int kMaxRank = 128;
 
 inline int rank32(int r) { return (r + 31) / 32 * 32; }
-inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+constexpr size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // K must hold whole scale groups of the 4-bit GEMM's K step: 64 channels
 // (INT4) or 128 (MXFP4); N whole 16-byte runs of bf16 Y (8 channels).
@@ -367,62 +367,204 @@ inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group
   return p.runs > 1 ? (size_t)groups * p.runs * 4 * C * 4 : 0;
 }
 
-// Attention: how the held rows (keys, for their gradients) lie in blocks of
-// `block` and, where these are fewer than the CUs, the passing tiles in parts
-// of at least four, whose results are joined: about two workgroups a CU.
-// (Workspaces' sizes are asked for without a device, so the plan is this
-// card's.)
-constexpr int kAttnCus = 256, kAttnTile = 64, kAttnBlock = 256, kAttnPrepRows = 256;
-struct AttnSplit {
-  int blocks, splits, each;   // each: passing rows of a part
+// Attention: the held rows (keys, for their gradients) of a key head lie in
+// `blocks` of kAttnBlock, the other side passes by in tiles of kAttnTile; a
+// unit is a block's walk along its tiles. With as many units as CUs a workgroup
+// takes a unit. With fewer, up to one workgroup a CU share the units evenly,
+// tile by tile: a unit whose tiles fall to several has its parts joined by
+// another kernel. (More units than CUs even out badly, too, 432 units in two
+// rounds, but there power bounds the products: with half of the CUs busy each
+// is a third faster. Workspaces' sizes are asked for without a device, so the
+// plan is this card's.)
+constexpr int kAttnCus = 256, kAttnTile = 64, kAttnBlock = 256, kAttnKeyRun = 256;
+struct AttnCost {
+  int held, passing, group;   // rows (queries times the group, or keys) and the group's heads
+  int offset;                 // keys - queries where causal
+  int causal, by_keys;        // by_keys: keys are held
 };
-inline AttnSplit attn_split(int64_t held, int64_t passing, int64_t heads, int block) {
-  const int64_t blocks = (held + block - 1) / block, tiles = (passing + kAttnTile - 1) / kAttnTile;
-  int64_t splits = 1;
-  if (blocks > 0 && blocks * heads < kAttnCus) splits = std::min(2 * kAttnCus / (blocks * heads), tiles / 4);
-  if (splits < 1) splits = 1;
-  const int64_t each = tiles > 0 ? (tiles + splits - 1) / splits : 1;
-  return AttnSplit{(int)blocks, tiles > 0 ? (int)((tiles + each - 1) / each) : 1, (int)each * kAttnTile};
+// the tiles of block b: first and one past the last
+SVDQ_HD inline void attn_tiles(const AttnCost& c, int b, int* first, int* last) {
+  const int all = (c.passing + kAttnTile - 1) / kAttnTile;
+  *first = 0;
+  *last = all;
+  if (!c.causal) return;
+  if (c.by_keys) {   // from the first row that sees the block's first key on
+    const int64_t q = (int64_t)b * kAttnBlock - c.offset, r = q > 0 ? q * c.group : 0;
+    *first = r < c.passing ? (int)r / kAttnTile : all;
+  } else {   // up to the last key that the block's last row sees
+    const int end = c.held - b * kAttnBlock < kAttnBlock ? c.held : (b + 1) * kAttnBlock;
+    const int k = (int)((unsigned)(end - 1) / (unsigned)c.group) + c.offset + 1;
+    *last = k <= 0 ? 0 : k < c.passing ? (k + kAttnTile - 1) / kAttnTile : all;
+  }
+}
+// (a block without tiles still writes its zeros)
+SVDQ_HD inline int attn_cost(const AttnCost& c, int b) {
+  int first, last;
+  attn_tiles(c, b, &first, &last);
+  return last > first ? last - first : 1;
+}
+struct AttnPlan {
+  int blocks, grid, heads;
+  int shared;   // the units are shared: workgroup w's tiles start at total w / grid of their sequence
+  int total;
+};
+inline AttnPlan attn_plan(const AttnCost& c, int64_t heads) {
+  AttnPlan p;
+  p.blocks = (int)(((int64_t)c.held + kAttnBlock - 1) / kAttnBlock);
+  p.heads = (int)heads;
+  const int64_t units = p.blocks * heads;
+  p.grid = (int)units;
+  p.shared = p.total = 0;
+  if (units == 0 || units >= kAttnCus) return p;
+  int64_t total = 0;
+  for (int b = 0; b < p.blocks; ++b) total += attn_cost(c, b);
+  total *= heads;
+  // a part is at least four tiles, and nearly a unit a workgroup is not worth joining
+  const int64_t grid = total / 4 < kAttnCus ? total / 4 : kAttnCus;
+  if (total >= ((int64_t)1 << 31) || (c.causal ? grid <= units : grid * 9 <= units * 10)) return p;
+  p.grid = (int)grid;
+  p.shared = 1;
+  p.total = (int)total;
+  return p;
+}
+// Where the workgroups of a shared launch start, found on the host.
+struct AttnStart {
+  uint16_t hb, block;
+  int skip;   // tiles of the block before
+};
+struct AttnShares {
+  AttnStart at[kAttnCus];
+};
+inline void attn_shares(const AttnCost& c, const AttnPlan& p, AttnShares* s) {
+  int hb = 0, block = 0;
+  int64_t before = 0, cost = attn_cost(c, 0);   // tiles before (hb, block), and its own
+  for (int w = 0; w < p.grid; ++w) {
+    const int64_t x = (int64_t)p.total * w / p.grid;
+    while (x >= before + cost) {
+      before += cost;
+      if (++block == p.blocks) {
+        block = 0;
+        ++hb;
+      }
+      cost = attn_cost(c, block);
+    }
+    s->at[w] = AttnStart{(uint16_t)hb, (uint16_t)block, (int)(x - before)};
+  }
+}
+// A workgroup's pieces: its unit, or its parts of shared units. Workgroup i
+// runs on XCD i % 8; each XCD takes a contiguous run of the heads' units, so
+// that the tiles that pass by stay in its L2.
+struct AttnPiece {
+  int hb, block, unit;
+  int first, last;       // tiles of the passing side
+  int part;              // its place in the workspace, -1: the unit is whole
+  bool starts, ends;     // the unit's first, last tile is in it
+};
+SVDQ_HD inline int attn_place(const AttnPlan& p, int id) {
+  const int xcd = id & 7, per = p.grid >> 3, rem = p.grid & 7;
+  return xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+}
+struct AttnWhole {   // a unit a workgroup
+  bool more = true;
+  SVDQ_HD bool next(const AttnCost& c, const AttnPlan& p, int w, AttnPiece& o) {
+    if (!more) return false;
+    more = false;
+    o.unit = w;
+    o.hb = w / p.blocks;
+    o.block = w - o.hb * p.blocks;
+    // (causal: the blocks that see most first)
+    if (c.causal && !c.by_keys) o.block = p.blocks - 1 - o.block;
+    attn_tiles(c, o.block, &o.first, &o.last);
+    o.part = -1;
+    o.starts = o.ends = true;
+    return true;
+  }
+};
+struct AttnWalk {   // parts of shared units
+  int hb, block, skip, left;
+  SVDQ_HD AttnWalk(const AttnPlan& p, int w, const AttnStart& at) : hb(at.hb), block(at.block), skip(at.skip) {
+    const int64_t x = (int64_t)p.total * w, y = x + p.total;
+    left = (int)(y / p.grid - x / p.grid);
+  }
+  SVDQ_HD bool next(const AttnCost& c, const AttnPlan& p, int w, AttnPiece& o) {
+    if (left <= 0) return false;
+    int first, last;
+    attn_tiles(c, block, &first, &last);
+    const int cost = last > first ? last - first : 1, n = cost - skip < left ? cost - skip : left;
+    o.unit = hb * p.blocks + block;
+    o.hb = hb;
+    o.block = block;
+    o.first = first + skip;
+    o.last = first + skip + n < last ? first + skip + n : last;
+    o.part = n == cost ? -1 : 2 * w + (skip == 0);
+    o.starts = skip == 0;
+    o.ends = skip + n == cost;
+    left -= n;
+    skip = 0;
+    if (++block == p.blocks) {
+      block = 0;
+      ++hb;
+    }
+    return true;
+  }
+};
+// The parts of a unit that started with workgroup w0 and ended with w1 > w0 lie
+// at 2 w0 + 1, 2 (w0 + 1), ... 2 w1.
+SVDQ_HD inline int64_t attn_part(int w0, int w) { return 2 * w + (w == w0); }
+// rows of a part in the workspace; each workgroup has at most two
+inline int64_t attn_part_rows(const AttnCost& c) { return c.held < kAttnBlock ? c.held : kAttnBlock; }
+inline size_t attn_parts(const AttnCost& c, const AttnPlan& p) {
+  return p.shared ? (size_t)2 * p.grid * attn_part_rows(c) : 0;
 }
 struct AttnSizes {
   int64_t B, Lq, Lk, H, Hk, D;
+  bool causal, scaled;   // scaled: fp16
 };
+inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
+  return AttnCost{(int)(s.Lq * (s.H / s.Hk)), (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0};
+}
+inline AttnCost attn_key_cost(const AttnSizes& s) {
+  return AttnCost{(int)s.Lk, (int)(s.Lq * (s.H / s.Hk)), (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1};
+}
+constexpr size_t kAttnSpans = align256((size_t)kAttnCus * 8);   // of shared units: the first and the last workgroup
 struct AttnWs {
-  AttnSplit split;
-  size_t part, part_lse, total;
+  AttnPlan plan;
+  size_t part, part_lse, spans, total;
 };
 inline AttnWs attn_ws(const AttnSizes& s) {
   AttnWs w;
-  const int64_t heads = s.B * s.Hk, rows = s.Lq * (s.H / s.Hk);
-  w.split = attn_split(rows, s.Lk, heads, kAttnBlock);
-  const size_t n = w.split.splits > 1 ? (size_t)w.split.splits * heads * rows : 0;
+  const AttnCost c = attn_row_cost(s);
+  w.plan = attn_plan(c, s.B * s.Hk);
+  const size_t n = attn_parts(c, w.plan);
   w.part = 0;
   w.part_lse = align256(n * s.D * 4);
-  w.total = w.part_lse + align256(n * 4);
+  w.spans = w.part_lse + align256(n * 4);
+  w.total = w.spans + (w.plan.shared ? kAttnSpans : 0);
   return w;
 }
-struct AttnGradPlan {
-  AttnSplit dkv, dq;
-};
+// The backward's: -lse / scale and -delta of the rows (whole blocks), the
+// largest |do| of a block of rows and |v| of a run of keys (fp16), and the
+// parts of dq, then of dk and dv.
 struct AttnGradWs {
-  AttnGradPlan plan;
-  int row_blocks, key_blocks;
-  size_t lse, delta, tops, part, total;
+  AttnPlan dkv, dq;
+  int key_runs;
+  size_t lse, delta, top_do, top_v, spans, part, total;
 };
-inline AttnGradWs attn_grad_ws(const AttnSizes& s, bool scaled) {
+inline AttnGradWs attn_grad_ws(const AttnSizes& s) {
   AttnGradWs w;
-  const int64_t heads = s.B * s.Hk, rows = s.Lq * (s.H / s.Hk);
-  w.plan.dkv = attn_split(s.Lk, rows, heads, kAttnBlock);
-  w.plan.dq = attn_split(rows, s.Lk, heads, kAttnBlock);
-  w.row_blocks = (int)((rows + kAttnPrepRows - 1) / kAttnPrepRows);
-  w.key_blocks = scaled ? (int)((s.Lk + kAttnPrepRows - 1) / kAttnPrepRows) : 0;
-  const size_t padded = align256((size_t)heads * w.row_blocks * kAttnPrepRows * 4);
+  const int64_t heads = s.B * s.Hk;
+  const AttnCost rows = attn_row_cost(s), keys = attn_key_cost(s);
+  w.dkv = attn_plan(keys, heads);
+  w.dq = attn_plan(rows, heads);
+  w.key_runs = s.scaled ? (int)((s.Lk + kAttnKeyRun - 1) / kAttnKeyRun) : 0;
+  const size_t padded = align256((size_t)heads * w.dq.blocks * kAttnBlock * 4);
   w.lse = 0;
   w.delta = padded;
-  w.tops = 2 * padded;
-  w.part = w.tops + (scaled ? align256((size_t)heads * (w.row_blocks + w.key_blocks) * 4) : 0);
-  const size_t a = w.plan.dkv.splits > 1 ? (size_t)w.plan.dkv.splits * heads * s.Lk * 2 * s.D * 4 : 0;
-  const size_t b = w.plan.dq.splits > 1 ? (size_t)w.plan.dq.splits * heads * rows * s.D * 4 : 0;
+  w.top_do = 2 * padded;
+  w.top_v = w.top_do + (s.scaled ? align256((size_t)heads * w.dq.blocks * 4) : 0);
+  w.spans = w.top_v + align256((size_t)heads * w.key_runs * 4);
+  w.part = w.spans + (w.dkv.shared || w.dq.shared ? kAttnSpans : 0);
+  const size_t a = attn_parts(keys, w.dkv) * 2 * s.D * 4, b = attn_parts(rows, w.dq) * s.D * 4;
   w.total = w.part + align256(a > b ? a : b);
   return w;
 }
