@@ -212,15 +212,15 @@ def lib() -> ctypes.CDLL:
         "svdq_fp8_backward_workspace_bytes": [P(Fp8Desc), i64, P(sz)],
         "svdq_fp8_backward": [P(Fp8Desc), P(Fp8Packed), vp, vp, i64, vp, vp, vp, vp, sz, vp],
         "svdq_fp8_quantize": [vp, i64, ctypes.c_int32, vp, vp, vp],
-        "svdq_residual_norm_forward": [P(ResidualDesc), vp, i64, vp, i64, P(ResidualParams), i64, vp, i64, vp, i64, vp, vp],
+        "svdq_residual_norm_forward": [P(ResidualDesc), vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
         "svdq_residual_norm_backward_workspace_bytes": [P(ResidualDesc), i64, P(sz)],
-        "svdq_residual_norm_backward": [P(ResidualDesc), vp, i64, vp, i64, vp, i64, vp, i64, P(ResidualParams), vp, i64, vp,
-                                        i64, vp, i64, P(ResidualGrads), ctypes.c_int32, vp, sz, vp],
-        "svdq_rope": [P(RopeDesc), P(Heads), P(Heads), vp, i64, vp, P(Heads), P(Heads), vp],
+        "svdq_residual_norm_backward": [P(ResidualDesc), vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp,
+                                        i64, vp, i64, vp, ctypes.c_int32, vp, sz, vp],
+        "svdq_rope": [P(RopeDesc), vp, vp, vp, i64, vp, vp, vp, vp],
         "svdq_attention_workspace_bytes": [P(AttentionDesc), P(sz)],
-        "svdq_attention_forward": [P(AttentionDesc), P(Heads), P(Heads), P(Heads), vp, i64, P(Heads), vp, vp, sz, vp],
+        "svdq_attention_forward": [P(AttentionDesc), vp, vp, vp, vp, i64, vp, vp, vp, sz, vp],
         "svdq_attention_backward_workspace_bytes": [P(AttentionDesc), P(sz)],
-        "svdq_attention_backward": [P(AttentionDesc)] + [P(Heads)] * 5 + [vp, vp, i64] + [P(Heads)] * 3 + [vp, sz, vp],
+        "svdq_attention_backward": [P(AttentionDesc)] + [vp] * 7 + [i64] + [vp] * 4 + [sz, vp],
         "svdq_mlp_workspace_bytes": [D, D, i64, P(sz), P(sz)],
         "svdq_mlp_fused": [D, D, i64, P(ctypes.c_int32)],
         "svdq_mlp_forward": [D, P(Packed), D, P(Packed), vp, i64, vp, vp, sz, ctypes.c_int32, vp],
@@ -1157,36 +1157,61 @@ class Fp8Linear:
 # autograd graph).
 # ----------------------------------------------------------------------------
 NORM_KINDS = {"layer": 0, "rms": 1}
+_EIGHT = ctypes.c_int64 * 8
+
+
+@functools.lru_cache(maxsize=1024)
+def _residual_desc(C, dt, pdt, kind, post, one_plus, groups, eps, alpha, rows_per_group):
+    """A reference to the descriptor (the library only reads it) and itself."""
+    d = ResidualDesc(C, dt, pdt, kind, post, one_plus, groups, eps, alpha, rows_per_group)
+    return ctypes.byref(d), d
 
 
 def _residual_setup(C, M, dtype, params, kind, post, alpha, eps, one_plus, rows_per_group):
-    """(descriptor, parameters, groups, whether they are vectors, rows_per_group) for (gate, weight, bias,
-    post_weight), each [C] or [groups][C] of one type, or None."""
-    groups, pdtype, flat = 1, dtype, True
-    for p in params:
-        if p is not None:
-            groups, pdtype, flat = p.shape[0] if p.dim() == 2 else 1, p.dtype, p.dim() == 1
-            break
-    _need(kind in NORM_KINDS, "kind: layer or rms")
-    s = ResidualParams()
-    for p, name, ld in zip(params, ("gate", "weight", "bias", "post_weight"), ("ld_gate", "ld_weight", "ld_bias", "ld_post")):
-        if p is not None:
-            at, step = _param(p, C, groups, pdtype, name)
-            _need((p.dim() == 1) == flat, "parameters: all [channels] or all [groups][channels]")
-            setattr(s, name, at)
-            setattr(s, ld, step)
+    """(descriptor reference, parameters, groups, whether they are vectors,
+    rows_per_group, type code) for (gate, weight, bias, post_weight), each [C]
+    or [groups][C] of one type, or None."""
+    groups, pdtype, flat, shape = 1, dtype, True, None
+    at = [0, 0, 0, 0, C, C, C, C]   # svdq_residual_params
+    for i, p in enumerate(params):
+        if p is None:
+            continue
+        if shape is None:
+            shape, pdtype = p.shape, p.dtype
+            flat = len(shape) == 1
+            groups = 1 if flat else shape[0]
+            plain = shape == ((C,) if flat else (groups, C))
+        if plain and p.shape == shape and p.dtype is pdtype and p.is_contiguous():
+            at[i] = p.data_ptr()
+        else:
+            name = ("gate", "weight", "bias", "post_weight")[i]
+            at[i], at[4 + i] = _param(p, C, groups, pdtype, name)
+            if (p.dim() == 1) != flat:
+                raise ValueError("parameters: all [channels] or all [groups][channels]")
     if rows_per_group is None:
         rows_per_group = max(1, -(-M // max(1, groups)))
-    d = ResidualDesc(C, _dt(dtype), _dt(pdtype), NORM_KINDS[kind], 1 if post else 0, 1 if one_plus else 0, groups, eps, alpha,
-                     rows_per_group)
-    return d, s, groups, flat, rows_per_group
+    code = NORM_KINDS.get(kind)
+    if code is None:
+        raise ValueError("kind: layer or rms")
+    dt = _dt(dtype)
+    d = _residual_desc(C, dt, dt if pdtype is dtype else _dt(pdtype), code, 1 if post else 0, 1 if one_plus else 0, groups, eps,
+                       alpha, rows_per_group)[0]
+    return d, _EIGHT(*at), groups, flat, rows_per_group, dt
 
 
 def _residual_out(t, x, what, stream):
     if t is None:
         return _rows_like(x, x.shape, stream)
-    _need(t.dtype == x.dtype and t.shape == x.shape, f"{what}: the shape and type of the rows")
+    if t.dtype != x.dtype or t.shape != x.shape:
+        raise ValueError(f"{what}: the shape and type of the rows")
     return t
+
+
+def _wants_grad(*tensors) -> bool:
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
 
 
 def residual_norm_forward(x, h, gate=None, weight=None, bias=None, post_weight=None, post_norm: bool = False,
@@ -1203,25 +1228,23 @@ def residual_norm_forward(x, h, gate=None, weight=None, bias=None, post_weight=N
     one_plus the gains are 1 + weight and 1 + post_weight. stats: float32
     [2 or 4 (rms: 1 or 2)][M], for residual_norm_backward. s and y may each be x
     or h."""
-    params = (gate, weight, bias, post_weight)
-    at = _on_device(x, h, s, y, *params)
-    if any(t is not None and t.requires_grad for t in (x, h) + params):
+    at = _on_device(x, h, s, y, gate, weight, bias, post_weight)
+    if _wants_grad(x, h, gate, weight, bias, post_weight):
         _no_graph("residual_norm_forward")
     post = post_norm or post_weight is not None
-    M, C = _matrix(x, "x")
-    _need(h.shape == x.shape and h.dtype == x.dtype, "h: the shape and type of x")
-    d, p, _, _, _ = _residual_setup(C, M, x.dtype, params, kind, post, alpha, eps, one_plus, rows_per_group)
+    xp, ldx = _rows(x, "x")
+    hp, ldh = _rows(h, "h")
+    shape = x.shape
+    M, C = shape
+    if h.shape != shape or h.dtype != x.dtype:
+        raise ValueError("h: the shape and type of x")
+    d, p, _, _, _, _ = _residual_setup(C, M, x.dtype, (gate, weight, bias, post_weight), kind, post, alpha, eps, one_plus,
+                                       rows_per_group)
     s, y = _residual_out(s, x, "s", stream), _residual_out(y, x, "y", stream)
-    stats = _empty(((1 + d.post_norm) * (2 - d.norm), M), _t.float32, x, stream)
-    (xp, ldx), (hp, ldh), (sp, lds), (yp, ldy) = _rows(x, "x"), _rows(h, "h"), _rows(s, "s"), _rows(y, "y")
-    _call("svdq_residual_norm_forward", at, stream, ctypes.byref(d), xp, ldx, hp, ldh, ctypes.byref(p), M, sp, lds, yp, ldy,
-          stats.data_ptr())
+    stats = _empty(((2 if post else 1) * (2 if kind == "layer" else 1), M), _t.float32, x, stream)
+    (sp, lds), (yp, ldy) = _rows(s, "s"), _rows(y, "y")
+    _call("svdq_residual_norm_forward", at, stream, d, xp, ldx, hp, ldh, p, M, sp, lds, yp, ldy, stats.data_ptr())
     return s, y, stats
-
-
-def _matrix(t, what):
-    _need(t.dim() == 2, f"{what}: a matrix [rows][channels]")
-    return t.shape
 
 
 def residual_norm_backward(dy, s, h, stats, gate=None, weight=None, post_weight=None, ds=None, post_norm: bool = False,
@@ -1233,35 +1256,44 @@ def residual_norm_backward(dy, s, h, stats, gate=None, weight=None, post_weight=
     gradients are [C], or [groups][C] for such parameters, of grad_dtype
     (default: the parameters' type, float32 without any); dpost_weight is None
     without post_norm, all four without param_grads."""
-    params = (gate, weight, None, post_weight)
-    at = _on_device(dy, s, h, stats, ds, dx, dh, *params)
-    if dy.requires_grad or (ds is not None and ds.requires_grad):
+    at = _on_device(dy, s, h, stats, ds, dx, dh, gate, weight, post_weight)
+    if _wants_grad(dy, ds):
         _no_graph("residual_norm_backward")
     post = post_norm or post_weight is not None
-    M, C = _matrix(s, "s")
+    sp, lds = _rows(s, "s")
+    shape, dtype = s.shape, s.dtype
+    M, C = shape
     for t, name in ((dy, "dy"), (h, "h"), (ds, "ds")):
-        _need(t is None or (t.shape == s.shape and t.dtype == s.dtype), f"{name}: the shape and type of s")
-    d, p, groups, flat, rpg = _residual_setup(C, M, s.dtype, params, kind, post, alpha, 0.0, one_plus, rows_per_group)
-    f32 = _torch().float32
-    _need(stats.dtype == f32 and stats.is_contiguous() and stats.shape == ((1 + d.post_norm) * (2 - d.norm), M),
-          "stats: of the forward")
-    some = [t for t in params if t is not None]
-    gdt = grad_dtype if grad_dtype is not None else (some[0].dtype if some else f32)
+        if t is not None and (t.shape != shape or t.dtype != dtype):
+            raise ValueError(f"{name}: the shape and type of s")
+    d, p, groups, flat, rpg, dt = _residual_setup(C, M, dtype, (gate, weight, None, post_weight), kind, post, alpha, 0.0, one_plus,
+                                                  rows_per_group)
+    f32 = _t.float32
+    if stats.dtype != f32 or not stats.is_contiguous() or \
+            stats.shape != ((2 if post else 1) * (2 if kind == "layer" else 1), M):
+        raise ValueError("stats: of the forward")
+    gdt = grad_dtype
+    if gdt is None:
+        some = gate if gate is not None else weight if weight is not None else post_weight
+        gdt = f32 if some is None else some.dtype
     dx, dh = _residual_out(dx, s, "dx", stream), _residual_out(dh, s, "dh", stream)
-    grads, out, ws, size = None, [None] * 4, None, 0
+    grads, out, ws, wsp, size = None, (None, None, None, None), None, None, 0
     if param_grads:
         n = 4 if post else 3
         both = _empty((n, C) if flat else (n, groups, C), gdt, s, stream)
-        out[:n] = list(both)
-        grads = ctypes.byref(ResidualGrads(*[_ptr(t) for t in out]))
-        size = _residual_ws(C, d.dtype, groups, rpg, M)
+        out = both.unbind(0)
+        step, first = both.stride(0) * both.element_size(), both.data_ptr()
+        grads = _EIGHT(first, first + step, first + 2 * step, first + 3 * step if post else 0)
+        if not post:
+            out = (*out, None)
+        size = _residual_ws(C, dt, groups, rpg, M)
         if size:
             ws = _empty((size,), _t.uint8, s, stream)
-    (yp, ldy), (sp, lds), (hp, ldh) = _rows(dy, "dy"), _rows(s, "s"), _rows(h, "h")
-    (xp, ldx), (gp, ldg) = _rows(dx, "dx"), _rows(dh, "dh")
+            wsp = ws.data_ptr()
+    (yp, ldy), (hp, ldh), (xp, ldx), (gp, ldg) = _rows(dy, "dy"), _rows(h, "h"), _rows(dx, "dx"), _rows(dh, "dh")
     tp, ldt = _rows(ds, "ds") if ds is not None else (None, 0)
-    _call("svdq_residual_norm_backward", at, stream, ctypes.byref(d), yp, ldy, tp, ldt, sp, lds, hp, ldh, ctypes.byref(p),
-          stats.data_ptr(), M, xp, ldx, gp, ldg, grads, _dt(gdt), _ptr(ws), size)
+    _call("svdq_residual_norm_backward", at, stream, d, yp, ldy, tp, ldt, sp, lds, hp, ldh, p, stats.data_ptr(), M, xp, ldx, gp,
+          ldg, grads, _dt(gdt), wsp, size)
     return (dx, dh, *out)
 
 
@@ -1274,13 +1306,27 @@ def _residual_ws(C, dt, groups, rows_per_group, M) -> int:
     return need.value
 
 
-def _heads(t, what, shape=None, dtype=None) -> Heads:
-    """A tensor [samples][tokens][heads][head_dim] for the library."""
-    _need(t.dim() == 4 and (t.shape[3] <= 1 or t.stride(3) == 1),
-          f"{what}: [samples][tokens][heads][head_dim], contiguous along the head")
-    _need(shape is None or t.shape == shape, f"{what}: shape {None if shape is None else list(shape)}")
-    _need(dtype is None or t.dtype == dtype, f"{what}: of type {dtype}")
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+def _heads(t, what, shape, dtype) -> tuple:
+    """(address, strides between samples, tokens and heads) of a tensor
+    [samples][tokens][heads][head_dim]: the fields of svdq_heads."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what}: shape {list(shape)} of {dtype}")
+    a, b, c, d = t.stride()
+    if d != 1 and shape[3] > 1:
+        raise ValueError(f"{what}: [samples][tokens][heads][head_dim], contiguous along the head")
+    return t.data_ptr(), a, b, c
+
+
+@functools.lru_cache(maxsize=64)
+def _heads_type(n: int):
+    return ctypes.c_int64 * (4 * n)
+
+
+def _all_heads(*heads):
+    """(to keep, the addresses of so many svdq_heads)"""
+    flat = _heads_type(len(heads))(*[v for h in heads for v in h])
+    at = ctypes.addressof(flat)
+    return flat, [at + 32 * i for i in range(len(heads))]
 
 
 def rope_frequencies(pairs, theta: float = 10000.0, shared: bool = False, device="cuda"):
@@ -1293,6 +1339,12 @@ def rope_frequencies(pairs, theta: float = 10000.0, shared: bool = False, device
     return (float(theta) ** -torch.cat(ladder)).to(device)
 
 
+@functools.lru_cache(maxsize=1024)
+def _rope_desc(dt, pos, D, H, Hk, pairs, half, inverse, B, L):
+    d = RopeDesc(dt, pos, D, H, Hk, len(pairs), (ctypes.c_int32 * 4)(*pairs), half, inverse, B, L)
+    return ctypes.byref(d), d, sum(pairs)
+
+
 def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool = False, q_out=None, k_out=None, stream=None):
     """svdq_rope: (q, k) turned, of q [samples][tokens][heads][head_dim] and k
     (its own number of heads, or None), bfloat16, float16 or float32, any
@@ -1301,32 +1353,42 @@ def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool 
     float64 [sum of pairs] (rope_frequencies). interleaved: pairs (2 j, 2 j + 1),
     else (j, j + sum of pairs). inverse turns back, as the gradient does. q_out
     and k_out may be q and k."""
-    torch = _torch()
     at = _on_device(q, k, positions, freqs, q_out, k_out)
-    if q.requires_grad or (k is not None and k.requires_grad):
+    if _wants_grad(q, k):
         _no_graph("rope")
-    qh = _heads(q, "q")
-    B, L, H, D = q.shape
-    pairs = [int(p) for p in pairs]
-    _need(1 <= len(pairs) <= 4, "pairs: of one to four axes")
-    _need(positions.is_contiguous() and positions.shape in ((L, len(pairs)), (B, L, len(pairs))) and
-          positions.dtype in (torch.int32, torch.float32), "positions: contiguous int32 or float32 [tokens][axes]")
-    _need(freqs.is_contiguous() and freqs.dtype == torch.float64 and freqs.shape == (sum(pairs),),
-          "freqs: contiguous float64, one for each pair")
-    _need(k is None or (k.dim() == 4 and k.shape[:2] == q.shape[:2] and k.shape[3] == D and k.dtype == q.dtype),
-          "k: samples, tokens, head_dim and type of q")
-    d = RopeDesc(_dt(q.dtype), int(positions.dtype == torch.float32), D, H, 0 if k is None else k.shape[2], len(pairs),
-                 (ctypes.c_int32 * 4)(*pairs), int(not interleaved), int(inverse), B, L)
-    kh = ko = None
-    if q_out is None:
-        q_out = _empty(q.shape, q.dtype, q, stream)
-    qo = _heads(q_out, "q_out", q.shape, q.dtype)
+    torch = _torch()
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4:
+        raise ValueError("q: [samples][tokens][heads][head_dim]")
+    B, L, H, D = shape
+    axes = len(pairs)
+    _need(1 <= axes <= 4, "pairs: of one to four axes")
+    pos = positions.dtype
+    if not positions.is_contiguous() or positions.shape not in ((L, axes), (B, L, axes)) or \
+            (pos != torch.int32 and pos != torch.float32):
+        raise ValueError("positions: contiguous int32 or float32 [tokens][axes]")
+    Hk, kshape = 0, None
     if k is not None:
+        kshape = k.shape
+        if len(kshape) != 4 or kshape[:2] != shape[:2] or kshape[3] != D or k.dtype != dtype:
+            raise ValueError("k: samples, tokens, head_dim and type of q")
+        Hk = kshape[2]
+    d, _, n = _rope_desc(_dt(dtype), 1 if pos == torch.float32 else 0, D, H, Hk, tuple(map(int, pairs)), 0 if interleaved else 1,
+                         1 if inverse else 0, B, L)
+    if not freqs.is_contiguous() or freqs.dtype != torch.float64 or freqs.shape != (n,):
+        raise ValueError("freqs: contiguous float64, one for each pair")
+    if q_out is None:
+        q_out = _empty(shape, dtype, q, stream)
+    qs, qo = _heads(q, "q", shape, dtype), _heads(q_out, "q_out", shape, dtype)
+    if k is None:
+        keep, (a, b) = _all_heads(qs, qo)
+        ka = kb = None
+    else:
         if k_out is None:
-            k_out = _empty(k.shape, k.dtype, k, stream)
-        kh, ko = ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(k_out, "k_out", k.shape, k.dtype))
-    _call("svdq_rope", at, stream, ctypes.byref(d), ctypes.byref(qh), kh, positions.data_ptr(),
-          L * len(pairs) if positions.dim() == 3 else 0, freqs.data_ptr(), ctypes.byref(qo), ko)
+            k_out = _empty(kshape, dtype, k, stream)
+        keep, (a, b, ka, kb) = _all_heads(qs, qo, _heads(k, "k", kshape, dtype), _heads(k_out, "k_out", kshape, dtype))
+    _call("svdq_rope", at, stream, d, a, ka, positions.data_ptr(), L * axes if len(positions.shape) == 3 else 0, freqs.data_ptr(),
+          b, kb)
     return q_out, k_out
 
 
@@ -1342,29 +1404,33 @@ def _attention_plan(dt, D, H, Hk, causal, scale, B, Lq, Lk):
     return ctypes.byref(d), d, sizes[0], sizes[1]
 
 
-def attention_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None) -> int:
-    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, 0, 1.0, samples, queries, keys)[2]
+def attention_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None, causal: bool = False) -> int:
+    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, int(causal), 1.0, samples, queries, keys)[2]
 
 
-def attention_backward_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None) -> int:
-    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, 0, 1.0, samples, queries, keys)[3]
+def attention_backward_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None, causal: bool = False) -> int:
+    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, int(causal), 1.0, samples, queries, keys)[3]
 
 
 def _attention_setup(q, k, v, key_mask, causal, scale):
-    _need(q.dim() == 4 and k.dim() == 4, "q, k, v: [samples][tokens][heads][head_dim]")
-    B, Lq, H, D = q.shape
-    Lk, Hk = k.shape[1], k.shape[2]
-    _need(k.shape == (B, Lk, Hk, D) and v.shape == k.shape and k.dtype == q.dtype and v.dtype == q.dtype,
-          "k, v: [samples][keys][kv_heads][head_dim] of the type of q")
-    mask = ld = None
+    """((descriptor reference, itself, workspace bytes), mask pointer, stride)"""
+    shape, kshape, dtype = q.shape, k.shape, q.dtype
+    if len(shape) != 4 or len(kshape) != 4:
+        raise ValueError("q, k, v: [samples][tokens][heads][head_dim]")
+    B, Lq, H, D = shape
+    _, Lk, Hk, _ = kshape
+    if kshape[0] != B or kshape[3] != D or v.shape != kshape or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("k, v: [samples][keys][kv_heads][head_dim] of the type of q")
+    mask, ld = None, 0
     if key_mask is not None:
         torch = _torch()
-        _need(key_mask.shape == (B, Lk) and key_mask.dtype in (torch.bool, torch.uint8) and
-              (Lk <= 1 or key_mask.stride(1) == 1), "key_mask: bool or uint8 [samples][keys], contiguous along the keys")
+        if key_mask.shape != (B, Lk) or (key_mask.dtype != torch.bool and key_mask.dtype != torch.uint8) or \
+                (Lk > 1 and key_mask.stride(1) != 1):
+            raise ValueError("key_mask: bool or uint8 [samples][keys], contiguous along the keys")
         mask, ld = key_mask.data_ptr(), key_mask.stride(0)
-    plan = _attention_plan(_dt(q.dtype), D, H, Hk, int(bool(causal)), float(scale if scale is not None else max(D, 1) ** -0.5), B,
+    plan = _attention_plan(_dt(dtype), D, H, Hk, 1 if causal else 0, float(scale) if scale is not None else max(D, 1) ** -0.5, B,
                            Lq, Lk)
-    return plan, mask, ld or 0
+    return plan, mask, ld
 
 
 def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, out=None, workspace=None, stream=None):
@@ -1375,17 +1441,17 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
     scale: default head_dim^(-1/2). lse: float32 [samples][heads][queries]. A
     query without keys has o = 0, lse = -inf."""
     at = _on_device(q, k, v, key_mask, out, workspace)
-    if q.requires_grad or k.requires_grad or v.requires_grad:
+    if _wants_grad(q, k, v):
         _no_graph("attention_forward")
     (d, _, size, _), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
-    B, Lq, H, D = q.shape
+    shape, kshape, dtype = q.shape, k.shape, q.dtype
     if out is None:
-        out = _empty(q.shape, q.dtype, q, stream)
-    lse = _empty((B, H, Lq), _t.float32, q, stream)
+        out = _empty(shape, dtype, q, stream)
+    lse = _empty((shape[0], shape[2], shape[1]), _t.float32, q, stream)
     ws, wsp, size = _scratch(workspace, size, q, stream)
-    b = ctypes.byref
-    _call("svdq_attention_forward", at, stream, d, b(_heads(q, "q")), b(_heads(k, "k")), b(_heads(v, "v")), mask, ldm,
-          b(_heads(out, "out", q.shape, q.dtype)), lse.data_ptr(), wsp, size)
+    keep, (a, b, c, o) = _all_heads(_heads(q, "q", shape, dtype), _heads(k, "k", kshape, dtype), _heads(v, "v", kshape, dtype),
+                                    _heads(out, "out", shape, dtype))
+    _call("svdq_attention_forward", at, stream, d, a, b, c, mask, ldm, o, lse.data_ptr(), wsp, size)
     return out, lse
 
 
@@ -1394,19 +1460,18 @@ def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = Fals
     """svdq_attention_backward: (dq, dk, dv) for dout of o, from the forward's
     inputs and its o and lse."""
     at = _on_device(q, dout, k, v, o, lse, key_mask, dq, dk, dv, workspace)
-    if dout.requires_grad:
+    if _wants_grad(dout):
         _no_graph("attention_backward")
     (d, _, _, size), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
-    B, Lq, H, D = q.shape
-    _need(lse.dtype == _torch().float32 and lse.shape == (B, H, Lq) and lse.is_contiguous(),
-          "lse: float32 [samples][heads][queries]")
-    dq = _empty(q.shape, q.dtype, q, stream) if dq is None else dq
-    dk = _empty(k.shape, q.dtype, q, stream) if dk is None else dk
-    dv = _empty(k.shape, q.dtype, q, stream) if dv is None else dv
+    shape, kshape, dtype = q.shape, k.shape, q.dtype
+    if lse.dtype != _t.float32 or lse.shape != (shape[0], shape[2], shape[1]) or not lse.is_contiguous():
+        raise ValueError("lse: float32 [samples][heads][queries]")
+    dq = _empty(shape, dtype, q, stream) if dq is None else dq
+    dk = _empty(kshape, dtype, q, stream) if dk is None else dk
+    dv = _empty(kshape, dtype, q, stream) if dv is None else dv
     ws, wsp, size = _scratch(workspace, size, q, stream)
-    b = ctypes.byref
-    t = [b(_heads(x, n, s, q.dtype)) for x, n, s in ((dout, "dout", q.shape), (q, "q", None), (k, "k", None), (v, "v", None),
-                                                    (o, "o", q.shape), (dq, "dq", q.shape), (dk, "dk", k.shape),
-                                                    (dv, "dv", k.shape))]
-    _call("svdq_attention_backward", at, stream, d, *t[:5], lse.data_ptr(), mask, ldm, *t[5:], wsp, size)
+    keep, h = _all_heads(_heads(dout, "dout", shape, dtype), _heads(q, "q", shape, dtype), _heads(k, "k", kshape, dtype),
+                         _heads(v, "v", kshape, dtype), _heads(o, "o", shape, dtype), _heads(dq, "dq", shape, dtype),
+                         _heads(dk, "dk", kshape, dtype), _heads(dv, "dv", kshape, dtype))
+    _call("svdq_attention_backward", at, stream, d, *h[:5], lse.data_ptr(), mask, ldm, *h[5:], wsp, size)
     return dq, dk, dv

@@ -23,26 +23,22 @@ namespace svdq {
 
 constexpr int kAttnRows = kAttnTile;   // of a tile
 
-// A workgroup's pieces, from its arguments.
-template <bool SHARED>
-struct AttnDeal;
-template <>
-struct AttnDeal<false> {
-  struct Shares {};
-  AttnWhole walk;
-  __device__ __forceinline__ AttnDeal(const AttnPlan&, int, const Shares&) {}
+struct AttnUnits {};   // in the place of AttnParts where a workgroup has a unit
+template <bool PARTS>
+struct AttnDealOf {
+  typedef AttnUnits type;
 };
 template <>
-struct AttnDeal<true> {
-  typedef AttnShares Shares;
-  AttnWalk walk;
-  __device__ __forceinline__ AttnDeal(const AttnPlan& p, int w, const Shares& s) : walk(p, w, s.at[w]) {}
+struct AttnDealOf<true> {
+  typedef AttnParts type;
 };
-__device__ __forceinline__ void note_span(const AttnArgs& a, const AttnPiece& at, int w) {
-  if (threadIdx.x == 0) {
-    if (at.starts) a.spans[2 * at.unit] = w;
-    if (at.ends) a.spans[2 * at.unit + 1] = w;
-  }
+template <bool PARTS>
+using AttnDeal = typename AttnDealOf<PARTS>::type;
+__device__ __forceinline__ AttnPiece piece_of(const AttnArgs& a, const AttnUnits&, int place) {
+  return attn_piece(a.cost, a.plan, place);
+}
+__device__ __forceinline__ AttnPiece piece_of(const AttnArgs& a, const AttnParts& deal, int place) {
+  return attn_piece(a.cost, a.plan, deal.at[place]);
 }
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));

@@ -27,8 +27,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // exponentials: 4608 tokens, 24 heads of 128 with a mask 252 us (1.03
 // PFLOP/s), with one wave a SIMD 411, with one of two blocks 355, with
 // workgroups of four waves instead of eight 270.
-template <typename T, int DP, int W, int NB, bool SHARED>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_fwd_kernel(AttnArgs a, typename AttnDeal<SHARED>::Shares shares) {
+template <typename T, int DP, int W, int NB, bool PARTS>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 64 ? 4 : 2, DP == 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   constexpr int NT = TL::kTransfers / W;   // transfers of a wave for one tile
   extern __shared__ __align__(1024) uint8_t smem[];   // [2][K, V][kBytes]
@@ -47,228 +47,215 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     vv[n] = c * 8 < D ? (uint32_t)((row_of[n] * a.v.token + c * 8) * 2) : kPastEnd;
   }
   const int place = attn_place(a.plan, blockIdx.x);
-  AttnDeal<SHARED> deal(a.plan, place, shares);
-  auto run = [&](const AttnPiece& at) __attribute__((always_inline)) {
-    const int b = at.hb / a.Hk, hk = at.hb % a.Hk;
-    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
-    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
-    const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
-    const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch : nullptr;
+  const AttnPiece at = piece_of(a, deal, place);
+  const int b = at.hb / a.Hk, hk = at.hb % a.Hk;
+  const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
+  const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
+  const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch : nullptr;
 
-    // this lane's rows and the last keys that they see
-    const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
-    u32x4 qf[NB][TL::kSteps];
-    int last[NB];   // of a row without keys (and past the last row) below 0
+  // this lane's rows and the last keys that they see
+  const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
+  u32x4 qf[NB][TL::kSteps];
+  int last[NB];   // of a row without keys (and past the last row) below 0
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int r = r0 + 32 * n + lr, i = r / G;
-      const T* row = qp + (int64_t)i * a.q.token + (int64_t)(r - i * G) * a.q.head;
-      last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
+  for (int n = 0; n < NB; ++n) {
+    const int r = r0 + 32 * n + lr, i = r / G;
+    const T* row = qp + (int64_t)i * a.q.token + (int64_t)(r - i * G) * a.q.head;
+    last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
 #pragma unroll
-      for (int s = 0; s < TL::kSteps; ++s) {
-        const int d = 16 * s + 8 * h;
-        qf[n][s] = r < R && d < D ? *reinterpret_cast<const u32x4*>(row + d) : u32x4{0, 0, 0, 0};
-      }
+    for (int s = 0; s < TL::kSteps; ++s) {
+      const int d = 16 * s + 8 * h;
+      qf[n][s] = r < R && d < D ? *reinterpret_cast<const u32x4*>(row + d) : u32x4{0, 0, 0, 0};
     }
-    const int k_begin = at.first * kAttnRows, tiles = at.last - at.first;
-    // what every and what any row of this wave sees
-    const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
-    const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
+  }
+  const int k_begin = at.first * kAttnRows, tiles = at.last - at.first;
+  // what every and what any row of this wave sees
+  const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
+  const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
 
-    auto fetch = [&](int k0, int stage, uint64_t keep) {
-      const int rows = min(kAttnRows, a.Lk - k0);
-      const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
-      const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
-      uint8_t *tk = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
-      // (a key that the mask drops is not read: whatever stands there, it is zero)
-      if (keep == ~0ull) {
+  auto fetch = [&](int k0, int stage, uint64_t keep) {
+    const int rows = min(kAttnRows, a.Lk - k0);
+    const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
+    const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
+    uint8_t *tk = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
+    // (a key that the mask drops is not read: whatever stands there, it is zero)
+    if (keep == ~0ull) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          lds_transfer_16(rk, tk + n * 1024, vk[n]);
-          lds_transfer_16(rv, tv + n * 1024, vv[n]);
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const bool in = keep >> row_of[n] & 1;
-          lds_transfer_16(rk, tk + n * 1024, in ? vk[n] : kPastEnd);
-          lds_transfer_16(rv, tv + n * 1024, in ? vv[n] : kPastEnd);
-        }
+      for (int n = 0; n < NT; ++n) {
+        lds_transfer_16(rk, tk + n * 1024, vk[n]);
+        lds_transfer_16(rv, tv + n * 1024, vv[n]);
       }
-    };
-    // the mask's byte of key `lane` of a tile
-    auto mask_byte = [&](int k0) -> int {
-      const int k = k0 + lane;
-      return k < a.Lk ? (mask ? (int)mask[k] : 1) : 0;
-    };
-
-    f32x16 o[TL::kBlocks][NB];
-    float m[NB], l[NB];
+    } else {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      m[n] = -__builtin_inff();
-      l[n] = 0.f;
-#pragma unroll
-      for (int i = 0; i < TL::kBlocks; ++i) o[i][n] = f32x16{};
-    }
-    uint64_t now, keep = 0;   // which keys of the tile, and of the next, take part
-    int next_byte = 0;
-    if (tiles > 0) {
-      keep = __ballot(mask_byte(k_begin) != 0);
-      fetch(k_begin, 0, keep);
-      next_byte = mask_byte(k_begin + kAttnRows);
-    }
-    for (int t = 0, k0 = k_begin; t < tiles; ++t, k0 += kAttnRows) {
-      now = keep;
-      tile_barrier();
-      if (t + 1 < tiles) {
-        keep = __ballot(next_byte != 0);
-        fetch(k0 + kAttnRows, (t + 1) & 1, keep);
-        next_byte = mask_byte(k0 + 2 * kAttnRows);
-      }
-      const uint8_t *tk = smem + (t & 1) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
-      if (k0 > w_last || now == 0) continue;   // nothing that this wave's rows see
-      f32x16 s[2][NB];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int n = 0; n < NB; ++n) s[kb][n] = f32x16{};
-#pragma unroll
-      for (int st = 0; st < TL::kSteps; ++st)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const u32x4 kf = TL::straight(tk, pl, kb, st);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) s[kb][n] = mma<T>(kf, qf[n][st], s[kb][n]);
-        }
-      sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
-      if (now != ~0ull || k0 + kAttnRows - 1 > w_first) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const int lim = last[n] - k0 - 4 * h;
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
-            const uint32_t bits = (uint32_t)(now >> (32 * kb)) >> (4 * h);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int c = 8 * (i / 4) + i % 4;
-              s[kb][n][i] = (bits >> c & 1) && 32 * kb + c <= lim ? s[kb][n][i] : -__builtin_inff();
-            }
-          }
-        }
-      }
-      u32x4 p[4][NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        float top = s[0][n][0];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kb][n][i]);
-        top = max_halves(top) * a.scale_log2;
-        // The maximum that is subtracted follows the true one when that is more
-        // than 8 (in base 2) above it: up to there the probabilities stay below
-        // 2^8, which neither the sums nor either type's rounding minds, and most
-        // tiles leave the accumulators as they are.
-        if (__any(top > m[n] + 8.f)) {
-          const float mn = __builtin_fmaxf(m[n], top);
-          const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
-          m[n] = mn;
-          l[n] *= f;
-#pragma unroll
-          for (int i = 0; i < TL::kBlocks; ++i) o[i][n] *= f;
-        }
-        const float base = m[n] == -__builtin_inff() ? 0.f : m[n];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            s[kb][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][n][i], a.scale_log2, -base));
-            l[n] += s[kb][n][i];
-          }
-          p[2 * kb][n] = as_operand<T>(s[kb][n], 0);
-          p[2 * kb + 1][n] = as_operand<T>(s[kb][n], 1);
-        }
-      }
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-        for (int i = 0; i < TL::kBlocks; ++i) {
-          const u32x4 vf = TL::turned(tv, pl, kt, i);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) o[i][n] = mma<T>(vf, p[kt][n], o[i][n]);
-        }
-      sched_products<4 * TL::kBlocks * NB, 8 * TL::kBlocks, 2, 8>();
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int r = r0 + 32 * n + lr, i = r / G, g = r - i * G;
-      const float sum = sum_halves(l[n]);
-      const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = m[n] + __builtin_log2f(sum);   // (no key: -inf)
-      if (r >= R) continue;
-      if (SHARED && at.part >= 0) {
-        const int64_t row = (int64_t)at.part * a.part_rows + r - at.block * (32 * NB * W);
-        if (h == 0) a.part_lse[row] = lse2;
-#pragma unroll
-        for (int blk = 0; blk < TL::kBlocks; ++blk)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int d = 32 * blk + 8 * q + 4 * h;
-            if (d < D)
-              *reinterpret_cast<f32x4*>(a.part + row * D + d) =
-                  f32x4{o[blk][n][4 * q], o[blk][n][4 * q + 1], o[blk][n][4 * q + 2], o[blk][n][4 * q + 3]} * f;
-          }
-        continue;
-      }
-      const int head = hk * G + g;
-      if (h == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + i] = lse2 * kLn2;
-      T* row = static_cast<T*>(a.o.p) + b * a.o.batch + i * a.o.token + head * a.o.head;
-#pragma unroll
-      for (int blk = 0; blk < TL::kBlocks; ++blk) {
-        u32x4 c[2];
-        head_chunks<T>(o[blk][n], f, c);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int d = 32 * blk + 16 * q + 8 * h;
-          if (d < D) *reinterpret_cast<u32x4*>(row + d) = c[q];
-        }
+      for (int n = 0; n < NT; ++n) {
+        const bool in = keep >> row_of[n] & 1;
+        lds_transfer_16(rk, tk + n * 1024, in ? vk[n] : kPastEnd);
+        lds_transfer_16(rv, tv + n * 1024, in ? vv[n] : kPastEnd);
       }
     }
   };
-  AttnPiece at;
-  if constexpr (SHARED) {
-    while (deal.walk.next(a.cost, a.plan, place, at)) {
-      note_span(a, at, place);
-      run(at);
-      __syncthreads();   // (the piece's tiles are read)
+  // the mask's byte of key `lane` of a tile
+  auto mask_byte = [&](int k0) -> int {
+    const int k = k0 + lane;
+    return k < a.Lk ? (mask ? (int)mask[k] : 1) : 0;
+  };
+
+  f32x16 o[TL::kBlocks][NB];
+  float m[NB], l[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    m[n] = -__builtin_inff();
+    l[n] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TL::kBlocks; ++i) o[i][n] = f32x16{};
+  }
+  uint64_t now, keep = 0;   // which keys of the tile, and of the next, take part
+  int next_byte = 0;
+  if (tiles > 0) {
+    keep = __ballot(mask_byte(k_begin) != 0);
+    fetch(k_begin, 0, keep);
+    next_byte = mask_byte(k_begin + kAttnRows);
+  }
+  for (int t = 0, k0 = k_begin; t < tiles; ++t, k0 += kAttnRows) {
+    now = keep;
+    tile_barrier();
+    if (t + 1 < tiles) {
+      keep = __ballot(next_byte != 0);
+      fetch(k0 + kAttnRows, (t + 1) & 1, keep);
+      next_byte = mask_byte(k0 + 2 * kAttnRows);
     }
-  } else {
-    deal.walk.next(a.cost, a.plan, place, at);
-    run(at);
+    const uint8_t *tk = smem + (t & 1) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
+    if (k0 > w_last || now == 0) continue;   // nothing that this wave's rows see
+    f32x16 s[2][NB];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) s[kb][n] = f32x16{};
+#pragma unroll
+    for (int st = 0; st < TL::kSteps; ++st)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const u32x4 kf = TL::straight(tk, pl, kb, st);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[kb][n] = mma<T>(kf, qf[n][st], s[kb][n]);
+      }
+    sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
+    if (now != ~0ull || k0 + kAttnRows - 1 > w_first) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int lim = last[n] - k0 - 4 * h;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          const uint32_t bits = (uint32_t)(now >> (32 * kb)) >> (4 * h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = 8 * (i / 4) + i % 4;
+            s[kb][n][i] = (bits >> c & 1) && 32 * kb + c <= lim ? s[kb][n][i] : -__builtin_inff();
+          }
+        }
+      }
+    }
+    u32x4 p[4][NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float top = s[0][n][0];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kb][n][i]);
+      top = max_halves(top) * a.scale_log2;
+      // The maximum that is subtracted follows the true one when that is more
+      // than 8 (in base 2) above it: up to there the probabilities stay below
+      // 2^8, which neither the sums nor either type's rounding minds, and most
+      // tiles leave the accumulators as they are.
+      if (__any(top > m[n] + 8.f)) {
+        const float mn = __builtin_fmaxf(m[n], top);
+        const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+        m[n] = mn;
+        l[n] *= f;
+#pragma unroll
+        for (int i = 0; i < TL::kBlocks; ++i) o[i][n] *= f;
+      }
+      const float base = m[n] == -__builtin_inff() ? 0.f : m[n];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[kb][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][n][i], a.scale_log2, -base));
+          l[n] += s[kb][n][i];
+        }
+        p[2 * kb][n] = as_operand<T>(s[kb][n], 0);
+        p[2 * kb + 1][n] = as_operand<T>(s[kb][n], 1);
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+      for (int i = 0; i < TL::kBlocks; ++i) {
+        const u32x4 vf = TL::turned(tv, pl, kt, i);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) o[i][n] = mma<T>(vf, p[kt][n], o[i][n]);
+      }
+    sched_products<4 * TL::kBlocks * NB, 8 * TL::kBlocks, 2, 8>();
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int r = r0 + 32 * n + lr, i = r / G, g = r - i * G;
+    const float sum = sum_halves(l[n]);
+    const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = m[n] + __builtin_log2f(sum);   // (no key: -inf)
+    if (r >= R) continue;
+    if (PARTS && !at.whole) {
+      const int64_t row = (int64_t)place * a.part_rows + r - at.block * (32 * NB * W);
+      if (h == 0) a.part_lse[row] = lse2;
+#pragma unroll
+      for (int blk = 0; blk < TL::kBlocks; ++blk)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int d = 32 * blk + 8 * q + 4 * h;
+          if (d < D)
+            *reinterpret_cast<f32x4*>(a.part + row * D + d) =
+                f32x4{o[blk][n][4 * q], o[blk][n][4 * q + 1], o[blk][n][4 * q + 2], o[blk][n][4 * q + 3]} * f;
+        }
+      continue;
+    }
+    const int head = hk * G + g;
+    if (h == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + i] = lse2 * kLn2;
+    T* row = static_cast<T*>(a.o.p) + b * a.o.batch + i * a.o.token + head * a.o.head;
+#pragma unroll
+    for (int blk = 0; blk < TL::kBlocks; ++blk) {
+      u32x4 c[2];
+      head_chunks<T>(o[blk][n], f, c);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int d = 32 * blk + 16 * q + 8 * h;
+        if (d < D) *reinterpret_cast<u32x4*>(row + d) = c[q];
+      }
+    }
   }
 }
 
-// The parts of shared units joined: with the parts' lse, o = sum 2^(lse_s - m)
-// o_s / sum 2^(lse_s - m). WAYS half waves (32 lanes of four elements) have a
-// row, each every WAYS-th part; theirs are then joined in order through LDS.
+// The parts of units joined: with the parts' lse, o = sum 2^(lse_s - m) o_s /
+// sum 2^(lse_s - m). WAYS half waves (32 lanes of four elements) have a row,
+// each every WAYS-th part; theirs are then joined in order through LDS.
 template <typename T, int WAYS>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnParts deal) {
   constexpr int ROWS = 8 / WAYS;
   __shared__ float ms[8], sums[8];
   __shared__ f32x4 os[8][32];
-  const int unit = blockIdx.x, w0 = a.spans[2 * unit], w1 = a.spans[2 * unit + 1];
-  if (w0 == w1) return;   // one workgroup had all of it
-  const int hb = unit / a.plan.blocks, block = unit - hb * a.plan.blocks;
+  const AttnPart at = deal.at[blockIdx.x];
+  if (at.part != 0 || at.parts == 1) return;   // (a unit's first workgroup's place joins it)
+  const int hb = at.unit / a.plan.blocks, block = at.unit - hb * a.plan.blocks;
   const int lane = threadIdx.x & 31, half = threadIdx.x >> 5, way = half % WAYS;
-  const int in = (int)blockIdx.y * ROWS + half / WAYS, r = block * kAttnBlock + in, d = lane * 4;
+  const int in = (int)blockIdx.y * ROWS + half / WAYS, r = block * a.cost.block + in, d = lane * 4;
   const bool live = in < a.part_rows && r < a.Lq * a.G;
   float m = -__builtin_inff(), sum = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
-    for (int w = w0 + way; w <= w1; w += WAYS) m = __builtin_fmaxf(m, a.part_lse[attn_part(w0, w) * a.part_rows + in]);
+    for (int w = way; w < at.parts; w += WAYS) m = __builtin_fmaxf(m, a.part_lse[(int64_t)(blockIdx.x + w) * a.part_rows + in]);
     const float base = m == -__builtin_inff() ? 0.f : m;
-    for (int w = w0 + way; w <= w1; w += WAYS) {
-      const int64_t row = attn_part(w0, w) * a.part_rows + in;
+    for (int w = way; w < at.parts; w += WAYS) {
+      const int64_t row = (int64_t)(blockIdx.x + w) * a.part_rows + in;
       const float f = __builtin_amdgcn_exp2f(a.part_lse[row] - base);
       sum += f;
       if (d < a.D) o += *reinterpret_cast<const f32x4*>(a.part + row * a.D + d) * f;
@@ -305,54 +292,61 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
         u32x2{cvt_x2<T>(o[0], o[1]), cvt_x2<T>(o[2], o[3])};
 }
 
-template <typename T, int DP, bool SHARED>
-constexpr auto fwd_kernel = attn_fwd_kernel<T, DP, 8, 1, SHARED>;
 template <int DP>
 constexpr int kFwdLds = 4 * AttnTile<DP>::kBytes;
 
-template <typename T, int DP>
+template <typename T, int DP, int W>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.plan.grid), block(512);
-  if (!a.plan.shared) {
-    hipLaunchKernelGGL((fwd_kernel<T, DP, false>), grid, block, kFwdLds<DP>, st, a, AttnDeal<false>::Shares{});
+  const dim3 grid((unsigned)a.plan.grid), block(64 * W);
+  if (!a.plan.each) {
+    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, false>), grid, block, kFwdLds<DP>, st, a, AttnUnits{});
     return hipGetLastError();
   }
-  AttnShares shares;
-  attn_shares(a.cost, a.plan, &shares);
-  hipLaunchKernelGGL((fwd_kernel<T, DP, true>), grid, block, kFwdLds<DP>, st, a, shares);
+  AttnParts deal;
+  attn_parts(a.cost, a.plan, &deal);
+  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, true>), grid, block, kFwdLds<DP>, st, a, deal);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // with many parts a row, all of a workgroup for one
-  const int units = a.plan.blocks * a.plan.heads;
-  const bool deep = a.plan.grid >= 4 * units;
-  const dim3 rows((unsigned)units, (unsigned)(deep ? a.part_rows : (a.part_rows + 7) / 8));
+  const bool deep = a.plan.grid >= 4 * a.plan.blocks * a.plan.heads;
+  const dim3 rows((unsigned)a.plan.grid, (unsigned)(deep ? a.part_rows : (a.part_rows + 7) / 8));
   if (deep)
-    hipLaunchKernelGGL((attn_join_kernel<T, 8>), rows, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attn_join_kernel<T, 8>), rows, dim3(256), 0, st, a, deal);
   else
-    hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, deal);
   return hipGetLastError();
 }
+template <typename T>
+hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
+  const bool wide = a.cost.block == 8 * kAttnWave;
+  if (a.D <= 64) return wide ? launch_fwd<T, 64, 8>(a, st) : launch_fwd<T, 64, 4>(a, st);
+  return wide ? launch_fwd<T, 128, 8>(a, st) : launch_fwd<T, 128, 4>(a, st);
+}
 
-template <typename T, int DP>
+template <typename T, int DP, int W>
 hipError_t prepare_fwd() {
-  for (const void* f : {(const void*)fwd_kernel<T, DP, false>, (const void*)fwd_kernel<T, DP, true>}) {
+  for (const void* f : {(const void*)attn_fwd_kernel<T, DP, W, 1, false>, (const void*)attn_fwd_kernel<T, DP, W, 1, true>}) {
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds<DP>);
     if (e != hipSuccess) return e;
   }
+  return hipSuccess;
+}
+template <typename T>
+hipError_t prepare_fwd() {
+  for (hipError_t e : {prepare_fwd<T, 64, 4>(), prepare_fwd<T, 64, 8>(), prepare_fwd<T, 128, 4>(), prepare_fwd<T, 128, 8>()})
+    if (e != hipSuccess) return e;
   return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t prepare_attention() {
-  for (hipError_t e : {prepare_fwd<Bf16, 64>(), prepare_fwd<Bf16, 128>(), prepare_fwd<Half, 64>(), prepare_fwd<Half, 128>()})
-    if (e != hipSuccess) return e;
-  return hipSuccess;
+  const hipError_t e = prepare_fwd<Bf16>();
+  return e != hipSuccess ? e : prepare_fwd<Half>();
 }
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t st) {
-  if (a.dtype == SVDQ_DT_BF16) return a.D <= 64 ? launch_fwd<Bf16, 64>(a, st) : launch_fwd<Bf16, 128>(a, st);
-  return a.D <= 64 ? launch_fwd<Half, 64>(a, st) : launch_fwd<Half, 128>(a, st);
+  return a.dtype == SVDQ_DT_BF16 ? launch_fwd<Bf16>(a, st) : launch_fwd<Half>(a, st);
 }
 
 }  // namespace svdq

@@ -101,8 +101,8 @@ __device__ __forceinline__ float ds_scale(int D, float x, float y) {
 // waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads: 574
 // us against 760 with V in registers, of which 53 spill, 768 with one wave a
 // SIMD and two blocks of keys, 870 with workgroups of four waves).
-template <typename T, int DP, int W, int NB, bool SHARED>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_dkv_kernel(AttnGradArgs g, typename AttnDeal<SHARED>::Shares shares) {
+template <typename T, int DP, int W, int NB, bool PARTS>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
@@ -115,234 +115,221 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const int G = a.G, R = a.Lq * G, D = a.D;
   const typename TL::Lane pl(lane);
   const int place = attn_place(a.plan, blockIdx.x);
-  AttnDeal<SHARED> deal(a.plan, place, shares);
-  auto run = [&](const AttnPiece& at) __attribute__((always_inline)) {
-    const int b = at.hb / a.Hk, hk = at.hb % a.Hk;
-    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
-    const T* dop = static_cast<const T*>(g.dout.p) + b * g.dout.batch + (int64_t)hk * G * g.dout.head;
-    const int64_t Rp = (int64_t)g.row_blocks * kAttnBlock;
-    const float *lse = g.lse + at.hb * Rp, *delta = g.delta + at.hb * Rp;
-    const float top_do = kScaled<T> ? wave_top(g.top_do + at.hb * g.row_blocks, g.row_blocks, lane) : 0.f;
+  const AttnPiece at = piece_of(a, deal, place);
+  const int b = at.hb / a.Hk, hk = at.hb % a.Hk;
+  const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
+  const T* dop = static_cast<const T*>(g.dout.p) + b * g.dout.batch + (int64_t)hk * G * g.dout.head;
+  const int64_t Rp = g.rows_padded;
+  const float *lse = g.lse + at.hb * Rp, *delta = g.delta + at.hb * Rp;
+  const float top_do = kScaled<T> ? wave_top(g.top_do + at.hb * g.row_blocks, g.row_blocks, lane) : 0.f;
 
-    // this lane's keys, as operand B (of both products that give scores)
-    const int key0 = at.block * (32 * NB * W) + wave * (32 * NB);
-    u32x4 kf[NB][TL::kSteps], vf[kHoldV ? NB : 1][TL::kSteps];
-    bool live[NB];
-    int first[NB];   // the first row that sees the key
-    float dsc[NB], fk[NB];   // fp16: the factor of a key's ds; of its dk
+  // this lane's keys, as operand B (of both products that give scores)
+  const int key0 = at.block * (32 * NB * W) + wave * (32 * NB);
+  u32x4 kf[NB][TL::kSteps], vf[kHoldV ? NB : 1][TL::kSteps];
+  bool live[NB];
+  int first[NB];   // the first row that sees the key
+  float dsc[NB], fk[NB];   // fp16: the factor of a key's ds; of its dk
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int key = key0 + 32 * n + lr;
-      live[n] = key < a.Lk && (!a.mask || a.mask[b * a.mask_batch + key]);
-      first[n] = a.causal ? max(key - (a.Lk - a.Lq), 0) * G : 0;
-      float top_v = 0.f;
-      const T* kr = static_cast<const T*>(a.k.p) + b * a.k.batch + key * a.k.token + hk * a.k.head;
-      const T* vr = static_cast<const T*>(a.v.p) + b * a.v.batch + key * a.v.token + hk * a.v.head;
+  for (int n = 0; n < NB; ++n) {
+    const int key = key0 + 32 * n + lr;
+    live[n] = key < a.Lk && (!a.mask || a.mask[b * a.mask_batch + key]);
+    first[n] = a.causal ? max(key - (a.Lk - a.Lq), 0) * G : 0;
+    float top_v = 0.f;
+    const T* kr = static_cast<const T*>(a.k.p) + b * a.k.batch + key * a.k.token + hk * a.k.head;
+    const T* vr = static_cast<const T*>(a.v.p) + b * a.v.batch + key * a.v.token + hk * a.v.head;
 #pragma unroll
-      for (int s = 0; s < TL::kSteps; ++s) {
-        const int d = 16 * s + 8 * h;
-        const bool in = live[n] && d < D;
-        kf[n][s] = in ? *reinterpret_cast<const u32x4*>(kr + d) : u32x4{0, 0, 0, 0};
-        const u32x4 v = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
-        if constexpr (kScaled<T>) top_v = amax_x8<T>(top_v, v);
-        if constexpr (kHoldV)
-          vf[n][s] = v;
-        else   // (read by this wave alone)
-          *reinterpret_cast<u32x4*>(held + (wave * NB + n) * 32 * TL::kRowBytes + (pl.straight ^ (s << 5))) = v;
-      }
-      const float c = kScaled<T> ? ds_scale(D, top_do, max_halves(top_v)) : 1.f;
-      dsc[n] = c / kProbScale;
-      fk[n] = a.scale / c;
+    for (int s = 0; s < TL::kSteps; ++s) {
+      const int d = 16 * s + 8 * h;
+      const bool in = live[n] && d < D;
+      kf[n][s] = in ? *reinterpret_cast<const u32x4*>(kr + d) : u32x4{0, 0, 0, 0};
+      const u32x4 v = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
+      if constexpr (kScaled<T>) top_v = amax_x8<T>(top_v, v);
+      if constexpr (kHoldV)
+        vf[n][s] = v;
+      else   // (read by this wave alone)
+        *reinterpret_cast<u32x4*>(held + (wave * NB + n) * 32 * TL::kRowBytes + (pl.straight ^ (s << 5))) = v;
     }
-    const uint8_t* my_v = held + (kHoldV ? 0 : wave * NB * 32 * TL::kRowBytes);
-    // rows that see no key at all are read as zeros
-    int dead = 0;
-    if (a.causal) {
-      int k = 0;   // the first key that the mask keeps
-      if (a.mask) {
-        const uint8_t* mask = a.mask + b * a.mask_batch;
-        uint64_t some = 0;
-        for (; k < a.Lk && some == 0; k += 64) some = __ballot(k + lane < a.Lk && mask[k + lane]);
-        k = some ? k - 64 + __builtin_ctzll(some) : a.Lk;
-      }
-      dead = min(max(k - (a.Lk - a.Lq), 0), a.Lq) * G;
+    const float c = kScaled<T> ? ds_scale(D, top_do, max_halves(top_v)) : 1.f;
+    dsc[n] = c / kProbScale;
+    fk[n] = a.scale / c;
+  }
+  const uint8_t* my_v = held + (kHoldV ? 0 : wave * NB * 32 * TL::kRowBytes);
+  // rows that see no key at all are read as zeros
+  int dead = 0;
+  if (a.causal) {
+    int k = 0;   // the first key that the mask keeps
+    if (a.mask) {
+      const uint8_t* mask = a.mask + b * a.mask_batch;
+      uint64_t some = 0;
+      for (; k < a.Lk && some == 0; k += 64) some = __ballot(k + lane < a.Lk && mask[k + lane]);
+      k = some ? k - 64 + __builtin_ctzll(some) : a.Lk;
     }
-    const int r_begin = at.first * kAttnRows, tiles = at.last - at.first;
-    const int w_first = a.causal ? max(key0 - (a.Lk - a.Lq), 0) * G : 0;
-    const int w_all = a.causal ? max(key0 + 32 * NB - 1 - (a.Lk - a.Lq), 0) * G : 0;   // from here on rows see all of the wave's keys
+    dead = min(max(k - (a.Lk - a.Lq), 0), a.Lq) * G;
+  }
+  const int r_begin = at.first * kAttnRows, tiles = at.last - at.first;
+  const int w_first = a.causal ? max(key0 - (a.Lk - a.Lq), 0) * G : 0;
+  const int w_all = a.causal ? max(key0 + 32 * NB - 1 - (a.Lk - a.Lq), 0) * G : 0;   // from here on rows see all of the wave's keys
 
-    auto fetch = [&](int row0, int stage) {
-      const int i0 = row0 / G, i1 = min(row0 + kAttnRows - 1, R - 1) / G;
-      // the heads of the queries i0 .. i1
-      const auto rq = rows_resource(qp + i0 * a.q.token, (int)((i1 - i0) * a.q.token + (G - 1) * a.q.head + D) * 2);
-      const auto rd = rows_resource(dop + i0 * g.dout.token, (int)((i1 - i0) * g.dout.token + (G - 1) * g.dout.head + D) * 2);
-      uint8_t *tq = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *td = tq + TL::kBytes;
+  auto fetch = [&](int row0, int stage) {
+    const int i0 = row0 / G, i1 = min(row0 + kAttnRows - 1, R - 1) / G;
+    // the heads of the queries i0 .. i1
+    const auto rq = rows_resource(qp + i0 * a.q.token, (int)((i1 - i0) * a.q.token + (G - 1) * a.q.head + D) * 2);
+    const auto rd = rows_resource(dop + i0 * g.dout.token, (int)((i1 - i0) * g.dout.token + (G - 1) * g.dout.head + D) * 2);
+    uint8_t *tq = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *td = tq + TL::kBytes;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int j = wave * NT + n, ch = TL::chunk_of(j, lane), r = row0 + TL::row_of(j, lane);
-        const int i = G == 1 ? r : r / G, hd = r - i * G;
-        const bool in = r < R && r >= dead && ch * 8 < D;
-        lds_transfer_16(rq, tq + n * 1024, in ? (uint32_t)(((i - i0) * a.q.token + hd * a.q.head + ch * 8) * 2) : kPastEnd);
-        lds_transfer_16(rd, td + n * 1024, in ? (uint32_t)(((i - i0) * g.dout.token + hd * g.dout.head + ch * 8) * 2) : kPastEnd);
-      }
-      if (wave < 2) {   // (rows up to whole tiles are there)
-        const auto rs = rows_resource((wave == 0 ? lse : delta) + row0, kAttnRows * 4);
-        lds_transfer_4(rs, reinterpret_cast<uint8_t*>(stats[stage][wave]), lane * 4);
-      }
-    };
-
-    f32x16 dk[TL::kBlocks][NB], dv[TL::kBlocks][NB];
-#pragma unroll
-    for (int i = 0; i < TL::kBlocks; ++i)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) dk[i][n] = dv[i][n] = f32x16{};
-    if (tiles > 0) fetch(r_begin, 0);
-    for (int t = 0, row0 = r_begin; t < tiles; ++t, row0 += kAttnRows) {
-      tile_barrier();
-      if (t + 1 < tiles) fetch(row0 + kAttnRows, (t + 1) & 1);
-      const uint8_t *tq = smem + (t & 1) * 2 * TL::kBytes, *td = tq + TL::kBytes;
-      const float *tl = stats[t & 1][0], *tD = stats[t & 1][1];
-#pragma unroll
-      for (int rb = 0; rb < 2; ++rb) {
-        if (row0 + 32 * rb + 31 < w_first) continue;   // none of these rows sees a key of this wave
-        // The scores' accumulators start with -lse / scale, those of do v^T with
-        // -delta, each row's in its registers.
-        f32x16 s[NB], dp[NB];
-        u32x4 p[2][NB];
-        auto start = [&](const float* rows, f32x16(&to)[NB]) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(rows + 32 * rb + 8 * q + 4 * h);
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) to[n][4 * q + i] = v[i];
-          }
-        };
-        const bool part = row0 + 32 * rb < w_all;
-        start(tl, s);
-#pragma unroll
-        for (int st = 0; st < TL::kSteps; ++st) {
-          const u32x4 qf = TL::straight(tq, pl, rb, st);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) s[n] = mma<T>(qf, kf[n][st], s[n]);
-        }
-        sched_products<TL::kSteps * NB, 4 + TL::kSteps, 1, 8>();
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[n][i] = __builtin_amdgcn_exp2f(kScaled<T> ? __builtin_fmaf(s[n][i], a.scale_log2, 10.f) : s[n][i] * a.scale_log2);
-          if (part) {
-            const int lim = first[n] - row0 - 32 * rb - 4 * h;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[n][i] = 8 * (i / 4) + i % 4 >= lim ? s[n][i] : 0.f;
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(s[n], u);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < TL::kBlocks; ++i) {
-            const u32x4 df = TL::turned(td, pl, 2 * rb + u, i);
-#pragma unroll
-            for (int n = 0; n < NB; ++n) dv[i][n] = mma<T>(df, p[u][n], dv[i][n]);
-          }
-        start(tD, dp);
-#pragma unroll
-        for (int st = 0; st < TL::kSteps; ++st) {
-          const u32x4 df = TL::straight(td, pl, rb, st);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if constexpr (kHoldV)
-              dp[n] = mma<T>(df, vf[n][st], dp[n]);
-            else
-              dp[n] = mma<T>(df, TL::straight(my_v, pl, n, st), dp[n]);
-          }
-        }
-        sched_products<(2 * TL::kBlocks + TL::kSteps) * NB, 4 * TL::kBlocks + (kHoldV ? 1 : 2) * TL::kSteps, 2, 4>();
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dp[n][i] *= kScaled<T> ? s[n][i] * dsc[n] : s[n][i];
-          if (part) {   // (do may hold what times 0 is NaN)
-            const int lim = first[n] - row0 - 32 * rb - 4 * h;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dp[n][i] = 8 * (i / 4) + i % 4 >= lim ? dp[n][i] : 0.f;
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(dp[n], u);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < TL::kBlocks; ++i) {
-            const u32x4 qf = TL::turned(tq, pl, 2 * rb + u, i);
-#pragma unroll
-            for (int n = 0; n < NB; ++n) dk[i][n] = mma<T>(qf, p[u][n], dk[i][n]);
-          }
-        sched_products<2 * TL::kBlocks * NB, 4 * TL::kBlocks, 2, 4>();
-      }
+    for (int n = 0; n < NT; ++n) {
+      const int j = wave * NT + n, ch = TL::chunk_of(j, lane), r = row0 + TL::row_of(j, lane);
+      const int i = G == 1 ? r : r / G, hd = r - i * G;
+      const bool in = r < R && r >= dead && ch * 8 < D;
+      lds_transfer_16(rq, tq + n * 1024, in ? (uint32_t)(((i - i0) * a.q.token + hd * a.q.head + ch * 8) * 2) : kPastEnd);
+      lds_transfer_16(rd, td + n * 1024, in ? (uint32_t)(((i - i0) * g.dout.token + hd * g.dout.head + ch * 8) * 2) : kPastEnd);
     }
-    const float fv = kScaled<T> ? 1.f / kProbScale : 1.f;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int key = key0 + 32 * n + lr;
-      if (key >= a.Lk) continue;
-      if (SHARED && at.part >= 0) {
-        float* row = a.part + ((int64_t)at.part * a.part_rows + key - at.block * (32 * NB * W)) * 2 * D;
-#pragma unroll
-        for (int blk = 0; blk < TL::kBlocks; ++blk)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int d = 32 * blk + 8 * q + 4 * h;
-            if (d >= D) continue;
-            f32x4 x, y;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[i] = live[n] ? dk[blk][n][4 * q + i] * fk[n] : 0.f;
-              y[i] = live[n] ? dv[blk][n][4 * q + i] * fv : 0.f;
-            }
-            *reinterpret_cast<f32x4*>(row + d) = x;
-            *reinterpret_cast<f32x4*>(row + D + d) = y;
-          }
-        continue;
-      }
-      T* kr = static_cast<T*>(g.dk.p) + b * g.dk.batch + key * g.dk.token + hk * g.dk.head;
-      T* vr = static_cast<T*>(g.dv.p) + b * g.dv.batch + key * g.dv.token + hk * g.dv.head;
-#pragma unroll
-      for (int blk = 0; blk < TL::kBlocks; ++blk) {
-        u32x4 x[2], y[2];
-        head_chunks<T>(dk[blk][n], fk[n], x);
-        head_chunks<T>(dv[blk][n], fv, y);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int d = 32 * blk + 16 * q + 8 * h;
-          if (d >= D) continue;
-          *reinterpret_cast<u32x4*>(kr + d) = live[n] ? x[q] : u32x4{0, 0, 0, 0};   // (a dropped key has no gradient)
-          *reinterpret_cast<u32x4*>(vr + d) = live[n] ? y[q] : u32x4{0, 0, 0, 0};
-        }
-      }
+    if (wave < 2) {   // (rows up to whole tiles are there)
+      const auto rs = rows_resource((wave == 0 ? lse : delta) + row0, kAttnRows * 4);
+      lds_transfer_4(rs, reinterpret_cast<uint8_t*>(stats[stage][wave]), lane * 4);
     }
   };
-  AttnPiece at;
-  if constexpr (SHARED) {
-    while (deal.walk.next(a.cost, a.plan, place, at)) {
-      note_span(a, at, place);
-      run(at);
-      __syncthreads();   // (the piece's tiles are read)
+
+  f32x16 dk[TL::kBlocks][NB], dv[TL::kBlocks][NB];
+#pragma unroll
+  for (int i = 0; i < TL::kBlocks; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) dk[i][n] = dv[i][n] = f32x16{};
+  if (tiles > 0) fetch(r_begin, 0);
+  for (int t = 0, row0 = r_begin; t < tiles; ++t, row0 += kAttnRows) {
+    tile_barrier();
+    if (t + 1 < tiles) fetch(row0 + kAttnRows, (t + 1) & 1);
+    const uint8_t *tq = smem + (t & 1) * 2 * TL::kBytes, *td = tq + TL::kBytes;
+    const float *tl = stats[t & 1][0], *tD = stats[t & 1][1];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      if (row0 + 32 * rb + 31 < w_first) continue;   // none of these rows sees a key of this wave
+      // The scores' accumulators start with -lse / scale, those of do v^T with
+      // -delta, each row's in its registers.
+      f32x16 s[NB], dp[NB];
+      u32x4 p[2][NB];
+      auto start = [&](const float* rows, f32x16(&to)[NB]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(rows + 32 * rb + 8 * q + 4 * h);
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[n][4 * q + i] = v[i];
+        }
+      };
+      const bool part = row0 + 32 * rb < w_all;
+      start(tl, s);
+#pragma unroll
+      for (int st = 0; st < TL::kSteps; ++st) {
+        const u32x4 qf = TL::straight(tq, pl, rb, st);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[n] = mma<T>(qf, kf[n][st], s[n]);
+      }
+      sched_products<TL::kSteps * NB, 4 + TL::kSteps, 1, 8>();
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[n][i] = __builtin_amdgcn_exp2f(kScaled<T> ? __builtin_fmaf(s[n][i], a.scale_log2, 10.f) : s[n][i] * a.scale_log2);
+        if (part) {
+          const int lim = first[n] - row0 - 32 * rb - 4 * h;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[n][i] = 8 * (i / 4) + i % 4 >= lim ? s[n][i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(s[n], u);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < TL::kBlocks; ++i) {
+          const u32x4 df = TL::turned(td, pl, 2 * rb + u, i);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) dv[i][n] = mma<T>(df, p[u][n], dv[i][n]);
+        }
+      start(tD, dp);
+#pragma unroll
+      for (int st = 0; st < TL::kSteps; ++st) {
+        const u32x4 df = TL::straight(td, pl, rb, st);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          if constexpr (kHoldV)
+            dp[n] = mma<T>(df, vf[n][st], dp[n]);
+          else
+            dp[n] = mma<T>(df, TL::straight(my_v, pl, n, st), dp[n]);
+        }
+      }
+      sched_products<(2 * TL::kBlocks + TL::kSteps) * NB, 4 * TL::kBlocks + (kHoldV ? 1 : 2) * TL::kSteps, 2, 4>();
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[n][i] *= kScaled<T> ? s[n][i] * dsc[n] : s[n][i];
+        if (part) {   // (do may hold what times 0 is NaN)
+          const int lim = first[n] - row0 - 32 * rb - 4 * h;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dp[n][i] = 8 * (i / 4) + i % 4 >= lim ? dp[n][i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(dp[n], u);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < TL::kBlocks; ++i) {
+          const u32x4 qf = TL::turned(tq, pl, 2 * rb + u, i);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) dk[i][n] = mma<T>(qf, p[u][n], dk[i][n]);
+        }
+      sched_products<2 * TL::kBlocks * NB, 4 * TL::kBlocks, 2, 4>();
     }
-  } else {
-    deal.walk.next(a.cost, a.plan, place, at);
-    run(at);
+  }
+  const float fv = kScaled<T> ? 1.f / kProbScale : 1.f;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int key = key0 + 32 * n + lr;
+    if (key >= a.Lk) continue;
+    if (PARTS && !at.whole) {
+      float* row = a.part + ((int64_t)place * a.part_rows + key - at.block * (32 * NB * W)) * 2 * D;
+#pragma unroll
+      for (int blk = 0; blk < TL::kBlocks; ++blk)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int d = 32 * blk + 8 * q + 4 * h;
+          if (d >= D) continue;
+          f32x4 x, y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = live[n] ? dk[blk][n][4 * q + i] * fk[n] : 0.f;
+            y[i] = live[n] ? dv[blk][n][4 * q + i] * fv : 0.f;
+          }
+          *reinterpret_cast<f32x4*>(row + d) = x;
+          *reinterpret_cast<f32x4*>(row + D + d) = y;
+        }
+      continue;
+    }
+    T* kr = static_cast<T*>(g.dk.p) + b * g.dk.batch + key * g.dk.token + hk * g.dk.head;
+    T* vr = static_cast<T*>(g.dv.p) + b * g.dv.batch + key * g.dv.token + hk * g.dv.head;
+#pragma unroll
+    for (int blk = 0; blk < TL::kBlocks; ++blk) {
+      u32x4 x[2], y[2];
+      head_chunks<T>(dk[blk][n], fk[n], x);
+      head_chunks<T>(dv[blk][n], fv, y);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int d = 32 * blk + 16 * q + 8 * h;
+        if (d >= D) continue;
+        *reinterpret_cast<u32x4*>(kr + d) = live[n] ? x[q] : u32x4{0, 0, 0, 0};   // (a dropped key has no gradient)
+        *reinterpret_cast<u32x4*>(vr + d) = live[n] ? y[q] : u32x4{0, 0, 0, 0};
+      }
+    }
   }
 }
 
 // dq of 32 NB query rows a wave; the keys pass by, as in the forward (4608
 // tokens, 24 heads of 128: 345 us, 1.13 PFLOP/s).
-template <typename T, int DP, int W, int NB, bool SHARED>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_dq_kernel(AttnGradArgs g, typename AttnDeal<SHARED>::Shares shares) {
+template <typename T, int DP, int W, int NB, bool PARTS>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
@@ -362,237 +349,225 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     vv[n] = ch * 8 < D ? (uint32_t)((row_of[n] * a.v.token + ch * 8) * 2) : kPastEnd;
   }
   const int place = attn_place(a.plan, blockIdx.x);
-  AttnDeal<SHARED> deal(a.plan, place, shares);
-  auto run = [&](const AttnPiece& at) __attribute__((always_inline)) {
-    const int b = at.hb / a.Hk, hk = at.hb % a.Hk;
-    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
-    const T* dop = static_cast<const T*>(g.dout.p) + b * g.dout.batch + (int64_t)hk * G * g.dout.head;
-    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
-    const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
-    const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch : nullptr;
-    const T* op = static_cast<const T*>(a.o.p) + b * a.o.batch + (int64_t)hk * G * a.o.head;
-    const int64_t Rp = (int64_t)g.row_blocks * kAttnBlock;
-    const float top_v = kScaled<T> ? wave_top(g.top_v + at.hb * g.key_runs, g.key_runs, lane) : 0.f;
+  const AttnPiece at = piece_of(a, deal, place);
+  const int b = at.hb / a.Hk, hk = at.hb % a.Hk;
+  const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + (int64_t)hk * G * a.q.head;
+  const T* dop = static_cast<const T*>(g.dout.p) + b * g.dout.batch + (int64_t)hk * G * g.dout.head;
+  const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
+  const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch : nullptr;
+  const T* op = static_cast<const T*>(a.o.p) + b * a.o.batch + (int64_t)hk * G * a.o.head;
+  const int64_t Rp = g.rows_padded;
+  const float top_v = kScaled<T> ? wave_top(g.top_v + at.hb * g.key_runs, g.key_runs, lane) : 0.f;
 
-    const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
-    u32x4 qf[NB][TL::kSteps], df[NB][TL::kSteps];
-    int last[NB];
-    float lse[NB], delta[NB], c[NB], wg_top = 0.f;   // (lse and delta negative)
+  const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
+  u32x4 qf[NB][TL::kSteps], df[NB][TL::kSteps];
+  int last[NB];
+  float lse[NB], delta[NB], c[NB], wg_top = 0.f;   // (lse and delta negative)
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int r = r0 + 32 * n + lr, i = r / G, hd = r - i * G;
-      last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
-      float top_do = 0.f, sum = 0.f;
+  for (int n = 0; n < NB; ++n) {
+    const int r = r0 + 32 * n + lr, i = r / G, hd = r - i * G;
+    last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
+    float top_do = 0.f, sum = 0.f;
 #pragma unroll
-      for (int s = 0; s < TL::kSteps; ++s) {
-        const int d = 16 * s + 8 * h;
-        const bool in = r < R && d < D;
-        qf[n][s] = in ? *reinterpret_cast<const u32x4*>(qp + i * a.q.token + hd * a.q.head + d) : u32x4{0, 0, 0, 0};
-        df[n][s] = in ? *reinterpret_cast<const u32x4*>(dop + i * g.dout.token + hd * g.dout.head + d) : u32x4{0, 0, 0, 0};
-        const u32x4 o = in ? *reinterpret_cast<const u32x4*>(op + i * a.o.token + hd * a.o.head + d) : u32x4{0, 0, 0, 0};
+    for (int s = 0; s < TL::kSteps; ++s) {
+      const int d = 16 * s + 8 * h;
+      const bool in = r < R && d < D;
+      qf[n][s] = in ? *reinterpret_cast<const u32x4*>(qp + i * a.q.token + hd * a.q.head + d) : u32x4{0, 0, 0, 0};
+      df[n][s] = in ? *reinterpret_cast<const u32x4*>(dop + i * g.dout.token + hd * g.dout.head + d) : u32x4{0, 0, 0, 0};
+      const u32x4 o = in ? *reinterpret_cast<const u32x4*>(op + i * a.o.token + hd * a.o.head + d) : u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) sum = dot_x2<T>(sum, df[n][s][w], o[w]);
-        if constexpr (kScaled<T>) top_do = amax_x8<T>(top_do, df[n][s]);
-      }
-      // -lse / scale and -delta; of a row without keys (and behind the last
-      // row) -infinity, which makes its probabilities zero, and 0
-      const float l = r < R ? a.lse[((int64_t)b * a.H + hk * G + hd) * a.Lq + i] : -__builtin_inff();
-      const bool none = l == -__builtin_inff();
-      lse[n] = none ? l : -l / a.scale;
-      sum = sum_halves(sum);
-      delta[n] = none ? 0.f : -sum;
-      if (at.starts) {   // for the keys' gradients, which start with them
-        if (h == 0) g.lse[at.hb * Rp + r] = lse[n];
-        if (h == 1) g.delta[at.hb * Rp + r] = delta[n];
-      }
-      lse[n] *= a.scale_log2;   // in base 2
-      if constexpr (kScaled<T>) {
-        top_do = none ? 0.f : max_halves(top_do);   // (a row that sees no key may hold anything)
-        c[n] = ds_scale(D, top_do, top_v);
-        wg_top = __builtin_fmaxf(wg_top, top_do);
-      } else {
-        c[n] = 1.f;
-      }
+      for (int w = 0; w < 4; ++w) sum = dot_x2<T>(sum, df[n][s][w], o[w]);
+      if constexpr (kScaled<T>) top_do = amax_x8<T>(top_do, df[n][s]);
     }
-    if (kScaled<T> && at.starts) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) wg_top = __builtin_fmaxf(wg_top, __shfl_xor(wg_top, d));
-      if (lane == 0) tops[wave] = wg_top;
-      __syncthreads();
-      if (tid == 0) {
-#pragma unroll
-        for (int w = 1; w < W; ++w) wg_top = __builtin_fmaxf(wg_top, tops[w]);
-        g.top_do[at.hb * g.row_blocks + at.block] = wg_top;
-      }
+    // -lse / scale and -delta; of a row without keys (and behind the last
+    // row) -infinity, which makes its probabilities zero, and 0
+    const float l = r < R ? a.lse[((int64_t)b * a.H + hk * G + hd) * a.Lq + i] : -__builtin_inff();
+    const bool none = l == -__builtin_inff();
+    lse[n] = none ? l : -l / a.scale;
+    sum = sum_halves(sum);
+    delta[n] = none ? 0.f : -sum;
+    if (at.starts) {   // for the keys' gradients, which start with them
+      if (h == 0) g.lse[at.hb * Rp + r] = lse[n];
+      if (h == 1) g.delta[at.hb * Rp + r] = delta[n];
     }
-    const int k_begin = at.first * kAttnRows, tiles = at.last - at.first;
-    const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
-    const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
+    lse[n] *= a.scale_log2;   // in base 2
+    if constexpr (kScaled<T>) {
+      top_do = none ? 0.f : max_halves(top_do);   // (a row that sees no key may hold anything)
+      c[n] = ds_scale(D, top_do, top_v);
+      wg_top = __builtin_fmaxf(wg_top, top_do);
+    } else {
+      c[n] = 1.f;
+    }
+  }
+  if (kScaled<T> && at.starts) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) wg_top = __builtin_fmaxf(wg_top, __shfl_xor(wg_top, d));
+    if (lane == 0) tops[wave] = wg_top;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 1; w < W; ++w) wg_top = __builtin_fmaxf(wg_top, tops[w]);
+      g.top_do[at.hb * g.row_blocks + at.block] = wg_top;
+    }
+  }
+  const int k_begin = at.first * kAttnRows, tiles = at.last - at.first;
+  const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
+  const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
 
-    auto fetch = [&](int k0, int stage, uint64_t keep) {
-      const int rows = min(kAttnRows, a.Lk - k0);
-      const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
-      const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
-      uint8_t *tk = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
-      if (keep == ~0ull) {
+  auto fetch = [&](int k0, int stage, uint64_t keep) {
+    const int rows = min(kAttnRows, a.Lk - k0);
+    const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
+    const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
+    uint8_t *tk = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
+    if (keep == ~0ull) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          lds_transfer_16(rk, tk + n * 1024, vk[n]);
-          lds_transfer_16(rv, tv + n * 1024, vv[n]);
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const bool in = keep >> row_of[n] & 1;
-          lds_transfer_16(rk, tk + n * 1024, in ? vk[n] : kPastEnd);
-          lds_transfer_16(rv, tv + n * 1024, in ? vv[n] : kPastEnd);
-        }
+      for (int n = 0; n < NT; ++n) {
+        lds_transfer_16(rk, tk + n * 1024, vk[n]);
+        lds_transfer_16(rv, tv + n * 1024, vv[n]);
       }
-    };
-    auto mask_byte = [&](int k0) -> int {
-      const int k = k0 + lane;
-      return k < a.Lk ? (mask ? (int)mask[k] : 1) : 0;
-    };
-
-    f32x16 dq[TL::kBlocks][NB];
+    } else {
 #pragma unroll
-    for (int i = 0; i < TL::kBlocks; ++i)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) dq[i][n] = f32x16{};
-    uint64_t keep = 0, next_keep = 0;
-    int next_byte = 0;
-    if (tiles > 0) {
-      next_keep = __ballot(mask_byte(k_begin) != 0);
-      fetch(k_begin, 0, next_keep);
-      next_byte = mask_byte(k_begin + kAttnRows);
-    }
-    for (int t = 0, k0 = k_begin; t < tiles; ++t, k0 += kAttnRows) {
-      keep = next_keep;
-      tile_barrier();
-      if (t + 1 < tiles) {
-        next_keep = __ballot(next_byte != 0);
-        fetch(k0 + kAttnRows, (t + 1) & 1, next_keep);
-        next_byte = mask_byte(k0 + 2 * kAttnRows);
-      }
-      if (k0 > w_last || keep == 0) continue;
-      const uint8_t *tk = smem + (t & 1) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
-      const bool part = keep != ~0ull || k0 + kAttnRows - 1 > w_first;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        f32x16 s[NB], dp[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          s[n] = f32x16{};
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dp[n][i] = delta[n];
-        }
-#pragma unroll
-        for (int st = 0; st < TL::kSteps; ++st) {
-          const u32x4 f = TL::straight(tk, pl, kb, st);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) s[n] = mma<T>(f, qf[n][st], s[n]);
-        }
-#pragma unroll
-        for (int st = 0; st < TL::kSteps; ++st) {
-          const u32x4 f = TL::straight(tv, pl, kb, st);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) dp[n] = mma<T>(f, df[n][st], dp[n]);
-        }
-        sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
-        u32x4 ds[2][NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], a.scale_log2, lse[n]));
-            dp[n][i] *= kScaled<T> ? p * c[n] : p;
-          }
-          if (part) {
-            const int lim = last[n] - k0 - 32 * kb - 4 * h;
-            const uint32_t bits = (uint32_t)(keep >> (32 * kb)) >> (4 * h);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at_key = 8 * (i / 4) + i % 4;
-              dp[n][i] = (bits >> at_key & 1) && at_key <= lim ? dp[n][i] : 0.f;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) ds[u][n] = as_operand<T>(dp[n], u);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < TL::kBlocks; ++i) {
-            const u32x4 f = TL::turned(tk, pl, 2 * kb + u, i);
-#pragma unroll
-            for (int n = 0; n < NB; ++n) dq[i][n] = mma<T>(f, ds[u][n], dq[i][n]);
-          }
-        sched_products<2 * TL::kBlocks * NB, 4 * TL::kBlocks, 2, 8>();
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int r = r0 + 32 * n + lr, i = r / G, hd = hk * G + r - i * G;
-      const float f = a.scale / c[n];
-      if (r >= R) continue;
-      if (SHARED && at.part >= 0) {
-        float* row = a.part + ((int64_t)at.part * a.part_rows + r - at.block * (32 * NB * W)) * D;
-#pragma unroll
-        for (int blk = 0; blk < TL::kBlocks; ++blk)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int d = 32 * blk + 8 * q + 4 * h;
-            if (d < D)
-              *reinterpret_cast<f32x4*>(row + d) = f32x4{dq[blk][n][4 * q], dq[blk][n][4 * q + 1], dq[blk][n][4 * q + 2],
-                                                         dq[blk][n][4 * q + 3]} * f;
-          }
-        continue;
-      }
-      T* row = static_cast<T*>(g.dq.p) + b * g.dq.batch + i * g.dq.token + hd * g.dq.head;
-#pragma unroll
-      for (int blk = 0; blk < TL::kBlocks; ++blk) {
-        u32x4 x[2];
-        head_chunks<T>(dq[blk][n], f, x);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int d = 32 * blk + 16 * q + 8 * h;
-          if (d < D) *reinterpret_cast<u32x4*>(row + d) = x[q];
-        }
+      for (int n = 0; n < NT; ++n) {
+        const bool in = keep >> row_of[n] & 1;
+        lds_transfer_16(rk, tk + n * 1024, in ? vk[n] : kPastEnd);
+        lds_transfer_16(rv, tv + n * 1024, in ? vv[n] : kPastEnd);
       }
     }
   };
-  AttnPiece at;
-  if constexpr (SHARED) {
-    while (deal.walk.next(a.cost, a.plan, place, at)) {
-      note_span(a, at, place);
-      run(at);
-      __syncthreads();   // (the piece's tiles are read)
+  auto mask_byte = [&](int k0) -> int {
+    const int k = k0 + lane;
+    return k < a.Lk ? (mask ? (int)mask[k] : 1) : 0;
+  };
+
+  f32x16 dq[TL::kBlocks][NB];
+#pragma unroll
+  for (int i = 0; i < TL::kBlocks; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) dq[i][n] = f32x16{};
+  uint64_t keep = 0, next_keep = 0;
+  int next_byte = 0;
+  if (tiles > 0) {
+    next_keep = __ballot(mask_byte(k_begin) != 0);
+    fetch(k_begin, 0, next_keep);
+    next_byte = mask_byte(k_begin + kAttnRows);
+  }
+  for (int t = 0, k0 = k_begin; t < tiles; ++t, k0 += kAttnRows) {
+    keep = next_keep;
+    tile_barrier();
+    if (t + 1 < tiles) {
+      next_keep = __ballot(next_byte != 0);
+      fetch(k0 + kAttnRows, (t + 1) & 1, next_keep);
+      next_byte = mask_byte(k0 + 2 * kAttnRows);
     }
-  } else {
-    deal.walk.next(a.cost, a.plan, place, at);
-    run(at);
+    if (k0 > w_last || keep == 0) continue;
+    const uint8_t *tk = smem + (t & 1) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
+    const bool part = keep != ~0ull || k0 + kAttnRows - 1 > w_first;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16 s[NB], dp[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        s[n] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[n][i] = delta[n];
+      }
+#pragma unroll
+      for (int st = 0; st < TL::kSteps; ++st) {
+        const u32x4 f = TL::straight(tk, pl, kb, st);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[n] = mma<T>(f, qf[n][st], s[n]);
+      }
+#pragma unroll
+      for (int st = 0; st < TL::kSteps; ++st) {
+        const u32x4 f = TL::straight(tv, pl, kb, st);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) dp[n] = mma<T>(f, df[n][st], dp[n]);
+      }
+      sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
+      u32x4 ds[2][NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], a.scale_log2, lse[n]));
+          dp[n][i] *= kScaled<T> ? p * c[n] : p;
+        }
+        if (part) {
+          const int lim = last[n] - k0 - 32 * kb - 4 * h;
+          const uint32_t bits = (uint32_t)(keep >> (32 * kb)) >> (4 * h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at_key = 8 * (i / 4) + i % 4;
+            dp[n][i] = (bits >> at_key & 1) && at_key <= lim ? dp[n][i] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) ds[u][n] = as_operand<T>(dp[n], u);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < TL::kBlocks; ++i) {
+          const u32x4 f = TL::turned(tk, pl, 2 * kb + u, i);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) dq[i][n] = mma<T>(f, ds[u][n], dq[i][n]);
+        }
+      sched_products<2 * TL::kBlocks * NB, 4 * TL::kBlocks, 2, 8>();
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int r = r0 + 32 * n + lr, i = r / G, hd = hk * G + r - i * G;
+    const float f = a.scale / c[n];
+    if (r >= R) continue;
+    if (PARTS && !at.whole) {
+      float* row = a.part + ((int64_t)place * a.part_rows + r - at.block * (32 * NB * W)) * D;
+#pragma unroll
+      for (int blk = 0; blk < TL::kBlocks; ++blk)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int d = 32 * blk + 8 * q + 4 * h;
+          if (d < D)
+            *reinterpret_cast<f32x4*>(row + d) = f32x4{dq[blk][n][4 * q], dq[blk][n][4 * q + 1], dq[blk][n][4 * q + 2],
+                                                       dq[blk][n][4 * q + 3]} * f;
+        }
+      continue;
+    }
+    T* row = static_cast<T*>(g.dq.p) + b * g.dq.batch + i * g.dq.token + hd * g.dq.head;
+#pragma unroll
+    for (int blk = 0; blk < TL::kBlocks; ++blk) {
+      u32x4 x[2];
+      head_chunks<T>(dq[blk][n], f, x);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int d = 32 * blk + 16 * q + 8 * h;
+        if (d < D) *reinterpret_cast<u32x4*>(row + d) = x[q];
+      }
+    }
   }
 }
 
-// The parts of shared units added in order, a half wave a row: rows of dq, or
+// The parts of units added in order, a half wave a row: rows of dq, or
 // of dk and dv side by side.
 template <typename T, bool KEYS>
-__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g) {
+__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, AttnParts deal) {
   const AttnArgs& a = g.f;
-  const int unit = blockIdx.x, w0 = a.spans[2 * unit], w1 = a.spans[2 * unit + 1];
-  if (w0 == w1) return;   // one workgroup had all of it
-  const int hb = unit / a.plan.blocks, block = unit - hb * a.plan.blocks;
-  const int lane = threadIdx.x & 31, in = (int)blockIdx.y * 8 + (threadIdx.x >> 5), r = block * kAttnBlock + in;
+  const AttnPart at = deal.at[blockIdx.x];
+  if (at.part != 0 || at.parts == 1) return;   // (a unit's first workgroup's place joins it)
+  const int hb = at.unit / a.plan.blocks, block = at.unit - hb * a.plan.blocks;
+  const int lane = threadIdx.x & 31, in = (int)blockIdx.y * 8 + (threadIdx.x >> 5), r = block * a.cost.block + in;
   const int width = KEYS ? 2 * a.D : a.D, b = hb / a.Hk, hk = hb % a.Hk, i = r / a.G;
   if (in >= a.part_rows || r >= a.cost.held) return;
   for (int d = lane * 4; d < width; d += 128) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int w = w0; w <= w1; w += 8) {   // eight loads at a time
+    for (int w = 0; w < at.parts; w += 8) {   // eight loads at a time
       f32x4 u[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        u[k] = w + k <= w1 ? *reinterpret_cast<const f32x4*>(a.part + (attn_part(w0, w + k) * a.part_rows + in) * width + d)
-                           : f32x4{0.f, 0.f, 0.f, 0.f};
+        u[k] = w + k < at.parts
+                   ? *reinterpret_cast<const f32x4*>(a.part + ((int64_t)(blockIdx.x + w + k) * a.part_rows + in) * width + d)
+                   : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 8; ++k) v += u[k];
     }
@@ -607,35 +582,42 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g) {
   }
 }
 
-template <typename T, int DP, bool KEYS, bool SHARED>
+template <typename T, int DP, int W, bool KEYS, bool PARTS>
 constexpr auto grad_kernel() {
   if constexpr (KEYS)
-    return attn_dkv_kernel<T, DP, 8, 1, SHARED>;
+    return attn_dkv_kernel<T, DP, W, 1, PARTS>;
   else
-    return attn_dq_kernel<T, DP, 8, 1, SHARED>;
+    return attn_dq_kernel<T, DP, W, 1, PARTS>;
 }
-template <int DP, bool KEYS>
-constexpr int kGradLds = 4 * AttnTile<DP>::kBytes + (KEYS && DP != 64 ? kAttnBlock * DP * 2 : 0);
+template <int DP, int W, bool KEYS>
+constexpr int kGradLds = 4 * AttnTile<DP>::kBytes + (KEYS && DP != 64 ? W * kAttnWave * DP * 2 : 0);
 
-template <typename T, int DP, bool KEYS>
+template <typename T, int DP, int W, bool KEYS>
 hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
   if (plan.grid == 0) return hipSuccess;
   g.f.cost = cost;
   g.f.plan = plan;
   g.f.part_rows = (int)attn_part_rows(cost);
-  const dim3 grid((unsigned)plan.grid), block(512);
-  if (!plan.shared) {
-    hipLaunchKernelGGL((grad_kernel<T, DP, KEYS, false>()), grid, block, (kGradLds<DP, KEYS>), st, g, AttnDeal<false>::Shares{});
+  const dim3 grid((unsigned)plan.grid), block(64 * W);
+  if (!plan.each) {
+    hipLaunchKernelGGL((grad_kernel<T, DP, W, KEYS, false>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, AttnUnits{});
     return hipGetLastError();
   }
-  AttnShares shares;
-  attn_shares(cost, plan, &shares);
-  hipLaunchKernelGGL((grad_kernel<T, DP, KEYS, true>()), grid, block, (kGradLds<DP, KEYS>), st, g, shares);
+  AttnParts deal;
+  attn_parts(cost, plan, &deal);
+  hipLaunchKernelGGL((grad_kernel<T, DP, W, KEYS, true>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, deal);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 rows((unsigned)(plan.blocks * plan.heads), (unsigned)((g.f.part_rows + 7) / 8));
-  hipLaunchKernelGGL((attn_grad_join_kernel<T, KEYS>), rows, dim3(256), 0, st, g);
+  const dim3 rows((unsigned)plan.grid, (unsigned)((g.f.part_rows + 7) / 8));
+  hipLaunchKernelGGL((attn_grad_join_kernel<T, KEYS>), rows, dim3(256), 0, st, g, deal);
   return hipGetLastError();
+}
+// (heads above 64: a workgroup of keys has eight waves, see attn_key_cost)
+template <typename T, int DP, bool KEYS>
+hipError_t launch_pass(const AttnGradArgs& g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
+  if constexpr (!KEYS || DP == 64)
+    if (cost.block == 4 * kAttnWave) return launch_pass<T, DP, 4, KEYS>(g, cost, plan, st);
+  return launch_pass<T, DP, 8, KEYS>(g, cost, plan, st);
 }
 
 template <typename T, int DP>
@@ -648,23 +630,24 @@ hipError_t launch_bwd(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }
-  const AttnSizes s = {a.B, a.Lq, a.Lk, a.H, a.Hk, a.D, a.causal != 0, kScaled<T>};
   // (dq's pass leaves what dk and dv's starts with)
-  if ((e = launch_pass<T, DP, false>(g, attn_row_cost(s), w.dq, st)) != hipSuccess) return e;
-  return launch_pass<T, DP, true>(g, attn_key_cost(s), w.dkv, st);
+  if ((e = launch_pass<T, DP, false>(g, w.rows, w.dq, st)) != hipSuccess) return e;
+  return launch_pass<T, DP, true>(g, w.keys, w.dkv, st);
 }
 
-template <typename T, int DP, bool KEYS>
+template <typename T, int DP, int W, bool KEYS>
 hipError_t prepare_pass() {
-  for (const void* f : {(const void*)grad_kernel<T, DP, KEYS, false>(), (const void*)grad_kernel<T, DP, KEYS, true>()}) {
-    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kGradLds<DP, KEYS>);
+  for (const void* f : {(const void*)grad_kernel<T, DP, W, KEYS, false>(), (const void*)grad_kernel<T, DP, W, KEYS, true>()}) {
+    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kGradLds<DP, W, KEYS>);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 template <typename T>
 hipError_t prepare_bwd() {
-  for (hipError_t e : {prepare_pass<T, 64, false>(), prepare_pass<T, 64, true>(), prepare_pass<T, 128, false>(), prepare_pass<T, 128, true>()})
+  for (hipError_t e : {prepare_pass<T, 64, 4, false>(), prepare_pass<T, 64, 8, false>(), prepare_pass<T, 64, 4, true>(),
+                       prepare_pass<T, 64, 8, true>(), prepare_pass<T, 128, 4, false>(), prepare_pass<T, 128, 8, false>(),
+                       prepare_pass<T, 128, 8, true>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
 }

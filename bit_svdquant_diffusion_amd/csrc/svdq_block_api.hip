@@ -146,7 +146,7 @@ svdq_status check_attention(const svdq_attention_desc* d) {
   if (d->samples < 0 || d->queries < 0 || d->keys < 0 || d->samples > 65535 || d->queries >= most || d->keys >= most)
     return SVDQ_ERR_SHAPE;
   const int64_t heads = d->samples * d->kv_heads, rows = d->queries * group;
-  const int64_t blocks = (std::max(rows, d->keys) + kAttnBlock - 1) / kAttnBlock;
+  const int64_t blocks = (std::max(rows, d->keys) + 4 * kAttnWave - 1) / (4 * kAttnWave);
   if (heads > 65535 || rows >= most || blocks * std::max<int64_t>(heads, 1) > ((int64_t)1 << 22)) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
@@ -364,12 +364,11 @@ svdq_status svdq_attention_forward(const svdq_attention_desc* d, const svdq_head
   SVDQ_TRY(check_ws(ws, ws_bytes, w.total));
   SVDQ_TRY(check_device(nullptr, nullptr, kKernelsAttention));
   a.lse = lse;
-  a.cost = attn_row_cost(sizes_of(d));
+  a.cost = w.cost;
   a.plan = w.plan;
   a.part_rows = (int)attn_part_rows(a.cost);
   a.part = (float*)((uint8_t*)ws + w.part);
   a.part_lse = (float*)((uint8_t*)ws + w.part_lse);
-  a.spans = (int*)((uint8_t*)ws + w.spans);
   hipStream_t st = (hipStream_t)stream;
   return after_launch(launch_attention(a, st), st);
 }
@@ -419,8 +418,8 @@ svdq_status svdq_attention_backward(const svdq_attention_desc* d, const svdq_hea
   g.top_do = (float*)(at + w.top_do);
   g.top_v = (float*)(at + w.top_v);
   g.f.part = (float*)(at + w.part);
-  g.f.spans = (int*)(at + w.spans);
   g.row_blocks = w.dq.blocks;
+  g.rows_padded = (int64_t)w.dq.blocks * w.rows.block;
   g.key_runs = w.key_runs;
   hipStream_t st = (hipStream_t)stream;
   return after_launch(launch_attention_grad(g, w, st), st);

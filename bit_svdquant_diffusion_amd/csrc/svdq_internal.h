@@ -205,15 +205,15 @@ struct AttnArgs {
   AttnCost cost;             // the launch: what is held and what passes,
   AttnPlan plan;             // and how it is dealt
   int part_rows;
-  float* part;               // parts of shared units: [2 grid][part_rows][D] (dk and dv: [2][D])
-  float* part_lse;           // [2 grid][part_rows]
-  int* spans;                // of shared units: the first and the last workgroup
+  float* part;               // parts of units: [grid][part_rows][D] (dk and dv: [2][D])
+  float* part_lse;           // [grid][part_rows]
 };
 struct AttnGradArgs {
   AttnArgs f;
   Heads dout, dq, dk, dv;
-  float *lse, *delta;        // -lse / scale and -delta, [B Hk][whole blocks of rows]
-  int row_blocks;
+  float *lse, *delta;        // -lse / scale and -delta, [B Hk][rows_padded]
+  int row_blocks;            // of dq's pass
+  int64_t rows_padded;       // whole blocks
   float *top_do, *top_v;     // fp16: the largest magnitudes [B Hk][row_blocks], [B Hk][key_runs]
   int key_runs;
 };

@@ -368,19 +368,20 @@ inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group
 }
 
 // Attention: the held rows (keys, for their gradients) of a key head lie in
-// `blocks` of kAttnBlock, the other side passes by in tiles of kAttnTile; a
-// unit is a block's walk along its tiles. With as many units as CUs a workgroup
-// takes a unit. With fewer, up to one workgroup a CU share the units evenly,
-// tile by tile: a unit whose tiles fall to several has its parts joined by
-// another kernel. (More units than CUs even out badly, too, 432 units in two
-// rounds, but there power bounds the products: with half of the CUs busy each
-// is a third faster. Workspaces' sizes are asked for without a device, so the
-// plan is this card's.)
-constexpr int kAttnCus = 256, kAttnTile = 64, kAttnBlock = 256, kAttnKeyRun = 256;
+// blocks of kAttnWave a wave, four or eight waves; the other side passes by in
+// tiles of kAttnTile. A unit is a block's walk along its tiles, and a
+// workgroup's work, unless there are fewer units than `slots` workgroups that
+// run at once: then units are cut into parts of about as many tiles as let all
+// parts run at once, whose results another kernel joins. (More units than slots
+// even out badly, too, 432 units in two rounds of 256, but there power bounds
+// the products: with half of the CUs busy each is a third faster. Workspaces'
+// sizes are asked for without a device, so the plan is this card's.)
+constexpr int kAttnCus = 256, kAttnSlots = 2 * kAttnCus, kAttnTile = 64, kAttnWave = 32, kAttnKeyRun = 256;
 struct AttnCost {
   int held, passing, group;   // rows (queries times the group, or keys) and the group's heads
   int offset;                 // keys - queries where causal
   int causal, by_keys;        // by_keys: keys are held
+  int block;                  // held rows of a workgroup
 };
 // the tiles of block b: first and one past the last
 SVDQ_HD inline void attn_tiles(const AttnCost& c, int b, int* first, int* last) {
@@ -389,182 +390,169 @@ SVDQ_HD inline void attn_tiles(const AttnCost& c, int b, int* first, int* last) 
   *last = all;
   if (!c.causal) return;
   if (c.by_keys) {   // from the first row that sees the block's first key on
-    const int64_t q = (int64_t)b * kAttnBlock - c.offset, r = q > 0 ? q * c.group : 0;
+    const int64_t q = (int64_t)b * c.block - c.offset, r = q > 0 ? q * c.group : 0;
     *first = r < c.passing ? (int)r / kAttnTile : all;
   } else {   // up to the last key that the block's last row sees
-    const int end = c.held - b * kAttnBlock < kAttnBlock ? c.held : (b + 1) * kAttnBlock;
+    const int end = c.held - b * c.block < c.block ? c.held : (b + 1) * c.block;
     const int k = (int)((unsigned)(end - 1) / (unsigned)c.group) + c.offset + 1;
     *last = k <= 0 ? 0 : k < c.passing ? (k + kAttnTile - 1) / kAttnTile : all;
   }
 }
-// (a block without tiles still writes its zeros)
-SVDQ_HD inline int attn_cost(const AttnCost& c, int b) {
+inline int attn_cost(const AttnCost& c, int b) {
   int first, last;
   attn_tiles(c, b, &first, &last);
-  return last > first ? last - first : 1;
+  return last - first;
 }
 struct AttnPlan {
-  int blocks, grid, heads;
-  int shared;   // the units are shared: workgroup w's tiles start at total w / grid of their sequence
-  int total;
+  int blocks, heads, grid;
+  int each;   // tiles of a part at most, 0: a workgroup has a unit
 };
-inline AttnPlan attn_plan(const AttnCost& c, int64_t heads) {
+// parts of a unit of `cost` tiles (one without tiles still writes its zeros)
+inline int attn_parts_of(int cost, int each) { return cost > each ? (cost + each - 1) / each : 1; }
+inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, int slots) {
   AttnPlan p;
-  p.blocks = (int)(((int64_t)c.held + kAttnBlock - 1) / kAttnBlock);
+  p.blocks = (int)(((int64_t)c.held + c.block - 1) / c.block);
   p.heads = (int)heads;
-  const int64_t units = p.blocks * heads;
-  p.grid = (int)units;
-  p.shared = p.total = 0;
-  if (units == 0 || units >= kAttnCus) return p;
+  p.grid = (int)(p.blocks * heads);
+  p.each = 0;
+  if (p.grid == 0 || p.grid >= kAttnCus) return p;
   int64_t total = 0;
-  for (int b = 0; b < p.blocks; ++b) total += attn_cost(c, b);
-  total *= heads;
-  // a part is at least four tiles, and nearly a unit a workgroup is not worth joining
-  const int64_t grid = total / 4 < kAttnCus ? total / 4 : kAttnCus;
-  if (total >= ((int64_t)1 << 31) || (c.causal ? grid <= units : grid * 9 <= units * 10)) return p;
-  p.grid = (int)grid;
-  p.shared = 1;
-  p.total = (int)total;
+  int most = 0;
+  for (int b = 0; b < p.blocks; ++b) {
+    const int n = attn_cost(c, b);
+    total += n;
+    most = n > most ? n : most;
+  }
+  // the smallest parts, of four tiles at least, that run at once
+  int64_t each = total * heads / slots;
+  for (each = each < 4 ? 4 : each; each < most; each += (each + 15) / 16) {
+    int64_t parts = 0;
+    for (int b = 0; b < p.blocks; ++b) parts += attn_parts_of(attn_cost(c, b), (int)each);
+    if (parts * heads <= slots) {
+      p.grid = (int)(parts * heads);
+      p.each = (int)each;
+      return p;
+    }
+  }
   return p;
 }
-// Where the workgroups of a shared launch start, found on the host.
-struct AttnStart {
-  uint16_t hb, block;
-  int skip;   // tiles of the block before
+// A workgroup's part, one of `parts` of the unit (hb, block); found on the host
+// where units have several. Those of a unit stand side by side.
+struct AttnPart {
+  uint32_t unit : 8, part : 12, parts : 12;
 };
-struct AttnShares {
-  AttnStart at[kAttnCus];
+struct AttnParts {
+  AttnPart at[kAttnSlots];
 };
-inline void attn_shares(const AttnCost& c, const AttnPlan& p, AttnShares* s) {
-  int hb = 0, block = 0;
-  int64_t before = 0, cost = attn_cost(c, 0);   // tiles before (hb, block), and its own
-  for (int w = 0; w < p.grid; ++w) {
-    const int64_t x = (int64_t)p.total * w / p.grid;
-    while (x >= before + cost) {
-      before += cost;
-      if (++block == p.blocks) {
-        block = 0;
-        ++hb;
-      }
-      cost = attn_cost(c, block);
-    }
-    s->at[w] = AttnStart{(uint16_t)hb, (uint16_t)block, (int)(x - before)};
+inline void attn_parts(const AttnCost& c, const AttnPlan& p, AttnParts* s) {
+  int n = 0;
+  for (int u = 0; u < p.blocks * p.heads; ++u) {   // (fewer than 256, and at most 512 parts)
+    const int parts = attn_parts_of(attn_cost(c, u % p.blocks), p.each);
+    for (int i = 0; i < parts; ++i) s->at[n++] = AttnPart{(uint32_t)u, (uint32_t)i, (uint32_t)parts};
   }
 }
-// A workgroup's pieces: its unit, or its parts of shared units. Workgroup i
-// runs on XCD i % 8; each XCD takes a contiguous run of the heads' units, so
-// that the tiles that pass by stay in its L2.
-struct AttnPiece {
-  int hb, block, unit;
-  int first, last;       // tiles of the passing side
-  int part;              // its place in the workspace, -1: the unit is whole
-  bool starts, ends;     // the unit's first, last tile is in it
-};
+// Workgroup i runs on XCD i % 8; each XCD takes a contiguous run of the heads'
+// units, so that the tiles that pass by stay in its L2.
 SVDQ_HD inline int attn_place(const AttnPlan& p, int id) {
   const int xcd = id & 7, per = p.grid >> 3, rem = p.grid & 7;
   return xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
 }
-struct AttnWhole {   // a unit a workgroup
-  bool more = true;
-  SVDQ_HD bool next(const AttnCost& c, const AttnPlan& p, int w, AttnPiece& o) {
-    if (!more) return false;
-    more = false;
-    o.unit = w;
-    o.hb = w / p.blocks;
-    o.block = w - o.hb * p.blocks;
-    // (causal: the blocks that see most first)
-    if (c.causal && !c.by_keys) o.block = p.blocks - 1 - o.block;
-    attn_tiles(c, o.block, &o.first, &o.last);
-    o.part = -1;
-    o.starts = o.ends = true;
-    return true;
-  }
+struct AttnPiece {
+  int hb, block;
+  int first, last;   // tiles of the passing side
+  bool whole, starts;   // all of the unit; its first tile
 };
-struct AttnWalk {   // parts of shared units
-  int hb, block, skip, left;
-  SVDQ_HD AttnWalk(const AttnPlan& p, int w, const AttnStart& at) : hb(at.hb), block(at.block), skip(at.skip) {
-    const int64_t x = (int64_t)p.total * w, y = x + p.total;
-    left = (int)(y / p.grid - x / p.grid);
-  }
-  SVDQ_HD bool next(const AttnCost& c, const AttnPlan& p, int w, AttnPiece& o) {
-    if (left <= 0) return false;
-    int first, last;
-    attn_tiles(c, block, &first, &last);
-    const int cost = last > first ? last - first : 1, n = cost - skip < left ? cost - skip : left;
-    o.unit = hb * p.blocks + block;
-    o.hb = hb;
-    o.block = block;
-    o.first = first + skip;
-    o.last = first + skip + n < last ? first + skip + n : last;
-    o.part = n == cost ? -1 : 2 * w + (skip == 0);
-    o.starts = skip == 0;
-    o.ends = skip + n == cost;
-    left -= n;
-    skip = 0;
-    if (++block == p.blocks) {
-      block = 0;
-      ++hb;
-    }
-    return true;
-  }
-};
-// The parts of a unit that started with workgroup w0 and ended with w1 > w0 lie
-// at 2 w0 + 1, 2 (w0 + 1), ... 2 w1.
-SVDQ_HD inline int64_t attn_part(int w0, int w) { return 2 * w + (w == w0); }
-// rows of a part in the workspace; each workgroup has at most two
-inline int64_t attn_part_rows(const AttnCost& c) { return c.held < kAttnBlock ? c.held : kAttnBlock; }
-inline size_t attn_parts(const AttnCost& c, const AttnPlan& p) {
-  return p.shared ? (size_t)2 * p.grid * attn_part_rows(c) : 0;
+SVDQ_HD inline AttnPiece attn_piece(const AttnCost& c, const AttnPlan& p, int place) {
+  AttnPiece o;
+  o.hb = place / p.blocks;
+  o.block = place - o.hb * p.blocks;
+  // (causal: the blocks that see most first)
+  if (c.causal && !c.by_keys) o.block = p.blocks - 1 - o.block;
+  attn_tiles(c, o.block, &o.first, &o.last);
+  o.whole = o.starts = true;
+  return o;
 }
+SVDQ_HD inline AttnPiece attn_piece(const AttnCost& c, const AttnPlan& p, const AttnPart& at) {
+  AttnPiece o;
+  o.hb = at.unit / p.blocks;
+  o.block = at.unit - o.hb * p.blocks;
+  int first, last;
+  attn_tiles(c, o.block, &first, &last);
+  const int64_t n = last - first;
+  o.first = first + (int)(n * at.part / at.parts);
+  o.last = first + (int)(n * (at.part + 1) / at.parts);
+  o.whole = at.parts == 1;
+  o.starts = at.part == 0;
+  return o;
+}
+// rows of a part in the workspace
+inline int64_t attn_part_rows(const AttnCost& c) { return c.held < c.block ? c.held : c.block; }
+inline size_t attn_all_part_rows(const AttnCost& c, const AttnPlan& p) { return p.each ? (size_t)p.grid * attn_part_rows(c) : 0; }
 struct AttnSizes {
   int64_t B, Lq, Lk, H, Hk, D;
   bool causal, scaled;   // scaled: fp16
 };
+// Waves of a workgroup: eight where there is such a block for every CU, since
+// they share a tile (4608 tokens, 24 heads of 128: 250 us against 269 with
+// four), else four, two workgroups a CU (2 x 1531 causal queries: 37 us against
+// 48); eight again where a wave holds all rows and the tiles' stream is what
+// takes time (one query over 65536 keys: 65 against 68).
+inline int attn_waves(int64_t held, int64_t heads) {
+  return held > kAttnWave && (held + 8 * kAttnWave - 1) / (8 * kAttnWave) * heads < kAttnCus ? 4 : 8;
+}
 inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
-  return AttnCost{(int)(s.Lq * (s.H / s.Hk)), (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0};
+  const int64_t rows = s.Lq * (s.H / s.Hk);
+  return AttnCost{(int)rows, (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0,
+                  kAttnWave * attn_waves(rows, s.B * s.Hk)};
 }
 inline AttnCost attn_key_cost(const AttnSizes& s) {
-  return AttnCost{(int)s.Lk, (int)(s.Lq * (s.H / s.Hk)), (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1};
+  const int64_t rows = s.Lq * (s.H / s.Hk);
+  // (with heads above 64 what a workgroup of four waves needs of LDS lets no second one in)
+  return AttnCost{(int)s.Lk, (int)rows, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1,
+                  kAttnWave * (s.D > 64 ? 8 : attn_waves(s.Lk, s.B * s.Hk))};
 }
-constexpr size_t kAttnSpans = align256((size_t)kAttnCus * 8);   // of shared units: the first and the last workgroup
+inline AttnPlan attn_plan(const AttnCost& c, int64_t heads) {
+  return attn_plan(c, heads, c.block == 8 * kAttnWave ? kAttnCus : 2 * kAttnCus);
+}
 struct AttnWs {
+  AttnCost cost;
   AttnPlan plan;
-  size_t part, part_lse, spans, total;
+  size_t part, part_lse, total;
 };
 inline AttnWs attn_ws(const AttnSizes& s) {
   AttnWs w;
-  const AttnCost c = attn_row_cost(s);
-  w.plan = attn_plan(c, s.B * s.Hk);
-  const size_t n = attn_parts(c, w.plan);
+  w.cost = attn_row_cost(s);
+  w.plan = attn_plan(w.cost, s.B * s.Hk);
+  const size_t n = attn_all_part_rows(w.cost, w.plan);
   w.part = 0;
   w.part_lse = align256(n * s.D * 4);
-  w.spans = w.part_lse + align256(n * 4);
-  w.total = w.spans + (w.plan.shared ? kAttnSpans : 0);
+  w.total = w.part_lse + align256(n * 4);
   return w;
 }
 // The backward's: -lse / scale and -delta of the rows (whole blocks), the
 // largest |do| of a block of rows and |v| of a run of keys (fp16), and the
 // parts of dq, then of dk and dv.
 struct AttnGradWs {
-  AttnPlan dkv, dq;
+  AttnCost rows, keys;
+  AttnPlan dq, dkv;
   int key_runs;
-  size_t lse, delta, top_do, top_v, spans, part, total;
+  size_t lse, delta, top_do, top_v, part, total;
 };
 inline AttnGradWs attn_grad_ws(const AttnSizes& s) {
   AttnGradWs w;
   const int64_t heads = s.B * s.Hk;
-  const AttnCost rows = attn_row_cost(s), keys = attn_key_cost(s);
-  w.dkv = attn_plan(keys, heads);
-  w.dq = attn_plan(rows, heads);
+  w.rows = attn_row_cost(s);
+  w.keys = attn_key_cost(s);
+  w.dq = attn_plan(w.rows, heads);
+  w.dkv = attn_plan(w.keys, heads);
   w.key_runs = s.scaled ? (int)((s.Lk + kAttnKeyRun - 1) / kAttnKeyRun) : 0;
-  const size_t padded = align256((size_t)heads * w.dq.blocks * kAttnBlock * 4);
+  const size_t padded = align256((size_t)heads * w.dq.blocks * w.rows.block * 4);
   w.lse = 0;
   w.delta = padded;
   w.top_do = 2 * padded;
   w.top_v = w.top_do + (s.scaled ? align256((size_t)heads * w.dq.blocks * 4) : 0);
-  w.spans = w.top_v + align256((size_t)heads * w.key_runs * 4);
-  w.part = w.spans + (w.dkv.shared || w.dq.shared ? kAttnSpans : 0);
-  const size_t a = attn_parts(keys, w.dkv) * 2 * s.D * 4, b = attn_parts(rows, w.dq) * s.D * 4;
+  w.part = w.top_v + align256((size_t)heads * w.key_runs * 4);
+  const size_t a = attn_all_part_rows(w.keys, w.dkv) * 2 * s.D * 4, b = attn_all_part_rows(w.rows, w.dq) * s.D * 4;
   w.total = w.part + align256(a > b ? a : b);
   return w;
 }

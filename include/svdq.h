@@ -816,7 +816,7 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * but lie in the same tile.
  * Limits: head_dim a multiple of 8 up to 128; 1 <= kv_heads, heads a multiple
  * of kv_heads, samples * kv_heads <= 65535; queries * heads / kv_heads < 2^30
- * and keys < 2^30; blocks of 256 of those times samples * kv_heads <= 2^22;
+ * and keys < 2^30; blocks of 128 of those times samples * kv_heads <= 2^22;
  * scale > 0 and finite; 64 tokens (and the heads of one key head) of a tensor
  * span less than 2^30 elements. Outputs must not overlap inputs or one another.
  * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_WORKSPACE,

@@ -165,7 +165,7 @@ def one(dtype, samples, queries, keys, heads, kv, causal=0):
     st.append(S.lib().svdq_attention_backward(d, h(), h(), h(), h(), h(), P, None, 0, h(), h(), h(), P, n.value, None))
     return [st, sizes, f, launches()]
 for case in [(0, 1, 1, 1, 8, 8), (0, 1, 1, 65536, 8, 2), (1, 2, 4096, 77, 8, 8), (0, 1, 4608, 4608, 24, 24), (0, 1, 5, 0, 8, 8),
-             (0, 1, 0, 5, 8, 8), (1, 32, 1 << 20, 1 << 22, 8, 8), (0, 1, 1 << 26, 1 << 26, 8, 8)]:
+             (0, 1, 0, 5, 8, 8), (1, 16, 1 << 20, 1 << 22, 8, 8), (0, 1, 1 << 26, 1 << 26, 8, 8)]:
     result.append(one(*case))
 """)
     for st, sizes, f, g in got:
@@ -195,7 +195,9 @@ def test_python_refusals():
         S._residual_setup(64, 4, torch.bfloat16, (torch.ones(64), None, None, torch.ones(64).half()), "rms", True, 1.0, 1e-6,
                           False, None)
     with pytest.raises(ValueError, match="contiguous along the head"):
-        S._heads(q.transpose(2, 3), "q")
+        S._heads(q.transpose(2, 3), "q", (1, 4, 64, 2), q.dtype)
+    with pytest.raises(ValueError, match="shape"):
+        S._heads(q, "o", (1, 4, 2, 32), q.dtype)
     with pytest.raises(ValueError, match="k, v"):
         S._attention_setup(q, q[..., :32], q, None, False, None)
     with pytest.raises(ValueError, match="key_mask"):
