@@ -1286,7 +1286,7 @@ def residual_norm_backward(dy, s, h, stats, gate=None, weight=None, post_weight=
         grads = _EIGHT(first, first + step, first + 2 * step, first + 3 * step if post else 0)
         if not post:
             out = (*out, None)
-        size = _residual_ws(C, dt, groups, rpg, M)
+        size = _residual_ws(C, dt, groups, rpg, M, 1 if post else 0)
         if size:
             ws = _empty((size,), _t.uint8, s, stream)
             wsp = ws.data_ptr()
@@ -1298,9 +1298,9 @@ def residual_norm_backward(dy, s, h, stats, gate=None, weight=None, post_weight=
 
 
 @functools.lru_cache(maxsize=4096)
-def _residual_ws(C, dt, groups, rows_per_group, M) -> int:
+def _residual_ws(C, dt, groups, rows_per_group, M, post) -> int:
     need = ctypes.c_size_t()
-    d = ResidualDesc(C, dt, 0, 0, 0, 0, groups, 0.0, 1.0, rows_per_group)
+    d = ResidualDesc(C, dt, 0, 0, post, 0, groups, 0.0, 1.0, rows_per_group)
     _check(lib().svdq_residual_norm_backward_workspace_bytes(ctypes.byref(d), M, ctypes.byref(need)),
            "svdq_residual_norm_backward_workspace_bytes")
     return need.value
@@ -1370,7 +1370,7 @@ def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool 
     Hk, kshape = 0, None
     if k is not None:
         kshape = k.shape
-        if len(kshape) != 4 or kshape[:2] != shape[:2] or kshape[3] != D or k.dtype != dtype:
+        if len(kshape) != 4 or kshape[0] != B or kshape[1] != L or kshape[3] != D or k.dtype != dtype:
             raise ValueError("k: samples, tokens, head_dim and type of q")
         Hk = kshape[2]
     d, _, n = _rope_desc(_dt(dtype), 1 if pos == torch.float32 else 0, D, H, Hk, tuple(map(int, pairs)), 0 if interleaved else 1,

@@ -1,10 +1,10 @@
 // Device-side pieces that the attention kernels share: tiles of 64 rows (keys,
 // or queries) of a head in LDS, the fragments read from them, and the products.
 //
-// A tile's rows are DP elements (the head's D, padded with zeros to 64 or
-// 128) of two bytes. They come by `buffer_load_dwordx4 ... lds` transfers of 1
+// A tile's rows are 64 or 128 elements of two bytes, of which the products take
+// DP (64, 96 or 128: the head's D and zeros behind it). They come by `buffer_load_dwordx4 ... lds` transfers of 1
 // KiB, whose lanes fetch their 16-byte chunks permuted: chunk c of row r lies
-// at place c ^ place<DP>(r). Both kinds of fragment then meet every LDS bank
+// at place c ^ place(r). Both kinds of fragment then meet every LDS bank
 // evenly: 32 rows at one chunk (an operand whose contraction runs along the
 // head), and, by the transposing read ds_read_b64_tr_b16, columns of 8 rows at
 // four chunks (an operand whose contraction runs along the rows).
@@ -136,19 +136,17 @@ __device__ __forceinline__ void sched_products() {
 }
 
 template <int DP>
-__device__ __forceinline__ int place(int row) {
-  return DP == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-}
-
-template <int DP>
 struct AttnTile {
-  static constexpr int kRowBytes = DP * 2, kChunks = DP / 8, kBytes = kAttnRows * kRowBytes;
+  static constexpr int kRow = DP > 64 ? 128 : 64, kRowBytes = kRow * 2, kChunks = kRow / 8, kBytes = kAttnRows * kRowBytes;
   static constexpr int kTransfers = kBytes / 1024, kRowsEach = 64 / kChunks;
   static constexpr int kSteps = DP / 16, kBlocks = DP / 32;
 
+  static __device__ __forceinline__ int place(int row) {
+    return kRow == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  }
   // transfer j, this lane: its row of the tile and the chunk of the head
   static __device__ __forceinline__ int row_of(int j, int lane) { return j * kRowsEach + lane / kChunks; }
-  static __device__ __forceinline__ int chunk_of(int j, int lane) { return (lane % kChunks) ^ place<DP>(row_of(j, lane)); }
+  static __device__ __forceinline__ int chunk_of(int j, int lane) { return (lane % kChunks) ^ place(row_of(j, lane)); }
 
   // this lane's places in a tile: `straight` for operand A of rows 32 b + l %
   // 32 and head elements 16 step + 8 h + (0..7); `turned[u]` for the head
@@ -157,11 +155,11 @@ struct AttnTile {
     uint32_t straight, turned[2];
     __device__ __forceinline__ explicit Lane(int lane) {
       const int h = lane >> 5, lr = lane & 31, i = lane & 15;
-      straight = lr * kRowBytes + ((h ^ place<DP>(lr)) << 4);
+      straight = lr * kRowBytes + ((h ^ place(lr)) << 4);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int row = 8 * u + 4 * h + (i >> 2), chunk = 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
-        turned[u] = row * kRowBytes + ((chunk ^ place<DP>(row)) << 4) + (i & 1) * 8;
+        turned[u] = row * kRowBytes + ((chunk ^ place(row)) << 4) + (i & 1) * 8;
       }
     }
   };

@@ -239,12 +239,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 64
 // sum 2^(lse_s - m). WAYS half waves (32 lanes of four elements) have a row,
 // each every WAYS-th part; theirs are then joined in order through LDS.
 template <typename T, int WAYS>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnParts deal) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins joins) {
   constexpr int ROWS = 8 / WAYS;
   __shared__ float ms[8], sums[8];
   __shared__ f32x4 os[8][32];
-  const AttnPart at = deal.at[blockIdx.x];
-  if (at.part != 0 || at.parts == 1) return;   // (a unit's first workgroup's place joins it)
+  const AttnJoin at = joins.at[blockIdx.x];
   const int hb = at.unit / a.plan.blocks, block = at.unit - hb * a.plan.blocks;
   const int lane = threadIdx.x & 31, half = threadIdx.x >> 5, way = half % WAYS;
   const int in = (int)blockIdx.y * ROWS + half / WAYS, r = block * a.cost.block + in, d = lane * 4;
@@ -252,10 +251,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnParts de
   float m = -__builtin_inff(), sum = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
-    for (int w = way; w < at.parts; w += WAYS) m = __builtin_fmaxf(m, a.part_lse[(int64_t)(blockIdx.x + w) * a.part_rows + in]);
+    for (int w = way; w < at.parts; w += WAYS) m = __builtin_fmaxf(m, a.part_lse[(int64_t)(at.first + w) * a.part_rows + in]);
     const float base = m == -__builtin_inff() ? 0.f : m;
     for (int w = way; w < at.parts; w += WAYS) {
-      const int64_t row = (int64_t)(blockIdx.x + w) * a.part_rows + in;
+      const int64_t row = (int64_t)(at.first + w) * a.part_rows + in;
       const float f = __builtin_amdgcn_exp2f(a.part_lse[row] - base);
       sum += f;
       if (d < a.D) o += *reinterpret_cast<const f32x4*>(a.part + row * a.D + d) * f;
@@ -307,19 +306,22 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, true>), grid, block, kFwdLds<DP>, st, a, deal);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  AttnJoins joins;
+  const int units = attn_joins(a.plan, deal, &joins);
   // with many parts a row, all of a workgroup for one
-  const bool deep = a.plan.grid >= 4 * a.plan.blocks * a.plan.heads;
-  const dim3 rows((unsigned)a.plan.grid, (unsigned)(deep ? a.part_rows : (a.part_rows + 7) / 8));
+  const bool deep = a.plan.grid >= 12 * units;
+  const dim3 rows((unsigned)units, (unsigned)(deep ? a.part_rows : (a.part_rows + 7) / 8));
   if (deep)
-    hipLaunchKernelGGL((attn_join_kernel<T, 8>), rows, dim3(256), 0, st, a, deal);
+    hipLaunchKernelGGL((attn_join_kernel<T, 8>), rows, dim3(256), 0, st, a, joins);
   else
-    hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, deal);
+    hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, joins);
   return hipGetLastError();
 }
 template <typename T>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
   const bool wide = a.cost.block == 8 * kAttnWave;
   if (a.D <= 64) return wide ? launch_fwd<T, 64, 8>(a, st) : launch_fwd<T, 64, 4>(a, st);
+  if (a.D <= 96) return wide ? launch_fwd<T, 96, 8>(a, st) : launch_fwd<T, 96, 4>(a, st);
   return wide ? launch_fwd<T, 128, 8>(a, st) : launch_fwd<T, 128, 4>(a, st);
 }
 
@@ -333,7 +335,8 @@ hipError_t prepare_fwd() {
 }
 template <typename T>
 hipError_t prepare_fwd() {
-  for (hipError_t e : {prepare_fwd<T, 64, 4>(), prepare_fwd<T, 64, 8>(), prepare_fwd<T, 128, 4>(), prepare_fwd<T, 128, 8>()})
+  for (hipError_t e : {prepare_fwd<T, 64, 4>(), prepare_fwd<T, 64, 8>(), prepare_fwd<T, 96, 4>(), prepare_fwd<T, 96, 8>(),
+                       prepare_fwd<T, 128, 4>(), prepare_fwd<T, 128, 8>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
 }

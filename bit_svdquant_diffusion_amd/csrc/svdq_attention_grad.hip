@@ -59,15 +59,17 @@ __global__ __launch_bounds__(256) void attn_top_v_kernel(AttnGradArgs g) {
   __shared__ float red[16];
   const int hb = blockIdx.y, b = hb / a.Hk, hk = hb % a.Hk, lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
   float top = 0.f;
+  u32x4 x[kAttnKeyRun / 16];   // (all loads at once)
 #pragma unroll
   for (int k = 0; k < kAttnKeyRun / 16; ++k) {
-    const int key = blockIdx.x * kAttnKeyRun + k * 16 + slot;
-    if (key < a.Lk && lane * 8 < a.D && (!a.mask || a.mask[b * a.mask_batch + key])) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + key * a.v.token +
-                                                      hk * a.v.head + lane * 8);
-      top = amax_x8<T>(top, x);
-    }
+    const int key = blockIdx.x * kAttnKeyRun + k * 16 + slot, at = min(key, a.Lk - 1);
+    const bool in = key < a.Lk && lane * 8 < a.D && (!a.mask || a.mask[b * a.mask_batch + at]);
+    x[k] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + at * a.v.token + hk * a.v.head +
+                                           (lane * 8 < a.D ? lane * 8 : 0));
+    if (!in) x[k] = u32x4{0, 0, 0, 0};
   }
+#pragma unroll
+  for (int k = 0; k < kAttnKeyRun / 16; ++k) top = amax_x8<T>(top, x[k]);
   const uint32_t m = max_dpp16(__float_as_uint(top));   // (magnitudes: their bits are in order)
   if (lane == 0) red[slot] = __uint_as_float(m);
   __syncthreads();
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
   extern __shared__ __align__(1024) uint8_t smem[];   // [2][q, do][kBytes], then V where it is held there
-  constexpr bool kHoldV = DP == 64;   // in registers, else in LDS
+  constexpr bool kHoldV = DP < 128;   // in registers, else in LDS
   uint8_t* held = smem + 4 * TL::kBytes;
   __shared__ __align__(1024) float stats[2][2][kAttnRows];   // -lse / scale and -delta of a tile's rows
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
@@ -551,10 +553,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 // The parts of units added in order, a half wave a row: rows of dq, or
 // of dk and dv side by side.
 template <typename T, bool KEYS>
-__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, AttnParts deal) {
+__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, AttnJoins joins) {
   const AttnArgs& a = g.f;
-  const AttnPart at = deal.at[blockIdx.x];
-  if (at.part != 0 || at.parts == 1) return;   // (a unit's first workgroup's place joins it)
+  const AttnJoin at = joins.at[blockIdx.x];
   const int hb = at.unit / a.plan.blocks, block = at.unit - hb * a.plan.blocks;
   const int lane = threadIdx.x & 31, in = (int)blockIdx.y * 8 + (threadIdx.x >> 5), r = block * a.cost.block + in;
   const int width = KEYS ? 2 * a.D : a.D, b = hb / a.Hk, hk = hb % a.Hk, i = r / a.G;
@@ -566,7 +567,7 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, Att
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         u[k] = w + k < at.parts
-                   ? *reinterpret_cast<const f32x4*>(a.part + ((int64_t)(blockIdx.x + w + k) * a.part_rows + in) * width + d)
+                   ? *reinterpret_cast<const f32x4*>(a.part + ((int64_t)(at.first + w + k) * a.part_rows + in) * width + d)
                    : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 8; ++k) v += u[k];
@@ -590,7 +591,7 @@ constexpr auto grad_kernel() {
     return attn_dq_kernel<T, DP, W, 1, PARTS>;
 }
 template <int DP, int W, bool KEYS>
-constexpr int kGradLds = 4 * AttnTile<DP>::kBytes + (KEYS && DP != 64 ? W * kAttnWave * DP * 2 : 0);
+constexpr int kGradLds = 4 * AttnTile<DP>::kBytes + (KEYS && DP == 128 ? W * kAttnWave * AttnTile<DP>::kRowBytes : 0);
 
 template <typename T, int DP, int W, bool KEYS>
 hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
@@ -608,8 +609,9 @@ hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& pla
   hipLaunchKernelGGL((grad_kernel<T, DP, W, KEYS, true>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, deal);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 rows((unsigned)plan.grid, (unsigned)((g.f.part_rows + 7) / 8));
-  hipLaunchKernelGGL((attn_grad_join_kernel<T, KEYS>), rows, dim3(256), 0, st, g, deal);
+  AttnJoins joins;
+  const dim3 rows((unsigned)attn_joins(plan, deal, &joins), (unsigned)((g.f.part_rows + 7) / 8));
+  hipLaunchKernelGGL((attn_grad_join_kernel<T, KEYS>), rows, dim3(256), 0, st, g, joins);
   return hipGetLastError();
 }
 // (heads above 64: a workgroup of keys has eight waves, see attn_key_cost)
@@ -635,6 +637,12 @@ hipError_t launch_bwd(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st
   return launch_pass<T, DP, true>(g, w.keys, w.dkv, st);
 }
 
+template <typename T>
+hipError_t launch_bwd(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st) {
+  if (g.f.D <= 64) return launch_bwd<T, 64>(g, w, st);
+  return g.f.D <= 96 ? launch_bwd<T, 96>(g, w, st) : launch_bwd<T, 128>(g, w, st);
+}
+
 template <typename T, int DP, int W, bool KEYS>
 hipError_t prepare_pass() {
   for (const void* f : {(const void*)grad_kernel<T, DP, W, KEYS, false>(), (const void*)grad_kernel<T, DP, W, KEYS, true>()}) {
@@ -646,7 +654,8 @@ hipError_t prepare_pass() {
 template <typename T>
 hipError_t prepare_bwd() {
   for (hipError_t e : {prepare_pass<T, 64, 4, false>(), prepare_pass<T, 64, 8, false>(), prepare_pass<T, 64, 4, true>(),
-                       prepare_pass<T, 64, 8, true>(), prepare_pass<T, 128, 4, false>(), prepare_pass<T, 128, 8, false>(),
+                       prepare_pass<T, 64, 8, true>(), prepare_pass<T, 96, 4, false>(), prepare_pass<T, 96, 8, false>(),
+                       prepare_pass<T, 96, 8, true>(), prepare_pass<T, 128, 4, false>(), prepare_pass<T, 128, 8, false>(),
                        prepare_pass<T, 128, 8, true>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
@@ -660,8 +669,7 @@ hipError_t prepare_attention_grad() {
 }
 
 hipError_t launch_attention_grad(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st) {
-  if (g.f.dtype == SVDQ_DT_BF16) return g.f.D <= 64 ? launch_bwd<Bf16, 64>(g, w, st) : launch_bwd<Bf16, 128>(g, w, st);
-  return g.f.D <= 64 ? launch_bwd<Half, 64>(g, w, st) : launch_bwd<Half, 128>(g, w, st);
+  return g.f.dtype == SVDQ_DT_BF16 ? launch_bwd<Bf16>(g, w, st) : launch_bwd<Half>(g, w, st);
 }
 
 }  // namespace svdq

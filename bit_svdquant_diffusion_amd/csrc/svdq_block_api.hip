@@ -236,7 +236,7 @@ svdq_status svdq_residual_norm_forward(const svdq_residual_desc* d, const void* 
 svdq_status svdq_residual_norm_backward_workspace_bytes(const svdq_residual_desc* d, int64_t M, size_t* out) {
   SVDQ_TRY(check_residual(d, M));
   if (!out) return SVDQ_ERR_NULL;
-  *out = residual_grad_ws(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype));
+  *out = residual_grad_ws(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype), d->post_norm);
   return SVDQ_OK;
 }
 
@@ -273,7 +273,7 @@ svdq_status svdq_residual_norm_backward(const svdq_residual_desc* d, const void*
     if (!stats) return SVDQ_ERR_NULL;
     if (dx == dh || !aligned(stats, 4)) return SVDQ_ERR_SHAPE;
   }
-  const size_t need = any ? residual_grad_ws(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype)) : 0;
+  const size_t need = any ? residual_grad_ws(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype), d->post_norm) : 0;
   SVDQ_TRY(check_ws(ws, ws_bytes, need));
   SVDQ_TRY(check_device());
   g.f = residual_args(d, s, lds, h, ldh, params, M);
@@ -290,7 +290,7 @@ svdq_status svdq_residual_norm_backward(const svdq_residual_desc* d, const void*
   g.part = need > 0 ? (float*)ws : nullptr;
   hipStream_t st = (hipStream_t)stream;
   return after_launch(
-      launch_residual_grad(g, residual_grad_plan(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype)), st), st);
+      launch_residual_grad(g, residual_grad_plan(M, d->groups, d->rows_per_group, d->channels, elem_bytes(d->dtype), d->post_norm), st), st);
 }
 
 svdq_status svdq_rope(const svdq_rope_desc* d, const svdq_heads* q, const svdq_heads* k, const void* positions,

@@ -343,17 +343,19 @@ inline ResidualTeam residual_team(int C, int vec, int most_nv) {
 }
 // Its gradients: workgroups of sixteen waves (as many teams as these hold),
 // every group's rows in `runs` runs of one workgroup each.
-constexpr int kResidualRuns = 256;
+constexpr int kResidualRuns = 256, kResidualPostWaves = 12;
 struct ResidualGradPlan {
   int runs, teams;   // teams of a workgroup
   int64_t rows_per_run;
 };
-inline ResidualGradPlan residual_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
+inline ResidualGradPlan residual_grad_plan(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes,
+                                           bool post) {
   const int64_t rows = rows_per_group < M ? rows_per_group : M;
   const int64_t live = M > 0 ? (M - 1) / rows_per_group + 1 : 1;   // groups that have rows
   const ResidualTeam t = residual_team(C, 16 / elem_bytes, elem_bytes == 4 ? 2 : 1);
   ResidualGradPlan p;
-  p.teams = 16 / t.waves * t.sub;
+  const int waves = post && t.waves <= kResidualPostWaves ? kResidualPostWaves : 16;
+  p.teams = waves / t.waves * t.sub;
   int64_t runs = kResidualRuns / live;
   if (runs > (rows + 3) / 4) runs = (rows + 3) / 4;   // at least four rows each
   if (runs < 1 || groups > kResidualRuns || rows <= 2 * p.teams) runs = 1;
@@ -362,21 +364,21 @@ inline ResidualGradPlan residual_grad_plan(int64_t M, int64_t groups, int64_t ro
   if (p.teams > p.rows_per_run) p.teams = (int)((p.rows_per_run + t.sub - 1) / t.sub * t.sub);
   return p;
 }
-inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes) {
-  const ResidualGradPlan p = residual_grad_plan(M, groups, rows_per_group, C, elem_bytes);
+inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group, int C, int elem_bytes, bool post) {
+  const ResidualGradPlan p = residual_grad_plan(M, groups, rows_per_group, C, elem_bytes, post);
   return p.runs > 1 ? (size_t)groups * p.runs * 4 * C * 4 : 0;
 }
 
 // Attention: the held rows (keys, for their gradients) of a key head lie in
 // blocks of kAttnWave a wave, four or eight waves; the other side passes by in
 // tiles of kAttnTile. A unit is a block's walk along its tiles, and a
-// workgroup's work, unless there are fewer units than `slots` workgroups that
-// run at once: then units are cut into parts of about as many tiles as let all
-// parts run at once, whose results another kernel joins. (More units than slots
+// workgroup's work, unless there are fewer units than `below`: then units are
+// cut into parts of about as many tiles as let all parts run at once, `slots`
+// workgroups, and another kernel joins their results. (More units than slots
 // even out badly, too, 432 units in two rounds of 256, but there power bounds
 // the products: with half of the CUs busy each is a third faster. Workspaces'
 // sizes are asked for without a device, so the plan is this card's.)
-constexpr int kAttnCus = 256, kAttnSlots = 2 * kAttnCus, kAttnTile = 64, kAttnWave = 32, kAttnKeyRun = 256;
+constexpr int kAttnCus = 256, kAttnSlots = 2 * kAttnCus, kAttnTile = 64, kAttnWave = 32, kAttnKeyRun = 64;
 struct AttnCost {
   int held, passing, group;   // rows (queries times the group, or keys) and the group's heads
   int offset;                 // keys - queries where causal
@@ -409,13 +411,13 @@ struct AttnPlan {
 };
 // parts of a unit of `cost` tiles (one without tiles still writes its zeros)
 inline int attn_parts_of(int cost, int each) { return cost > each ? (cost + each - 1) / each : 1; }
-inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, int slots) {
+inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, int slots, int below) {
   AttnPlan p;
   p.blocks = (int)(((int64_t)c.held + c.block - 1) / c.block);
   p.heads = (int)heads;
   p.grid = (int)(p.blocks * heads);
   p.each = 0;
-  if (p.grid == 0 || p.grid >= kAttnCus) return p;
+  if (p.grid == 0 || p.grid >= below) return p;
   int64_t total = 0;
   int most = 0;
   for (int b = 0; b < p.blocks; ++b) {
@@ -439,17 +441,31 @@ inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, int slots) {
 // A workgroup's part, one of `parts` of the unit (hb, block); found on the host
 // where units have several. Those of a unit stand side by side.
 struct AttnPart {
-  uint32_t unit : 8, part : 12, parts : 12;
+  uint32_t unit : 10, part : 11, parts : 11;
 };
 struct AttnParts {
   AttnPart at[kAttnSlots];
 };
 inline void attn_parts(const AttnCost& c, const AttnPlan& p, AttnParts* s) {
   int n = 0;
-  for (int u = 0; u < p.blocks * p.heads; ++u) {   // (fewer than 256, and at most 512 parts)
+  for (int u = 0; u < p.blocks * p.heads; ++u) {   // (fewer than the slots, 512 at most, and no more parts)
     const int parts = attn_parts_of(attn_cost(c, u % p.blocks), p.each);
     for (int i = 0; i < parts; ++i) s->at[n++] = AttnPart{(uint32_t)u, (uint32_t)i, (uint32_t)parts};
   }
+}
+// The units that have several parts, and where the first of these stands; how
+// many such units there are.
+struct AttnJoin {
+  uint32_t unit : 10, first : 11, parts : 11;
+};
+struct AttnJoins {
+  AttnJoin at[kAttnSlots];
+};
+inline int attn_joins(const AttnPlan& p, const AttnParts& s, AttnJoins* j) {
+  int n = 0;
+  for (int w = 0; w < p.grid; ++w)
+    if (s.at[w].part == 0 && s.at[w].parts > 1) j->at[n++] = AttnJoin{s.at[w].unit, (uint32_t)w, s.at[w].parts};
+  return n;
 }
 // Workgroup i runs on XCD i % 8; each XCD takes a contiguous run of the heads'
 // units, so that the tiles that pass by stay in its L2.
@@ -507,12 +523,15 @@ inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
 }
 inline AttnCost attn_key_cost(const AttnSizes& s) {
   const int64_t rows = s.Lq * (s.H / s.Hk);
-  // (with heads above 64 what a workgroup of four waves needs of LDS lets no second one in)
+  // (with heads above 64 a workgroup of four waves of keys gains nothing: 2 x 1601 keys, heads of 72, 106 us against 93)
   return AttnCost{(int)s.Lk, (int)rows, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1,
                   kAttnWave * (s.D > 64 ? 8 : attn_waves(s.Lk, s.B * s.Hk))};
 }
-inline AttnPlan attn_plan(const AttnCost& c, int64_t heads) {
-  return attn_plan(c, heads, c.block == 8 * kAttnWave ? kAttnCus : 2 * kAttnCus);
+// (The forward's parts cost more to join than an uneven last round does: 288
+// units of 2 x 1531 causal queries 34 us whole, 38 in parts, their dq 57 and 47.)
+inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, bool forward) {
+  const int slots = c.block == 8 * kAttnWave ? kAttnCus : kAttnSlots;
+  return attn_plan(c, heads, slots, forward ? kAttnCus : slots);
 }
 struct AttnWs {
   AttnCost cost;
@@ -522,7 +541,7 @@ struct AttnWs {
 inline AttnWs attn_ws(const AttnSizes& s) {
   AttnWs w;
   w.cost = attn_row_cost(s);
-  w.plan = attn_plan(w.cost, s.B * s.Hk);
+  w.plan = attn_plan(w.cost, s.B * s.Hk, true);
   const size_t n = attn_all_part_rows(w.cost, w.plan);
   w.part = 0;
   w.part_lse = align256(n * s.D * 4);
@@ -543,8 +562,8 @@ inline AttnGradWs attn_grad_ws(const AttnSizes& s) {
   const int64_t heads = s.B * s.Hk;
   w.rows = attn_row_cost(s);
   w.keys = attn_key_cost(s);
-  w.dq = attn_plan(w.rows, heads);
-  w.dkv = attn_plan(w.keys, heads);
+  w.dq = attn_plan(w.rows, heads, false);
+  w.dkv = attn_plan(w.keys, heads, false);
   w.key_runs = s.scaled ? (int)((s.Lk + kAttnKeyRun - 1) / kAttnKeyRun) : 0;
   const size_t padded = align256((size_t)heads * w.dq.blocks * w.rows.block * 4);
   w.lse = 0;

@@ -213,8 +213,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void residual_fwd_kernel(ResidualAr
 // through LDS, one parameter after the other (P = 4 with a norm after the
 // block, else 3), and written once: to the workspace [run][4][C] in fp32, or,
 // where a group is one run, as the gradients.
-template <typename T, int NV, int SUB, bool POST>
-__global__ __launch_bounds__(64 * kMaxWaves) void residual_bwd_kernel(ResidualGradArgs g, int W, int runs) {
+template <typename T, int NV, int SUB, bool POST, int MAXW>
+__global__ __launch_bounds__(64 * MAXW) void residual_bwd_kernel(ResidualGradArgs g, int W, int runs) {
   constexpr int VEC = kVec<T>, LANES = 64 / SUB, P = POST ? 4 : 3;
   const ResidualArgs& a = g.f;
   __shared__ float red[2][2][kMaxWaves][2];
@@ -405,15 +405,6 @@ __global__ __launch_bounds__(1024) void residual_join_kernel(ResidualGradArgs g,
   }
 }
 
-#define SVDQ_RESIDUAL_LAUNCH(KERNEL, POST, WIDE, ...)                                   \
-  if (t.sub == 4)                                                                       \
-    hipLaunchKernelGGL((KERNEL<T, 1, 4, POST>), grid, block, 0, st, __VA_ARGS__);       \
-  else if (t.nv == 1)                                                                   \
-    hipLaunchKernelGGL((KERNEL<T, 1, 1, POST>), grid, block, 0, st, __VA_ARGS__);       \
-  else if constexpr (WIDE)                                                              \
-    hipLaunchKernelGGL((KERNEL<T, 2, 1, POST>), grid, block, 0, st, __VA_ARGS__);       \
-  return hipGetLastError();
-
 template <typename T, bool POST>
 hipError_t launch_fwd(const ResidualArgs& a, int num_cus, hipStream_t st) {
   const ResidualTeam t = residual_team(a.C, kVec<T>, 2);
@@ -423,14 +414,36 @@ hipError_t launch_fwd(const ResidualArgs& a, int num_cus, hipStream_t st) {
   const int64_t wgs = std::min(most, (a.M + wg_teams - 1) / wg_teams), all = wgs * wg_teams;
   const dim3 grid((unsigned)wgs), block(64 * wg_waves);
   const int per = (int)(a.M / all), extra = (int)(a.M % all);
-  SVDQ_RESIDUAL_LAUNCH(residual_fwd_kernel, POST, true, a, t.waves, per, extra)
+  if (t.sub == 4)
+    hipLaunchKernelGGL((residual_fwd_kernel<T, 1, 4, POST>), grid, block, 0, st, a, t.waves, per, extra);
+  else if (t.nv == 1)
+    hipLaunchKernelGGL((residual_fwd_kernel<T, 1, 1, POST>), grid, block, 0, st, a, t.waves, per, extra);
+  else
+    hipLaunchKernelGGL((residual_fwd_kernel<T, 2, 1, POST>), grid, block, 0, st, a, t.waves, per, extra);
+  return hipGetLastError();
 }
 
-template <typename T, bool POST>
+template <typename T, bool POST, int MAXW>
 hipError_t launch_bwd(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st) {
-  const ResidualTeam t = residual_team(g.f.C, kVec<T>, kVec<T> == 4 ? 2 : 1);
+  constexpr int NV = kVec<T> == 4 ? 2 : 1;
+  const ResidualTeam t = residual_team(g.f.C, kVec<T>, NV);
   const dim3 grid = many_groups((int64_t)g.f.G * p.runs), block(t.waves * 64 / t.sub * p.teams);
-  SVDQ_RESIDUAL_LAUNCH(residual_bwd_kernel, POST, kVec<T> == 4, g, t.waves, p.runs)
+  constexpr bool kLong = POST && MAXW == kMaxWaves;   // rows of many waves alone
+  if (!kLong && t.sub == 4) {
+    if constexpr (!kLong) hipLaunchKernelGGL((residual_bwd_kernel<T, 1, 4, POST, MAXW>), grid, block, 0, st, g, t.waves, p.runs);
+  } else if (!(kLong && NV == 2) && t.nv == 1) {
+    if constexpr (!(kLong && NV == 2))
+      hipLaunchKernelGGL((residual_bwd_kernel<T, 1, 1, POST, MAXW>), grid, block, 0, st, g, t.waves, p.runs);
+  } else if constexpr (NV == 2) {
+    hipLaunchKernelGGL((residual_bwd_kernel<T, 2, 1, POST, MAXW>), grid, block, 0, st, g, t.waves, p.runs);
+  }
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t launch_bwd(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st) {
+  if (!g.f.post) return launch_bwd<T, false, kMaxWaves>(g, p, st);
+  const int waves = residual_team(g.f.C, kVec<T>, kVec<T> == 4 ? 2 : 1).waves;
+  return waves > kResidualPostWaves ? launch_bwd<T, true, kMaxWaves>(g, p, st) : launch_bwd<T, true, kResidualPostWaves>(g, p, st);
 }
 
 }  // namespace
@@ -442,10 +455,9 @@ hipError_t launch_residual(const ResidualArgs& a, int num_cus, hipStream_t st) {
 }
 
 hipError_t launch_residual_grad(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st) {
-  const bool post = g.f.post;
-  const hipError_t e = g.f.dtype == SVDQ_DT_F32    ? (post ? launch_bwd<float, true>(g, p, st) : launch_bwd<float, false>(g, p, st))
-                       : g.f.dtype == SVDQ_DT_BF16 ? (post ? launch_bwd<Bf16, true>(g, p, st) : launch_bwd<Bf16, false>(g, p, st))
-                                                   : (post ? launch_bwd<Half, true>(g, p, st) : launch_bwd<Half, false>(g, p, st));
+  const hipError_t e = g.f.dtype == SVDQ_DT_F32    ? launch_bwd<float>(g, p, st)
+                       : g.f.dtype == SVDQ_DT_BF16 ? launch_bwd<Bf16>(g, p, st)
+                                                   : launch_bwd<Half>(g, p, st);
   if (e != hipSuccess || !g.part) return e;
   hipLaunchKernelGGL(residual_join_kernel, dim3((g.f.C + 31) / 32, (unsigned)g.f.G, g.f.post ? 4 : 3), dim3(1024), 0, st, g, p.runs);
   return hipGetLastError();

@@ -1,5 +1,5 @@
 // The attention kernels' deal of tiles to workgroups, on the host: for each
-// line "held passing group offset causal by_keys heads block" of the input,
+// line "held passing group offset causal by_keys heads block forward" of the input,
 // every workgroup's part; prints "ok grid each" or what is wrong.
 #include <stdio.h>
 
@@ -10,17 +10,18 @@
 using namespace svdq;
 
 int main() {
-  long long held, passing, group, offset, causal, by_keys, heads, block;
-  while (scanf("%lld %lld %lld %lld %lld %lld %lld %lld", &held, &passing, &group, &offset, &causal, &by_keys, &heads, &block) == 8) {
+  long long held, passing, group, offset, causal, by_keys, heads, block, forward;
+  while (scanf("%lld %lld %lld %lld %lld %lld %lld %lld %lld", &held, &passing, &group, &offset, &causal, &by_keys, &heads, &block,
+               &forward) == 9) {
     const AttnCost c = {(int)held, (int)passing, (int)group, (int)offset, (int)causal, (int)by_keys, (int)block};
     const int slots = block == 256 ? kAttnCus : kAttnSlots;
-    const AttnPlan p = attn_plan(c, heads);
+    const AttnPlan p = attn_plan(c, heads, forward);
     const int units = p.blocks * (int)heads;
     const char* bad = nullptr;
     std::vector<int> seen(p.grid, 0), at(units, 0), count(units, 0);
     AttnParts deal;
     if (p.each) {
-      if (p.grid > slots || units > 255) bad = "more parts than run at once";
+      if (p.grid > slots || units >= slots) bad = "more parts than run at once";
       else attn_parts(c, p, &deal);
     }
     int last_unit = -1;
@@ -49,6 +50,18 @@ int main() {
       int first, last;
       attn_tiles(c, u % p.blocks, &first, &last);
       if (count[u] == 0 || at[u] != last) bad = "tiles missing";
+    }
+    if (p.each && !bad) {
+      AttnJoins joins;
+      int several = 0;
+      const int n = attn_joins(p, deal, &joins);
+      for (int u = 0; u < units; ++u) several += count[u] > 1;
+      if (n != several || n == 0) bad = "units to join";
+      for (int i = 0; i < n && !bad; ++i) {
+        const AttnJoin j = joins.at[i];
+        const AttnPiece o = attn_piece(c, p, deal.at[j.first]);
+        if (o.hb * p.blocks + o.block != (int)j.unit || !o.starts || (int)j.parts != count[j.unit]) bad = "a unit to join";
+      }
     }
     if (bad)
       printf("%s: held %lld passing %lld group %lld offset %lld causal %lld keys %lld heads %lld block %lld\n", bad, held, passing,
