@@ -341,9 +341,14 @@ inline ResidualTeam residual_team(int C, int vec, int most_nv) {
   const int nv = n <= 64 ? 1 : most_nv;
   return ResidualTeam{nv, (n + 64 * nv - 1) / (64 * nv), 1};
 }
-// Its gradients: workgroups of sixteen waves (as many teams as these hold),
-// every group's rows in `runs` runs of one workgroup each.
-constexpr int kResidualRuns = 256, kResidualPostWaves = 12;
+// Its gradients: workgroups of sixteen waves (as many teams as these hold), or
+// of twelve with a norm after the block or eight fp32 elements a lane, whose
+// sums and values take 143 (165) registers of the 168 that twelve leave; every
+// group's rows in `runs` runs of one workgroup each. (Two workgroups a CU of
+// half the waves and 512 runs: 4608 x 2560 bf16 with a norm after the block 69 us
+// against 44, 8192 x 4096 without 84 against 80.)
+constexpr int kResidualRuns = 256;
+inline int residual_grad_waves(const ResidualTeam& t, bool post) { return (post || t.nv == 2) && t.waves <= 12 ? 12 : 16; }
 struct ResidualGradPlan {
   int runs, teams;   // teams of a workgroup
   int64_t rows_per_run;
@@ -354,8 +359,7 @@ inline ResidualGradPlan residual_grad_plan(int64_t M, int64_t groups, int64_t ro
   const int64_t live = M > 0 ? (M - 1) / rows_per_group + 1 : 1;   // groups that have rows
   const ResidualTeam t = residual_team(C, 16 / elem_bytes, elem_bytes == 4 ? 2 : 1);
   ResidualGradPlan p;
-  const int waves = post && t.waves <= kResidualPostWaves ? kResidualPostWaves : 16;
-  p.teams = waves / t.waves * t.sub;
+  p.teams = residual_grad_waves(t, post) / t.waves * t.sub;
   int64_t runs = kResidualRuns / live;
   if (runs > (rows + 3) / 4) runs = (rows + 3) / 4;   // at least four rows each
   if (runs < 1 || groups > kResidualRuns || rows <= 2 * p.teams) runs = 1;

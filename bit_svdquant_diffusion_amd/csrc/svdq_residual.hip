@@ -17,6 +17,7 @@
 // over the wave, the waves in order; the parameters' over a run's rows per
 // lane, then the teams and the runs in order.
 #include <algorithm>
+#include <type_traits>
 
 #include "svdq_internal.h"
 #include "svdq_layout.h"
@@ -27,6 +28,7 @@ namespace svdq {
 namespace {
 
 constexpr int kMaxWaves = 16;
+
 
 // Sums over a team, the same in each of its lanes. The caller alternates
 // areas, so one barrier per call is enough.
@@ -244,16 +246,23 @@ __global__ __launch_bounds__(64 * MAXW) void residual_bwd_kernel(ResidualGradArg
     m = min(m, m_end - 1);   // past the end: the last row again, not used
     const T *s = static_cast<const T*>(a.x) + m * a.ldx, *h = static_cast<const T*>(a.h) + m * a.ldh;
     const T *dy = static_cast<const T*>(g.dy) + m * g.lddy, *ds = static_cast<const T*>(g.ds) + m * g.ldds;
+    auto load = [&](auto once) {
+      constexpr bool ONCE = decltype(once)::value;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      ns[j] = load_vec<T>(s, pl.at(j), pl.len(j));
-      ndy[j] = load_vec<T>(dy, pl.at(j), pl.len(j));
-      nh[j] = load_vec<T>(h, pl.at(j), pl.len(j));
-      if (g.ds)
-        nds[j] = load_vec<T>(ds, pl.at(j), pl.len(j));
-      else
-        nds[j].w = u32x4{0, 0, 0, 0};
-    }
+      for (int j = 0; j < NV; ++j) {
+        ns[j] = load_vec<T, ONCE>(s, pl.at(j), pl.len(j));
+        ndy[j] = load_vec<T, ONCE>(dy, pl.at(j), pl.len(j));
+        nh[j] = load_vec<T, ONCE>(h, pl.at(j), pl.len(j));
+        if (g.ds)
+          nds[j] = load_vec<T, ONCE>(ds, pl.at(j), pl.len(j));
+        else
+          nds[j].w = u32x4{0, 0, 0, 0};
+      }
+    };
+    if (g.once)
+      load(std::true_type());
+    else
+      load(std::false_type());
     const float* st = a.stats + m;
     if (a.layer) {
       nst[0] = *st;
@@ -408,7 +417,7 @@ __global__ __launch_bounds__(1024) void residual_join_kernel(ResidualGradArgs g,
 template <typename T, bool POST>
 hipError_t launch_fwd(const ResidualArgs& a, int num_cus, hipStream_t st) {
   const ResidualTeam t = residual_team(a.C, kVec<T>, 2);
-  const int fit = t.nv * kVec<T> > 8 ? 12 : 16;   // waves of a CU at once
+  const int fit = 16;   // waves of a CU at once (8: 4608 x 2560 with a norm after the block 30 us against 25, 24: 30)
   const int wg_waves = t.waves == 1 ? 4 : t.waves, wg_teams = t.waves == 1 ? 4 * t.sub : 1;
   const int64_t most = (int64_t)num_cus * std::max(1, fit / wg_waves);
   const int64_t wgs = std::min(most, (a.M + wg_teams - 1) / wg_teams), all = wgs * wg_teams;
@@ -423,27 +432,29 @@ hipError_t launch_fwd(const ResidualArgs& a, int num_cus, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, bool POST, int MAXW>
+template <typename T, bool POST>
 hipError_t launch_bwd(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st) {
   constexpr int NV = kVec<T> == 4 ? 2 : 1;
+  constexpr int WAVES = POST ? 12 : kMaxWaves;   // of workgroups whose lanes hold a vector (residual_grad_waves)
   const ResidualTeam t = residual_team(g.f.C, kVec<T>, NV);
   const dim3 grid = many_groups((int64_t)g.f.G * p.runs), block(t.waves * 64 / t.sub * p.teams);
-  constexpr bool kLong = POST && MAXW == kMaxWaves;   // rows of many waves alone
-  if (!kLong && t.sub == 4) {
-    if constexpr (!kLong) hipLaunchKernelGGL((residual_bwd_kernel<T, 1, 4, POST, MAXW>), grid, block, 0, st, g, t.waves, p.runs);
-  } else if (!(kLong && NV == 2) && t.nv == 1) {
-    if constexpr (!(kLong && NV == 2))
-      hipLaunchKernelGGL((residual_bwd_kernel<T, 1, 1, POST, MAXW>), grid, block, 0, st, g, t.waves, p.runs);
-  } else if constexpr (NV == 2) {
-    hipLaunchKernelGGL((residual_bwd_kernel<T, 2, 1, POST, MAXW>), grid, block, 0, st, g, t.waves, p.runs);
-  }
+#define SVDQ_RESIDUAL_BWD(NV, SUB, WAVES) \
+  hipLaunchKernelGGL((residual_bwd_kernel<T, NV, SUB, POST, WAVES>), grid, block, 0, st, g, t.waves, p.runs)
+  if (t.sub == 4)
+    SVDQ_RESIDUAL_BWD(1, 4, WAVES);
+  else if (t.nv == 2) {
+    if constexpr (NV == 2) {
+      if (t.waves <= 12)
+        SVDQ_RESIDUAL_BWD(2, 1, 12);
+      else
+        SVDQ_RESIDUAL_BWD(2, 1, kMaxWaves);
+    }
+  } else if (t.waves <= WAVES)
+    SVDQ_RESIDUAL_BWD(1, 1, WAVES);
+  else if constexpr (NV == 1 && POST)
+    SVDQ_RESIDUAL_BWD(1, 1, kMaxWaves);
+#undef SVDQ_RESIDUAL_BWD
   return hipGetLastError();
-}
-template <typename T>
-hipError_t launch_bwd(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st) {
-  if (!g.f.post) return launch_bwd<T, false, kMaxWaves>(g, p, st);
-  const int waves = residual_team(g.f.C, kVec<T>, kVec<T> == 4 ? 2 : 1).waves;
-  return waves > kResidualPostWaves ? launch_bwd<T, true, kMaxWaves>(g, p, st) : launch_bwd<T, true, kResidualPostWaves>(g, p, st);
 }
 
 }  // namespace
@@ -454,10 +465,16 @@ hipError_t launch_residual(const ResidualArgs& a, int num_cus, hipStream_t st) {
   return a.post ? launch_fwd<Half, true>(a, num_cus, st) : launch_fwd<Half, false>(a, num_cus, st);
 }
 
-hipError_t launch_residual_grad(const ResidualGradArgs& g, const ResidualGradPlan& p, hipStream_t st) {
-  const hipError_t e = g.f.dtype == SVDQ_DT_F32    ? launch_bwd<float>(g, p, st)
-                       : g.f.dtype == SVDQ_DT_BF16 ? launch_bwd<Bf16>(g, p, st)
-                                                   : launch_bwd<Half>(g, p, st);
+hipError_t launch_residual_grad(const ResidualGradArgs& args, const ResidualGradPlan& p, hipStream_t st) {
+  // What the caches (256 MB) cannot keep until it is used again is read past
+  // them (8192 x 4096 bf16, 403 MB: 80 us against 92, 4608 x 5120 fp32, 472 MB:
+  // 111 against 130; 4608 x 2560 bf16, 142 MB: 45.5 against 43.2).
+  ResidualGradArgs g = args;
+  g.once = (double)g.f.M * g.f.C * (g.ds ? 6 : 5) * (g.f.dtype == SVDQ_DT_F32 ? 4 : 2) > 256e6;
+  const bool post = g.f.post;
+  const hipError_t e = g.f.dtype == SVDQ_DT_F32    ? (post ? launch_bwd<float, true>(g, p, st) : launch_bwd<float, false>(g, p, st))
+                       : g.f.dtype == SVDQ_DT_BF16 ? (post ? launch_bwd<Bf16, true>(g, p, st) : launch_bwd<Bf16, false>(g, p, st))
+                                                   : (post ? launch_bwd<Half, true>(g, p, st) : launch_bwd<Half, false>(g, p, st));
   if (e != hipSuccess || !g.part) return e;
   hipLaunchKernelGGL(residual_join_kernel, dim3((g.f.C + 31) / 32, (unsigned)g.f.G, g.f.post ? 4 : 3), dim3(1024), 0, st, g, p.runs);
   return hipGetLastError();
