@@ -2,9 +2,9 @@
 // or queries) of a head in LDS, the fragments read from them, and the products.
 //
 // A tile's rows are 64 or 128 elements of two bytes, of which the products take
-// DP (64, 96 or 128: the head's D and zeros behind it). They come by `buffer_load_dwordx4 ... lds` transfers of 1
-// KiB, whose lanes fetch their 16-byte chunks permuted: chunk c of row r lies
-// at place c ^ place(r). Both kinds of fragment then meet every LDS bank
+// DP (32, 64, 96 or 128: the head's D and zeros behind it). They come by
+// `buffer_load_dwordx4 ... lds` transfers of 1 KiB, whose lanes fetch their
+// 16-byte chunks permuted: chunk c of row r lies at place c ^ place(r). Both kinds of fragment then meet every LDS bank
 // evenly: 32 rows at one chunk (an operand whose contraction runs along the
 // head), and, by the transposing read ds_read_b64_tr_b16, columns of 8 rows at
 // four chunks (an operand whose contraction runs along the rows).
@@ -69,6 +69,33 @@ __device__ __forceinline__ u32x4 as_operand(const f32x16& v, int t) {
                cvt_x2<T>(v[8 * t + 6], v[8 * t + 7])};
 }
 
+// what that rounding took off, rounded itself: with both parts a product has
+// 2^-17 (bf16) or 2^-22 (fp16) of its operand's rounding left
+template <typename T>
+__device__ __forceinline__ u32x4 as_operand_rest(const f32x16& v, u32x4 whole, int t) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    if constexpr (__is_same(T, Bf16)) {
+      lo = bf16lo(whole[i]);
+      hi = bf16hi(whole[i]);
+    } else {
+      const uint32_t pair = whole[i];   // (a vector's element taken as another type as it stands is its first)
+      const f16x2 x = __builtin_bit_cast(f16x2, pair);
+      lo = (float)x[0];
+      hi = (float)x[1];
+    }
+    o[i] = cvt_x2<T>(v[8 * t + 2 * i] - lo, v[8 * t + 2 * i + 1] - hi);
+  }
+  return o;
+}
+template <typename T, int NP>
+__device__ __forceinline__ void as_operands(const f32x16& v, int t, u32x4 (&o)[NP]) {
+  o[0] = as_operand<T>(v, t);
+  if constexpr (NP == 2) o[1] = as_operand_rest<T>(v, o[0], t);
+}
+
 // the other half wave's value of the same column
 __device__ __forceinline__ float max_halves(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -127,7 +154,7 @@ __device__ __forceinline__ void tile_barrier() {
 // product and wait for it: the forward at 4608 tokens 270 us against 244.)
 template <int PRODUCTS, int READS, int STEP, int AHEAD, int I = 0>
 __device__ __forceinline__ void sched_products() {
-  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, AHEAD < READS ? AHEAD : READS, 0);
   if constexpr (I < PRODUCTS) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if constexpr (AHEAD + (I + 1) * STEP <= READS) __builtin_amdgcn_sched_group_barrier(0x100, STEP, 0);

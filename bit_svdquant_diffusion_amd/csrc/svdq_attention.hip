@@ -27,8 +27,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // exponentials: 4608 tokens, 24 heads of 128 with a mask 252 us (1.03
 // PFLOP/s), with one wave a SIMD 411, with one of two blocks 355, with
 // workgroups of four waves instead of eight 270.
-template <typename T, int DP, int W, int NB, bool PARTS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 64 ? 4 : 2, DP == 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
+template <typename T, int DP, int W, int NB, int NP, bool PARTS>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   constexpr int NT = TL::kTransfers / W;   // transfers of a wave for one tile
   extern __shared__ __align__(1024) uint8_t smem[];   // [2][K, V][kBytes]
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 64
         }
       }
     }
-    u32x4 p[4][NB];
+    u32x4 p[4][NB][NP];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       float top = s[0][n][0];
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 64
           s[kb][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][n][i], a.scale_log2, -base));
           l[n] += s[kb][n][i];
         }
-        p[2 * kb][n] = as_operand<T>(s[kb][n], 0);
-        p[2 * kb + 1][n] = as_operand<T>(s[kb][n], 1);
+        as_operands<T>(s[kb][n], 0, p[2 * kb][n]);
+        as_operands<T>(s[kb][n], 1, p[2 * kb + 1][n]);
       }
     }
 #pragma unroll
@@ -195,9 +195,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 64
       for (int i = 0; i < TL::kBlocks; ++i) {
         const u32x4 vf = TL::turned(tv, pl, kt, i);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) o[i][n] = mma<T>(vf, p[kt][n], o[i][n]);
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int w = 0; w < NP; ++w) o[i][n] = mma<T>(vf, p[kt][n][w], o[i][n]);
       }
-    sched_products<4 * TL::kBlocks * NB, 8 * TL::kBlocks, 2, 8>();
+    sched_products<4 * TL::kBlocks * NB * NP, 8 * TL::kBlocks, 2, 8>();
   }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -294,16 +296,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins jo
 template <int DP>
 constexpr int kFwdLds = 4 * AttnTile<DP>::kBytes;
 
-template <typename T, int DP, int W>
+template <typename T, int DP, int W, int NP>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)a.plan.grid), block(64 * W);
   if (!a.plan.each) {
-    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, false>), grid, block, kFwdLds<DP>, st, a, AttnUnits{});
+    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, NP, false>), grid, block, kFwdLds<DP>, st, a, AttnUnits{});
     return hipGetLastError();
   }
   AttnParts deal;
   attn_parts(a.cost, a.plan, &deal);
-  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, true>), grid, block, kFwdLds<DP>, st, a, deal);
+  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, NP, true>), grid, block, kFwdLds<DP>, st, a, deal);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   AttnJoins joins;
@@ -317,17 +319,26 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, joins);
   return hipGetLastError();
 }
-template <typename T>
+template <typename T, int DP>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
   const bool wide = a.cost.block == 8 * kAttnWave;
-  if (a.D <= 64) return wide ? launch_fwd<T, 64, 8>(a, st) : launch_fwd<T, 64, 4>(a, st);
-  if (a.D <= 96) return wide ? launch_fwd<T, 96, 8>(a, st) : launch_fwd<T, 96, 4>(a, st);
-  return wide ? launch_fwd<T, 128, 8>(a, st) : launch_fwd<T, 128, 4>(a, st);
+  if constexpr (DP == 32) {
+    return wide ? launch_fwd<T, DP, 8, 2>(a, st) : launch_fwd<T, DP, 4, 2>(a, st);
+  } else {
+    if (a.cost.fine) return launch_fwd<T, DP, 8, 2>(a, st);
+    return wide ? launch_fwd<T, DP, 8, 1>(a, st) : launch_fwd<T, DP, 4, 1>(a, st);
+  }
+}
+template <typename T>
+hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
+  if (a.D <= 32) return launch_fwd<T, 32>(a, st);
+  if (a.D <= 64) return launch_fwd<T, 64>(a, st);
+  return a.D <= 96 ? launch_fwd<T, 96>(a, st) : launch_fwd<T, 128>(a, st);
 }
 
-template <typename T, int DP, int W>
+template <typename T, int DP, int W, int NP>
 hipError_t prepare_fwd() {
-  for (const void* f : {(const void*)attn_fwd_kernel<T, DP, W, 1, false>, (const void*)attn_fwd_kernel<T, DP, W, 1, true>}) {
+  for (const void* f : {(const void*)attn_fwd_kernel<T, DP, W, 1, NP, false>, (const void*)attn_fwd_kernel<T, DP, W, 1, NP, true>}) {
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds<DP>);
     if (e != hipSuccess) return e;
   }
@@ -335,8 +346,9 @@ hipError_t prepare_fwd() {
 }
 template <typename T>
 hipError_t prepare_fwd() {
-  for (hipError_t e : {prepare_fwd<T, 64, 4>(), prepare_fwd<T, 64, 8>(), prepare_fwd<T, 96, 4>(), prepare_fwd<T, 96, 8>(),
-                       prepare_fwd<T, 128, 4>(), prepare_fwd<T, 128, 8>()})
+  for (hipError_t e : {prepare_fwd<T, 32, 4, 2>(), prepare_fwd<T, 32, 8, 2>(), prepare_fwd<T, 64, 4, 1>(), prepare_fwd<T, 64, 8, 1>(),
+                       prepare_fwd<T, 64, 8, 2>(), prepare_fwd<T, 96, 4, 1>(), prepare_fwd<T, 96, 8, 1>(), prepare_fwd<T, 96, 8, 2>(),
+                       prepare_fwd<T, 128, 4, 1>(), prepare_fwd<T, 128, 8, 1>(), prepare_fwd<T, 128, 8, 2>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
 }

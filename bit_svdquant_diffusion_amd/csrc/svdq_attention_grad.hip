@@ -36,7 +36,8 @@ template <typename T>
 __device__ __forceinline__ float amax_x8(float m, u32x4 w) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f16x2 v = __builtin_bit_cast(f16x2, w[i]);
+    const uint32_t pair = w[i];   // (a vector's element taken as another type as it stands is its first)
+    const f16x2 v = __builtin_bit_cast(f16x2, pair);
     m = __builtin_fmaxf(m, __builtin_fmaxf(__builtin_fabsf((float)v[0]), __builtin_fabsf((float)v[1])));
   }
   return m;
@@ -103,8 +104,8 @@ __device__ __forceinline__ float ds_scale(int D, float x, float y) {
 // waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads: 574
 // us against 760 with V in registers, of which 53 spill, 768 with one wave a
 // SIMD and two blocks of keys, 870 with workgroups of four waves).
-template <typename T, int DP, int W, int NB, bool PARTS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
+template <typename T, int DP, int W, int NB, int NP, bool PARTS>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       // The scores' accumulators start with -lse / scale, those of do v^T with
       // -delta, each row's in its registers.
       f32x16 s[NB], dp[NB];
-      u32x4 p[2][NB];
+      u32x4 p[2][NB][NP];
       auto start = [&](const float* rows, f32x16(&to)[NB]) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
           for (int i = 0; i < 16; ++i) s[n][i] = 8 * (i / 4) + i % 4 >= lim ? s[n][i] : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(s[n], u);
+        for (int u = 0; u < 2; ++u) as_operands<T>(s[n], u, p[u][n]);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -248,7 +249,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         for (int i = 0; i < TL::kBlocks; ++i) {
           const u32x4 df = TL::turned(td, pl, 2 * rb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) dv[i][n] = mma<T>(df, p[u][n], dv[i][n]);
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int w = 0; w < NP; ++w) dv[i][n] = mma<T>(df, p[u][n][w], dv[i][n]);
         }
       start(tD, dp);
 #pragma unroll
@@ -262,7 +265,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
             dp[n] = mma<T>(df, TL::straight(my_v, pl, n, st), dp[n]);
         }
       }
-      sched_products<(2 * TL::kBlocks + TL::kSteps) * NB, 4 * TL::kBlocks + (kHoldV ? 1 : 2) * TL::kSteps, 2, 4>();
+      sched_products<(2 * TL::kBlocks * NP + TL::kSteps) * NB, 4 * TL::kBlocks + (kHoldV ? 1 : 2) * TL::kSteps, 2, 4>();
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
@@ -273,7 +276,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
           for (int i = 0; i < 16; ++i) dp[n][i] = 8 * (i / 4) + i % 4 >= lim ? dp[n][i] : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) p[u][n] = as_operand<T>(dp[n], u);
+        for (int u = 0; u < 2; ++u) as_operands<T>(dp[n], u, p[u][n]);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -281,9 +284,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         for (int i = 0; i < TL::kBlocks; ++i) {
           const u32x4 qf = TL::turned(tq, pl, 2 * rb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) dk[i][n] = mma<T>(qf, p[u][n], dk[i][n]);
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int w = 0; w < NP; ++w) dk[i][n] = mma<T>(qf, p[u][n][w], dk[i][n]);
         }
-      sched_products<2 * TL::kBlocks * NB, 4 * TL::kBlocks, 2, 4>();
+      sched_products<2 * TL::kBlocks * NB * NP, 4 * TL::kBlocks, 2, 4>();
     }
   }
   const float fv = kScaled<T> ? 1.f / kProbScale : 1.f;
@@ -330,8 +335,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 
 // dq of 32 NB query rows a wave; the keys pass by, as in the forward (4608
 // tokens, 24 heads of 128: 345 us, 1.13 PFLOP/s).
-template <typename T, int DP, int W, int NB, bool PARTS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
+template <typename T, int DP, int W, int NB, int NP, bool PARTS>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
@@ -487,7 +492,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         for (int n = 0; n < NB; ++n) dp[n] = mma<T>(f, df[n][st], dp[n]);
       }
       sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
-      u32x4 ds[2][NB];
+      u32x4 ds[2][NB][NP];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
@@ -505,7 +510,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
           }
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) ds[u][n] = as_operand<T>(dp[n], u);
+        for (int u = 0; u < 2; ++u) as_operands<T>(dp[n], u, ds[u][n]);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -513,9 +518,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         for (int i = 0; i < TL::kBlocks; ++i) {
           const u32x4 f = TL::turned(tk, pl, 2 * kb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) dq[i][n] = mma<T>(f, ds[u][n], dq[i][n]);
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int w = 0; w < NP; ++w) dq[i][n] = mma<T>(f, ds[u][n][w], dq[i][n]);
         }
-      sched_products<2 * TL::kBlocks * NB, 4 * TL::kBlocks, 2, 8>();
+      sched_products<2 * TL::kBlocks * NB * NP, 4 * TL::kBlocks, 2, 8>();
     }
   }
 #pragma unroll
@@ -583,17 +590,17 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, Att
   }
 }
 
-template <typename T, int DP, int W, bool KEYS, bool PARTS>
+template <typename T, int DP, int W, int NP, bool KEYS, bool PARTS>
 constexpr auto grad_kernel() {
   if constexpr (KEYS)
-    return attn_dkv_kernel<T, DP, W, 1, PARTS>;
+    return attn_dkv_kernel<T, DP, W, 1, NP, PARTS>;
   else
-    return attn_dq_kernel<T, DP, W, 1, PARTS>;
+    return attn_dq_kernel<T, DP, W, 1, NP, PARTS>;
 }
 template <int DP, int W, bool KEYS>
 constexpr int kGradLds = 4 * AttnTile<DP>::kBytes + (KEYS && DP == 128 ? W * kAttnWave * AttnTile<DP>::kRowBytes : 0);
 
-template <typename T, int DP, int W, bool KEYS>
+template <typename T, int DP, int W, int NP, bool KEYS>
 hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
   if (plan.grid == 0) return hipSuccess;
   g.f.cost = cost;
@@ -601,12 +608,12 @@ hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& pla
   g.f.part_rows = (int)attn_part_rows(cost);
   const dim3 grid((unsigned)plan.grid), block(64 * W);
   if (!plan.each) {
-    hipLaunchKernelGGL((grad_kernel<T, DP, W, KEYS, false>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, AttnUnits{});
+    hipLaunchKernelGGL((grad_kernel<T, DP, W, NP, KEYS, false>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, AttnUnits{});
     return hipGetLastError();
   }
   AttnParts deal;
   attn_parts(cost, plan, &deal);
-  hipLaunchKernelGGL((grad_kernel<T, DP, W, KEYS, true>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, deal);
+  hipLaunchKernelGGL((grad_kernel<T, DP, W, NP, KEYS, true>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, deal);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   AttnJoins joins;
@@ -617,9 +624,12 @@ hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& pla
 // (heads above 64: a workgroup of keys has eight waves, see attn_key_cost)
 template <typename T, int DP, bool KEYS>
 hipError_t launch_pass(const AttnGradArgs& g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
-  if constexpr (!KEYS || DP == 64)
-    if (cost.block == 4 * kAttnWave) return launch_pass<T, DP, 4, KEYS>(g, cost, plan, st);
-  return launch_pass<T, DP, 8, KEYS>(g, cost, plan, st);
+  constexpr int NP = DP == 32 ? 2 : 1;
+  if constexpr (!KEYS || DP <= 64)
+    if (cost.block == 4 * kAttnWave) return launch_pass<T, DP, 4, NP, KEYS>(g, cost, plan, st);
+  if constexpr (DP > 32)
+    if (cost.fine) return launch_pass<T, DP, 8, 2, KEYS>(g, cost, plan, st);
+  return launch_pass<T, DP, 8, NP, KEYS>(g, cost, plan, st);
 }
 
 template <typename T, int DP>
@@ -639,13 +649,14 @@ hipError_t launch_bwd(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st
 
 template <typename T>
 hipError_t launch_bwd(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st) {
+  if (g.f.D <= 32) return launch_bwd<T, 32>(g, w, st);
   if (g.f.D <= 64) return launch_bwd<T, 64>(g, w, st);
   return g.f.D <= 96 ? launch_bwd<T, 96>(g, w, st) : launch_bwd<T, 128>(g, w, st);
 }
 
-template <typename T, int DP, int W, bool KEYS>
+template <typename T, int DP, int W, int NP, bool KEYS>
 hipError_t prepare_pass() {
-  for (const void* f : {(const void*)grad_kernel<T, DP, W, KEYS, false>(), (const void*)grad_kernel<T, DP, W, KEYS, true>()}) {
+  for (const void* f : {(const void*)grad_kernel<T, DP, W, NP, KEYS, false>(), (const void*)grad_kernel<T, DP, W, NP, KEYS, true>()}) {
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kGradLds<DP, W, KEYS>);
     if (e != hipSuccess) return e;
   }
@@ -653,10 +664,13 @@ hipError_t prepare_pass() {
 }
 template <typename T>
 hipError_t prepare_bwd() {
-  for (hipError_t e : {prepare_pass<T, 64, 4, false>(), prepare_pass<T, 64, 8, false>(), prepare_pass<T, 64, 4, true>(),
-                       prepare_pass<T, 64, 8, true>(), prepare_pass<T, 96, 4, false>(), prepare_pass<T, 96, 8, false>(),
-                       prepare_pass<T, 96, 8, true>(), prepare_pass<T, 128, 4, false>(), prepare_pass<T, 128, 8, false>(),
-                       prepare_pass<T, 128, 8, true>()})
+  for (hipError_t e : {prepare_pass<T, 32, 4, 2, false>(), prepare_pass<T, 32, 8, 2, false>(), prepare_pass<T, 32, 4, 2, true>(),
+                       prepare_pass<T, 32, 8, 2, true>(), prepare_pass<T, 64, 4, 1, false>(), prepare_pass<T, 64, 8, 1, false>(),
+                       prepare_pass<T, 64, 8, 2, false>(), prepare_pass<T, 64, 4, 1, true>(), prepare_pass<T, 64, 8, 1, true>(),
+                       prepare_pass<T, 64, 8, 2, true>(), prepare_pass<T, 96, 4, 1, false>(), prepare_pass<T, 96, 8, 1, false>(),
+                       prepare_pass<T, 96, 8, 2, false>(), prepare_pass<T, 96, 8, 1, true>(), prepare_pass<T, 96, 8, 2, true>(),
+                       prepare_pass<T, 128, 4, 1, false>(), prepare_pass<T, 128, 8, 1, false>(), prepare_pass<T, 128, 8, 2, false>(),
+                       prepare_pass<T, 128, 8, 1, true>(), prepare_pass<T, 128, 8, 2, true>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
 }

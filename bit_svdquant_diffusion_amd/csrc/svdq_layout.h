@@ -388,6 +388,7 @@ struct AttnCost {
   int offset;                 // keys - queries where causal
   int causal, by_keys;        // by_keys: keys are held
   int block;                  // held rows of a workgroup
+  int fine;                   // probabilities and ds enter their products in two parts
 };
 // the tiles of block b: first and one past the last
 SVDQ_HD inline void attn_tiles(const AttnCost& c, int b, int* first, int* last) {
@@ -520,16 +521,28 @@ struct AttnSizes {
 inline int attn_waves(int64_t held, int64_t heads) {
   return held > kAttnWave && (held + 8 * kAttnWave - 1) / (8 * kAttnWave) * heads < kAttnCus ? 4 : 8;
 }
+// Probabilities (and ds) rounded once add about an output's own rounding to its
+// error, more where a sum has few terms or a head few elements to even that
+// out. With a second operand for what the rounding left they add nothing. That
+// is taken where the products are not what takes time: for heads up to 32
+// elements, whose fragments are half as many (2 x 4608 tokens, 12 heads of 32,
+// backward: 459 us, rounded once as heads of 64 500), and where a side fits
+// a tile.
+inline bool attn_fine(int64_t held, int64_t passing, int64_t D) {
+  return D <= 32 || held <= kAttnTile || passing <= kAttnTile;
+}
 inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
   const int64_t rows = s.Lq * (s.H / s.Hk);
+  const bool fine = attn_fine(rows, s.Lk, s.D);
   return AttnCost{(int)rows, (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0,
-                  kAttnWave * attn_waves(rows, s.B * s.Hk)};
+                  kAttnWave * (fine && s.D > 32 ? 8 : attn_waves(rows, s.B * s.Hk)), fine};
 }
 inline AttnCost attn_key_cost(const AttnSizes& s) {
   const int64_t rows = s.Lq * (s.H / s.Hk);
+  const bool fine = attn_fine(s.Lk, rows, s.D);
   // (with heads above 64 a workgroup of four waves of keys gains nothing: 2 x 1601 keys, heads of 72, 106 us against 93)
   return AttnCost{(int)s.Lk, (int)rows, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1,
-                  kAttnWave * (s.D > 64 ? 8 : attn_waves(s.Lk, s.B * s.Hk))};
+                  kAttnWave * (s.D > 64 || (fine && s.D > 32) ? 8 : attn_waves(s.Lk, s.B * s.Hk)), fine};
 }
 // (The forward's parts cost more to join than an uneven last round does: 288
 // units of 2 x 1531 causal queries 34 us whole, 38 in parts, their dq 57 and 47.)

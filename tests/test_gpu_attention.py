@@ -44,6 +44,11 @@ def _run(q, k, v, dout, mask, causal, scale=None, check=True):
 @pytest.mark.parametrize("B,Lq,Lk,H,Hk,D,dtype,causal,masked", [
     (1, 1, 1, 1, 1, 8, BF, False, False),
     (1, 1, 1, 1, 1, 128, HF, True, False),
+    (1, 1, 500, 6, 2, 32, BF, False, True),
+    (2, 90, 150, 4, 1, 24, HF, True, True),
+    (1, 310, 5, 9, 9, 16, BF, False, False),
+    (1, 2000, 300, 24, 24, 32, HF, True, False),     # whole units in workgroups of eight waves
+    (1, 40, 3000, 2, 2, 32, BF, True, False),
     (2, 1, 77, 4, 2, 64, BF, False, True),
     (1, 33, 31, 2, 1, 40, HF, False, False),
     (1, 64, 64, 2, 2, 64, BF, False, False),
@@ -142,6 +147,18 @@ def test_fp16_gradients_of_any_size(small):
     v = (v * 8).to(HF)
     dout = (dout * small).to(HF)
     _run(q, k, v, dout, None, False, scale=0.05)
+
+
+@pytest.mark.parametrize("D", [24, 64, 128])
+@pytest.mark.parametrize("at", range(0, 8, 2))
+def test_fp16_gradients_whose_largest_inputs_stand_anywhere(at, D):
+    """The scale of ds follows the largest |dout| and |v|, at whichever two of
+    eight elements these stand."""
+    q, k, v, dout = _inputs(2, 150, 200, 2, 1, D, HF, 14)
+    few = torch.zeros(D, dtype=torch.bool, device="cuda")
+    few[at::8] = few[at + 1::8] = True
+    v, dout = (torch.where(few, x * 64, x * 2.0 ** -10) for x in (v, dout))
+    _run(q, k, v, dout, _mask(2, 200, 5), True)
 
 
 def test_strides_and_orders():
