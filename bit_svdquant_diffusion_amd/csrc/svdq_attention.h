@@ -41,6 +41,14 @@ __device__ __forceinline__ AttnPiece piece_of(const AttnArgs& a, const AttnParts
   return attn_piece(a.cost, a.plan, deal.at[place]);
 }
 
+// Units are cut into parts where there are fewer than CUs, and then workgroups
+// have eight waves.
+template <int W, int KW>
+constexpr bool kAttnCut = W * KW == 8;
+inline hipError_t attn_shared_memory(const void* kernel, int bytes) {
+  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -22,18 +22,19 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// W waves of NB blocks of 32 query rows; DP the padded head. Two waves a SIMD
+// W waves of NB blocks of 32 query rows, KW times (each way takes every KW-th
+// tile); DP the padded head; NP operands for probabilities. Two waves a SIMD
 // (up to 256 registers), so that one's products run under the other's
 // exponentials: 4608 tokens, 24 heads of 128 with a mask 252 us (1.03
 // PFLOP/s), with one wave a SIMD 411, with one of two blocks 355, with
 // workgroups of four waves instead of eight 270.
-template <typename T, int DP, int W, int NB, int NP, bool PARTS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
+template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
+__global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   constexpr int NT = TL::kTransfers / W;   // transfers of a wave for one tile
-  extern __shared__ __align__(1024) uint8_t smem[];   // [2][K, V][kBytes]
+  extern __shared__ __align__(1024) uint8_t smem[];   // [KW][2][K, V][kBytes]
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w_id = __builtin_amdgcn_readfirstlane(tid >> 6), wave = KW == 1 ? w_id : w_id % W, way = KW == 1 ? 0 : w_id / W;
   const int G = a.G, R = a.Lq * G, D = a.D;
   const typename TL::Lane pl(lane);
   // transfers
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP <= 64
       qf[n][s] = r < R && d < D ? *reinterpret_cast<const u32x4*>(row + d) : u32x4{0, 0, 0, 0};
     }
   }
-  const int k_begin = at.first * kAttnRows, tiles = at.last - at.first;
+  const int k_begin = (at.first + way) * kAttnRows, k_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   // what every and what any row of this wave sees
   const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
   const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP <= 64
     const int rows = min(kAttnRows, a.Lk - k0);
     const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
     const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
-    uint8_t *tk = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
+    uint8_t *tk = smem + (way * 2 + stage) * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
     // (a key that the mask drops is not read: whatever stands there, it is zero)
     if (keep == ~0ull) {
 #pragma unroll
@@ -112,21 +113,22 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP <= 64
   }
   uint64_t now, keep = 0;   // which keys of the tile, and of the next, take part
   int next_byte = 0;
-  if (tiles > 0) {
+  constexpr int kStep = KW * kAttnRows;
+  if (k_begin < k_end) {
     keep = __ballot(mask_byte(k_begin) != 0);
     fetch(k_begin, 0, keep);
-    next_byte = mask_byte(k_begin + kAttnRows);
+    next_byte = mask_byte(k_begin + kStep);
   }
-  for (int t = 0, k0 = k_begin; t < tiles; ++t, k0 += kAttnRows) {
+  for (int t = 0, k0 = k_begin; t < rounds; ++t, k0 += kStep) {
     now = keep;
     tile_barrier();
-    if (t + 1 < tiles) {
+    if (k0 + kStep < k_end) {
       keep = __ballot(next_byte != 0);
-      fetch(k0 + kAttnRows, (t + 1) & 1, keep);
-      next_byte = mask_byte(k0 + 2 * kAttnRows);
+      fetch(k0 + kStep, (t + 1) & 1, keep);
+      next_byte = mask_byte(k0 + 2 * kStep);
     }
-    const uint8_t *tk = smem + (t & 1) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
-    if (k0 > w_last || now == 0) continue;   // nothing that this wave's rows see
+    const uint8_t *tk = smem + (way * 2 + (t & 1)) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
+    if (k0 > w_last || now == 0 || (KW > 1 && k0 >= k_end)) continue;   // nothing that this wave's rows see
     f32x16 s[2][NB];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -200,6 +202,34 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP <= 64
           for (int w = 0; w < NP; ++w) o[i][n] = mma<T>(vf, p[kt][n][w], o[i][n]);
       }
     sched_products<4 * TL::kBlocks * NB * NP, 8 * TL::kBlocks, 2, 8>();
+  }
+  if constexpr (KW > 1) {   // the second way's results join the first's
+    f32x4* box = reinterpret_cast<f32x4*>(smem) + wave * (4 * TL::kBlocks * 64) + lane;
+    f32x2* stat = reinterpret_cast<f32x2*>(smem + W * TL::kBlocks * 4096) + wave * 64 + lane;
+    tile_barrier();
+    if (way == 1) {
+#pragma unroll
+      for (int i = 0; i < TL::kBlocks; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          box[(4 * i + q) * 64] = f32x4{o[i][0][4 * q], o[i][0][4 * q + 1], o[i][0][4 * q + 2], o[i][0][4 * q + 3]};
+      *stat = f32x2{m[0], l[0]};
+    }
+    tile_barrier();
+    if (way == 1) return;
+    const f32x2 other = *stat;
+    const float top = __builtin_fmaxf(m[0], other[0]), base = top == -__builtin_inff() ? 0.f : top;
+    const float f = __builtin_amdgcn_exp2f(m[0] - base), fo = __builtin_amdgcn_exp2f(other[0] - base);
+    m[0] = top;
+    l[0] = l[0] * f + other[1] * fo;
+#pragma unroll
+    for (int i = 0; i < TL::kBlocks; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = box[(4 * i + q) * 64];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][0][4 * q + k] = o[i][0][4 * q + k] * f + v[k] * fo;
+      }
   }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -293,40 +323,43 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins jo
         u32x2{cvt_x2<T>(o[0], o[1]), cvt_x2<T>(o[2], o[3])};
 }
 
-template <int DP>
-constexpr int kFwdLds = 4 * AttnTile<DP>::kBytes;
+template <int DP, int KW>
+constexpr int kFwdLds = 4 * KW * AttnTile<DP>::kBytes;
 
-template <typename T, int DP, int W, int NP>
+template <typename T, int DP, int W, int KW, int NP>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.plan.grid), block(64 * W);
-  if (!a.plan.each) {
-    hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, NP, false>), grid, block, kFwdLds<DP>, st, a, AttnUnits{});
-    return hipGetLastError();
-  }
-  AttnParts deal;
-  attn_parts(a.cost, a.plan, &deal);
-  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, 1, NP, true>), grid, block, kFwdLds<DP>, st, a, deal);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  AttnJoins joins;
-  const int units = attn_joins(a.plan, deal, &joins);
-  // with many parts a row, all of a workgroup for one
-  const bool deep = a.plan.grid >= 12 * units;
-  const dim3 rows((unsigned)units, (unsigned)(deep ? a.part_rows : (a.part_rows + 7) / 8));
-  if (deep)
-    hipLaunchKernelGGL((attn_join_kernel<T, 8>), rows, dim3(256), 0, st, a, joins);
-  else
-    hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, joins);
+  const dim3 grid((unsigned)a.plan.grid), block(64 * W * KW);
+  if constexpr (kAttnCut<W, KW>)
+    if (a.plan.each) {
+      AttnParts deal;
+      attn_parts(a.cost, a.plan, &deal);
+      hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, KW, 1, NP, true>), grid, block, (kFwdLds<DP, KW>), st, a, deal);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      AttnJoins joins;
+      const int units = attn_joins(a.plan, deal, &joins);
+      // with many parts a row, all of a workgroup for one
+      const bool deep = a.plan.grid >= 12 * units;
+      const dim3 rows((unsigned)units, (unsigned)(deep ? a.part_rows : (a.part_rows + 7) / 8));
+      if (deep)
+        hipLaunchKernelGGL((attn_join_kernel<T, 8>), rows, dim3(256), 0, st, a, joins);
+      else
+        hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, joins);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, KW, 1, NP, false>), grid, block, (kFwdLds<DP, KW>), st, a, AttnUnits{});
   return hipGetLastError();
 }
 template <typename T, int DP>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
   const bool wide = a.cost.block == 8 * kAttnWave;
   if constexpr (DP == 32) {
-    return wide ? launch_fwd<T, DP, 8, 2>(a, st) : launch_fwd<T, DP, 4, 2>(a, st);
+    if (a.cost.ways == 2) return launch_fwd<T, DP, 4, 2, 2>(a, st);
+    return wide ? launch_fwd<T, DP, 8, 1, 2>(a, st) : launch_fwd<T, DP, 4, 1, 2>(a, st);
   } else {
-    if (a.cost.fine) return launch_fwd<T, DP, 8, 2>(a, st);
-    return wide ? launch_fwd<T, DP, 8, 1>(a, st) : launch_fwd<T, DP, 4, 1>(a, st);
+    if (a.cost.fine) return launch_fwd<T, DP, 8, 1, 2>(a, st);
+    if (a.cost.ways == 2) return launch_fwd<T, DP, 4, 2, 1>(a, st);
+    return wide ? launch_fwd<T, DP, 8, 1, 1>(a, st) : launch_fwd<T, DP, 4, 1, 1>(a, st);
   }
 }
 template <typename T>
@@ -336,19 +369,24 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
   return a.D <= 96 ? launch_fwd<T, 96>(a, st) : launch_fwd<T, 128>(a, st);
 }
 
-template <typename T, int DP, int W, int NP>
+template <typename T, int DP, int W, int KW, int NP>
 hipError_t prepare_fwd() {
-  for (const void* f : {(const void*)attn_fwd_kernel<T, DP, W, 1, NP, false>, (const void*)attn_fwd_kernel<T, DP, W, 1, NP, true>}) {
-    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds<DP>);
+  hipError_t e = attn_shared_memory((const void*)attn_fwd_kernel<T, DP, W, KW, 1, NP, false>, kFwdLds<DP, KW>);
+  if constexpr (kAttnCut<W, KW>)
+    if (e == hipSuccess) e = attn_shared_memory((const void*)attn_fwd_kernel<T, DP, W, KW, 1, NP, true>, kFwdLds<DP, KW>);
+  return e;
+}
+template <typename T, int DP>
+hipError_t prepare_fwd_of() {
+  for (hipError_t e : {prepare_fwd<T, DP, 4, 1, 1>(), prepare_fwd<T, DP, 4, 2, 1>(), prepare_fwd<T, DP, 8, 1, 1>(),
+                       prepare_fwd<T, DP, 8, 1, 2>()})
     if (e != hipSuccess) return e;
-  }
   return hipSuccess;
 }
 template <typename T>
 hipError_t prepare_fwd() {
-  for (hipError_t e : {prepare_fwd<T, 32, 4, 2>(), prepare_fwd<T, 32, 8, 2>(), prepare_fwd<T, 64, 4, 1>(), prepare_fwd<T, 64, 8, 1>(),
-                       prepare_fwd<T, 64, 8, 2>(), prepare_fwd<T, 96, 4, 1>(), prepare_fwd<T, 96, 8, 1>(), prepare_fwd<T, 96, 8, 2>(),
-                       prepare_fwd<T, 128, 4, 1>(), prepare_fwd<T, 128, 8, 1>(), prepare_fwd<T, 128, 8, 2>()})
+  for (hipError_t e : {prepare_fwd<T, 32, 4, 1, 2>(), prepare_fwd<T, 32, 4, 2, 2>(), prepare_fwd<T, 32, 8, 1, 2>(),
+                       prepare_fwd_of<T, 64>(), prepare_fwd_of<T, 96>(), prepare_fwd_of<T, 128>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
 }

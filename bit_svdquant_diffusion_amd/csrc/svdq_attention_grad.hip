@@ -99,22 +99,51 @@ __device__ __forceinline__ float ds_scale(int D, float x, float y) {
   return exp2_int(min(15 - e, 100));
 }
 
+// The second way's results join the first's through LDS, I-th of a wave's sums.
+template <int DP, int W, int I, int NB>
+__device__ __forceinline__ f32x4* join_place(uint8_t* smem, int wave, int lane) {
+  static_assert(NB == 1, "");
+  return reinterpret_cast<f32x4*>(smem) + (I * W + wave) * (AttnTile<DP>::kBlocks * 256) + lane;
+}
+template <int DP, int W, int I, int NB>
+__device__ __forceinline__ void join_put(uint8_t* smem, int wave, int lane, const f32x16 (&v)[AttnTile<DP>::kBlocks][NB]) {
+  f32x4* to = join_place<DP, W, I, NB>(smem, wave, lane);
+#pragma unroll
+  for (int i = 0; i < AttnTile<DP>::kBlocks; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      to[(4 * i + q) * 64] = f32x4{v[i][0][4 * q], v[i][0][4 * q + 1], v[i][0][4 * q + 2], v[i][0][4 * q + 3]};
+}
+template <int DP, int W, int I, int NB>
+__device__ __forceinline__ void join_add(uint8_t* smem, int wave, int lane, f32x16 (&v)[AttnTile<DP>::kBlocks][NB]) {
+  const f32x4* from = join_place<DP, W, I, NB>(smem, wave, lane);
+#pragma unroll
+  for (int i = 0; i < AttnTile<DP>::kBlocks; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 x = from[(4 * i + q) * 64];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i][0][4 * q + k] += x[k];
+    }
+}
+
 // dk and dv of 32 NB keys a wave; the query rows pass by. With heads of 128
 // the accumulators and the K fragments take 160 of the 256 registers that two
 // waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads: 574
 // us against 760 with V in registers, of which 53 spill, 768 with one wave a
 // SIMD and two blocks of keys, 870 with workgroups of four waves).
-template <typename T, int DP, int W, int NB, int NP, bool PARTS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
+template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
+__global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
-  extern __shared__ __align__(1024) uint8_t smem[];   // [2][q, do][kBytes], then V where it is held there
+  static_assert(KW == 1 || DP < 128, "V is held for each way");
+  extern __shared__ __align__(1024) uint8_t smem[];   // [KW][2][q, do][kBytes], then V where it is held there
   constexpr bool kHoldV = DP < 128;   // in registers, else in LDS
   uint8_t* held = smem + 4 * TL::kBytes;
-  __shared__ __align__(1024) float stats[2][2][kAttnRows];   // -lse / scale and -delta of a tile's rows
+  __shared__ __align__(1024) float stats[KW][2][2][kAttnRows];   // -lse / scale and -delta of a tile's rows
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w_id = __builtin_amdgcn_readfirstlane(tid >> 6), wave = KW == 1 ? w_id : w_id % W, way = KW == 1 ? 0 : w_id / W;
   const int G = a.G, R = a.Lq * G, D = a.D;
   const typename TL::Lane pl(lane);
   const int place = attn_place(a.plan, blockIdx.x);
@@ -169,7 +198,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
     }
     dead = min(max(k - (a.Lk - a.Lq), 0), a.Lq) * G;
   }
-  const int r_begin = at.first * kAttnRows, tiles = at.last - at.first;
+  const int r_begin = (at.first + way) * kAttnRows, r_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   const int w_first = a.causal ? max(key0 - (a.Lk - a.Lq), 0) * G : 0;
   const int w_all = a.causal ? max(key0 + 32 * NB - 1 - (a.Lk - a.Lq), 0) * G : 0;   // from here on rows see all of the wave's keys
 
@@ -178,7 +207,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
     // the heads of the queries i0 .. i1
     const auto rq = rows_resource(qp + i0 * a.q.token, (int)((i1 - i0) * a.q.token + (G - 1) * a.q.head + D) * 2);
     const auto rd = rows_resource(dop + i0 * g.dout.token, (int)((i1 - i0) * g.dout.token + (G - 1) * g.dout.head + D) * 2);
-    uint8_t *tq = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *td = tq + TL::kBytes;
+    uint8_t *tq = smem + (way * 2 + stage) * 2 * TL::kBytes + wave * NT * 1024, *td = tq + TL::kBytes;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j = wave * NT + n, ch = TL::chunk_of(j, lane), r = row0 + TL::row_of(j, lane);
@@ -189,7 +218,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
     }
     if (wave < 2) {   // (rows up to whole tiles are there)
       const auto rs = rows_resource((wave == 0 ? lse : delta) + row0, kAttnRows * 4);
-      lds_transfer_4(rs, reinterpret_cast<uint8_t*>(stats[stage][wave]), lane * 4);
+      lds_transfer_4(rs, reinterpret_cast<uint8_t*>(stats[way][stage][wave]), lane * 4);
     }
   };
 
@@ -198,12 +227,14 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
   for (int i = 0; i < TL::kBlocks; ++i)
 #pragma unroll
     for (int n = 0; n < NB; ++n) dk[i][n] = dv[i][n] = f32x16{};
-  if (tiles > 0) fetch(r_begin, 0);
-  for (int t = 0, row0 = r_begin; t < tiles; ++t, row0 += kAttnRows) {
+  constexpr int kStep = KW * kAttnRows;
+  if (r_begin < r_end) fetch(r_begin, 0);
+  for (int t = 0, row0 = r_begin; t < rounds; ++t, row0 += kStep) {
     tile_barrier();
-    if (t + 1 < tiles) fetch(row0 + kAttnRows, (t + 1) & 1);
-    const uint8_t *tq = smem + (t & 1) * 2 * TL::kBytes, *td = tq + TL::kBytes;
-    const float *tl = stats[t & 1][0], *tD = stats[t & 1][1];
+    if (row0 + kStep < r_end) fetch(row0 + kStep, (t + 1) & 1);
+    if (KW > 1 && row0 >= r_end) continue;
+    const uint8_t *tq = smem + (way * 2 + (t & 1)) * 2 * TL::kBytes, *td = tq + TL::kBytes;
+    const float *tl = stats[way][t & 1][0], *tD = stats[way][t & 1][1];
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) {
       if (row0 + 32 * rb + 31 < w_first) continue;   // none of these rows sees a key of this wave
@@ -291,6 +322,18 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
       sched_products<2 * TL::kBlocks * NB * NP, 4 * TL::kBlocks, 2, 4>();
     }
   }
+  if constexpr (KW > 1) {
+    const bool second = way == 1;
+    tile_barrier();
+    if (second) {
+      join_put<DP, W, 0>(smem, wave, lane, dk);
+      join_put<DP, W, 1>(smem, wave, lane, dv);
+    }
+    tile_barrier();
+    if (second) return;
+    join_add<DP, W, 0>(smem, wave, lane, dk);
+    join_add<DP, W, 1>(smem, wave, lane, dv);
+  }
   const float fv = kScaled<T> ? 1.f / kProbScale : 1.f;
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -335,15 +378,15 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
 
 // dq of 32 NB query rows a wave; the keys pass by, as in the forward (4608
 // tokens, 24 heads of 128: 345 us, 1.13 PFLOP/s).
-template <typename T, int DP, int W, int NB, int NP, bool PARTS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
+template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
+__global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
   constexpr int NT = TL::kTransfers / W;
-  extern __shared__ __align__(1024) uint8_t smem[];   // [2][K, V][kBytes]
+  extern __shared__ __align__(1024) uint8_t smem[];   // [KW][2][K, V][kBytes]
   __shared__ float tops[W];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, lr = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w_id = __builtin_amdgcn_readfirstlane(tid >> 6), wave = KW == 1 ? w_id : w_id % W, way = KW == 1 ? 0 : w_id / W;
   const int G = a.G, R = a.Lq * G, D = a.D;
   const typename TL::Lane pl(lane);
   uint32_t vk[NT], vv[NT];
@@ -394,7 +437,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
     lse[n] = none ? l : -l / a.scale;
     sum = sum_halves(sum);
     delta[n] = none ? 0.f : -sum;
-    if (at.starts) {   // for the keys' gradients, which start with them
+    if (at.starts && way == 0) {   // for the keys' gradients, which start with them
       if (h == 0) g.lse[at.hb * Rp + r] = lse[n];
       if (h == 1) g.delta[at.hb * Rp + r] = delta[n];
     }
@@ -407,10 +450,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
       c[n] = 1.f;
     }
   }
-  if (kScaled<T> && at.starts) {
+  if (kScaled<T> && at.starts) {   // (all waves)
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) wg_top = __builtin_fmaxf(wg_top, __shfl_xor(wg_top, d));
-    if (lane == 0) tops[wave] = wg_top;
+    if (lane == 0 && way == 0) tops[wave] = wg_top;
     __syncthreads();
     if (tid == 0) {
 #pragma unroll
@@ -418,7 +461,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
       g.top_do[at.hb * g.row_blocks + at.block] = wg_top;
     }
   }
-  const int k_begin = at.first * kAttnRows, tiles = at.last - at.first;
+  const int k_begin = (at.first + way) * kAttnRows, k_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
   const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
 
@@ -426,7 +469,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
     const int rows = min(kAttnRows, a.Lk - k0);
     const auto rk = rows_resource(kp + k0 * a.k.token, (int)((rows - 1) * a.k.token + D) * 2);
     const auto rv = rows_resource(vp + k0 * a.v.token, (int)((rows - 1) * a.v.token + D) * 2);
-    uint8_t *tk = smem + stage * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
+    uint8_t *tk = smem + (way * 2 + stage) * 2 * TL::kBytes + wave * NT * 1024, *tv = tk + TL::kBytes;
     if (keep == ~0ull) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -454,21 +497,22 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
     for (int n = 0; n < NB; ++n) dq[i][n] = f32x16{};
   uint64_t keep = 0, next_keep = 0;
   int next_byte = 0;
-  if (tiles > 0) {
+  constexpr int kStep = KW * kAttnRows;
+  if (k_begin < k_end) {
     next_keep = __ballot(mask_byte(k_begin) != 0);
     fetch(k_begin, 0, next_keep);
-    next_byte = mask_byte(k_begin + kAttnRows);
+    next_byte = mask_byte(k_begin + kStep);
   }
-  for (int t = 0, k0 = k_begin; t < tiles; ++t, k0 += kAttnRows) {
+  for (int t = 0, k0 = k_begin; t < rounds; ++t, k0 += kStep) {
     keep = next_keep;
     tile_barrier();
-    if (t + 1 < tiles) {
+    if (k0 + kStep < k_end) {
       next_keep = __ballot(next_byte != 0);
-      fetch(k0 + kAttnRows, (t + 1) & 1, next_keep);
-      next_byte = mask_byte(k0 + 2 * kAttnRows);
+      fetch(k0 + kStep, (t + 1) & 1, next_keep);
+      next_byte = mask_byte(k0 + 2 * kStep);
     }
-    if (k0 > w_last || keep == 0) continue;
-    const uint8_t *tk = smem + (t & 1) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
+    if (k0 > w_last || keep == 0 || (KW > 1 && k0 >= k_end)) continue;
+    const uint8_t *tk = smem + (way * 2 + (t & 1)) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
     const bool part = keep != ~0ull || k0 + kAttnRows - 1 > w_first;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -524,6 +568,14 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 32
         }
       sched_products<2 * TL::kBlocks * NB * NP, 4 * TL::kBlocks, 2, 8>();
     }
+  }
+  if constexpr (KW > 1) {
+    const bool second = way == 1;
+    tile_barrier();
+    if (second) join_put<DP, W, 0>(smem, wave, lane, dq);
+    tile_barrier();
+    if (second) return;
+    join_add<DP, W, 0>(smem, wave, lane, dq);
   }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -590,46 +642,49 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, Att
   }
 }
 
-template <typename T, int DP, int W, int NP, bool KEYS, bool PARTS>
+template <typename T, int DP, int W, int KW, int NP, bool KEYS, bool PARTS>
 constexpr auto grad_kernel() {
   if constexpr (KEYS)
-    return attn_dkv_kernel<T, DP, W, 1, NP, PARTS>;
+    return attn_dkv_kernel<T, DP, W, KW, 1, NP, PARTS>;
   else
-    return attn_dq_kernel<T, DP, W, 1, NP, PARTS>;
+    return attn_dq_kernel<T, DP, W, KW, 1, NP, PARTS>;
 }
-template <int DP, int W, bool KEYS>
-constexpr int kGradLds = 4 * AttnTile<DP>::kBytes + (KEYS && DP == 128 ? W * kAttnWave * AttnTile<DP>::kRowBytes : 0);
+template <int DP, int W, int KW, bool KEYS>
+constexpr int kGradLds = 4 * KW * AttnTile<DP>::kBytes + (KEYS && DP == 128 ? W * kAttnWave * AttnTile<DP>::kRowBytes : 0);
 
-template <typename T, int DP, int W, int NP, bool KEYS>
+template <typename T, int DP, int W, int KW, int NP, bool KEYS>
 hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
   if (plan.grid == 0) return hipSuccess;
   g.f.cost = cost;
   g.f.plan = plan;
   g.f.part_rows = (int)attn_part_rows(cost);
-  const dim3 grid((unsigned)plan.grid), block(64 * W);
-  if (!plan.each) {
-    hipLaunchKernelGGL((grad_kernel<T, DP, W, NP, KEYS, false>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, AttnUnits{});
-    return hipGetLastError();
-  }
-  AttnParts deal;
-  attn_parts(cost, plan, &deal);
-  hipLaunchKernelGGL((grad_kernel<T, DP, W, NP, KEYS, true>()), grid, block, (kGradLds<DP, W, KEYS>), st, g, deal);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  AttnJoins joins;
-  const dim3 rows((unsigned)attn_joins(plan, deal, &joins), (unsigned)((g.f.part_rows + 7) / 8));
-  hipLaunchKernelGGL((attn_grad_join_kernel<T, KEYS>), rows, dim3(256), 0, st, g, joins);
+  const dim3 grid((unsigned)plan.grid), block(64 * W * KW);
+  if constexpr (kAttnCut<W, KW>)
+    if (plan.each) {
+      AttnParts deal;
+      attn_parts(cost, plan, &deal);
+      hipLaunchKernelGGL((grad_kernel<T, DP, W, KW, NP, KEYS, true>()), grid, block, (kGradLds<DP, W, KW, KEYS>), st, g, deal);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      AttnJoins joins;
+      const dim3 rows((unsigned)attn_joins(plan, deal, &joins), (unsigned)((g.f.part_rows + 7) / 8));
+      hipLaunchKernelGGL((attn_grad_join_kernel<T, KEYS>), rows, dim3(256), 0, st, g, joins);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((grad_kernel<T, DP, W, KW, NP, KEYS, false>()), grid, block, (kGradLds<DP, W, KW, KEYS>), st, g, AttnUnits{});
   return hipGetLastError();
 }
 // (heads above 64: a workgroup of keys has eight waves, see attn_key_cost)
 template <typename T, int DP, bool KEYS>
 hipError_t launch_pass(const AttnGradArgs& g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
   constexpr int NP = DP == 32 ? 2 : 1;
-  if constexpr (!KEYS || DP <= 64)
-    if (cost.block == 4 * kAttnWave) return launch_pass<T, DP, 4, NP, KEYS>(g, cost, plan, st);
   if constexpr (DP > 32)
-    if (cost.fine) return launch_pass<T, DP, 8, 2, KEYS>(g, cost, plan, st);
-  return launch_pass<T, DP, 8, NP, KEYS>(g, cost, plan, st);
+    if (cost.fine) return launch_pass<T, DP, 8, 1, 2, KEYS>(g, cost, plan, st);
+  if constexpr (!KEYS || DP < 128)
+    if (cost.ways == 2) return launch_pass<T, DP, 4, 2, NP, KEYS>(g, cost, plan, st);
+  if constexpr (!KEYS || DP <= 64)
+    if (cost.block == 4 * kAttnWave) return launch_pass<T, DP, 4, 1, NP, KEYS>(g, cost, plan, st);
+  return launch_pass<T, DP, 8, 1, NP, KEYS>(g, cost, plan, st);
 }
 
 template <typename T, int DP>
@@ -654,23 +709,30 @@ hipError_t launch_bwd(const AttnGradArgs& g, const AttnGradWs& w, hipStream_t st
   return g.f.D <= 96 ? launch_bwd<T, 96>(g, w, st) : launch_bwd<T, 128>(g, w, st);
 }
 
-template <typename T, int DP, int W, int NP, bool KEYS>
+template <typename T, int DP, int W, int KW, int NP, bool KEYS>
 hipError_t prepare_pass() {
-  for (const void* f : {(const void*)grad_kernel<T, DP, W, NP, KEYS, false>(), (const void*)grad_kernel<T, DP, W, NP, KEYS, true>()}) {
-    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kGradLds<DP, W, KEYS>);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  constexpr int lds = kGradLds<DP, W, KW, KEYS>;
+  hipError_t e = attn_shared_memory((const void*)grad_kernel<T, DP, W, KW, NP, KEYS, false>(), lds);
+  if constexpr (kAttnCut<W, KW>)
+    if (e == hipSuccess) e = attn_shared_memory((const void*)grad_kernel<T, DP, W, KW, NP, KEYS, true>(), lds);
+  return e;
+}
+template <typename T, int DP, bool KEYS>
+hipError_t prepare_of() {
+  constexpr int NP = DP == 32 ? 2 : 1;
+  hipError_t e = prepare_pass<T, DP, 8, 1, NP, KEYS>();
+  if constexpr (!KEYS || DP <= 64)
+    if (e == hipSuccess) e = prepare_pass<T, DP, 4, 1, NP, KEYS>();
+  if constexpr (!KEYS || DP < 128)
+    if (e == hipSuccess) e = prepare_pass<T, DP, 4, 2, NP, KEYS>();
+  if constexpr (DP > 32)
+    if (e == hipSuccess) e = prepare_pass<T, DP, 8, 1, 2, KEYS>();
+  return e;
 }
 template <typename T>
 hipError_t prepare_bwd() {
-  for (hipError_t e : {prepare_pass<T, 32, 4, 2, false>(), prepare_pass<T, 32, 8, 2, false>(), prepare_pass<T, 32, 4, 2, true>(),
-                       prepare_pass<T, 32, 8, 2, true>(), prepare_pass<T, 64, 4, 1, false>(), prepare_pass<T, 64, 8, 1, false>(),
-                       prepare_pass<T, 64, 8, 2, false>(), prepare_pass<T, 64, 4, 1, true>(), prepare_pass<T, 64, 8, 1, true>(),
-                       prepare_pass<T, 64, 8, 2, true>(), prepare_pass<T, 96, 4, 1, false>(), prepare_pass<T, 96, 8, 1, false>(),
-                       prepare_pass<T, 96, 8, 2, false>(), prepare_pass<T, 96, 8, 1, true>(), prepare_pass<T, 96, 8, 2, true>(),
-                       prepare_pass<T, 128, 4, 1, false>(), prepare_pass<T, 128, 8, 1, false>(), prepare_pass<T, 128, 8, 2, false>(),
-                       prepare_pass<T, 128, 8, 1, true>(), prepare_pass<T, 128, 8, 2, true>()})
+  for (hipError_t e : {prepare_of<T, 32, false>(), prepare_of<T, 64, false>(), prepare_of<T, 96, false>(), prepare_of<T, 128, false>(),
+                       prepare_of<T, 32, true>(), prepare_of<T, 64, true>(), prepare_of<T, 96, true>(), prepare_of<T, 128, true>()})
     if (e != hipSuccess) return e;
   return hipSuccess;
 }

@@ -376,19 +376,20 @@ inline size_t residual_grad_ws(int64_t M, int64_t groups, int64_t rows_per_group
 // Attention: the held rows (keys, for their gradients) of a key head lie in
 // blocks of kAttnWave a wave, four or eight waves; the other side passes by in
 // tiles of kAttnTile. A unit is a block's walk along its tiles, and a
-// workgroup's work, unless there are fewer units than `below`: then units are
-// cut into parts of about as many tiles as let all parts run at once, `slots`
-// workgroups, and another kernel joins their results. (More units than slots
-// even out badly, too, 432 units in two rounds of 256, but there power bounds
-// the products: with half of the CUs busy each is a third faster. Workspaces'
-// sizes are asked for without a device, so the plan is this card's.)
-constexpr int kAttnCus = 256, kAttnSlots = 2 * kAttnCus, kAttnTile = 64, kAttnWave = 32, kAttnKeyRun = 64;
+// workgroup's work, unless there are fewer units than CUs: then units are cut
+// into parts of about as many tiles as let all parts run at once, and another
+// kernel joins their results. (More units than CUs even out badly, too, 432
+// units in two rounds of 256, but there power bounds the products: with half
+// of the CUs busy each is a third faster. Workspaces' sizes are asked for
+// without a device, so the plan is this card's.)
+constexpr int kAttnCus = 256, kAttnTile = 64, kAttnWave = 32, kAttnKeyRun = 64;
 struct AttnCost {
   int held, passing, group;   // rows (queries times the group, or keys) and the group's heads
   int offset;                 // keys - queries where causal
   int causal, by_keys;        // by_keys: keys are held
   int block;                  // held rows of a workgroup
   int fine;                   // probabilities and ds enter their products in two parts
+  int ways;                   // of a workgroup: every so many-th tile
 };
 // the tiles of block b: first and one past the last
 SVDQ_HD inline void attn_tiles(const AttnCost& c, int b, int* first, int* last) {
@@ -416,13 +417,13 @@ struct AttnPlan {
 };
 // parts of a unit of `cost` tiles (one without tiles still writes its zeros)
 inline int attn_parts_of(int cost, int each) { return cost > each ? (cost + each - 1) / each : 1; }
-inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, int slots, int below) {
+inline AttnPlan attn_plan(const AttnCost& c, int64_t heads) {
   AttnPlan p;
   p.blocks = (int)(((int64_t)c.held + c.block - 1) / c.block);
   p.heads = (int)heads;
   p.grid = (int)(p.blocks * heads);
   p.each = 0;
-  if (p.grid == 0 || p.grid >= below) return p;
+  if (p.grid == 0 || p.grid >= kAttnCus) return p;
   int64_t total = 0;
   int most = 0;
   for (int b = 0; b < p.blocks; ++b) {
@@ -431,11 +432,11 @@ inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, int slots, int below
     most = n > most ? n : most;
   }
   // the smallest parts, of four tiles at least, that run at once
-  int64_t each = total * heads / slots;
+  int64_t each = total * heads / kAttnCus;
   for (each = each < 4 ? 4 : each; each < most; each += (each + 15) / 16) {
     int64_t parts = 0;
     for (int b = 0; b < p.blocks; ++b) parts += attn_parts_of(attn_cost(c, b), (int)each);
-    if (parts * heads <= slots) {
+    if (parts * heads <= kAttnCus) {
       p.grid = (int)(parts * heads);
       p.each = (int)each;
       return p;
@@ -449,11 +450,11 @@ struct AttnPart {
   uint32_t unit : 10, part : 11, parts : 11;
 };
 struct AttnParts {
-  AttnPart at[kAttnSlots];
+  AttnPart at[kAttnCus];
 };
 inline void attn_parts(const AttnCost& c, const AttnPlan& p, AttnParts* s) {
   int n = 0;
-  for (int u = 0; u < p.blocks * p.heads; ++u) {   // (fewer than the slots, 512 at most, and no more parts)
+  for (int u = 0; u < p.blocks * p.heads; ++u) {   // (fewer than CUs, and no more parts)
     const int parts = attn_parts_of(attn_cost(c, u % p.blocks), p.each);
     for (int i = 0; i < parts; ++i) s->at[n++] = AttnPart{(uint32_t)u, (uint32_t)i, (uint32_t)parts};
   }
@@ -464,7 +465,7 @@ struct AttnJoin {
   uint32_t unit : 10, first : 11, parts : 11;
 };
 struct AttnJoins {
-  AttnJoin at[kAttnSlots];
+  AttnJoin at[kAttnCus];
 };
 inline int attn_joins(const AttnPlan& p, const AttnParts& s, AttnJoins* j) {
   int n = 0;
@@ -513,9 +514,9 @@ struct AttnSizes {
   int64_t B, Lq, Lk, H, Hk, D;
   bool causal, scaled;   // scaled: fp16
 };
-// Waves of a workgroup: eight where there is such a block for every CU, since
-// they share a tile (4608 tokens, 24 heads of 128: 250 us against 269 with
-// four), else four, two workgroups a CU (2 x 1531 causal queries: 37 us against
+// Waves that hold rows of their own: eight where there is such a block for
+// every CU, since they share a tile (4608 tokens, 24 heads of 128: 250 us
+// against 269 with four), else four (2 x 1531 causal queries: 37 us against
 // 48); eight again where a wave holds all rows and the tiles' stream is what
 // takes time (one query over 65536 keys: 65 against 68).
 inline int attn_waves(int64_t held, int64_t heads) {
@@ -531,24 +532,34 @@ inline int attn_waves(int64_t held, int64_t heads) {
 inline bool attn_fine(int64_t held, int64_t passing, int64_t D) {
   return D <= 32 || held <= kAttnTile || passing <= kAttnTile;
 }
+// Four waves leave a CU half empty unless it gets two such workgroups. With two
+// ways a workgroup has four more waves for the same rows, which take every
+// other tile, and the ways' results meet in LDS. Where blocks take different
+// times, or no CU would get a second one, that is faster: 2 x 1531 causal
+// queries over as many keys, 12 heads of 72, 28 us against 34, 2 x 2048 causal,
+// 12 heads of 128, 52 against 60, backward 2 x 4096 queries over 77 keys 59
+// against 61; with 384 even blocks (2 x 1500, 16 heads of 128) 57 against 52.
+inline int attn_ways(int64_t held, int64_t heads, bool causal) {
+  return causal || (held + 4 * kAttnWave - 1) / (4 * kAttnWave) * heads <= kAttnCus ? 2 : 1;
+}
 inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
   const int64_t rows = s.Lq * (s.H / s.Hk);
   const bool fine = attn_fine(rows, s.Lk, s.D);
+  const int waves = fine && s.D > 32 ? 8 : attn_waves(rows, s.B * s.Hk);
   return AttnCost{(int)rows, (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0,
-                  kAttnWave * (fine && s.D > 32 ? 8 : attn_waves(rows, s.B * s.Hk)), fine};
+                  kAttnWave * waves, fine, waves == 4 ? attn_ways(rows, s.B * s.Hk, s.causal) : 1};
 }
 inline AttnCost attn_key_cost(const AttnSizes& s) {
   const int64_t rows = s.Lq * (s.H / s.Hk);
   const bool fine = attn_fine(s.Lk, rows, s.D);
-  // (with heads above 64 a workgroup of four waves of keys gains nothing: 2 x 1601 keys, heads of 72, 106 us against 93)
+  // (V's fragments of heads above 96 leave no room in LDS for a second way;
+  // with heads above 64 four waves alone gain nothing: 2 x 1601 keys, heads of
+  // 72, 106 us against 93)
+  int waves = (fine && s.D > 32) || s.D > 96 ? 8 : attn_waves(s.Lk, s.B * s.Hk);
+  const int ways = waves == 4 ? attn_ways(s.Lk, s.B * s.Hk, s.causal) : 1;
+  if (s.D > 64 && ways == 1) waves = 8;
   return AttnCost{(int)s.Lk, (int)rows, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1,
-                  kAttnWave * (s.D > 64 || (fine && s.D > 32) ? 8 : attn_waves(s.Lk, s.B * s.Hk)), fine};
-}
-// (The forward's parts cost more to join than an uneven last round does: 288
-// units of 2 x 1531 causal queries 34 us whole, 38 in parts, their dq 57 and 47.)
-inline AttnPlan attn_plan(const AttnCost& c, int64_t heads, bool forward) {
-  const int slots = c.block == 8 * kAttnWave ? kAttnCus : kAttnSlots;
-  return attn_plan(c, heads, slots, forward ? kAttnCus : slots);
+                  kAttnWave * waves, fine, ways};
 }
 struct AttnWs {
   AttnCost cost;
@@ -558,7 +569,7 @@ struct AttnWs {
 inline AttnWs attn_ws(const AttnSizes& s) {
   AttnWs w;
   w.cost = attn_row_cost(s);
-  w.plan = attn_plan(w.cost, s.B * s.Hk, true);
+  w.plan = attn_plan(w.cost, s.B * s.Hk);
   const size_t n = attn_all_part_rows(w.cost, w.plan);
   w.part = 0;
   w.part_lse = align256(n * s.D * 4);
@@ -579,8 +590,8 @@ inline AttnGradWs attn_grad_ws(const AttnSizes& s) {
   const int64_t heads = s.B * s.Hk;
   w.rows = attn_row_cost(s);
   w.keys = attn_key_cost(s);
-  w.dq = attn_plan(w.rows, heads, false);
-  w.dkv = attn_plan(w.keys, heads, false);
+  w.dq = attn_plan(w.rows, heads);
+  w.dkv = attn_plan(w.keys, heads);
   w.key_runs = s.scaled ? (int)((s.Lk + kAttnKeyRun - 1) / kAttnKeyRun) : 0;
   const size_t padded = align256((size_t)heads * w.dq.blocks * w.rows.block * 4);
   w.lse = 0;

@@ -1,5 +1,5 @@
 // The attention kernels' deal of tiles to workgroups, on the host: for each
-// line "held passing group offset causal by_keys heads block forward" of the input,
+// line "held passing group offset causal by_keys heads block" of the input,
 // every workgroup's part; prints "ok grid each" or what is wrong.
 #include <stdio.h>
 
@@ -10,18 +10,16 @@
 using namespace svdq;
 
 int main() {
-  long long held, passing, group, offset, causal, by_keys, heads, block, forward;
-  while (scanf("%lld %lld %lld %lld %lld %lld %lld %lld %lld", &held, &passing, &group, &offset, &causal, &by_keys, &heads, &block,
-               &forward) == 9) {
+  long long held, passing, group, offset, causal, by_keys, heads, block;
+  while (scanf("%lld %lld %lld %lld %lld %lld %lld %lld", &held, &passing, &group, &offset, &causal, &by_keys, &heads, &block) == 8) {
     const AttnCost c = {(int)held, (int)passing, (int)group, (int)offset, (int)causal, (int)by_keys, (int)block};
-    const int slots = block == 256 ? kAttnCus : kAttnSlots;
-    const AttnPlan p = attn_plan(c, heads, forward);
+    const AttnPlan p = attn_plan(c, heads);
     const int units = p.blocks * (int)heads;
     const char* bad = nullptr;
     std::vector<int> seen(p.grid, 0), at(units, 0), count(units, 0);
     AttnParts deal;
     if (p.each) {
-      if (p.grid > slots || units >= slots) bad = "more parts than run at once";
+      if (p.grid > kAttnCus || units >= kAttnCus) bad = "more parts than run at once";
       else attn_parts(c, p, &deal);
     }
     int last_unit = -1;
