@@ -20,7 +20,7 @@ namespace svdq {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 // W waves of NB blocks of 32 query rows, KW times (each way takes every KW-th
 // tile); DP the padded head; NP operands for probabilities. Two waves a SIMD

@@ -140,7 +140,7 @@ svdq_status check_attention(const svdq_attention_desc* d) {
   if (!d) return SVDQ_ERR_NULL;
   if (d->dtype != SVDQ_DT_BF16 && d->dtype != SVDQ_DT_F16) return SVDQ_ERR_FORMAT;
   if (d->head_dim < 8 || d->head_dim > 128 || d->head_dim % 8 != 0 || d->kv_heads < 1 || d->heads < d->kv_heads ||
-      d->heads > 65535 || d->heads % d->kv_heads != 0 || !(d->scale > 0.f) || !std::isfinite(d->scale))
+      d->heads > 65535 || d->heads % d->kv_heads != 0 || !(d->scale >= 0x1p-64f && d->scale <= 0x1p64f))   // (lse / scale is fp32)
     return SVDQ_ERR_SHAPE;
   const int64_t most = (int64_t)1 << 30, group = d->heads / d->kv_heads;
   if (d->samples < 0 || d->queries < 0 || d->keys < 0 || d->samples > 65535 || d->queries >= most || d->keys >= most)

@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 
-
 // Sums over a team, the same in each of its lanes. The caller alternates
 // areas, so one barrier per call is enough.
 template <int n, int LANES>

@@ -808,8 +808,11 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * [samples][keys][kv_heads][head_dim], of type bf16 or fp16; lse fp32
  * [samples][heads][queries]. Scores, statistics and sums are fp32; the
  * probabilities (and in the backward the scores' gradients) are rounded to the
- * type for the matrix products, fp16 with powers of two taken out so that small
- * ones keep their digits. All orders of summation are fixed by the sizes.
+ * type for the matrix products, fp16 with powers of two taken out in the
+ * backward so that small ones keep their digits. For heads up to 32 elements,
+ * and up to 64 keys or queries times heads / kv_heads, they enter the products
+ * as two values of the type, the second what the first's rounding left. All
+ * orders of summation are fixed by the sizes.
  * Keys and values that the mask drops, and the q and dout of queries that see
  * no key, are not used whatever they hold. A value that is not finite makes
  * every row that sees it NaN, and causal may also reach rows that do not see it
@@ -817,7 +820,7 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * Limits: head_dim a multiple of 8 up to 128; 1 <= kv_heads, heads a multiple
  * of kv_heads, samples * kv_heads <= 65535; queries * heads / kv_heads < 2^30
  * and keys < 2^30; blocks of 128 of those times samples * kv_heads <= 2^22;
- * scale > 0 and finite; 64 tokens (and the heads of one key head) of a tensor
+ * 2^-64 <= scale <= 2^64; 64 tokens (and the heads of one key head) of a tensor
  * span less than 2^30 elements. Outputs must not overlap inputs or one another.
  * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_WORKSPACE,
  * SVDQ_ERR_DEVICE.

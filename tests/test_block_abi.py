@@ -109,6 +109,7 @@ def abwd(d, do=heads(), q=heads(), k=heads(), v=heads(), o=heads(), lse=P, mask=
     (dict(dtype=2), FORMAT), (dict(dtype=-1), FORMAT), (dict(head_dim=0), SHAPE), (dict(head_dim=132), SHAPE),
     (dict(head_dim=12), SHAPE), (dict(kv_heads=0), SHAPE), (dict(kv_heads=3), SHAPE), (dict(heads=4), SHAPE),
     (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=math.nan), SHAPE), (dict(scale=math.inf), SHAPE),
+    (dict(scale=2.0 ** -65), SHAPE), (dict(scale=2.0 ** 65), SHAPE),
     (dict(samples=-1), SHAPE), (dict(queries=-1), SHAPE), (dict(keys=1 << 30), SHAPE), (dict(samples=10000), SHAPE),
     (dict(kv_heads=1, queries=1 << 27), SHAPE), (dict(queries=1 << 27), SHAPE)])
 def test_attention_descriptor(desc, status):

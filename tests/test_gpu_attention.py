@@ -45,6 +45,7 @@ def _run(q, k, v, dout, mask, causal, scale=None, check=True):
     (1, 1, 1, 1, 1, 8, BF, False, False),
     (1, 1, 1, 1, 1, 128, HF, True, False),
     (1, 1, 500, 6, 2, 32, BF, False, True),
+    (1, 70, 200, 4, 2, 8, BF, False, True),
     (2, 90, 150, 4, 1, 24, HF, True, True),
     (1, 310, 5, 9, 9, 16, BF, False, False),
     (1, 2000, 300, 24, 24, 32, HF, True, False),     # whole units in workgroups of eight waves
@@ -137,6 +138,13 @@ def test_peaked_flat_and_rising_scores(dtype):
     q = q.abs()
     _run(q, k.to(dtype), v, dout, None, False, scale=0.1)
     _run(q, -k.to(dtype), v, dout, None, True, scale=0.1)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** -20, 8.0])
+def test_scales(scale, dtype):
+    q, k, v, dout = _inputs(1, 130, 300, 2, 2, 64, dtype, 15)
+    _run(q, k, v, dout, _mask(1, 300, 6), True, scale=scale)
 
 
 @pytest.mark.parametrize("small", [1e-6, 1.0, 1e4])
