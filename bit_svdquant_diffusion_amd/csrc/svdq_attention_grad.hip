@@ -674,7 +674,7 @@ hipError_t launch_pass(AttnGradArgs g, const AttnCost& cost, const AttnPlan& pla
   hipLaunchKernelGGL((grad_kernel<T, DP, W, KW, NP, KEYS, false>()), grid, block, (kGradLds<DP, W, KW, KEYS>), st, g, AttnUnits{});
   return hipGetLastError();
 }
-// (heads above 64: a workgroup of keys has eight waves, see attn_key_cost)
+// (heads above 96: a workgroup of keys has eight waves, see attn_key_cost)
 template <typename T, int DP, bool KEYS>
 hipError_t launch_pass(const AttnGradArgs& g, const AttnCost& cost, const AttnPlan& plan, hipStream_t st) {
   constexpr int NP = DP == 32 ? 2 : 1;
@@ -682,7 +682,7 @@ hipError_t launch_pass(const AttnGradArgs& g, const AttnCost& cost, const AttnPl
     if (cost.fine) return launch_pass<T, DP, 8, 1, 2, KEYS>(g, cost, plan, st);
   if constexpr (!KEYS || DP < 128)
     if (cost.ways == 2) return launch_pass<T, DP, 4, 2, NP, KEYS>(g, cost, plan, st);
-  if constexpr (!KEYS || DP <= 64)
+  if constexpr (!KEYS || DP < 128)
     if (cost.block == 4 * kAttnWave) return launch_pass<T, DP, 4, 1, NP, KEYS>(g, cost, plan, st);
   return launch_pass<T, DP, 8, 1, NP, KEYS>(g, cost, plan, st);
 }
@@ -721,10 +721,10 @@ template <typename T, int DP, bool KEYS>
 hipError_t prepare_of() {
   constexpr int NP = DP == 32 ? 2 : 1;
   hipError_t e = prepare_pass<T, DP, 8, 1, NP, KEYS>();
-  if constexpr (!KEYS || DP <= 64)
+  if constexpr (!KEYS || DP < 128) {
     if (e == hipSuccess) e = prepare_pass<T, DP, 4, 1, NP, KEYS>();
-  if constexpr (!KEYS || DP < 128)
     if (e == hipSuccess) e = prepare_pass<T, DP, 4, 2, NP, KEYS>();
+  }
   if constexpr (DP > 32)
     if (e == hipSuccess) e = prepare_pass<T, DP, 8, 1, 2, KEYS>();
   return e;

@@ -542,24 +542,36 @@ inline bool attn_fine(int64_t held, int64_t passing, int64_t D) {
 inline int attn_ways(int64_t held, int64_t heads, bool causal) {
   return causal || (held + 4 * kAttnWave - 1) / (4 * kAttnWave) * heads <= kAttnCus ? 2 : 1;
 }
+// Four waves (one way) of held rows also where there are blocks of eight for
+// every CU: where the last block of eight would hold little (64 x 300 queries,
+// 12 heads of 128, forward 74 us against 95, backward 290 against 336; 8 x 1100,
+// 16 heads, 102 against 113 and 368 against 387), and, with heads up to 64, of
+// which CUs hold three such workgroups, where a unit has few tiles, so that its
+// start and end are what takes time (2 x 4096 queries, 20 heads of 64, over 77
+// keys, backward 57 against 61; over 500 keys, 24 heads, forward 41.5 against
+// 40.6).
+inline bool attn_shorter(int64_t held, int64_t passing, int64_t D) {
+  const int64_t four = (held + 4 * kAttnWave - 1) / (4 * kAttnWave), eight = (held + 8 * kAttnWave - 1) / (8 * kAttnWave);
+  return held > kAttnWave && (four * 10 <= eight * 18 || (D <= 64 && passing <= 5 * kAttnTile));
+}
 inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
-  const int64_t rows = s.Lq * (s.H / s.Hk);
-  const bool fine = attn_fine(rows, s.Lk, s.D);
-  const int waves = fine && s.D > 32 ? 8 : attn_waves(rows, s.B * s.Hk);
-  return AttnCost{(int)rows, (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0,
-                  kAttnWave * waves, fine, waves == 4 ? attn_ways(rows, s.B * s.Hk, s.causal) : 1};
+  const int64_t rows = s.Lq * (s.H / s.Hk), heads = s.B * s.Hk;
+  const bool fine = attn_fine(rows, s.Lk, s.D), eight = fine && s.D > 32;
+  int waves = eight ? 8 : attn_waves(rows, heads);
+  const int ways = waves == 4 ? attn_ways(rows, heads, s.causal) : 1;
+  if (!eight && ways == 1 && attn_shorter(rows, s.Lk, s.D)) waves = 4;
+  return AttnCost{(int)rows, (int)s.Lk, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 0, kAttnWave * waves, fine, ways};
 }
 inline AttnCost attn_key_cost(const AttnSizes& s) {
-  const int64_t rows = s.Lq * (s.H / s.Hk);
-  const bool fine = attn_fine(s.Lk, rows, s.D);
-  // (V's fragments of heads above 96 leave no room in LDS for a second way;
-  // with heads above 64 four waves alone gain nothing: 2 x 1601 keys, heads of
-  // 72, 106 us against 93)
-  int waves = (fine && s.D > 32) || s.D > 96 ? 8 : attn_waves(s.Lk, s.B * s.Hk);
-  const int ways = waves == 4 ? attn_ways(s.Lk, s.B * s.Hk, s.causal) : 1;
+  const int64_t rows = s.Lq * (s.H / s.Hk), heads = s.B * s.Hk;
+  // (V's fragments of heads above 96 leave no room in LDS for a second way or
+  // workgroup; with heads above 64 four waves alone gain nothing otherwise)
+  const bool fine = attn_fine(s.Lk, rows, s.D), eight = (fine && s.D > 32) || s.D > 96;
+  int waves = eight ? 8 : attn_waves(s.Lk, heads);
+  const int ways = waves == 4 ? attn_ways(s.Lk, heads, s.causal) : 1;
   if (s.D > 64 && ways == 1) waves = 8;
-  return AttnCost{(int)s.Lk, (int)rows, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1,
-                  kAttnWave * waves, fine, ways};
+  if (!eight && ways == 1 && attn_shorter(s.Lk, rows, s.D)) waves = 4;
+  return AttnCost{(int)s.Lk, (int)rows, (int)(s.H / s.Hk), (int)(s.Lk - s.Lq), s.causal, 1, kAttnWave * waves, fine, ways};
 }
 struct AttnWs {
   AttnCost cost;

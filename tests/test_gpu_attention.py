@@ -65,6 +65,10 @@ def _run(q, k, v, dout, mask, causal, scale=None, check=True):
     (1, 700, 700, 2, 2, 16, HF, False, False),
     (4, 130, 70, 24, 24, 128, BF, False, True),
     (1, 300, 260, 64, 1, 64, BF, True, False),       # all heads share one key head
+    (22, 150, 290, 12, 6, 96, BF, True, True),       # many short units: workgroups of four waves
+    (13, 300, 300, 20, 20, 64, HF, False, True),
+    (20, 290, 140, 14, 14, 128, HF, True, False),
+    (15, 140, 270, 18, 18, 24, BF, False, False),
 ])
 def test_against_float64(B, Lq, Lk, H, Hk, D, dtype, causal, masked):
     q, k, v, dout = _inputs(B, Lq, Lk, H, Hk, D, dtype, Lq + Lk)
