@@ -169,7 +169,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void residual_fwd_kernel(ResidualAr
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[j][i] = __builtin_fmaf(gate[j][i], h[j][i], a.alpha * v[j][i]);
+      for (int i = 0; i < VEC; ++i) {
+        v[j][i] = __builtin_fmaf(gate[j][i], h[j][i], a.alpha * v[j][i]);
+        // (an fp32 sum that is then rounded, for every type: fused into the
+        // conversion an fp16 row would round the exact sum)
+        if constexpr (__is_same(T, Half)) asm("" : "+v"(v[j][i]));
+      }
       out[j].set(v[j]);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v[j][i] = out[j].at(i);   // the norm is of what was written
