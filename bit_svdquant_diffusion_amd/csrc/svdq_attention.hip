@@ -25,9 +25,13 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // W waves of NB blocks of 32 query rows, KW times (each way takes every KW-th
 // tile); DP the padded head; NP operands for probabilities. Two waves a SIMD
 // (up to 256 registers), so that one's products run under the other's
-// exponentials: 4608 tokens, 24 heads of 128 with a mask 252 us (1.03
+// exponentials: 4608 tokens, 24 heads of 128 with a mask 250 us (1.04
 // PFLOP/s), with one wave a SIMD 411, with one of two blocks 355, with
-// workgroups of four waves instead of eight 270.
+// workgroups of four waves instead of eight 270. What bounds it: a tile's
+// exponentials, maxima, sums and roundings take the vector unit as long as its
+// products the matrix unit (40% of the cycles), at a clock that power holds
+// near 2 GHz; LDS is busy a fifth of the time. One query over 65536 keys
+// streams its cache at 5.5 TB/s.
 template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;

@@ -129,9 +129,10 @@ __device__ __forceinline__ void join_add(uint8_t* smem, int wave, int lane, f32x
 
 // dk and dv of 32 NB keys a wave; the query rows pass by. With heads of 128
 // the accumulators and the K fragments take 160 of the 256 registers that two
-// waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads: 574
-// us against 760 with V in registers, of which 53 spill, 768 with one wave a
-// SIMD and two blocks of keys, 870 with workgroups of four waves).
+// waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads, of
+// the same step: 574 us against 760 with V in registers, of which 53 spill, 768
+// with one wave a SIMD and two blocks of keys, 870 with workgroups of four
+// waves; now 535, 0.98 PFLOP/s, with the matrix unit busy 43% of the cycles).
 template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
@@ -377,7 +378,8 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
 }
 
 // dq of 32 NB query rows a wave; the keys pass by, as in the forward (4608
-// tokens, 24 heads of 128: 345 us, 1.13 PFLOP/s).
+// tokens, 24 heads of 128: 350 us, 1.12 PFLOP/s, the matrix unit busy 45% of
+// the cycles). It also leaves what the keys' pass starts its sums with.
 template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
