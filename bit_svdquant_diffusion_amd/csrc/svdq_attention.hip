@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   int last[NB];   // of a row without keys (and past the last row) below 0
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = r / G;
+    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r);
     const T* row = qp + (int64_t)i * a.q.token + (int64_t)(r - i * G) * a.q.head;
     last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
 #pragma unroll
@@ -76,8 +76,8 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   }
   const int k_begin = (at.first + way) * kAttnRows, k_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   // what every and what any row of this wave sees
-  const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
-  const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
+  const int w_first = a.causal ? attn_query(a.group, r0) + a.Lk - a.Lq : a.Lk - 1;
+  const int w_last = r0 >= R ? -1 : a.causal ? attn_query(a.group, min(r0 + 32 * NB, R) - 1) + a.Lk - a.Lq : a.Lk - 1;
 
   auto fetch = [&](int k0, int stage, uint64_t keep) {
     const int rows = min(kAttnRows, a.Lk - k0);
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = r / G, g = r - i * G;
+    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), g = r - i * G;
     const float sum = sum_halves(l[n]);
     const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = m[n] + __builtin_log2f(sum);   // (no key: -inf)
     if (r >= R) continue;
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins jo
     m = top;
   }
   if (!live) return;
-  const int i = r / a.G, head = hb % a.Hk * a.G + r - i * a.G, b = hb / a.Hk;
+  const int i = attn_query(a.group, r), head = hb % a.Hk * a.G + r - i * a.G, b = hb / a.Hk;
   o *= sum == 0.f ? 0.f : 1.f / sum;
   if (lane == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + i] = (m + __builtin_log2f(sum)) * kLn2;
   if (d < a.D)

@@ -204,7 +204,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   const int w_all = a.causal ? max(key0 + 32 * NB - 1 - (a.Lk - a.Lq), 0) * G : 0;   // from here on rows see all of the wave's keys
 
   auto fetch = [&](int row0, int stage) {
-    const int i0 = row0 / G, i1 = min(row0 + kAttnRows - 1, R - 1) / G;
+    const int i0 = attn_query(a.group, row0), i1 = attn_query(a.group, min(row0 + kAttnRows, R) - 1);
     // the heads of the queries i0 .. i1
     const auto rq = rows_resource(qp + i0 * a.q.token, (int)((i1 - i0) * a.q.token + (G - 1) * a.q.head + D) * 2);
     const auto rd = rows_resource(dop + i0 * g.dout.token, (int)((i1 - i0) * g.dout.token + (G - 1) * g.dout.head + D) * 2);
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j = wave * NT + n, ch = TL::chunk_of(j, lane), r = row0 + TL::row_of(j, lane);
-      const int i = G == 1 ? r : r / G, hd = r - i * G;
+      const int i = attn_query(a.group, r), hd = r - i * G;
       const bool in = r < R && r >= dead && ch * 8 < D;
       lds_transfer_16(rq, tq + n * 1024, in ? (uint32_t)(((i - i0) * a.q.token + hd * a.q.head + ch * 8) * 2) : kPastEnd);
       lds_transfer_16(rd, td + n * 1024, in ? (uint32_t)(((i - i0) * g.dout.token + hd * g.dout.head + ch * 8) * 2) : kPastEnd);
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   float lse[NB], delta[NB], c[NB], wg_top = 0.f;   // (lse and delta negative)
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = r / G, hd = r - i * G;
+    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), hd = r - i * G;
     last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
     float top_do = 0.f, sum = 0.f;
 #pragma unroll
@@ -464,8 +464,8 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     }
   }
   const int k_begin = (at.first + way) * kAttnRows, k_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
-  const int w_first = a.causal ? r0 / G + a.Lk - a.Lq : a.Lk - 1;
-  const int w_last = r0 >= R ? -1 : a.causal ? (min(r0 + 32 * NB, R) - 1) / G + a.Lk - a.Lq : a.Lk - 1;
+  const int w_first = a.causal ? attn_query(a.group, r0) + a.Lk - a.Lq : a.Lk - 1;
+  const int w_last = r0 >= R ? -1 : a.causal ? attn_query(a.group, min(r0 + 32 * NB, R) - 1) + a.Lk - a.Lq : a.Lk - 1;
 
   auto fetch = [&](int k0, int stage, uint64_t keep) {
     const int rows = min(kAttnRows, a.Lk - k0);
@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = r / G, hd = hk * G + r - i * G;
+    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), hd = hk * G + r - i * G;
     const float f = a.scale / c[n];
     if (r >= R) continue;
     if (PARTS && !at.whole) {
@@ -619,7 +619,7 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, Att
   const AttnJoin at = joins.at[blockIdx.x];
   const int hb = at.unit / a.plan.blocks, block = at.unit - hb * a.plan.blocks;
   const int lane = threadIdx.x & 31, in = (int)blockIdx.y * 8 + (threadIdx.x >> 5), r = block * a.cost.block + in;
-  const int width = KEYS ? 2 * a.D : a.D, b = hb / a.Hk, hk = hb % a.Hk, i = r / a.G;
+  const int width = KEYS ? 2 * a.D : a.D, b = hb / a.Hk, hk = hb % a.Hk, i = attn_query(a.group, r);
   if (in >= a.part_rows || r >= a.cost.held) return;
   for (int d = lane * 4; d < width; d += 128) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};

@@ -179,6 +179,7 @@ AttnArgs attn_args(const svdq_attention_desc* d, const uint8_t* mask, int64_t ma
   a.H = d->heads;
   a.Hk = d->kv_heads;
   a.G = d->heads / d->kv_heads;
+  a.group = attn_group(a.G);
   a.D = d->head_dim;
   a.causal = d->causal ? 1 : 0;
   a.scale = d->scale;

@@ -203,6 +203,7 @@ struct AttnArgs {
   const uint8_t* mask;       // [B][Lk], may be null
   int64_t mask_batch;
   float* lse;                // [B][H][Lq]
+  AttnGroup group;           // of G
   AttnCost cost;             // the launch: what is held and what passes,
   AttnPlan plan;             // and how it is dealt
   int part_rows;

@@ -510,6 +510,20 @@ SVDQ_HD inline AttnPiece attn_piece(const AttnCost& c, const AttnPlan& p, const 
 // rows of a part in the workspace
 inline int64_t attn_part_rows(const AttnCost& c) { return c.held < c.block ? c.held : c.block; }
 inline size_t attn_all_part_rows(const AttnCost& c, const AttnPlan& p) { return p.each ? (size_t)p.grid * attn_part_rows(c) : 0; }
+// The query of row r < 2^30 (its quotient by the group, a product and a shift
+// on the device: mul = floor(2^(30 + shift) / group) + 1 is at most 2^(30 +
+// shift) / group + 1, which with 2^shift >= group is too little to carry).
+struct AttnGroup {
+  uint32_t mul, shift;
+};
+inline AttnGroup attn_group(int group) {
+  uint32_t shift = 0;
+  while ((1 << shift) < group) ++shift;
+  return AttnGroup{(uint32_t)(((uint64_t)1 << (30 + shift)) / (uint32_t)group) + 1, shift};
+}
+SVDQ_HD inline int attn_query(const AttnGroup& g, int r) {
+  return (int)((uint32_t)(((uint64_t)((uint32_t)r << 2) * g.mul) >> 32) >> g.shift);
+}
 struct AttnSizes {
   int64_t B, Lq, Lk, H, Hk, D;
   bool causal, scaled;   // scaled: fp16

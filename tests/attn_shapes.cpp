@@ -30,6 +30,10 @@ int main() {
     if (!bad) bad = check(g.rows, g.dq, D, false);
     if (!bad) bad = check(g.keys, g.dkv, D, true);
     if (!bad && (int64_t)g.dq.blocks * g.rows.block % kAttnTile) bad = "rows up to a part of a tile";
+    const int G = (int)(H / Hk), rows = (int)(Lq * G);
+    const AttnGroup group = attn_group(G);
+    for (int r : {0, 1, G - 1, G, rows - 1, rows, (1 << 30) - 1, (1 << 30) / G * G - 1 + (G == 1), 0x2aaaaaaa, 0x3fedcba9})
+      if (!bad && r >= 0 && r < 1 << 30 && attn_query(group, r) != r / G) bad = "the query of a row";
     if (bad)
       printf("%s: %lld %lld %lld %lld %lld %lld %lld %lld\n", bad, B, Lq, Lk, H, Hk, D, causal, scaled);
     else
