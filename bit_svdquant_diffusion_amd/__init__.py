@@ -853,7 +853,7 @@ def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, group
 
 
 def _rows_like(x, shape, stream):
-    """An uninitialised matrix of x's type."""
+    """An uninitialised tensor of x's type (contiguous)."""
     if stream is None and x.is_contiguous():
         return _t.empty_like(x)
     return _empty(shape, x.dtype, x, stream)
@@ -1378,14 +1378,14 @@ def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool 
     if not freqs.is_contiguous() or freqs.dtype != torch.float64 or freqs.shape != (n,):
         raise ValueError("freqs: contiguous float64, one for each pair")
     if q_out is None:
-        q_out = _empty(shape, dtype, q, stream)
+        q_out = _rows_like(q, shape, stream)
     qs, qo = _heads(q, "q", shape, dtype), _heads(q_out, "q_out", shape, dtype)
     if k is None:
         keep, (a, b) = _all_heads(qs, qo)
         ka = kb = None
     else:
         if k_out is None:
-            k_out = _empty(kshape, dtype, k, stream)
+            k_out = _rows_like(k, kshape, stream)
         keep, (a, b, ka, kb) = _all_heads(qs, qo, _heads(k, "k", kshape, dtype), _heads(k_out, "k_out", kshape, dtype))
     _call("svdq_rope", at, stream, d, a, ka, positions.data_ptr(), L * axes if len(positions.shape) == 3 else 0, freqs.data_ptr(),
           b, kb)
@@ -1446,7 +1446,7 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
     (d, _, size, _), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if out is None:
-        out = _empty(shape, dtype, q, stream)
+        out = _rows_like(q, shape, stream)
     lse = _empty((shape[0], shape[2], shape[1]), _t.float32, q, stream)
     ws, wsp, size = _scratch(workspace, size, q, stream)
     keep, (a, b, c, o) = _all_heads(_heads(q, "q", shape, dtype), _heads(k, "k", kshape, dtype), _heads(v, "v", kshape, dtype),
@@ -1466,9 +1466,9 @@ def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = Fals
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if lse.dtype != _t.float32 or lse.shape != (shape[0], shape[2], shape[1]) or not lse.is_contiguous():
         raise ValueError("lse: float32 [samples][heads][queries]")
-    dq = _empty(shape, dtype, q, stream) if dq is None else dq
-    dk = _empty(kshape, dtype, q, stream) if dk is None else dk
-    dv = _empty(kshape, dtype, q, stream) if dv is None else dv
+    dq = _rows_like(q, shape, stream) if dq is None else dq
+    dk = _rows_like(k, kshape, stream) if dk is None else dk
+    dv = _rows_like(k, kshape, stream) if dv is None else dv
     ws, wsp, size = _scratch(workspace, size, q, stream)
     keep, h = _all_heads(_heads(dout, "dout", shape, dtype), _heads(q, "q", shape, dtype), _heads(k, "k", kshape, dtype),
                          _heads(v, "v", kshape, dtype), _heads(o, "o", shape, dtype), _heads(dq, "dq", shape, dtype),
