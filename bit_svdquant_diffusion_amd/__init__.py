@@ -1439,7 +1439,7 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
     strides of 16 bytes). key_mask: bool or uint8 [samples][keys], true for the
     keys that take part; causal: query i sees the keys j <= i + keys - queries;
     scale: default head_dim^(-1/2). lse: float32 [samples][heads][queries]. A
-    query without keys has o = 0, lse = -inf."""
+    query without keys has o = 0, lse = -inf. out must not overlap an input."""
     at = _on_device(q, k, v, key_mask, out, workspace)
     if _wants_grad(q, k, v):
         _no_graph("attention_forward")
@@ -1458,7 +1458,7 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
 def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = False, scale=None, dq=None, dk=None, dv=None,
                        workspace=None, stream=None):
     """svdq_attention_backward: (dq, dk, dv) for dout of o, from the forward's
-    inputs and its o and lse."""
+    inputs and its o and lse. They must not overlap an input or one another."""
     at = _on_device(q, dout, k, v, o, lse, key_mask, dq, dk, dv, workspace)
     if _wants_grad(dout):
         _no_graph("attention_backward")
