@@ -15,7 +15,9 @@
 // fp16 holds 2^-24 at least. Gradients and probabilities go well below that,
 // so p enters its product times 2^10, and ds times the power of two that
 // brings the largest value it could have, 2 D max|do| max|v|, to 2^15; both
-// are taken out of the sums in fp32. bf16 has fp32's exponents and needs none.
+// are taken out of the sums in fp32. The largest |v| is that of all keys, also
+// for one key's ds: delta is do . o, which any key that the row sees may make
+// large. bf16 has fp32's exponents and needs none.
 #include <algorithm>
 
 #include "svdq_attention.h"
@@ -154,20 +156,21 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   const T* dop = static_cast<const T*>(g.dout.p) + b * g.dout.batch + (int64_t)hk * G * g.dout.head;
   const int64_t Rp = g.rows_padded;
   const float *lse = g.lse + at.hb * Rp, *delta = g.delta + at.hb * Rp;
-  const float top_do = kScaled<T> ? wave_top(g.top_do + at.hb * g.row_blocks, g.row_blocks, lane) : 0.f;
+  const float c = kScaled<T> ? ds_scale(D, wave_top(g.top_do + at.hb * g.row_blocks, g.row_blocks, lane),
+                                        wave_top(g.top_v + at.hb * g.key_runs, g.key_runs, lane))
+                             : 1.f;
+  const float dsc = c / kProbScale, fk = a.scale / c;   // the factor of ds (of fp16 probabilities); of dk
 
   // this lane's keys, as operand B (of both products that give scores)
   const int key0 = at.block * (32 * NB * W) + wave * (32 * NB);
   u32x4 kf[NB][TL::kSteps], vf[kHoldV ? NB : 1][TL::kSteps];
   bool live[NB];
   int first[NB];   // the first row that sees the key
-  float dsc[NB], fk[NB];   // fp16: the factor of a key's ds; of its dk
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const int key = key0 + 32 * n + lr;
     live[n] = key < a.Lk && (!a.mask || a.mask[b * a.mask_batch + key]);
     first[n] = a.causal ? max(key - (a.Lk - a.Lq), 0) * G : 0;
-    float top_v = 0.f;
     const T* kr = static_cast<const T*>(a.k.p) + b * a.k.batch + key * a.k.token + hk * a.k.head;
     const T* vr = static_cast<const T*>(a.v.p) + b * a.v.batch + key * a.v.token + hk * a.v.head;
 #pragma unroll
@@ -176,15 +179,11 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
       const bool in = live[n] && d < D;
       kf[n][s] = in ? *reinterpret_cast<const u32x4*>(kr + d) : u32x4{0, 0, 0, 0};
       const u32x4 v = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
-      if constexpr (kScaled<T>) top_v = amax_x8<T>(top_v, v);
       if constexpr (kHoldV)
         vf[n][s] = v;
       else   // (read by this wave alone)
         *reinterpret_cast<u32x4*>(held + (wave * NB + n) * 32 * TL::kRowBytes + (pl.straight ^ (s << 5))) = v;
     }
-    const float c = kScaled<T> ? ds_scale(D, top_do, max_halves(top_v)) : 1.f;
-    dsc[n] = c / kProbScale;
-    fk[n] = a.scale / c;
   }
   const uint8_t* my_v = held + (kHoldV ? 0 : wave * NB * 32 * TL::kRowBytes);
   // rows that see no key at all are read as zeros
@@ -301,7 +300,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dp[n][i] *= kScaled<T> ? s[n][i] * dsc[n] : s[n][i];
+        for (int i = 0; i < 16; ++i) dp[n][i] *= kScaled<T> ? s[n][i] * dsc : s[n][i];
         if (part) {   // (do may hold what times 0 is NaN)
           const int lim = first[n] - row0 - 32 * rb - 4 * h;
 #pragma unroll
@@ -351,7 +350,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
           f32x4 x, y;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[i] = live[n] ? dk[blk][n][4 * q + i] * fk[n] : 0.f;
+            x[i] = live[n] ? dk[blk][n][4 * q + i] * fk : 0.f;
             y[i] = live[n] ? dv[blk][n][4 * q + i] * fv : 0.f;
           }
           *reinterpret_cast<f32x4*>(row + d) = x;
@@ -364,7 +363,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
 #pragma unroll
     for (int blk = 0; blk < TL::kBlocks; ++blk) {
       u32x4 x[2], y[2];
-      head_chunks<T>(dk[blk][n], fk[n], x);
+      head_chunks<T>(dk[blk][n], fk, x);
       head_chunks<T>(dv[blk][n], fv, y);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
