@@ -22,6 +22,17 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// From here on a row's reference (in base 2) is too coarse: half a step of fp32
+// at 2^20 is 2^-5, by which its largest probability is off a power of two.
+constexpr float kFarScore = 0x1p20f;
+__device__ __forceinline__ float reference(float m, float scale_log2) {
+  return m == -__builtin_inff() ? 0.f : m * scale_log2;
+}
+// what m scale_log2 is above the reference that the sums have
+__device__ __forceinline__ float reference_off(float m, float base, float scale_log2) {
+  return m == -__builtin_inff() || __builtin_fabsf(base) > kFarScore ? 0.f : __builtin_fmaf(m, scale_log2, -base);
+}
+
 // W waves of NB blocks of 32 query rows, KW times (each way takes every KW-th
 // tile); DP the padded head; NP operands for probabilities. Two waves a SIMD
 // (up to 256 registers), so that one's products run under the other's
@@ -106,12 +117,19 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     return k < a.Lk ? (mask ? (int)mask[k] : 1) : 0;
   };
 
+  // Of a row: m, the score (before the scale) that its maximum is taken at, and
+  // the reference of its sums in base 2, base = fp32(m scale_log2), so that a
+  // probability is one fused product. Where that is far from zero its rounding
+  // is no longer small beside 1: there (far: a row of the wave) the reference
+  // is m scale_log2 itself, and m is subtracted before the scale.
   f32x16 o[TL::kBlocks][NB];
-  float m[NB], l[NB];
+  float m[NB], base[NB], l[NB];
+  bool far[NB];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     m[n] = -__builtin_inff();
-    l[n] = 0.f;
+    base[n] = l[n] = 0.f;
+    far[n] = false;
 #pragma unroll
     for (int i = 0; i < TL::kBlocks; ++i) o[i][n] = f32x16{};
   }
@@ -170,25 +188,37 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kb][n][i]);
-      top = max_halves(top) * a.scale_log2;
+      top = max_halves(top);
       // The maximum that is subtracted follows the true one when that is more
       // than 8 (in base 2) above it: up to there the probabilities stay below
       // 2^8, which neither the sums nor either type's rounding minds, and most
       // tiles leave the accumulators as they are.
-      if (__any(top > m[n] + 8.f)) {
-        const float mn = __builtin_fmaxf(m[n], top);
-        const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+      if (__any((top - m[n]) * a.scale_log2 > 8.f)) {
+        const float mn = __builtin_fmaxf(m[n], top), bn = reference(mn, a.scale_log2);
+        const float step = (m[n] - mn) * a.scale_log2 + (reference_off(mn, bn, a.scale_log2) - reference_off(m[n], base[n], a.scale_log2));
+        const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(step);
         m[n] = mn;
+        base[n] = bn;
+        far[n] = __any(__builtin_fabsf(bn) > kFarScore);
         l[n] *= f;
 #pragma unroll
         for (int i = 0; i < TL::kBlocks; ++i) o[i][n] *= f;
       }
-      const float base = m[n] == -__builtin_inff() ? 0.f : m[n];
+      float sub = base[n];
+      if (far[n]) {
+        const bool before = __builtin_fabsf(sub) > kFarScore;   // (this row's)
+        const float off = before ? m[n] : 0.f;
+        sub = before ? 0.f : sub;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[kb][n][i] -= off;
+      }
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[kb][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][n][i], a.scale_log2, -base));
+          s[kb][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][n][i], a.scale_log2, -sub));
           l[n] += s[kb][n][i];
         }
         as_operands<T>(s[kb][n], 0, p[2 * kb][n]);
@@ -207,9 +237,12 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
       }
     sched_products<4 * TL::kBlocks * NB * NP, 8 * TL::kBlocks, 2, 8>();
   }
+  float lo[NB];   // what the reference of the sums is below m scale_log2
+#pragma unroll
+  for (int n = 0; n < NB; ++n) lo[n] = reference_off(m[n], base[n], a.scale_log2);
   if constexpr (KW > 1) {   // the second way's results join the first's
     f32x4* box = reinterpret_cast<f32x4*>(smem) + wave * (4 * TL::kBlocks * 64) + lane;
-    f32x2* stat = reinterpret_cast<f32x2*>(smem + W * TL::kBlocks * 4096) + wave * 64 + lane;
+    f32x4* stat = reinterpret_cast<f32x4*>(smem + W * TL::kBlocks * 4096) + wave * 64 + lane;
     tile_barrier();
     if (way == 1) {
 #pragma unroll
@@ -217,14 +250,17 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           box[(4 * i + q) * 64] = f32x4{o[i][0][4 * q], o[i][0][4 * q + 1], o[i][0][4 * q + 2], o[i][0][4 * q + 3]};
-      *stat = f32x2{m[0], l[0]};
+      *stat = f32x4{m[0], l[0], lo[0], 0.f};
     }
     tile_barrier();
     if (way == 1) return;
-    const f32x2 other = *stat;
-    const float top = __builtin_fmaxf(m[0], other[0]), base = top == -__builtin_inff() ? 0.f : top;
-    const float f = __builtin_amdgcn_exp2f(m[0] - base), fo = __builtin_amdgcn_exp2f(other[0] - base);
+    const f32x4 other = *stat;
+    const float top = __builtin_fmaxf(m[0], other[0]), from = top == -__builtin_inff() ? 0.f : top;
+    const float f = __builtin_amdgcn_exp2f((m[0] - from) * a.scale_log2 - lo[0]);
+    const float fo = __builtin_amdgcn_exp2f((other[0] - from) * a.scale_log2 - other[2]);
     m[0] = top;
+    base[0] = reference(top, a.scale_log2);
+    lo[0] = 0.f;
     l[0] = l[0] * f + other[1] * fo;
 #pragma unroll
     for (int i = 0; i < TL::kBlocks; ++i)
@@ -239,11 +275,11 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   for (int n = 0; n < NB; ++n) {
     const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), g = r - i * G;
     const float sum = sum_halves(l[n]);
-    const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = m[n] + __builtin_log2f(sum);   // (no key: -inf)
+    const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = base[n] + __builtin_log2f(sum);   // (no key: -inf)
     if (r >= R) continue;
     if (PARTS && !at.whole) {
       const int64_t row = (int64_t)place * a.part_rows + r - at.block * (32 * NB * W);
-      if (h == 0) a.part_lse[row] = lse2;
+      if (h == 0) reinterpret_cast<f32x2*>(a.part_stat)[row] = f32x2{m[n], sum * __builtin_amdgcn_exp2f(-lo[n])};
 #pragma unroll
       for (int blk = 0; blk < TL::kBlocks; ++blk)
 #pragma unroll
@@ -271,8 +307,8 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   }
 }
 
-// The parts of units joined: with the parts' lse, o = sum 2^(lse_s - m) o_s /
-// sum 2^(lse_s - m). WAYS half waves (32 lanes of four elements) have a row,
+// The parts of units joined: with the parts' maxima (before the scale) and sums,
+// w_s = l_s 2^((m_s - m) scale_log2), o = sum w_s o_s / sum w_s. WAYS half waves (32 lanes of four elements) have a row,
 // each every WAYS-th part; theirs are then joined in order through LDS.
 template <typename T, int WAYS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins joins) {
@@ -287,11 +323,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins jo
   float m = -__builtin_inff(), sum = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
-    for (int w = way; w < at.parts; w += WAYS) m = __builtin_fmaxf(m, a.part_lse[(int64_t)(at.first + w) * a.part_rows + in]);
+    for (int w = way; w < at.parts; w += WAYS) m = __builtin_fmaxf(m, a.part_stat[((int64_t)(at.first + w) * a.part_rows + in) * 2]);
     const float base = m == -__builtin_inff() ? 0.f : m;
     for (int w = way; w < at.parts; w += WAYS) {
       const int64_t row = (int64_t)(at.first + w) * a.part_rows + in;
-      const float f = __builtin_amdgcn_exp2f(a.part_lse[row] - base);
+      const f32x2 stat = reinterpret_cast<const f32x2*>(a.part_stat)[row];
+      const float f = stat[1] * __builtin_amdgcn_exp2f((stat[0] - base) * a.scale_log2);
       sum += f;
       if (d < a.D) o += *reinterpret_cast<const f32x4*>(a.part + row * a.D + d) * f;
     }
@@ -308,11 +345,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins jo
 #pragma unroll
     for (int i = 1; i < WAYS; ++i) top = __builtin_fmaxf(top, ms[half + i]);
     const float base = top == -__builtin_inff() ? 0.f : top;
-    o *= __builtin_amdgcn_exp2f(m - base);
-    sum *= __builtin_amdgcn_exp2f(m - base);
+    const float own = __builtin_amdgcn_exp2f((m - base) * a.scale_log2);
+    o *= own;
+    sum *= own;
 #pragma unroll
     for (int i = 1; i < WAYS; ++i) {
-      const float f = __builtin_amdgcn_exp2f(ms[half + i] - base);
+      const float f = __builtin_amdgcn_exp2f((ms[half + i] - base) * a.scale_log2);
       sum = __builtin_fmaf(sums[half + i], f, sum);
       o += os[half + i][lane] * f;
     }
@@ -321,7 +359,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnJoins jo
   if (!live) return;
   const int i = attn_query(a.group, r), head = hb % a.Hk * a.G + r - i * a.G, b = hb / a.Hk;
   o *= sum == 0.f ? 0.f : 1.f / sum;
-  if (lane == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + i] = (m + __builtin_log2f(sum)) * kLn2;
+  if (lane == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + i] = (reference(m, a.scale_log2) + __builtin_log2f(sum)) * kLn2;
   if (d < a.D)
     *reinterpret_cast<u32x2*>(static_cast<T*>(a.o.p) + b * a.o.batch + i * a.o.token + head * a.o.head + d) =
         u32x2{cvt_x2<T>(o[0], o[1]), cvt_x2<T>(o[2], o[3])};

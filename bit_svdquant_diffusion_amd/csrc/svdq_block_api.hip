@@ -15,6 +15,9 @@ namespace svdq {
 namespace {
 
 constexpr int64_t kMaxRows = 1 << 24;
+// Attention's gradients recompute exp(s - lse) from an lse in fp32, whose
+// rounding grows with the scores; the forward subtracts before it scales.
+constexpr float kAttnGradScale = 0x1p10f;
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 int elem_bytes(int dtype) { return dtype == SVDQ_DT_F32 ? 4 : 2; }
@@ -369,7 +372,7 @@ svdq_status svdq_attention_forward(const svdq_attention_desc* d, const svdq_head
   a.plan = w.plan;
   a.part_rows = (int)attn_part_rows(a.cost);
   a.part = (float*)((uint8_t*)ws + w.part);
-  a.part_lse = (float*)((uint8_t*)ws + w.part_lse);
+  a.part_stat = (float*)((uint8_t*)ws + w.part_stat);
   hipStream_t st = (hipStream_t)stream;
   return after_launch(launch_attention(a, st), st);
 }
@@ -386,6 +389,7 @@ svdq_status svdq_attention_backward(const svdq_attention_desc* d, const svdq_hea
                                     const uint8_t* key_mask, int64_t mask_batch, const svdq_heads* dq, const svdq_heads* dk,
                                     const svdq_heads* dv, void* ws, size_t ws_bytes, void* stream) {
   SVDQ_TRY(check_attention(d));
+  if (d->scale > kAttnGradScale) return SVDQ_ERR_SHAPE;
   if (d->samples * (d->queries + d->keys) == 0) return SVDQ_OK;
   AttnGradArgs g;
   std::memset(&g, 0, sizeof(g));

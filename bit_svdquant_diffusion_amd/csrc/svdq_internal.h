@@ -208,7 +208,7 @@ struct AttnArgs {
   AttnPlan plan;             // and how it is dealt
   int part_rows;
   float* part;               // parts of units: [grid][part_rows][D] (dk and dv: [2][D])
-  float* part_lse;           // [grid][part_rows]
+  float* part_stat;          // [grid][part_rows][2]: a part's maximum (before the scale) and sum
 };
 struct AttnGradArgs {
   AttnArgs f;

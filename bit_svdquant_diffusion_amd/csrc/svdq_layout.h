@@ -590,7 +590,7 @@ inline AttnCost attn_key_cost(const AttnSizes& s) {
 struct AttnWs {
   AttnCost cost;
   AttnPlan plan;
-  size_t part, part_lse, total;
+  size_t part, part_stat, total;
 };
 inline AttnWs attn_ws(const AttnSizes& s) {
   AttnWs w;
@@ -598,8 +598,8 @@ inline AttnWs attn_ws(const AttnSizes& s) {
   w.plan = attn_plan(w.cost, s.B * s.Hk);
   const size_t n = attn_all_part_rows(w.cost, w.plan);
   w.part = 0;
-  w.part_lse = align256(n * s.D * 4);
-  w.total = w.part_lse + align256(n * 4);
+  w.part_stat = align256(n * s.D * 4);
+  w.total = w.part_stat + align256(n * 8);
   return w;
 }
 // The backward's: -lse / scale and -delta of the rows (whole blocks), the

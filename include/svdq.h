@@ -820,8 +820,8 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * Limits: head_dim a multiple of 8 up to 128; 1 <= kv_heads, heads a multiple
  * of kv_heads, samples * kv_heads <= 65535; queries * heads / kv_heads < 2^30
  * and keys < 2^30; blocks of 128 of those times samples * kv_heads <= 2^22;
- * 2^-64 <= scale <= 2^64; 64 tokens (and the heads of one key head) of a tensor
- * span less than 2^30 elements. Outputs must not overlap inputs or one another.
+ * 2^-64 <= scale <= 2^64 (the backward: 2^10); 64 tokens (and the heads of one
+ * key head) of a tensor span less than 2^30 elements. Outputs must not overlap inputs or one another.
  * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_WORKSPACE,
  * SVDQ_ERR_DEVICE.
  * ---------------------------------------------------------------------------
@@ -845,7 +845,9 @@ SVDQ_API svdq_status svdq_attention_forward(const svdq_attention_desc* desc, con
  *   p = exp(s - lse),  ds = p (dout . v - dout . o),
  *   dv = sum p dout,  dq = scale sum ds k,  dk = scale sum ds q
  * (sums over the heads that share a key head, too). The probabilities are
- * computed again; none are kept. workspace: as above. */
+ * computed again; none are kept. That makes them as exact as lse is in fp32: a
+ * relative error of up to |lse| 2^-20, which leaves nothing where scores pass
+ * 2^20 (the forward holds for all scores that fp32 holds). workspace: as above. */
 SVDQ_API svdq_status svdq_attention_backward_workspace_bytes(const svdq_attention_desc* desc, size_t* out);
 SVDQ_API svdq_status svdq_attention_backward(const svdq_attention_desc* desc, const svdq_heads* dout, const svdq_heads* q,
                                              const svdq_heads* k, const svdq_heads* v, const svdq_heads* o,

@@ -147,6 +147,19 @@ def test_attention_arguments():
     assert afwd(attention(kv_heads=1), q=heads(head=1 << 28)) == SHAPE
 
 
+def test_scales_of_attention():
+    """The forward takes scales up to 2^64, the backward up to 2^10."""
+    got = H.run("""
+heads = ctypes.byref(S.Heads(P, 1 << 38, 24 * 128, 128))
+def both(scale):
+    d = ctypes.byref(S.AttentionDesc(0, 128, 8, 8, 0, scale, 1, 300, 300))
+    return [S.lib().svdq_attention_forward(d, heads, heads, heads, None, 0, heads, P, P, 1 << 40, None),
+            S.lib().svdq_attention_backward(d, heads, heads, heads, heads, heads, P, None, 0, heads, heads, heads, P, 1 << 40, None)]
+result = [both(2.0 ** e) for e in (-65, -64, 10, 11, 64, 65)]
+""")
+    assert got == [[SHAPE, SHAPE], [0, 0], [0, 0], [0, SHAPE], [0, SHAPE], [SHAPE, SHAPE]]
+
+
 def test_launches_and_workspaces():
     """Which kernels a call launches (over a stand-in for the runtime): grids
     within a dimension's limit at the largest sizes, a join where there are
