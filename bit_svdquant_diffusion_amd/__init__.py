@@ -848,8 +848,8 @@ def _norm_params(C, weight, bias, one_plus, eps, rows_per_group, M, dtype, group
     if rows_per_group is None:
         rows_per_group = M if groups == 1 and M > 0 else max(1, -(-M // max(1, groups)))
     dt = _dt(dtype)
-    return (_norm_desc(C, dt, dt if pdt is dtype else _dt(pdt), 1 if one_plus else 0, groups, eps, rows_per_group)[0], groups,
-            wp, ldw, bp, ldb)
+    return (_norm_desc(C, dt, dt if pdt is dtype else _dt(pdt), 1 if one_plus else 0, groups, float(eps), rows_per_group)[0],
+            groups, wp, ldw, bp, ldb)
 
 
 def _rows_like(x, shape, stream):
@@ -1194,8 +1194,8 @@ def _residual_setup(C, M, dtype, params, kind, post, alpha, eps, one_plus, rows_
     if code is None:
         raise ValueError("kind: layer or rms")
     dt = _dt(dtype)
-    d = _residual_desc(C, dt, dt if pdtype is dtype else _dt(pdtype), code, 1 if post else 0, 1 if one_plus else 0, groups, eps,
-                       alpha, rows_per_group)[0]
+    d = _residual_desc(C, dt, dt if pdtype is dtype else _dt(pdtype), code, 1 if post else 0, 1 if one_plus else 0, groups,
+                       float(eps), float(alpha), rows_per_group)[0]
     return d, _EIGHT(*at), groups, flat, rows_per_group, dt
 
 

@@ -228,3 +228,25 @@ def test_rope_frequencies():
     assert f.dtype == torch.float64 and torch.allclose(f, torch.tensor([1, 100 ** -0.25, 0.1, 100 ** -0.75, 1, 0.1]).double())
     f = S.rope_frequencies([4, 0, 2], 100.0, shared=True, device="cpu")
     assert torch.allclose(f, 100.0 ** -(torch.arange(6).double() / 6))
+
+
+def test_numbers_that_change_in_place():
+    """alpha and eps may be any number, also one that is written in place
+    between two calls: a descriptor is kept by value."""
+    torch = pytest.importorskip("torch")
+
+    def residual_of(alpha, eps):
+        d = S._residual_setup(64, 4, torch.bfloat16, (None,) * 4, "rms", False, alpha, eps, False, None)[0]
+        return ctypes.cast(d, ctypes.POINTER(S.ResidualDesc)).contents
+
+    def norm_of(eps):
+        d = S._norm_params(64, None, None, False, eps, None, 4, torch.bfloat16)[0]
+        return ctypes.cast(d, ctypes.POINTER(S.NormDesc)).contents
+
+    alpha, eps = torch.tensor(0.5), torch.tensor(0.25)
+    assert residual_of(alpha, eps).alpha == 0.5 and residual_of(alpha, eps).eps == 0.25 and norm_of(eps).eps == 0.25
+    alpha.fill_(2.0)
+    eps.fill_(1.0)
+    assert residual_of(alpha, eps).alpha == 2.0 and residual_of(alpha, eps).eps == 1.0 and norm_of(eps).eps == 1.0
+    with pytest.raises((TypeError, ValueError)):
+        residual_of("a", 0.0)
