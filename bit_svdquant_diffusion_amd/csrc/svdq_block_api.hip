@@ -290,6 +290,7 @@ svdq_status svdq_residual_norm_backward(const svdq_residual_desc* d, const void*
   g.lddx = lddx;
   g.dh = dh;
   g.lddh = lddh;
+  for (const void* in : {dy, ds, s, h}) g.in_place |= M > 0 && in && (in == dx || in == dh);
   g.gdtype = grad_dtype;
   g.part = need > 0 ? (float*)ws : nullptr;
   hipStream_t st = (hipStream_t)stream;

@@ -171,6 +171,7 @@ struct ResidualGradArgs {
   void* out[4];      // of gate, w, b, pw: [G][C] of gdtype, each may be null
   int gdtype;
   float* part;       // [G][runs][4][C], null when a group is one run
+  int in_place;      // dx or dh is an input
   int once;          // set by launch_residual_grad: the inputs are read past the caches
 };
 struct ResidualGradPlan;

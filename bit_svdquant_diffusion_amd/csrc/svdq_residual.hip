@@ -314,6 +314,12 @@ __global__ __launch_bounds__(64 * MAXW) void residual_bwd_kernel(ResidualGradArg
         }
       }
     if (base + teams < m_end) fetch(m + teams);
+    // Where dx or dh is an input: the vector that ends a row shares elements
+    // with the one before it, maybe another wave's, so all loads of the row
+    // have returned before the barrier behind which it is stored. (Always
+    // waiting for h and ds here: 5003 x 1283 fp16 with a norm after the block
+    // 35.2 us against 33.5.)
+    if (g.in_place) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     team_sum<2, LANES>(s, red[flip][0], wg_wave, team * W, W, lane);
     const float a1 = a.layer ? -(s[0] / fc) * rstd : 0.f, a2 = -(s[1] / fc) * rstd;
     s[0] = s[1] = 0.f;
