@@ -1214,6 +1214,61 @@ def _wants_grad(*tensors) -> bool:
     return False
 
 
+class _Shell:
+    """A tensor's elements as numpy sees them: addresses alone, nothing is read."""
+
+    def __init__(self, shape, strides, size, at):
+        self.__array_interface__ = {"version": 3, "typestr": f"|V{size}", "shape": tuple(shape), "data": (at, False),
+                                    "strides": tuple(size * step for step in strides)}
+
+
+def _span(t):
+    """A tensor's first byte and the one behind its last (of None: no bytes)."""
+    if t is None or t.numel() == 0:
+        return 0, 0
+    at = t.data_ptr()
+    if t.is_contiguous():
+        return at, at + t.nbytes
+    return at, at + (1 + sum((n - 1) * step for n, step in zip(t.shape, t.stride()))) * t.element_size()
+
+
+@functools.lru_cache(maxsize=1024)
+def _meet(shape, strides, size, shape1, strides1, size1, apart) -> bool:
+    """Whether elements of two tensors coincide, of which the second starts
+    `apart` bytes behind the first. (Slices of one buffer lie in one another's
+    span and need not; strides too unlike to tell in 10^4 steps count as apart.)"""
+    at = 1 << 48
+    try:
+        return bool(np.shares_memory(np.asarray(_Shell(shape, strides, size, at)),
+                                     np.asarray(_Shell(shape1, strides1, size1, at + apart)), max_work=10000))
+    except (np.exceptions if hasattr(np, "exceptions") else np).TooHardError:
+        return False
+
+
+def _same_places(a, b) -> bool:
+    return a.data_ptr() == b.data_ptr() and a.shape == b.shape and \
+        all(p == q for p, q, n in zip(a.stride(), b.stride(), a.shape) if n > 1)
+
+
+def _refuse_overlaps(outs, ins, over=()):
+    """The caller's outputs may not share memory with an input or with one
+    another; an output may be one of `over` itself. All are (name, tensor or
+    None)."""
+    others = [(name, t, *_span(t)) for name, t in (*outs, *ins, *over)]
+    first_over = len(outs) + len(ins)
+    for i, (name, t, lo, hi) in enumerate(others[:len(outs)]):
+        for j, (other, u, begin, end) in enumerate(others):
+            if begin >= hi or lo >= end or i >= j:
+                continue
+            if any(n > 1 and step == 0 for n, step in zip(t.shape, t.stride())):
+                continue   # (one that overlaps itself is the library's to refuse)
+            if j >= first_over and _same_places(t, u):
+                continue
+            if _meet(t.shape, t.stride(), t.element_size(), u.shape, u.stride(), u.element_size(),
+                     u.data_ptr() - t.data_ptr()):
+                raise ValueError(f"{name}: overlaps {other}" + (f" and is not {other} itself" if j >= first_over else ""))
+
+
 def residual_norm_forward(x, h, gate=None, weight=None, bias=None, post_weight=None, post_norm: bool = False,
                           kind: str = "layer", alpha: float = 1.0, eps: float = 1e-6, one_plus: bool = False,
                           rows_per_group=None, s=None, y=None, stream=None):
@@ -1227,7 +1282,7 @@ def residual_norm_forward(x, h, gate=None, weight=None, bias=None, post_weight=N
     groups of rows_per_group (default: the rows split evenly), of one type; with
     one_plus the gains are 1 + weight and 1 + post_weight. stats: float32
     [2 or 4 (rms: 1 or 2)][M], for residual_norm_backward. s and y may each be x
-    or h."""
+    or h; outputs that overlap otherwise are refused."""
     at = _on_device(x, h, s, y, gate, weight, bias, post_weight)
     if _wants_grad(x, h, gate, weight, bias, post_weight):
         _no_graph("residual_norm_forward")
@@ -1240,6 +1295,9 @@ def residual_norm_forward(x, h, gate=None, weight=None, bias=None, post_weight=N
         raise ValueError("h: the shape and type of x")
     d, p, _, _, _, _ = _residual_setup(C, M, x.dtype, (gate, weight, bias, post_weight), kind, post, alpha, eps, one_plus,
                                        rows_per_group)
+    if s is not None or y is not None:
+        _refuse_overlaps((("s", s), ("y", y)), (("gate", gate), ("weight", weight), ("bias", bias), ("post_weight", post_weight)),
+                         (("x", x), ("h", h)))
     s, y = _residual_out(s, x, "s", stream), _residual_out(y, x, "y", stream)
     stats = _empty(((2 if post else 1) * (2 if kind == "layer" else 1), M), _t.float32, x, stream)
     (sp, lds), (yp, ldy) = _rows(s, "s"), _rows(y, "y")
@@ -1276,6 +1334,9 @@ def residual_norm_backward(dy, s, h, stats, gate=None, weight=None, post_weight=
     if gdt is None:
         some = gate if gate is not None else weight if weight is not None else post_weight
         gdt = f32 if some is None else some.dtype
+    if dx is not None or dh is not None:
+        _refuse_overlaps((("dx", dx), ("dh", dh)), (("gate", gate), ("weight", weight), ("post_weight", post_weight), ("stats", stats)),
+                         (("dy", dy), ("ds", ds), ("s", s), ("h", h)))
     dx, dh = _residual_out(dx, s, "dx", stream), _residual_out(dh, s, "dh", stream)
     grads, out, ws, wsp, size = None, (None, None, None, None), None, None, 0
     if param_grads:
@@ -1352,7 +1413,7 @@ def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool 
     [samples][tokens][axes]; pairs: the pairs of each axis (up to four); freqs:
     float64 [sum of pairs] (rope_frequencies). interleaved: pairs (2 j, 2 j + 1),
     else (j, j + sum of pairs). inverse turns back, as the gradient does. q_out
-    and k_out may be q and k."""
+    and k_out may be q and k; outputs that overlap otherwise are refused."""
     at = _on_device(q, k, positions, freqs, q_out, k_out)
     if _wants_grad(q, k):
         _no_graph("rope")
@@ -1377,6 +1438,11 @@ def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool 
                          1 if inverse else 0, B, L)
     if not freqs.is_contiguous() or freqs.dtype != torch.float64 or freqs.shape != (n,):
         raise ValueError("freqs: contiguous float64, one for each pair")
+    if q_out is not None or k_out is not None:
+        places = (("positions", positions), ("freqs", freqs))
+        _refuse_overlaps((("q_out", q_out), ("k_out", k_out)), places)
+        _refuse_overlaps((("q_out", q_out),), (("k", k),), (("q", q),))
+        _refuse_overlaps((("k_out", k_out),), (("q", q),), (("k", k),))
     if q_out is None:
         q_out = _rows_like(q, shape, stream)
     qs, qo = _heads(q, "q", shape, dtype), _heads(q_out, "q_out", shape, dtype)
@@ -1439,7 +1505,8 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
     strides of 16 bytes). key_mask: bool or uint8 [samples][keys], true for the
     keys that take part; causal: query i sees the keys j <= i + keys - queries;
     scale: default head_dim^(-1/2). lse: float32 [samples][heads][queries]. A
-    query without keys has o = 0, lse = -inf. out must not overlap an input."""
+    query without keys has o = 0, lse = -inf. An out that overlaps an input is
+    refused."""
     at = _on_device(q, k, v, key_mask, out, workspace)
     if _wants_grad(q, k, v):
         _no_graph("attention_forward")
@@ -1447,6 +1514,8 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if out is None:
         out = _rows_like(q, shape, stream)
+    else:
+        _refuse_overlaps((("out", out),), (("q", q), ("k", k), ("v", v), ("key_mask", key_mask), ("workspace", workspace)))
     lse = _empty((shape[0], shape[2], shape[1]), _t.float32, q, stream)
     ws, wsp, size = _scratch(workspace, size, q, stream)
     keep, (a, b, c, o) = _all_heads(_heads(q, "q", shape, dtype), _heads(k, "k", kshape, dtype), _heads(v, "v", kshape, dtype),
@@ -1458,7 +1527,8 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
 def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = False, scale=None, dq=None, dk=None, dv=None,
                        workspace=None, stream=None):
     """svdq_attention_backward: (dq, dk, dv) for dout of o, from the forward's
-    inputs and its o and lse. They must not overlap an input or one another."""
+    inputs and its o and lse. Given ones that overlap an input or one another are
+    refused."""
     at = _on_device(q, dout, k, v, o, lse, key_mask, dq, dk, dv, workspace)
     if _wants_grad(dout):
         _no_graph("attention_backward")
@@ -1466,6 +1536,10 @@ def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = Fals
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if lse.dtype != _t.float32 or lse.shape != (shape[0], shape[2], shape[1]) or not lse.is_contiguous():
         raise ValueError("lse: float32 [samples][heads][queries]")
+    if dq is not None or dk is not None or dv is not None:
+        _refuse_overlaps((("dq", dq), ("dk", dk), ("dv", dv)),
+                         (("dout", dout), ("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse), ("key_mask", key_mask),
+                          ("workspace", workspace)))
     dq = _rows_like(q, shape, stream) if dq is None else dq
     dk = _rows_like(k, kshape, stream) if dk is None else dk
     dv = _rows_like(k, kshape, stream) if dv is None else dv
