@@ -688,8 +688,9 @@ SVDQ_API svdq_status svdq_fp8_quantize(const uint16_t* x, int64_t M, int32_t K, 
  * at p + group * ld, in elements. Sums are in fp32 from one read of the rows.
  * Strides and alignment as in the layer norm. Limits: 1 <= channels <= 8192,
  * 1 <= groups <= 2^24, rows_per_group >= 1, 0 <= M <= 2^24, M <= groups *
- * rows_per_group, eps >= 0, alpha finite. A row that holds an infinity or a
- * NaN gives NaN in that row alone (and in its group's parameter gradients).
+ * rows_per_group, eps >= 0, alpha finite. A value that is not
+ * finite spoils its own row alone (and its group's parameter gradients): all NaN,
+ * but for an infinity of an rms norm, whose other elements become 0.
  * ---------------------------------------------------------------------------
  */
 typedef enum { SVDQ_NORM_LAYER = 0, SVDQ_NORM_RMS = 1 } svdq_norm_kind;
@@ -814,9 +815,13 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * as two values of the type, the second what the first's rounding left. All
  * orders of summation are fixed by the sizes.
  * Keys and values that the mask drops, and the q and dout of queries that see
- * no key, are not used whatever they hold. A value that is not finite makes
- * every row that sees it NaN, and causal may also reach rows that do not see it
- * but lie in the same tile.
+ * no key, are not used whatever they hold. Other values that are not finite do
+ * what the formulas say: a NaN in q makes its row NaN, one in k every row that
+ * sees the key; an infinity in an element of v makes that element of o infinite
+ * (or NaN, where probabilities are two values) in the rows that see it; a score
+ * of -infinity is a key without weight. Causal, one in v (for the gradients also
+ * in k, q or dout) may reach rows and keys that do not see each other but lie in
+ * one tile.
  * Limits: head_dim a multiple of 8 up to 128; 1 <= kv_heads, heads a multiple
  * of kv_heads, samples * kv_heads <= 65535; queries * heads / kv_heads < 2^30
  * and keys < 2^30; blocks of 128 of those times samples * kv_heads <= 2^22;
