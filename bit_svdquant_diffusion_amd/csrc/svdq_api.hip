@@ -27,13 +27,15 @@ std::atomic<int> g_dev_state[kMaxDevices];   // 0 unknown, 1 gfx950 ready, 2 uns
 std::atomic<int> g_dev_cus[kMaxDevices];     // compute units of each ready device
 std::atomic<void*> g_dev_scratch[kMaxDevices];   // device address of `scratch` on each ready device
 std::atomic<unsigned> g_dev_kernels[kMaxDevices];   // KernelSets that are ready on each ready device
+std::atomic<bool> g_dev_attention[kMaxDevices];   // attention's set has been set up, or has failed to be
 std::mutex g_dev_mu;
 
 }  // namespace
 
 // One-time set-up per device, with that device current: the gfx950 check,
 // the kernels' LDS attributes and the address of this device's `scratch`. A
-// kernel set whose set-up fails stops the calls that name it alone.
+// kernel set whose set-up fails stops the calls that name it alone. Attention's
+// set, of 150 kernels, takes 3.5 ms and waits for the first call that names it.
 svdq_status check_device(int* cus, void** scratch_ptr, unsigned kernels) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return SVDQ_ERR_DEVICE;
@@ -51,14 +53,23 @@ svdq_status check_device(int* cus, void** scratch_ptr, unsigned kernels) {
       s = ok ? 1 : 2;
       if (ok) {
         const unsigned sets =
-            (prepare_norm() == hipSuccess ? kKernelsNorm : 0) | (prepare_fp8() == hipSuccess ? kKernelsFp8 : 0) |
-            (prepare_attention() == hipSuccess && prepare_attention_grad() == hipSuccess ? kKernelsAttention : 0);
-        if (sets != (kKernelsNorm | kKernelsFp8 | kKernelsAttention)) (void)hipGetLastError();   // not the next launch's error
+            (prepare_norm() == hipSuccess ? kKernelsNorm : 0) | (prepare_fp8() == hipSuccess ? kKernelsFp8 : 0);
+        if (sets != (kKernelsNorm | kKernelsFp8)) (void)hipGetLastError();   // not the next launch's error
         g_dev_kernels[dev].store(sets, std::memory_order_relaxed);
         g_dev_cus[dev].store(p.multiProcessorCount, std::memory_order_relaxed);
         g_dev_scratch[dev].store(sp, std::memory_order_relaxed);
       }
       g_dev_state[dev].store(s, std::memory_order_release);
+    }
+  }
+  if (s == 1 && (kernels & kKernelsAttention) && !g_dev_attention[dev].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(g_dev_mu);
+    if (!g_dev_attention[dev].load(std::memory_order_acquire)) {
+      if (prepare_attention() == hipSuccess && prepare_attention_grad() == hipSuccess)
+        g_dev_kernels[dev].fetch_or(kKernelsAttention, std::memory_order_relaxed);
+      else
+        (void)hipGetLastError();
+      g_dev_attention[dev].store(true, std::memory_order_release);
     }
   }
   if (s != 1 || (kernels & ~g_dev_kernels[dev].load(std::memory_order_relaxed))) return SVDQ_ERR_DEVICE;

@@ -34,3 +34,14 @@ def test_attention_kernels_that_refuse_their_attributes(refused, stopped):
     got = H.run(_CALLS + f"refuse({refused!r})\nresult = {{n: [globals()[n](), len(launches())] for n in names * 2}}")
     for name, (status, n) in got.items():
         assert (status, n == 0) == ((DEVICE, True) if name in stopped else (0, False)), (name, status, n)
+
+
+def test_attention_is_set_up_by_its_own_calls():
+    """What attention's kernels refuse at another call's time does not count."""
+    got = H.run(_CALLS + """
+refuse("attn_")
+result = [norm(), residual(), rope()]
+refuse("nothing")
+result += [attention(), attention_grad(), len(launches())]
+""")
+    assert got[:5] == [0] * 5 and got[5] >= 5
