@@ -146,12 +146,11 @@ __device__ __forceinline__ u32x4 rows_resource(const void* base, int bytes) {
   return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)bytes, 0x00020000u};
 }
 
-// all but the last N transfers have arrived and all LDS reads returned, then
-// the workgroup's barrier; nothing moves across
-template <int N = 0>
+// all transfers have arrived and all LDS reads returned, then the workgroup's
+// barrier; nothing moves across
 __device__ __forceinline__ void tile_barrier() {
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));   // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 }

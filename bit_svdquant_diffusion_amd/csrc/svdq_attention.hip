@@ -4,7 +4,7 @@
 //   lse = m + log sum exp(s_j - m).
 //
 // One pass over the keys with the running maximum and sum: a workgroup holds
-// 32 NB query rows a wave, K and V pass by in tiles of 64 keys. The product is
+// 32 query rows a wave, K and V pass by in tiles of 64 keys. The product is
 // taken as S^T = K Q^T, so that a lane's registers hold one query's scores:
 // the maximum and the sum are the lane's own but for one exchange between the
 // half waves, and exp(S^T) is in the right registers to be the operand B of
@@ -33,8 +33,7 @@ __device__ __forceinline__ float reference_off(float m, float base, float scale_
   return m == -__builtin_inff() || __builtin_fabsf(base) > kFarScore ? 0.f : __builtin_fmaf(m, scale_log2, -base);
 }
 
-// W waves of NB blocks of 32 query rows, KW times (each way takes every KW-th
-// tile); DP the padded head; NP operands for probabilities. Two waves a SIMD
+// W waves of 32 query rows, KW times (each way takes every KW-th tile); DP the padded head; NP operands for probabilities. Two waves a SIMD
 // (up to 256 registers), so that one's products run under the other's
 // exponentials: 4608 tokens, 24 heads of 128 with a mask 250 us (1.04
 // PFLOP/s), with one wave a SIMD 411, with one of two blocks 355, with
@@ -43,7 +42,7 @@ __device__ __forceinline__ float reference_off(float m, float base, float scale_
 // products the matrix unit (40% of the cycles), at a clock that power holds
 // near 2 GHz; LDS is busy a fifth of the time. One query over 65536 keys
 // streams its cache at 5.5 TB/s.
-template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
+template <typename T, int DP, int W, int KW, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   constexpr int NT = TL::kTransfers / W;   // transfers of a wave for one tile
@@ -71,24 +70,20 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch : nullptr;
 
   // this lane's rows and the last keys that they see
-  const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
-  u32x4 qf[NB][TL::kSteps];
-  int last[NB];   // of a row without keys (and past the last row) below 0
+  const int r0 = at.block * (32 * W) + wave * 32;
+  u32x4 qf[TL::kSteps];
+  const int r = r0 + lr, query = attn_query(a.group, r), g = r - query * G;
+  const T* q_row = qp + (int64_t)query * a.q.token + (int64_t)g * a.q.head;
+  const int last = r >= R ? -1 : a.causal ? min(query + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;   // of a row without keys below 0
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r);
-    const T* row = qp + (int64_t)i * a.q.token + (int64_t)(r - i * G) * a.q.head;
-    last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
-#pragma unroll
-    for (int s = 0; s < TL::kSteps; ++s) {
-      const int d = 16 * s + 8 * h;
-      qf[n][s] = r < R && d < D ? *reinterpret_cast<const u32x4*>(row + d) : u32x4{0, 0, 0, 0};
-    }
+  for (int s = 0; s < TL::kSteps; ++s) {
+    const int d = 16 * s + 8 * h;
+    qf[s] = r < R && d < D ? *reinterpret_cast<const u32x4*>(q_row + d) : u32x4{0, 0, 0, 0};
   }
   const int k_begin = (at.first + way) * kAttnRows, k_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   // what every and what any row of this wave sees
   const int w_first = a.causal ? attn_query(a.group, r0) + a.Lk - a.Lq : a.Lk - 1;
-  const int w_last = r0 >= R ? -1 : a.causal ? attn_query(a.group, min(r0 + 32 * NB, R) - 1) + a.Lk - a.Lq : a.Lk - 1;
+  const int w_last = r0 >= R ? -1 : a.causal ? attn_query(a.group, min(r0 + 32, R) - 1) + a.Lk - a.Lq : a.Lk - 1;
 
   auto fetch = [&](int k0, int stage, uint64_t keep) {
     const int rows = min(kAttnRows, a.Lk - k0);
@@ -122,17 +117,11 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   // probability is one fused product. Where that is far from zero its rounding
   // is no longer small beside 1: there (far: a row of the wave) the reference
   // is m scale_log2 itself, and m is subtracted before the scale.
-  f32x16 o[TL::kBlocks][NB];
-  float m[NB], base[NB], l[NB];
-  bool far[NB];
+  f32x16 o[TL::kBlocks];
+  float m = -__builtin_inff(), base = 0.f, l = 0.f;
+  bool far = false;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    m[n] = -__builtin_inff();
-    base[n] = l[n] = 0.f;
-    far[n] = false;
-#pragma unroll
-    for (int i = 0; i < TL::kBlocks; ++i) o[i][n] = f32x16{};
-  }
+  for (int i = 0; i < TL::kBlocks; ++i) o[i] = f32x16{};
   uint64_t now, keep = 0;   // which keys of the tile, and of the next, take part
   int next_byte = 0;
   constexpr int kStep = KW * kAttnRows;
@@ -151,79 +140,71 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     }
     const uint8_t *tk = smem + (way * 2 + (t & 1)) * 2 * TL::kBytes, *tv = tk + TL::kBytes;
     if (k0 > w_last || now == 0 || (KW > 1 && k0 >= k_end)) continue;   // nothing that this wave's rows see
-    f32x16 s[2][NB];
+    f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) s[kb][n] = f32x16{};
+      s[kb] = f32x16{};
 #pragma unroll
     for (int st = 0; st < TL::kSteps; ++st)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         const u32x4 kf = TL::straight(tk, pl, kb, st);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) s[kb][n] = mma<T>(kf, qf[n][st], s[kb][n]);
+        s[kb] = mma<T>(kf, qf[st], s[kb]);
       }
-    sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
+    sched_products<2 * TL::kSteps, 2 * TL::kSteps, 1, 4>();
     if (now != ~0ull || k0 + kAttnRows - 1 > w_first) {
+      const int lim = last - k0 - 4 * h;
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int lim = last[n] - k0 - 4 * h;
+      for (int kb = 0; kb < 2; ++kb) {
+        const uint32_t bits = (uint32_t)(now >> (32 * kb)) >> (4 * h);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const uint32_t bits = (uint32_t)(now >> (32 * kb)) >> (4 * h);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = 8 * (i / 4) + i % 4;
-            s[kb][n][i] = (bits >> c & 1) && 32 * kb + c <= lim ? s[kb][n][i] : -__builtin_inff();
-          }
+        for (int i = 0; i < 16; ++i) {
+          const int c = 8 * (i / 4) + i % 4;
+          s[kb][i] = (bits >> c & 1) && 32 * kb + c <= lim ? s[kb][i] : -__builtin_inff();
         }
       }
     }
-    u32x4 p[4][NB][NP];
+    u32x4 p[4][NP];
+    float top = s[0][0];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      float top = s[0][n][0];
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kb][i]);
+    top = max_halves(top);
+    // The maximum that is subtracted follows the true one when that is more
+    // than 8 (in base 2) above it: up to there the probabilities stay below
+    // 2^8, which neither the sums nor either type's rounding minds, and most
+    // tiles leave the accumulators as they are.
+    if (__any((top - m) * a.scale_log2 > 8.f)) {
+      const float mn = __builtin_fmaxf(m, top), bn = reference(mn, a.scale_log2);
+      const float step = (m - mn) * a.scale_log2 + (reference_off(mn, bn, a.scale_log2) - reference_off(m, base, a.scale_log2));
+      const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(step);
+      m = mn;
+      base = bn;
+      far = __any(__builtin_fabsf(bn) > kFarScore);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < TL::kBlocks; ++i) o[i] *= f;
+    }
+    float sub = base;
+    if (far) {
+      const bool before = __builtin_fabsf(sub) > kFarScore;   // (this row's)
+      const float off = before ? m : 0.f;
+      sub = before ? 0.f : sub;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kb][n][i]);
-      top = max_halves(top);
-      // The maximum that is subtracted follows the true one when that is more
-      // than 8 (in base 2) above it: up to there the probabilities stay below
-      // 2^8, which neither the sums nor either type's rounding minds, and most
-      // tiles leave the accumulators as they are.
-      if (__any((top - m[n]) * a.scale_log2 > 8.f)) {
-        const float mn = __builtin_fmaxf(m[n], top), bn = reference(mn, a.scale_log2);
-        const float step = (m[n] - mn) * a.scale_log2 + (reference_off(mn, bn, a.scale_log2) - reference_off(m[n], base[n], a.scale_log2));
-        const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(step);
-        m[n] = mn;
-        base[n] = bn;
-        far[n] = __any(__builtin_fabsf(bn) > kFarScore);
-        l[n] *= f;
+        for (int i = 0; i < 16; ++i) s[kb][i] -= off;
+    }
 #pragma unroll
-        for (int i = 0; i < TL::kBlocks; ++i) o[i][n] *= f;
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], a.scale_log2, -sub));
+        l += s[kb][i];
       }
-      float sub = base[n];
-      if (far[n]) {
-        const bool before = __builtin_fabsf(sub) > kFarScore;   // (this row's)
-        const float off = before ? m[n] : 0.f;
-        sub = before ? 0.f : sub;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[kb][n][i] -= off;
-      }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[kb][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][n][i], a.scale_log2, -sub));
-          l[n] += s[kb][n][i];
-        }
-        as_operands<T>(s[kb][n], 0, p[2 * kb][n]);
-        as_operands<T>(s[kb][n], 1, p[2 * kb + 1][n]);
-      }
+      as_operands<T>(s[kb], 0, p[2 * kb]);
+      as_operands<T>(s[kb], 1, p[2 * kb + 1]);
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
@@ -231,15 +212,11 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
       for (int i = 0; i < TL::kBlocks; ++i) {
         const u32x4 vf = TL::turned(tv, pl, kt, i);
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int w = 0; w < NP; ++w) o[i][n] = mma<T>(vf, p[kt][n][w], o[i][n]);
+        for (int w = 0; w < NP; ++w) o[i] = mma<T>(vf, p[kt][w], o[i]);
       }
-    sched_products<4 * TL::kBlocks * NB * NP, 8 * TL::kBlocks, 2, 8>();
+    sched_products<4 * TL::kBlocks * NP, 8 * TL::kBlocks, 2, 8>();
   }
-  float lo[NB];   // what the reference of the sums is below m scale_log2
-#pragma unroll
-  for (int n = 0; n < NB; ++n) lo[n] = reference_off(m[n], base[n], a.scale_log2);
+  float lo = reference_off(m, base, a.scale_log2);   // what the reference of the sums is below m scale_log2
   if constexpr (KW > 1) {   // the second way's results join the first's
     f32x4* box = reinterpret_cast<f32x4*>(smem) + wave * (4 * TL::kBlocks * 64) + lane;
     f32x4* stat = reinterpret_cast<f32x4*>(smem + W * TL::kBlocks * 4096) + wave * 64 + lane;
@@ -249,60 +226,56 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
       for (int i = 0; i < TL::kBlocks; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          box[(4 * i + q) * 64] = f32x4{o[i][0][4 * q], o[i][0][4 * q + 1], o[i][0][4 * q + 2], o[i][0][4 * q + 3]};
-      *stat = f32x4{m[0], l[0], lo[0], 0.f};
+          box[(4 * i + q) * 64] = f32x4{o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]};
+      *stat = f32x4{m, l, lo, 0.f};
     }
     tile_barrier();
     if (way == 1) return;
     const f32x4 other = *stat;
-    const float top = __builtin_fmaxf(m[0], other[0]), from = top == -__builtin_inff() ? 0.f : top;
-    const float f = __builtin_amdgcn_exp2f((m[0] - from) * a.scale_log2 - lo[0]);
+    const float top = __builtin_fmaxf(m, other[0]), from = top == -__builtin_inff() ? 0.f : top;
+    const float f = __builtin_amdgcn_exp2f((m - from) * a.scale_log2 - lo);
     const float fo = __builtin_amdgcn_exp2f((other[0] - from) * a.scale_log2 - other[2]);
-    m[0] = top;
-    base[0] = reference(top, a.scale_log2);
-    lo[0] = 0.f;
-    l[0] = l[0] * f + other[1] * fo;
+    m = top;
+    base = reference(top, a.scale_log2);
+    lo = 0.f;
+    l = l * f + other[1] * fo;
 #pragma unroll
     for (int i = 0; i < TL::kBlocks; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const f32x4 v = box[(4 * i + q) * 64];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][0][4 * q + k] = o[i][0][4 * q + k] * f + v[k] * fo;
+        for (int k = 0; k < 4; ++k) o[i][4 * q + k] = o[i][4 * q + k] * f + v[k] * fo;
       }
   }
+  const float sum = sum_halves(l);
+  const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = base + __builtin_log2f(sum);   // (no key: -inf)
+  if (r >= R) return;
+  if (PARTS && !at.whole) {
+    const int64_t row = (int64_t)place * a.part_rows + r - at.block * (32 * W);
+    if (h == 0) reinterpret_cast<f32x2*>(a.part_stat)[row] = f32x2{m, sum * __builtin_amdgcn_exp2f(-lo)};
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), g = r - i * G;
-    const float sum = sum_halves(l[n]);
-    const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = base[n] + __builtin_log2f(sum);   // (no key: -inf)
-    if (r >= R) continue;
-    if (PARTS && !at.whole) {
-      const int64_t row = (int64_t)place * a.part_rows + r - at.block * (32 * NB * W);
-      if (h == 0) reinterpret_cast<f32x2*>(a.part_stat)[row] = f32x2{m[n], sum * __builtin_amdgcn_exp2f(-lo[n])};
+    for (int blk = 0; blk < TL::kBlocks; ++blk)
 #pragma unroll
-      for (int blk = 0; blk < TL::kBlocks; ++blk)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int d = 32 * blk + 8 * q + 4 * h;
-          if (d < D)
-            *reinterpret_cast<f32x4*>(a.part + row * D + d) =
-                f32x4{o[blk][n][4 * q], o[blk][n][4 * q + 1], o[blk][n][4 * q + 2], o[blk][n][4 * q + 3]} * f;
-        }
-      continue;
-    }
-    const int head = hk * G + g;
-    if (h == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + i] = lse2 * kLn2;
-    T* row = static_cast<T*>(a.o.p) + b * a.o.batch + i * a.o.token + head * a.o.head;
-#pragma unroll
-    for (int blk = 0; blk < TL::kBlocks; ++blk) {
-      u32x4 c[2];
-      head_chunks<T>(o[blk][n], f, c);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int d = 32 * blk + 16 * q + 8 * h;
-        if (d < D) *reinterpret_cast<u32x4*>(row + d) = c[q];
+      for (int q = 0; q < 4; ++q) {
+        const int d = 32 * blk + 8 * q + 4 * h;
+        if (d < D)
+          *reinterpret_cast<f32x4*>(a.part + row * D + d) =
+              f32x4{o[blk][4 * q], o[blk][4 * q + 1], o[blk][4 * q + 2], o[blk][4 * q + 3]} * f;
       }
+    return;
+  }
+  const int head = hk * G + g;
+  if (h == 0) a.lse[((int64_t)b * a.H + head) * a.Lq + query] = lse2 * kLn2;
+  T* row = static_cast<T*>(a.o.p) + b * a.o.batch + query * a.o.token + head * a.o.head;
+#pragma unroll
+  for (int blk = 0; blk < TL::kBlocks; ++blk) {
+    u32x4 c[2];
+    head_chunks<T>(o[blk], f, c);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int d = 32 * blk + 16 * q + 8 * h;
+      if (d < D) *reinterpret_cast<u32x4*>(row + d) = c[q];
     }
   }
 }
@@ -375,7 +348,7 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
     if (a.plan.each) {
       AttnParts deal;
       attn_parts(a.cost, a.plan, &deal);
-      hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, KW, 1, NP, true>), grid, block, (kFwdLds<DP, KW>), st, a, deal);
+      hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, KW, NP, true>), grid, block, (kFwdLds<DP, KW>), st, a, deal);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       AttnJoins joins;
@@ -389,7 +362,7 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((attn_join_kernel<T, 1>), rows, dim3(256), 0, st, a, joins);
       return hipGetLastError();
     }
-  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, KW, 1, NP, false>), grid, block, (kFwdLds<DP, KW>), st, a, AttnUnits{});
+  hipLaunchKernelGGL((attn_fwd_kernel<T, DP, W, KW, NP, false>), grid, block, (kFwdLds<DP, KW>), st, a, AttnUnits{});
   return hipGetLastError();
 }
 template <typename T, int DP>
@@ -413,9 +386,9 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t st) {
 
 template <typename T, int DP, int W, int KW, int NP>
 hipError_t prepare_fwd() {
-  hipError_t e = attn_shared_memory((const void*)attn_fwd_kernel<T, DP, W, KW, 1, NP, false>, kFwdLds<DP, KW>);
+  hipError_t e = attn_shared_memory((const void*)attn_fwd_kernel<T, DP, W, KW, NP, false>, kFwdLds<DP, KW>);
   if constexpr (kAttnCut<W, KW>)
-    if (e == hipSuccess) e = attn_shared_memory((const void*)attn_fwd_kernel<T, DP, W, KW, 1, NP, true>, kFwdLds<DP, KW>);
+    if (e == hipSuccess) e = attn_shared_memory((const void*)attn_fwd_kernel<T, DP, W, KW, NP, true>, kFwdLds<DP, KW>);
   return e;
 }
 template <typename T, int DP>

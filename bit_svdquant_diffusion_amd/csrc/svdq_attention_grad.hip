@@ -4,8 +4,8 @@
 //   dv = p^T do,  dk = scale ds^T q,  dq = scale ds k.
 //
 // Two passes over the scores, each with its results in registers, so that no
-// sum is joined by atomics and every order is fixed: one holds 32 NB keys a
-// wave (dk, dv) while the query rows pass by in tiles of 64, one holds 32 NB
+// sum is joined by atomics and every order is fixed: one holds 32 keys a
+// wave (dk, dv) while the query rows pass by in tiles of 64, one holds 32
 // query rows (dq) while the keys do. That is seven products instead of five,
 // against a float of traffic per pair of a row and a tile of keys for joining
 // dq. As in the forward, the products whose results are the next ones'
@@ -102,40 +102,39 @@ __device__ __forceinline__ float ds_scale(int D, float x, float y) {
 }
 
 // The second way's results join the first's through LDS, I-th of a wave's sums.
-template <int DP, int W, int I, int NB>
+template <int DP, int W, int I>
 __device__ __forceinline__ f32x4* join_place(uint8_t* smem, int wave, int lane) {
-  static_assert(NB == 1, "");
   return reinterpret_cast<f32x4*>(smem) + (I * W + wave) * (AttnTile<DP>::kBlocks * 256) + lane;
 }
-template <int DP, int W, int I, int NB>
-__device__ __forceinline__ void join_put(uint8_t* smem, int wave, int lane, const f32x16 (&v)[AttnTile<DP>::kBlocks][NB]) {
-  f32x4* to = join_place<DP, W, I, NB>(smem, wave, lane);
+template <int DP, int W, int I>
+__device__ __forceinline__ void join_put(uint8_t* smem, int wave, int lane, const f32x16 (&v)[AttnTile<DP>::kBlocks]) {
+  f32x4* to = join_place<DP, W, I>(smem, wave, lane);
 #pragma unroll
   for (int i = 0; i < AttnTile<DP>::kBlocks; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      to[(4 * i + q) * 64] = f32x4{v[i][0][4 * q], v[i][0][4 * q + 1], v[i][0][4 * q + 2], v[i][0][4 * q + 3]};
+      to[(4 * i + q) * 64] = f32x4{v[i][4 * q], v[i][4 * q + 1], v[i][4 * q + 2], v[i][4 * q + 3]};
 }
-template <int DP, int W, int I, int NB>
-__device__ __forceinline__ void join_add(uint8_t* smem, int wave, int lane, f32x16 (&v)[AttnTile<DP>::kBlocks][NB]) {
-  const f32x4* from = join_place<DP, W, I, NB>(smem, wave, lane);
+template <int DP, int W, int I>
+__device__ __forceinline__ void join_add(uint8_t* smem, int wave, int lane, f32x16 (&v)[AttnTile<DP>::kBlocks]) {
+  const f32x4* from = join_place<DP, W, I>(smem, wave, lane);
 #pragma unroll
   for (int i = 0; i < AttnTile<DP>::kBlocks; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const f32x4 x = from[(4 * i + q) * 64];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[i][0][4 * q + k] += x[k];
+      for (int k = 0; k < 4; ++k) v[i][4 * q + k] += x[k];
     }
 }
 
-// dk and dv of 32 NB keys a wave; the query rows pass by. With heads of 128
+// dk and dv of 32 keys a wave; the query rows pass by. With heads of 128
 // the accumulators and the K fragments take 160 of the 256 registers that two
 // waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads, of
 // the same step: 574 us against 760 with V in registers, of which 53 spill, 768
 // with one wave a SIMD and two blocks of keys, 870 with workgroups of four
 // waves; now 535, 0.98 PFLOP/s, with the matrix unit busy 43% of the cycles).
-template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
+template <typename T, int DP, int W, int KW, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
@@ -162,30 +161,25 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   const float dsc = c / kProbScale, fk = a.scale / c;   // the factor of ds (of fp16 probabilities); of dk
 
   // this lane's keys, as operand B (of both products that give scores)
-  const int key0 = at.block * (32 * NB * W) + wave * (32 * NB);
-  u32x4 kf[NB][TL::kSteps], vf[kHoldV ? NB : 1][TL::kSteps];
-  bool live[NB];
-  int first[NB];   // the first row that sees the key
+  const int key0 = at.block * (32 * W) + wave * 32;
+  u32x4 kf[TL::kSteps], vf[TL::kSteps];
+  const int key = key0 + lr;
+  const bool live = key < a.Lk && (!a.mask || a.mask[b * a.mask_batch + key]);
+  const int first = a.causal ? max(key - (a.Lk - a.Lq), 0) * G : 0;   // the first row that sees the key
+  const T* kr = static_cast<const T*>(a.k.p) + b * a.k.batch + key * a.k.token + hk * a.k.head;
+  const T* vr = static_cast<const T*>(a.v.p) + b * a.v.batch + key * a.v.token + hk * a.v.head;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int key = key0 + 32 * n + lr;
-    live[n] = key < a.Lk && (!a.mask || a.mask[b * a.mask_batch + key]);
-    first[n] = a.causal ? max(key - (a.Lk - a.Lq), 0) * G : 0;
-    const T* kr = static_cast<const T*>(a.k.p) + b * a.k.batch + key * a.k.token + hk * a.k.head;
-    const T* vr = static_cast<const T*>(a.v.p) + b * a.v.batch + key * a.v.token + hk * a.v.head;
-#pragma unroll
-    for (int s = 0; s < TL::kSteps; ++s) {
-      const int d = 16 * s + 8 * h;
-      const bool in = live[n] && d < D;
-      kf[n][s] = in ? *reinterpret_cast<const u32x4*>(kr + d) : u32x4{0, 0, 0, 0};
-      const u32x4 v = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
-      if constexpr (kHoldV)
-        vf[n][s] = v;
-      else   // (read by this wave alone)
-        *reinterpret_cast<u32x4*>(held + (wave * NB + n) * 32 * TL::kRowBytes + (pl.straight ^ (s << 5))) = v;
-    }
+  for (int s = 0; s < TL::kSteps; ++s) {
+    const int d = 16 * s + 8 * h;
+    const bool in = live && d < D;
+    kf[s] = in ? *reinterpret_cast<const u32x4*>(kr + d) : u32x4{0, 0, 0, 0};
+    const u32x4 v = in ? *reinterpret_cast<const u32x4*>(vr + d) : u32x4{0, 0, 0, 0};
+    if constexpr (kHoldV)
+      vf[s] = v;
+    else   // (read by this wave alone)
+      *reinterpret_cast<u32x4*>(held + wave * 32 * TL::kRowBytes + (pl.straight ^ (s << 5))) = v;
   }
-  const uint8_t* my_v = held + (kHoldV ? 0 : wave * NB * 32 * TL::kRowBytes);
+  const uint8_t* my_v = held + (kHoldV ? 0 : wave * 32 * TL::kRowBytes);
   // rows that see no key at all are read as zeros
   int dead = 0;
   if (a.causal) {
@@ -200,7 +194,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   }
   const int r_begin = (at.first + way) * kAttnRows, r_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   const int w_first = a.causal ? max(key0 - (a.Lk - a.Lq), 0) * G : 0;
-  const int w_all = a.causal ? max(key0 + 32 * NB - 1 - (a.Lk - a.Lq), 0) * G : 0;   // from here on rows see all of the wave's keys
+  const int w_all = a.causal ? max(key0 + 31 - (a.Lk - a.Lq), 0) * G : 0;   // from here on rows see all of the wave's keys
 
   auto fetch = [&](int row0, int stage) {
     const int i0 = attn_query(a.group, row0), i1 = attn_query(a.group, min(row0 + kAttnRows, R) - 1);
@@ -222,11 +216,10 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     }
   };
 
-  f32x16 dk[TL::kBlocks][NB], dv[TL::kBlocks][NB];
+  f32x16 dk[TL::kBlocks], dv[TL::kBlocks];
 #pragma unroll
   for (int i = 0; i < TL::kBlocks; ++i)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) dk[i][n] = dv[i][n] = f32x16{};
+    dk[i] = dv[i] = f32x16{};
   constexpr int kStep = KW * kAttnRows;
   if (r_begin < r_end) fetch(r_begin, 0);
   for (int t = 0, row0 = r_begin; t < rounds; ++t, row0 += kStep) {
@@ -240,16 +233,14 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
       if (row0 + 32 * rb + 31 < w_first) continue;   // none of these rows sees a key of this wave
       // The scores' accumulators start with -lse / scale, those of do v^T with
       // -delta, each row's in its registers.
-      f32x16 s[NB], dp[NB];
-      u32x4 p[2][NB][NP];
-      auto start = [&](const float* rows, f32x16(&to)[NB]) {
+      f32x16 s, dp;
+      u32x4 p[2][NP];
+      auto start = [&](const float* rows, f32x16& to) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f32x4 v = *reinterpret_cast<const f32x4*>(rows + 32 * rb + 8 * q + 4 * h);
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) to[n][4 * q + i] = v[i];
+          for (int i = 0; i < 4; ++i) to[4 * q + i] = v[i];
         }
       };
       const bool part = row0 + 32 * rb < w_all;
@@ -257,69 +248,55 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
         const u32x4 qf = TL::straight(tq, pl, rb, st);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) s[n] = mma<T>(qf, kf[n][st], s[n]);
+        s = mma<T>(qf, kf[st], s);
       }
-      sched_products<TL::kSteps * NB, 4 + TL::kSteps, 1, 8>();
+      sched_products<TL::kSteps, 4 + TL::kSteps, 1, 8>();
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+      for (int i = 0; i < 16; ++i)
+        s[i] = __builtin_amdgcn_exp2f(kScaled<T> ? __builtin_fmaf(s[i], a.scale_log2, 10.f) : s[i] * a.scale_log2);
+      if (part) {
+        const int lim = first - row0 - 32 * rb - 4 * h;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[n][i] = __builtin_amdgcn_exp2f(kScaled<T> ? __builtin_fmaf(s[n][i], a.scale_log2, 10.f) : s[n][i] * a.scale_log2);
-        if (part) {
-          const int lim = first[n] - row0 - 32 * rb - 4 * h;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[n][i] = 8 * (i / 4) + i % 4 >= lim ? s[n][i] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) as_operands<T>(s[n], u, p[u][n]);
+        for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 >= lim ? s[i] : 0.f;
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) as_operands<T>(s, u, p[u]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < TL::kBlocks; ++i) {
           const u32x4 df = TL::turned(td, pl, 2 * rb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int w = 0; w < NP; ++w) dv[i][n] = mma<T>(df, p[u][n][w], dv[i][n]);
+          for (int w = 0; w < NP; ++w) dv[i] = mma<T>(df, p[u][w], dv[i]);
         }
       start(tD, dp);
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
         const u32x4 df = TL::straight(td, pl, rb, st);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          if constexpr (kHoldV)
-            dp[n] = mma<T>(df, vf[n][st], dp[n]);
-          else
-            dp[n] = mma<T>(df, TL::straight(my_v, pl, n, st), dp[n]);
-        }
+        if constexpr (kHoldV)
+          dp = mma<T>(df, vf[st], dp);
+        else
+          dp = mma<T>(df, TL::straight(my_v, pl, 0, st), dp);
       }
-      sched_products<(2 * TL::kBlocks * NP + TL::kSteps) * NB, 4 * TL::kBlocks + (kHoldV ? 1 : 2) * TL::kSteps, 2, 4>();
+      sched_products<2 * TL::kBlocks * NP + TL::kSteps, 4 * TL::kBlocks + (kHoldV ? 1 : 2) * TL::kSteps, 2, 4>();
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+      for (int i = 0; i < 16; ++i) dp[i] *= kScaled<T> ? s[i] * dsc : s[i];
+      if (part) {   // (do may hold what times 0 is NaN)
+        const int lim = first - row0 - 32 * rb - 4 * h;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dp[n][i] *= kScaled<T> ? s[n][i] * dsc : s[n][i];
-        if (part) {   // (do may hold what times 0 is NaN)
-          const int lim = first[n] - row0 - 32 * rb - 4 * h;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dp[n][i] = 8 * (i / 4) + i % 4 >= lim ? dp[n][i] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) as_operands<T>(dp[n], u, p[u][n]);
+        for (int i = 0; i < 16; ++i) dp[i] = 8 * (i / 4) + i % 4 >= lim ? dp[i] : 0.f;
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) as_operands<T>(dp, u, p[u]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < TL::kBlocks; ++i) {
           const u32x4 qf = TL::turned(tq, pl, 2 * rb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int w = 0; w < NP; ++w) dk[i][n] = mma<T>(qf, p[u][n][w], dk[i][n]);
+          for (int w = 0; w < NP; ++w) dk[i] = mma<T>(qf, p[u][w], dk[i]);
         }
-      sched_products<2 * TL::kBlocks * NB * NP, 4 * TL::kBlocks, 2, 4>();
+      sched_products<2 * TL::kBlocks * NP, 4 * TL::kBlocks, 2, 4>();
     }
   }
   if constexpr (KW > 1) {
@@ -335,51 +312,47 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     join_add<DP, W, 1>(smem, wave, lane, dv);
   }
   const float fv = kScaled<T> ? 1.f / kProbScale : 1.f;
+  if (key >= a.Lk) return;
+  if (PARTS && !at.whole) {
+    float* row = a.part + ((int64_t)place * a.part_rows + key - at.block * (32 * W)) * 2 * D;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int key = key0 + 32 * n + lr;
-    if (key >= a.Lk) continue;
-    if (PARTS && !at.whole) {
-      float* row = a.part + ((int64_t)place * a.part_rows + key - at.block * (32 * NB * W)) * 2 * D;
+    for (int blk = 0; blk < TL::kBlocks; ++blk)
 #pragma unroll
-      for (int blk = 0; blk < TL::kBlocks; ++blk)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int d = 32 * blk + 8 * q + 4 * h;
-          if (d >= D) continue;
-          f32x4 x, y;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = live[n] ? dk[blk][n][4 * q + i] * fk : 0.f;
-            y[i] = live[n] ? dv[blk][n][4 * q + i] * fv : 0.f;
-          }
-          *reinterpret_cast<f32x4*>(row + d) = x;
-          *reinterpret_cast<f32x4*>(row + D + d) = y;
-        }
-      continue;
-    }
-    T* kr = static_cast<T*>(g.dk.p) + b * g.dk.batch + key * g.dk.token + hk * g.dk.head;
-    T* vr = static_cast<T*>(g.dv.p) + b * g.dv.batch + key * g.dv.token + hk * g.dv.head;
-#pragma unroll
-    for (int blk = 0; blk < TL::kBlocks; ++blk) {
-      u32x4 x[2], y[2];
-      head_chunks<T>(dk[blk][n], fk, x);
-      head_chunks<T>(dv[blk][n], fv, y);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int d = 32 * blk + 16 * q + 8 * h;
+      for (int q = 0; q < 4; ++q) {
+        const int d = 32 * blk + 8 * q + 4 * h;
         if (d >= D) continue;
-        *reinterpret_cast<u32x4*>(kr + d) = live[n] ? x[q] : u32x4{0, 0, 0, 0};   // (a dropped key has no gradient)
-        *reinterpret_cast<u32x4*>(vr + d) = live[n] ? y[q] : u32x4{0, 0, 0, 0};
+        f32x4 x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = live ? dk[blk][4 * q + i] * fk : 0.f;
+          y[i] = live ? dv[blk][4 * q + i] * fv : 0.f;
+        }
+        *reinterpret_cast<f32x4*>(row + d) = x;
+        *reinterpret_cast<f32x4*>(row + D + d) = y;
       }
+    return;
+  }
+  T* to_dk = static_cast<T*>(g.dk.p) + b * g.dk.batch + key * g.dk.token + hk * g.dk.head;
+  T* to_dv = static_cast<T*>(g.dv.p) + b * g.dv.batch + key * g.dv.token + hk * g.dv.head;
+#pragma unroll
+  for (int blk = 0; blk < TL::kBlocks; ++blk) {
+    u32x4 x[2], y[2];
+    head_chunks<T>(dk[blk], fk, x);
+    head_chunks<T>(dv[blk], fv, y);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int d = 32 * blk + 16 * q + 8 * h;
+      if (d >= D) continue;
+      *reinterpret_cast<u32x4*>(to_dk + d) = live ? x[q] : u32x4{0, 0, 0, 0};   // (a dropped key has no gradient)
+      *reinterpret_cast<u32x4*>(to_dv + d) = live ? y[q] : u32x4{0, 0, 0, 0};
     }
   }
 }
 
-// dq of 32 NB query rows a wave; the keys pass by, as in the forward (4608
+// dq of 32 query rows a wave; the keys pass by, as in the forward (4608
 // tokens, 24 heads of 128: 350 us, 1.12 PFLOP/s, the matrix unit busy 45% of
 // the cycles). It also leaves what the keys' pass starts its sums with.
-template <typename T, int DP, int W, int KW, int NB, int NP, bool PARTS>
+template <typename T, int DP, int W, int KW, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dq_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;
   const AttnArgs& a = g.f;
@@ -411,45 +384,39 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   const int64_t Rp = g.rows_padded;
   const float top_v = kScaled<T> ? wave_top(g.top_v + at.hb * g.key_runs, g.key_runs, lane) : 0.f;
 
-  const int r0 = at.block * (32 * NB * W) + wave * (32 * NB);
-  u32x4 qf[NB][TL::kSteps], df[NB][TL::kSteps];
-  int last[NB];
-  float lse[NB], delta[NB], c[NB], wg_top = 0.f;   // (lse and delta negative)
+  const int r0 = at.block * (32 * W) + wave * 32;
+  u32x4 qf[TL::kSteps], df[TL::kSteps];
+  const int r = r0 + lr, query = attn_query(a.group, r), hd = r - query * G;
+  const int last = r >= R ? -1 : a.causal ? min(query + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
+  float top_do = 0.f, sum = 0.f;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), hd = r - i * G;
-    last[n] = r >= R ? -1 : a.causal ? min(i + a.Lk - a.Lq, a.Lk - 1) : a.Lk - 1;
-    float top_do = 0.f, sum = 0.f;
+  for (int s = 0; s < TL::kSteps; ++s) {
+    const int d = 16 * s + 8 * h;
+    const bool in = r < R && d < D;
+    qf[s] = in ? *reinterpret_cast<const u32x4*>(qp + query * a.q.token + hd * a.q.head + d) : u32x4{0, 0, 0, 0};
+    df[s] = in ? *reinterpret_cast<const u32x4*>(dop + query * g.dout.token + hd * g.dout.head + d) : u32x4{0, 0, 0, 0};
+    const u32x4 o = in ? *reinterpret_cast<const u32x4*>(op + query * a.o.token + hd * a.o.head + d) : u32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < TL::kSteps; ++s) {
-      const int d = 16 * s + 8 * h;
-      const bool in = r < R && d < D;
-      qf[n][s] = in ? *reinterpret_cast<const u32x4*>(qp + i * a.q.token + hd * a.q.head + d) : u32x4{0, 0, 0, 0};
-      df[n][s] = in ? *reinterpret_cast<const u32x4*>(dop + i * g.dout.token + hd * g.dout.head + d) : u32x4{0, 0, 0, 0};
-      const u32x4 o = in ? *reinterpret_cast<const u32x4*>(op + i * a.o.token + hd * a.o.head + d) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) sum = dot_x2<T>(sum, df[n][s][w], o[w]);
-      if constexpr (kScaled<T>) top_do = amax_x8<T>(top_do, df[n][s]);
-    }
-    // -lse / scale and -delta; of a row without keys (and behind the last
-    // row) -infinity, which makes its probabilities zero, and 0
-    const float l = r < R ? a.lse[((int64_t)b * a.H + hk * G + hd) * a.Lq + i] : -__builtin_inff();
-    const bool none = l == -__builtin_inff();
-    lse[n] = none ? l : -l / a.scale;
-    sum = sum_halves(sum);
-    delta[n] = none ? 0.f : -sum;
-    if (at.starts && way == 0) {   // for the keys' gradients, which start with them
-      if (h == 0) g.lse[at.hb * Rp + r] = lse[n];
-      if (h == 1) g.delta[at.hb * Rp + r] = delta[n];
-    }
-    lse[n] *= a.scale_log2;   // in base 2
-    if constexpr (kScaled<T>) {
-      top_do = none ? 0.f : max_halves(top_do);   // (a row that sees no key may hold anything)
-      c[n] = ds_scale(D, top_do, top_v);
-      wg_top = __builtin_fmaxf(wg_top, top_do);
-    } else {
-      c[n] = 1.f;
-    }
+    for (int w = 0; w < 4; ++w) sum = dot_x2<T>(sum, df[s][w], o[w]);
+    if constexpr (kScaled<T>) top_do = amax_x8<T>(top_do, df[s]);
+  }
+  // -lse / scale and -delta; of a row without keys (and behind the last
+  // row) -infinity, which makes its probabilities zero, and 0
+  const float l = r < R ? a.lse[((int64_t)b * a.H + hk * G + hd) * a.Lq + query] : -__builtin_inff();
+  const bool none = l == -__builtin_inff();
+  float lse = none ? l : -l / a.scale;   // (negative, as delta)
+  sum = sum_halves(sum);
+  const float delta = none ? 0.f : -sum;
+  if (at.starts && way == 0) {   // for the keys' gradients, which start with them
+    if (h == 0) g.lse[at.hb * Rp + r] = lse;
+    if (h == 1) g.delta[at.hb * Rp + r] = delta;
+  }
+  lse *= a.scale_log2;   // in base 2
+  float c = 1.f, wg_top = 0.f;
+  if constexpr (kScaled<T>) {
+    top_do = none ? 0.f : max_halves(top_do);   // (a row that sees no key may hold anything)
+    c = ds_scale(D, top_do, top_v);
+    wg_top = top_do;
   }
   if (kScaled<T> && at.starts) {   // (all waves)
 #pragma unroll
@@ -464,7 +431,7 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
   }
   const int k_begin = (at.first + way) * kAttnRows, k_end = at.last * kAttnRows, rounds = (at.last - at.first + KW - 1) / KW;
   const int w_first = a.causal ? attn_query(a.group, r0) + a.Lk - a.Lq : a.Lk - 1;
-  const int w_last = r0 >= R ? -1 : a.causal ? attn_query(a.group, min(r0 + 32 * NB, R) - 1) + a.Lk - a.Lq : a.Lk - 1;
+  const int w_last = r0 >= R ? -1 : a.causal ? attn_query(a.group, min(r0 + 32, R) - 1) + a.Lk - a.Lq : a.Lk - 1;
 
   auto fetch = [&](int k0, int stage, uint64_t keep) {
     const int rows = min(kAttnRows, a.Lk - k0);
@@ -491,11 +458,10 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     return k < a.Lk ? (mask ? (int)mask[k] : 1) : 0;
   };
 
-  f32x16 dq[TL::kBlocks][NB];
+  f32x16 dq[TL::kBlocks];
 #pragma unroll
   for (int i = 0; i < TL::kBlocks; ++i)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) dq[i][n] = f32x16{};
+    dq[i] = f32x16{};
   uint64_t keep = 0, next_keep = 0;
   int next_byte = 0;
   constexpr int kStep = KW * kAttnRows;
@@ -517,57 +483,47 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     const bool part = keep != ~0ull || k0 + kAttnRows - 1 > w_first;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      f32x16 s[NB], dp[NB];
+      f32x16 s, dp;
+      s = f32x16{};
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        s[n] = f32x16{};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dp[n][i] = delta[n];
-      }
+      for (int i = 0; i < 16; ++i) dp[i] = delta;
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
         const u32x4 f = TL::straight(tk, pl, kb, st);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) s[n] = mma<T>(f, qf[n][st], s[n]);
+        s = mma<T>(f, qf[st], s);
       }
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
         const u32x4 f = TL::straight(tv, pl, kb, st);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) dp[n] = mma<T>(f, df[n][st], dp[n]);
+        dp = mma<T>(f, df[st], dp);
       }
-      sched_products<2 * TL::kSteps * NB, 2 * TL::kSteps, 1, 4>();
-      u32x4 ds[2][NB][NP];
+      sched_products<2 * TL::kSteps, 2 * TL::kSteps, 1, 4>();
+      u32x4 ds[2][NP];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+      for (int i = 0; i < 16; ++i) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.scale_log2, lse));
+        dp[i] *= kScaled<T> ? p * c : p;
+      }
+      if (part) {
+        const int lim = last - k0 - 32 * kb - 4 * h;
+        const uint32_t bits = (uint32_t)(keep >> (32 * kb)) >> (4 * h);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], a.scale_log2, lse[n]));
-          dp[n][i] *= kScaled<T> ? p * c[n] : p;
+          const int at_key = 8 * (i / 4) + i % 4;
+          dp[i] = (bits >> at_key & 1) && at_key <= lim ? dp[i] : 0.f;
         }
-        if (part) {
-          const int lim = last[n] - k0 - 32 * kb - 4 * h;
-          const uint32_t bits = (uint32_t)(keep >> (32 * kb)) >> (4 * h);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at_key = 8 * (i / 4) + i % 4;
-            dp[n][i] = (bits >> at_key & 1) && at_key <= lim ? dp[n][i] : 0.f;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) as_operands<T>(dp[n], u, ds[u][n]);
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) as_operands<T>(dp, u, ds[u]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < TL::kBlocks; ++i) {
           const u32x4 f = TL::turned(tk, pl, 2 * kb + u, i);
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int w = 0; w < NP; ++w) dq[i][n] = mma<T>(f, ds[u][n][w], dq[i][n]);
+          for (int w = 0; w < NP; ++w) dq[i] = mma<T>(f, ds[u][w], dq[i]);
         }
-      sched_products<2 * TL::kBlocks * NB * NP, 4 * TL::kBlocks, 2, 8>();
+      sched_products<2 * TL::kBlocks * NP, 4 * TL::kBlocks, 2, 8>();
     }
   }
   if constexpr (KW > 1) {
@@ -578,34 +534,30 @@ __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP 
     if (second) return;
     join_add<DP, W, 0>(smem, wave, lane, dq);
   }
+  const float f = a.scale / c;
+  if (r >= R) return;
+  if (PARTS && !at.whole) {
+    float* row = a.part + ((int64_t)place * a.part_rows + r - at.block * (32 * W)) * D;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int r = r0 + 32 * n + lr, i = attn_query(a.group, r), hd = hk * G + r - i * G;
-    const float f = a.scale / c[n];
-    if (r >= R) continue;
-    if (PARTS && !at.whole) {
-      float* row = a.part + ((int64_t)place * a.part_rows + r - at.block * (32 * NB * W)) * D;
+    for (int blk = 0; blk < TL::kBlocks; ++blk)
 #pragma unroll
-      for (int blk = 0; blk < TL::kBlocks; ++blk)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int d = 32 * blk + 8 * q + 4 * h;
-          if (d < D)
-            *reinterpret_cast<f32x4*>(row + d) = f32x4{dq[blk][n][4 * q], dq[blk][n][4 * q + 1], dq[blk][n][4 * q + 2],
-                                                       dq[blk][n][4 * q + 3]} * f;
-        }
-      continue;
-    }
-    T* row = static_cast<T*>(g.dq.p) + b * g.dq.batch + i * g.dq.token + hd * g.dq.head;
-#pragma unroll
-    for (int blk = 0; blk < TL::kBlocks; ++blk) {
-      u32x4 x[2];
-      head_chunks<T>(dq[blk][n], f, x);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int d = 32 * blk + 16 * q + 8 * h;
-        if (d < D) *reinterpret_cast<u32x4*>(row + d) = x[q];
+      for (int q = 0; q < 4; ++q) {
+        const int d = 32 * blk + 8 * q + 4 * h;
+        if (d < D)
+          *reinterpret_cast<f32x4*>(row + d) = f32x4{dq[blk][4 * q], dq[blk][4 * q + 1], dq[blk][4 * q + 2],
+                                                     dq[blk][4 * q + 3]} * f;
       }
+    return;
+  }
+  T* row = static_cast<T*>(g.dq.p) + b * g.dq.batch + query * g.dq.token + (hk * G + hd) * g.dq.head;
+#pragma unroll
+  for (int blk = 0; blk < TL::kBlocks; ++blk) {
+    u32x4 x[2];
+    head_chunks<T>(dq[blk], f, x);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int d = 32 * blk + 16 * q + 8 * h;
+      if (d < D) *reinterpret_cast<u32x4*>(row + d) = x[q];
     }
   }
 }
@@ -646,9 +598,9 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs g, Att
 template <typename T, int DP, int W, int KW, int NP, bool KEYS, bool PARTS>
 constexpr auto grad_kernel() {
   if constexpr (KEYS)
-    return attn_dkv_kernel<T, DP, W, KW, 1, NP, PARTS>;
+    return attn_dkv_kernel<T, DP, W, KW, NP, PARTS>;
   else
-    return attn_dq_kernel<T, DP, W, KW, 1, NP, PARTS>;
+    return attn_dq_kernel<T, DP, W, KW, NP, PARTS>;
 }
 template <int DP, int W, int KW, bool KEYS>
 constexpr int kGradLds = 4 * KW * AttnTile<DP>::kBytes + (KEYS && DP == 128 ? W * kAttnWave * AttnTile<DP>::kRowBytes : 0);
