@@ -147,7 +147,8 @@ class RopeDesc(ctypes.Structure):
 
 class AttentionDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "head_dim", "heads", "kv_heads", "causal")] + \
-               [("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("samples", "queries", "keys")]
+               [("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("samples", "queries", "keys")] + \
+               [("fine", ctypes.c_int32)]
 
 
 _lib = None
@@ -1459,9 +1460,9 @@ def rope(q, k, positions, freqs, pairs, interleaved: bool = True, inverse: bool 
 
 
 @functools.lru_cache(maxsize=1024)
-def _attention_plan(dt, D, H, Hk, causal, scale, B, Lq, Lk):
+def _attention_plan(dt, D, H, Hk, causal, scale, B, Lq, Lk, fine):
     """(descriptor reference, itself, forward's and backward's workspace bytes)"""
-    d = AttentionDesc(dt, D, H, Hk, causal, scale, B, Lq, Lk)
+    d = AttentionDesc(dt, D, H, Hk, causal, scale, B, Lq, Lk, fine)
     sizes = []
     for name in ("svdq_attention_workspace_bytes", "svdq_attention_backward_workspace_bytes"):
         n = ctypes.c_size_t()
@@ -1470,15 +1471,19 @@ def _attention_plan(dt, D, H, Hk, causal, scale, B, Lq, Lk):
     return ctypes.byref(d), d, sizes[0], sizes[1]
 
 
-def attention_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None, causal: bool = False) -> int:
-    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, int(causal), 1.0, samples, queries, keys)[2]
+def attention_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None, causal: bool = False,
+                              fine: bool = False) -> int:
+    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, int(causal), 1.0, samples, queries, keys,
+                           int(fine))[2]
 
 
-def attention_backward_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None, causal: bool = False) -> int:
-    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, int(causal), 1.0, samples, queries, keys)[3]
+def attention_backward_workspace_bytes(samples, queries, keys, heads, kv_heads, head_dim, dtype=None, causal: bool = False,
+                                       fine: bool = False) -> int:
+    return _attention_plan(_dt(dtype or _torch().bfloat16), head_dim, heads, kv_heads, int(causal), 1.0, samples, queries, keys,
+                           int(fine))[3]
 
 
-def _attention_setup(q, k, v, key_mask, causal, scale):
+def _attention_setup(q, k, v, key_mask, causal, scale, fine=False):
     """((descriptor reference, itself, workspace bytes), mask pointer, stride)"""
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if len(shape) != 4 or len(kshape) != 4:
@@ -1495,22 +1500,24 @@ def _attention_setup(q, k, v, key_mask, causal, scale):
             raise ValueError("key_mask: bool or uint8 [samples][keys], contiguous along the keys")
         mask, ld = key_mask.data_ptr(), key_mask.stride(0)
     plan = _attention_plan(_dt(dtype), D, H, Hk, 1 if causal else 0, float(scale) if scale is not None else max(D, 1) ** -0.5, B,
-                           Lq, Lk)
+                           Lq, Lk, 1 if fine else 0)
     return plan, mask, ld
 
 
-def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, out=None, workspace=None, stream=None):
+def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, out=None, workspace=None, stream=None,
+                      fine: bool = False):
     """svdq_attention_forward: (o, lse) of q [samples][queries][heads][head_dim]
     and k, v [samples][keys][kv_heads][head_dim] (bfloat16 or float16, any
     strides of 16 bytes). key_mask: bool or uint8 [samples][keys], true for the
     keys that take part; causal: query i sees the keys j <= i + keys - queries;
-    scale: default head_dim^(-1/2). lse: float32 [samples][heads][queries]. A
+    scale: default head_dim^(-1/2). fine: probabilities enter their product as
+    two values, whatever the sizes. lse: float32 [samples][heads][queries]. A
     query without keys has o = 0, lse = -inf. An out that overlaps an input is
     refused."""
     at = _on_device(q, k, v, key_mask, out, workspace)
     if _wants_grad(q, k, v):
         _no_graph("attention_forward")
-    (d, _, size, _), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
+    (d, _, size, _), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale, fine)
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if out is None:
         out = _rows_like(q, shape, stream)
@@ -1525,14 +1532,14 @@ def attention_forward(q, k, v, key_mask=None, causal: bool = False, scale=None, 
 
 
 def attention_backward(dout, q, k, v, o, lse, key_mask=None, causal: bool = False, scale=None, dq=None, dk=None, dv=None,
-                       workspace=None, stream=None):
+                       workspace=None, stream=None, fine: bool = False):
     """svdq_attention_backward: (dq, dk, dv) for dout of o, from the forward's
     inputs and its o and lse. Given ones that overlap an input or one another are
     refused."""
     at = _on_device(q, dout, k, v, o, lse, key_mask, dq, dk, dv, workspace)
     if _wants_grad(dout):
         _no_graph("attention_backward")
-    (d, _, _, size), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale)
+    (d, _, _, size), mask, ldm = _attention_setup(q, k, v, key_mask, causal, scale, fine)
     shape, kshape, dtype = q.shape, k.shape, q.dtype
     if lse.dtype != _t.float32 or lse.shape != (shape[0], shape[2], shape[1]) or not lse.is_contiguous():
         raise ValueError("lse: float32 [samples][heads][queries]")

@@ -170,7 +170,8 @@ Heads attn_heads(const svdq_heads* t, const svdq_attention_desc* d, bool of_q) {
   return heads_of(t, d->samples, of_q ? d->queries : d->keys, of_q ? d->heads : d->kv_heads);
 }
 AttnSizes sizes_of(const svdq_attention_desc* d) {
-  return AttnSizes{d->samples, d->queries, d->keys, d->heads, d->kv_heads, d->head_dim, d->causal != 0, d->dtype == SVDQ_DT_F16};
+  return AttnSizes{d->samples, d->queries, d->keys, d->heads, d->kv_heads, d->head_dim,
+                   d->causal != 0, d->dtype == SVDQ_DT_F16, d->fine != 0};
 }
 AttnArgs attn_args(const svdq_attention_desc* d, const uint8_t* mask, int64_t mask_batch) {
   AttnArgs a;

@@ -527,6 +527,7 @@ SVDQ_HD inline int attn_query(const AttnGroup& g, int r) {
 struct AttnSizes {
   int64_t B, Lq, Lk, H, Hk, D;
   bool causal, scaled;   // scaled: fp16
+  bool fine;             // the caller asks for it
 };
 // Waves that hold rows of their own: eight where there is such a block for
 // every CU, since they share a tile (4608 tokens, 24 heads of 128: 250 us
@@ -542,9 +543,10 @@ inline int attn_waves(int64_t held, int64_t heads) {
 // is taken where the products are not what takes time: for heads up to 32
 // elements, whose fragments are half as many (2 x 4608 tokens, 12 heads of 32,
 // backward: 459 us, rounded once as heads of 64 500), and where a side fits
-// a tile.
-inline bool attn_fine(int64_t held, int64_t passing, int64_t D) {
-  return D <= 32 || held <= kAttnTile || passing <= kAttnTile;
+// a tile. Elsewhere a caller may ask for it (4608 tokens, 24 heads of 128:
+// forward 324 us against 245, backward 1118 against 825).
+inline bool attn_fine(const AttnSizes& s, int64_t held, int64_t passing) {
+  return s.fine || s.D <= 32 || held <= kAttnTile || passing <= kAttnTile;
 }
 // Four waves leave a CU half empty unless it gets two such workgroups. With two
 // ways a workgroup has four more waves for the same rows, which take every
@@ -570,7 +572,7 @@ inline bool attn_shorter(int64_t held, int64_t passing, int64_t D) {
 }
 inline AttnCost attn_row_cost(const AttnSizes& s) {   // rows are held
   const int64_t rows = s.Lq * (s.H / s.Hk), heads = s.B * s.Hk;
-  const bool fine = attn_fine(rows, s.Lk, s.D), eight = fine && s.D > 32;
+  const bool fine = attn_fine(s, rows, s.Lk), eight = fine && s.D > 32;
   int waves = eight ? 8 : attn_waves(rows, heads);
   const int ways = waves == 4 ? attn_ways(rows, heads, s.causal) : 1;
   if (!eight && ways == 1 && attn_shorter(rows, s.Lk, s.D)) waves = 4;
@@ -580,7 +582,7 @@ inline AttnCost attn_key_cost(const AttnSizes& s) {
   const int64_t rows = s.Lq * (s.H / s.Hk), heads = s.B * s.Hk;
   // (V's fragments of heads above 96 leave no room in LDS for a second way or
   // workgroup; with heads above 64 four waves alone gain nothing otherwise)
-  const bool fine = attn_fine(s.Lk, rows, s.D), eight = (fine && s.D > 32) || s.D > 96;
+  const bool fine = attn_fine(s, s.Lk, rows), eight = (fine && s.D > 32) || s.D > 96;
   int waves = eight ? 8 : attn_waves(s.Lk, heads);
   const int ways = waves == 4 ? attn_ways(s.Lk, heads, s.causal) : 1;
   if (s.D > 64 && ways == 1) waves = 8;

@@ -810,10 +810,11 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * [samples][heads][queries]. Scores, statistics and sums are fp32; the
  * probabilities (and in the backward the scores' gradients) are rounded to the
  * type for the matrix products, fp16 with powers of two taken out in the
- * backward so that small ones keep their digits. For heads up to 32 elements,
- * and up to 64 keys or queries times heads / kv_heads, they enter the products
- * as two values of the type, the second what the first's rounding left. All
- * orders of summation are fixed by the sizes.
+ * backward so that small ones keep their digits. That rounding adds about an
+ * output's own to its error. With `fine`, and for heads up to 32 elements and up
+ * to 64 keys or queries times heads / kv_heads, they enter the products as two
+ * values of the type, the second what the first's rounding left, and add
+ * nothing. All orders of summation are fixed by the sizes and `fine`.
  * Keys and values that the mask drops, and the q and dout of queries that see
  * no key, are not used whatever they hold. Other values that are not finite do
  * what the formulas say: a NaN in q makes its row NaN, one in k every row that
@@ -835,6 +836,7 @@ typedef struct {
   int32_t dtype, head_dim, heads, kv_heads, causal;
   float scale;
   int64_t samples, queries, keys;
+  int32_t fine;
 } svdq_attention_desc;
 
 /* With few query rows the keys are cut into parts, whose results pass through

@@ -157,12 +157,12 @@ def _scores(q, k, see, scale):
     return s, (q.shape[1] + 4) * U * mag
 
 
-def attention(q, k, v, mask, causal, scale, grad=None):
+def attention(q, k, v, mask, causal, scale, grad=None, fine=False):
     """{name: (value, error)}: o and lse; with grad = (dout, o, lse) dq, dk and dv."""
     B, Lq, H, D = q.shape
     Lk, Hk, dt = k.shape[1], k.shape[2], q.dtype
     half, tiny = half_step(dt), dt == torch.float16
-    if D <= 32 or Lq * (H // Hk) <= 64 or Lk <= 64:   # probabilities and ds enter their products as two values, the second what the first's rounding left
+    if fine or D <= 32 or Lq * (H // Hk) <= 64 or Lk <= 64:   # probabilities and ds enter their products as two values, the second what the first's rounding left
         half = 1.01 * half * half
     dev = q.device
 
