@@ -22,8 +22,9 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// From here on a row's reference (in base 2) is too coarse: half a step of fp32
-// at 2^20 is 2^-5, by which its largest probability is off a power of two.
+// Up to here a row's reference (in base 2) is off by half a step of fp32, 2^-5 at
+// most, which its largest probability has room for; from 2^30 on it would be off
+// by more than fp32's exponents hold.
 constexpr float kFarScore = 0x1p20f;
 __device__ __forceinline__ float reference(float m, float scale_log2) {
   return m == -__builtin_inff() ? 0.f : m * scale_log2;
@@ -33,15 +34,16 @@ __device__ __forceinline__ float reference_off(float m, float base, float scale_
   return m == -__builtin_inff() || __builtin_fabsf(base) > kFarScore ? 0.f : __builtin_fmaf(m, scale_log2, -base);
 }
 
-// W waves of 32 query rows, KW times (each way takes every KW-th tile); DP the padded head; NP operands for probabilities. Two waves a SIMD
-// (up to 256 registers), so that one's products run under the other's
-// exponentials: 4608 tokens, 24 heads of 128 with a mask 250 us (1.04
-// PFLOP/s), with one wave a SIMD 411, with one of two blocks 355, with
-// workgroups of four waves instead of eight 270. What bounds it: a tile's
+// W waves of 32 query rows, KW times (each way takes every KW-th tile); DP the
+// padded head; NP operands for probabilities. Two waves a SIMD (up to 256
+// registers), so that one's products run under the other's exponentials: 4608
+// tokens, 24 heads of 128 with a mask 245 us (1.06 PFLOP/s), with one wave a
+// SIMD 411, with one of two blocks 355, with workgroups of four waves instead of
+// eight 270. What bounds it: a tile's
 // exponentials, maxima, sums and roundings take the vector unit as long as its
 // products the matrix unit (40% of the cycles), at a clock that power holds
 // near 2 GHz; LDS is busy a fifth of the time. One query over 65536 keys
-// streams its cache at 5.5 TB/s.
+// streams caches of 268 MB in turn at 4.8 TB/s (56 us; a call with the join 61).
 template <typename T, int DP, int W, int KW, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2))) void attn_fwd_kernel(AttnArgs a, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;

@@ -133,7 +133,7 @@ __device__ __forceinline__ void join_add(uint8_t* smem, int wave, int lane, f32x
 // waves a SIMD leave, so V's fragments wait in LDS (4608 tokens, 24 heads, of
 // the same step: 574 us against 760 with V in registers, of which 53 spill, 768
 // with one wave a SIMD and two blocks of keys, 870 with workgroups of four
-// waves; now 535, 0.98 PFLOP/s, with the matrix unit busy 43% of the cycles).
+// waves; now 530, 0.99 PFLOP/s, with the matrix unit busy 45% of the cycles).
 template <typename T, int DP, int W, int KW, int NP, bool PARTS>
 __global__ __launch_bounds__(64 * W * KW) __attribute__((amdgpu_waves_per_eu(DP == 32 ? 4 : 2, DP == 32 ? 4 : 2))) void attn_dkv_kernel(AttnGradArgs g, AttnDeal<PARTS> deal) {
   typedef AttnTile<DP> TL;

@@ -11,7 +11,8 @@
 //
 // (rms: without the first mean of each). Bound by memory: the forward reads x
 // and h and writes s and y, the backward reads s, h, dy and ds and writes dx
-// and dh, each once (8192 x 4096 bf16: 50 us, 5.4 TB/s, and 80, 5.0). A team
+// and dh, each once (8192 x 4096 bf16, calls with three sets of inputs in turn:
+// 58.5 us, 4.6 TB/s, and 80, 5.0; fp32 8192 x 2048: 47, 5.8, and 75, 5.4). A team
 // of lanes holds a row in registers, so the chained sums (up to four) cost no
 // second read; the next row's loads are in flight. All sums are in fp32, in an
 // order fixed by the sizes: per lane, a butterfly over the wave, the waves in
@@ -478,8 +479,9 @@ hipError_t launch_residual(const ResidualArgs& a, int num_cus, hipStream_t st) {
 
 hipError_t launch_residual_grad(const ResidualGradArgs& args, const ResidualGradPlan& p, hipStream_t st) {
   // What the caches (256 MB) cannot keep until it is used again is read past
-  // them (8192 x 4096 bf16, 403 MB: 80 us against 92, 4608 x 5120 fp32, 472 MB:
-  // 111 against 130; 4608 x 2560 bf16, 142 MB: 45.5 against 43.2).
+  // them (three sets of inputs in turn, 8192 x 4096 bf16, 403 MB: 81 us against
+  // 93, 8192 x 2048 fp32, 403 MB: 76 against 89, 4608 x 5120 fp32, 566 MB: 122
+  // against 128; one set, 4608 x 2560 bf16, 142 MB: 45.5 against 43.2).
   ResidualGradArgs g = args;
   g.once = (double)g.f.M * g.f.C * (g.ds ? 6 : 5) * (g.f.dtype == SVDQ_DT_F32 ? 4 : 2) > 256e6;
   const bool post = g.f.post;

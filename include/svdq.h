@@ -827,7 +827,8 @@ SVDQ_API svdq_status svdq_rope(const svdq_rope_desc* desc, const svdq_heads* q, 
  * of kv_heads, samples * kv_heads <= 65535; queries * heads / kv_heads < 2^30
  * and keys < 2^30; blocks of 128 of those times samples * kv_heads <= 2^22;
  * 2^-64 <= scale <= 2^64 (the backward: 2^10); 64 tokens (and the heads of one
- * key head) of a tensor span less than 2^30 elements. Outputs must not overlap inputs or one another.
+ * key head) of a tensor span less than 2^30 elements. Outputs must not overlap
+ * inputs or one another (the binding refuses those; these functions do not look).
  * Errors: SVDQ_ERR_NULL, SVDQ_ERR_SHAPE, SVDQ_ERR_FORMAT, SVDQ_ERR_WORKSPACE,
  * SVDQ_ERR_DEVICE.
  * ---------------------------------------------------------------------------
